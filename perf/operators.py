@@ -350,7 +350,6 @@ def _to_e4m3(x, dither, least):
     code = torch.where(a < 2.0 ** -6,
                        torch.floor(a * 512 + dither.float() * 2.0 ** -20) * 2.0 ** -9,
                        ((a.view(torch.int32).long() + dither) & ~0xFFFFF).to(torch.int32).view(torch.float32))
-    code = code.clamp(max=448.0)
     if least:
         code = torch.where((a > 0) & (code == 0), 2.0 ** -9, code)
     return torch.copysign(code, x).to(torch.float8_e4m3fn)
@@ -362,10 +361,10 @@ def _blocks(x):
 
 
 def _quantise(x, codes, scales, dither, least):
+    # the power of two that leaves a block's largest magnitude in [128, 256)
     top = _blocks(x.abs()).amax(1)
-    scale = top / 448.0
-    inv = torch.where(top > 0, 448.0 / top, 0.0)
-    y = (_blocks(x) * inv[:, None]).reshape(-1)[:x.numel()]
+    scale = torch.where(top > 0, torch.ldexp(torch.ones_like(top), torch.frexp(top)[1] - 8), 0.0)
+    y = (_blocks(x) / torch.where(top > 0, scale, 1.0)[:, None]).reshape(-1)[:x.numel()]
     codes.copy_(_to_e4m3(y, dither, least))
     scales.copy_(scale)
 
@@ -495,7 +494,7 @@ def _grid64(x, dither, least):
     """|x| on e4m3's grid (three bits of a number's leading one, 2^-9 at the least), rounded down with the dither."""
     a = x.abs()
     unit = torch.pow(2.0, (torch.frexp(a)[1].double() - 4).clamp(min=-9))
-    q = (torch.floor(a / unit + dither.double() / 2 ** 20) * unit).clamp(max=448)
+    q = torch.floor(a / unit + dither.double() / 2 ** 20) * unit
     return torch.sign(x) * (torch.where(a > 0, q.clamp(min=2.0 ** -9), q) if least else q)
 
 
@@ -509,9 +508,10 @@ def _exact_adamw(s, c):
 
     def held(key, view, scales, x, dither, least):
         top = _blocks(x.abs()).amax(1)
-        unit = (448 / top.clamp(min=1e-300)).repeat_interleave(BLOCK)[:x.numel()]
-        put(key, view, _grid64(x * unit, dither, least))
-        put(key + "s", scales, top / 448)
+        two = torch.where(top > 0, torch.exp2(torch.floor(torch.log2(top.clamp(min=1e-300))) - 7), 0.0)
+        unit = torch.where(two > 0, two, 1.0).repeat_interleave(BLOCK)[:x.numel()]
+        put(key, view, _grid64(x / unit, dither, least))
+        put(key + "s", scales, two)
 
     for p, g, w, m, v, ms, vs, dec in zip(s["p"], s["g"], s["w"], s["m"], s["v"], s["ms"], s["vs"], s["decay"]):
         n, g = p.numel(), g.double()
