@@ -287,6 +287,124 @@ MOE_API moe_status_t moe_soft_balance_window_backward(const moe_config_t* cfg, c
 MOE_API moe_status_t moe_coselect(const moe_config_t* cfg, const int32_t* idx, int32_t* H,
                                   moe_stream_t stream);
 
+/* ------------------------------------------------------------------------------------------
+ * The layer in a training step: token embedding (the layer's x, and the gradient that takes
+ * its dx), the policy loss on the logits, and the AdamW step over the weights. The pages train
+ * the layer inside such a step (PithTrain page, section 4.1) and leave these parts to the host
+ * framework. The conventions at the top of this file hold; each call has a small
+ * configuration of its own, checked on every call (nothing to initialise). */
+
+/* Token embedding. W [V,d] act, ids [T] int32.
+ *   moe_embed:          y[t] = scale * W[ids[t]]                      (y [T,d] act, one rounding)
+ *   moe_embed_backward: dW[v] = scale * sum over tokens t with ids[t] = v of dy[t]
+ * dy [T,d] act, dW [V,d] in grad_dtype. accumulate = 0 writes all of dW (zero rows for tokens
+ * that do not occur); accumulate = 1 adds to dW and touches only the rows of tokens that do
+ * (a table tied to the output head). Tokens equal to padding_id get no gradient (-1: none);
+ * the forward looks them up like any other. Sums are fp32 in a fixed order (tokens sorted
+ * stably by id), so results repeat bit for bit. An id outside [0,V) sets
+ * MOE_ERR_DEVICE_BOUNDS: its y row is zero and its dy row is left out.
+ * W, y, dy, dW and ws are 16-byte aligned; T = 0 is allowed (an overwritten dW is zeroed). */
+typedef struct {
+    int32_t T;             /* tokens, >= 0 */
+    int32_t V;             /* rows of the table, >= 1 */
+    int32_t d;             /* row length, >= 1 */
+    float scale;           /* finite */
+    int32_t padding_id;    /* in [-1, V) */
+    int32_t dtype;         /* moe_dtype_t of W, y, dy */
+    int32_t grad_dtype;    /* moe_dtype_t of dW */
+    int32_t accumulate;    /* 0/1 */
+} moe_embed_config_t;
+MOE_API moe_status_t moe_embed(const moe_embed_config_t* cfg, const int32_t* ids, const void* W, void* y,
+                               moe_stream_t stream);
+/* Bytes of `ws` for moe_embed_backward; 0 for an invalid cfg. */
+MOE_API size_t moe_embed_workspace_bytes(const moe_embed_config_t* cfg);
+MOE_API moe_status_t moe_embed_backward(const moe_embed_config_t* cfg, const int32_t* ids, const void* dy,
+                                        void* dW, void* ws, moe_stream_t stream);
+
+/* Clipped policy loss with a KL term, on the logits of the chosen tokens.
+ *   lp = log softmax(logits[t] / temperature)[target[t]],   r = exp(lp - old_logp[t]),
+ *   u  = ref_logp[t] - lp,
+ *   l  = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl_weight (exp(u) - u - 1),
+ *   loss = sum_t weight[t] l_t          (A = advantage[t]; weight carries mask and mean)
+ *   dlogits[t,v] = weight[t] / temperature * dl/dlp * (1[v = target[t]] - softmax_v),
+ *   dl/dlp = (-A r where r A <= clip(r) A, else 0) + kl_weight (1 - exp(u)).
+ * logits [T,V] act with rows ld elements apart; dlogits [T,V] act, rows ld_grad apart; it may be
+ * logits itself (then ld_grad = ld), any other overlap is not allowed. target [T] int32;
+ * advantage, old_logp, ref_logp, weight, logp [T] fp32; loss [1] fp32. One reading of the
+ * logits gives the loss and the gradient.
+ *   old_logp null: on-policy, r = 1 with its gradient. ref_logp: needed iff kl_weight != 0.
+ *   weight null: 1 for each token. logp, loss, dlogits: each may be null (not wanted).
+ *   ws (moe_policy_workspace_bytes): needed when loss is not null.
+ * A token with weight 0 or a negative target is left out: its logits are not read, whatever
+ * they hold, logp = 0 and its dlogits row is zero. A target >= V sets MOE_ERR_DEVICE_BOUNDS and
+ * the token is left out. Logits of -inf are tokens of probability 0; a row whose every logit
+ * is -inf, or that holds +inf or NaN, has no distribution and gives NaN (row and loss).
+ * Softmax statistics and loss sums are fp32, in a fixed order. logits and dlogits start on a
+ * 16-byte boundary; V, ld, ld_grad may be odd. */
+typedef struct {
+    int32_t T;             /* tokens, >= 0 */
+    int32_t V;             /* vocabulary, >= 1 */
+    int64_t ld;            /* elements between logits rows, >= V */
+    int64_t ld_grad;       /* elements between dlogits rows, >= V */
+    int32_t dtype;         /* moe_dtype_t of logits and dlogits */
+    float temperature;     /* > 0 */
+    float clip_low;        /* in [0, 1] */
+    float clip_high;       /* >= 0 */
+    float kl_weight;       /* finite */
+} moe_policy_config_t;
+/* Bytes of `ws` for moe_policy_loss; 0 for an invalid cfg. */
+MOE_API size_t moe_policy_workspace_bytes(const moe_policy_config_t* cfg);
+MOE_API moe_status_t moe_policy_loss(const moe_policy_config_t* cfg, const void* logits, const int32_t* target,
+                                     const float* advantage, const float* old_logp, const float* ref_logp,
+                                     const float* weight, float* logp, float* loss, void* dlogits, void* ws,
+                                     moe_stream_t stream);
+/* lp alone (what old_logp and ref_logp are made of, and what a server returns beside a sampled
+ * token): T, V, ld, dtype and temperature of cfg. A negative target gives logp = 0. */
+MOE_API moe_status_t moe_token_logp(const moe_policy_config_t* cfg, const void* logits, const int32_t* target,
+                                    float* logp, moe_stream_t stream);
+
+/* AdamW over many tensors in one call. With t = steps done + 1, g = grad (times *grad_scale):
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2,
+ *   x = x (1 - lr weight_decay) - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps),
+ * all in fp32. x is the fp32 master if there is one (p is then x rounded to its type), else p.
+ * States: fp32 m and v [n]; or, where m_scale and v_scale are given, 8 bits each: m holds
+ * e4m3 values of m, v holds e4m3 values of sqrt(v), both times one fp32 scale to a block of
+ * MOE_ADAMW_BLOCK elements (m_scale, v_scale [ceil(n / MOE_ADAMW_BLOCK)]: the power of two that
+ * leaves the block's largest magnitude in [128, 256), 0 for a block below 2^-100). They are
+ * rounded with a dither, a Weyl sequence over elements and steps: rounding to nearest would
+ * hold sqrt(v) still, because beta2 = 0.999 moves it by 0.05 % a step and half a step of e4m3
+ * is 3 to 6 %. sqrt(v) > 0 never becomes 0. A value that is not finite is held as NaN and
+ * leaves the rest of its block alone. The step itself uses m and v before they are rounded.
+ * Zeroed states (and scales) are the start of training. Arrays are 16-byte aligned (scales,
+ * lr, grad_scale: 4), tensors do not overlap; n = 0 is allowed.
+ *   cfg, tensors [count]: host memory, read before the call returns
+ *   lr: device fp32, replaces cfg->lr (a schedule under a captured graph); null: cfg->lr
+ *   grad_scale: device fp32, multiplies every gradient (clipping, unscaling); null: 1
+ *   state: MOE_ADAMW_STATE_BYTES of device memory, 8-byte aligned: the steps done, advanced by
+ *     the call; zeroed before the first. Layout: 1 - beta1^t and 1 - beta2^t (double), t (int64),
+ *     and 8 bytes that are zero between calls. Calls on one state are ordered on the GPU. */
+#define MOE_ADAMW_BLOCK 256
+#define MOE_ADAMW_STATE_BYTES 32
+typedef struct {
+    double lr, beta1, beta2, eps;   /* lr finite, betas in [0, 1), eps > 0 */
+} moe_adamw_config_t;
+typedef struct {
+    void* p;                /* [n] weights, dtype */
+    const void* g;          /* [n] gradient, grad_dtype */
+    float* master;          /* [n] fp32 weights, or null */
+    void* m;                /* [n] fp32, or e4m3 when m_scale is set */
+    void* v;                /* [n] fp32, or e4m3 of the root when v_scale is set */
+    float* m_scale;         /* both or neither */
+    float* v_scale;
+    int64_t n;              /* elements, 0 .. 2^38 */
+    int32_t dtype;          /* moe_dtype_t */
+    int32_t grad_dtype;     /* moe_dtype_t */
+    float weight_decay;     /* finite, >= 0 */
+    int32_t reserved;       /* 0 */
+} moe_adamw_tensor_t;
+MOE_API moe_status_t moe_adamw(const moe_adamw_config_t* cfg, const moe_adamw_tensor_t* tensors, int32_t count,
+                               const float* lr, const float* grad_scale, void* state, moe_stream_t stream);
+
 /* Synchronises `stream`, then returns and clears the device error word of the current
  * device: MOE_OK, MOE_ERR_DEVICE_TIMEOUT or MOE_ERR_DEVICE_BOUNDS; MOE_ERR_CUDA if the
  * stream reports a CUDA error. */

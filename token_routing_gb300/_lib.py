@@ -23,6 +23,8 @@ MOE_ROW_ALIGN = 128
 MOE_MAX_EXPERTS = 256
 MOE_MAX_K = 8
 MOE_MAX_WINDOW = 4096
+MOE_ADAMW_BLOCK = 256
+MOE_ADAMW_STATE_BYTES = 32
 
 
 class MoeConfig(ctypes.Structure):
@@ -40,6 +42,30 @@ class MoeConfig(ctypes.Structure):
         return "MoeConfig(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
 
 
+class MoeEmbedConfig(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("V", ctypes.c_int32), ("d", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("padding_id", ctypes.c_int32), ("dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+                ("accumulate", ctypes.c_int32)]
+
+
+class MoePolicyConfig(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("V", ctypes.c_int32), ("ld", ctypes.c_int64), ("ld_grad", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("temperature", ctypes.c_float), ("clip_low", ctypes.c_float),
+                ("clip_high", ctypes.c_float), ("kl_weight", ctypes.c_float)]
+
+
+class MoeAdamwConfig(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double)]
+
+
+class MoeAdamwTensor(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("g", ctypes.c_void_p), ("master", ctypes.c_void_p), ("m", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("n", ctypes.c_int64), ("dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+                ("weight_decay", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, fn, status):
         self.status = status
@@ -48,6 +74,8 @@ class MoeError(RuntimeError):
 
 _P = ctypes.c_void_p
 _CFG = ctypes.POINTER(MoeConfig)
+_EMB = ctypes.POINTER(MoeEmbedConfig)
+_POL = ctypes.POINTER(MoePolicyConfig)
 _SIGS = {
     "moe_config_init": (ctypes.c_int, [_CFG]),
     "moe_workspace_bytes": (ctypes.c_size_t, [_CFG]),
@@ -69,6 +97,14 @@ _SIGS = {
     "moe_soft_balance_window_backward": (ctypes.c_int, [_CFG, _P, _P, ctypes.c_float, _P, _P, _P, _P, _P, _P,
                                                         _P, _P]),
     "moe_dispatch_noalloc": (ctypes.c_int, [_CFG, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "moe_embed": (ctypes.c_int, [_EMB, _P, _P, _P, _P]),
+    "moe_embed_workspace_bytes": (ctypes.c_size_t, [_EMB]),
+    "moe_embed_backward": (ctypes.c_int, [_EMB, _P, _P, _P, _P, _P]),
+    "moe_policy_workspace_bytes": (ctypes.c_size_t, [_POL]),
+    "moe_policy_loss": (ctypes.c_int, [_POL] + [_P] * 11),
+    "moe_token_logp": (ctypes.c_int, [_POL, _P, _P, _P, _P]),
+    "moe_adamw": (ctypes.c_int, [ctypes.POINTER(MoeAdamwConfig), ctypes.POINTER(MoeAdamwTensor), ctypes.c_int32,
+                                 _P, _P, _P, _P]),
     "moe_trace_begin": (ctypes.c_int, [ctypes.c_int32]),
     "moe_trace_end": (ctypes.c_int32, []),
     "moe_trace_record": (ctypes.c_int, [ctypes.c_int32, ctypes.POINTER(ctypes.c_char_p),
