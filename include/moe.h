@@ -371,9 +371,9 @@ MOE_API moe_status_t moe_token_logp(const moe_policy_config_t* cfg, const void* 
  * e4m3 values of m, v holds e4m3 values of sqrt(v), both times one fp32 scale to a block of
  * MOE_ADAMW_BLOCK elements (m_scale, v_scale [ceil(n / MOE_ADAMW_BLOCK)]: the power of two that
  * leaves the block's largest magnitude in [128, 256), 0 for a block below 2^-100). They are
- * rounded with a dither, a Weyl sequence over elements and steps: rounding to nearest would
- * hold sqrt(v) still, because beta2 = 0.999 moves it by 0.05 % a step and half a step of e4m3
- * is 3 to 6 %. sqrt(v) > 0 never becomes 0. A value that is not finite is held as NaN and
+ * rounded up or down by a dither, a hash of element and step, so that m and v are right on
+ * average: rounding to nearest would hold sqrt(v) still, because beta2 = 0.999 moves it by
+ * 0.05 % a step and half a step of e4m3 is 3 to 6 %. sqrt(v) > 0 never becomes 0. A value that is not finite is held as NaN and
  * leaves the rest of its block alone. The step itself uses m and v before they are rounded.
  * Zeroed states (and scales) are the start of training. Arrays are 16-byte aligned (scales,
  * lr, grad_scale: 4), tensors do not overlap; n = 0 is allowed.

@@ -85,12 +85,14 @@ def e4m3_values():
     return out
 
 
-def dither(n, step, flip=0, start=0):
-    """20 bits of a Weyl sequence over elements and steps."""
+def dither(n, step, start=0):
+    """20 bits for each element and step, twice: for m and for v."""
     i = np.arange(start, start + n, dtype=np.uint64)
+    low, c, e = np.uint64(0xFFFFFFFF), np.uint64(0x85EBCA6B), np.uint64(0xC2B2AE35)
     with np.errstate(over="ignore"):
-        h = (i * np.uint64(0x9E3779B1) + np.uint64(step * 0x61C88647)) & np.uint64(0xFFFFFFFF)
-    return ((h >> np.uint64(12)) ^ np.uint64(flip)).astype(np.float64)
+        h = (i * np.uint64(0x9E3779B1) + np.uint64(step * 0x61C88647)) & low
+        h = ((h ^ (h >> np.uint64(15))) * c) & low
+        return (h >> np.uint64(12)).astype(np.float64), (((h * e) & low) >> np.uint64(12)).astype(np.float64)
 
 
 def blocks(x):
@@ -104,12 +106,16 @@ def block_scale(x):
     return np.where(top > 0, 2.0 ** (np.floor(np.log2(np.where(top > 0, top, 1.0))) - 7), 0.0)
 
 
-def held(y, d, least):
-    """The e4m3 value that y is held as: rounded down on the grid after the dither d (20 bits)."""
+def held(y, d, root):
+    """The e4m3 value that y is held as: one of its two neighbours on the grid, the upper one where
+    the share of the way to it, of y or (a root) of y^2, and the dither d (20 bits) come to 1. A
+    root above zero keeps the least step."""
     a = np.abs(y)
-    with np.errstate(divide="ignore"):
-        unit = 2.0 ** np.maximum(np.floor(np.log2(np.where(a > 0, a, 1e-30))) - 3, -9)
-    q = np.minimum(np.floor(a / unit + d / 2 ** 20) * unit, 448.0)
-    if least:
+    unit = 2.0 ** np.maximum(np.floor(np.log2(np.where(a > 0, a, 1e-30))) - 3, -9)
+    low = np.floor(a / unit) * unit
+    k = 2 if root else 1
+    share = (a ** k - low ** k) / ((low + unit) ** k - low ** k)
+    q = np.where(share + d / 2 ** 20 >= 1, low + unit, low)
+    if root:
         q = np.where(a > 0, np.maximum(q, 2.0 ** -9), q)
     return np.sign(y) * q

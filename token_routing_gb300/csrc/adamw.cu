@@ -54,7 +54,7 @@ struct Step {
     float rate;                        // lr / (1 - beta1^t)
     float rc2;                         // 1 / sqrt(1 - beta2^t)
     float eps, gs;
-    uint32_t dither;                   // step * the sequence's second multiplier
+    uint32_t dither;                   // the step's part of the hash
 };
 
 template <typename T>
@@ -105,17 +105,29 @@ __device__ __forceinline__ void load_codes(const uint8_t* p, int live, float sca
     }
 }
 
-// e4m3 code of y (|y| < 256 if finite) rounded down to the grid after `d` (20 bits of a grid
-// step) was added. Above 2^-6 a grid step is the 20 low bits of the fp32 mantissa, below it is
-// 2^-9. `least`: a value above zero keeps at least the smallest code.
-__device__ __forceinline__ uint8_t encode(float y, uint32_t d, bool least) {
+// e4m3 code of y (|y| < 256 if finite): one of its two neighbours on the grid, chosen by the
+// dither d (20 bits). kRoot false: up with the probability of the share of the way up, so that
+// the value is right on average. kRoot true: y is the root of a second moment, and the share is
+// taken between the squares, so that the moment is right on average (rounding the root evenly
+// would raise it: the mean of squares is above the square of the mean); a root above zero keeps
+// at least the smallest code. Above 2^-6 a grid step is 2^-3 of the leading bit, below it 2^-9.
+template <bool kRoot>
+__device__ __forceinline__ uint8_t encode(float y, uint32_t d) {
     const float a = fabsf(y);
+    const uint32_t bits = __float_as_uint(a);
     float q;
-    if (a < 0.015625f)
-        q = floorf(__fadd_rn(a * 512.f, (float)d * 9.5367431640625e-7f)) * 0.001953125f;
-    else
-        q = __uint_as_float((__float_as_uint(a) + d) & ~0xfffffu);
-    if (least && a > 0.f && q == 0.f) q = 0.001953125f;
+    if (kRoot) {
+        const bool high = a >= 0.015625f;
+        const float low = high ? __uint_as_float(bits & ~0xfffffu) : floorf(a * 512.f) * 0.001953125f;
+        const float unit = high ? __uint_as_float((bits & 0x7f800000u) - (3u << 23)) : 0.001953125f;
+        const float over = __fmul_rn(__fsub_rn(a, low), __fadd_rn(a, low));
+        const float step = __fmul_rn(unit, __fadd_rn(2.f * low, unit));
+        q = over >= __fmul_rn((float)(0x100000u - d) * 9.5367431640625e-7f, step) ? low + unit : low;
+        if (a > 0.f && q == 0.f) q = 0.001953125f;
+    } else {
+        q = a >= 0.015625f ? __uint_as_float((bits + d) & ~0xfffffu)
+                           : floorf(__fadd_rn(a * 512.f, (float)d * 9.5367431640625e-7f)) * 0.001953125f;
+    }
     q = copysignf(q, y);
     if (!finite(y)) q = NAN;                         // infinities and NaN are held as NaN
     return __nv_fp8_e4m3(q).__x;
@@ -125,8 +137,9 @@ __device__ __forceinline__ uint8_t encode(float y, uint32_t d, bool least) {
 // magnitude into [128, 256): the grid of held values then stays where it is from step to step
 // (a scale that followed the largest magnitude would move it, and re-round every value, at
 // each step), scaling is exact, and the dither's carry cannot pass 448.
-__device__ __forceinline__ void store_codes(uint8_t* p, float* scale, int live, const float (&f)[8], uint32_t i0,
-                                            uint32_t step, uint32_t flip, bool least) {
+template <bool kRoot>
+__device__ __forceinline__ void store_codes(uint8_t* p, float* scale, int live, const float (&f)[8],
+                                            const uint32_t (&hash)[8]) {
     float top = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -139,8 +152,8 @@ __device__ __forceinline__ void store_codes(uint8_t* p, float* scale, int live, 
     uint8_t b[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const uint32_t d = (((i0 + i) * 0x9E3779B1u + step) >> 12) ^ flip;
-        b[i] = encode(some ? f[i] * inv : finite(f[i]) ? 0.f : NAN, d, least);
+        const uint32_t d = (kRoot ? hash[i] * 0xC2B2AE35u : hash[i]) >> 12;
+        b[i] = encode<kRoot>(some ? f[i] * inv : finite(f[i]) ? 0.f : NAN, d);
     }
     if (live == 8) {
         *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(b);
@@ -183,8 +196,15 @@ __device__ __forceinline__ void unit(const TensorArg& t, const Step& s, int64_t 
     store8(p, live, x);
     if (t.w) store8(t.w + i0, live, x);
     if (narrow) {
-        store_codes(static_cast<uint8_t*>(t.m) + i0, t.ms + u, live, m, (uint32_t)i0, s.dither, 0u, false);
-        store_codes(static_cast<uint8_t*>(t.v) + i0, t.vs + u, live, root, (uint32_t)i0, s.dither, 0x80000u, true);
+        // one hash of element and step: its top bits dither m, those of an odd multiple v
+        uint32_t hash[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t h = ((uint32_t)i0 + i) * 0x9E3779B1u + s.dither;
+            hash[i] = (h ^ (h >> 15)) * 0x85EBCA6Bu;
+        }
+        store_codes<false>(static_cast<uint8_t*>(t.m) + i0, t.ms + u, live, m, hash);
+        store_codes<true>(static_cast<uint8_t*>(t.v) + i0, t.vs + u, live, root, hash);
     } else {
         store8(static_cast<float*>(t.m) + i0, live, m);
         store8(static_cast<float*>(t.v) + i0, live, v);
