@@ -1,7 +1,7 @@
 // Policy loss on the logits of the chosen tokens, its gradient, and token log-probabilities.
 #include <cmath>
 
-#include "internal.cuh"
+#include "tc_ptx.cuh"
 
 namespace moe {
 
@@ -10,14 +10,11 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kThreads = 512;
-
-// 2^x for the gradient: unlike ex2_approx, results below 2^-126 are not flushed to zero (in the
-// sum they are far below its rounding).
-__device__ __forceinline__ float ex2_tail(float x) {
-    float r;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
+constexpr int kMaxCluster = 8;
+constexpr int kPiece = 1024;                  // 16-byte vectors of one bulk copy
+constexpr int kMaxPieces = 8;
+// Row bytes a CTA keeps in shared memory: three CTAs of 512 threads share an SM.
+constexpr int kStageBytes = 72 * 1024;
 
 // Running maximum of the logits and sum_i 2^(k (z_i - max)), k = log2(e) / tau. The difference is
 // taken first: it is exact for near logits, however large they are. A pair whose maximum is
@@ -45,27 +42,87 @@ struct PolicyArgs {
     int* err;
 };
 
+// The 16 bytes of a vector as fp32 pairs.
+template <typename T> struct Pairs { static constexpr int N = 8 / sizeof(T); };
 template <typename T>
-__device__ __forceinline__ void add_chunk(MaxSum& a, const float (&x)[Vec16<T>::N], float k) {
-    float top = x[0];
+__device__ __forceinline__ void to_pairs(const uint4& u, uint64_t (&p)[Pairs<T>::N]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    if constexpr (sizeof(T) == 2) {
 #pragma unroll
-    for (int i = 1; i < Vec16<T>::N; ++i) top = fmaxf(top, x[i]);
+        for (int i = 0; i < 4; ++i) p[i] = pk2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    } else {
+        p[0] = pk2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+        p[1] = pk2(__uint_as_float(w[2]), __uint_as_float(w[3]));
+    }
+}
+template <typename T>
+__device__ __forceinline__ uint4 from_pairs(const uint64_t (&p)[Pairs<T>::N]) {
+    uint32_t w[4];
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float lo, hi;
+            upk2(p[i], lo, hi);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+    } else {
+        float f[4];
+        upk2(p[0], f[0], f[1]);
+        upk2(p[1], f[2], f[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(f[i]);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <typename T>
+__device__ __forceinline__ float vec_max(const uint4& u) {
+    if constexpr (sizeof(T) == 2) {
+        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
+        const __nv_bfloat162 t = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+        return fmaxf(__low2float(t), __high2float(t));
+    } else {
+        return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)), fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
+    }
+}
+
+// A thread's own running maximum, and its sum as a pair.
+struct Running {
+    float m;
+    uint64_t s;
+};
+template <typename T, int U>
+__device__ __forceinline__ void add_vecs(Running& a, const uint4 (&u)[U], float k) {
+    float top = vec_max<T>(u[0]);
+#pragma unroll
+    for (int j = 1; j < U; ++j) top = fmaxf(top, vec_max<T>(u[j]));
     if (top > a.m) {
-        a.s *= ex2_approx((a.m - top) * k);
+        const float f = ex2_approx((a.m - top) * k);
+        a.s = mul2(a.s, splat2(f));
         a.m = top;
     }
     // a row of -inf so far: measured from 0, so that -inf gives 0 and not NaN
-    const float m = a.m == -INFINITY ? 0.f : a.m;
+    const uint64_t minus = splat2(a.m == -INFINITY ? 0.f : -a.m), kk = splat2(k);
 #pragma unroll
-    for (int i = 0; i < Vec16<T>::N; ++i) a.s += ex2_approx((x[i] - m) * k);
+    for (int j = 0; j < U; ++j) {
+        uint64_t p[Pairs<T>::N];
+        to_pairs<T>(u[j], p);
+#pragma unroll
+        for (int i = 0; i < Pairs<T>::N; ++i) {
+            float x0, x1;
+            upk2(mul2(add2(p[i], minus), kk), x0, x1);
+            a.s = add2(a.s, pk2(ex2_approx(x0), ex2_approx(x1)));
+        }
+    }
 }
 
 // What one token adds: its log-probability, its term of the loss, and the factor c of its
 // gradient row c (1[v = target] - p_v).
-__device__ __forceinline__ float token_terms(const PolicyArgs& a, int t, float w, float zt, MaxSum row, float k) {
+__device__ __forceinline__ float token_terms(const PolicyArgs& a, int t, bool put, float w, float zt, MaxSum row,
+                                             float k) {
     // a row of -inf alone has no distribution
     const float lp = row.s != 0.f ? ((zt - row.m) * k - log2f(row.s)) * kLn2 : NAN;
-    if (a.logp) a.logp[t] = lp;
+    if (a.logp && put) a.logp[t] = lp;
     if (!a.advantage) return 0.f;
     const float A = a.advantage[t];
     const float r = a.old_logp ? expf(lp - a.old_logp[t]) : 1.f;
@@ -78,71 +135,204 @@ __device__ __forceinline__ float token_terms(const PolicyArgs& a, int t, float w
         l += a.kl * (u == INFINITY ? u : eu - u);
         slope -= a.kl * eu;
     }
-    if (a.tok_loss) a.tok_loss[t] = w * l;
+    if (a.tok_loss && put) a.tok_loss[t] = w * l;
     return w * slope * a.inv_tau;
 }
 
-// One block a token.
+// What the gradient of one row needs: dz = c 1[v = target] - q 2^(k (z - top)).
+struct RowGrad {
+    float c, top, q;
+    float lift;        // see grad_vec
+};
+
+// Gradient of one vector. Exponentials are computed as 2^(x + lift) with q carrying 2^-lift: the
+// fast exponential flushes results below 2^-126, and with lift = 64 what it flushes is below
+// the smallest fp32 number once multiplied by q.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) policy_kernel(PolicyArgs a, const T* logits, T* dlogits) {
+__device__ __forceinline__ uint4 grad_vec(const uint4& u, const RowGrad& g, float k) {
+    uint64_t p[Pairs<T>::N];
+    to_pairs<T>(u, p);
+    const uint64_t minus = splat2(-g.top), kk = splat2(k), lift = splat2(g.lift), q = splat2(-g.q);
+#pragma unroll
+    for (int i = 0; i < Pairs<T>::N; ++i) {
+        float x0, x1;
+        upk2(fma2(add2(p[i], minus), kk, lift), x0, x1);
+        p[i] = mul2(pk2(ex2_approx(x0), ex2_approx(x1)), q);
+    }
+    return from_pairs<T>(p);
+}
+
+template <typename T>
+__device__ __forceinline__ T grad_one(float x, const RowGrad& g, float k, bool hot) {
+    const float e = ex2_approx(fmaf(x - g.top, k, g.lift));
+    return Elem<T>::from_f(fmaf(-g.q, e, hot ? g.c : 0.f));
+}
+
+// One token to a cluster of CTAs (1, 2, 4 or 8), each with its share of the row's 16-byte
+// vectors; the first CTA also takes the elements before the first and after the last whole
+// vector. Every CTA hands its (max, sum) to all others through distributed shared memory, and
+// each computes the token's scalars for itself.
+// kStaged: the share stays in shared memory between the sum and the gradient (one reading of
+// the logits); else it is read again (log-probabilities alone, or rows past 8 x 72 KB). Both
+// take the same vectors in the same order: a token's logp has the same bits from either.
+template <typename T, bool kStaged>
+__global__ void __launch_bounds__(kThreads, 3) policy_kernel(PolicyArgs a, const T* logits, T* dlogits) {
     constexpr int N = Vec16<T>::N;
-    __shared__ MaxSum part[kThreads / 32];
-    __shared__ float sh[3];
+    extern __shared__ __align__(128) unsigned char stage[];
+    __shared__ uint64_t full[kMaxPieces];
+    __shared__ MaxSum part[kThreads / 32], peer[kMaxCluster];
+    __shared__ RowGrad row;
+    const int tid = threadIdx.x, nt = blockDim.x;
+    uint32_t rank, cs;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(cs));
+    if (kStaged && tid == 0) {
+        for (int i = 0; i < kMaxPieces; ++i) tc::mbar_init(&full[i], 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
     pdl_wait();
-    const int t = blockIdx.x;
+    const int t = blockIdx.x / cs;
     const float w = a.weight ? a.weight[t] : 1.f;
     const int target = a.target[t];
-    if (target >= a.V && w != 0.f && threadIdx.x == 0) raise_error(a.err, kErrBounds);
+    if (target >= a.V && w != 0.f && rank == 0 && tid == 0) raise_error(a.err, kErrBounds);
     const bool kept = w != 0.f && (uint32_t)target < (uint32_t)a.V;
     const T* z = logits + t * a.ld;
     T* dz = dlogits ? dlogits + t * a.ld_grad : nullptr;
     const int V = a.V;
     const int head = min(V, (int)(((16 - (reinterpret_cast<uintptr_t>(z) & 15)) & 15) / sizeof(T)));
     const int nvec = (V - head) / N;
+    const int share = (nvec + cs - 1) / cs;
+    const int v0 = min(nvec, (int)rank * share), nv = min(nvec, v0 + share) - v0;
+    const uint4* zv = reinterpret_cast<const uint4*>(z + head) + v0;
+    const int rest = rank == 0 ? V - nvec * N : 0;
+    const int odd = tid < head ? tid : nvec * N + tid;      // this thread's single element, if tid < rest
+    // 16-byte stores need the gradient's row on the same alignment as the logits' row
+    const bool wide = ((reinterpret_cast<uintptr_t>(z) ^ reinterpret_cast<uintptr_t>(dz)) & 15) == 0;
+    if (!kept) {
+        if (rank == 0 && tid == 0) {
+            if (a.logp) a.logp[t] = 0.f;
+            if (a.tok_loss) a.tok_loss[t] = 0.f;
+        }
+        if (dz) {
+            const T zero = Elem<T>::from_f(0.f);
+            if (wide) {
+                uint4* o = reinterpret_cast<uint4*>(dz + head) + v0;
+                for (int i = tid; i < nv; i += nt) o[i] = make_uint4(0u, 0u, 0u, 0u);
+            } else {
+                for (int i = tid; i < nv * N; i += nt) dz[head + v0 * N + i] = zero;
+            }
+            if (tid < rest) dz[odd] = zero;
+        }
+        return;      // every CTA of the cluster: none waits for another
+    }
+    // distributed shared memory may be written once every CTA of the cluster runs
+    if (cs > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+    if constexpr (kStaged) {
+        if (tid == 0) {
+            for (int i = 0, c = 0; i < nv; i += kPiece, ++c) {
+                const uint32_t bytes = (uint32_t)min(kPiece, nv - i) * 16u;
+                tc::mbar_expect_tx(&full[c], bytes);
+                asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                             ::"r"(tc::smem_u32(stage) + i * 16), "l"(zv + i), "r"(bytes), "r"(tc::smem_u32(&full[c]))
+                             : "memory");
+            }
+        }
+        __syncthreads();     // the barriers are set up
+    }
     const float k = a.inv_tau * kLog2e;
-    float c = 0.f, top = 0.f, q = 0.f;
-    if (kept) {
-        MaxSum acc{-INFINITY, 0.f};
-        for (int i = threadIdx.x; i < nvec; i += kThreads) {
-            float x[N];
-            const uint4 u = *reinterpret_cast<const uint4*>(z + head + (int64_t)i * N);
-            unpack16<T>(u, x);
-            add_chunk<T>(acc, x, k);
+    // read before any CTA of the cluster may write the row (dlogits may be logits)
+    const float zt = Elem<T>::to_f(z[target]);
+    const float lone = tid < rest ? Elem<T>::to_f(z[odd]) : 0.f;
+    const uint4* sv = reinterpret_cast<const uint4*>(stage);
+    Running run{-INFINITY, 0};
+    bool ok = true;
+    if constexpr (kStaged) {
+        for (int i0 = 0, c = 0; i0 < nv; i0 += kPiece, ++c) {
+            ok = ok && tc::mbar_wait(&full[c], 0, a.err);
+            const int end = min(i0 + kPiece, nv);
+            int i = i0 + tid;
+            for (; i + nt < end; i += 2 * nt) {
+                const uint4 u[2] = {sv[i], sv[i + nt]};
+                add_vecs<T, 2>(run, u, k);
+            }
+            if (i < end) {
+                const uint4 u[1] = {sv[i]};
+                add_vecs<T, 1>(run, u, k);
+            }
         }
-        const int rest = V - nvec * N;      // the unaligned head and tail
-        if ((int)threadIdx.x < rest) {
-            const int v = (int)threadIdx.x < head ? (int)threadIdx.x : head + nvec * N + ((int)threadIdx.x - head);
-            const float x = Elem<T>::to_f(z[v]);
-            acc = join(acc, MaxSum{x, x == -INFINITY ? 0.f : 1.f}, k);
+    } else {
+        int i = tid;
+        for (; i + 3 * nt < nv; i += 4 * nt) {
+            const uint4 u[2] = {zv[i], zv[i + nt]}, v[2] = {zv[i + 2 * nt], zv[i + 3 * nt]};
+            add_vecs<T, 2>(run, u, k);
+            add_vecs<T, 2>(run, v, k);
         }
+        for (; i + nt < nv; i += 2 * nt) {
+            const uint4 u[2] = {zv[i], zv[i + nt]};
+            add_vecs<T, 2>(run, u, k);
+        }
+        if (i < nv) {
+            const uint4 u[1] = {zv[i]};
+            add_vecs<T, 1>(run, u, k);
+        }
+    }
+    float s0, s1;
+    upk2(run.s, s0, s1);
+    MaxSum acc{run.m, s0 + s1};
+    if (tid < rest) acc = join(acc, MaxSum{lone, lone == -INFINITY ? 0.f : 1.f}, k);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        acc = join(acc, MaxSum{__shfl_xor_sync(0xffffffffu, acc.m, o), __shfl_xor_sync(0xffffffffu, acc.s, o)}, k);
+    if ((tid & 31) == 0) part[tid >> 5] = acc;
+    __syncthreads();
+    if (tid < 32) {
+        acc = tid < nt / 32 ? part[tid] : MaxSum{-INFINITY, 0.f};
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             acc = join(acc, MaxSum{__shfl_xor_sync(0xffffffffu, acc.m, o), __shfl_xor_sync(0xffffffffu, acc.s, o)}, k);
-        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = acc;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            for (int i = 1; i < kThreads / 32; ++i) acc = join(acc, part[i], k);
-            sh[0] = token_terms(a, t, w, Elem<T>::to_f(z[target]), acc, k);
-            sh[1] = acc.m;
-            sh[2] = acc.s;
+    }
+    if (cs > 1) {
+        asm volatile("barrier.cluster.wait;" ::: "memory");
+        if (tid < (int)cs) {
+            uint32_t to;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(tc::smem_u32(&peer[rank])), "r"(tid));
+            asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(acc.m), "f"(acc.s) : "memory");
         }
-        __syncthreads();
-        c = sh[0];
-        top = sh[1];
-        q = c / sh[2];
-    } else if (threadIdx.x == 0) {
-        if (a.logp) a.logp[t] = 0.f;
-        if (a.tok_loss) a.tok_loss[t] = 0.f;
+        asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    }
+    if (tid == 0) {
+        if (cs > 1) {
+            acc = peer[0];
+            for (uint32_t i = 1; i < cs; ++i) acc = join(acc, peer[i], k);
+        }
+        RowGrad g;
+        g.c = token_terms(a, t, rank == 0, w, zt, acc, k);
+        g.top = acc.m;
+        const float q = g.c / acc.s;
+        g.lift = fabsf(q) > 9.0949470e-13f ? 64.f : 0.f;               // 2^-40
+        g.q = g.lift != 0.f ? q * 5.4210109e-20f : q;                   // 2^-64
+        row = g;
     }
     if (!dz) return;
-    if (kept) {
-        for (int v = threadIdx.x; v < V; v += kThreads) {
-            const float e = ex2_tail((Elem<T>::to_f(z[v]) - top) * k);
-            dz[v] = Elem<T>::from_f(fmaf(-q, e, v == target ? c : 0.f));
+    __syncthreads();
+    const RowGrad g = row;
+    const int hot = target - head - v0 * N;          // the target's place in this CTA's vectors
+    const int hot_vec = hot >= 0 && hot < nv * N ? hot / N : -1;
+    for (int i = tid; i < nv; i += nt) {
+        const uint4 u = kStaged ? sv[i] : zv[i];
+        uint4 o = grad_vec<T>(u, g, k);
+        if (i == hot_vec) reinterpret_cast<T*>(&o)[hot % N] = grad_one<T>(zt, g, k, true);
+        if (wide) {
+            (reinterpret_cast<uint4*>(dz + head) + v0)[i] = o;
+        } else {
+            T* to = dz + head + (int64_t)(v0 + i) * N;
+#pragma unroll
+            for (int j = 0; j < N; ++j) to[j] = reinterpret_cast<const T*>(&o)[j];
         }
-    } else {
-        for (int v = threadIdx.x; v < V; v += kThreads) dz[v] = Elem<T>::from_f(0.f);
     }
+    if (tid < rest) dz[odd] = grad_one<T>(lone, g, k, odd == target);
+    (void)ok;            // a wait that ran out has set the error word
 }
 
 // loss = sum of the tokens' terms, one block, in a fixed order.
@@ -160,12 +350,58 @@ __global__ void __launch_bounds__(1024) policy_sum_kernel(const float* __restric
     }
 }
 
+template <typename T, bool kStaged>
+cudaError_t launch_rows(const PolicyArgs& a, int cs, int threads, size_t smem, const T* z, T* dz, cudaStream_t s) {
+    if (kStaged) {
+        const cudaError_t e = cudaFuncSetAttribute(policy_kernel<T, kStaged>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   kStageBytes);
+        if (e != cudaSuccess) return e;
+    }
+    // grids are numbered in 31 bits: a batch of more CTAs goes in several launches
+    const int rows = (1 << 30) / cs;
+    for (int64_t t0 = 0; t0 < a.T; t0 += rows) {
+        PolicyArgs b = a;
+        const int n = (int)std::min<int64_t>(rows, a.T - t0);
+        b.target += t0;
+        for (const float** p : {&b.advantage, &b.old_logp, &b.ref_logp, &b.weight})
+            if (*p) *p += t0;
+        if (b.logp) b.logp += t0;
+        if (b.tok_loss) b.tok_loss += t0;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)n * cs);
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        cudaLaunchAttribute at[2];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        at[1].id = cudaLaunchAttributeClusterDimension;
+        at[1].val.clusterDim.x = cs;
+        at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 2;
+        const cudaError_t e = launch_ex(cfg, policy_kernel<T, kStaged>, b, z + t0 * a.ld, dz ? dz + t0 * a.ld_grad : dz);
+        count_launch();
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
 template <typename T>
 cudaError_t launch_policy(const PolicyArgs& a, const void* logits, void* dlogits, cudaStream_t s) {
-    const cudaError_t e = launch_pdl(policy_kernel<T>, dim3(a.T), dim3(kThreads), 0, s, a,
-                                     static_cast<const T*>(logits), static_cast<T*>(dlogits));
-    count_launch();
-    return e;
+    const int64_t vecs = a.V / Vec16<T>::N;
+    auto share = [&](int cs) { return (vecs + cs - 1) / cs; };
+    int cs = 1;
+    while (cs < kMaxCluster && share(cs) * 16 > kStageBytes) cs *= 2;
+    // for the gradient, rows that fit the cluster's shared memory are kept there
+    const bool staged = dlogits && share(cs) * 16 <= kStageBytes;
+    // few rows: a row over more CTAs, while SMs are idle and a share is long
+    while (cs < kMaxCluster && (int64_t)a.T * cs * 2 <= num_sms() && share(cs) > 2 * kThreads) cs *= 2;
+    const int threads = share(cs) >= 2 * kThreads ? kThreads : 128;
+    const T* z = static_cast<const T*>(logits);
+    T* dz = static_cast<T*>(dlogits);
+    return staged ? launch_rows<T, true>(a, cs, threads, (size_t)share(cs) * 16, z, dz, s)
+                  : launch_rows<T, false>(a, cs, threads, 0, z, dz, s);
 }
 
 moe_status_t check_policy(const moe_policy_config_t* c) {
