@@ -118,6 +118,24 @@ def test_policy_more_rows_than_sms(T, V, moe_lib, cuda_device):
     check(moe_lib, make(T, V, "bf16"), "bf16")
 
 
+@pytest.mark.parametrize("dtype,V", [("bf16", 458752), ("bf16", 600001), ("f32", 229376), ("f32", 250003)])
+def test_policy_rows_past_shared_memory(dtype, V, moe_lib, cuda_device):
+    """The longest rows that a cluster keeps, and longer ones; also in place."""
+    check(moe_lib, make(3, V, dtype), dtype)
+    check(moe_lib, make(3, V, dtype), dtype, in_place=True)
+
+
+@pytest.mark.parametrize("V", [300, 20001, 131072, 600001])
+def test_token_logp_has_the_bits_of_the_loss(V, moe_lib, cuda_device):
+    """Log-probabilities kept from token_logp give a ratio of exactly one."""
+    s = make(40, V, "bf16")
+    c = moe_lib.make_policy_config(40, V)
+    a, b = torch.empty(40, device="cuda"), torch.empty(40, device="cuda")
+    moe_lib.token_logp(c, s["z"], s["target"], a)
+    moe_lib.policy_loss(c, s["z"], s["target"], s["adv"], a, None, None, b, None, torch.empty_like(s["z"]), None)
+    assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("kl,old,weight,tau,lo,hi", [(0.0, True, True, 1.0, 0.2, 0.2), (0.1, False, True, 0.7, 0.2, 0.3),
                                                      (0.1, True, False, 1.3, 0.1, 0.4), (0.0, False, False, 2.0, 1.0, 0.0),

@@ -9,12 +9,20 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kThreads = 512;
+constexpr int kWarps = 8;                     // warps that compute; one more warp loads
+constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCluster = 8;
-constexpr int kPiece = 1024;                  // 16-byte vectors of one bulk copy
-constexpr int kMaxPieces = 8;
-// Row bytes a CTA keeps in shared memory: three CTAs of 512 threads share an SM.
-constexpr int kStageBytes = 72 * 1024;
+constexpr int kPiece = 1024;                  // 16-byte vectors of one bulk copy: four a thread
+constexpr int kEach = kPiece / kThreads;
+constexpr int kSlots = 7;                     // pieces in a CTA's ring: 112 KB, two CTAs to an SM
+constexpr int kShare = 4;                     // pieces of a row that a CTA takes, while clusters last
+
+// What becomes of a piece of a row after its sum was taken.
+enum Reuse : int {
+    kFree = 0,      // no gradient wanted: its slot takes the next piece
+    kKeep = 1,      // it stays for the gradient: the logits are read once
+    kAgain = 2,     // the share is longer than the ring: all of its pieces come a second time
+};
 
 // Running maximum of the logits and sum_i 2^(k (z_i - max)), k = log2(e) / tau. The difference is
 // taken first: it is exact for near logits, however large they are. A pair whose maximum is
@@ -26,6 +34,14 @@ __device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b, float k) {
     const float m = fmaxf(a.m, b.m);
     if (m == -INFINITY) return {m, a.s + b.s};       // keeps a NaN sum
     return {m, a.s * ex2_approx((a.m - m) * k) + b.s * ex2_approx((b.m - m) * k)};
+}
+
+// All lanes' pairs as one, in every lane.
+__device__ __forceinline__ MaxSum warp_join(MaxSum a, float k) {
+    float m = a.m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return {m, warp_sum(m == -INFINITY ? a.s : a.s * ex2_approx((a.m - m) * k))};
 }
 
 struct PolicyArgs {
@@ -118,7 +134,7 @@ __device__ __forceinline__ void add_vecs(Running& a, const uint4 (&u)[U], float 
 
 // What one token adds: its log-probability, its term of the loss, and the factor c of its
 // gradient row c (1[v = target] - p_v).
-__device__ __forceinline__ float token_terms(const PolicyArgs& a, int t, bool put, float w, float zt, MaxSum row,
+__device__ __forceinline__ float token_terms(const PolicyArgs& a, int64_t t, bool put, float w, float zt, MaxSum row,
                                              float k) {
     // a row of -inf alone has no distribution
     const float lp = row.s != 0.f ? ((zt - row.m) * k - log2f(row.s)) * kLn2 : NAN;
@@ -168,171 +184,271 @@ __device__ __forceinline__ T grad_one(float x, const RowGrad& g, float k, bool h
     return Elem<T>::from_f(fmaf(-g.q, e, hot ? g.c : 0.f));
 }
 
-// One token to a cluster of CTAs (1, 2, 4 or 8), each with its share of the row's 16-byte
-// vectors; the first CTA also takes the elements before the first and after the last whole
-// vector. Every CTA hands its (max, sum) to all others through distributed shared memory, and
-// each computes the token's scalars for itself.
-// kStaged: the share stays in shared memory between the sum and the gradient (one reading of
-// the logits); else it is read again (log-probabilities alone, or rows past 8 x 72 KB). Both
-// take the same vectors in the same order: a token's logp has the same bits from either.
-template <typename T, bool kStaged>
-__global__ void __launch_bounds__(kThreads, 3) policy_kernel(PolicyArgs a, const T* logits, T* dlogits) {
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+
+// Phase wait whose acquire covers what the other CTAs of the cluster have written.
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, int* err) {
+    const long long t0 = clock64();
+    for (;;) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(tc::smem_u32(bar)), "r"(parity)
+            : "memory");
+        if (done) return true;
+        if (clock64() - t0 > kSpinBudgetCycles) {
+            raise_error(err, kErrTimeout);
+            return false;
+        }
+    }
+}
+
+// This CTA's part of a row: whole 16-byte vectors, shared out over the cluster; the elements
+// before the first and after the last whole vector are the first CTA's.
+template <typename T>
+struct Share {
+    const T* z;
+    int head, nvec, v0, nv, rest;
+    __device__ __forceinline__ Share(const T* row, int V, uint32_t rank, uint32_t cs) : z(row) {
+        constexpr int N = Vec16<T>::N;
+        head = min(V, (int)(((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / sizeof(T)));
+        nvec = (V - head) / N;
+        const int share = (nvec + (int)cs - 1) / (int)cs;
+        v0 = min(nvec, (int)rank * share);
+        nv = min(nvec, v0 + share) - v0;
+        rest = rank == 0 ? V - nvec * N : 0;
+    }
+    __device__ __forceinline__ const uint4* vecs() const { return reinterpret_cast<const uint4*>(z + head) + v0; }
+};
+
+// Place in the ring: the slot, and the parity of its full barrier's phase.
+struct Ring {
+    uint32_t slot = 0, phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == kSlots) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ void put_elements(T* to, const uint4& o) {
+    const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 2) {
+            reinterpret_cast<uint16_t*>(to)[2 * i] = (uint16_t)w[i];
+            reinterpret_cast<uint16_t*>(to)[2 * i + 1] = (uint16_t)(w[i] >> 16);
+        } else {
+            reinterpret_cast<uint32_t*>(to)[i] = w[i];
+        }
+    }
+}
+
+// Rows over clusters of 1, 2, 4 or 8 CTAs, two CTAs to an SM, resident for the whole batch: a
+// cluster takes every n-th row. In each CTA one warp keeps a ring of bulk copies running, rows
+// ahead of the eight that compute, so that the loads of the next row pass under the
+// reductions, the cluster's exchange and the gradient's stores of this one. Each CTA hands its
+// (max, sum) to all CTAs of the cluster by asynchronous remote stores that complete on the
+// receiver's barrier, and computes the token's scalars for itself.
+// All uses (gradient or not) take a row's vectors in the same order: a token's logp has the
+// same bits from each.
+template <typename T>
+__global__ void __launch_bounds__(kThreads + 32, 2)
+policy_ring_kernel(PolicyArgs a, const T* logits, T* dlogits, int reuse) {
     constexpr int N = Vec16<T>::N;
     extern __shared__ __align__(128) unsigned char stage[];
-    __shared__ uint64_t full[kMaxPieces];
-    __shared__ MaxSum part[kThreads / 32], peer[kMaxCluster];
+    __shared__ uint64_t full[kSlots], empty[kSlots], xbar[2];
+    __shared__ MaxSum part[kWarps];
+    __shared__ __align__(8) MaxSum peer[2][kMaxCluster];
     __shared__ RowGrad row;
-    const int tid = threadIdx.x, nt = blockDim.x;
+    const int tid = threadIdx.x, lane = tid & 31;
     uint32_t rank, cs;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(cs));
-    if (kStaged && tid == 0) {
-        for (int i = 0; i < kMaxPieces; ++i) tc::mbar_init(&full[i], 1);
+    if (tid == 0) {
+        for (int i = 0; i < kSlots; ++i) {
+            tc::mbar_init(&full[i], 1);
+            tc::mbar_init(&empty[i], kWarps);
+        }
+        tc::mbar_init(&xbar[0], 1);
+        tc::mbar_init(&xbar[1], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    __syncthreads();
+    // remote stores may come once every CTA of the cluster has its barriers
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     pdl_wait();
-    const int t = blockIdx.x / cs;
-    const float w = a.weight ? a.weight[t] : 1.f;
-    const int target = a.target[t];
-    if (target >= a.V && w != 0.f && rank == 0 && tid == 0) raise_error(a.err, kErrBounds);
-    const bool kept = w != 0.f && (uint32_t)target < (uint32_t)a.V;
-    const T* z = logits + t * a.ld;
-    T* dz = dlogits ? dlogits + t * a.ld_grad : nullptr;
-    const int V = a.V;
-    const int head = min(V, (int)(((16 - (reinterpret_cast<uintptr_t>(z) & 15)) & 15) / sizeof(T)));
-    const int nvec = (V - head) / N;
-    const int share = (nvec + cs - 1) / cs;
-    const int v0 = min(nvec, (int)rank * share), nv = min(nvec, v0 + share) - v0;
-    const uint4* zv = reinterpret_cast<const uint4*>(z + head) + v0;
-    const int rest = rank == 0 ? V - nvec * N : 0;
-    const int odd = tid < head ? tid : nvec * N + tid;      // this thread's single element, if tid < rest
-    // 16-byte stores need the gradient's row on the same alignment as the logits' row
-    const bool wide = ((reinterpret_cast<uintptr_t>(z) ^ reinterpret_cast<uintptr_t>(dz)) & 15) == 0;
-    if (!kept) {
-        if (rank == 0 && tid == 0) {
-            if (a.logp) a.logp[t] = 0.f;
-            if (a.tok_loss) a.tok_loss[t] = 0.f;
-        }
-        if (dz) {
-            const T zero = Elem<T>::from_f(0.f);
-            if (wide) {
-                uint4* o = reinterpret_cast<uint4*>(dz + head) + v0;
-                for (int i = tid; i < nv; i += nt) o[i] = make_uint4(0u, 0u, 0u, 0u);
-            } else {
-                for (int i = tid; i < nv * N; i += nt) dz[head + v0 * N + i] = zero;
-            }
-            if (tid < rest) dz[odd] = zero;
-        }
-        return;      // every CTA of the cluster: none waits for another
-    }
-    // distributed shared memory may be written once every CTA of the cluster runs
-    if (cs > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
-    if constexpr (kStaged) {
-        if (tid == 0) {
-            for (int i = 0, c = 0; i < nv; i += kPiece, ++c) {
-                const uint32_t bytes = (uint32_t)min(kPiece, nv - i) * 16u;
-                tc::mbar_expect_tx(&full[c], bytes);
-                asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                             ::"r"(tc::smem_u32(stage) + i * 16), "l"(zv + i), "r"(bytes), "r"(tc::smem_u32(&full[c]))
-                             : "memory");
-            }
-        }
-        __syncthreads();     // the barriers are set up
-    }
-    const float k = a.inv_tau * kLog2e;
-    // read before any CTA of the cluster may write the row (dlogits may be logits)
-    const float zt = Elem<T>::to_f(z[target]);
-    const float lone = tid < rest ? Elem<T>::to_f(z[odd]) : 0.f;
-    const uint4* sv = reinterpret_cast<const uint4*>(stage);
-    Running run{-INFINITY, 0};
-    bool ok = true;
-    if constexpr (kStaged) {
-        for (int i0 = 0, c = 0; i0 < nv; i0 += kPiece, ++c) {
-            ok = ok && tc::mbar_wait(&full[c], 0, a.err);
-            const int end = min(i0 + kPiece, nv);
-            int i = i0 + tid;
-            for (; i + nt < end; i += 2 * nt) {
-                const uint4 u[2] = {sv[i], sv[i + nt]};
-                add_vecs<T, 2>(run, u, k);
-            }
-            if (i < end) {
-                const uint4 u[1] = {sv[i]};
-                add_vecs<T, 1>(run, u, k);
-            }
+    const int first = blockIdx.x / cs, stride = gridDim.x / cs;
+    const auto kept_row = [&](float w, int target) { return w != 0.f && (uint32_t)target < (uint32_t)a.V; };
+
+    if (tid >= kThreads) {
+        // ---- the loading warp: looks 32 of its rows ahead for the ones that are not left out
+        Ring at;
+        bool ok = true, reused = false;
+        for (int64_t t0 = first; t0 < a.T && ok; t0 += 32LL * stride) {
+            const int64_t tl = t0 + (int64_t)lane * stride;
+            const uint32_t rows = __ballot_sync(
+                0xffffffffu, tl < a.T && kept_row(a.weight ? a.weight[tl] : 1.f, a.target[tl]));
+            if (lane == 0)
+                for (uint32_t left = rows; left && ok; left &= left - 1) {
+                    const Share<T> s(logits + (t0 + (int64_t)(__ffs(left) - 1) * stride) * a.ld, a.V, rank, cs);
+                    for (int pass = 0; pass < (reuse == kAgain ? 2 : 1); ++pass)
+                        for (int i = 0; i < s.nv && ok; i += kPiece) {
+                            const uint32_t slot = at.slot;
+                            if (reused && !tc::mbar_wait(&empty[slot], at.phase ^ 1, a.err)) {
+                                ok = false;
+                                break;
+                            }
+                            at.next();
+                            reused = reused || at.slot == 0;
+                            const uint32_t bytes = (uint32_t)min(kPiece, s.nv - i) * 16u;
+                            tc::mbar_expect_tx(&full[slot], bytes);
+                            asm volatile(
+                                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                                ::"r"(tc::smem_u32(stage) + slot * (kPiece * 16u)), "l"(s.vecs() + i), "r"(bytes),
+                                "r"(tc::smem_u32(&full[slot]))
+                                : "memory");
+                        }
+                }
+            ok = __shfl_sync(0xffffffffu, (int)ok, 0);
         }
     } else {
-        int i = tid;
-        for (; i + 3 * nt < nv; i += 4 * nt) {
-            const uint4 u[2] = {zv[i], zv[i + nt]}, v[2] = {zv[i + 2 * nt], zv[i + 3 * nt]};
-            add_vecs<T, 2>(run, u, k);
-            add_vecs<T, 2>(run, v, k);
-        }
-        for (; i + nt < nv; i += 2 * nt) {
-            const uint4 u[2] = {zv[i], zv[i + nt]};
-            add_vecs<T, 2>(run, u, k);
-        }
-        if (i < nv) {
-            const uint4 u[1] = {zv[i]};
-            add_vecs<T, 1>(run, u, k);
-        }
-    }
-    float s0, s1;
-    upk2(run.s, s0, s1);
-    MaxSum acc{run.m, s0 + s1};
-    if (tid < rest) acc = join(acc, MaxSum{lone, lone == -INFINITY ? 0.f : 1.f}, k);
+        const float k = a.inv_tau * kLog2e;
+        Ring at;
+        uint32_t turn = 0;                     // kept rows so far
+        bool ok = true;
+        for (int64_t t = first; t < a.T; t += stride) {
+            const float w = a.weight ? a.weight[t] : 1.f;
+            const int target = a.target[t];
+            const Share<T> s(logits + t * a.ld, a.V, rank, cs);
+            T* dz = dlogits ? dlogits + t * a.ld_grad : nullptr;
+            // 16-byte stores need the gradient's row on the same alignment as the logits' row
+            const bool wide = ((reinterpret_cast<uintptr_t>(s.z) ^ reinterpret_cast<uintptr_t>(dz)) & 15) == 0;
+            uint4* out = reinterpret_cast<uint4*>(dz + s.head) + s.v0;
+            const int odd = tid < s.head ? tid : s.nvec * N + tid;   // this thread's single element, if tid < rest
+            if (!kept_row(w, target)) {
+                if (rank == 0 && tid == 0) {
+                    if (w != 0.f && target >= a.V) raise_error(a.err, kErrBounds);
+                    if (a.logp) a.logp[t] = 0.f;
+                    if (a.tok_loss) a.tok_loss[t] = 0.f;
+                }
+                if (dz) {
+                    const T zero = Elem<T>::from_f(0.f);
+                    if (wide)
+                        for (int i = tid; i < s.nv; i += kThreads) out[i] = make_uint4(0u, 0u, 0u, 0u);
+                    else
+                        for (int i = tid; i < s.nv * N; i += kThreads) dz[s.head + s.v0 * N + i] = zero;
+                    if (tid < s.rest) dz[odd] = zero;
+                }
+                continue;
+            }
+            const float zt = tid == 0 ? Elem<T>::to_f(s.z[target]) : 0.f;
+            const float lone = tid < s.rest ? Elem<T>::to_f(s.z[odd]) : 0.f;
+            // ---- sum
+            Running run{-INFINITY, 0};
+            const Ring at0 = at;
+            for (int i0 = 0; i0 < s.nv; i0 += kPiece, at.next()) {
+                ok = ok && tc::mbar_wait(&full[at.slot], at.phase, a.err);
+                const uint4* v = reinterpret_cast<const uint4*>(stage + at.slot * (kPiece * 16)) + tid;
+                const int left = s.nv - i0 - tid;
+                if (left > kPiece - kThreads) {
+                    uint4 u[kEach];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        acc = join(acc, MaxSum{__shfl_xor_sync(0xffffffffu, acc.m, o), __shfl_xor_sync(0xffffffffu, acc.s, o)}, k);
-    if ((tid & 31) == 0) part[tid >> 5] = acc;
-    __syncthreads();
-    if (tid < 32) {
-        acc = tid < nt / 32 ? part[tid] : MaxSum{-INFINITY, 0.f};
+                    for (int h = 0; h < kEach; ++h) u[h] = v[h * kThreads];
+                    add_vecs<T, kEach>(run, u, k);
+                } else {
+#pragma unroll 1
+                    for (int j = 0; j < left; j += kThreads) {
+                        const uint4 u[1] = {v[j]};
+                        add_vecs<T, 1>(run, u, k);
+                    }
+                }
+                if (reuse != kKeep) {
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&empty[at.slot]);
+                }
+            }
+            float s0, s1;
+            upk2(run.s, s0, s1);
+            MaxSum acc{run.m, s0 + s1};
+            if (tid < s.rest) acc = join(acc, MaxSum{lone, lone == -INFINITY ? 0.f : 1.f}, k);
+            acc = warp_join(acc, k);
+            if (lane == 0) part[tid >> 5] = acc;
+            consumers_sync();
+            if (tid < 32) {
+                acc = warp_join(lane < kWarps ? part[lane] : MaxSum{-INFINITY, 0.f}, k);
+                if (cs > 1) {
+                    const uint32_t b = turn & 1;
+                    if (lane == 0) tc::mbar_expect_tx(&xbar[b], cs * (uint32_t)sizeof(MaxSum));
+                    // the target's logit has arrived before a peer can write over it (dlogits may be logits)
+                    asm volatile("" ::"f"(zt), "f"(lone) : "memory");
+                    if (lane < (int)cs) {
+                        uint32_t to, bar;
+                        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(tc::smem_u32(&peer[b][rank])), "r"(lane));
+                        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(bar) : "r"(tc::smem_u32(&xbar[b])), "r"(lane));
+                        asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];"
+                                     ::"r"(to), "r"(__float_as_uint(acc.m)), "r"(__float_as_uint(acc.s)), "r"(bar)
+                                     : "memory");
+                    }
+                    __syncwarp();
+                    ok = wait_cluster(&xbar[b], (turn >> 1) & 1, a.err) && ok;
+                    acc = warp_join(lane < (int)cs ? peer[b][lane] : MaxSum{-INFINITY, 0.f}, k);
+                }
+                if (lane == 0) {
+                    RowGrad g;
+                    g.c = token_terms(a, t, rank == 0, w, zt, acc, k);
+                    g.top = acc.m;
+                    const float q = g.c / acc.s;
+                    g.lift = fabsf(q) > 9.0949470e-13f ? 64.f : 0.f;               // 2^-40
+                    g.q = g.lift != 0.f ? q * 5.4210109e-20f : q;                   // 2^-64
+                    row = g;
+                }
+            }
+            ++turn;
+            consumers_sync();
+            if (!dz) continue;
+            // ---- gradient
+            const RowGrad g = row;
+            const int hot = target - s.head - s.v0 * N;      // the target's place in this CTA's vectors
+            const int hot_vec = hot >= 0 && hot < s.nv * N ? hot / N : -1;
+            if (reuse == kKeep) at = at0;
+            for (int i0 = 0; i0 < s.nv; i0 += kPiece, at.next()) {
+                if (reuse == kAgain) ok = ok && tc::mbar_wait(&full[at.slot], at.phase, a.err);
+                const uint4* v = reinterpret_cast<const uint4*>(stage + at.slot * (kPiece * 16)) + tid;
+                const int left = s.nv - i0 - tid;
+                if (wide && left > kPiece - kThreads) {
+                    uint4* o = out + i0 + tid;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            acc = join(acc, MaxSum{__shfl_xor_sync(0xffffffffu, acc.m, o), __shfl_xor_sync(0xffffffffu, acc.s, o)}, k);
-    }
-    if (cs > 1) {
-        asm volatile("barrier.cluster.wait;" ::: "memory");
-        if (tid < (int)cs) {
-            uint32_t to;
-            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(tc::smem_u32(&peer[rank])), "r"(tid));
-            asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(acc.m), "f"(acc.s) : "memory");
+                    for (int h = 0; h < kEach; ++h) o[h * kThreads] = grad_vec<T>(v[h * kThreads], g, k);
+                } else {
+#pragma unroll 1
+                    for (int j = 0; j < min(left, kPiece - tid); j += kThreads) {
+                        const uint4 o = grad_vec<T>(v[j], g, k);
+                        if (wide) out[i0 + tid + j] = o;
+                        else put_elements<T>(dz + s.head + (int64_t)(s.v0 + i0 + tid + j) * N, o);
+                    }
+                }
+                // the target's element again, by the thread that has just written its vector
+                const int mine = hot_vec - i0 - tid;
+                if (hot_vec >= 0 && mine >= 0 && mine < kPiece - tid && mine % kThreads == 0)
+                    dz[target] = grad_one<T>(Elem<T>::to_f(reinterpret_cast<const T*>(v + mine)[hot % N]), g, k, true);
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&empty[at.slot]);
+            }
+            if (tid < s.rest) dz[odd] = grad_one<T>(lone, g, k, odd == target);
         }
-        asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-        asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+        (void)ok;            // a wait that ran out has set the error word
     }
-    if (tid == 0) {
-        if (cs > 1) {
-            acc = peer[0];
-            for (uint32_t i = 1; i < cs; ++i) acc = join(acc, peer[i], k);
-        }
-        RowGrad g;
-        g.c = token_terms(a, t, rank == 0, w, zt, acc, k);
-        g.top = acc.m;
-        const float q = g.c / acc.s;
-        g.lift = fabsf(q) > 9.0949470e-13f ? 64.f : 0.f;               // 2^-40
-        g.q = g.lift != 0.f ? q * 5.4210109e-20f : q;                   // 2^-64
-        row = g;
-    }
-    if (!dz) return;
-    __syncthreads();
-    const RowGrad g = row;
-    const int hot = target - head - v0 * N;          // the target's place in this CTA's vectors
-    const int hot_vec = hot >= 0 && hot < nv * N ? hot / N : -1;
-    for (int i = tid; i < nv; i += nt) {
-        const uint4 u = kStaged ? sv[i] : zv[i];
-        uint4 o = grad_vec<T>(u, g, k);
-        if (i == hot_vec) reinterpret_cast<T*>(&o)[hot % N] = grad_one<T>(zt, g, k, true);
-        if (wide) {
-            (reinterpret_cast<uint4*>(dz + head) + v0)[i] = o;
-        } else {
-            T* to = dz + head + (int64_t)(v0 + i) * N;
-#pragma unroll
-            for (int j = 0; j < N; ++j) to[j] = reinterpret_cast<const T*>(&o)[j];
-        }
-    }
-    if (tid < rest) dz[odd] = grad_one<T>(lone, g, k, odd == target);
-    (void)ok;            // a wait that ran out has set the error word
+    // no CTA leaves while another of its cluster may still write to it
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // loss = sum of the tokens' terms, one block, in a fixed order.
@@ -350,58 +466,72 @@ __global__ void __launch_bounds__(1024) policy_sum_kernel(const float* __restric
     }
 }
 
-template <typename T, bool kStaged>
-cudaError_t launch_rows(const PolicyArgs& a, int cs, int threads, size_t smem, const T* z, T* dz, cudaStream_t s) {
-    if (kStaged) {
-        const cudaError_t e = cudaFuncSetAttribute(policy_kernel<T, kStaged>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   kStageBytes);
+// Clusters of `cs` CTAs that are resident at once (asked of the runtime once for each type and
+// size on a device).
+template <typename T>
+cudaError_t resident_clusters(int cs, size_t smem, int* out) {
+    constexpr int kMaxDevices = 64;
+    static std::mutex mu;
+    static int known[kMaxDevices][kMaxCluster + 1];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lk(mu);
+    int& n = known[dev][cs];
+    if (!n) {
+        e = cudaFuncSetAttribute(policy_ring_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
-    }
-    // grids are numbered in 31 bits: a batch of more CTAs goes in several launches
-    const int rows = (1 << 30) / cs;
-    for (int64_t t0 = 0; t0 < a.T; t0 += rows) {
-        PolicyArgs b = a;
-        const int n = (int)std::min<int64_t>(rows, a.T - t0);
-        b.target += t0;
-        for (const float** p : {&b.advantage, &b.old_logp, &b.ref_logp, &b.weight})
-            if (*p) *p += t0;
-        if (b.logp) b.logp += t0;
-        if (b.tok_loss) b.tok_loss += t0;
         cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3((unsigned)n * cs);
-        cfg.blockDim = dim3(threads);
+        cfg.gridDim = dim3(num_sms() * 2 / cs * cs);
+        cfg.blockDim = dim3(kThreads + 32);
         cfg.dynamicSmemBytes = smem;
-        cfg.stream = s;
-        cudaLaunchAttribute at[2];
-        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at[0].val.programmaticStreamSerializationAllowed = 1;
-        at[1].id = cudaLaunchAttributeClusterDimension;
-        at[1].val.clusterDim.x = cs;
-        at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = cs;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
         cfg.attrs = at;
-        cfg.numAttrs = 2;
-        const cudaError_t e = launch_ex(cfg, policy_kernel<T, kStaged>, b, z + t0 * a.ld, dz ? dz + t0 * a.ld_grad : dz);
-        count_launch();
-        if (e != cudaSuccess) return e;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&n, policy_ring_kernel<T>, &cfg);
+        if (e != cudaSuccess) {
+            n = 0;
+            return e;
+        }
+        n = std::max(n, 1);
     }
+    *out = n;
     return cudaSuccess;
 }
 
 template <typename T>
 cudaError_t launch_policy(const PolicyArgs& a, const void* logits, void* dlogits, cudaStream_t s) {
+    constexpr size_t smem = (size_t)kSlots * kPiece * 16;
     const int64_t vecs = a.V / Vec16<T>::N;
-    auto share = [&](int cs) { return (vecs + cs - 1) / cs; };
+    const auto pieces = [&](int cs) { return (vecs + (int64_t)cs * kPiece - 1) / ((int64_t)cs * kPiece); };
     int cs = 1;
-    while (cs < kMaxCluster && share(cs) * 16 > kStageBytes) cs *= 2;
-    // for the gradient, rows that fit the cluster's shared memory are kept there
-    const bool staged = dlogits && share(cs) * 16 <= kStageBytes;
-    // few rows: a row over more CTAs, while SMs are idle and a share is long
-    while (cs < kMaxCluster && (int64_t)a.T * cs * 2 <= num_sms() && share(cs) > 2 * kThreads) cs *= 2;
-    const int threads = share(cs) >= 2 * kThreads ? kThreads : 128;
-    const T* z = static_cast<const T*>(logits);
-    T* dz = static_cast<T*>(dlogits);
-    return staged ? launch_rows<T, true>(a, cs, threads, (size_t)share(cs) * 16, z, dz, s)
-                  : launch_rows<T, false>(a, cs, threads, 0, z, dz, s);
+    while (cs < kMaxCluster && pieces(cs) > kShare) cs *= 2;
+    // few rows: a row over more CTAs, while SMs are idle and a share is longer than a piece
+    while (cs < kMaxCluster && (int64_t)a.T * cs * 2 <= num_sms() && pieces(cs) > 1) cs *= 2;
+    const int reuse = !dlogits ? kFree : pieces(cs) <= kSlots ? kKeep : kAgain;
+    int clusters = 0;
+    cudaError_t e = resident_clusters<T>(cs, smem, &clusters);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)std::min(a.T, clusters) * cs);
+    cfg.blockDim = dim3(kThreads + 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cs;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    e = launch_ex(cfg, policy_ring_kernel<T>, a, static_cast<const T*>(logits), static_cast<T*>(dlogits), reuse);
+    count_launch();
+    return e;
 }
 
 moe_status_t check_policy(const moe_policy_config_t* c) {
