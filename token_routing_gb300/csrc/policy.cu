@@ -12,9 +12,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kWarps = 8;                     // warps that compute; one more warp loads
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCluster = 8;
-constexpr int kPiece = 1024;                  // 16-byte vectors of one bulk copy: four a thread
-constexpr int kEach = kPiece / kThreads;
-constexpr int kSlots = 7;                     // pieces in a CTA's ring: 112 KB, two CTAs to an SM
+constexpr int kEach = 4;                      // 16-byte vectors of a piece to a thread
+constexpr int kPiece = kEach * kThreads;      // vectors of one bulk copy: 16 KB
+constexpr int kSlots = 6;                     // pieces in a CTA's ring: two CTAs to an SM
 constexpr int kShare = 4;                     // pieces of a row that a CTA takes, while clusters last
 
 // What becomes of a piece of a row after its sum was taken.
@@ -132,27 +132,33 @@ __device__ __forceinline__ void add_vecs(Running& a, const uint4 (&u)[U], float 
     }
 }
 
-// What one token adds: its log-probability, its term of the loss, and the factor c of its
-// gradient row c (1[v = target] - p_v).
-__device__ __forceinline__ float token_terms(const PolicyArgs& a, int64_t t, bool put, float w, float zt, MaxSum row,
-                                             float k) {
+// One row's scalars, as the loading warp hands them to the computing warps.
+struct Row {
+    int t;             // token, or -1 past the last
+    int target;
+    float w;           // 0: left out
+    float zt, adv, old, ref;
+};
+
+// What one token adds: its log-probability and its term of the loss (written if `put`), and the
+// factor c of its gradient row c (1[v = target] - p_v).
+__device__ __forceinline__ float token_terms(const PolicyArgs& a, const Row& r, bool put, MaxSum row, float k) {
     // a row of -inf alone has no distribution
-    const float lp = row.s != 0.f ? ((zt - row.m) * k - log2f(row.s)) * kLn2 : NAN;
-    if (a.logp && put) a.logp[t] = lp;
+    const float lp = row.s != 0.f ? ((r.zt - row.m) * k - log2f(row.s)) * kLn2 : NAN;
+    if (a.logp && put) a.logp[r.t] = lp;
     if (!a.advantage) return 0.f;
-    const float A = a.advantage[t];
-    const float r = a.old_logp ? expf(lp - a.old_logp[t]) : 1.f;
-    const float un = r * A, cl = fminf(fmaxf(r, 1.f - a.clip_low), 1.f + a.clip_high) * A;
+    const float ratio = a.old_logp ? expf(lp - r.old) : 1.f;
+    const float un = ratio * r.adv, cl = fminf(fmaxf(ratio, 1.f - a.clip_low), 1.f + a.clip_high) * r.adv;
     float l = -fminf(un, cl);
     float slope = un <= cl ? -un : 0.f;
     if (lp != lp) l = slope = lp;
     if (a.kl != 0.f) {
-        const float u = a.ref_logp[t] - lp, eu = expm1f(u);
+        const float u = r.ref - lp, eu = expm1f(u);
         l += a.kl * (u == INFINITY ? u : eu - u);
         slope -= a.kl * eu;
     }
-    if (a.tok_loss && put) a.tok_loss[t] = w * l;
-    return w * slope * a.inv_tau;
+    if (a.tok_loss && put) a.tok_loss[r.t] = r.w * l;
+    return r.w * slope * a.inv_tau;
 }
 
 // What the gradient of one row needs: dz = c 1[v = target] - q 2^(k (z - top)).
@@ -183,8 +189,6 @@ __device__ __forceinline__ T grad_one(float x, const RowGrad& g, float k, bool h
     const float e = ex2_approx(fmaf(x - g.top, k, g.lift));
     return Elem<T>::from_f(fmaf(-g.q, e, hot ? g.c : 0.f));
 }
-
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
 
 // Phase wait whose acquire covers what the other CTAs of the cluster have written.
 __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, int* err) {
@@ -224,14 +228,24 @@ struct Share {
     __device__ __forceinline__ const uint4* vecs() const { return reinterpret_cast<const uint4*>(z + head) + v0; }
 };
 
-// Place in the ring: the slot, and the parity of its full barrier's phase.
+// Place in a ring of SLOTS: the slot, the parity of its barrier's phase, and whether it was used before.
+template <int SLOTS>
 struct Ring {
-    uint32_t slot = 0, phase = 0;
+    int slot = 0;
+    uint32_t phase = 0;
+    bool again = false;
     __device__ __forceinline__ void next() {
-        if (++slot == kSlots) {
+        if (++slot == SLOTS) {
             slot = 0;
             phase ^= 1;
+            again = true;
         }
+    }
+    __device__ __forceinline__ void from(int src) {      // as lane src has it
+        const uint32_t all = __shfl_sync(0xffffffffu, (uint32_t)slot | phase << 8 | (uint32_t)again << 9, src);
+        slot = all & 255;
+        phase = all >> 8 & 1;
+        again = all >> 9;
     }
 };
 
@@ -249,12 +263,16 @@ __device__ __forceinline__ void put_elements(T* to, const uint4& o) {
     }
 }
 
-// Rows over clusters of 1, 2, 4 or 8 CTAs, two CTAs to an SM, resident for the whole batch: a
-// cluster takes every n-th row. In each CTA one warp keeps a ring of bulk copies running, rows
-// ahead of the eight that compute, so that the loads of the next row pass under the
-// reductions, the cluster's exchange and the gradient's stores of this one. Each CTA hands its
-// (max, sum) to all CTAs of the cluster by asynchronous remote stores that complete on the
-// receiver's barrier, and computes the token's scalars for itself.
+constexpr int kRows = 8;        // rows handed over and not yet taken
+
+// Rows over clusters of 1, 2, 4 or 8 CTAs, two CTAs to an SM, resident for the whole batch. In
+// each CTA one warp keeps a ring of bulk copies running, rows ahead of the eight that compute,
+// so that the loads of the next rows pass under this row's reductions, exchange and stores. The
+// rows that are not left out are dealt out evenly, and so are the others, whose gradient is
+// only zeroed.
+// The eight warps of a CTA never meet at a barrier: each sends the (max, sum) of its vectors to
+// every CTA of the cluster by an asynchronous remote store that completes on the receiver's
+// barrier, waits there for all of them, and works out the token's scalars for itself.
 // All uses (gradient or not) take a row's vectors in the same order: a token's logp has the
 // same bits from each.
 template <typename T>
@@ -262,11 +280,10 @@ __global__ void __launch_bounds__(kThreads + 32, 2)
 policy_ring_kernel(PolicyArgs a, const T* logits, T* dlogits, int reuse) {
     constexpr int N = Vec16<T>::N;
     extern __shared__ __align__(128) unsigned char stage[];
-    __shared__ uint64_t full[kSlots], empty[kSlots], xbar[2];
-    __shared__ MaxSum part[kWarps];
-    __shared__ __align__(8) MaxSum peer[2][kMaxCluster];
-    __shared__ RowGrad row;
-    const int tid = threadIdx.x, lane = tid & 31;
+    __shared__ uint64_t full[kSlots], empty[kSlots], given[kRows], taken[kRows], xbar[2];
+    __shared__ __align__(8) MaxSum peer[2][kMaxCluster * kWarps];
+    __shared__ Row rows[kRows];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint32_t rank, cs;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(cs));
@@ -274,6 +291,10 @@ policy_ring_kernel(PolicyArgs a, const T* logits, T* dlogits, int reuse) {
         for (int i = 0; i < kSlots; ++i) {
             tc::mbar_init(&full[i], 1);
             tc::mbar_init(&empty[i], kWarps);
+        }
+        for (int i = 0; i < kRows; ++i) {
+            tc::mbar_init(&given[i], 1);
+            tc::mbar_init(&taken[i], kWarps);
         }
         tc::mbar_init(&xbar[0], 1);
         tc::mbar_init(&xbar[1], 1);
@@ -284,59 +305,134 @@ policy_ring_kernel(PolicyArgs a, const T* logits, T* dlogits, int reuse) {
     asm volatile("barrier.cluster.arrive.release;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     pdl_wait();
-    const int first = blockIdx.x / cs, stride = gridDim.x / cs;
-    const auto kept_row = [&](float w, int target) { return w != 0.f && (uint32_t)target < (uint32_t)a.V; };
 
-    if (tid >= kThreads) {
-        // ---- the loading warp: looks 32 of its rows ahead for the ones that are not left out
-        Ring at;
-        bool ok = true, reused = false;
-        for (int64_t t0 = first; t0 < a.T && ok; t0 += 32LL * stride) {
-            const int64_t tl = t0 + (int64_t)lane * stride;
-            const uint32_t rows = __ballot_sync(
-                0xffffffffu, tl < a.T && kept_row(a.weight ? a.weight[tl] : 1.f, a.target[tl]));
-            if (lane == 0)
-                for (uint32_t left = rows; left && ok; left &= left - 1) {
-                    const Share<T> s(logits + (t0 + (int64_t)(__ffs(left) - 1) * stride) * a.ld, a.V, rank, cs);
-                    for (int pass = 0; pass < (reuse == kAgain ? 2 : 1); ++pass)
-                        for (int i = 0; i < s.nv && ok; i += kPiece) {
-                            const uint32_t slot = at.slot;
-                            if (reused && !tc::mbar_wait(&empty[slot], at.phase ^ 1, a.err)) {
-                                ok = false;
-                                break;
-                            }
-                            at.next();
-                            reused = reused || at.slot == 0;
-                            const uint32_t bytes = (uint32_t)min(kPiece, s.nv - i) * 16u;
-                            tc::mbar_expect_tx(&full[slot], bytes);
-                            asm volatile(
-                                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                                ::"r"(tc::smem_u32(stage) + slot * (kPiece * 16u)), "l"(s.vecs() + i), "r"(bytes),
-                                "r"(tc::smem_u32(&full[slot]))
-                                : "memory");
-                        }
+    if (warp == kWarps) {
+        // ---- the loading warp
+        const uint32_t clusters = gridDim.x / cs, mine = blockIdx.x / cs;
+        uint32_t dealt_kept = 0, dealt_out = 0;        // rows of each sort so far, modulo the clusters
+        Ring<kSlots> at;
+        Ring<kRows> to;
+        bool ok = true;
+        constexpr int kAhead = 4;
+        float w[kAhead], w_next[kAhead];
+        int target[kAhead], target_next[kAhead];
+        const auto look = [&](int64_t t0) {
+#pragma unroll
+            for (int h = 0; h < kAhead; ++h) {
+                const int64_t t = t0 + 32 * h + lane;
+                w_next[h] = t < a.T && a.weight ? a.weight[t] : 1.f;
+                target_next[h] = t < a.T ? a.target[t] : -1;
+            }
+        };
+        look(0);
+        for (int64_t t0 = 0; t0 < a.T && ok; t0 += 32 * kAhead) {
+#pragma unroll
+            for (int h = 0; h < kAhead; ++h) {
+                w[h] = w_next[h];
+                target[h] = target_next[h];
+            }
+            look(t0 + 32 * kAhead);      // in flight while these rows are dealt out
+#pragma unroll
+            for (int h = 0; h < kAhead; ++h) {
+                const int64_t t = t0 + 32 * h + lane;
+                if (t0 + 32 * h >= a.T) break;
+                const bool kept = w[h] != 0.f && (uint32_t)target[h] < (uint32_t)a.V;
+                const uint32_t all = __ballot_sync(0xffffffffu, t < a.T), in = __ballot_sync(0xffffffffu, kept);
+                const uint32_t before = (1u << lane) - 1u, same = kept ? in : all & ~in;
+                const bool me = t < a.T && ((kept ? dealt_kept : dealt_out) + __popc(same & before)) % clusters == mine;
+                dealt_kept = (dealt_kept + __popc(in)) % clusters;
+                dealt_out = (dealt_out + __popc(all & ~in)) % clusters;
+                Row r{(int)t, target[h], kept ? w[h] : 0.f, 0.f, 0.f, 0.f, 0.f};
+                if (me && kept) {
+                    // here, before a CTA of the cluster may write the row (dlogits may be logits)
+                    r.zt = Elem<T>::to_f(logits[t * a.ld + r.target]);
+                    if (a.advantage) r.adv = a.advantage[t];
+                    if (a.old_logp) r.old = a.old_logp[t];
+                    if (a.kl != 0.f) r.ref = a.ref_logp[t];
                 }
-            ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+                if (me && !kept && w[h] != 0.f && target[h] >= a.V) raise_error(a.err, kErrBounds);
+                for (uint32_t left = __ballot_sync(0xffffffffu, me); left && ok; left &= left - 1) {
+                    if (lane == __ffs(left) - 1) {
+                        ok = !to.again || tc::mbar_wait(&taken[to.slot], to.phase ^ 1, a.err);
+                        if (ok) {
+                            rows[to.slot] = r;
+                            tc::mbar_arrive(&given[to.slot]);
+                        }
+                        const Share<T> s(logits + t * a.ld, a.V, rank, cs);
+                        for (int pass = kept ? reuse == kAgain ? 0 : 1 : 2; pass < 2; ++pass)
+                            for (int i = 0; i < s.nv && ok; i += kPiece) {
+                                ok = !at.again || tc::mbar_wait(&empty[at.slot], at.phase ^ 1, a.err);
+                                if (!ok) break;
+                                const uint32_t bytes = (uint32_t)min(kPiece, s.nv - i) * 16u;
+                                tc::mbar_expect_tx(&full[at.slot], bytes);
+                                asm volatile(
+                                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                                    ::"r"(tc::smem_u32(stage) + at.slot * (kPiece * 16u)), "l"(s.vecs() + i), "r"(bytes),
+                                    "r"(tc::smem_u32(&full[at.slot]))
+                                    : "memory");
+                                at.next();
+                            }
+                    }
+                    const int src = __ffs(left) - 1;
+                    ok = __shfl_sync(0xffffffffu, (int)ok, src);
+                    at.from(src);
+                    to.next();
+                }
+            }
+        }
+        if (lane == 0 && ok && (!to.again || tc::mbar_wait(&taken[to.slot], to.phase ^ 1, a.err))) {
+            rows[to.slot] = Row{-1, 0, 0.f, 0.f, 0.f, 0.f, 0.f};
+            tc::mbar_arrive(&given[to.slot]);
         }
     } else {
         const float k = a.inv_tau * kLog2e;
-        Ring at;
+        Ring<kSlots> at;
+        Ring<kRows> from;
         uint32_t turn = 0;                     // kept rows so far
         bool ok = true;
-        for (int64_t t = first; t < a.T; t += stride) {
-            const float w = a.weight ? a.weight[t] : 1.f;
-            const int target = a.target[t];
-            const Share<T> s(logits + t * a.ld, a.V, rank, cs);
-            T* dz = dlogits ? dlogits + t * a.ld_grad : nullptr;
+        Row before{};
+        // A warp's pair to every CTA of the cluster; all pairs of the cluster as one. The two
+        // buffers suffice: whoever sends for a row has received all pairs of the row before it,
+        // whose senders have read those of the row before that.
+        const auto send = [&](MaxSum acc, uint32_t row) {
+            const uint32_t b = row & 1;
+            if (tid == 0) tc::mbar_expect_tx(&xbar[b], cs * kWarps * (uint32_t)sizeof(MaxSum));
+            if (lane < (int)cs) {
+                uint32_t to, bar;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                             : "=r"(to) : "r"(tc::smem_u32(&peer[b][rank * kWarps + warp])), "r"(lane));
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(bar) : "r"(tc::smem_u32(&xbar[b])), "r"(lane));
+                asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];"
+                             ::"r"(to), "r"(__float_as_uint(acc.m)), "r"(__float_as_uint(acc.s)), "r"(bar)
+                             : "memory");
+            }
+            __syncwarp();
+        };
+        const auto receive = [&](uint32_t row) {
+            const uint32_t b = row & 1;
+            ok = wait_cluster(&xbar[b], (row >> 1) & 1, a.err) && ok;
+            const int n = (int)cs * kWarps;
+            MaxSum acc = lane < n ? peer[b][lane] : MaxSum{-INFINITY, 0.f};
+            if (lane + 32 < n) acc = join(acc, peer[b][lane + 32], k);
+            return warp_join(acc, k);
+        };
+        while (ok) {
+            if (!tc::mbar_wait(&given[from.slot], from.phase, a.err)) break;
+            const Row r = rows[from.slot];
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&taken[from.slot]);
+            from.next();
+            if (r.t < 0) break;
+            const Share<T> s(logits + r.t * a.ld, a.V, rank, cs);
+            T* dz = dlogits ? dlogits + r.t * a.ld_grad : nullptr;
             // 16-byte stores need the gradient's row on the same alignment as the logits' row
             const bool wide = ((reinterpret_cast<uintptr_t>(s.z) ^ reinterpret_cast<uintptr_t>(dz)) & 15) == 0;
             uint4* out = reinterpret_cast<uint4*>(dz + s.head) + s.v0;
             const int odd = tid < s.head ? tid : s.nvec * N + tid;   // this thread's single element, if tid < rest
-            if (!kept_row(w, target)) {
+            if (r.w == 0.f) {
                 if (rank == 0 && tid == 0) {
-                    if (w != 0.f && target >= a.V) raise_error(a.err, kErrBounds);
-                    if (a.logp) a.logp[t] = 0.f;
-                    if (a.tok_loss) a.tok_loss[t] = 0.f;
+                    if (a.logp) a.logp[r.t] = 0.f;
+                    if (a.tok_loss) a.tok_loss[r.t] = 0.f;
                 }
                 if (dz) {
                     const T zero = Elem<T>::from_f(0.f);
@@ -348,16 +444,15 @@ policy_ring_kernel(PolicyArgs a, const T* logits, T* dlogits, int reuse) {
                 }
                 continue;
             }
-            const float zt = tid == 0 ? Elem<T>::to_f(s.z[target]) : 0.f;
             const float lone = tid < s.rest ? Elem<T>::to_f(s.z[odd]) : 0.f;
             // ---- sum
             Running run{-INFINITY, 0};
-            const Ring at0 = at;
+            const Ring<kSlots> at0 = at;
             for (int i0 = 0; i0 < s.nv; i0 += kPiece, at.next()) {
                 ok = ok && tc::mbar_wait(&full[at.slot], at.phase, a.err);
                 const uint4* v = reinterpret_cast<const uint4*>(stage + at.slot * (kPiece * 16)) + tid;
-                const int left = s.nv - i0 - tid;
-                if (left > kPiece - kThreads) {
+                const int left = min(kPiece, s.nv - i0) - tid;
+                if (left + lane > 31 + (kEach - 1) * kThreads) {          // all of the warp's vectors
                     uint4 u[kEach];
 #pragma unroll
                     for (int h = 0; h < kEach; ++h) u[h] = v[h * kThreads];
@@ -379,71 +474,55 @@ policy_ring_kernel(PolicyArgs a, const T* logits, T* dlogits, int reuse) {
             MaxSum acc{run.m, s0 + s1};
             if (tid < s.rest) acc = join(acc, MaxSum{lone, lone == -INFINITY ? 0.f : 1.f}, k);
             acc = warp_join(acc, k);
-            if (lane == 0) part[tid >> 5] = acc;
-            consumers_sync();
-            if (tid < 32) {
-                acc = warp_join(lane < kWarps ? part[lane] : MaxSum{-INFINITY, 0.f}, k);
-                if (cs > 1) {
-                    const uint32_t b = turn & 1;
-                    if (lane == 0) tc::mbar_expect_tx(&xbar[b], cs * (uint32_t)sizeof(MaxSum));
-                    // the target's logit has arrived before a peer can write over it (dlogits may be logits)
-                    asm volatile("" ::"f"(zt), "f"(lone) : "memory");
-                    if (lane < (int)cs) {
-                        uint32_t to, bar;
-                        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(tc::smem_u32(&peer[b][rank])), "r"(lane));
-                        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(bar) : "r"(tc::smem_u32(&xbar[b])), "r"(lane));
-                        asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];"
-                                     ::"r"(to), "r"(__float_as_uint(acc.m)), "r"(__float_as_uint(acc.s)), "r"(bar)
-                                     : "memory");
-                    }
-                    __syncwarp();
-                    ok = wait_cluster(&xbar[b], (turn >> 1) & 1, a.err) && ok;
-                    acc = warp_join(lane < (int)cs ? peer[b][lane] : MaxSum{-INFINITY, 0.f}, k);
-                }
-                if (lane == 0) {
-                    RowGrad g;
-                    g.c = token_terms(a, t, rank == 0, w, zt, acc, k);
-                    g.top = acc.m;
-                    const float q = g.c / acc.s;
-                    g.lift = fabsf(q) > 9.0949470e-13f ? 64.f : 0.f;               // 2^-40
-                    g.q = g.lift != 0.f ? q * 5.4210109e-20f : q;                   // 2^-64
-                    row = g;
-                }
+            // ---- exchange
+            if (reuse == kFree) {
+                // nothing of this row waits for its sum: the row before it is finished now, its
+                // exchange having passed under this row's work
+                if (turn) token_terms(a, before, rank == 0 && tid == 0, receive(turn - 1), k);
+                before = r;
+                send(acc, turn++);
+                continue;
             }
-            ++turn;
-            consumers_sync();
-            if (!dz) continue;
+            send(acc, turn);
+            acc = receive(turn++);
+            RowGrad g;
+            g.c = token_terms(a, r, rank == 0 && tid == 0, acc, k);
+            g.top = acc.m;
+            const float q = g.c / acc.s;
+            g.lift = fabsf(q) > 9.0949470e-13f ? 64.f : 0.f;               // 2^-40
+            g.q = g.lift != 0.f ? q * 5.4210109e-20f : q;                   // 2^-64
             // ---- gradient
-            const RowGrad g = row;
-            const int hot = target - s.head - s.v0 * N;      // the target's place in this CTA's vectors
+            const int hot = r.target - s.head - s.v0 * N;    // the target's place in this CTA's vectors
             const int hot_vec = hot >= 0 && hot < s.nv * N ? hot / N : -1;
             if (reuse == kKeep) at = at0;
             for (int i0 = 0; i0 < s.nv; i0 += kPiece, at.next()) {
                 if (reuse == kAgain) ok = ok && tc::mbar_wait(&full[at.slot], at.phase, a.err);
                 const uint4* v = reinterpret_cast<const uint4*>(stage + at.slot * (kPiece * 16)) + tid;
-                const int left = s.nv - i0 - tid;
-                if (wide && left > kPiece - kThreads) {
-                    uint4* o = out + i0 + tid;
+                const int left = min(kPiece, s.nv - i0) - tid;
+                uint4* o = out + i0 + tid;
+                if (wide && left + lane > 31 + (kEach - 1) * kThreads) {
 #pragma unroll
                     for (int h = 0; h < kEach; ++h) o[h * kThreads] = grad_vec<T>(v[h * kThreads], g, k);
+                } else if (wide) {
+#pragma unroll
+                    for (int h = 0; h < kEach; ++h)
+                        if (h * kThreads < left) o[h * kThreads] = grad_vec<T>(v[h * kThreads], g, k);
                 } else {
 #pragma unroll 1
-                    for (int j = 0; j < min(left, kPiece - tid); j += kThreads) {
-                        const uint4 o = grad_vec<T>(v[j], g, k);
-                        if (wide) out[i0 + tid + j] = o;
-                        else put_elements<T>(dz + s.head + (int64_t)(s.v0 + i0 + tid + j) * N, o);
+                    for (int j = 0; j < left; j += kThreads) {
+                        put_elements<T>(dz + s.head + (int64_t)(s.v0 + i0 + tid + j) * N, grad_vec<T>(v[j], g, k));
                     }
                 }
                 // the target's element again, by the thread that has just written its vector
-                const int mine = hot_vec - i0 - tid;
-                if (hot_vec >= 0 && mine >= 0 && mine < kPiece - tid && mine % kThreads == 0)
-                    dz[target] = grad_one<T>(Elem<T>::to_f(reinterpret_cast<const T*>(v + mine)[hot % N]), g, k, true);
+                const int hit = hot_vec - i0 - tid;
+                if (hot_vec >= 0 && hit >= 0 && hit < left && hit % kThreads == 0)
+                    dz[r.target] = grad_one<T>(r.zt, g, k, true);
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&empty[at.slot]);
             }
-            if (tid < s.rest) dz[odd] = grad_one<T>(lone, g, k, odd == target);
+            if (tid < s.rest) dz[odd] = grad_one<T>(lone, g, k, odd == r.target);
         }
-        (void)ok;            // a wait that ran out has set the error word
+        if (reuse == kFree && turn && ok) token_terms(a, before, rank == 0 && tid == 0, receive(turn - 1), k);
     }
     // no CTA leaves while another of its cluster may still write to it
     __syncwarp();
