@@ -132,17 +132,22 @@ __device__ __forceinline__ void add_vecs(Running& a, const uint4 (&u)[U], float 
     }
 }
 
-// One row's scalars, as the loading warp hands them to the computing warps.
+// A row, as the loading warp hands it to the computing warps.
 struct Row {
     int t;             // token, or -1 past the last
     int target;
     float w;           // 0: left out
-    float zt, adv, old, ref;
+};
+
+// A kept row's scalars, loaded when its work begins.
+struct Token {
+    int t;
+    float w, zt, adv, old, ref;
 };
 
 // What one token adds: its log-probability and its term of the loss (written if `put`), and the
 // factor c of its gradient row c (1[v = target] - p_v).
-__device__ __forceinline__ float token_terms(const PolicyArgs& a, const Row& r, bool put, MaxSum row, float k) {
+__device__ __forceinline__ float token_terms(const PolicyArgs& a, const Token& r, bool put, MaxSum row, float k) {
     // a row of -inf alone has no distribution
     const float lp = row.s != 0.f ? ((r.zt - row.m) * k - log2f(row.s)) * kLn2 : NAN;
     if (a.logp && put) a.logp[r.t] = lp;
@@ -309,7 +314,7 @@ policy_ring_kernel(PolicyArgs a, const T* logits, T* dlogits, int reuse) {
     if (warp == kWarps) {
         // ---- the loading warp
         const uint32_t clusters = gridDim.x / cs, mine = blockIdx.x / cs;
-        uint32_t dealt_kept = 0, dealt_out = 0;        // rows of each sort so far, modulo the clusters
+        uint32_t skip_kept = mine, skip_out = mine;    // rows of each sort before the next that is dealt here
         Ring<kSlots> at;
         Ring<kRows> to;
         bool ok = true;
@@ -338,24 +343,24 @@ policy_ring_kernel(PolicyArgs a, const T* logits, T* dlogits, int reuse) {
                 if (t0 + 32 * h >= a.T) break;
                 const bool kept = w[h] != 0.f && (uint32_t)target[h] < (uint32_t)a.V;
                 const uint32_t all = __ballot_sync(0xffffffffu, t < a.T), in = __ballot_sync(0xffffffffu, kept);
-                const uint32_t before = (1u << lane) - 1u, same = kept ? in : all & ~in;
-                const bool me = t < a.T && ((kept ? dealt_kept : dealt_out) + __popc(same & before)) % clusters == mine;
-                dealt_kept = (dealt_kept + __popc(in)) % clusters;
-                dealt_out = (dealt_out + __popc(all & ~in)) % clusters;
-                Row r{(int)t, target[h], kept ? w[h] : 0.f, 0.f, 0.f, 0.f, 0.f};
-                if (me && kept) {
-                    // here, before a CTA of the cluster may write the row (dlogits may be logits)
-                    r.zt = Elem<T>::to_f(logits[t * a.ld + r.target]);
-                    if (a.advantage) r.adv = a.advantage[t];
-                    if (a.old_logp) r.old = a.old_logp[t];
-                    if (a.kl != 0.f) r.ref = a.ref_logp[t];
+                const uint32_t kept_here = __popc(in), out_here = __popc(all & ~in);
+                if (skip_kept >= kept_here && skip_out >= out_here) {
+                    skip_kept -= kept_here;
+                    skip_out -= out_here;
+                    continue;
                 }
+                const uint32_t before = __popc((kept ? in : all & ~in) & ((1u << lane) - 1u)), skip = kept ? skip_kept : skip_out;
+                const bool me = t < a.T && before >= skip && (before - skip) % clusters == 0;
+                while (skip_kept < kept_here) skip_kept += clusters;
+                while (skip_out < out_here) skip_out += clusters;
+                skip_kept -= kept_here;
+                skip_out -= out_here;
                 if (me && !kept && w[h] != 0.f && target[h] >= a.V) raise_error(a.err, kErrBounds);
                 for (uint32_t left = __ballot_sync(0xffffffffu, me); left && ok; left &= left - 1) {
                     if (lane == __ffs(left) - 1) {
                         ok = !to.again || tc::mbar_wait(&taken[to.slot], to.phase ^ 1, a.err);
                         if (ok) {
-                            rows[to.slot] = r;
+                            rows[to.slot] = Row{(int)t, target[h], kept ? w[h] : 0.f};
                             tc::mbar_arrive(&given[to.slot]);
                         }
                         const Share<T> s(logits + t * a.ld, a.V, rank, cs);
@@ -381,7 +386,7 @@ policy_ring_kernel(PolicyArgs a, const T* logits, T* dlogits, int reuse) {
             }
         }
         if (lane == 0 && ok && (!to.again || tc::mbar_wait(&taken[to.slot], to.phase ^ 1, a.err))) {
-            rows[to.slot] = Row{-1, 0, 0.f, 0.f, 0.f, 0.f, 0.f};
+            rows[to.slot] = Row{-1, 0, 0.f};
             tc::mbar_arrive(&given[to.slot]);
         }
     } else {
@@ -390,7 +395,7 @@ policy_ring_kernel(PolicyArgs a, const T* logits, T* dlogits, int reuse) {
         Ring<kRows> from;
         uint32_t turn = 0;                     // kept rows so far
         bool ok = true;
-        Row before{};
+        Token before{};
         // A warp's pair to every CTA of the cluster; all pairs of the cluster as one. The two
         // buffers suffice: whoever sends for a row has received all pairs of the row before it,
         // whose senders have read those of the row before that.
@@ -444,6 +449,10 @@ policy_ring_kernel(PolicyArgs a, const T* logits, T* dlogits, int reuse) {
                 }
                 continue;
             }
+            Token x{r.t, r.w, Elem<T>::to_f(s.z[r.target]), 0.f, 0.f, 0.f};
+            if (a.advantage) x.adv = a.advantage[r.t];
+            if (a.old_logp) x.old = a.old_logp[r.t];
+            if (a.kl != 0.f) x.ref = a.ref_logp[r.t];
             const float lone = tid < s.rest ? Elem<T>::to_f(s.z[odd]) : 0.f;
             // ---- sum
             Running run{-INFINITY, 0};
@@ -474,19 +483,21 @@ policy_ring_kernel(PolicyArgs a, const T* logits, T* dlogits, int reuse) {
             MaxSum acc{run.m, s0 + s1};
             if (tid < s.rest) acc = join(acc, MaxSum{lone, lone == -INFINITY ? 0.f : 1.f}, k);
             acc = warp_join(acc, k);
-            // ---- exchange
+            // ---- exchange. What this warp reads of the row itself has arrived: once all warps have
+            // sent, any of them may write over it (dlogits may be logits)
+            asm volatile("" ::"f"(x.zt), "f"(lone) : "memory");
             if (reuse == kFree) {
                 // nothing of this row waits for its sum: the row before it is finished now, its
                 // exchange having passed under this row's work
                 if (turn) token_terms(a, before, rank == 0 && tid == 0, receive(turn - 1), k);
-                before = r;
+                before = x;
                 send(acc, turn++);
                 continue;
             }
             send(acc, turn);
             acc = receive(turn++);
             RowGrad g;
-            g.c = token_terms(a, r, rank == 0 && tid == 0, acc, k);
+            g.c = token_terms(a, x, rank == 0 && tid == 0, acc, k);
             g.top = acc.m;
             const float q = g.c / acc.s;
             g.lift = fabsf(q) > 9.0949470e-13f ? 64.f : 0.f;               // 2^-40
@@ -516,7 +527,7 @@ policy_ring_kernel(PolicyArgs a, const T* logits, T* dlogits, int reuse) {
                 // the target's element again, by the thread that has just written its vector
                 const int hit = hot_vec - i0 - tid;
                 if (hot_vec >= 0 && hit >= 0 && hit < left && hit % kThreads == 0)
-                    dz[r.target] = grad_one<T>(r.zt, g, k, true);
+                    dz[r.target] = grad_one<T>(x.zt, g, k, true);
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&empty[at.slot]);
             }
