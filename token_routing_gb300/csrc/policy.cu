@@ -15,6 +15,7 @@ constexpr int kMaxCluster = 8;
 constexpr int kEach = 4;                      // 16-byte vectors of a piece to a thread
 constexpr int kPiece = kEach * kThreads;      // vectors of one bulk copy: 16 KB
 constexpr int kSlots = 6;                     // pieces in a CTA's ring: two CTAs to an SM
+constexpr int kHeld = 8;                      // vectors a thread holds of a short row
 constexpr int kShare = 4;                     // pieces of a row that a CTA takes, while clusters last
 
 // What becomes of a piece of a row after its sum was taken.
@@ -170,6 +171,10 @@ __device__ __forceinline__ float token_terms(const PolicyArgs& a, const Token& r
 struct RowGrad {
     float c, top, q;
     float lift;        // see grad_vec
+    __device__ __forceinline__ void set_q(float x) {
+        lift = fabsf(x) > 9.0949470e-13f ? 64.f : 0.f;             // 2^-40
+        q = lift != 0.f ? x * 5.4210109e-20f : x;                   // 2^-64
+    }
 };
 
 // Gradient of one vector. Exponentials are computed as 2^(x + lift) with q carrying 2^-lift: the
@@ -499,9 +504,7 @@ policy_ring_kernel(PolicyArgs a, const T* logits, T* dlogits, int reuse) {
             RowGrad g;
             g.c = token_terms(a, x, rank == 0 && tid == 0, acc, k);
             g.top = acc.m;
-            const float q = g.c / acc.s;
-            g.lift = fabsf(q) > 9.0949470e-13f ? 64.f : 0.f;               // 2^-40
-            g.q = g.lift != 0.f ? q * 5.4210109e-20f : q;                   // 2^-64
+            g.set_q(g.c / acc.s);
             // ---- gradient
             const int hot = r.target - s.head - s.v0 * N;    // the target's place in this CTA's vectors
             const int hot_vec = hot >= 0 && hot < s.nv * N ? hot / N : -1;
@@ -539,6 +542,103 @@ policy_ring_kernel(PolicyArgs a, const T* logits, T* dlogits, int reuse) {
     __syncwarp();
     asm volatile("barrier.cluster.arrive.release;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// Short rows: G threads (a warp, or the block) hold a row in registers, up to eight vectors each.
+constexpr int short_block(int G) { return G == 32 ? 256 : G; }
+template <typename T, int G>
+__global__ void __launch_bounds__(short_block(G), 1024 / short_block(G)) policy_short_kernel(PolicyArgs a, const T* logits, T* dlogits) {
+    constexpr int N = Vec16<T>::N;
+    __shared__ MaxSum part[8];
+    pdl_wait();
+    const int tid = threadIdx.x % G, lane = threadIdx.x & 31;
+    const int64_t t = (int64_t)blockIdx.x * (short_block(G) / G) + threadIdx.x / G;
+    if (t >= a.T) return;                     // a whole warp (G = 32) or block
+    const float w = a.weight ? a.weight[t] : 1.f;
+    const int target = a.target[t];
+    const Share<T> s(logits + t * a.ld, a.V, 0, 1);
+    T* dz = dlogits ? dlogits + t * a.ld_grad : nullptr;
+    const bool wide = ((reinterpret_cast<uintptr_t>(s.z) ^ reinterpret_cast<uintptr_t>(dz)) & 15) == 0;
+    uint4* out = reinterpret_cast<uint4*>(dz + s.head);
+    const int odd = tid < s.head ? tid : s.nvec * N + tid;
+    if (w == 0.f || (uint32_t)target >= (uint32_t)a.V) {
+        if (tid == 0) {
+            if (w != 0.f && target >= a.V) raise_error(a.err, kErrBounds);
+            if (a.logp) a.logp[t] = 0.f;
+            if (a.tok_loss) a.tok_loss[t] = 0.f;
+        }
+        if (dz) {
+            const T zero = Elem<T>::from_f(0.f);
+            if (wide)
+                for (int i = tid; i < s.nvec; i += G) out[i] = make_uint4(0u, 0u, 0u, 0u);
+            else
+                for (int i = tid; i < s.nvec * N; i += G) dz[s.head + i] = zero;
+            if (tid < s.rest) dz[odd] = zero;
+        }
+        return;
+    }
+    const float k = a.inv_tau * kLog2e;
+    Token x{(int)t, w, Elem<T>::to_f(s.z[target]), 0.f, 0.f, 0.f};
+    if (a.advantage) x.adv = a.advantage[t];
+    if (a.old_logp) x.old = a.old_logp[t];
+    if (a.kl != 0.f) x.ref = a.ref_logp[t];
+    const float lone = tid < s.rest ? Elem<T>::to_f(s.z[odd]) : -INFINITY;
+    const uint32_t none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;       // -inf, which adds 0
+    uint4 u[kHeld];
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {
+        u[h] = make_uint4(none, none, none, none);
+        if (tid + h * G < s.nvec) u[h] = s.vecs()[tid + h * G];
+    }
+    MaxSum acc{lone, 0.f};
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h)
+        if (h * G < s.nvec) acc.m = fmaxf(acc.m, vec_max<T>(u[h]));
+    const float base = acc.m == -INFINITY ? 0.f : acc.m;
+    const uint64_t minus = splat2(-base), kk = splat2(k);
+    uint64_t sum = 0;
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h)
+        if (h * G < s.nvec) {
+            uint64_t p[Pairs<T>::N];
+            to_pairs<T>(u[h], p);
+#pragma unroll
+            for (int i = 0; i < Pairs<T>::N; ++i) {
+                float x0, x1;
+                upk2(mul2(add2(p[i], minus), kk), x0, x1);
+                sum = add2(sum, pk2(ex2_approx(x0), ex2_approx(x1)));
+            }
+        }
+    float s0, s1;
+    upk2(sum, s0, s1);
+    acc.s = s0 + s1;
+    if (tid < s.rest) acc.s += ex2_approx((lone - base) * k);
+    acc = warp_join(acc, k);
+    // what this thread reads of the row has arrived before any thread writes it (dlogits may be logits)
+    asm volatile("" ::"f"(x.zt), "f"(lone) : "memory");
+    if constexpr (G > 32) {
+        if (lane == 0) part[threadIdx.x >> 5] = acc;
+        __syncthreads();
+        acc = warp_join(lane < G / 32 ? part[lane] : MaxSum{-INFINITY, 0.f}, k);
+    }
+    __syncwarp();
+    RowGrad g;
+    g.c = token_terms(a, x, tid == 0, acc, k);
+    if (!dz) return;
+    g.top = acc.m;
+    g.set_q(g.c / acc.s);
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {
+        const int i = tid + h * G;
+        if (i >= s.nvec) break;
+        const uint4 o = grad_vec<T>(u[h], g, k);
+        if (wide) out[i] = o;
+        else put_elements<T>(dz + s.head + i * N, o);
+    }
+    // the target's element again, by the thread that has just written its vector
+    const int hot = target - s.head, hot_vec = hot >= 0 && hot < s.nvec * N ? hot / N : -1;
+    if (hot_vec >= 0 && hot_vec % G == tid) dz[target] = grad_one<T>(x.zt, g, k, true);
+    if (tid < s.rest) dz[odd] = grad_one<T>(lone, g, k, odd == target);
 }
 
 // loss = sum of the tokens' terms, one block, in a fixed order.
@@ -597,6 +697,18 @@ template <typename T>
 cudaError_t launch_policy(const PolicyArgs& a, const void* logits, void* dlogits, cudaStream_t s) {
     constexpr size_t smem = (size_t)kSlots * kPiece * 16;
     const int64_t vecs = a.V / Vec16<T>::N;
+    // rows that a warp, or a block, holds in registers
+    if (vecs <= 256 * kHeld) {
+        const T* z = static_cast<const T*>(logits);
+        T* dz = static_cast<T*>(dlogits);
+        const cudaError_t e =
+            vecs <= 32 * kHeld    ? launch_pdl(policy_short_kernel<T, 32>, dim3(ceil_div(a.T, 8)), dim3(256), 0, s, a, z, dz)
+            : vecs <= 64 * kHeld  ? launch_pdl(policy_short_kernel<T, 64>, dim3(a.T), dim3(64), 0, s, a, z, dz)
+            : vecs <= 128 * kHeld ? launch_pdl(policy_short_kernel<T, 128>, dim3(a.T), dim3(128), 0, s, a, z, dz)
+                                  : launch_pdl(policy_short_kernel<T, 256>, dim3(a.T), dim3(256), 0, s, a, z, dz);
+        count_launch();
+        return e;
+    }
     const auto pieces = [&](int cs) { return (vecs + (int64_t)cs * kPiece - 1) / ((int64_t)cs * kPiece); };
     int cs = 1;
     while (cs < kMaxCluster && pieces(cs) > kShare) cs *= 2;
