@@ -386,7 +386,7 @@ MOE_API moe_status_t moe_token_logp(const moe_policy_config_t* cfg, const void* 
 #define MOE_ADAMW_BLOCK 256
 #define MOE_ADAMW_STATE_BYTES 32
 typedef struct {
-    double lr, beta1, beta2, eps;   /* lr finite, betas in [0, 1), eps > 0 */
+    double lr, beta1, beta2, eps;   /* lr finite, betas in [0, 1), eps in [1e-30, 1e30] */
 } moe_adamw_config_t;
 typedef struct {
     void* p;                /* [n] weights, dtype */

@@ -113,7 +113,7 @@ def test_adamw_refuses_tensors(moe_lib, bad, status):
 
 
 @pytest.mark.parametrize("bad", [dict(lr=float("inf")), dict(beta1=1.0), dict(beta1=-0.1), dict(beta2=1.0),
-                                 dict(beta2=float("nan")), dict(eps=0.0), dict(eps=float("inf"))])
+                                 dict(beta2=float("nan")), dict(eps=0.0), dict(eps=1e-31), dict(eps=float("inf"))])
 def test_adamw_refuses_settings(moe_lib, bad):
     lib, kw = moe_lib.load(), dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8)
     kw.update(bad)

@@ -51,7 +51,7 @@ static_assert(sizeof(State) == MOE_ADAMW_STATE_BYTES, "state layout");
 struct Step {
     float b1, ob1, b2, ob2;            // betas and 1 - betas
     float keep;                        // 1 - lr * decay
-    float rate;                        // lr / (1 - beta1^t)
+    float rate;                        // -lr / (1 - beta1^t)
     float rc2;                         // 1 / sqrt(1 - beta2^t)
     float eps, gs;
     uint32_t dither;                   // the step's part of the hash
@@ -89,88 +89,117 @@ __device__ __forceinline__ void store8(T* p, int live, const float (&f)[8]) {
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.4028235e38f; }
 
+__device__ __forceinline__ float sqrt_approx(float x) {
+    float r;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 __device__ __forceinline__ void load_codes(const uint8_t* p, int live, float scale, float (&f)[8]) {
-    uint8_t b[8];
+    uint16_t b[4];
     if (live == 8) {
         *reinterpret_cast<uint2*>(b) = *reinterpret_cast<const uint2*>(p);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) b[i] = i < live ? p[i] : 0;
+        for (int i = 0; i < 4; ++i)
+            b[i] = (uint16_t)((2 * i < live ? p[2 * i] : 0) | (2 * i + 1 < live ? p[2 * i + 1] : 0) << 8);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        __nv_fp8_e4m3 e;
-        e.__x = b[i];
-        f[i] = __fmul_rn(static_cast<float>(e), scale);
+    for (int i = 0; i < 4; ++i) {
+        const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2(b[i], __NV_E4M3));
+        const float2 v = __half22float2(h);
+        f[2 * i] = v.x * scale;
+        f[2 * i + 1] = v.y * scale;
     }
 }
 
-// e4m3 code of y (|y| < 256 if finite): one of its two neighbours on the grid, chosen by the
-// dither d (20 bits). kRoot false: up with the probability of the share of the way up, so that
-// the value is right on average. kRoot true: y is the root of a second moment, and the share is
-// taken between the squares, so that the moment is right on average (rounding the root evenly
-// would raise it: the mean of squares is above the square of the mean); a root above zero keeps
-// at least the smallest code. Above 2^-6 a grid step is 2^-3 of the leading bit, below it 2^-9.
-template <bool kRoot>
-__device__ __forceinline__ uint8_t encode(float y, uint32_t d) {
-    const float a = fabsf(y);
-    const uint32_t bits = __float_as_uint(a);
-    float q;
-    if (kRoot) {
-        const bool high = a >= 0.015625f;
-        const float low = high ? __uint_as_float(bits & ~0xfffffu) : floorf(a * 512.f) * 0.001953125f;
-        const float unit = high ? __uint_as_float((bits & 0x7f800000u) - (3u << 23)) : 0.001953125f;
-        const float over = __fmul_rn(__fsub_rn(a, low), __fadd_rn(a, low));
-        const float step = __fmul_rn(unit, __fadd_rn(2.f * low, unit));
-        q = over >= __fmul_rn((float)(0x100000u - d) * 9.5367431640625e-7f, step) ? low + unit : low;
-        if (a > 0.f && q == 0.f) q = 0.001953125f;
-    } else {
-        q = a >= 0.015625f ? __uint_as_float((bits + d) & ~0xfffffu)
-                           : floorf(__fadd_rn(a * 512.f, (float)d * 9.5367431640625e-7f)) * 0.001953125f;
-    }
-    q = copysignf(q, y);
-    if (!finite(y)) q = NAN;                         // infinities and NaN are held as NaN
-    return __nv_fp8_e4m3(q).__x;
+// The grid of e4m3 in fp32: three bits after the leading one, a step of 2^-9 below 2^-6. Adding
+// 2^-6 to a number below it puts it where the fp32 mantissa has that step too, so that the 20
+// low bits of t are the share of the way to the next grid value everywhere.
+constexpr float kTiny = 0.015625f;      // 2^-6
+
+// y on the grid, up with the probability of its share of the way: d is the dither, 20 bits.
+__device__ __forceinline__ float to_grid(float y, uint32_t d) {
+    const float off = copysignf(fabsf(y) < kTiny ? kTiny : 0.f, y);
+    return __uint_as_float((__float_as_uint(y + off) + d) & ~0xfffffu) - off;
 }
 
-// Scale and codes of one block. The scale is the power of two that puts the largest finite
-// magnitude into [128, 256): the grid of held values then stays where it is from step to step
-// (a scale that followed the largest magnitude would move it, and re-round every value, at
-// each step), scaling is exact, and the dither's carry cannot pass 448.
+// A root y >= 0 on the grid, the share of the way taken between the squares, so that the square
+// is right on average (rounding the root evenly would raise it: the mean of squares is above the
+// square of the mean). A root above zero keeps at least the smallest step.
+__device__ __forceinline__ float root_to_grid(float y, uint32_t d) {
+    const float off = y < kTiny ? kTiny : 0.f;
+    const float t = y + off;
+    const float low_t = __uint_as_float(__float_as_uint(t) & ~0xfffffu), low = low_t - off;
+    const float unit = __uint_as_float((__float_as_uint(t) & 0x7f800000u) - (3u << 23));
+    const float over = (t - low_t) * (y + low);                       // y^2 - low^2
+    const float step = unit * fmaf(2.f, low, unit);                   // (low + unit)^2 - low^2
+    const float rest = 2.f - __uint_as_float(0x3f800000u | d << 3);   // 1 - dither
+    const float q = over >= rest * step ? low + unit : low;
+    return fmaxf(q, y > 0.f ? 0.001953125f : 0.f);
+}
+
+// Codes and scale of one block of 256, eight elements a lane. The scale is the power of two that
+// puts the block's largest finite magnitude (`top`, the same in all lanes) into [128, 256): the
+// grid of held values then stays where it is from step to step (a scale that followed the
+// largest magnitude would move it, and re-round every value, at each step), scaling is exact,
+// and no carry passes 448.
+// kRoot: f are roots of second moments. odd: a value of this lane is infinite or NaN, held as NaN.
 template <bool kRoot>
-__device__ __forceinline__ void store_codes(uint8_t* p, float* scale, int live, const float (&f)[8],
-                                            const uint32_t (&hash)[8]) {
-    float top = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < live && finite(f[i])) top = fmaxf(top, fabsf(f[i]));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+__device__ __forceinline__ void store_codes(uint8_t* p, float* scale, int live, const float (&f)[8], float top,
+                                            bool odd, const uint32_t (&hash)[8]) {
     const bool some = top >= 7.8886091e-31f;         // 2^-100: a block below it counts as 0
     const uint32_t pow2 = (__float_as_uint(top) & 0x7f800000u) - (7u << 23);
-    const float inv = __uint_as_float((254u << 23) - pow2);
-    uint8_t b[8];
+    const float inv = some ? __uint_as_float((254u << 23) - pow2) : 0.f;
+    uint16_t b[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t d = (kRoot ? hash[i] * 0xC2B2AE35u : hash[i]) >> 12;
-        b[i] = encode<kRoot>(some ? f[i] * inv : finite(f[i]) ? 0.f : NAN, d);
+    for (int i = 0; i < 4; ++i) {
+        float q[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float y = f[2 * i + j] * inv;
+            q[j] = kRoot ? root_to_grid(y, (hash[2 * i + j] * 0xC2B2AE35u) >> 12) : to_grid(y, hash[2 * i + j] >> 12);
+        }
+        b[i] = (uint16_t)__nv_cvt_float2_to_fp8x2(make_float2(q[0], q[1]), __NV_SATFINITE, __NV_E4M3);
+    }
+    if (odd) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (!finite(f[i])) b[i / 2] |= 0x7f << 8 * (i % 2);
     }
     if (live == 8) {
         *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(b);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < live) p[i] = b[i];
+            if (i < live) p[i] = (uint8_t)(b[i / 2] >> 8 * (i % 2));
     }
     if ((threadIdx.x & 31) == 0) *scale = some ? __uint_as_float(pow2) : 0.f;
 }
 
-// One unit of one tensor by one warp. live: this lane's elements (0 .. 8).
+// Largest finite magnitude of the warp's 256 values, as bits (which order like the values);
+// odd: whether one of this lane's is not finite.
+__device__ __forceinline__ float block_top(const float (&f)[8], bool& odd) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
+    odd = top >= 0x7f800000u;
+    if (odd) {
+        top = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (finite(f[i])) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
+    }
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, top));
+}
+
+// One unit of one tensor by one warp. live: this lane's elements (0 .. 8). m and v are sums of
+// rounded products (no fma): the same bits on any machine, so that a block's scale is too.
 template <typename P, typename G>
 __device__ __forceinline__ void unit(const TensorArg& t, const Step& s, int64_t u, int lane) {
     const int64_t i0 = u * kUnit + lane * 8;
     const int live = (int)max((int64_t)0, min((int64_t)8, t.n - i0));
-    float x[8], g[8], m[8], v[8];
+    float x[8], g[8], m[8], v[8], root[8];
     P* p = static_cast<P*>(t.p) + i0;
     if (t.w) load8(t.w + i0, live, x);
     else load8(p, live, x);
@@ -179,19 +208,25 @@ __device__ __forceinline__ void unit(const TensorArg& t, const Step& s, int64_t 
     if (narrow) {
         load_codes(static_cast<const uint8_t*>(t.m) + i0, live, t.ms[u], m);
         load_codes(static_cast<const uint8_t*>(t.v) + i0, live, t.vs[u], v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= v[i];
     } else {
         load8(static_cast<const float*>(t.m) + i0, live, m);
         load8(static_cast<const float*>(t.v) + i0, live, v);
     }
-    float root[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float gi = g[i] * s.gs;
-        if (narrow) v[i] = __fmul_rn(v[i], v[i]);
-        m[i] = __fadd_rn(__fmul_rn(s.b1, m[i]), __fmul_rn(s.ob1, gi));
-        v[i] = __fadd_rn(__fmul_rn(s.b2, v[i]), __fmul_rn(s.ob2, __fmul_rn(gi, gi)));
-        root[i] = __fsqrt_rn(v[i]);
-        x[i] = x[i] * s.keep - __fdividef(m[i] * s.rate, fmaf(root[i], s.rc2, s.eps));
+    for (int i = 0; i < 8; i += 2) {
+        const uint64_t gg = mul2(pk2(g[i], g[i + 1]), splat2(s.gs));
+        const uint64_t mm = add2(mul2(splat2(s.b1), pk2(m[i], m[i + 1])), mul2(splat2(s.ob1), gg));
+        const uint64_t vv = add2(mul2(splat2(s.b2), pk2(v[i], v[i + 1])), mul2(splat2(s.ob2), mul2(gg, gg)));
+        upk2(mm, m[i], m[i + 1]);
+        upk2(vv, v[i], v[i + 1]);
+        root[i] = sqrt_approx(v[i]);
+        root[i + 1] = sqrt_approx(v[i + 1]);
+        float d0, d1;
+        upk2(fma2(pk2(root[i], root[i + 1]), splat2(s.rc2), splat2(s.eps)), d0, d1);
+        const uint64_t up = mul2(mul2(mm, splat2(s.rate)), pk2(rcp_approx(d0), rcp_approx(d1)));
+        upk2(fma2(pk2(x[i], x[i + 1]), splat2(s.keep), up), x[i], x[i + 1]);
     }
     store8(p, live, x);
     if (t.w) store8(t.w + i0, live, x);
@@ -203,8 +238,11 @@ __device__ __forceinline__ void unit(const TensorArg& t, const Step& s, int64_t 
             const uint32_t h = ((uint32_t)i0 + i) * 0x9E3779B1u + s.dither;
             hash[i] = (h ^ (h >> 15)) * 0x85EBCA6Bu;
         }
-        store_codes<false>(static_cast<uint8_t*>(t.m) + i0, t.ms + u, live, m, hash);
-        store_codes<true>(static_cast<uint8_t*>(t.v) + i0, t.vs + u, live, root, hash);
+        bool odd;
+        const float top_m = block_top(m, odd);
+        store_codes<false>(static_cast<uint8_t*>(t.m) + i0, t.ms + u, live, m, top_m, odd, hash);
+        const float top_v = block_top(v, odd);
+        store_codes<true>(static_cast<uint8_t*>(t.v) + i0, t.vs + u, live, root, __fsqrt_rn(top_v), odd, hash);
     } else {
         store8(static_cast<float*>(t.m) + i0, live, m);
         store8(static_cast<float*>(t.v) + i0, live, v);
@@ -223,18 +261,21 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     s.ob1 = (float)(1.0 - a.beta1);
     s.b2 = (float)a.beta2;
     s.ob2 = (float)(1.0 - a.beta2);
-    s.rate = lr / (float)c1;
+    s.rate = -lr / (float)c1;
     s.rc2 = 1.f / sqrtf((float)c2);
     s.eps = a.eps;
     s.gs = a.grad_scale ? *a.grad_scale : 1.f;
     s.dither = (uint32_t)step * 0x61C88647u;
     const int lane = threadIdx.x & 31;
     const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
+    int lo = 0;
     for (int64_t q = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); q < a.units; q += warps) {
-        int lo = 0, hi = a.count;                       // the last tensor whose first unit is <= q
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (a.first[mid] <= q) lo = mid; else hi = mid;
+        if (lo + 1 < a.count && a.first[lo + 1] <= q) {
+            int hi = a.count;                           // the last tensor whose first unit is <= q
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (a.first[mid] <= q) lo = mid; else hi = mid;
+            }
         }
         const TensorArg& t = a.t[lo];
         s.keep = 1.f - lr * t.decay;
@@ -266,7 +307,7 @@ bool misaligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintpt
 moe_status_t check_adamw(const moe_adamw_config_t* c, const moe_adamw_tensor_t* ts, int32_t count) {
     if (!c || count < 0 || (count > 0 && !ts)) return MOE_ERR_INVALID_ARG;
     if (!std::isfinite(c->lr) || !(c->beta1 >= 0.0 && c->beta1 < 1.0) || !(c->beta2 >= 0.0 && c->beta2 < 1.0) ||
-        !(c->eps > 0.0) || !std::isfinite(c->eps))
+        !(c->eps >= 1e-30 && c->eps <= 1e30))
         return MOE_ERR_INVALID_ARG;
     for (int i = 0; i < count; ++i) {
         const moe_adamw_tensor_t& t = ts[i];
