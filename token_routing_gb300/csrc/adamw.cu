@@ -1,6 +1,7 @@
 // AdamW over many tensors in one launch, with fp32 or 8-bit states.
 #include <cuda_fp8.h>
 
+#include <climits>
 #include <cmath>
 #include <type_traits>
 
@@ -12,7 +13,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kUnit = MOE_ADAMW_BLOCK;     // elements a warp takes at a time: 8 a lane, one scale block
-constexpr int kBlocks = 4;                 // blocks to an SM
+constexpr uint32_t kTicket = 1024;         // blocks that may take a ticket each
+constexpr int kRun = 16;                    // longest run
 constexpr int kBatch = 256;                // tensors in one launch's parameters
 
 struct TensorArg {
@@ -25,7 +27,7 @@ struct TensorArg {
     float* vs;
     int64_t n;
     float decay;
-    int32_t kind;      // bit 0: p is bf16, bit 1: g is bf16, bit 2: master, bit 3: 8-bit states
+    int32_t kind;      // bit 0: p is bf16, bit 1: g is bf16, bit 2: master
 };
 
 struct AdamArgs {
@@ -36,9 +38,9 @@ struct AdamArgs {
     const float* lr_dev;
     const float* grad_scale;
     unsigned char* state;
-    int run;                           // units of one tensor that a warp takes in a row
-    int64_t runs;
-    int64_t first[kBatch];             // first run of each tensor
+    int run;                           // eights of units of one tensor that a block takes in a row
+    uint32_t runs;
+    uint32_t first[kBatch];            // first run of each tensor
     TensorArg t[kBatch];
 };
 static_assert(sizeof(AdamArgs) <= 32000, "kernel parameters");
@@ -70,12 +72,12 @@ __device__ __forceinline__ float sqrt_approx(float x) {
 
 // Eight elements as fp32 pairs, from 16 or 32 bytes, and back.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, uint64_t (&f)[4]) {
+__device__ __forceinline__ void unpack8(const uint4* u, uint64_t (&f)[4]) {
     if constexpr (sizeof(T) == 2) {
-        to_pairs<T>(*reinterpret_cast<const uint4*>(p), f);
+        to_pairs<T>(u[0], f);
     } else {
-        to_pairs<T>(reinterpret_cast<const uint4*>(p)[0], reinterpret_cast<uint64_t(&)[2]>(f[0]));
-        to_pairs<T>(reinterpret_cast<const uint4*>(p)[1], reinterpret_cast<uint64_t(&)[2]>(f[2]));
+        to_pairs<T>(u[0], reinterpret_cast<uint64_t(&)[2]>(f[0]));
+        to_pairs<T>(u[1], reinterpret_cast<uint64_t(&)[2]>(f[2]));
     }
 }
 template <typename T>
@@ -99,30 +101,41 @@ __device__ __forceinline__ void decode8(uint2 codes, float scale, uint64_t (&f)[
     }
 }
 
-// The grid of e4m3 in fp32: three bits after the leading one, a step of 2^-9 below 2^-6. Adding
-// 2^-6 to a number below it puts it where the fp32 mantissa has that step too, so that the 20
-// low bits of t are the share of the way to the next grid value everywhere.
-constexpr float kTiny = 0.015625f;      // 2^-6
+// e4m3 in fp32. A value times 2^-120 has its e4m3 code in bits 26 .. 20 of the fp32 number: e4m3's
+// exponent bias is then that of fp32, its numbers below 2^-6 are fp32's own subnormal ones, and
+// the 20 bits below are the share of the way to the next code, for all of them alike.
+constexpr float kToCode = 7.5231638e-37f;       // 2^-120
+constexpr float kFromCode = 1.3292280e+36f;     // 2^120
 
-// y on the grid, up with the probability of its share of the way: d is the dither, 20 bits.
-__device__ __forceinline__ float to_grid(float y, uint32_t d) {
-    const float off = copysignf(fabsf(y) < kTiny ? kTiny : 0.f, y);
-    return __uint_as_float((__float_as_uint(y + off) + d) & ~0xfffffu) - off;
+// Code of y 2^-120 in the top byte, up with the probability of its share of the way: the 20 top
+// bits of the hash are added to it.
+__device__ __forceinline__ uint32_t value_code(float y, uint32_t hash) {
+    const uint32_t t = __float_as_uint(y) + (hash >> 12);
+    return (t << 4 & 0x7f000000u) | (t & 0x80000000u);
 }
 
-// A root y >= 0 on the grid, the share of the way taken between the squares, so that the square
-// is right on average (rounding the root evenly would raise it: the mean of squares is above the
-// square of the mean). A root above zero keeps at least the smallest step.
-__device__ __forceinline__ float root_to_grid(float y, uint32_t d) {
-    const float off = y < kTiny ? kTiny : 0.f;
-    const float t = y + off;
-    const float low_t = __uint_as_float(__float_as_uint(t) & ~0xfffffu), low = low_t - off;
-    const float unit = __uint_as_float((__float_as_uint(t) & 0x7f800000u) - (3u << 23));
-    const float over = (t - low_t) * (y + low);                       // y^2 - low^2
-    const float step = unit * fmaf(2.f, low, unit);                   // (low + unit)^2 - low^2
-    const float rest = 2.f - __uint_as_float(0x3f800000u | d << 3);   // 1 - dither
-    const float q = over >= rest * step ? low + unit : low;
-    return fmaxf(q, y > 0.f ? 0.001953125f : 0.f);
+// Codes of two roots y >= 0 (and y 2^-120) in the top bytes. The share of the way is taken between
+// the squares, so that the square is right on average (rounding the root evenly would raise it:
+// the mean of squares is above the square of the mean). A root above zero keeps at least code 1.
+__device__ __forceinline__ void root_codes(uint64_t y, uint64_t down, uint32_t hash0, uint32_t hash1, uint32_t& c0,
+                                           uint32_t& c1) {
+    const uint32_t b0 = (uint32_t)down, b1 = (uint32_t)(down >> 32);
+    const uint32_t l0 = b0 & ~0xfffffu, l1 = b1 & ~0xfffffu, n0 = l0 + 0x100000u, n1 = l1 + 0x100000u;
+    uint64_t low = mul2((uint64_t)l1 << 32 | l0, splat2(kFromCode)), next = mul2((uint64_t)n1 << 32 | n0, splat2(kFromCode));
+    const uint64_t minus = splat2(-1.f);
+    low = mul2(low, low);
+    const uint64_t over = fma2(low, minus, mul2(y, y)), step = fma2(low, minus, mul2(next, next));
+    // 1 + the share that is not reached, from the hash's 23 top bits
+    const uint64_t rest = (uint64_t)(0x3f800000u | ~hash1 >> 9) << 32 | (0x3f800000u | ~hash0 >> 9);
+    float e0, e1;
+    upk2(add2(fma2(mul2(rest, minus), step, step), over), e0, e1);
+    c0 = max(e0 > 0.f ? n0 : l0, min((uint32_t)y, 0x100000u)) << 4;
+    c1 = max(e1 > 0.f ? n1 : l1, min((uint32_t)(y >> 32), 0x100000u)) << 4;
+}
+
+// Top bytes of four words as one word.
+__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x7300), 0x7610);
 }
 
 // Eight of the codes of one block. `inv` is one over the block's scale, the power of two that
@@ -132,20 +145,20 @@ __device__ __forceinline__ float root_to_grid(float y, uint32_t d) {
 // kRoot: f are roots of second moments. odd: one of them is infinite or NaN, held as NaN.
 template <bool kRoot>
 __device__ __forceinline__ uint2 encode8(const uint64_t (&f)[4], float inv, bool odd, const uint32_t (&hash)[8]) {
-    uint32_t w[2] = {0, 0};
+    uint32_t c[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float y0, y1;
-        upk2(mul2(f[i], splat2(inv)), y0, y1);
+        const uint64_t y = mul2(f[i], splat2(inv)), down = mul2(y, splat2(kToCode));
         if constexpr (kRoot) {
-            y0 = root_to_grid(y0, (hash[2 * i] * 0xC2B2AE35u) >> 12);
-            y1 = root_to_grid(y1, (hash[2 * i + 1] * 0xC2B2AE35u) >> 12);
+            root_codes(y, down, hash[2 * i] * 0xC2B2AE35u, hash[2 * i + 1] * 0xC2B2AE35u, c[2 * i], c[2 * i + 1]);
         } else {
-            y0 = to_grid(y0, hash[2 * i] >> 12);
-            y1 = to_grid(y1, hash[2 * i + 1] >> 12);
+            float y0, y1;
+            upk2(down, y0, y1);
+            c[2 * i] = value_code(y0, hash[2 * i]);
+            c[2 * i + 1] = value_code(y1, hash[2 * i + 1]);
         }
-        w[i / 2] |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(y0, y1), __NV_SATFINITE, __NV_E4M3) << 16 * (i % 2);
     }
+    uint32_t w[2] = {top_bytes(c[0], c[1], c[2], c[3]), top_bytes(c[4], c[5], c[6], c[7])};
     if (odd) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -220,70 +233,107 @@ __device__ __forceinline__ void hold(const uint64_t (&m)[4], const uint64_t (&v)
     cv = encode8<true>(root, inv, odd, hash);
 }
 
-// Whole units u0 .. u0 + count - 1 of one tensor by one warp, eight elements a lane and unit.
+// What a lane reads of one unit, as it is in memory.
 template <typename P, typename G, bool kMaster, bool kNarrow>
-__device__ __forceinline__ void run_units(const TensorArg& t, const Step& s, int64_t u0, int count, int lane) {
-    const int64_t i0 = u0 * kUnit + lane * 8;
-    P* p = static_cast<P*>(t.p) + i0;
-    const G* g = static_cast<const G*>(t.g) + i0;
-    float* w = kMaster ? t.w + i0 : nullptr;
+struct Raw {
+    static constexpr int kX = (kMaster || sizeof(P) == 4) ? 2 : 1, kG = sizeof(G) / 2;
+    uint4 x[kX], g[kG], m[kNarrow ? 1 : 2], v[kNarrow ? 1 : 2];     // 8 bits: both states' codes in m[0]
+    float ms, vs;
+};
+
+// Whole units of one block's run: the block's eight warps take units u0 + 8 k + warp, eight
+// elements a lane, while they are whole. Addresses are the run's bases, the same for the block,
+// plus a 32-bit place.
+template <typename P, typename G, bool kMaster, bool kNarrow>
+__device__ __forceinline__ void run_units(const TensorArg& t, const Step& s, int64_t u0, int count, int run) {
+    __shared__ float scales[2][kNarrow ? kRun * 8 : 1];
+    using R = Raw<P, G, kMaster, kNarrow>;
     using S = std::conditional_t<kNarrow, uint8_t, float>;
-    S* m = static_cast<S*>(t.m) + i0;
-    S* v = static_cast<S*>(t.v) + i0;
-    float* ms = t.ms + u0;
-    float* vs = t.vs + u0;
-    uint32_t h0 = (uint32_t)i0 * 0x9E3779B1u + s.dither;
-    for (int k = 0; k < count; ++k) {
-        uint64_t X[4], Gr[4], M[4], V[4], R[4];
-        if constexpr (kMaster) load8(w, X);
-        else load8(p, X);
-        load8(g, Gr);
-        if constexpr (kNarrow) {
-            const uint2 cm = *reinterpret_cast<const uint2*>(m), cv = *reinterpret_cast<const uint2*>(v);
-            decode8(cm, *ms, M);
-            decode8(cv, *vs, V);
+    const int64_t i0 = u0 * kUnit;
+    P* const p = static_cast<P*>(t.p) + i0;
+    const G* const g = static_cast<const G*>(t.g) + i0;
+    float* const w = kMaster ? t.w + i0 : nullptr;
+    S* const m = static_cast<S*>(t.m) + i0;
+    S* const v = static_cast<S*>(t.v) + i0;
+    float* const ms = kNarrow ? t.ms + u0 : nullptr;
+    float* const vs = kNarrow ? t.vs + u0 : nullptr;
+    const uint32_t warp = threadIdx.x >> 5;
+    const auto fetch = [&](uint32_t u, R& r) {
+        const uint32_t i = u * kUnit + (threadIdx.x & 31) * 8;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) V[i] = mul2(V[i], V[i]);
+        for (int j = 0; j < R::kX; ++j)
+            r.x[j] = kMaster ? reinterpret_cast<const uint4*>(w + i)[j] : reinterpret_cast<const uint4*>(p + i)[j];
+#pragma unroll
+        for (int j = 0; j < R::kG; ++j) r.g[j] = reinterpret_cast<const uint4*>(g + i)[j];
+        if constexpr (kNarrow) {
+            const uint2 a = *reinterpret_cast<const uint2*>(m + i), b = *reinterpret_cast<const uint2*>(v + i);
+            r.m[0] = make_uint4(a.x, a.y, b.x, b.y);
+            r.ms = ms[u];
+            r.vs = vs[u];
         } else {
-            load8(m, M);
-            load8(v, V);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                r.m[j] = reinterpret_cast<const uint4*>(m + i)[j];
+                r.v[j] = reinterpret_cast<const uint4*>(v + i)[j];
+            }
         }
-        advance8(s, Gr, X, M, V, R);
-        store8(p, X);
-        if constexpr (kMaster) store8(w, X);
+    };
+    R r;
+    if ((int)warp < count) fetch(warp, r);
+    for (uint32_t u = warp; (int)u < min(count, run * 8); u += 8) {
+        uint64_t X[4], Gr[4], M[4], V[4], root[4];
+        if constexpr (kMaster) unpack8<float>(r.x, X);
+        else unpack8<P>(r.x, X);
+        unpack8<G>(r.g, Gr);
+        if constexpr (kNarrow) {
+            decode8(make_uint2(r.m[0].x, r.m[0].y), r.ms, M);
+            decode8(make_uint2(r.m[0].z, r.m[0].w), r.vs, V);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) V[j] = mul2(V[j], V[j]);
+            // much arithmetic to a byte: the next unit is on its way meanwhile
+            if ((int)u + 8 < min(count, run * 8)) fetch(u + 8, r);
+        } else {
+            unpack8<float>(r.m, M);
+            unpack8<float>(r.v, V);
+        }
+        advance8(s, Gr, X, M, V, root);
+        const uint32_t i = u * kUnit + (threadIdx.x & 31) * 8;
+        store8(p + i, X);
+        if constexpr (kMaster) store8(w + i, X);
         if constexpr (kNarrow) {
             uint2 cm, cv;
             float sm, sv;
-            hold(M, V, R, h0, cm, cv, sm, sv);
-            *reinterpret_cast<uint2*>(m) = cm;
-            *reinterpret_cast<uint2*>(v) = cv;
-            if (lane == 0) {
-                *ms = sm;
-                *vs = sv;
+            hold(M, V, root, ((uint32_t)i0 + i) * 0x9E3779B1u + s.dither, cm, cv, sm, sv);
+            *reinterpret_cast<uint2*>(m + i) = cm;
+            *reinterpret_cast<uint2*>(v + i) = cv;
+            if ((threadIdx.x & 31) == 0) {
+                scales[0][u] = sm;
+                scales[1][u] = sv;
             }
         } else {
-            store8(m, M);
-            store8(v, V);
+            store8(m + i, M);
+            store8(v + i, V);
+            if ((int)u + 8 < min(count, run * 8)) fetch(u + 8, r);
         }
-        p += kUnit;
-        g += kUnit;
-        if (kMaster) w += kUnit;
-        m += kUnit;
-        v += kUnit;
-        if (kNarrow) {
-            ++ms;
-            ++vs;
+    }
+    if constexpr (kNarrow) {
+        // The scales go out by whole sectors: four bytes at a time from one warp after the other made
+        // the memory fill and rewrite sectors (1.1G weights: 3240 - 3820 us against 2840).
+        __syncthreads();
+        for (int u = threadIdx.x; u < min(count, run * 8); u += kThreads) {
+            ms[u] = scales[0][u];
+            vs[u] = scales[1][u];
         }
-        h0 += kUnit * 0x9E3779B1u;
     }
 }
 
 // The unit that a tensor's end cuts short, element by element.
+template <bool kNarrow>
 __device__ __noinline__ void last_unit(const TensorArg& t, const Step& s, int64_t u, int lane) {
     const int64_t i0 = u * kUnit + lane * 8;
     float f[4][8];
     const auto live = [&](int i) { return i0 + i < t.n; };
-    const bool narrow = t.ms != nullptr;
+    constexpr bool narrow = kNarrow;
     for (int i = 0; i < 8; ++i) {
         f[0][i] = f[1][i] = f[2][i] = f[3][i] = 0.f;
         if (!live(i)) continue;
@@ -345,58 +395,57 @@ __device__ __noinline__ void last_unit(const TensorArg& t, const Step& s, int64_
     }
 }
 
-__global__ void __launch_bounds__(kThreads, kBlocks) adamw_kernel(const __grid_constant__ AdamArgs a) {
+template <bool kNarrow>
+__global__ void __launch_bounds__(kThreads, kNarrow ? 3 : 2) adamw_kernel(const __grid_constant__ AdamArgs a) {
     pdl_wait();
+    // The step's scalars, by one thread: double precision is slow here, and every block pays for it.
+    __shared__ float corr[2];
     State* st = reinterpret_cast<State*>(a.state);
-    // 1 - beta^(t+1) = beta (1 - beta^t) + (1 - beta)
-    const double c1 = st->c1 * a.beta1 + (1.0 - a.beta1), c2 = st->c2 * a.beta2 + (1.0 - a.beta2);
     const long long step = st->step + 1;
+    double c1 = 0.0, c2 = 0.0;
+    if (threadIdx.x == 0) {
+        // 1 - beta^(t+1) = beta (1 - beta^t) + (1 - beta)
+        c1 = st->c1 * a.beta1 + (1.0 - a.beta1);
+        c2 = st->c2 * a.beta2 + (1.0 - a.beta2);
+        corr[0] = (float)c1;
+        corr[1] = (float)c2;
+    }
+    __syncthreads();
     const float lr = a.lr_dev ? *a.lr_dev : a.lr;
     Step s;
     s.b1 = a.b1;
     s.ob1 = a.ob1;
     s.b2 = a.b2;
     s.ob2 = a.ob2;
-    s.rate = -lr / (float)c1;
-    s.rc2 = 1.f / sqrtf((float)c2);
+    s.rate = -lr / corr[0];
+    s.rc2 = 1.f / sqrtf(corr[1]);
     s.eps = a.eps;
     s.gs = a.grad_scale ? *a.grad_scale : 1.f;
     s.dither = (uint32_t)step * 0x61C88647u;
-    const int lane = threadIdx.x & 31;
-    const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
-    int lo = 0;
-    for (int64_t q = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); q < a.runs; q += warps) {
-        if (lo + 1 < a.count && a.first[lo + 1] <= q) {
-            int hi = a.count;                           // the last tensor whose first run is <= q
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (a.first[mid] <= q) lo = mid; else hi = mid;
-            }
+    if (blockIdx.x < a.runs) {
+        int lo = 0, hi = a.count;                       // the last tensor whose first run is <= this block's
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (a.first[mid] <= blockIdx.x) lo = mid; else hi = mid;
         }
         const TensorArg& t = a.t[lo];
         s.keep = 1.f - lr * t.decay;
-        const int64_t u = (q - a.first[lo]) * a.run, whole = t.n / kUnit;
-        const int count = (int)min((int64_t)a.run, whole - u);
+        const int64_t u0 = (int64_t)(blockIdx.x - a.first[lo]) * a.run * 8, whole = t.n / kUnit - u0;
+        const int count = (int)min((int64_t)a.run * 8, whole);
         using B = __nv_bfloat16;
         switch (t.kind) {
-            case 0: run_units<float, float, false, false>(t, s, u, count, lane); break;
-            case 1: run_units<B, float, false, false>(t, s, u, count, lane); break;
-            case 2: run_units<float, B, false, false>(t, s, u, count, lane); break;
-            case 3: run_units<B, B, false, false>(t, s, u, count, lane); break;
-            case 4: run_units<float, float, true, false>(t, s, u, count, lane); break;
-            case 5: run_units<B, float, true, false>(t, s, u, count, lane); break;
-            case 6: run_units<float, B, true, false>(t, s, u, count, lane); break;
-            case 7: run_units<B, B, true, false>(t, s, u, count, lane); break;
-            case 8: run_units<float, float, false, true>(t, s, u, count, lane); break;
-            case 9: run_units<B, float, false, true>(t, s, u, count, lane); break;
-            case 10: run_units<float, B, false, true>(t, s, u, count, lane); break;
-            case 11: run_units<B, B, false, true>(t, s, u, count, lane); break;
-            case 12: run_units<float, float, true, true>(t, s, u, count, lane); break;
-            case 13: run_units<B, float, true, true>(t, s, u, count, lane); break;
-            case 14: run_units<float, B, true, true>(t, s, u, count, lane); break;
-            default: run_units<B, B, true, true>(t, s, u, count, lane); break;
+            case 0: run_units<float, float, false, kNarrow>(t, s, u0, count, a.run); break;
+            case 1: run_units<B, float, false, kNarrow>(t, s, u0, count, a.run); break;
+            case 2: run_units<float, B, false, kNarrow>(t, s, u0, count, a.run); break;
+            case 3: run_units<B, B, false, kNarrow>(t, s, u0, count, a.run); break;
+            case 4: run_units<float, float, true, kNarrow>(t, s, u0, count, a.run); break;
+            case 5: run_units<B, float, true, kNarrow>(t, s, u0, count, a.run); break;
+            case 6: run_units<float, B, true, kNarrow>(t, s, u0, count, a.run); break;
+            default: run_units<B, B, true, kNarrow>(t, s, u0, count, a.run); break;
         }
-        if (count < a.run && whole * kUnit < t.n && u + count == whole) last_unit(t, s, whole, lane);
+        // the unit that the tensor's end cuts short
+        if (t.n % kUnit && whole < (int64_t)a.run * 8 && (int)(threadIdx.x >> 5) == (int)(whole & 7))
+            last_unit<kNarrow>(t, s, u0 + whole, threadIdx.x & 31);
     }
     // the last block to get here counts the step: every block has read the old count by then
     if (a.advance) {
@@ -411,6 +460,15 @@ __global__ void __launch_bounds__(kThreads, kBlocks) adamw_kernel(const __grid_c
             }
         }
     }
+}
+
+// The step's count as a launch of its own, after all others.
+__global__ void adamw_count_kernel(unsigned char* state, double beta1, double beta2) {
+    pdl_wait();
+    State* st = reinterpret_cast<State*>(state);
+    st->c1 = st->c1 * beta1 + (1.0 - beta1);
+    st->c2 = st->c2 * beta2 + (1.0 - beta2);
+    st->step += 1;
 }
 
 bool misaligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
@@ -460,30 +518,46 @@ extern "C" MOE_API moe_status_t moe_adamw(const moe_adamw_config_t* cfg, const m
     a.lr_dev = lr;
     a.grad_scale = grad_scale;
     a.state = static_cast<unsigned char*>(state);
-    // long runs spare a warp the start of a run, short ones spread small tensors over more warps
-    int64_t units = 0;
-    for (int k = 0; k < count; ++k) units += (tensors[k].n + kUnit - 1) / kUnit;
-    const int64_t warps = (int64_t)num_sms() * kBlocks * (kThreads / 32);
-    a.run = units >= 16 * warps ? 8 : 1;
-    int i = 0;
-    do {
-        a.count = 0;
-        a.runs = 0;
-        for (; i < count && a.count < kBatch; ++i) {
-            const moe_adamw_tensor_t& t = tensors[i];
-            if (t.n == 0) continue;
-            a.first[a.count] = a.runs;
-            a.t[a.count] = {t.p, t.g, t.master, t.m, t.v, t.m_scale, t.v_scale, t.n, t.weight_decay,
-                            (t.dtype == MOE_BF16 ? 1 : 0) | (t.grad_dtype == MOE_BF16 ? 2 : 0) | (t.master ? 4 : 0) |
-                                (t.m_scale ? 8 : 0)};
-            a.runs += (t.n + (int64_t)kUnit * a.run - 1) / ((int64_t)kUnit * a.run);
-            ++a.count;
+    // fp32 and 8-bit states go to launches of their own
+    int64_t units[2] = {0, 0};
+    for (int k = 0; k < count; ++k) units[tensors[k].m_scale != nullptr] += (tensors[k].n + kUnit - 1) / kUnit;
+    const int launches[2] = {units[0] > 0 || units[1] == 0, units[1] > 0};
+    for (int narrow = 0; narrow < 2; ++narrow) {
+        if (!launches[narrow]) continue;
+        // long runs spare blocks their start, short ones spread small tensors over more blocks
+        a.run = (int)std::min<int64_t>(kRun, std::max<int64_t>(1, units[narrow] / (8LL * 4 * num_sms())));
+        if (units[narrow] / (8 * a.run) + count > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+        int i = 0;
+        bool last = false;
+        while (!last) {
+            a.count = 0;
+            a.runs = 0;
+            for (; i < count && a.count < kBatch; ++i) {
+                const moe_adamw_tensor_t& t = tensors[i];
+                if (t.n == 0 || (t.m_scale != nullptr) != (narrow != 0)) continue;
+                a.first[a.count] = a.runs;
+                a.t[a.count] = {t.p, t.g, t.master, t.m, t.v, t.m_scale, t.v_scale, t.n, t.weight_decay,
+                                (t.dtype == MOE_BF16 ? 1 : 0) | (t.grad_dtype == MOE_BF16 ? 2 : 0) | (t.master ? 4 : 0)};
+                const int64_t per = (int64_t)kUnit * 8 * a.run;
+                a.runs += (uint32_t)((t.n + per - 1) / per);
+                ++a.count;
+            }
+            last = i == count;
+            // Many blocks would queue at the ticket (20 ns each); few are done sooner with it than a
+            // second launch takes.
+            const bool ends = last && (narrow || !launches[1]), apart = a.runs > kTicket;
+            a.advance = ends && !apart;
+            const cudaError_t e = launch_pdl(narrow ? adamw_kernel<true> : adamw_kernel<false>,
+                                             dim3(std::max(1u, a.runs)), dim3(kThreads), 0, (cudaStream_t)stream, a);
+            count_launch();
+            if (e != cudaSuccess) return MOE_ERR_CUDA;
+            if (ends && apart) {
+                const cudaError_t f = launch_pdl(adamw_count_kernel, dim3(1), dim3(1), 0, (cudaStream_t)stream,
+                                                 a.state, a.beta1, a.beta2);
+                count_launch();
+                if (f != cudaSuccess) return MOE_ERR_CUDA;
+            }
         }
-        a.advance = i == count;
-        const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((a.runs + 7) / 8, (int64_t)num_sms() * kBlocks));
-        const cudaError_t e = launch_pdl(adamw_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, (cudaStream_t)stream, a);
-        count_launch();
-        if (e != cudaSuccess) return MOE_ERR_CUDA;
-    } while (i < count);
+    }
     return MOE_OK;
 }
