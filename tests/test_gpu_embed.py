@@ -119,9 +119,18 @@ def test_gradient_vocabulary_sizes(V, moe_lib, cuda_device):
     check_backward(moe_lib, ids.cuda(), dy, V, 1.0, "f32", "f32", False, pad=V - 1)
 
 
-def test_many_chunks(moe_lib, cuda_device):
-    ids, _, dy = make(70001, 3001, 24, "bf16")
+@pytest.mark.parametrize("T", [1023, 1024, 16383, 16384, 16385, 70001])
+def test_many_chunks(T, moe_lib, cuda_device):
+    """Around the sizes at which the sort takes one more pair a thread, or more than one block."""
+    ids, _, dy = make(T, 3001, 24, "bf16")
     check_backward(moe_lib, ids, dy, 3001, 1.0, "bf16", "f32", False, pad=0)
+    check_backward(moe_lib, ids, dy, 3001, 1.0, "bf16", "bf16", True, pad=-1)
+
+
+@pytest.mark.parametrize("T,V,d", [(16384, 262145, 8), (5000, 400000, 4), (20000, 1, 3)])
+def test_gradient_more_vocabularies(T, V, d, moe_lib, cuda_device):
+    ids, _, dy = make(T, V, d, "f32")
+    check_backward(moe_lib, ids, dy, V, 1.0, "f32", "f32", False, pad=-1)
 
 
 def test_empty_batch(moe_lib, cuda_device):

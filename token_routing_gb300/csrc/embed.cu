@@ -16,6 +16,18 @@ template <> struct Raw<4> { using T = uint32_t; };
 template <> struct Raw<8> { using T = uint2; };
 template <> struct Raw<16> { using T = uint4; };
 
+// VE elements as they are in memory.
+template <typename T, int VE>
+struct Bits {
+    static constexpr int kBytes = (int)sizeof(T) * VE, kPart = kBytes > 16 ? 16 : kBytes, kParts = kBytes / kPart;
+    typename Raw<kPart>::T u[kParts];
+    __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) u[i] = reinterpret_cast<const typename Raw<kPart>::T*>(p)[i];
+    }
+    __device__ __forceinline__ float at(int i) const { return Elem<T>::to_f(reinterpret_cast<const T*>(u)[i]); }
+};
+
 template <typename T, int VE>
 struct Vec {
     static constexpr int kBytes = (int)sizeof(T) * VE;
@@ -118,20 +130,39 @@ cudaError_t launch_embed(const moe_embed_config_t& c, const int32_t* ids, const 
 }
 
 // ---------------------------------------------------------------- gradient: sort by token
-// Stable radix sort of (id, token) pairs, least digit first, by ordinary launches: per digit a
-// histogram of every chunk of kChunk pairs, then each chunk's ranks and the scatter. Left-out
-// tokens (padding, ids out of range) take the key V and end up behind all others.
+// Stable radix sort of (id, token) pairs, least digit first, by ordinary launches: a histogram of
+// every chunk of kChunk pairs for the first digit, then for each digit the chunks' ranks and the
+// scatter, which also counts the next digit's histogram by integer atomics. Left-out tokens
+// (padding, ids out of range) take the key V and end up behind all others.
+// The sort needs few of the SMs: the other blocks of its launches zero the first rows of a dW that
+// is overwritten, whether or not they get a sum later.
+struct ZeroArgs {
+    uint4* p;
+    int64_t n;               // 16-byte vectors
+};
+
+__device__ __forceinline__ void zero_share(const ZeroArgs& z, int block, int blocks) {
+    const int64_t step = (int64_t)blocks * blockDim.x;
+    for (int64_t i = (int64_t)block * blockDim.x + threadIdx.x; i < z.n; i += step) z.p[i] = make_uint4(0u, 0u, 0u, 0u);
+}
+
 constexpr int kChunk = 1024;         // pairs a block of 256 threads ranks
 constexpr int kWarps = 8;
 constexpr int kPerLane = kChunk / 256;
 constexpr int kMaxBits = 9;          // bits of a digit
 constexpr int kMaxBins = 1 << kMaxBits;
+constexpr int kMaxPasses = 4;        // 31 bits of keys
+// Bytes zeroed beside one launch of the sort: about what the memory takes in its time.
+constexpr int64_t kZeroOne = 24 << 20, kZeroHist = 12 << 20, kZeroScatter = 20 << 20;
 
 struct SortArgs {
     const int32_t* ids;      // first pass: keys are made from the ids
     const uint2* in;         // later passes: (key, token)
     uint2* out;
-    int32_t* hist;           // [chunks, bins]
+    int32_t* hist;           // [chunks, bins] of this pass
+    int32_t* hist_next;      // of the next, or null
+    int64_t later;           // first launch: counts of the later passes' histograms, to zero
+    int32_t* crossing;       // counts of crossing runs, zeroed here (see SumArgs)
     int T, V, pad;
     int shift, bits, chunks;
     int* err;
@@ -145,12 +176,32 @@ __device__ __forceinline__ uint2 sort_pair(const SortArgs& a, int i, bool report
     return make_uint2(in_range && id != a.pad ? (uint32_t)id : (uint32_t)a.V, (uint32_t)i);
 }
 
-__global__ void __launch_bounds__(256) embed_hist_kernel(SortArgs a) {
+// Lanes whose digit is this lane's, by one ballot a bit (a match instruction takes three times as
+// long where a whole SM ranks: 90 cycles a warp).
+__device__ __forceinline__ uint32_t same_digit(uint32_t dg, int bits) {
+    uint32_t same = 0xffffffffu;
+#pragma unroll
+    for (int b = 0; b <= kMaxBits; ++b) {
+        if (b > bits) break;                         // one bit more than the digit: lanes past the end
+        const uint32_t set = __ballot_sync(0xffffffffu, dg >> b & 1);
+        same &= dg >> b & 1 ? set : ~set;
+    }
+    return same;
+}
+
+__global__ void __launch_bounds__(256) embed_hist_kernel(SortArgs a, ZeroArgs z) {
     __shared__ int h[kMaxBins];
     const int bins = 1 << a.bits;
     for (int b = threadIdx.x; b < bins; b += 256) h[b] = 0;
     pdl_wait();
+    if ((int)blockIdx.x >= a.chunks) {
+        zero_share(z, blockIdx.x - a.chunks, gridDim.x - a.chunks);
+        return;
+    }
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < a.later; i += (int64_t)a.chunks * 256)
+        a.hist_next[i] = 0;
     __syncthreads();
+    if (blockIdx.x == 0 && threadIdx.x < 2) a.crossing[threadIdx.x] = 0;
     const int i0 = blockIdx.x * kChunk;
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) {
@@ -181,13 +232,17 @@ __device__ __forceinline__ void block_scan2(int& v0, int& v1, int* tmp) {
     v0 = excl;
 }
 
-__global__ void __launch_bounds__(256) embed_scatter_kernel(SortArgs a) {
+__global__ void __launch_bounds__(256) embed_scatter_kernel(SortArgs a, ZeroArgs z) {
     __shared__ int cnt[kWarps][kMaxBins];
     __shared__ int base[kMaxBins];
     __shared__ int tmp[kWarps];
     const int bins = 1 << a.bits, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int b = threadIdx.x; b < kWarps * kMaxBins; b += 256) (&cnt[0][0])[b] = 0;
     pdl_wait();
+    if ((int)blockIdx.x >= a.chunks) {
+        zero_share(z, blockIdx.x - a.chunks, gridDim.x - a.chunks);
+        return;
+    }
     __syncthreads();
     // ranks within the warp's 128 consecutive pairs: the lanes of one digit, in lane order
     uint2 pr[kPerLane];
@@ -201,8 +256,8 @@ __global__ void __launch_bounds__(256) embed_scatter_kernel(SortArgs a) {
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) {
         const bool live = i0 + k * 32 + lane < a.T;
-        const int dg = live ? (int)((pr[k].x >> a.shift) & (bins - 1)) : kMaxBins;
-        const uint32_t same = __match_any_sync(0xffffffffu, dg);
+        const int dg = live ? (int)((pr[k].x >> a.shift) & (bins - 1)) : bins;
+        const uint32_t same = same_digit(dg, a.bits);
         const int before = __popc(same & ((1u << lane) - 1u));
         const int had = live ? cnt[warp][dg] : 0;
         __syncwarp();
@@ -212,15 +267,18 @@ __global__ void __launch_bounds__(256) embed_scatter_kernel(SortArgs a) {
     }
     // every block reads the whole histogram: totals of all digits, and of the chunks before it
     int tot[2] = {0, 0}, mine[2] = {0, 0};
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int b = 2 * (int)threadIdx.x + q;
-        if (b < bins)
-            for (int c = 0; c < a.chunks; ++c) {
-                const int v = __ldg(a.hist + (int64_t)c * bins + b);
-                tot[q] += v;
-                if (c < (int)blockIdx.x) mine[q] += v;
+    if (2 * (int)threadIdx.x < bins) {
+        const int2* h = reinterpret_cast<const int2*>(a.hist) + threadIdx.x;
+#pragma unroll 8
+        for (int c = 0; c < a.chunks; ++c) {
+            const int2 v = h[(int64_t)c * (bins / 2)];
+            tot[0] += v.x;
+            tot[1] += v.y;
+            if (c < (int)blockIdx.x) {
+                mine[0] += v.x;
+                mine[1] += v.y;
             }
+        }
     }
     block_scan2(tot[0], tot[1], tmp);
 #pragma unroll
@@ -241,81 +299,131 @@ __global__ void __launch_bounds__(256) embed_scatter_kernel(SortArgs a) {
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k)
-        if (i0 + k * 32 + lane < a.T) a.out[cnt[warp][(pr[k].x >> a.shift) & (bins - 1)] + rank[k]] = pr[k];
+        if (i0 + k * 32 + lane < a.T) {
+            const int to = cnt[warp][(pr[k].x >> a.shift) & (bins - 1)] + rank[k];
+            a.out[to] = pr[k];
+            if (a.hist_next)
+                atomicAdd(a.hist_next + (int64_t)(to / kChunk) * bins + (pr[k].x >> (a.shift + a.bits) & (bins - 1)), 1);
+        }
+}
+
+// A batch of at most kOneBlock tokens is sorted by one block in one launch, in shared memory:
+// keys, tokens (16 bits) and the warps' digit counts.
+constexpr int kOneBlock = 4096;
+constexpr int kOneThreads = 1024;
+constexpr int kOneWarps = kOneThreads / 32;
+constexpr int kOneEach = kOneBlock / kOneThreads;
+
+__global__ void __launch_bounds__(kOneThreads) embed_sort_kernel(SortArgs a, int passes, ZeroArgs z) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    uint32_t* keys = reinterpret_cast<uint32_t*>(smem);
+    uint16_t* toks = reinterpret_cast<uint16_t*>(keys + kOneBlock);
+    uint16_t(*cnt)[kMaxBins] = reinterpret_cast<uint16_t(*)[kMaxBins]>(toks + kOneBlock);
+    __shared__ int total[kMaxBins], tmp[kOneWarps];
+    pdl_wait();
+    if (blockIdx.x > 0) {
+        zero_share(z, blockIdx.x - 1, gridDim.x - 1);
+        return;
+    }
+    if (threadIdx.x < 2) a.crossing[threadIdx.x] = 0;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, bins = 1 << a.bits;
+    // a warp holds consecutive pairs, `each` to a lane; a shorter batch takes fewer
+    const int each = (a.T + kOneThreads - 1) / kOneThreads, i0 = warp * each * 32;
+    uint32_t key[kOneEach], tok[kOneEach], rank[kOneEach];
+#pragma unroll
+    for (int k = 0; k < kOneEach; ++k) {
+        const int i = i0 + k * 32 + lane;
+        key[k] = 0;
+        tok[k] = (uint32_t)i;
+        if (k < each && i < a.T) key[k] = sort_pair(a, i, true).x;
+    }
+    for (int p = 0; p < passes; ++p) {
+        const int shift = p * a.bits;
+        for (int b = threadIdx.x; b < kOneWarps * kMaxBins / 2; b += kOneThreads) reinterpret_cast<uint32_t*>(cnt)[b] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kOneEach; ++k) {
+            if (k >= each) break;
+            const bool live = i0 + k * 32 + lane < a.T;
+            const uint32_t dg = live ? key[k] >> shift & (bins - 1) : (uint32_t)bins;
+            const uint32_t same = same_digit(dg, a.bits);
+            const uint32_t before = __popc(same & ((1u << lane) - 1u));
+            const uint32_t had = live ? cnt[warp][dg] : 0u;
+            __syncwarp();
+            if (live && before == 0) cnt[warp][dg] = (uint16_t)(had + __popc(same));
+            __syncwarp();
+            rank[k] = had + before;
+        }
+        __syncthreads();
+        // counts before each warp within a digit, then before each digit
+        if (threadIdx.x < kMaxBins) {
+            int run = 0;
+            if ((int)threadIdx.x < bins)
+#pragma unroll 8
+                for (int w = 0; w < kOneWarps; ++w) {
+                    const int n = cnt[w][threadIdx.x];
+                    cnt[w][threadIdx.x] = (uint16_t)run;
+                    run += n;
+                }
+            int x = run;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int n = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += n;
+            }
+            if (lane == 31) tmp[warp] = x;
+            total[threadIdx.x] = x - run;
+        }
+        __syncthreads();
+        if (threadIdx.x < kMaxBins) {
+            int before = 0;
+            for (int w = 0; w < warp; ++w) before += tmp[w];
+            total[threadIdx.x] += before;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kOneEach; ++k) {
+            if (k >= each) break;
+            if (i0 + k * 32 + lane < a.T) {
+                const uint32_t dg = key[k] >> shift & (bins - 1);
+                const uint32_t to = (uint32_t)total[dg] + cnt[warp][dg] + rank[k];
+                keys[to] = key[k];
+                toks[to] = (uint16_t)tok[k];
+            }
+        }
+        __syncthreads();
+        if (p + 1 < passes)
+#pragma unroll
+            for (int k = 0; k < kOneEach; ++k) {
+                const int i = i0 + k * 32 + lane;
+                if (k < each && i < a.T) {
+                    key[k] = keys[i];
+                    tok[k] = toks[i];
+                }
+            }
+    }
+    for (int i = threadIdx.x; i < a.T; i += kOneThreads) a.out[i] = make_uint2(keys[i], toks[i]);
 }
 
 // ---------------------------------------------------------------- gradient: sums over runs
-// The sorted pairs are cut into groups of kGroup. A thread owns VE columns of one group and
-// walks its rows in order; a run of one token that lies inside the group is finished there. A
-// run that crosses groups leaves one fp32 partial row in each (slot 0: the run the group begins
-// with, slot 1: the run it ends with and that begins in it), and embed_join_kernel adds them
+// The sorted pairs are cut into groups of kGroup. A thread owns VE columns of one group, loads
+// them of all its rows (and of the dW rows that it will add to) at once, and walks them in
+// order; a run of one token that lies inside the group is finished there. A run that crosses
+// groups leaves one fp32 partial row in each (slot 0: the run the group begins with, slot 1: the
+// run it ends with and that begins in it) and an entry in a list, and embed_join_kernel adds them
 // in group order. Every row of dW has one writer and a fixed order of sums.
-constexpr int kGroup = 32;
+constexpr int kGroup = 8;
+constexpr int kLong = 32;        // a run over more groups than this is joined by a whole block
 
 struct SumArgs {
     const uint2* pairs;      // sorted (key, token)
     float* part;             // [groups, 2, d]
+    int32_t* crossing;       // counts of crossing runs: short ones, long ones
+    uint2* heads;            // [2, groups] their keys and the groups they begin in, in any order
     int T, V, d, groups;
-    int accumulate;
+    int zero_from;           // first row that this launch zeroes if it gets no sum; V: none
     float scale;
 };
-
-template <typename G, int VE>
-__device__ __forceinline__ void put_row(const SumArgs& a, G* dW, uint32_t key, int col, float (&s)[VE]) {
-    G* p = dW + (int64_t)key * a.d + col;
-#pragma unroll
-    for (int i = 0; i < VE; ++i) s[i] *= a.scale;
-    if (a.accumulate) {
-        float o[VE];
-        Vec<G, VE>::load(p, o);
-#pragma unroll
-        for (int i = 0; i < VE; ++i) s[i] += o[i];
-    }
-    Vec<G, VE>::store(p, s);
-}
-
-template <typename T, typename G, int VE>
-__global__ void __launch_bounds__(256) embed_sum_kernel(SumArgs a, const T* __restrict__ dy, G* __restrict__ dW) {
-    __shared__ uint2 pr[kGroup + 2];   // the group's pairs, with a neighbour on either side
-    pdl_wait();
-    const int g = blockIdx.x, i0 = g * kGroup, n = min(kGroup, a.T - i0);
-    for (int j = threadIdx.x; j < kGroup + 2; j += blockDim.x) {
-        const int i = i0 + j - 1;
-        pr[j] = i >= 0 && i < a.T ? a.pairs[i] : make_uint2(0xffffffffu, 0u);
-    }
-    __syncthreads();
-    for (int col = (blockIdx.y * blockDim.x + threadIdx.x) * VE; col < a.d; col += gridDim.y * blockDim.x * VE) {
-        float s[VE];
-#pragma unroll
-        for (int i = 0; i < VE; ++i) s[i] = 0.f;
-        bool from_before = pr[0].x == pr[1].x;
-        for (int j0 = 0; j0 < n; j0 += 8) {
-            float r[8][VE];
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j0 + j < n && pr[j0 + j + 1].x < (uint32_t)a.V)
-                    Vec<T, VE>::load(dy + (int64_t)pr[j0 + j + 1].y * a.d + col, r[j]);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (j0 + j >= n) break;
-                const uint32_t key = pr[j0 + j + 1].x;
-                if (key >= (uint32_t)a.V) break;
-#pragma unroll
-                for (int i = 0; i < VE; ++i) s[i] += r[j][i];
-                const bool ends = pr[j0 + j + 2].x != key;
-                if (ends || j0 + j + 1 == n) {
-                    if (ends && !from_before)
-                        put_row(a, dW, key, col, s);
-                    else
-                        Vec<float, VE>::store(a.part + ((int64_t)g * 2 + (from_before ? 0 : 1)) * a.d + col, s);
-                    from_before = false;
-#pragma unroll
-                    for (int i = 0; i < VE; ++i) s[i] = 0.f;
-                }
-            }
-        }
-    }
-}
 
 // First position whose key is >= key.
 __device__ __forceinline__ int lower_bound(const uint2* p, int n, uint32_t key) {
@@ -327,33 +435,143 @@ __device__ __forceinline__ int lower_bound(const uint2* p, int n, uint32_t key) 
     return lo;
 }
 
-// Runs that begin in group blockIdx.x and go on past it: their partial rows, in order. Eight
-// warps take every eighth partial of the same columns; their sums are added in warp order.
+// Zero rows of tokens that do not occur. A block owns 64 rows: one search for its first key,
+// then the sorted keys of its rows mark the ones that were seen.
+constexpr int kZeroRows = 64;
 template <typename G, int VE>
+__device__ __forceinline__ void zero_rows(const SumArgs& a, G* dW, int block) {
+    __shared__ int seen[kZeroRows];
+    __shared__ int lo, hi;
+    for (int i = threadIdx.x; i < kZeroRows; i += blockDim.x) seen[i] = 0;
+    const int v0 = a.zero_from + block * kZeroRows, v1 = min(v0 + kZeroRows, a.V);
+    if (threadIdx.x == 0) lo = lower_bound(a.pairs, a.T, (uint32_t)v0);
+    if (threadIdx.x == 32) hi = lower_bound(a.pairs, a.T, (uint32_t)v1);
+    __syncthreads();
+    for (int i = lo + threadIdx.x; i < hi; i += blockDim.x) seen[a.pairs[i].x - v0] = 1;
+    __syncthreads();
+    float z[VE];
+#pragma unroll
+    for (int i = 0; i < VE; ++i) z[i] = 0.f;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int v = v0 + warp; v < v1; v += blockDim.x >> 5)
+        if (!seen[v - v0])
+            for (int c = lane * VE; c < a.d; c += 32 * VE) Vec<G, VE>::store(dW + (int64_t)v * a.d + c, z);
+}
+
+template <typename T, typename G, int VE, bool kAdd>
+__global__ void __launch_bounds__(256) embed_sum_kernel(SumArgs a, const T* __restrict__ dy, G* __restrict__ dW) {
+    __shared__ uint2 pr[kGroup + 2];   // the group's pairs, with a neighbour on either side
+    pdl_wait();
+    if ((int)blockIdx.x >= a.groups) {
+        if (blockIdx.y == 0) zero_rows<G, VE>(a, dW, blockIdx.x - a.groups);
+        return;
+    }
+    const int g = blockIdx.x, i0 = g * kGroup;
+    if ((int)threadIdx.x < kGroup + 2) {
+        const int i = i0 + (int)threadIdx.x - 1;
+        pr[threadIdx.x] = i >= 0 && i < a.T ? a.pairs[i] : make_uint2(0xffffffffu, 0u);
+    }
+    __syncthreads();
+    for (int col = (blockIdx.y * blockDim.x + threadIdx.x) * VE; col < a.d; col += gridDim.y * blockDim.x * VE) {
+        float s[VE];
+#pragma unroll
+        for (int i = 0; i < VE; ++i) s[i] = 0.f;
+        bool from_before = pr[0].x == pr[1].x;
+        // adding to dW, half a group at a time: its old rows take registers too
+        constexpr int kAtOnce = kAdd ? kGroup / 2 : kGroup;
+#pragma unroll
+        for (int j0 = 0; j0 < kGroup; j0 += kAtOnce) {
+            Bits<T, VE> r[kAtOnce];
+            Bits<G, kAdd ? VE : 1> old[kAtOnce];
+            bool before = from_before;
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+                const uint2 q = pr[j0 + j + 1];
+                if (q.x >= (uint32_t)a.V) continue;
+                r[j].load(dy + (int64_t)q.y * a.d + col);
+                if constexpr (kAdd) {
+                    const bool ends = pr[j0 + j + 2].x != q.x;
+                    if (ends && !before) old[j].load(dW + (int64_t)q.x * a.d + col);
+                    before = before && !ends;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+                const uint32_t key = pr[j0 + j + 1].x;
+                if (key >= (uint32_t)a.V) break;
+#pragma unroll
+                for (int i = 0; i < VE; ++i) s[i] += r[j].at(i);
+                const bool ends = pr[j0 + j + 2].x != key;
+                if (!ends && j0 + j + 1 < kGroup) continue;
+                if (ends && !from_before) {
+#pragma unroll
+                    for (int i = 0; i < VE; ++i) s[i] *= a.scale;
+                    if constexpr (kAdd)
+#pragma unroll
+                        for (int i = 0; i < VE; ++i) s[i] += old[j].at(i);
+                    Vec<G, VE>::store(dW + (int64_t)key * a.d + col, s);
+                } else {
+                    Vec<float, VE>::store(a.part + ((int64_t)g * 2 + (from_before ? 0 : 1)) * a.d + col, s);
+                    if (!ends && !from_before && col == 0) {
+                        const int64_t far = (int64_t)(g + kLong) * kGroup;
+                        const int is_long = far < a.T && a.pairs[far].x == key;
+                        a.heads[(int64_t)is_long * a.groups + atomicAdd(a.crossing + is_long, 1)] = make_uint2(key, g);
+                    }
+                }
+                from_before = false;
+#pragma unroll
+                for (int i = 0; i < VE; ++i) s[i] = 0.f;
+            }
+        }
+    }
+}
+
+// The crossing runs' partial rows, in order, 32 * VE columns at a time: one by a warp, or a long
+// one by a block, whose eight warps take every eighth partial and whose sums are added in warp
+// order.
+template <typename G, int VE, bool kAdd>
+__device__ __forceinline__ void join_row(const SumArgs& a, G* dW, uint32_t key, int col, float (&s)[VE]) {
+    G* p = dW + (int64_t)key * a.d + col;
+    float old[VE];
+    if constexpr (kAdd) Vec<G, VE>::load(p, old);
+#pragma unroll
+    for (int i = 0; i < VE; ++i) s[i] = kAdd ? fmaf(s[i], a.scale, old[i]) : s[i] * a.scale;
+    Vec<G, VE>::store(p, s);
+}
+
+template <typename G, int VE, bool kAdd>
 __global__ void __launch_bounds__(256) embed_join_kernel(SumArgs a, G* __restrict__ dW) {
     __shared__ float part[kWarps][32 * VE];
     pdl_wait();
-    const int g = blockIdx.x, last = (g + 1) * kGroup - 1;
-    if (last + 1 >= a.T) return;
-    const uint32_t key = a.pairs[last].x;
-    if (key >= (uint32_t)a.V || a.pairs[last + 1].x != key) return;
-    if (g > 0 && a.pairs[g * kGroup - 1].x == key) return;     // it began before this group
-    const int end = lower_bound(a.pairs, a.T, key + 1);
-    const int parts = (end - 1) / kGroup - g + 1;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int c0 = blockIdx.y * 32 * VE; c0 < a.d; c0 += gridDim.y * 32 * VE) {
-        const int col = c0 + lane * VE;
+    const int slabs = (a.d + 32 * VE - 1) / (32 * VE);
+    const auto add = [&](float (&s)[VE], int g, int k, int col) {
+        float r[VE];
+        Vec<float, VE>::load(a.part + ((int64_t)(g + k) * 2 + (k ? 0 : 1)) * a.d + col, r);
+#pragma unroll
+        for (int i = 0; i < VE; ++i) s[i] += r[i];
+    };
+    // groups after g that the run of `key` reaches into, looked at 32 at a time
+    const auto reach = [&](int g, uint32_t key) {
+        int n = 0;
+        for (;; n += 32) {
+            const int64_t i = (int64_t)(g + 1 + n + lane) * kGroup;
+            const uint32_t in = __ballot_sync(0xffffffffu, i < a.T && a.pairs[i].x == key);
+            if (in != 0xffffffffu) return n + __popc(in);
+        }
+    };
+    const int64_t n_long = (int64_t)a.crossing[1] * slabs, n_short = (int64_t)a.crossing[0] * slabs;
+    for (int64_t q = blockIdx.x; q < n_long; q += gridDim.x) {
+        const uint2 head = a.heads[a.groups + q / slabs];
+        const int g = (int)head.y, col = ((int)(q % slabs) * 32 + lane) * VE;
+        const uint32_t key = head.x;
+        const int parts = 1 + reach(g, key);
         float s[VE];
 #pragma unroll
         for (int i = 0; i < VE; ++i) s[i] = 0.f;
         if (col < a.d)
 #pragma unroll 4
-            for (int k = warp; k < parts; k += kWarps) {
-                float r[VE];
-                Vec<float, VE>::load(a.part + ((int64_t)(g + k) * 2 + (k ? 0 : 1)) * a.d + col, r);
-#pragma unroll
-                for (int i = 0; i < VE; ++i) s[i] += r[i];
-            }
+            for (int k = warp; k < parts; k += kWarps) add(s, g, k, col);
 #pragma unroll
         for (int i = 0; i < VE; ++i) part[warp][lane * VE + i] = s[i];
         __syncthreads();
@@ -362,40 +580,35 @@ __global__ void __launch_bounds__(256) embed_join_kernel(SumArgs a, G* __restric
             for (int w = 1; w < kWarps; ++w)
 #pragma unroll
                 for (int i = 0; i < VE; ++i) s[i] += part[w][lane * VE + i];
-            put_row(a, dW, key, col, s);
+            join_row<G, VE, kAdd>(a, dW, key, col, s);
         }
         __syncthreads();
     }
-}
-
-// Zero rows of tokens that do not occur. A block owns 64 rows: one search for its first key,
-// then the sorted keys of its rows mark the ones that were seen.
-constexpr int kZeroRows = 64;
-template <typename G, int VE>
-__global__ void __launch_bounds__(256) embed_zero_kernel(const uint2* __restrict__ pairs, G* __restrict__ dW, int T, int V, int d) {
-    __shared__ int seen[kZeroRows];
-    __shared__ int lo, hi;
-    for (int i = threadIdx.x; i < kZeroRows; i += 256) seen[i] = 0;
-    pdl_wait();
-    const int v0 = blockIdx.x * kZeroRows, v1 = min(v0 + kZeroRows, V);
-    if (threadIdx.x == 0) lo = lower_bound(pairs, T, (uint32_t)v0);
-    if (threadIdx.x == 32) hi = lower_bound(pairs, T, (uint32_t)v1);
-    __syncthreads();
-    for (int i = lo + threadIdx.x; i < hi; i += 256) seen[pairs[i].x - v0] = 1;
-    __syncthreads();
-    float z[VE];
+    for (int64_t q = (int64_t)blockIdx.x * kWarps + warp; q < n_short; q += (int64_t)gridDim.x * kWarps) {
+        const uint2 head = a.heads[q / slabs];
+        const int g = (int)head.y, col = ((int)(q % slabs) * 32 + lane) * VE;
+        const uint32_t key = head.x;
+        float s[VE];
 #pragma unroll
-    for (int i = 0; i < VE; ++i) z[i] = 0.f;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int v = v0 + warp; v < v1; v += kWarps)
-        if (!seen[v - v0])
-            for (int c = lane * VE; c < d; c += 32 * VE) Vec<G, VE>::store(dW + (int64_t)v * d + c, z);
+        for (int i = 0; i < VE; ++i) s[i] = 0.f;
+        if (col < a.d) {
+            add(s, g, 0, col);                       // there are two parts at least
+            add(s, g, 1, col);
+        }
+        const int parts = 1 + reach(g, key);
+        if (col >= a.d) continue;
+#pragma unroll 4
+        for (int k = 2; k < parts; ++k) add(s, g, k, col);
+        join_row<G, VE, kAdd>(a, dW, key, col, s);
+    }
 }
 
 struct EmbedScratch {
     uint2* a;
     uint2* b;
     int32_t* hist;
+    int32_t* crossing;
+    uint2* heads;
     float* part;
 };
 
@@ -405,35 +618,37 @@ size_t carve_embed(const moe_embed_config_t& c, void* base, EmbedScratch* s) {
     Workspace ws{static_cast<char*>(base), 0};
     s->a = ws.take<uint2>((size_t)c.T + 1);
     s->b = ws.take<uint2>((size_t)c.T + 1);
-    s->hist = ws.take<int32_t>((size_t)ceil_div(c.T, kChunk) * kMaxBins + 1);
+    s->hist = ws.take<int32_t>((size_t)ceil_div(c.T, kChunk) * kMaxBins * kMaxPasses + 1);
+    s->crossing = ws.take<int32_t>(2);
+    s->heads = ws.take<uint2>((size_t)groups_of(c) * 2 + 1);
     s->part = ws.take<float>((size_t)groups_of(c) * 2 * c.d + 4);
     return align_up(ws.used, 256);
 }
 
-template <typename T, typename G, int VE>
-cudaError_t launch_embed_bwd_v(const moe_embed_config_t& c, const uint2* pairs, float* part, const void* dy, void* dW,
-                               cudaStream_t s) {
-    cudaError_t e = cudaSuccess;
+template <typename T, typename G, int VE, bool kAdd>
+cudaError_t launch_sums(const moe_embed_config_t& c, SumArgs a, const void* dy, void* dW, cudaStream_t s) {
     const int nvec = c.d / VE;
     G* out = static_cast<G*>(dW);
-    if (c.T > 0) {
-        SumArgs a{pairs, part, c.T, c.V, c.d, groups_of(c), c.accumulate, c.scale};
-        const int threads = std::min(256, ceil_div(nvec, 32) * 32);
-        e = launch_pdl(embed_sum_kernel<T, G, VE>, dim3(a.groups, std::min(ceil_div(nvec, threads), 64)), dim3(threads),
-                       0, s, a, static_cast<const T*>(dy), out);
-        count_launch();
-        if (e != cudaSuccess) return e;
-        e = launch_pdl(embed_join_kernel<G, VE>, dim3(a.groups, std::min(ceil_div(nvec, 32), 64)), dim3(256), 0, s, a,
-                       out);
-        count_launch();
-        if (e != cudaSuccess) return e;
-    }
-    if (!c.accumulate) {
-        e = launch_pdl(embed_zero_kernel<G, VE>, dim3(ceil_div(c.V, kZeroRows)), dim3(256), 0, s, pairs, out, c.T, c.V,
-                       c.d);
+    const int threads = std::max(64, std::min(256, ceil_div(nvec, 32) * 32));
+    const int zero = kAdd ? 0 : ceil_div(a.V - a.zero_from, kZeroRows);
+    cudaError_t e = cudaSuccess;
+    if (a.groups + zero > 0) {
+        e = launch_pdl(embed_sum_kernel<T, G, VE, kAdd>, dim3(a.groups + zero, std::min(ceil_div(nvec, threads), 64)),
+                       dim3(threads), 0, s, a, static_cast<const T*>(dy), out);
         count_launch();
     }
+    if (e != cudaSuccess || a.groups < 2) return e;      // one group has no run that leaves it
+    // as many warps as there can be items, up to what the SMs hold
+    const int64_t items = (int64_t)a.groups * ceil_div(nvec, 32);
+    e = launch_pdl(embed_join_kernel<G, VE, kAdd>, dim3((unsigned)std::min<int64_t>((items + 7) / 8, num_sms() * 6)),
+                   dim3(256), 0, s, a, out);
+    count_launch();
     return e;
+}
+
+template <typename T, typename G, int VE>
+cudaError_t launch_embed_bwd_v(const moe_embed_config_t& c, const SumArgs& a, const void* dy, void* dW, cudaStream_t s) {
+    return c.accumulate ? launch_sums<T, G, VE, true>(c, a, dy, dW, s) : launch_sums<T, G, VE, false>(c, a, dy, dW, s);
 }
 
 template <typename T, typename G>
@@ -441,32 +656,61 @@ cudaError_t launch_embed_bwd(const moe_embed_config_t& c, const int32_t* ids, co
                              cudaStream_t s) {
     EmbedScratch w;
     carve_embed(c, ws, &w);
-    const uint2* sorted = w.a;
+    SumArgs sums{w.a, w.part, w.crossing, w.heads, c.T, c.V, c.d, groups_of(c), 0, c.scale};
     if (c.T > 0) {
         int bits = 1;
         while (((int64_t)1 << bits) <= c.V) ++bits;          // keys 0 .. V
         const int passes = ceil_div(bits, kMaxBits), digit = ceil_div(bits, passes);
-        SortArgs a{ids, nullptr, w.a, w.hist, c.T, c.V, c.padding_id, 0, digit, ceil_div(c.T, kChunk),
-                   device_error_word()};
-        for (int p = 0; p < passes; ++p) {
-            a.shift = p * digit;
-            cudaError_t e = launch_pdl(embed_hist_kernel, dim3(a.chunks), dim3(256), 0, s, a);
+        SortArgs a{ids, nullptr, w.a, w.hist, nullptr, 0, w.crossing, c.T, c.V, c.padding_id, 0, digit,
+                   ceil_div(c.T, kChunk), device_error_word()};
+        // the next `wish` bytes of dW, in whole rows whose bytes are a multiple of 16, and blocks for them
+        const int64_t row = (int64_t)c.d * (int64_t)sizeof(G);
+        unsigned blocks = 0;
+        const auto zero_next = [&](int64_t wish) {
+            const int rows = c.accumulate ? 0 : (int)std::min<int64_t>(c.V - sums.zero_from, wish / row) & ~15;
+            ZeroArgs z{reinterpret_cast<uint4*>(static_cast<char*>(dW) + sums.zero_from * row), rows * row / 16};
+            sums.zero_from += rows;
+            blocks = (unsigned)std::min<int64_t>(4 * num_sms(), (z.n + 2047) / 2048);
+            return z;
+        };
+        cudaError_t e;
+        if (c.T <= kOneBlock) {
+            constexpr int smem = kOneBlock * 6 + kOneWarps * kMaxBins * 2;
+            e = cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
             if (e != cudaSuccess) return e;
-            e = launch_pdl(embed_scatter_kernel, dim3(a.chunks), dim3(256), 0, s, a);
+            const ZeroArgs z = zero_next(kZeroOne);
+            e = launch_pdl(embed_sort_kernel, dim3(1 + blocks), dim3(kOneThreads), (size_t)smem, s, a, passes, z);
+            count_launch();
             if (e != cudaSuccess) return e;
-            count_launch(2);
-            sorted = a.out;
-            a.in = a.out;
-            a.out = a.out == w.a ? w.b : w.a;
+        } else {
+            const int64_t size = (int64_t)a.chunks << digit;
+            a.hist_next = w.hist + size;
+            a.later = size * (passes - 1);
+            ZeroArgs z = zero_next(kZeroHist);
+            e = launch_pdl(embed_hist_kernel, dim3(a.chunks + blocks), dim3(256), 0, s, a, z);
+            count_launch();
+            if (e != cudaSuccess) return e;
+            for (int p = 0; p < passes; ++p) {
+                a.shift = p * digit;
+                a.hist = w.hist + size * p;
+                a.hist_next = p + 1 < passes ? a.hist + size : nullptr;
+                z = zero_next(kZeroScatter);
+                e = launch_pdl(embed_scatter_kernel, dim3(a.chunks + blocks), dim3(256), 0, s, a, z);
+                count_launch();
+                if (e != cudaSuccess) return e;
+                sums.pairs = a.out;
+                a.in = a.out;
+                a.out = a.out == w.a ? w.b : w.a;
+            }
         }
     }
     // the widest vector of the dy rows; a dW of another type moves as many elements at once
     switch (row_vec(c.d, (int)sizeof(T))) {
         case 8:
-            if constexpr (sizeof(T) == 2) return launch_embed_bwd_v<T, G, 8>(c, sorted, w.part, dy, dW, s);
-        case 4: return launch_embed_bwd_v<T, G, 4>(c, sorted, w.part, dy, dW, s);
-        case 2: return launch_embed_bwd_v<T, G, 2>(c, sorted, w.part, dy, dW, s);
-        default: return launch_embed_bwd_v<T, G, 1>(c, sorted, w.part, dy, dW, s);
+            if constexpr (sizeof(T) == 2) return launch_embed_bwd_v<T, G, 8>(c, sums, dy, dW, s);
+        case 4: return launch_embed_bwd_v<T, G, 4>(c, sums, dy, dW, s);
+        case 2: return launch_embed_bwd_v<T, G, 2>(c, sums, dy, dW, s);
+        default: return launch_embed_bwd_v<T, G, 1>(c, sums, dy, dW, s);
     }
 }
 
