@@ -253,18 +253,6 @@ __global__ void __launch_bounds__(256) embed_scatter_kernel(SortArgs a, ZeroArgs
         const int i = i0 + k * 32 + lane;
         pr[k] = i < a.T ? sort_pair(a, i, false) : make_uint2(0u, 0u);
     }
-#pragma unroll
-    for (int k = 0; k < kPerLane; ++k) {
-        const bool live = i0 + k * 32 + lane < a.T;
-        const int dg = live ? (int)((pr[k].x >> a.shift) & (bins - 1)) : bins;
-        const uint32_t same = same_digit(dg, a.bits);
-        const int before = __popc(same & ((1u << lane) - 1u));
-        const int had = live ? cnt[warp][dg] : 0;
-        __syncwarp();
-        if (live && before == 0) cnt[warp][dg] = had + __popc(same);
-        __syncwarp();
-        rank[k] = had + before;
-    }
     // every block reads the whole histogram: totals of all digits, and of the chunks before it
     int tot[2] = {0, 0}, mine[2] = {0, 0};
     if (2 * (int)threadIdx.x < bins) {
@@ -279,6 +267,18 @@ __global__ void __launch_bounds__(256) embed_scatter_kernel(SortArgs a, ZeroArgs
                 mine[1] += v.y;
             }
         }
+    }
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) {
+        const bool live = i0 + k * 32 + lane < a.T;
+        const int dg = live ? (int)((pr[k].x >> a.shift) & (bins - 1)) : bins;
+        const uint32_t same = same_digit(dg, a.bits);
+        const int before = __popc(same & ((1u << lane) - 1u));
+        const int had = live ? cnt[warp][dg] : 0;
+        __syncwarp();
+        if (live && before == 0) cnt[warp][dg] = had + __popc(same);
+        __syncwarp();
+        rank[k] = had + before;
     }
     block_scan2(tot[0], tot[1], tmp);
 #pragma unroll
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(kOneThreads) embed_sort_kernel(SortArgs a, int
 // run it ends with and that begins in it) and an entry in a list, and embed_join_kernel adds them
 // in group order. Every row of dW has one writer and a fixed order of sums.
 constexpr int kGroup = 8;
-constexpr int kLong = 32;        // a run over more groups than this is joined by a whole block
+constexpr int kLong = 16;        // a run over more groups than this is joined by a whole block
 
 struct SumArgs {
     const uint2* pairs;      // sorted (key, token)
@@ -551,26 +551,22 @@ __global__ void __launch_bounds__(256) embed_join_kernel(SumArgs a, G* __restric
 #pragma unroll
         for (int i = 0; i < VE; ++i) s[i] += r[i];
     };
-    // groups after g that the run of `key` reaches into, looked at 32 at a time
-    const auto reach = [&](int g, uint32_t key) {
-        int n = 0;
-        for (;; n += 32) {
-            const int64_t i = (int64_t)(g + 1 + n + lane) * kGroup;
-            const uint32_t in = __ballot_sync(0xffffffffu, i < a.T && a.pairs[i].x == key);
-            if (in != 0xffffffffu) return n + __popc(in);
-        }
-    };
     const int64_t n_long = (int64_t)a.crossing[1] * slabs, n_short = (int64_t)a.crossing[0] * slabs;
     for (int64_t q = blockIdx.x; q < n_long; q += gridDim.x) {
         const uint2 head = a.heads[a.groups + q / slabs];
         const int g = (int)head.y, col = ((int)(q % slabs) * 32 + lane) * VE;
         const uint32_t key = head.x;
-        const int parts = 1 + reach(g, key);
+        // groups that the run reaches into, looked at 256 at a time
+        int parts = 1;
+        for (int in = 256; in == 256; parts += in) {
+            const int64_t i = (int64_t)(g + parts + (int)threadIdx.x) * kGroup;
+            in = __syncthreads_count(i < a.T && a.pairs[i].x == key);
+        }
         float s[VE];
 #pragma unroll
         for (int i = 0; i < VE; ++i) s[i] = 0.f;
         if (col < a.d)
-#pragma unroll 4
+#pragma unroll 8
             for (int k = warp; k < parts; k += kWarps) add(s, g, k, col);
 #pragma unroll
         for (int i = 0; i < VE; ++i) part[warp][lane * VE + i] = s[i];
@@ -595,9 +591,11 @@ __global__ void __launch_bounds__(256) embed_join_kernel(SumArgs a, G* __restric
             add(s, g, 0, col);                       // there are two parts at least
             add(s, g, 1, col);
         }
-        const int parts = 1 + reach(g, key);
+        static_assert(kLong <= 32, "one look finds a short run's end");
+        const int64_t i = (int64_t)(g + 1 + lane) * kGroup;
+        const int parts = 1 + __popc(__ballot_sync(0xffffffffu, i < a.T && a.pairs[i].x == key));
         if (col >= a.d) continue;
-#pragma unroll 4
+#pragma unroll 8
         for (int k = 2; k < parts; ++k) add(s, g, k, col);
         join_row<G, VE, kAdd>(a, dW, key, col, s);
     }

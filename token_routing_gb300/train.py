@@ -8,7 +8,19 @@ import math
 import torch
 
 from . import _lib as L
-from .layer import MOE_DTYPE, TORCH_DTYPE, _p, _s
+from .layer import MOE_DTYPE, TORCH_DTYPE
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream(stream, t):
+    """The stream's handle. The current one is asked for as a number: a torch.cuda.Stream object for
+    each call would take longer (3 us) than the call itself."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(t.device.index) if t.is_cuda else 0
 
 
 def _want(what, t, dtype, shape, optional=False):
@@ -45,7 +57,7 @@ def embed(cfg, ids, W, y, stream=None):
     _want("ids", ids, torch.int32, (cfg.T,))
     _want("W", W, dt, (cfg.V, cfg.d))
     _want("y", y, dt, (cfg.T, cfg.d))
-    L.check("moe_embed", L.load().moe_embed(ctypes.byref(cfg), _p(ids), _p(W), _p(y), _s(stream)))
+    L.check("moe_embed", L.load().moe_embed(ctypes.byref(cfg), _ptr(ids), _ptr(W), _ptr(y), _stream(stream, W)))
 
 
 def embed_workspace_bytes(cfg):
@@ -59,7 +71,7 @@ def embed_backward(cfg, ids, dy, dW, ws, stream=None):
     _want("dW", dW, _TORCH[cfg.grad_dtype], (cfg.V, cfg.d))
     _room("ws", ws, embed_workspace_bytes(cfg))
     L.check("moe_embed_backward", L.load().moe_embed_backward(
-        ctypes.byref(cfg), _p(ids), _p(dy), _p(dW), _p(ws), _s(stream)))
+        ctypes.byref(cfg), _ptr(ids), _ptr(dy), _ptr(dW), _ptr(ws), _stream(stream, dW)))
 
 
 # ---------------------------------------------------------------- policy loss
@@ -103,8 +115,8 @@ def policy_loss(cfg, logits, target, advantage, old_logp, ref_logp, weight, logp
     if loss is not None:
         _room("ws", ws, policy_workspace_bytes(cfg))
     L.check("moe_policy_loss", L.load().moe_policy_loss(
-        ctypes.byref(cfg), _p(logits), _p(target), _p(advantage), _p(old_logp), _p(ref_logp), _p(weight), _p(logp),
-        _p(loss), _p(dlogits), _p(ws), _s(stream)))
+        ctypes.byref(cfg), _ptr(logits), _ptr(target), _ptr(advantage), _ptr(old_logp), _ptr(ref_logp), _ptr(weight), _ptr(logp),
+        _ptr(loss), _ptr(dlogits), _ptr(ws), _stream(stream, logits)))
 
 
 def token_logp(cfg, logits, target, logp, stream=None):
@@ -112,7 +124,8 @@ def token_logp(cfg, logits, target, logp, stream=None):
     _rows("logits", logits, cfg, cfg.ld)
     _want("target", target, torch.int32, (cfg.T,))
     _want("logp", logp, torch.float32, (cfg.T,))
-    L.check("moe_token_logp", L.load().moe_token_logp(ctypes.byref(cfg), _p(logits), _p(target), _p(logp), _s(stream)))
+    L.check("moe_token_logp", L.load().moe_token_logp(ctypes.byref(cfg), _ptr(logits), _ptr(target), _ptr(logp),
+                                                           _stream(stream, logits)))
 
 
 # ---------------------------------------------------------------- AdamW
@@ -185,8 +198,8 @@ class AdamW:
         for what, t in (("lr", lr), ("grad_scale", grad_scale)):
             if t is not None and (t.dtype != torch.float32 or t.numel() != 1):
                 raise ValueError(f"{what}: one fp32 element")
-        L.check("moe_adamw", L.load().moe_adamw(ctypes.byref(self.cfg), self.table, len(self.tensors), _p(lr),
-                                                _p(grad_scale), _p(self.state), _s(stream)))
+        L.check("moe_adamw", L.load().moe_adamw(ctypes.byref(self.cfg), self.table, len(self.tensors), _ptr(lr),
+                                                _ptr(grad_scale), _ptr(self.state), _stream(stream, self.state)))
 
     def steps_done(self):
         """Steps that the device has counted (synchronises)."""
