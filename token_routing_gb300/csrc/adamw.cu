@@ -15,7 +15,7 @@ constexpr int kThreads = 256;
 constexpr int kUnit = MOE_ADAMW_BLOCK;     // elements a warp takes at a time: 8 a lane, one scale block
 constexpr uint32_t kTicket = 1024;         // blocks that may take a ticket each
 constexpr int kRun = 16;                    // longest run
-constexpr int kBatch = 256;                // tensors in one launch's parameters
+constexpr int kBatch = kThreads;           // tensors in one launch's parameters, one looked at by each thread
 
 struct TensorArg {
     void* p;
@@ -331,43 +331,55 @@ __device__ __forceinline__ void run_units(const TensorArg& t, const Step& s, int
 template <bool kNarrow>
 __device__ __noinline__ void last_unit(const TensorArg& t, const Step& s, int64_t u, int lane) {
     const int64_t i0 = u * kUnit + lane * 8;
-    float f[4][8];
     const auto live = [&](int i) { return i0 + i < t.n; };
-    constexpr bool narrow = kNarrow;
-    for (int i = 0; i < 8; ++i) {
-        f[0][i] = f[1][i] = f[2][i] = f[3][i] = 0.f;
-        if (!live(i)) continue;
-        f[0][i] = t.w ? t.w[i0 + i] : t.kind & 1 ? ld_f(static_cast<const __nv_bfloat16*>(t.p) + i0 + i)
-                                                 : static_cast<const float*>(t.p)[i0 + i];
-        f[1][i] = t.kind & 2 ? ld_f(static_cast<const __nv_bfloat16*>(t.g) + i0 + i) : static_cast<const float*>(t.g)[i0 + i];
-        if (!narrow) {
-            f[2][i] = static_cast<const float*>(t.m)[i0 + i];
-            f[3][i] = static_cast<const float*>(t.v)[i0 + i];
+    // all loads of the lane together
+    float x[8], g[8], m[8], v[8];
+    uint32_t b[4] = {0, 0, 0, 0};
+    const uint8_t* lm = static_cast<const uint8_t*>(t.m) + i0;
+    const uint8_t* lv = static_cast<const uint8_t*>(t.v) + i0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = g[i] = m[i] = v[i] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (live(i)) {
+            if (t.w) x[i] = t.w[i0 + i];
+            else if (t.kind & 1) x[i] = ld_f(static_cast<const __nv_bfloat16*>(t.p) + i0 + i);
+            else x[i] = static_cast<const float*>(t.p)[i0 + i];
         }
-    }
-    uint64_t X[4], Gr[4], M[4], V[4], R[4];
-    for (int i = 0; i < 4; ++i) {
-        X[i] = pk2(f[0][2 * i], f[0][2 * i + 1]);
-        Gr[i] = pk2(f[1][2 * i], f[1][2 * i + 1]);
-        M[i] = pk2(f[2][2 * i], f[2][2 * i + 1]);
-        V[i] = pk2(f[3][2 * i], f[3][2 * i + 1]);
-    }
-    uint8_t* cm = static_cast<uint8_t*>(t.m) + i0;
-    uint8_t* cv = static_cast<uint8_t*>(t.v) + i0;
-    if (narrow) {
-        uint32_t b[4] = {0, 0, 0, 0};
-        for (int i = 0; i < 8; ++i)
-            if (live(i)) {
-                b[i / 4] |= (uint32_t)cm[i] << 8 * (i % 4);
-                b[2 + i / 4] |= (uint32_t)cv[i] << 8 * (i % 4);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (live(i)) {
+            if (t.kind & 2) g[i] = ld_f(static_cast<const __nv_bfloat16*>(t.g) + i0 + i);
+            else g[i] = static_cast<const float*>(t.g)[i0 + i];
+        }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (live(i)) {
+            if constexpr (kNarrow) {
+                b[i / 4] |= (uint32_t)lm[i] << 8 * (i % 4);
+                b[2 + i / 4] |= (uint32_t)lv[i] << 8 * (i % 4);
+            } else {
+                m[i] = static_cast<const float*>(t.m)[i0 + i];
+                v[i] = static_cast<const float*>(t.v)[i0 + i];
             }
+        }
+    uint64_t X[4], Gr[4], M[4], V[4], R[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        X[i] = pk2(x[2 * i], x[2 * i + 1]);
+        Gr[i] = pk2(g[2 * i], g[2 * i + 1]);
+        M[i] = pk2(m[2 * i], m[2 * i + 1]);
+        V[i] = pk2(v[2 * i], v[2 * i + 1]);
+    }
+    if constexpr (kNarrow) {
         decode8(make_uint2(b[0], b[1]), t.ms[u], M);
         decode8(make_uint2(b[2], b[3]), t.vs[u], V);
+#pragma unroll
         for (int i = 0; i < 4; ++i) V[i] = mul2(V[i], V[i]);
     }
     advance8(s, Gr, X, M, V, R);
     uint2 km{}, kv{};
-    if (narrow) {
+    if constexpr (kNarrow) {
         float sm, sv;
         hold(M, V, R, (uint32_t)i0 * 0x9E3779B1u + s.dither, km, kv, sm, sv);
         if (lane == 0) {
@@ -375,17 +387,20 @@ __device__ __noinline__ void last_unit(const TensorArg& t, const Step& s, int64_
             t.vs[u] = sv;
         }
     }
+    uint8_t* cm = static_cast<uint8_t*>(t.m) + i0;
+    uint8_t* cv = static_cast<uint8_t*>(t.v) + i0;
+#pragma unroll
     for (int i = 0; i < 8; ++i) {
         if (!live(i)) continue;
         float x0, x1, m0, m1, v0, v1;
         upk2(X[i / 2], x0, x1);
         upk2(M[i / 2], m0, m1);
         upk2(V[i / 2], v0, v1);
-        const float x = i % 2 ? x1 : x0;
-        if (t.w) t.w[i0 + i] = x;
-        if (t.kind & 1) st_f(static_cast<__nv_bfloat16*>(t.p) + i0 + i, x);
-        else static_cast<float*>(t.p)[i0 + i] = x;
-        if (narrow) {
+        const float y = i % 2 ? x1 : x0;
+        if (t.w) t.w[i0 + i] = y;
+        if (t.kind & 1) st_f(static_cast<__nv_bfloat16*>(t.p) + i0 + i, y);
+        else static_cast<float*>(t.p)[i0 + i] = y;
+        if constexpr (kNarrow) {
             cm[i] = (uint8_t)((i < 4 ? km.x : km.y) >> 8 * (i % 4));
             cv[i] = (uint8_t)((i < 4 ? kv.x : kv.y) >> 8 * (i % 4));
         } else {
@@ -400,17 +415,26 @@ __global__ void __launch_bounds__(kThreads, kNarrow ? 3 : 2) adamw_kernel(const 
     pdl_wait();
     // The step's scalars, by one thread: double precision is slow here, and every block pays for it.
     __shared__ float corr[2];
+    __shared__ uint32_t step_low;
     State* st = reinterpret_cast<State*>(a.state);
-    const long long step = st->step + 1;
+    long long step = 0;
     double c1 = 0.0, c2 = 0.0;
+    unsigned ticket = 0;
     if (threadIdx.x == 0) {
         // 1 - beta^(t+1) = beta (1 - beta^t) + (1 - beta)
         c1 = st->c1 * a.beta1 + (1.0 - a.beta1);
         c2 = st->c2 * a.beta2 + (1.0 - a.beta2);
+        step = st->step + 1;
         corr[0] = (float)c1;
         corr[1] = (float)c2;
+        step_low = (uint32_t)step;
+        if (a.advance) {
+            __threadfence();                   // the state has been read before the ticket is taken
+            ticket = atomicAdd(&st->ticket, 1u);
+        }
     }
-    __syncthreads();
+    // the last tensor whose first run is <= this block's
+    const int lo = __syncthreads_count((int)threadIdx.x < a.count && a.first[threadIdx.x] <= blockIdx.x) - 1;
     const float lr = a.lr_dev ? *a.lr_dev : a.lr;
     Step s;
     s.b1 = a.b1;
@@ -421,13 +445,8 @@ __global__ void __launch_bounds__(kThreads, kNarrow ? 3 : 2) adamw_kernel(const 
     s.rc2 = 1.f / sqrtf(corr[1]);
     s.eps = a.eps;
     s.gs = a.grad_scale ? *a.grad_scale : 1.f;
-    s.dither = (uint32_t)step * 0x61C88647u;
+    s.dither = step_low * 0x61C88647u;
     if (blockIdx.x < a.runs) {
-        int lo = 0, hi = a.count;                       // the last tensor whose first run is <= this block's
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (a.first[mid] <= blockIdx.x) lo = mid; else hi = mid;
-        }
         const TensorArg& t = a.t[lo];
         s.keep = 1.f - lr * t.decay;
         const int64_t u0 = (int64_t)(blockIdx.x - a.first[lo]) * a.run * 8, whole = t.n / kUnit - u0;
@@ -447,18 +466,12 @@ __global__ void __launch_bounds__(kThreads, kNarrow ? 3 : 2) adamw_kernel(const 
         if (t.n % kUnit && whole < (int64_t)a.run * 8 && (int)(threadIdx.x >> 5) == (int)(whole & 7))
             last_unit<kNarrow>(t, s, u0 + whole, threadIdx.x & 31);
     }
-    // the last block to get here counts the step: every block has read the old count by then
-    if (a.advance) {
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            __threadfence();
-            if (atomicAdd(&st->ticket, 1u) == gridDim.x - 1) {
-                st->c1 = c1;
-                st->c2 = c2;
-                st->step = step;
-                st->ticket = 0;
-            }
-        }
+    // the last block to take a ticket counts the step: every block has read the old count by then
+    if (threadIdx.x == 0 && a.advance && ticket == gridDim.x - 1) {
+        st->c1 = c1;
+        st->c2 = c2;
+        st->step = step;
+        st->ticket = 0;
     }
 }
 

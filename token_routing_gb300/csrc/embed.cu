@@ -552,6 +552,9 @@ __global__ void __launch_bounds__(256) embed_join_kernel(SumArgs a, G* __restric
         for (int i = 0; i < VE; ++i) s[i] += r[i];
     };
     const int64_t n_long = (int64_t)a.crossing[1] * slabs, n_short = (int64_t)a.crossing[0] * slabs;
+    // While the long ones take less than half of the blocks, each has one and the other blocks take
+    // the short ones; else all blocks take both.
+    const bool apart = n_long * 2 <= gridDim.x;
     for (int64_t q = blockIdx.x; q < n_long; q += gridDim.x) {
         const uint2 head = a.heads[a.groups + q / slabs];
         const int g = (int)head.y, col = ((int)(q % slabs) * 32 + lane) * VE;
@@ -580,7 +583,9 @@ __global__ void __launch_bounds__(256) embed_join_kernel(SumArgs a, G* __restric
         }
         __syncthreads();
     }
-    for (int64_t q = (int64_t)blockIdx.x * kWarps + warp; q < n_short; q += (int64_t)gridDim.x * kWarps) {
+    const int64_t first = (int64_t)blockIdx.x - (apart ? n_long : 0), blocks = (int64_t)gridDim.x - (apart ? n_long : 0);
+    if (first < 0) return;
+    for (int64_t q = first * kWarps + warp; q < n_short; q += blocks * kWarps) {
         const uint2 head = a.heads[q / slabs];
         const int g = (int)head.y, col = ((int)(q % slabs) * 32 + lane) * VE;
         const uint32_t key = head.x;
