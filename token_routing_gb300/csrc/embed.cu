@@ -153,7 +153,7 @@ constexpr int kMaxBits = 9;          // bits of a digit
 constexpr int kMaxBins = 1 << kMaxBits;
 constexpr int kMaxPasses = 4;        // 31 bits of keys
 // Bytes zeroed beside one launch of the sort: about what the memory takes in its time.
-constexpr int64_t kZeroOne = 24 << 20, kZeroHist = 12 << 20, kZeroScatter = 20 << 20;
+constexpr int64_t kZeroOne = 24 << 20, kZeroHist = 32 << 20, kZeroScatter = 44 << 20;
 
 struct SortArgs {
     const int32_t* ids;      // first pass: keys are made from the ids
@@ -407,12 +407,12 @@ __global__ void __launch_bounds__(kOneThreads) embed_sort_kernel(SortArgs a, int
 
 // ---------------------------------------------------------------- gradient: sums over runs
 // The sorted pairs are cut into groups of kGroup. A thread owns VE columns of one group, loads
-// them of all its rows (and of the dW rows that it will add to) at once, and walks them in
+// them of several rows (and of the dW rows that it will add to) at once, and walks them in
 // order; a run of one token that lies inside the group is finished there. A run that crosses
 // groups leaves one fp32 partial row in each (slot 0: the run the group begins with, slot 1: the
 // run it ends with and that begins in it) and an entry in a list, and embed_join_kernel adds them
 // in group order. Every row of dW has one writer and a fixed order of sums.
-constexpr int kGroup = 8;
+constexpr int kGroup = 16;
 constexpr int kLong = 16;        // a run over more groups than this is joined by a whole block
 
 struct SumArgs {
@@ -421,7 +421,8 @@ struct SumArgs {
     int32_t* crossing;       // counts of crossing runs: short ones, long ones
     uint2* heads;            // [2, groups] their keys and the groups they begin in, in any order
     int T, V, d, groups;
-    int zero_from;           // first row that this launch zeroes if it gets no sum; V: none
+    int zero_from;           // first row that is zeroed here if it gets no sum
+    int joins;               // blocks of the last launch that join; the others zero rows
     float scale;
 };
 
@@ -462,10 +463,6 @@ template <typename T, typename G, int VE, bool kAdd>
 __global__ void __launch_bounds__(256) embed_sum_kernel(SumArgs a, const T* __restrict__ dy, G* __restrict__ dW) {
     __shared__ uint2 pr[kGroup + 2];   // the group's pairs, with a neighbour on either side
     pdl_wait();
-    if ((int)blockIdx.x >= a.groups) {
-        if (blockIdx.y == 0) zero_rows<G, VE>(a, dW, blockIdx.x - a.groups);
-        return;
-    }
     const int g = blockIdx.x, i0 = g * kGroup;
     if ((int)threadIdx.x < kGroup + 2) {
         const int i = i0 + (int)threadIdx.x - 1;
@@ -477,8 +474,8 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(SumArgs a, const T* __re
 #pragma unroll
         for (int i = 0; i < VE; ++i) s[i] = 0.f;
         bool from_before = pr[0].x == pr[1].x;
-        // adding to dW, half a group at a time: its old rows take registers too
-        constexpr int kAtOnce = kAdd ? kGroup / 2 : kGroup;
+        // eight rows in flight; four where dW is added to, whose old rows take registers too
+        constexpr int kAtOnce = kAdd ? 4 : 8;
 #pragma unroll
         for (int j0 = 0; j0 < kGroup; j0 += kAtOnce) {
             Bits<T, VE> r[kAtOnce];
@@ -543,6 +540,10 @@ template <typename G, int VE, bool kAdd>
 __global__ void __launch_bounds__(256) embed_join_kernel(SumArgs a, G* __restrict__ dW) {
     __shared__ float part[kWarps][32 * VE];
     pdl_wait();
+    if ((int)blockIdx.x >= a.joins) {
+        zero_rows<G, VE>(a, dW, blockIdx.x - a.joins);
+        return;
+    }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int slabs = (a.d + 32 * VE - 1) / (32 * VE);
     const auto add = [&](float (&s)[VE], int g, int k, int col) {
@@ -554,8 +555,8 @@ __global__ void __launch_bounds__(256) embed_join_kernel(SumArgs a, G* __restric
     const int64_t n_long = (int64_t)a.crossing[1] * slabs, n_short = (int64_t)a.crossing[0] * slabs;
     // While the long ones take less than half of the blocks, each has one and the other blocks take
     // the short ones; else all blocks take both.
-    const bool apart = n_long * 2 <= gridDim.x;
-    for (int64_t q = blockIdx.x; q < n_long; q += gridDim.x) {
+    const bool apart = n_long * 2 <= a.joins;
+    for (int64_t q = blockIdx.x; q < n_long; q += a.joins) {
         const uint2 head = a.heads[a.groups + q / slabs];
         const int g = (int)head.y, col = ((int)(q % slabs) * 32 + lane) * VE;
         const uint32_t key = head.x;
@@ -583,7 +584,7 @@ __global__ void __launch_bounds__(256) embed_join_kernel(SumArgs a, G* __restric
         }
         __syncthreads();
     }
-    const int64_t first = (int64_t)blockIdx.x - (apart ? n_long : 0), blocks = (int64_t)gridDim.x - (apart ? n_long : 0);
+    const int64_t first = (int64_t)blockIdx.x - (apart ? n_long : 0), blocks = a.joins - (apart ? n_long : 0);
     if (first < 0) return;
     for (int64_t q = first * kWarps + warp; q < n_short; q += blocks * kWarps) {
         const uint2 head = a.heads[q / slabs];
@@ -632,19 +633,20 @@ template <typename T, typename G, int VE, bool kAdd>
 cudaError_t launch_sums(const moe_embed_config_t& c, SumArgs a, const void* dy, void* dW, cudaStream_t s) {
     const int nvec = c.d / VE;
     G* out = static_cast<G*>(dW);
-    const int threads = std::max(64, std::min(256, ceil_div(nvec, 32) * 32));
-    const int zero = kAdd ? 0 : ceil_div(a.V - a.zero_from, kZeroRows);
+    const int threads = std::max(64, std::min(128, ceil_div(nvec, 32) * 32));
     cudaError_t e = cudaSuccess;
-    if (a.groups + zero > 0) {
-        e = launch_pdl(embed_sum_kernel<T, G, VE, kAdd>, dim3(a.groups + zero, std::min(ceil_div(nvec, threads), 64)),
+    if (a.groups > 0) {
+        e = launch_pdl(embed_sum_kernel<T, G, VE, kAdd>, dim3(a.groups, std::min(ceil_div(nvec, threads), 64)),
                        dim3(threads), 0, s, a, static_cast<const T*>(dy), out);
         count_launch();
+        if (e != cudaSuccess) return e;
     }
-    if (e != cudaSuccess || a.groups < 2) return e;      // one group has no run that leaves it
-    // as many warps as there can be items, up to what the SMs hold
+    // as many warps as there can be items, up to what the SMs hold; one group has no run that leaves it
     const int64_t items = (int64_t)a.groups * ceil_div(nvec, 32);
-    e = launch_pdl(embed_join_kernel<G, VE, kAdd>, dim3((unsigned)std::min<int64_t>((items + 7) / 8, num_sms() * 6)),
-                   dim3(256), 0, s, a, out);
+    a.joins = a.groups < 2 ? 0 : (int)std::min<int64_t>((items + 7) / 8, num_sms() * 6);
+    const int zero = kAdd ? 0 : ceil_div(a.V - a.zero_from, kZeroRows);
+    if (a.joins + zero == 0) return e;
+    e = launch_pdl(embed_join_kernel<G, VE, kAdd>, dim3(a.joins + zero), dim3(256), 0, s, a, out);
     count_launch();
     return e;
 }
@@ -659,7 +661,7 @@ cudaError_t launch_embed_bwd(const moe_embed_config_t& c, const int32_t* ids, co
                              cudaStream_t s) {
     EmbedScratch w;
     carve_embed(c, ws, &w);
-    SumArgs sums{w.a, w.part, w.crossing, w.heads, c.T, c.V, c.d, groups_of(c), 0, c.scale};
+    SumArgs sums{w.a, w.part, w.crossing, w.heads, c.T, c.V, c.d, groups_of(c), 0, 0, c.scale};
     if (c.T > 0) {
         int bits = 1;
         while (((int64_t)1 << bits) <= c.V) ++bits;          // keys 0 .. V
