@@ -114,23 +114,33 @@ __device__ __forceinline__ uint32_t value_code(float y, uint32_t hash) {
     return (t << 4 & 0x7f000000u) | (t & 0x80000000u);
 }
 
+// Both halves of y times 2^-120, cut off where fp32's subnormal numbers end: what is left says for
+// every value between which two codes it lies, and its share of the way to 20 bits.
+__device__ __forceinline__ uint64_t to_codes(uint64_t y) {
+    uint64_t r;
+    asm("mul.rz.f32x2 %0, %1, %2;" : "=l"(r) : "l"(y), "l"(splat2(kToCode)));
+    return r;
+}
+
 // Codes of two roots y >= 0 (and y 2^-120) in the top bytes. The share of the way is taken between
 // the squares, so that the square is right on average (rounding the root evenly would raise it:
 // the mean of squares is above the square of the mean). A root above zero keeps at least code 1.
 __device__ __forceinline__ void root_codes(uint64_t y, uint64_t down, uint32_t hash0, uint32_t hash1, uint32_t& c0,
                                            uint32_t& c1) {
-    const uint32_t b0 = (uint32_t)down, b1 = (uint32_t)(down >> 32);
-    const uint32_t l0 = b0 & ~0xfffffu, l1 = b1 & ~0xfffffu, n0 = l0 + 0x100000u, n1 = l1 + 0x100000u;
-    uint64_t low = mul2((uint64_t)l1 << 32 | l0, splat2(kFromCode)), next = mul2((uint64_t)n1 << 32 | n0, splat2(kFromCode));
+    const uint32_t l0 = (uint32_t)down & ~0xfffffu, l1 = (uint32_t)(down >> 32) & ~0xfffffu;
+    const uint32_t n0 = l0 + 0x100000u, n1 = l1 + 0x100000u;
+    const uint64_t low = mul2((uint64_t)l1 << 32 | l0, splat2(kFromCode));
+    const uint64_t next = mul2((uint64_t)n1 << 32 | n0, splat2(kFromCode));
     const uint64_t minus = splat2(-1.f);
-    low = mul2(low, low);
-    const uint64_t over = fma2(low, minus, mul2(y, y)), step = fma2(low, minus, mul2(next, next));
-    // 1 + the share that is not reached, from the hash's 23 top bits
-    const uint64_t rest = (uint64_t)(0x3f800000u | ~hash1 >> 9) << 32 | (0x3f800000u | ~hash0 >> 9);
-    float e0, e1;
-    upk2(add2(fma2(mul2(rest, minus), step, step), over), e0, e1);
-    c0 = max(e0 > 0.f ? n0 : l0, min((uint32_t)y, 0x100000u)) << 4;
-    c1 = max(e1 > 0.f ? n1 : l1, min((uint32_t)(y >> 32), 0x100000u)) << 4;
+    const uint64_t over = mul2(fma2(low, minus, y), add2(y, low));                   // y^2 - low^2
+    const uint64_t step = fma2(mul2(low, low), minus, mul2(next, next));             // next^2 - low^2
+    // 1 - the dither, from 1 + the dither
+    const uint64_t d = (uint64_t)(0x3f800000u | (hash1 >> 9 & 0x7ffff8u)) << 32 | (0x3f800000u | (hash0 >> 9 & 0x7ffff8u));
+    float o0, o1, t0, t1;
+    upk2(over, o0, o1);
+    upk2(mul2(fma2(d, minus, splat2(2.f)), step), t0, t1);
+    c0 = max(o0 >= t0 ? n0 : l0, min((uint32_t)y, 0x100000u)) << 4;
+    c1 = max(o1 >= t1 ? n1 : l1, min((uint32_t)(y >> 32), 0x100000u)) << 4;
 }
 
 // Top bytes of four words as one word.
@@ -148,7 +158,7 @@ __device__ __forceinline__ uint2 encode8(const uint64_t (&f)[4], float inv, bool
     uint32_t c[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint64_t y = mul2(f[i], splat2(inv)), down = mul2(y, splat2(kToCode));
+        const uint64_t y = mul2(f[i], splat2(inv)), down = to_codes(y);
         if constexpr (kRoot) {
             root_codes(y, down, hash[2 * i] * 0xC2B2AE35u, hash[2 * i + 1] * 0xC2B2AE35u, c[2 * i], c[2 * i + 1]);
         } else {
@@ -198,18 +208,34 @@ __device__ __forceinline__ float block_scale(float top, float& inv) {
     return some ? __uint_as_float(pow2) : 0.f;
 }
 
-// The step on eight elements. m and v are sums of rounded products (no fma): the same bits on any
-// machine, so that a block's scale is too.
+// a x + b y, each product rounded by itself.
+__device__ __forceinline__ uint64_t rounded_sum(float a, uint64_t x, float b, uint64_t y) {
+    float x0, x1, y0, y1;
+    upk2(x, x0, x1);
+    upk2(y, y0, y1);
+    return pk2(__fadd_rn(__fmul_rn(a, x0), __fmul_rn(b, y0)), __fadd_rn(__fmul_rn(a, x1), __fmul_rn(b, y1)));
+}
+
+// The step on eight elements. With 8-bit states m and v are sums of rounded products: a mean that
+// stays where it is (m = g) is then exactly what it was, and a block whose largest magnitude is a
+// power of two keeps its scale, where a fused product and sum would be a rounding off to either
+// side.
+template <bool kNarrow>
 __device__ __forceinline__ void advance8(const Step& s, const uint64_t (&g)[4], uint64_t (&x)[4], uint64_t (&m)[4],
                                          uint64_t (&v)[4], uint64_t (&root)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint64_t gg = mul2(g[i], splat2(s.gs));
-        m[i] = add2(mul2(splat2(s.b1), m[i]), mul2(splat2(s.ob1), gg));
-        v[i] = add2(mul2(splat2(s.b2), v[i]), mul2(splat2(s.ob2), mul2(gg, gg)));
+        if constexpr (kNarrow) {
+            m[i] = rounded_sum(s.b1, m[i], s.ob1, gg);
+            v[i] = rounded_sum(s.b2, v[i], s.ob2, mul2(gg, gg));
+        } else {
+            m[i] = fma2(splat2(s.ob1), gg, mul2(splat2(s.b1), m[i]));
+            v[i] = fma2(splat2(s.ob2), mul2(gg, gg), mul2(splat2(s.b2), v[i]));
+        }
         float v0, v1, d0, d1;
         upk2(v[i], v0, v1);
-        root[i] = pk2(sqrt_approx(v0), sqrt_approx(v1));
+        root[i] = kNarrow ? pk2(__fsqrt_rn(v0), __fsqrt_rn(v1)) : pk2(sqrt_approx(v0), sqrt_approx(v1));
         upk2(fma2(root[i], splat2(s.rc2), splat2(s.eps)), d0, d1);
         x[i] = fma2(x[i], splat2(s.keep), mul2(mul2(m[i], splat2(s.rate)), pk2(rcp_approx(d0), rcp_approx(d1))));
     }
@@ -296,7 +322,7 @@ __device__ __forceinline__ void run_units(const TensorArg& t, const Step& s, int
             unpack8<float>(r.m, M);
             unpack8<float>(r.v, V);
         }
-        advance8(s, Gr, X, M, V, root);
+        advance8<kNarrow>(s, Gr, X, M, V, root);
         const uint32_t i = u * kUnit + (threadIdx.x & 31) * 8;
         store8(p + i, X);
         if constexpr (kMaster) store8(w + i, X);
@@ -377,7 +403,7 @@ __device__ __noinline__ void last_unit(const TensorArg& t, const Step& s, int64_
 #pragma unroll
         for (int i = 0; i < 4; ++i) V[i] = mul2(V[i], V[i]);
     }
-    advance8(s, Gr, X, M, V, R);
+    advance8<kNarrow>(s, Gr, X, M, V, R);
     uint2 km{}, kv{};
     if constexpr (kNarrow) {
         float sm, sv;

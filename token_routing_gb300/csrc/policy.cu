@@ -8,7 +8,7 @@ namespace moe {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLn2High = 0.693145751953125f, kLn2Low = 1.4286068203094172e-6f;   // 16 bits, and the rest
 constexpr int kWarps = 8;                     // warps that compute; one more warp loads
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCluster = 8;
@@ -55,7 +55,7 @@ struct PolicyArgs {
     float* tok_loss;      // [T] weight * l, or null
     int T, V;
     int64_t ld, ld_grad;
-    float inv_tau, clip_low, clip_high, kl;
+    float tau, inv_tau, clip_low, clip_high, kl;
     int* err;
 };
 
@@ -115,18 +115,32 @@ struct Token {
 
 // What one token adds: its log-probability and its term of the loss (written if `put`), and the
 // factor c of its gradient row c (1[v = target] - p_v).
-__device__ __forceinline__ float token_terms(const PolicyArgs& a, const Token& r, bool put, MaxSum row, float k) {
-    // a row of -inf alone has no distribution
-    const float lp = row.s != 0.f ? ((r.zt - row.m) * k - log2f(row.s)) * kLn2 : NAN;
+__device__ __forceinline__ float token_terms(const PolicyArgs& a, const Token& r, bool put, MaxSum row) {
+    // lp = (z - max) / tau - ln(sum), with the sum as 2^e f: the quotient's and the partial sums'
+    // roundings are kept in `low`, so that the ratios to other policies, which differ by a little
+    // from numbers of ten and more, do not lose them.
+    const float d = r.zt - row.m, q = d / a.tau, q_low = fmaf(-q, a.tau, d) / a.tau;
+    const int e = (int)(__float_as_uint(row.s) >> 23) - 127;
+    const float f = __uint_as_float((__float_as_uint(row.s) & 0x7fffffu) | 0x3f800000u);
+    const float hi = fmaf(-(float)e, kLn2High, q), hi_low = fmaf(-(float)e, kLn2High, q - hi);
+    const float ln_f = fmaf((float)e, kLn2Low, logf(f));
+    const float sum = hi - ln_f, low = (hi - sum) - ln_f + hi_low + q_low;
+    float lp = sum, lp_low = low;
+    if (!(fabsf(q) <= 3.4028235e38f) || !(row.s >= 1.f && row.s <= 3.4028235e38f)) {
+        // a target of -inf has the log-probability -inf; a row of -inf alone, or with a NaN or
+        // +inf in it, has no distribution
+        lp = row.s >= 1.f && row.s <= 3.4028235e38f ? q : NAN;
+        lp_low = 0.f;
+    }
     if (a.logp && put) a.logp[r.t] = lp;
     if (!a.advantage) return 0.f;
-    const float ratio = a.old_logp ? expf(lp - r.old) : 1.f;
+    const float ratio = a.old_logp ? expf(lp - r.old + lp_low) : 1.f;
     const float un = ratio * r.adv, cl = fminf(fmaxf(ratio, 1.f - a.clip_low), 1.f + a.clip_high) * r.adv;
     float l = -fminf(un, cl);
     float slope = un <= cl ? -un : 0.f;
     if (lp != lp) l = slope = lp;
     if (a.kl != 0.f) {
-        const float u = r.ref - lp, eu = expm1f(u);
+        const float u = r.ref - lp - lp_low, eu = expm1f(u);
         l += a.kl * (u == INFINITY ? u : eu - u);
         slope -= a.kl * eu;
     }
@@ -461,7 +475,7 @@ policy_ring_kernel(PolicyArgs a, const T* logits, T* dlogits, int reuse) {
             if (reuse == kFree) {
                 // nothing of this row waits for its sum: the row before it is finished now, its
                 // exchange having passed under this row's work
-                if (turn) token_terms(a, before, rank == 0 && tid == 0, receive(turn - 1), k);
+                if (turn) token_terms(a, before, rank == 0 && tid == 0, receive(turn - 1));
                 before = x;
                 send(acc, turn++);
                 continue;
@@ -469,7 +483,7 @@ policy_ring_kernel(PolicyArgs a, const T* logits, T* dlogits, int reuse) {
             send(acc, turn);
             acc = receive(turn++);
             RowGrad g;
-            g.c = token_terms(a, x, rank == 0 && tid == 0, acc, k);
+            g.c = token_terms(a, x, rank == 0 && tid == 0, acc);
             g.top = acc.m;
             g.set_q(g.c / acc.s);
             // ---- gradient
@@ -503,7 +517,7 @@ policy_ring_kernel(PolicyArgs a, const T* logits, T* dlogits, int reuse) {
             }
             if (tid < s.rest) dz[odd] = grad_one<T>(lone, g, k, odd == r.target);
         }
-        if (reuse == kFree && turn && ok) token_terms(a, before, rank == 0 && tid == 0, receive(turn - 1), k);
+        if (reuse == kFree && turn && ok) token_terms(a, before, rank == 0 && tid == 0, receive(turn - 1));
     }
     // no CTA leaves while another of its cluster may still write to it
     __syncwarp();
@@ -590,7 +604,7 @@ __global__ void __launch_bounds__(short_block(G), 1024 / short_block(G)) policy_
     }
     __syncwarp();
     RowGrad g;
-    g.c = token_terms(a, x, tid == 0, acc, k);
+    g.c = token_terms(a, x, tid == 0, acc);
     if (!dz) return;
     g.top = acc.m;
     g.set_q(g.c / acc.s);
@@ -722,6 +736,7 @@ cudaError_t run_policy(const moe_policy_config_t& c, PolicyArgs a, const void* l
     a.V = c.V;
     a.ld = c.ld;
     a.ld_grad = c.ld_grad;
+    a.tau = c.temperature;
     a.inv_tau = 1.f / c.temperature;
     a.clip_low = c.clip_low;
     a.clip_high = c.clip_high;
