@@ -14,7 +14,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kUnit = MOE_ADAMW_BLOCK;     // elements a warp takes at a time: 8 a lane, one scale block
 constexpr uint32_t kTicket = 1024;         // blocks that may take a ticket each
-constexpr int kRun = 16;                    // longest run
+constexpr int kRun[2] = {16, 32};          // longest runs, with fp32 and with 8-bit states
 constexpr int kBatch = kThreads;           // tensors in one launch's parameters, one looked at by each thread
 
 struct TensorArg {
@@ -272,7 +272,7 @@ struct Raw {
 // plus a 32-bit place.
 template <typename P, typename G, bool kMaster, bool kNarrow>
 __device__ __forceinline__ void run_units(const TensorArg& t, const Step& s, int64_t u0, int count, int run) {
-    __shared__ float scales[2][kNarrow ? kRun * 8 : 1];
+    __shared__ float scales[2][kNarrow ? kRun[1] * 8 : 1];
     using R = Raw<P, G, kMaster, kNarrow>;
     using S = std::conditional_t<kNarrow, uint8_t, float>;
     const int64_t i0 = u0 * kUnit;
@@ -564,7 +564,7 @@ extern "C" MOE_API moe_status_t moe_adamw(const moe_adamw_config_t* cfg, const m
     for (int narrow = 0; narrow < 2; ++narrow) {
         if (!launches[narrow]) continue;
         // long runs spare blocks their start, short ones spread small tensors over more blocks
-        a.run = (int)std::min<int64_t>(kRun, std::max<int64_t>(1, units[narrow] / (8LL * 4 * num_sms())));
+        a.run = (int)std::min<int64_t>(kRun[narrow], std::max<int64_t>(1, units[narrow] / (8LL * 4 * num_sms())));
         if (units[narrow] / (8 * a.run) + count > INT32_MAX) return MOE_ERR_UNSUPPORTED;
         int i = 0;
         bool last = false;

@@ -119,7 +119,7 @@ __device__ __forceinline__ float token_terms(const PolicyArgs& a, const Token& r
     // lp = (z - max) / tau - ln(sum), with the sum as 2^e f: the quotient's and the partial sums'
     // roundings are kept in `low`, so that the ratios to other policies, which differ by a little
     // from numbers of ten and more, do not lose them.
-    const float d = r.zt - row.m, q = d / a.tau, q_low = fmaf(-q, a.tau, d) / a.tau;
+    const float d = r.zt - row.m, q = d * a.inv_tau, q_low = fmaf(-q, a.tau, d) * a.inv_tau;
     const int e = (int)(__float_as_uint(row.s) >> 23) - 127;
     const float f = __uint_as_float((__float_as_uint(row.s) & 0x7fffffu) | 0x3f800000u);
     const float hi = fmaf(-(float)e, kLn2High, q), hi_low = fmaf(-(float)e, kLn2High, q - hi);
@@ -407,6 +407,9 @@ policy_ring_kernel(PolicyArgs a, const T* logits, T* dlogits, int reuse) {
             if (lane + 32 < n) acc = join(acc, peer[b][lane + 32], k);
             return warp_join(acc, k);
         };
+        const auto finish = [&](const Token& x, MaxSum sum) {
+            if (rank == 0 && warp == 0) token_terms(a, x, lane == 0, sum);
+        };
         while (ok) {
             if (!tc::mbar_wait(&given[from.slot], from.phase, a.err)) break;
             const Row r = rows[from.slot];
@@ -475,7 +478,7 @@ policy_ring_kernel(PolicyArgs a, const T* logits, T* dlogits, int reuse) {
             if (reuse == kFree) {
                 // nothing of this row waits for its sum: the row before it is finished now, its
                 // exchange having passed under this row's work
-                if (turn) token_terms(a, before, rank == 0 && tid == 0, receive(turn - 1));
+                if (turn) finish(before, receive(turn - 1));
                 before = x;
                 send(acc, turn++);
                 continue;
@@ -517,7 +520,7 @@ policy_ring_kernel(PolicyArgs a, const T* logits, T* dlogits, int reuse) {
             }
             if (tid < s.rest) dz[odd] = grad_one<T>(lone, g, k, odd == r.target);
         }
-        if (reuse == kFree && turn && ok) token_terms(a, before, rank == 0 && tid == 0, receive(turn - 1));
+        if (reuse == kFree && turn && ok) finish(before, receive(turn - 1));
     }
     // no CTA leaves while another of its cluster may still write to it
     __syncwarp();
