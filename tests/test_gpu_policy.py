@@ -277,6 +277,16 @@ def test_token_logp(T, V, tau, pad, dtype, moe_lib, cuda_device):
     moe_lib.get_error()
 
 
+@pytest.mark.parametrize("V", [300, 20001])
+def test_token_logp_with_a_loss_configuration(V, moe_lib, cuda_device):
+    """The loss's own configuration, KL term and clipping set: token_logp has no reference to read."""
+    s = make(20, V, "bf16")
+    a, b = torch.empty(20, device="cuda"), torch.empty(20, device="cuda")
+    moe_lib.token_logp(moe_lib.make_policy_config(20, V), s["z"], s["target"], a)
+    moe_lib.token_logp(moe_lib.make_policy_config(20, V, clip_low=0.1, kl_weight=0.3), s["z"], s["target"], b)
+    assert torch.equal(a, b)
+
+
 def test_large_logits_lose_nothing(moe_lib, cuda_device):
     """Logits around 3e4: the log-probability of their differences, as for the same row around 0."""
     z = torch.randn(4, 3001, generator=torch.Generator().manual_seed(3)).mul(64).round().div(16).cuda()

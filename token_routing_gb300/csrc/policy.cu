@@ -743,7 +743,7 @@ cudaError_t run_policy(const moe_policy_config_t& c, PolicyArgs a, const void* l
     a.inv_tau = 1.f / c.temperature;
     a.clip_low = c.clip_low;
     a.clip_high = c.clip_high;
-    a.kl = c.kl_weight;
+    a.kl = a.advantage ? c.kl_weight : 0.f;      // without an advantage there is no loss, and no ref_logp
     a.err = device_error_word();
     return c.dtype == MOE_BF16 ? launch_policy<__nv_bfloat16>(a, logits, dlogits, s)
                                : launch_policy<float>(a, logits, dlogits, s);
