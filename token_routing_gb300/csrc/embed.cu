@@ -107,7 +107,7 @@ cudaError_t launch_embed_v(const moe_embed_config_t& c, const int32_t* ids, cons
         T* out = static_cast<T*>(y) + t0 * c.d;
         cudaError_t e;
         if (total >= 2048u * 4u * (uint32_t)num_sms())
-            e = launch_pdl(embed_kernel<T, VE, 4>, dim3(ceil_div(total, 1024)), dim3(256), 0, s, ids + t0, w, out, total,
+            e = launch_pdl(embed_kernel<T, VE, 2>, dim3(ceil_div(total, 512)), dim3(256), 0, s, ids + t0, w, out, total,
                            (uint32_t)nvec, (int)c.V, c.scale, device_error_word());
         else
             e = launch_pdl(embed_kernel<T, VE, 1>, dim3(ceil_div(total, 256)), dim3(256), 0, s, ids + t0, w, out, total,
@@ -460,7 +460,7 @@ __device__ __forceinline__ void zero_rows(const SumArgs& a, G* dW, int block) {
 }
 
 template <typename T, typename G, int VE, bool kAdd>
-__global__ void __launch_bounds__(256) embed_sum_kernel(SumArgs a, const T* __restrict__ dy, G* __restrict__ dW) {
+__global__ void __launch_bounds__(128, 8) embed_sum_kernel(SumArgs a, const T* __restrict__ dy, G* __restrict__ dW) {
     __shared__ uint2 pr[kGroup + 2];   // the group's pairs, with a neighbour on either side
     pdl_wait();
     const int g = blockIdx.x, i0 = g * kGroup;
@@ -474,8 +474,9 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(SumArgs a, const T* __re
 #pragma unroll
         for (int i = 0; i < VE; ++i) s[i] = 0.f;
         bool from_before = pr[0].x == pr[1].x;
-        // eight rows in flight; four where dW is added to, whose old rows take registers too
-        constexpr int kAtOnce = kAdd ? 4 : 8;
+        // four rows in flight, two where dW is added to, whose old rows take registers too: with eight
+        // (and four) half as many blocks fit an SM (32768 x 2048 into fp32: 88 against 81 us)
+        constexpr int kAtOnce = kAdd ? 2 : 4;
 #pragma unroll
         for (int j0 = 0; j0 < kGroup; j0 += kAtOnce) {
             Bits<T, VE> r[kAtOnce];
