@@ -676,7 +676,7 @@ cudaError_t launch_embed_bwd(const moe_embed_config_t& c, const int32_t* ids, co
             const int rows = c.accumulate ? 0 : (int)std::min<int64_t>(c.V - sums.zero_from, wish / row) & ~15;
             ZeroArgs z{reinterpret_cast<uint4*>(static_cast<char*>(dW) + sums.zero_from * row), rows * row / 16};
             sums.zero_from += rows;
-            blocks = (unsigned)std::min<int64_t>(4 * num_sms(), (z.n + 2047) / 2048);
+            blocks = (unsigned)((z.n + 1023) / 1024);
             return z;
         };
         cudaError_t e;
