@@ -1,4 +1,8 @@
 // AdamW over many tensors in one launch, with fp32 or 8-bit states.
+//
+// Per element: m = b1 m + (1 - b1) g, v = b2 v + (1 - b2) g^2, x = keep x - rate m / (sqrt(v) rc2 + eps),
+// with the bias corrections folded into rate and rc2. Bound by memory: 30 bytes an element with
+// fp32 states and a master (bf16 weight and gradient), 18 with 8-bit states.
 #include <cuda_fp8.h>
 
 #include <climits>
@@ -208,7 +212,8 @@ __device__ __forceinline__ float block_scale(float top, float& inv) {
     return some ? __uint_as_float(pow2) : 0.f;
 }
 
-// a x + b y, each product rounded by itself.
+// a x + b y, each product rounded by itself (packed products and sums are contracted by the
+// compiler, rounding modifier or not: seen in the results).
 __device__ __forceinline__ uint64_t rounded_sum(float a, uint64_t x, float b, uint64_t y) {
     float x0, x1, y0, y1;
     upk2(x, x0, x1);
@@ -436,6 +441,14 @@ __device__ __noinline__ void last_unit(const TensorArg& t, const Step& s, int64_
     }
 }
 
+// One block, one run: up to 16 (or, with 8-bit states, 32) times 2048 elements of one tensor, a unit
+// of 256 to a warp at a time; small batches of tensors take shorter runs over more blocks. The
+// tensors come as launch parameters (no table on the device to keep), a block finds its own by one
+// vote over all of them.
+// fp32 states, 156M weights with masters: 700 us, 6690 GB/s (99 %); 114 registers and two blocks to
+// an SM, against 720 us at three and 800 at four, whose loads are cut apart. 8-bit states, 1.1G
+// weights: 2800 us, 6350 GB/s (94 %), four fifths of the issue slots taken: the next unit's loads
+// pass under the arithmetic of this one (without: 3400), and blocks start seldom (runs of 8: 3000).
 template <bool kNarrow>
 __global__ void __launch_bounds__(kThreads, kNarrow ? 3 : 2) adamw_kernel(const __grid_constant__ AdamArgs a) {
     pdl_wait();

@@ -64,7 +64,10 @@ int row_vec(int d, int es) {
 }
 
 // ---------------------------------------------------------------- lookup
-// y[t] = scale * W[ids[t]]: U vectors a thread, all loads of a thread in flight together.
+// y[t] = scale * W[ids[t]]: U vectors a thread, all loads of a thread in flight together. Bound by
+// memory and the two latencies (id, then row) a block pays. 16384 x 1024 bf16 tokens: 10.6 us, 4590
+// GB/s of needed traffic (68 %); U = 1: 12.1, U = 4: 11.7, U = 8: 16.5. Fewer vectors than 8 to
+// each of an SM's 2048 threads take U = 1: there latency counts, not bytes.
 template <typename T, int VE, int U>
 __global__ void __launch_bounds__(256) embed_kernel(const int32_t* __restrict__ ids, const T* __restrict__ W,
                                                     T* __restrict__ y, uint32_t total, uint32_t nvec, int V,
@@ -134,6 +137,9 @@ cudaError_t launch_embed(const moe_embed_config_t& c, const int32_t* ids, const 
 // every chunk of kChunk pairs for the first digit, then for each digit the chunks' ranks and the
 // scatter, which also counts the next digit's histogram by integer atomics. Left-out tokens
 // (padding, ids out of range) take the key V and end up behind all others.
+// Bound by latency: two digits take three launches of 2, 4 and 4 us at up to 4096 tokens, 4, 6 and
+// 6 at 32768. One block for all of it takes 4 us at 777 tokens, 6 at 2048, 10 at 4096 and 45 at
+// 16384 (one SM then ranks and scatters everything): it sorts batches of up to 4096.
 // The sort needs few of the SMs: the other blocks of its launches zero the first rows of a dW that
 // is overwritten, whether or not they get a sum later.
 struct ZeroArgs {
@@ -412,6 +418,9 @@ __global__ void __launch_bounds__(kOneThreads) embed_sort_kernel(SortArgs a, int
 // groups leaves one fp32 partial row in each (slot 0: the run the group begins with, slot 1: the
 // run it ends with and that begins in it) and an entry in a list, and embed_join_kernel adds them
 // in group order. Every row of dW has one writer and a fixed order of sums.
+// Bound by memory (dy once, the touched rows of dW) and by the latency of gathered rows: 32768 x
+// 2048 bf16 into fp32 rows that are added to, 57 us of 81 in all, 274 MB at 4800 GB/s. Groups of 8
+// leave twice the partial rows (88 us in all), groups of 32 half the blocks (86).
 constexpr int kGroup = 16;
 constexpr int kLong = 16;        // a run over more groups than this is joined by a whole block
 
@@ -524,7 +533,7 @@ __global__ void __launch_bounds__(128, 8) embed_sum_kernel(SumArgs a, const T* _
     }
 }
 
-// The crossing runs' partial rows, in order, 32 * VE columns at a time: one by a warp, or a long
+// The crossing runs' partial rows (531 runs of 7264 in a batch of 16384 tokens), in order, 32 * VE columns at a time: one by a warp, or a long
 // one by a block, whose eight warps take every eighth partial and whose sums are added in warp
 // order.
 template <typename G, int VE, bool kAdd>
@@ -537,6 +546,9 @@ __device__ __forceinline__ void join_row(const SumArgs& a, G* dW, uint32_t key, 
     Vec<G, VE>::store(p, s);
 }
 
+// The other blocks zero the rows that get no sum and that the sort's launches have not zeroed: the
+// joins' chain of latencies (8 us) passes beside them. The whole gradient of 16384 x 1024 bf16 into
+// 131072 rows: 60.5 us, 4990 GB/s of needed traffic (74 %); zeros after the joins: 87.
 template <typename G, int VE, bool kAdd>
 __global__ void __launch_bounds__(256) embed_join_kernel(SumArgs a, G* __restrict__ dW) {
     __shared__ float part[kWarps][32 * VE];
