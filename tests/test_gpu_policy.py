@@ -118,7 +118,7 @@ def test_policy_more_rows_than_sms(T, V, moe_lib, cuda_device):
     check(moe_lib, make(T, V, "bf16"), "bf16")
 
 
-@pytest.mark.parametrize("dtype,V", [("bf16", 458752), ("bf16", 600001), ("f32", 229376), ("f32", 250003)])
+@pytest.mark.parametrize("dtype,V", [("bf16", 393216), ("bf16", 393300), ("bf16", 600001), ("f32", 196608), ("f32", 250003)])
 def test_policy_rows_past_shared_memory(dtype, V, moe_lib, cuda_device):
     """The longest rows that a cluster keeps, and longer ones; also in place."""
     check(moe_lib, make(3, V, dtype), dtype)
