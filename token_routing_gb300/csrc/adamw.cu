@@ -9,7 +9,7 @@
 #include <cmath>
 #include <type_traits>
 
-#include "internal.cuh"
+#include "pairs.cuh"
 
 namespace moe {
 

@@ -1,6 +1,7 @@
 // Policy loss on the logits of the chosen tokens, its gradient, and token log-probabilities.
 #include <cmath>
 
+#include "pairs.cuh"
 #include "tc_ptx.cuh"
 
 namespace moe {
