@@ -18,6 +18,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kUnit = MOE_ADAMW_BLOCK;     // elements a warp takes at a time: 8 a lane, one scale block
 constexpr uint32_t kTicket = 1024;         // blocks that may take a ticket each
+constexpr int kResident[2] = {2, 3};       // blocks to an SM, with fp32 and with 8-bit states
 constexpr int kRun[2] = {16, 32};          // longest runs, with fp32 and with 8-bit states
 constexpr int kBatch = kThreads;           // tensors in one launch's parameters, one looked at by each thread
 
@@ -450,7 +451,7 @@ __device__ __noinline__ void last_unit(const TensorArg& t, const Step& s, int64_
 // weights: 2800 us, 6350 GB/s (94 %), four fifths of the issue slots taken: the next unit's loads
 // pass under the arithmetic of this one (without: 3400), and blocks start seldom (runs of 8: 3000).
 template <bool kNarrow>
-__global__ void __launch_bounds__(kThreads, kNarrow ? 3 : 2) adamw_kernel(const __grid_constant__ AdamArgs a) {
+__global__ void __launch_bounds__(kThreads, kResident[kNarrow]) adamw_kernel(const __grid_constant__ AdamArgs a) {
     pdl_wait();
     // The step's scalars, by one thread: double precision is slow here, and every block pays for it.
     __shared__ float corr[2];
@@ -576,8 +577,13 @@ extern "C" MOE_API moe_status_t moe_adamw(const moe_adamw_config_t* cfg, const m
     const int launches[2] = {units[0] > 0 || units[1] == 0, units[1] > 0};
     for (int narrow = 0; narrow < 2; ++narrow) {
         if (!launches[narrow]) continue;
-        // long runs spare blocks their start, short ones spread small tensors over more blocks
-        a.run = (int)std::min<int64_t>(kRun[narrow], std::max<int64_t>(1, units[narrow] / (8LL * 4 * num_sms())));
+        // Runs that fill whole rounds of the SMs, as few as the longest run allows, with a block more to
+        // each tensor for its last, short run. A block's start (parameters, state, first loads) costs
+        // what several units do: 29M weights with 8-bit states 98 us in 1.3 rounds, 93 in ten.
+        const int64_t slots = (int64_t)num_sms() * kResident[narrow], per_slot = (units[narrow] + 8 * slots - 1) / (8 * slots);
+        const int64_t rounds = std::max<int64_t>(1, (per_slot + kRun[narrow] - 1) / kRun[narrow]);
+        const int64_t blocks = std::max<int64_t>(rounds * slots - std::min<int64_t>(count, slots / 2), 1);
+        a.run = (int)std::min<int64_t>(kRun[narrow], std::max<int64_t>(1, (units[narrow] + 8 * blocks - 1) / (8 * blocks)));
         if (units[narrow] / (8 * a.run) + count > INT32_MAX) return MOE_ERR_UNSUPPORTED;
         int i = 0;
         bool last = false;

@@ -141,15 +141,18 @@ cudaError_t launch_embed(const moe_embed_config_t& c, const int32_t* ids, const 
 // 6 at 32768. One block for all of it takes 4 us at 777 tokens, 6 at 2048, 10 at 4096 and 45 at
 // 16384 (one SM then ranks and scatters everything): it sorts batches of up to 4096.
 // The sort needs few of the SMs: the other blocks of its launches zero the first rows of a dW that
-// is overwritten, whether or not they get a sum later.
+// is overwritten, whether or not they get a sum later. (Where dW is added to, bringing dy into the
+// L2 cache meanwhile gained nothing: the sums wait for latencies, not for bytes.)
 struct ZeroArgs {
-    uint4* p;
-    int64_t n;               // 16-byte vectors
+    char* p;
+    int64_t bytes;                         // a multiple of 16
 };
+constexpr int kZeroBytes = 16384;          // a block's part
 
-__device__ __forceinline__ void zero_share(const ZeroArgs& z, int block, int blocks) {
-    const int64_t step = (int64_t)blocks * blockDim.x;
-    for (int64_t i = (int64_t)block * blockDim.x + threadIdx.x; i < z.n; i += step) z.p[i] = make_uint4(0u, 0u, 0u, 0u);
+__device__ __forceinline__ void zero_part(const ZeroArgs& z, int block) {
+    char* p = z.p + (int64_t)block * kZeroBytes;
+    const int n = (int)min((int64_t)kZeroBytes, z.bytes - (int64_t)block * kZeroBytes);
+    for (int i = threadIdx.x * 16; i < n; i += blockDim.x * 16) *reinterpret_cast<uint4*>(p + i) = make_uint4(0u, 0u, 0u, 0u);
 }
 
 constexpr int kChunk = 1024;         // pairs a block of 256 threads ranks
@@ -201,7 +204,7 @@ __global__ void __launch_bounds__(256) embed_hist_kernel(SortArgs a, ZeroArgs z)
     for (int b = threadIdx.x; b < bins; b += 256) h[b] = 0;
     pdl_wait();
     if ((int)blockIdx.x >= a.chunks) {
-        zero_share(z, blockIdx.x - a.chunks, gridDim.x - a.chunks);
+        zero_part(z, blockIdx.x - a.chunks);
         return;
     }
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < a.later; i += (int64_t)a.chunks * 256)
@@ -246,7 +249,7 @@ __global__ void __launch_bounds__(256) embed_scatter_kernel(SortArgs a, ZeroArgs
     for (int b = threadIdx.x; b < kWarps * kMaxBins; b += 256) (&cnt[0][0])[b] = 0;
     pdl_wait();
     if ((int)blockIdx.x >= a.chunks) {
-        zero_share(z, blockIdx.x - a.chunks, gridDim.x - a.chunks);
+        zero_part(z, blockIdx.x - a.chunks);
         return;
     }
     __syncthreads();
@@ -328,7 +331,7 @@ __global__ void __launch_bounds__(kOneThreads) embed_sort_kernel(SortArgs a, int
     __shared__ int total[kMaxBins], tmp[kOneWarps];
     pdl_wait();
     if (blockIdx.x > 0) {
-        zero_share(z, blockIdx.x - 1, gridDim.x - 1);
+        zero_part(z, blockIdx.x - 1);
         return;
     }
     if (threadIdx.x < 2) a.crossing[threadIdx.x] = 0;
@@ -463,9 +466,15 @@ __device__ __forceinline__ void zero_rows(const SumArgs& a, G* dW, int block) {
 #pragma unroll
     for (int i = 0; i < VE; ++i) z[i] = 0.f;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int v = v0 + warp; v < v1; v += blockDim.x >> 5)
-        if (!seen[v - v0])
+    const int64_t row = (int64_t)a.d * (int64_t)sizeof(G);
+    for (int v = v0 + warp; v < v1; v += blockDim.x >> 5) {
+        if (seen[v - v0]) continue;
+        char* p = reinterpret_cast<char*>(dW) + v * row;
+        if (row % 16 == 0)
+            for (int64_t c = lane * 16; c < row; c += 512) *reinterpret_cast<uint4*>(p + c) = make_uint4(0u, 0u, 0u, 0u);
+        else
             for (int c = lane * VE; c < a.d; c += 32 * VE) Vec<G, VE>::store(dW + (int64_t)v * a.d + c, z);
+    }
 }
 
 template <typename T, typename G, int VE, bool kAdd>
@@ -681,14 +690,14 @@ cudaError_t launch_embed_bwd(const moe_embed_config_t& c, const int32_t* ids, co
         const int passes = ceil_div(bits, kMaxBits), digit = ceil_div(bits, passes);
         SortArgs a{ids, nullptr, w.a, w.hist, nullptr, 0, w.crossing, c.T, c.V, c.padding_id, 0, digit,
                    ceil_div(c.T, kChunk), device_error_word()};
-        // the next `wish` bytes of dW, in whole rows whose bytes are a multiple of 16, and blocks for them
+        // the next `wish` bytes of dW, in whole rows whose bytes are a multiple of 16, and their blocks
         const int64_t row = (int64_t)c.d * (int64_t)sizeof(G);
         unsigned blocks = 0;
         const auto zero_next = [&](int64_t wish) {
             const int rows = c.accumulate ? 0 : (int)std::min<int64_t>(c.V - sums.zero_from, wish / row) & ~15;
-            ZeroArgs z{reinterpret_cast<uint4*>(static_cast<char*>(dW) + sums.zero_from * row), rows * row / 16};
+            const ZeroArgs z{static_cast<char*>(dW) + sums.zero_from * row, rows * row};
             sums.zero_from += rows;
-            blocks = (unsigned)((z.n + 1023) / 1024);
+            blocks = (unsigned)((z.bytes + kZeroBytes - 1) / kZeroBytes);
             return z;
         };
         cudaError_t e;
