@@ -742,7 +742,7 @@ cudaError_t launch_policy(const PolicyArgs& a, const void* logits, void* dlogits
 moe_status_t check_policy(const moe_policy_config_t* c) {
     if (!c || c->T < 0 || c->V < 1 || c->ld < c->V || c->ld_grad < c->V) return MOE_ERR_INVALID_ARG;
     if (c->dtype != MOE_F32 && c->dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
-    if (!(c->temperature > 0.f) || !std::isfinite(c->temperature) || !std::isfinite(1.f / c->temperature))
+    if (!(c->temperature > 0.f) || !std::isfinite(c->temperature) || !std::isfinite(2.f / c->temperature))
         return MOE_ERR_INVALID_ARG;
     if (!(c->clip_low >= 0.f && c->clip_low <= 1.f) || !(c->clip_high >= 0.f) || !std::isfinite(c->clip_high) ||
         !std::isfinite(c->kl_weight))
