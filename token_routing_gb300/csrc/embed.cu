@@ -542,9 +542,9 @@ __global__ void __launch_bounds__(128, 8) embed_sum_kernel(SumArgs a, const T* _
     }
 }
 
-// The crossing runs' partial rows (531 runs of 7264 in a batch of 16384 tokens), in order, 32 * VE columns at a time: one by a warp, or a long
-// one by a block, whose eight warps take every eighth partial and whose sums are added in warp
-// order.
+// The crossing runs' partial rows (531 runs of 7264 in a batch of 16384 tokens), in order,
+// 32 * VE columns at a time: one by a warp, or a long one by a block, whose eight warps take every
+// eighth partial and whose sums are added in warp order.
 template <typename G, int VE, bool kAdd>
 __device__ __forceinline__ void join_row(const SumArgs& a, G* dW, uint32_t key, int col, float (&s)[VE]) {
     G* p = dW + (int64_t)key * a.d + col;
