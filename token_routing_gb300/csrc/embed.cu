@@ -492,10 +492,12 @@ __global__ void __launch_bounds__(128, 8) embed_sum_kernel(SumArgs a, const T* _
 #pragma unroll
         for (int i = 0; i < VE; ++i) s[i] = 0.f;
         bool from_before = pr[0].x == pr[1].x;
-        // four rows in flight, two where dW is added to, whose old rows take registers too: with eight
-        // (and four) half as many blocks fit an SM (32768 x 2048 into fp32: 88 against 81 us). All 16
-        // staged in shared memory by asynchronous copies cost residency too: 65 against 53 us.
-        constexpr int kAtOnce = kAdd ? 2 : 4;
+        // Rows in flight: four, or two where dW is added to, whose old rows take registers too: with
+        // eight (and four) half as many blocks fit an SM (32768 x 2048 into fp32: 88 against 81 us). All
+        // 16 staged in shared memory by asynchronous copies cost residency too: 65 against 53 us.
+        // Vectors of one or two elements take few registers, and go 16 at once: 6566 x 1393 bf16 added
+        // to fp32 36 us against 51, 32768 x 511 54 against 81.
+        constexpr int kAtOnce = VE <= 2 ? kGroup : kAdd ? 2 : 4;
 #pragma unroll
         for (int j0 = 0; j0 < kGroup; j0 += kAtOnce) {
             Bits<T, VE> r[kAtOnce];
