@@ -85,6 +85,23 @@ def test_lookup_long_batch(moe_lib, cuda_device):
     check_forward(moe_lib, ids, W, 1.0, "bf16")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d", [(2001, 1021), (3001, 1022), (6001, 1020)])
+def test_lookup_long_batch_of_short_vectors(T, d, dtype, moe_lib, cuda_device):
+    """The same for rows of one, two and four elements a vector."""
+    ids, W, _ = make(T, 100, d, dtype)
+    check_forward(moe_lib, ids, W, 0.3, dtype)
+
+
+@pytest.mark.parametrize("dtype,grad", [("bf16", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("T,V,d", [(1029, 300, 131), (1029, 4000, 131), (1029, 60, 262)])
+def test_gradient_of_short_vectors(T, V, d, dtype, grad, accumulate, moe_lib, cuda_device):
+    """Whole groups in flight: runs inside them, across them, and both."""
+    ids, _, dy = make(T, V, d, dtype)
+    check_backward(moe_lib, ids, dy, V, 0.7, dtype, grad, accumulate, pad=-1)
+
+
 @pytest.mark.parametrize("dtype,grad", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32"), ("f32", "bf16")])
 @pytest.mark.parametrize("accumulate", [False, True])
 @pytest.mark.parametrize("T,V,d", [(1, 1, 1), (1, 700, 64), (31, 3, 37), (32, 40, 8), (33, 1000, 130), (257, 90, 6),

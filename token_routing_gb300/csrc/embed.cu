@@ -66,8 +66,10 @@ int row_vec(int d, int es) {
 // ---------------------------------------------------------------- lookup
 // y[t] = scale * W[ids[t]]: U vectors a thread, all loads of a thread in flight together. Bound by
 // memory and the two latencies (id, then row) a block pays. 16384 x 1024 bf16 tokens: 10.6 us, 4590
-// GB/s of needed traffic (68 %); U = 1: 12.1, U = 4: 11.7, U = 8: 16.5. Fewer vectors than 8 to
-// each of an SM's 2048 threads take U = 1: there latency counts, not bytes.
+// GB/s of needed traffic (68 %); U = 1: 12.1, U = 4: 11.7, U = 8: 16.5. Shorter vectors take more:
+// of four elements 4 (16384 x 1020 bf16 13.4 us, 14.8 with 2, 15.7 with 8), of one or two 8 (x 1022
+// 19.5, 23.9 with 2; x 1023 31.4, 41.6). Fewer vectors than 4 to each of an SM's 2048 threads take
+// U = 1: there latency counts, not bytes.
 template <typename T, int VE, int U>
 __global__ void __launch_bounds__(256) embed_kernel(const int32_t* __restrict__ ids, const T* __restrict__ W,
                                                     T* __restrict__ y, uint32_t total, uint32_t nvec, int V,
@@ -109,9 +111,10 @@ cudaError_t launch_embed_v(const moe_embed_config_t& c, const int32_t* ids, cons
         const T* w = static_cast<const T*>(W);
         T* out = static_cast<T*>(y) + t0 * c.d;
         cudaError_t e;
+        constexpr int kMany = VE >= 8 ? 2 : VE == 4 ? 4 : 8;
         if (total >= 2048u * 4u * (uint32_t)num_sms())
-            e = launch_pdl(embed_kernel<T, VE, 2>, dim3(ceil_div(total, 512)), dim3(256), 0, s, ids + t0, w, out, total,
-                           (uint32_t)nvec, (int)c.V, c.scale, device_error_word());
+            e = launch_pdl(embed_kernel<T, VE, kMany>, dim3(ceil_div(total, 256 * kMany)), dim3(256), 0, s,
+                           ids + t0, w, out, total, (uint32_t)nvec, (int)c.V, c.scale, device_error_word());
         else
             e = launch_pdl(embed_kernel<T, VE, 1>, dim3(ceil_div(total, 256)), dim3(256), 0, s, ids + t0, w, out, total,
                            (uint32_t)nvec, (int)c.V, c.scale, device_error_word());
