@@ -563,7 +563,7 @@ __device__ __forceinline__ void join_row(const SumArgs& a, G* dW, uint32_t key, 
 
 // The other blocks zero the rows that get no sum and that the sort's launches have not zeroed: the
 // joins' chain of latencies (8 us) passes beside them. The whole gradient of 16384 x 1024 bf16 into
-// 131072 rows: 60.5 us, 4990 GB/s of needed traffic (74 %); zeros after the joins: 87.
+// 131072 rows: 61 us, 4950 GB/s of needed traffic (73 %); zeros after the joins: 87.
 template <typename G, int VE, bool kAdd>
 __global__ void __launch_bounds__(256) embed_join_kernel(SumArgs a, G* __restrict__ dW) {
     __shared__ float part[kWarps][32 * VE];
