@@ -339,23 +339,18 @@ def _policy(s):
 
 
 def _dither(n, step):
-    """20 bits for each element and step, twice: what the 8-bit states of m and of v are rounded with."""
+    """A Weyl sequence over elements and steps, 20 bits: what the 8-bit states are rounded with."""
     i = torch.arange(n, dtype=torch.int64, device="cuda")
-    h = (i * 0x9E3779B1 + step * 0x61C88647) & 0xFFFFFFFF
-    h = ((h ^ (h >> 15)) * 0x85EBCA6B) & 0xFFFFFFFF
-    return h >> 12, ((h * 0xC2B2AE35) & 0xFFFFFFFF) >> 12
+    return ((i * 0x9E3779B1 + step * 0x61C88647) & 0xFFFFFFFF) >> 12
 
 
-def _to_e4m3(x, dither, root):
-    """x on e4m3's grid, one step up with a probability that leaves x (or, for a root, its square) as it is on
-    average. A root above zero keeps the least step."""
+def _to_e4m3(x, dither, least):
+    """x rounded down to e4m3's grid after `dither` (20 bits of one grid step) was added."""
     a = x.abs()
-    high = a >= 2.0 ** -6
-    low = torch.where(high, (a.view(torch.int32) & ~0xFFFFF).view(torch.float32), torch.floor(a * 512) * 2.0 ** -9)
-    unit = torch.where(high, ((a.view(torch.int32) & 0x7F800000) - (3 << 23)).view(torch.float32), 2.0 ** -9)
-    over, step = (a - low, unit) if not root else ((a - low) * (a + low), unit * (2 * low + unit))
-    code = torch.where(over >= (0x100000 - dither).float() * 2.0 ** -20 * step, low + unit, low)
-    if root:
+    code = torch.where(a < 2.0 ** -6,
+                       torch.floor(a * 512 + dither.float() * 2.0 ** -20) * 2.0 ** -9,
+                       ((a.view(torch.int32).long() + dither) & ~0xFFFFF).to(torch.int32).view(torch.float32))
+    if least:
         code = torch.where((a > 0) & (code == 0), 2.0 ** -9, code)
     return torch.copysign(code, x).to(torch.float8_e4m3fn)
 
@@ -365,12 +360,12 @@ def _blocks(x):
     return torch.nn.functional.pad(x, (0, -n % BLOCK)).view(-1, BLOCK)
 
 
-def _quantise(x, codes, scales, dither, root):
+def _quantise(x, codes, scales, dither, least):
     # the power of two that leaves a block's largest magnitude in [128, 256)
     top = _blocks(x.abs()).amax(1)
     scale = torch.where(top > 0, torch.ldexp(torch.ones_like(top), torch.frexp(top)[1] - 8), 0.0)
     y = (_blocks(x) / torch.where(top > 0, scale, 1.0)[:, None]).reshape(-1)[:x.numel()]
-    codes.copy_(_to_e4m3(y, dither, root))
+    codes.copy_(_to_e4m3(y, dither, least))
     scales.copy_(scale)
 
 
@@ -396,9 +391,9 @@ def _adamw_one(p, g, w, m, v, ms, vs, decay, step):
         m.copy_(m_new)
         v.copy_(v_new)
     else:
-        for_m, for_v = _dither(p.numel(), step)
-        _quantise(m_new, m, ms, for_m, False)
-        _quantise(root, v, vs, for_v, True)   # the root of v is what is held
+        dither = _dither(p.numel(), step)
+        _quantise(m_new, m, ms, dither, False)
+        _quantise(root, v, vs, dither ^ 0x80000, True)   # the root of v is what is held
 
 
 def _adamw(s):
@@ -495,32 +490,28 @@ def _exact_policy(s, c):
     return {"logp": torch.where(kept, lp.detach(), 0.0), "loss": loss.detach().reshape(1), "dlogits": dz}
 
 
-def _grid64(x, dither, root):
-    """|x| between two neighbours of e4m3's grid (three bits after a number's leading one, 2^-9 at the least): the
-    upper one where the share of the way, of x or of its square, and the dither come to one."""
+def _grid64(x, dither, least):
+    """|x| on e4m3's grid (three bits of a number's leading one, 2^-9 at the least), rounded down with the dither."""
     a = x.abs()
     unit = torch.pow(2.0, (torch.frexp(a)[1].double() - 4).clamp(min=-9))
-    low = torch.floor(a / unit) * unit
-    k = 2 if root else 1
-    share = (a ** k - low ** k) / ((low + unit) ** k - low ** k)
-    q = torch.where(share + dither.double() / 2 ** 20 >= 1, low + unit, low)
-    return torch.sign(x) * (torch.where(a > 0, q.clamp(min=2.0 ** -9), q) if root else q)
+    q = torch.floor(a / unit + dither.double() / 2 ** 20) * unit
+    return torch.sign(x) * (torch.where(a > 0, q.clamp(min=2.0 ** -9), q) if least else q)
 
 
 def _exact_adamw(s, c):
     h, step = HYPER, s["step"] + 1
-    # no value for the scales: a block's largest magnitude within rounding of a power of two may take either
-    out = {k: t.double() for k, t in s["flat"].items() if k not in ("g16", "g32", "ms", "vs") and t.numel()}
+    out = {k: t.double() for k, t in s["flat"].items() if k not in ("g16", "g32") and t.numel()}
 
     def put(key, view, x):
         at = view.storage_offset()
         out[key][at:at + x.numel()] = x
 
-    def held(key, view, x, dither, root):
+    def held(key, view, scales, x, dither, least):
         top = _blocks(x.abs()).amax(1)
         two = torch.where(top > 0, torch.exp2(torch.floor(torch.log2(top.clamp(min=1e-300))) - 7), 0.0)
         unit = torch.where(two > 0, two, 1.0).repeat_interleave(BLOCK)[:x.numel()]
-        put(key, view, _grid64(x / unit, dither, root))
+        put(key, view, _grid64(x / unit, dither, least))
+        put(key + "s", scales, two)
 
     for p, g, w, m, v, ms, vs, dec in zip(s["p"], s["g"], s["w"], s["m"], s["v"], s["ms"], s["vs"], s["decay"]):
         n, g = p.numel(), g.double()
@@ -541,7 +532,7 @@ def _exact_adamw(s, c):
             put("m", m, m1)
             put("v", v, v1)
         else:
-            for_m, for_v = _dither(n, step)
-            held("m", m, m1, for_m, False)
-            held("v", v, v1.sqrt(), for_v, True)
+            dither = _dither(n, step)
+            held("m", m, ms, m1, dither, False)
+            held("v", v, vs, v1.sqrt(), dither ^ 0x80000, True)
     return out
