@@ -371,9 +371,9 @@ MOE_API moe_status_t moe_token_logp(const moe_policy_config_t* cfg, const void* 
  * e4m3 values of m, v holds e4m3 values of sqrt(v), both times one fp32 scale to a block of
  * MOE_ADAMW_BLOCK elements (m_scale, v_scale [ceil(n / MOE_ADAMW_BLOCK)]: the power of two that
  * leaves the block's largest magnitude in [128, 256), 0 for a block below 2^-100). They are
- * rounded up or down by a dither, a hash of element and step, so that m and v are right on
- * average: rounding to nearest would hold sqrt(v) still, because beta2 = 0.999 moves it by
- * 0.05 % a step and half a step of e4m3 is 3 to 6 %. sqrt(v) > 0 never becomes 0. A value that is not finite is held as NaN and
+ * rounded up or down by a dither of element and step (cfg->rounding): rounding to nearest would
+ * hold sqrt(v) still, because beta2 = 0.999 moves it by 0.05 % a step and half a step of e4m3 is
+ * 3 to 6 %. sqrt(v) > 0 never becomes 0. A value that is not finite is held as NaN and
  * leaves the rest of its block alone. The step itself uses m and v before they are rounded.
  * Zeroed states (and scales) are the start of training. Arrays are 16-byte aligned (scales,
  * lr, grad_scale: 4), tensors do not overlap; n = 0 is allowed.
@@ -385,8 +385,19 @@ MOE_API moe_status_t moe_token_logp(const moe_policy_config_t* cfg, const void* 
  *     and 8 bytes that are zero between calls. Calls on one state are ordered on the GPU. */
 #define MOE_ADAMW_BLOCK 256
 #define MOE_ADAMW_STATE_BYTES 32
+/* How 8-bit states are rounded. With s the share of the way from the held value below to the one
+ * above, and d 20 bits of dither, the upper one is taken where s + d / 2^20 >= 1.
+ *   MOE_ADAMW_ROUND_EVEN: d from a hash of element and step, one for m and one for v; v's share is
+ *     taken between the squares. m and v are right on average.
+ *   MOE_ADAMW_ROUND_WEYL: d the top 20 bits of i 0x9E3779B1 + t 0x61C88647 (mod 2^32) for element i
+ *     of a tensor in step t; for v with its top bit turned, and the share taken in sqrt(v) itself.
+ *     Fewer instructions, but v comes out some per cent high (beta2 = 0.999: 3 to 9). */
+#define MOE_ADAMW_ROUND_EVEN 0
+#define MOE_ADAMW_ROUND_WEYL 1
 typedef struct {
     double lr, beta1, beta2, eps;   /* lr finite, betas in [0, 1), eps in [1e-30, 1e30] */
+    int32_t rounding;               /* MOE_ADAMW_ROUND_*: 8-bit states only */
+    int32_t reserved;               /* 0 */
 } moe_adamw_config_t;
 typedef struct {
     void* p;                /* [n] weights, dtype */

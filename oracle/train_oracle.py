@@ -95,6 +95,14 @@ def dither(n, step, start=0):
         return (h >> np.uint64(12)).astype(np.float64), (((h * e) & low) >> np.uint64(12)).astype(np.float64)
 
 
+def weyl(n, step, start=0):
+    """The 20 bits of a Weyl sequence over elements and steps, for m; for v with the top bit turned."""
+    i = np.arange(start, start + n, dtype=np.uint64)
+    with np.errstate(over="ignore"):
+        d = ((i * np.uint64(0x9E3779B1) + np.uint64(step * 0x61C88647)) & np.uint64(0xFFFFFFFF)) >> np.uint64(12)
+    return d.astype(np.float64), (d ^ np.uint64(0x80000)).astype(np.float64)
+
+
 def blocks(x):
     n = len(x)
     return np.pad(x, (0, -n % BLOCK)).reshape(-1, BLOCK)
@@ -106,14 +114,14 @@ def block_scale(x):
     return np.where(top > 0, 2.0 ** (np.floor(np.log2(np.where(top > 0, top, 1.0))) - 7), 0.0)
 
 
-def held(y, d, root):
+def held(y, d, root, even=True):
     """The e4m3 value that y is held as: one of its two neighbours on the grid, the upper one where
-    the share of the way to it, of y or (a root) of y^2, and the dither d (20 bits) come to 1. A
-    root above zero keeps the least step."""
+    the share of the way to it, of y or (a root, evened in its square) of y^2, and the dither d (20
+    bits) come to 1. A root above zero keeps the least step."""
     a = np.abs(y)
     unit = 2.0 ** np.maximum(np.floor(np.log2(np.where(a > 0, a, 1e-30))) - 3, -9)
     low = np.floor(a / unit) * unit
-    k = 2 if root else 1
+    k = 2 if root and even else 1
     share = (a ** k - low ** k) / ((low + unit) ** k - low ** k)
     q = np.where(share + d / 2 ** 20 >= 1, low + unit, low)
     if root:

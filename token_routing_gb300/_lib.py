@@ -25,6 +25,7 @@ MOE_MAX_K = 8
 MOE_MAX_WINDOW = 4096
 MOE_ADAMW_BLOCK = 256
 MOE_ADAMW_STATE_BYTES = 32
+MOE_ADAMW_ROUND = {"even": 0, "weyl": 1}
 
 
 class MoeConfig(ctypes.Structure):
@@ -56,7 +57,7 @@ class MoePolicyConfig(ctypes.Structure):
 
 class MoeAdamwConfig(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
-                ("eps", ctypes.c_double)]
+                ("eps", ctypes.c_double), ("rounding", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class MoeAdamwTensor(ctypes.Structure):

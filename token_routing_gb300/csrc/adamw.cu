@@ -158,13 +158,20 @@ __device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c
 // is from step to step (a scale that followed the largest magnitude would move it, and re-round
 // every value, at each step), scaling is exact, and no carry passes 448.
 // kRoot: f are roots of second moments. odd: one of them is infinite or NaN, held as NaN.
-template <bool kRoot>
+// kWeyl: the words are a Weyl sequence, and a root's share of the way is taken in the root itself,
+// with the top bit of its word turned; a root above zero keeps at least code 1 here too.
+template <bool kRoot, bool kWeyl>
 __device__ __forceinline__ uint2 encode8(const uint64_t (&f)[4], float inv, bool odd, const uint32_t (&hash)[8]) {
     uint32_t c[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint64_t y = mul2(f[i], splat2(inv)), down = to_codes(y);
-        if constexpr (kRoot) {
+        if constexpr (kRoot && kWeyl) {
+            float y0, y1;
+            upk2(down, y0, y1);
+            c[2 * i] = max(value_code(y0, hash[2 * i] ^ 0x80000000u), min((uint32_t)y, 0x100000u) << 4);
+            c[2 * i + 1] = max(value_code(y1, hash[2 * i + 1] ^ 0x80000000u), min((uint32_t)(y >> 32), 0x100000u) << 4);
+        } else if constexpr (kRoot) {
             root_codes(y, down, hash[2 * i] * 0xC2B2AE35u, hash[2 * i + 1] * 0xC2B2AE35u, c[2 * i], c[2 * i + 1]);
         } else {
             float y0, y1;
@@ -248,21 +255,23 @@ __device__ __forceinline__ void advance8(const Step& s, const uint64_t (&g)[4], 
 }
 
 // The codes and scales of one block of both states.
+template <bool kWeyl>
 __device__ __forceinline__ void hold(const uint64_t (&m)[4], const uint64_t (&v)[4], const uint64_t (&root)[4],
                                      uint32_t h0, uint2& cm, uint2& cv, float& sm, float& sv) {
-    // one hash of element and step: its top bits dither m, those of an odd multiple v
+    // The Weyl word of element and step, or one hash of it: its top bits dither m, those of an odd
+    // multiple v.
     uint32_t hash[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const uint32_t h = h0 + i * 0x9E3779B1u;
-        hash[i] = (h ^ (h >> 15)) * 0x85EBCA6Bu;
+        hash[i] = kWeyl ? h : (h ^ (h >> 15)) * 0x85EBCA6Bu;
     }
     bool odd;
     float inv;
     sm = block_scale(block_top(m, odd), inv);
-    cm = encode8<false>(m, inv, odd, hash);
+    cm = encode8<false, kWeyl>(m, inv, odd, hash);
     sv = block_scale(__fsqrt_rn(block_top(v, odd)), inv);
-    cv = encode8<true>(root, inv, odd, hash);
+    cv = encode8<true, kWeyl>(root, inv, odd, hash);
 }
 
 // What a lane reads of one unit, as it is in memory.
@@ -276,7 +285,7 @@ struct Raw {
 // Whole units of one block's run: the block's eight warps take units u0 + 8 k + warp, eight
 // elements a lane, while they are whole. Addresses are the run's bases, the same for the block,
 // plus a 32-bit place.
-template <typename P, typename G, bool kMaster, bool kNarrow>
+template <typename P, typename G, bool kMaster, bool kNarrow, bool kWeyl>
 __device__ __forceinline__ void run_units(const TensorArg& t, const Step& s, int64_t u0, int count, int run) {
     __shared__ float scales[2][kNarrow ? kRun[1] * 8 : 1];
     using R = Raw<P, G, kMaster, kNarrow>;
@@ -335,7 +344,7 @@ __device__ __forceinline__ void run_units(const TensorArg& t, const Step& s, int
         if constexpr (kNarrow) {
             uint2 cm, cv;
             float sm, sv;
-            hold(M, V, root, ((uint32_t)i0 + i) * 0x9E3779B1u + s.dither, cm, cv, sm, sv);
+            hold<kWeyl>(M, V, root, ((uint32_t)i0 + i) * 0x9E3779B1u + s.dither, cm, cv, sm, sv);
             *reinterpret_cast<uint2*>(m + i) = cm;
             *reinterpret_cast<uint2*>(v + i) = cv;
             if ((threadIdx.x & 31) == 0) {
@@ -360,7 +369,7 @@ __device__ __forceinline__ void run_units(const TensorArg& t, const Step& s, int
 }
 
 // The unit that a tensor's end cuts short, element by element.
-template <bool kNarrow>
+template <bool kNarrow, bool kWeyl>
 __device__ __noinline__ void last_unit(const TensorArg& t, const Step& s, int64_t u, int lane) {
     const int64_t i0 = u * kUnit + lane * 8;
     const auto live = [&](int i) { return i0 + i < t.n; };
@@ -413,7 +422,7 @@ __device__ __noinline__ void last_unit(const TensorArg& t, const Step& s, int64_
     uint2 km{}, kv{};
     if constexpr (kNarrow) {
         float sm, sv;
-        hold(M, V, R, (uint32_t)i0 * 0x9E3779B1u + s.dither, km, kv, sm, sv);
+        hold<kWeyl>(M, V, R, (uint32_t)i0 * 0x9E3779B1u + s.dither, km, kv, sm, sv);
         if (lane == 0) {
             t.ms[u] = sm;
             t.vs[u] = sv;
@@ -450,7 +459,7 @@ __device__ __noinline__ void last_unit(const TensorArg& t, const Step& s, int64_
 // an SM, against 720 us at three and 800 at four, whose loads are cut apart. 8-bit states, 1.1G
 // weights: 2800 us, 6350 GB/s (94 %), four fifths of the issue slots taken: the next unit's loads
 // pass under the arithmetic of this one (without: 3400), and blocks start seldom (runs of 8: 3000).
-template <bool kNarrow>
+template <bool kNarrow, bool kWeyl>
 __global__ void __launch_bounds__(kThreads, kResident[kNarrow]) adamw_kernel(const __grid_constant__ AdamArgs a) {
     pdl_wait();
     // The step's scalars, by one thread: double precision is slow here, and every block pays for it.
@@ -493,18 +502,18 @@ __global__ void __launch_bounds__(kThreads, kResident[kNarrow]) adamw_kernel(con
         const int count = (int)min((int64_t)a.run * 8, whole);
         using B = __nv_bfloat16;
         switch (t.kind) {
-            case 0: run_units<float, float, false, kNarrow>(t, s, u0, count, a.run); break;
-            case 1: run_units<B, float, false, kNarrow>(t, s, u0, count, a.run); break;
-            case 2: run_units<float, B, false, kNarrow>(t, s, u0, count, a.run); break;
-            case 3: run_units<B, B, false, kNarrow>(t, s, u0, count, a.run); break;
-            case 4: run_units<float, float, true, kNarrow>(t, s, u0, count, a.run); break;
-            case 5: run_units<B, float, true, kNarrow>(t, s, u0, count, a.run); break;
-            case 6: run_units<float, B, true, kNarrow>(t, s, u0, count, a.run); break;
-            default: run_units<B, B, true, kNarrow>(t, s, u0, count, a.run); break;
+            case 0: run_units<float, float, false, kNarrow, kWeyl>(t, s, u0, count, a.run); break;
+            case 1: run_units<B, float, false, kNarrow, kWeyl>(t, s, u0, count, a.run); break;
+            case 2: run_units<float, B, false, kNarrow, kWeyl>(t, s, u0, count, a.run); break;
+            case 3: run_units<B, B, false, kNarrow, kWeyl>(t, s, u0, count, a.run); break;
+            case 4: run_units<float, float, true, kNarrow, kWeyl>(t, s, u0, count, a.run); break;
+            case 5: run_units<B, float, true, kNarrow, kWeyl>(t, s, u0, count, a.run); break;
+            case 6: run_units<float, B, true, kNarrow, kWeyl>(t, s, u0, count, a.run); break;
+            default: run_units<B, B, true, kNarrow, kWeyl>(t, s, u0, count, a.run); break;
         }
         // the unit that the tensor's end cuts short
         if (t.n % kUnit && whole < (int64_t)a.run * 8 && (int)(threadIdx.x >> 5) == (int)(whole & 7))
-            last_unit<kNarrow>(t, s, u0 + whole, threadIdx.x & 31);
+            last_unit<kNarrow, kWeyl>(t, s, u0 + whole, threadIdx.x & 31);
     }
     // the last block to take a ticket counts the step: every block has read the old count by then
     if (threadIdx.x == 0 && a.advance && ticket == gridDim.x - 1) {
@@ -529,7 +538,8 @@ bool misaligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintpt
 moe_status_t check_adamw(const moe_adamw_config_t* c, const moe_adamw_tensor_t* ts, int32_t count) {
     if (!c || count < 0 || (count > 0 && !ts)) return MOE_ERR_INVALID_ARG;
     if (!std::isfinite(c->lr) || !(c->beta1 >= 0.0 && c->beta1 < 1.0) || !(c->beta2 >= 0.0 && c->beta2 < 1.0) ||
-        !(c->eps >= 1e-30 && c->eps <= 1e30))
+        !(c->eps >= 1e-30 && c->eps <= 1e30) || c->reserved != 0 ||
+        (c->rounding != MOE_ADAMW_ROUND_EVEN && c->rounding != MOE_ADAMW_ROUND_WEYL))
         return MOE_ERR_INVALID_ARG;
     for (int i = 0; i < count; ++i) {
         const moe_adamw_tensor_t& t = ts[i];
@@ -577,6 +587,8 @@ extern "C" MOE_API moe_status_t moe_adamw(const moe_adamw_config_t* cfg, const m
     const int launches[2] = {units[0] > 0 || units[1] == 0, units[1] > 0};
     for (int narrow = 0; narrow < 2; ++narrow) {
         if (!launches[narrow]) continue;
+        const auto kernel = !narrow ? adamw_kernel<false, false>
+                            : cfg->rounding == MOE_ADAMW_ROUND_WEYL ? adamw_kernel<true, true> : adamw_kernel<true, false>;
         // Runs that fill whole rounds of the SMs, as few as the longest run allows, with a block more to
         // each tensor for its last, short run. A block's start (parameters, state, first loads) costs
         // what several units do: 29M weights with 8-bit states 98 us in 1.3 rounds, 93 in ten.
@@ -605,7 +617,7 @@ extern "C" MOE_API moe_status_t moe_adamw(const moe_adamw_config_t* cfg, const m
             // second launch takes.
             const bool ends = last && (narrow || !launches[1]), apart = a.runs > kTicket;
             a.advance = ends && !apart;
-            const cudaError_t e = launch_pdl(narrow ? adamw_kernel<true> : adamw_kernel<false>,
+            const cudaError_t e = launch_pdl(kernel,
                                              dim3(std::max(1u, a.runs)), dim3(kThreads), 0, (cudaStream_t)stream, a);
             count_launch();
             if (e != cudaSuccess) return MOE_ERR_CUDA;

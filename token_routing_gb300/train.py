@@ -142,14 +142,20 @@ class AdamW:
                      MOE_ADAMW_BLOCK elements); left out, they are made, zeroed, by `bits`
       weight_decay   default: the class's
 
+    rounding: how 8-bit states are rounded, "even" (m and v right on average) or "weyl" (fewer
+    instructions, v some per cent high); see MOE_ADAMW_ROUND_*.
+
     step() takes one step on the current gradients; it may be captured into a CUDA graph, which
     then counts its own steps. The tensors are bound here: refill the gradients in place.
     `step` is the number of steps that the given states have seen."""
 
-    def __init__(self, tensors, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, bits=32, step=0):
+    def __init__(self, tensors, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, bits=32, step=0,
+                 rounding="even"):
         if bits not in (8, 32):
             raise ValueError("bits: 8 or 32")
-        self.cfg = L.MoeAdamwConfig(lr=lr, beta1=beta1, beta2=beta2, eps=eps)
+        if rounding not in L.MOE_ADAMW_ROUND:
+            raise ValueError(f"rounding: one of {sorted(L.MOE_ADAMW_ROUND)}")
+        self.cfg = L.MoeAdamwConfig(lr=lr, beta1=beta1, beta2=beta2, eps=eps, rounding=L.MOE_ADAMW_ROUND[rounding])
         self.tensors = [self._bind(dict(t), weight_decay, bits) for t in tensors]
         self.table = (L.MoeAdamwTensor * max(1, len(self.tensors)))()
         for e, t in zip(self.table, self.tensors):
