@@ -402,7 +402,8 @@ def _adamw(s):
         if "opt" not in s:
             s["opt"] = moe.AdamW([dict(p=p, g=g, master=w, m=m, v=v, m_scale=ms, v_scale=vs, weight_decay=dec)
                                   for p, g, w, m, v, ms, vs, dec in zip(s["p"], s["g"], s["w"], s["m"], s["v"],
-                                                                        s["ms"], s["vs"], s["decay"])], step=s["step"], **HYPER)
+                                                                        s["ms"], s["vs"], s["decay"])],
+                                 step=s["step"], rounding="weyl", **HYPER)
         s["opt"].step()
     else:
         s["step"] += 1
