@@ -1,0 +1,53 @@
+"""Policy loss and token log-probabilities at the edges of rows: the elements before a row's first and
+after its last whole 16-byte vector."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def masked_rows(T, V, dtype, seed=0):
+    """Rows of -inf with eight finite logits, whose vectors belong to no thread that has an edge element;
+    one of the eight is the target. An odd V starts the rows at every alignment."""
+    g = torch.Generator().manual_seed(seed)
+    n = 16 // (2 if dtype == "bf16" else 4)
+    at = V // 2 // (256 * n) * 256 * n + 100 * n + torch.arange(8) if V > 2 * 256 * n else V // 2 + torch.arange(8)
+    z = torch.full((T, V), -float("inf"))
+    z[:, at] = torch.randn(T, 8, generator=g)
+    target = at[torch.randint(0, 8, (T,), generator=g)]
+    return z.to(DT[dtype]).cuda(), target.int().cuda()
+
+
+@pytest.mark.parametrize("dtype,V", [("bf16", 301), ("bf16", 5003), ("bf16", 20001), ("bf16", 50257), ("bf16", 140003),
+                                     ("bf16", 600001), ("f32", 303), ("f32", 9001), ("f32", 70003), ("f32", 250003)])
+@pytest.mark.parametrize("bad", ["nan", "inf"])
+def test_edge_elements_of_masked_rows(dtype, V, bad, moe_lib, cuda_device):
+    """A NaN or +inf in a row's first or last element, all but a few of the others being -inf: NaN for the
+    row and the loss, and nothing for the other rows."""
+    T = 17
+    z, target = masked_rows(T, V, dtype)
+    adv, old = torch.ones(T, device="cuda"), torch.full((T,), -2.0, device="cuda")
+    cfg = moe_lib.make_policy_config(T, V, dtype)
+    ws = torch.empty(moe_lib.policy_workspace_bytes(cfg), dtype=torch.uint8, device="cuda")
+
+    def call():
+        lp, own, loss, dz = (torch.empty(*s, device="cuda", dtype=t) for s, t in
+                             (((T,), torch.float32), ((T,), torch.float32), ((1,), torch.float32), ((T, V), DT[dtype])))
+        moe_lib.policy_loss(cfg, z, target, adv, old, None, None, lp, loss, dz, ws)
+        moe_lib.token_logp(cfg, z, target, own)
+        return lp, own, loss, dz
+
+    clean = call()
+    assert all(x.isfinite().all() for x in clean)
+    rows = {t: (0 if t % 2 else V - 1) for t in range(1, T, 2)} | {t: (V - 1 if t % 4 else 0) for t in range(2, T, 4)}
+    for t, v in rows.items():
+        z[t, v] = float(bad)
+    lp, own, loss, dz = call()
+    hit = torch.tensor(sorted(rows), device="cuda")
+    rest = torch.tensor([t for t in range(T) if t not in rows], device="cuda")
+    assert lp[hit].isnan().all() and own[hit].isnan().all() and loss.isnan().all() and dz[hit].isnan().all()
+    for got, want in ((lp, clean[0]), (own, clean[1]), (dz, clean[3])):
+        assert torch.equal(got[rest], want[rest])
+    moe_lib.get_error()

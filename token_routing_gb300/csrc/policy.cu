@@ -485,7 +485,8 @@ policy_ring_kernel(PolicyArgs a, const T* logits, T* dlogits, int reuse) {
             float s0, s1;
             upk2(run.s, s0, s1);
             MaxSum acc{run.m, s0 + s1};
-            if (tid < s.rest) acc = join(acc, MaxSum{lone, lone == -INFINITY ? 0.f : 1.f}, k);
+            // a NaN goes into the sum, which keeps it: the maximum passes over it
+            if (tid < s.rest) acc = join(acc, MaxSum{lone, lone == -INFINITY ? 0.f : lone != lone ? lone : 1.f}, k);
             acc = warp_join(acc, k);
             // ---- exchange. What this warp reads of the row itself has arrived: once all warps have
             // sent, any of them may write over it (dlogits may be logits)
