@@ -47,3 +47,36 @@ def test_time_grows_with_the_batch(moe_lib, cuda_device):
             best = min(best, a.elapsed_time(b))
         took.append(best)
     assert took[1] < 8 * took[0], took
+
+
+def test_more_than_a_billion_tokens(moe_lib, cuda_device):
+    """Positions past 2^30, keys of four digits, rows left for the last launch to zero. One in three
+    tokens carries a one: each row of the gradient is a count, exact in fp32; odd ids do not occur."""
+    moe = moe_lib
+    T, V = 2 ** 30 + 4097, 2 ** 27 + 5
+    g = torch.Generator(device="cuda").manual_seed(0)
+    ids = torch.randint(0, V // 2, (T,), generator=g, device="cuda", dtype=torch.int32).mul_(2)
+    dy = torch.zeros(T, 1, dtype=torch.bfloat16, device="cuda")
+    dy[::3] = 1
+    cfg = moe.make_embed_config(T, V, 1, grad_dtype="f32")
+    dW = torch.full((V, 1), float("nan"), device="cuda")
+    ws = torch.empty(moe.embed_workspace_bytes(cfg), dtype=torch.uint8, device="cuda")
+    moe.embed_backward(cfg, ids, dy, dW, ws)
+    moe.get_error()
+    del ws, dy
+    assert torch.equal(dW[:, 0], torch.bincount(ids[::3].long(), minlength=V).float())
+    assert not dW[1::2].any()
+
+
+def test_lookup_of_more_than_a_billion_vectors(moe_lib, cuda_device):
+    """The vectors of one launch are numbered in 31 bits: a second launch takes the rest."""
+    moe = moe_lib
+    for T, d in ((2 ** 30 + 4097, 1), (2 ** 29 + 77, 3)):
+        g = torch.Generator(device="cuda").manual_seed(T)
+        W = torch.randn(1000, d, generator=g, device="cuda").bfloat16()
+        ids = torch.randint(0, 1000, (T,), generator=g, device="cuda", dtype=torch.int32)
+        y = torch.full((T, d), 9.0, dtype=torch.bfloat16, device="cuda")
+        moe.embed(moe.make_embed_config(T, 1000, d), ids, W, y)
+        for a in range(0, T, 2 ** 27):
+            assert torch.equal(y[a:a + 2 ** 27], W[ids[a:a + 2 ** 27]])
+    moe.get_error()

@@ -489,7 +489,7 @@ struct SumArgs {
 __device__ __forceinline__ int lower_bound(const uint2* p, int n, uint32_t key) {
     int lo = 0, hi = n;
     while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
+        const int mid = lo + (hi - lo) / 2;              // lo + hi passes 31 bits above 2^30 tokens
         if (p[mid].x < key) lo = mid + 1; else hi = mid;
     }
     return lo;
