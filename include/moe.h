@@ -305,9 +305,9 @@ MOE_API moe_status_t moe_coselect(const moe_config_t* cfg, const int32_t* idx, i
  * MOE_ERR_DEVICE_BOUNDS: its y row is zero and its dy row is left out.
  * W, y, dy, dW and ws are 16-byte aligned; T = 0 is allowed (an overwritten dW is zeroed). */
 typedef struct {
-    int32_t T;             /* tokens, >= 0 */
-    int32_t V;             /* rows of the table, >= 1 */
-    int32_t d;             /* row length, >= 1 */
+    int32_t T;             /* tokens, 0 .. 2^31 - 4097 */
+    int32_t V;             /* rows of the table, 1 .. 2^31 - 4097 */
+    int32_t d;             /* row length, 1 .. 2^28 */
     float scale;           /* finite */
     int32_t padding_id;    /* in [-1, V) */
     int32_t dtype;         /* moe_dtype_t of W, y, dy */
@@ -342,8 +342,8 @@ MOE_API moe_status_t moe_embed_backward(const moe_embed_config_t* cfg, const int
  * Softmax statistics and loss sums are fp32, in a fixed order. logits and dlogits start on a
  * 16-byte boundary; V, ld, ld_grad may be odd. */
 typedef struct {
-    int32_t T;             /* tokens, >= 0 */
-    int32_t V;             /* vocabulary, >= 1 */
+    int32_t T;             /* tokens, 0 .. 2^31 - 4097 */
+    int32_t V;             /* vocabulary, 1 .. 2^30 */
     int64_t ld;            /* elements between logits rows, >= V */
     int64_t ld_grad;       /* elements between dlogits rows, >= V */
     int32_t dtype;         /* moe_dtype_t of logits and dlogits */

@@ -748,7 +748,8 @@ moe_status_t check_policy(const moe_policy_config_t* c) {
     if (!(c->clip_low >= 0.f && c->clip_low <= 1.f) || !(c->clip_high >= 0.f) || !std::isfinite(c->clip_high) ||
         !std::isfinite(c->kl_weight))
         return MOE_ERR_INVALID_ARG;
-    if (c->V > (1 << 30) || c->ld > ((int64_t)1 << 40) || c->ld_grad > ((int64_t)1 << 40)) return MOE_ERR_UNSUPPORTED;
+    // a token past the last one that a loop steps to is numbered in 31 bits
+    if (c->T > INT32_MAX - 4096 || c->V > (1 << 30) || c->ld > ((int64_t)1 << 40) || c->ld_grad > ((int64_t)1 << 40)) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
 
