@@ -51,3 +51,44 @@ def test_edge_elements_of_masked_rows(dtype, V, bad, moe_lib, cuda_device):
     for got, want in ((lp, clean[0]), (own, clean[1]), (dz, clean[3])):
         assert torch.equal(got[rest], want[rest])
     moe_lib.get_error()
+
+
+@pytest.mark.parametrize("V", [2040, 40003])
+def test_fp32_gradient_keeps_its_bits(V, moe_lib, cuda_device):
+    """Probabilities of near logits, as quotients of two elements of one gradient row (which the row's sum
+    and the token's factor do not enter). One is exp(z - top): a product with a rounded constant (2 of
+    2^-24 of an exponent below 0.15), two fast exponentials (2^-22 each), two products, and as much less
+    the exponent for the top: under 2^-21 + 8 * 2^-24 of itself."""
+    g = torch.Generator().manual_seed(0)
+    T = 6
+    z = -torch.rand(T, V, generator=g) * 0.14
+    z[:, 7] = 0.0
+    z[:, 5] = 1.0e-3                                  # the target: the row's maximum, and no part of the quotients
+    z = z.cuda()
+    target = torch.full((T,), 5, dtype=torch.int32, device="cuda")
+    dz = torch.empty_like(z)
+    moe_lib.policy_loss(moe_lib.make_policy_config(T, V, "f32"), z, target, torch.ones(T, device="cuda"), None, None, None,
+                        None, None, dz, None)
+    got = dz.double() / dz[:, 7:8].double()
+    off = (got / z.double().exp() - 1).abs()
+    off[:, 5] = 0
+    assert float(off.max()) <= 2.0 ** -21 + 8 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gradient_of_tiny_probabilities(dtype, moe_lib, cuda_device):
+    """Probabilities from one down to below the least fp32 number, on a factor of 2^40: each element is
+    right to its type's resolution, the normal range's end included."""
+    V = 4 * 1001
+    z = torch.linspace(0, -160, V).repeat(2, 1).to(DT[dtype]).cuda()
+    target = torch.zeros(2, dtype=torch.int32, device="cuda")
+    dz = torch.empty_like(z)
+    adv = torch.tensor([1.0, 2.0 ** 40], device="cuda")
+    moe_lib.policy_loss(moe_lib.make_policy_config(2, V, dtype), z, target, adv, None, None, None, None, None, dz, None)
+    p = torch.softmax(z.double(), 1)
+    p[:, 0] -= 1
+    ref = p * adv.double()[:, None]
+    half, least = (2.0 ** -8, 2.0 ** -134) if dtype == "bf16" else (2.0 ** -24, 2.0 ** -150)
+    # the exponent, up to 231, has two roundings of 2^-24; the row's sum (over 256 threads and more) and the rest 2^-20
+    tol = ref.abs() * (half * 1.01 + 2 * 231 * 2.0 ** -24 + 2.0 ** -20) + 2 * least + 2.0 ** -148
+    assert ((dz.double() - ref).abs() <= tol).all()

@@ -155,37 +155,59 @@ __device__ __forceinline__ float token_terms(const PolicyArgs& a, const Token& r
     return r.w * slope * a.inv_tau;
 }
 
-// What the gradient of one row needs: dz = c 1[v = target] - q 2^(k (z - top)).
+// What the gradient of one row needs: dz = c 1[v = target] - q 2^(k (z - top)). The fast exponential
+// flushes results below 2^-126, which a gradient element times q need not be.
+//   bf16: 2^(x + lift), with q carrying 2^-lift. With lift = 64 what is flushed is below the smallest
+//     fp32 number once multiplied by q. An exponent near 0 loses six bits to the sum: probabilities
+//     are off by up to 2e-6, a thousandth of what the rounding to bf16 then adds.
+//   fp32: the square of 2^(x / 2), multiplied into q one factor at a time; halving is exact, and what
+//     the root flushes is below 2^-252 in the square. One multiplication more a pair, which bf16 rows
+//     do not hide (8192 x 131072: 619 us against 606) and fp32 rows do (4096 x 131072: 578 and 578).
+template <typename T>
 struct RowGrad {
-    float c, top, q;
-    float lift;        // see grad_vec
-    __device__ __forceinline__ void set_q(float x) {
-        lift = fabsf(x) > 9.0949470e-13f ? 64.f : 0.f;             // 2^-40
-        q = lift != 0.f ? x * 5.4210109e-20f : x;                   // 2^-64
+    static constexpr bool kLift = sizeof(T) == 2;
+    float c, top, q, k, lift;
+    __device__ __forceinline__ RowGrad(float c_, MaxSum row, float k_) : c(c_), top(row.m), q(c_ / row.s), k(k_), lift(0.f) {
+        if constexpr (kLift) {
+            lift = fabsf(q) > 9.0949470e-13f ? 64.f : 0.f;              // 2^-40
+            q = lift != 0.f ? q * 5.4210109e-20f : q;                    // 2^-64
+        } else {
+            k *= 0.5f;
+        }
     }
 };
 
-// Gradient of one vector. Exponentials are computed as 2^(x + lift) with q carrying 2^-lift: the
-// fast exponential flushes results below 2^-126, and with lift = 64 what it flushes is below
-// the smallest fp32 number once multiplied by q.
+// Gradient of one vector.
 template <typename T>
-__device__ __forceinline__ uint4 grad_vec(const uint4& u, const RowGrad& g, float k) {
+__device__ __forceinline__ uint4 grad_vec(const uint4& u, const RowGrad<T>& g) {
     uint64_t p[Pairs<T>::N];
     to_pairs<T>(u, p);
-    const uint64_t minus = splat2(-g.top), kk = splat2(k), lift = splat2(g.lift), q = splat2(-g.q);
+    const uint64_t minus = splat2(-g.top), k = splat2(g.k), lift = splat2(g.lift), q = splat2(-g.q);
 #pragma unroll
     for (int i = 0; i < Pairs<T>::N; ++i) {
         float x0, x1;
-        upk2(fma2(add2(p[i], minus), kk, lift), x0, x1);
-        p[i] = mul2(pk2(ex2_approx(x0), ex2_approx(x1)), q);
+        const uint64_t d = add2(p[i], minus);
+        if constexpr (RowGrad<T>::kLift) {
+            upk2(fma2(d, k, lift), x0, x1);
+            p[i] = mul2(pk2(ex2_approx(x0), ex2_approx(x1)), q);
+        } else {
+            upk2(mul2(d, k), x0, x1);
+            const uint64_t e = pk2(ex2_approx(x0), ex2_approx(x1));
+            p[i] = mul2(mul2(e, q), e);
+        }
     }
     return from_pairs<T>(p);
 }
 
 template <typename T>
-__device__ __forceinline__ T grad_one(float x, const RowGrad& g, float k, bool hot) {
-    const float e = ex2_approx(fmaf(x - g.top, k, g.lift));
-    return Elem<T>::from_f(fmaf(-g.q, e, hot ? g.c : 0.f));
+__device__ __forceinline__ T grad_one(float x, const RowGrad<T>& g, bool hot) {
+    const float c = hot ? g.c : 0.f;
+    if constexpr (RowGrad<T>::kLift) {
+        return Elem<T>::from_f(fmaf(-g.q, ex2_approx(fmaf(x - g.top, g.k, g.lift)), c));
+    } else {
+        const float e = ex2_approx((x - g.top) * g.k);
+        return Elem<T>::from_f(fmaf(-g.q * e, e, c));
+    }
 }
 
 // Phase wait whose acquire covers what the other CTAs of the cluster have written.
@@ -501,10 +523,7 @@ policy_ring_kernel(PolicyArgs a, const T* logits, T* dlogits, int reuse) {
             }
             send(acc, turn);
             acc = receive(turn++);
-            RowGrad g;
-            g.c = token_terms(a, x, rank == 0 && tid == 0, acc);
-            g.top = acc.m;
-            g.set_q(g.c / acc.s);
+            const RowGrad<T> g(token_terms(a, x, rank == 0 && tid == 0, acc), acc, k);
             // ---- gradient
             const int hot = r.target - s.head - s.v0 * N;    // the target's place in this CTA's vectors
             const int hot_vec = hot >= 0 && hot < s.nv * N ? hot / N : -1;
@@ -516,25 +535,25 @@ policy_ring_kernel(PolicyArgs a, const T* logits, T* dlogits, int reuse) {
                 uint4* o = out + i0 + tid;
                 if (wide && left + lane > 31 + (kEach - 1) * kThreads) {
 #pragma unroll
-                    for (int h = 0; h < kEach; ++h) o[h * kThreads] = grad_vec<T>(v[h * kThreads], g, k);
+                    for (int h = 0; h < kEach; ++h) o[h * kThreads] = grad_vec<T>(v[h * kThreads], g);
                 } else if (wide) {
 #pragma unroll
                     for (int h = 0; h < kEach; ++h)
-                        if (h * kThreads < left) o[h * kThreads] = grad_vec<T>(v[h * kThreads], g, k);
+                        if (h * kThreads < left) o[h * kThreads] = grad_vec<T>(v[h * kThreads], g);
                 } else {
 #pragma unroll 1
                     for (int j = 0; j < left; j += kThreads) {
-                        put_elements<T>(dz + s.head + (int64_t)(s.v0 + i0 + tid + j) * N, grad_vec<T>(v[j], g, k));
+                        put_elements<T>(dz + s.head + (int64_t)(s.v0 + i0 + tid + j) * N, grad_vec<T>(v[j], g));
                     }
                 }
                 // the target's element again, by the thread that has just written its vector
                 const int hit = hot_vec - i0 - tid;
                 if (hot_vec >= 0 && hit >= 0 && hit < left && hit % kThreads == 0)
-                    dz[r.target] = grad_one<T>(x.zt, g, k, true);
+                    dz[r.target] = grad_one<T>(x.zt, g, true);
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&empty[at.slot]);
             }
-            if (tid < s.rest) dz[odd] = grad_one<T>(lone, g, k, odd == r.target);
+            if (tid < s.rest) dz[odd] = grad_one<T>(lone, g, odd == r.target);
         }
         if (reuse == kFree && turn && ok) finish(before, receive(turn - 1));
     }
@@ -626,23 +645,20 @@ __global__ void __launch_bounds__(short_block(G), 1024 / short_block(G)) policy_
         acc = warp_join(lane < G / 32 ? part[lane] : MaxSum{-INFINITY, 0.f}, k);
     }
     __syncwarp();
-    RowGrad g;
-    g.c = token_terms(a, x, tid == 0, acc);
+    const RowGrad<T> g(token_terms(a, x, tid == 0, acc), acc, k);
     if (!dz) return;
-    g.top = acc.m;
-    g.set_q(g.c / acc.s);
 #pragma unroll
     for (int h = 0; h < kHeld; ++h) {
         const int i = tid + h * G;
         if (i >= s.nvec) break;
-        const uint4 o = grad_vec<T>(u[h], g, k);
+        const uint4 o = grad_vec<T>(u[h], g);
         if (wide) out[i] = o;
         else put_elements<T>(dz + s.head + i * N, o);
     }
     // the target's element again, by the thread that has just written its vector
     const int hot = target - s.head, hot_vec = hot >= 0 && hot < s.nvec * N ? hot / N : -1;
-    if (hot_vec >= 0 && hot_vec % G == tid) dz[target] = grad_one<T>(x.zt, g, k, true);
-    if (tid < s.rest) dz[odd] = grad_one<T>(lone, g, k, odd == target);
+    if (hot_vec >= 0 && hot_vec % G == tid) dz[target] = grad_one<T>(x.zt, g, true);
+    if (tid < s.rest) dz[odd] = grad_one<T>(lone, g, odd == target);
 }
 
 // loss = sum of the tokens' terms, one block, in a fixed order.
