@@ -332,7 +332,11 @@ MOE_API moe_status_t moe_embed_backward(const moe_embed_config_t* cfg, const int
  * logits itself (then ld_grad = ld), any other overlap is not allowed. target [T] int32;
  * advantage, old_logp, ref_logp, weight, logp [T] fp32; loss [1] fp32. One reading of the
  * logits gives the loss and the gradient.
- *   old_logp null: on-policy, r = 1 with its gradient. ref_logp: needed iff kl_weight != 0.
+ *   old_logp null: on-policy, r = 1 with its gradient. Where old_logp[t] is the lp that this call
+ *   computes, bit for bit, r is exactly 1 too; otherwise lp enters r with more than its 24 bits.
+ *   moe_token_logp gives those bits for the same logits, T, V, ld, dtype and temperature; with
+ *   another T or ld a row may be added up in another order, and lp differs by its rounding.
+ *   ref_logp: needed iff kl_weight != 0.
  *   weight null: 1 for each token. logp, loss, dlogits: each may be null (not wanted).
  *   ws (moe_policy_workspace_bytes): needed when loss is not null.
  * A token with weight 0 or a negative target is left out: its logits are not read, whatever

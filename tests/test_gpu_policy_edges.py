@@ -92,3 +92,40 @@ def test_gradient_of_tiny_probabilities(dtype, moe_lib, cuda_device):
     # the exponent, up to 231, has two roundings of 2^-24; the row's sum (over 256 threads and more) and the rest 2^-20
     tol = ref.abs() * (half * 1.01 + 2 * 231 * 2.0 ** -24 + 2.0 ** -20) + 2 * least + 2.0 ** -148
     assert ((dz.double() - ref).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,V", [(64, 300), (64, 5003), (300, 20001), (40, 131072), (5, 600001)])
+def test_fresh_log_probabilities_give_a_ratio_of_one(T, V, dtype, moe_lib, cuda_device):
+    """old_logp kept from token_logp of the same rows: the ratio is exactly one, so that with no room to
+    clip (clip_low = clip_high = 0) no token loses its gradient, and everything is as on-policy."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    z = (torch.randn(T, V, generator=g, device="cuda") * 2.5).to(DT[dtype])
+    target = torch.randint(0, V, (T,), generator=g, device="cuda", dtype=torch.int32)
+    adv = torch.randn(T, generator=g, device="cuda")
+    cfg = moe_lib.make_policy_config(T, V, dtype, temperature=0.7, clip_low=0.0, clip_high=0.0)
+    ws = torch.empty(moe_lib.policy_workspace_bytes(cfg), dtype=torch.uint8, device="cuda")
+    old = torch.empty(T, device="cuda")
+    moe_lib.token_logp(cfg, z, target, old)
+    got = []
+    for o in (old, None):
+        loss, dz = torch.empty(1, device="cuda"), torch.empty_like(z)
+        moe_lib.policy_loss(cfg, z, target, adv, o, None, None, None, loss, dz, ws)
+        got.append((loss, dz))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    assert (got[0][1][torch.arange(T, device="cuda"), target.long()] != 0).all()
+
+
+def test_log_probabilities_of_another_batch_size(moe_lib, cuda_device):
+    """The same row in a smaller batch may go over more blocks and be added up in another order: equal to
+    rounding. A sum of 131072 exponentials over 256 threads and more: 576 roundings of 2^-24, the rest
+    2^-22 (4 + ln V) and half a step of a number below 16."""
+    V = 131072
+    z = torch.randn(600, V, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").bfloat16()
+    target = torch.arange(600, device="cuda", dtype=torch.int32)
+    one = torch.empty(600, device="cuda")
+    moe_lib.token_logp(moe_lib.make_policy_config(600, V), z, target, one)
+    for T in (1, 7, 150, 599):
+        lp = torch.empty(T, device="cuda")
+        moe_lib.token_logp(moe_lib.make_policy_config(T, V), z[:T], target[:T], lp)
+        assert float((lp - one[:T]).abs().max()) <= 576 * 2.0 ** -24 + 16 * 2.0 ** -22 + 2.0 ** -21

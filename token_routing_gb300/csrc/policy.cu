@@ -141,7 +141,9 @@ __device__ __forceinline__ float token_terms(const PolicyArgs& a, const Token& r
     }
     if (a.logp && put) a.logp[r.t] = lp;
     if (!a.advantage) return 0.f;
-    const float ratio = a.old_logp ? expf(lp - r.old + lp_low) : 1.f;
+    // an old log-probability that is this one, rounded as this one is, stands for the same policy: its
+    // low part is not known, and the ratio is one
+    const float ratio = !a.old_logp || lp == r.old ? 1.f : expf(lp - r.old + lp_low);
     const float un = ratio * r.adv, cl = fminf(fmaxf(ratio, 1.f - a.clip_low), 1.f + a.clip_high) * r.adv;
     float l = -fminf(un, cl);
     float slope = un <= cl ? -un : 0.f;
