@@ -1,6 +1,6 @@
 """Thin torch-facing binding of the training-step calls around the layer: token embedding,
-policy loss and AdamW (the C calls of the same names). As in the layer's binding, the functions
-check what a tensor's type and shape say, and marshal pointers; nothing is computed here.
+policy loss and AdamW (the C calls of the same names). The functions check what a tensor's type,
+shape and device say, and marshal pointers; nothing is computed here.
 """
 import ctypes
 import math
@@ -15,12 +15,25 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream(stream, t):
+def _stream(stream, gpu):
     """The stream's handle. The current one is asked for as a number: a torch.cuda.Stream object for
     each call would take longer (3 us) than the call itself."""
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(t.device.index) if t.is_cuda else 0
+    return torch._C._cuda_getCurrentRawStream(gpu)
+
+
+def _one_gpu(first, *rest):
+    """The GPU that the tensors are on. Refuses others: the kernels would follow a host address."""
+    gpu = first.get_device()
+    if gpu >= 0:
+        for t in rest:
+            if t is not None and t.get_device() != gpu:
+                break
+        else:
+            return gpu
+    on = sorted({t.get_device() for t in (first, *rest) if t is not None})
+    raise ValueError(f"tensors on devices {on} (-1: the host): all have to be on one GPU")
 
 
 def _want(what, t, dtype, shape, optional=False):
@@ -57,7 +70,8 @@ def embed(cfg, ids, W, y, stream=None):
     _want("ids", ids, torch.int32, (cfg.T,))
     _want("W", W, dt, (cfg.V, cfg.d))
     _want("y", y, dt, (cfg.T, cfg.d))
-    L.check("moe_embed", L.load().moe_embed(ctypes.byref(cfg), _ptr(ids), _ptr(W), _ptr(y), _stream(stream, W)))
+    gpu = _one_gpu(W, ids, y)
+    L.check("moe_embed", L.load().moe_embed(ctypes.byref(cfg), _ptr(ids), _ptr(W), _ptr(y), _stream(stream, gpu)))
 
 
 def embed_workspace_bytes(cfg):
@@ -70,8 +84,9 @@ def embed_backward(cfg, ids, dy, dW, ws, stream=None):
     _want("dy", dy, _TORCH[cfg.dtype], (cfg.T, cfg.d))
     _want("dW", dW, _TORCH[cfg.grad_dtype], (cfg.V, cfg.d))
     _room("ws", ws, embed_workspace_bytes(cfg))
+    gpu = _one_gpu(dW, ids, dy, ws)
     L.check("moe_embed_backward", L.load().moe_embed_backward(
-        ctypes.byref(cfg), _ptr(ids), _ptr(dy), _ptr(dW), _ptr(ws), _stream(stream, dW)))
+        ctypes.byref(cfg), _ptr(ids), _ptr(dy), _ptr(dW), _ptr(ws), _stream(stream, gpu)))
 
 
 # ---------------------------------------------------------------- policy loss
@@ -114,9 +129,10 @@ def policy_loss(cfg, logits, target, advantage, old_logp, ref_logp, weight, logp
     _want("loss", loss, f32, (1,), True)
     if loss is not None:
         _room("ws", ws, policy_workspace_bytes(cfg))
+    gpu = _one_gpu(logits, target, advantage, old_logp, ref_logp, weight, logp, loss, dlogits, ws)
     L.check("moe_policy_loss", L.load().moe_policy_loss(
         ctypes.byref(cfg), _ptr(logits), _ptr(target), _ptr(advantage), _ptr(old_logp), _ptr(ref_logp), _ptr(weight), _ptr(logp),
-        _ptr(loss), _ptr(dlogits), _ptr(ws), _stream(stream, logits)))
+        _ptr(loss), _ptr(dlogits), _ptr(ws), _stream(stream, gpu)))
 
 
 def token_logp(cfg, logits, target, logp, stream=None):
@@ -124,12 +140,14 @@ def token_logp(cfg, logits, target, logp, stream=None):
     _rows("logits", logits, cfg, cfg.ld)
     _want("target", target, torch.int32, (cfg.T,))
     _want("logp", logp, torch.float32, (cfg.T,))
+    gpu = _one_gpu(logits, target, logp)
     L.check("moe_token_logp", L.load().moe_token_logp(ctypes.byref(cfg), _ptr(logits), _ptr(target), _ptr(logp),
-                                                           _stream(stream, logits)))
+                                                           _stream(stream, gpu)))
 
 
 # ---------------------------------------------------------------- AdamW
 
+_ARRAYS = ("p", "g", "master", "m", "v", "m_scale", "v_scale")
 _KIND = {torch.float32: L.MOE_F32, torch.bfloat16: L.MOE_BF16}
 
 
@@ -159,7 +177,7 @@ class AdamW:
         self.tensors = [self._bind(dict(t), weight_decay, bits) for t in tensors]
         self.table = (L.MoeAdamwTensor * max(1, len(self.tensors)))()
         for e, t in zip(self.table, self.tensors):
-            for k in ("p", "g", "master", "m", "v", "m_scale", "v_scale"):
+            for k in _ARRAYS:
                 setattr(e, k, None if t[k] is None else t[k].data_ptr())
             e.n, e.dtype, e.grad_dtype = t["p"].numel(), _KIND[t["p"].dtype], _KIND[t["g"].dtype]
             e.weight_decay = t["weight_decay"]
@@ -169,6 +187,7 @@ class AdamW:
             at[0], at[1] = (-math.expm1(step * math.log(b)) if b else 1.0 for b in (beta1, beta2))
             at.view(torch.int64)[2] = int(step)
         self.state = at.to(device)
+        self.placed = False             # whether the bound arrays have been seen to be on one GPU
 
     @staticmethod
     def _bind(t, weight_decay, bits):
@@ -204,8 +223,12 @@ class AdamW:
         for what, t in (("lr", lr), ("grad_scale", grad_scale)):
             if t is not None and (t.dtype != torch.float32 or t.numel() != 1):
                 raise ValueError(f"{what}: one fp32 element")
+        if not self.placed:
+            _one_gpu(self.state, *(t[k] for t in self.tensors for k in _ARRAYS))
+            self.placed = True
+        gpu = _one_gpu(self.state, lr, grad_scale)
         L.check("moe_adamw", L.load().moe_adamw(ctypes.byref(self.cfg), self.table, len(self.tensors), _ptr(lr),
-                                                _ptr(grad_scale), _ptr(self.state), _stream(stream, self.state)))
+                                                _ptr(grad_scale), _ptr(self.state), _stream(stream, gpu)))
 
     def steps_done(self):
         """Steps that the device has counted (synchronises)."""
