@@ -129,3 +129,24 @@ def test_log_probabilities_of_another_batch_size(moe_lib, cuda_device):
         lp = torch.empty(T, device="cuda")
         moe_lib.token_logp(moe_lib.make_policy_config(T, V), z[:T], target[:T], lp)
         assert float((lp - one[:T]).abs().max()) <= 576 * 2.0 ** -24 + 16 * 2.0 ** -22 + 2.0 ** -21
+
+
+def test_low_part_of_a_log_probability_near_the_maximum(moe_lib, cuda_device):
+    """A target a little below the maximum of a long, flat row: (z - max) is small beside ln(sum), and the
+    rounding of their difference has to be kept all the same. The row's sum is a whole number but for
+    the target's part (2^-24 of itself), the ratio's exponential is off by 2^-22, the gradient by three
+    roundings of 2^-24: 2^-21 in all; a low part lost to the larger term's rounding is 2^-20."""
+    V = 2 ** 24 + 2 ** 20
+    low = torch.tensor([5343222, 5447694, 5088830, 1473506, 4542106, 674442, 2514166, 3382610], device="cuda") * 2.0 ** -21
+    T = len(low)
+    z = torch.zeros(T, V, device="cuda")
+    target = torch.arange(T, device="cuda", dtype=torch.int32) * 999999
+    z[torch.arange(T, device="cuda"), target.long()] = -low
+    lp = -low.double() - torch.log(V - 1 + torch.exp(-low.double()))
+    old = lp.float() + 2.0 ** -10
+    want = torch.exp(lp - old.double())
+    dz = torch.empty_like(z)
+    cfg = moe_lib.make_policy_config(T, V, "f32", clip_low=1.0, clip_high=9.0)
+    moe_lib.policy_loss(cfg, z, target, torch.full((T,), -1.0, device="cuda"), old, None, None, None, None, dz, None)
+    got = dz[torch.arange(T, device="cuda"), target.long()].double() / (1 - lp.exp())
+    assert float((got / want - 1).abs().max()) <= 2.0 ** -21

@@ -120,18 +120,26 @@ struct Token {
     float w, zt, adv, old, ref;
 };
 
+// a + b, and what its rounding lost: exact whichever is the larger (Knuth's two-sum).
+__device__ __forceinline__ float exact_sum(float a, float b, float& lost) {
+    const float s = a + b, of_b = s - a;
+    lost = (a - (s - of_b)) + (b - of_b);
+    return s;
+}
+
 // What one token adds: its log-probability and its term of the loss (written if `put`), and the
 // factor c of its gradient row c (1[v = target] - p_v).
 __device__ __forceinline__ float token_terms(const PolicyArgs& a, const Token& r, bool put, MaxSum row) {
     // lp = (z - max) / tau - ln(sum), with the sum as 2^e f: the quotient's and the partial sums'
     // roundings are kept in `low`, so that the ratios to other policies, which differ by a little
-    // from numbers of ten and more, do not lose them.
+    // from numbers of ten and more, do not lose them. e times the upper part of ln 2 is exact.
     const float d = r.zt - row.m, q = d * a.inv_tau, q_low = fmaf(-q, a.tau, d) * a.inv_tau;
     const int e = (int)(__float_as_uint(row.s) >> 23) - 127;
     const float f = __uint_as_float((__float_as_uint(row.s) & 0x7fffffu) | 0x3f800000u);
-    const float hi = fmaf(-(float)e, kLn2High, q), hi_low = fmaf(-(float)e, kLn2High, q - hi);
+    float hi_low, sum_low;
+    const float hi = exact_sum(q, -(float)e * kLn2High, hi_low);
     const float ln_f = fmaf((float)e, kLn2Low, logf(f));
-    const float sum = hi - ln_f, low = (hi - sum) - ln_f + hi_low + q_low;
+    const float sum = exact_sum(hi, -ln_f, sum_low), low = sum_low + hi_low + q_low;
     float lp = sum, lp_low = low;
     if (!(fabsf(q) <= 3.4028235e38f) || !(row.s >= 1.f && row.s <= 3.4028235e38f)) {
         // a target of -inf has the log-probability -inf; a row of -inf alone, or with a NaN or
