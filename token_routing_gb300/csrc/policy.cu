@@ -422,6 +422,11 @@ policy_ring_kernel(PolicyArgs a, const T* logits, T* dlogits, int reuse) {
             rows[to.slot] = Row{-1, 0, 0.f};
             tc::mbar_arrive(&given[to.slot]);
         }
+        // No copy is in flight when the CTA leaves, also where a wait ran out and nobody takes the
+        // pieces any more: lane i waits for the last copy into slot i.
+        __syncwarp();
+        if (lane < kSlots && (lane < at.slot || at.again))
+            tc::mbar_wait(&full[lane], lane < at.slot ? at.phase : at.phase ^ 1, a.err);
     } else {
         const float k = a.inv_tau * kLog2e;
         Ring<kSlots> at;
@@ -565,7 +570,12 @@ policy_ring_kernel(PolicyArgs a, const T* logits, T* dlogits, int reuse) {
             }
             if (tid < s.rest) dz[odd] = grad_one<T>(lone, g, odd == r.target);
         }
-        if (reuse == kFree && turn && ok) finish(before, receive(turn - 1));
+        // (also where a wait ran out: whoever has sent a row's pairs waits for all of that row's before it
+        // leaves, so that none is under way by then)
+        if (reuse == kFree && turn) {
+            const MaxSum last = receive(turn - 1);
+            if (ok) finish(before, last);
+        }
     }
     // no CTA leaves while another of its cluster may still write to it
     __syncwarp();
