@@ -63,7 +63,8 @@ def check_held(codes, scale, y, e, d, root, even):
     assert (np.sign(codes)[sure & (codes != 0)] == np.sign(u)[sure & (codes != 0)]).all()
 
 
-def check_step(opt, rounding="even"):
+def check_step(opt, rounding="even", every=1):
+    """One step, checked on every so many chunks of a tensor and on its last."""
     cfg = opt.cfg
     b1, b2, eps, lr = cfg.beta1, cfg.beta2, np.float64(np.float32(cfg.eps)), cfg.lr
     before = [{k: None if t[k] is None else t[k].clone() for k in ("p", "master", "m", "v", "m_scale", "v_scale")}
@@ -77,6 +78,8 @@ def check_step(opt, rounding="even"):
             assert torch.equal(t["p"], t["master"].to(t["p"].dtype))
         for a in range(0, n, CHUNK):
             b = min(n, a + CHUNK)
+            if a // CHUNK % every and b < n:
+                continue
             x, grad, (m, v) = part(old, key, a, b), part(t, "g", a, b), moments(old, a, b)
             nx, nm, nv, up = O.adamw(x, grad, m, v, step, lr, b1, b2, eps, np.float64(np.float32(t["weight_decay"])))
             tm = (6 * U) * (b1 * np.abs(m) + (1 - b1) * np.abs(grad))
@@ -124,7 +127,8 @@ def test_rounding_of_resumed_states(moe_lib, cuda_device):
 
 
 def test_rounding_leaves_wide_states_alone(moe_lib, cuda_device):
-    a, b = (moe_lib.AdamW(tensors(SHORT, torch.Generator(device="cuda").manual_seed(2)), rounding=r) for r in ("even", "weyl"))
+    a, b = (moe_lib.AdamW(tensors(SHORT, torch.Generator(device="cuda").manual_seed(2)), rounding=r)
+            for r in ("even", "weyl"))
     a.step()
     b.step()
     for x, y in zip(a.tensors, b.tensors):
@@ -146,3 +150,45 @@ def test_weyl_rounding_of_values_that_are_not_finite(moe_lib, cuda_device):
     for k in ("p", "m", "v"):
         x, y = oa.tensors[0][k].float(), ob.tensors[0][k].float()
         assert torch.equal(x[rest], y[rest]) and not torch.isfinite(y[bad]).any()
+
+
+KINDS = [(p, g, master) for p in ("f32", "bf16") for g in ("f32", "bf16") for master in (False, True)]
+
+
+@pytest.mark.parametrize("bits,rounding", [(32, "even"), (8, "even"), (8, "weyl")])
+@pytest.mark.parametrize("n", [170_001, 410_777, 1_000_003])
+def test_runs_of_many_units(n, bits, rounding, moe_lib, cuda_device):
+    """Every kind of tensor in runs of several units a warp: the next unit's loads pass under this one's
+    arithmetic, the scales go out together, and the tensor's end cuts a run and a unit short."""
+    g = torch.Generator(device="cuda").manual_seed(n)
+    opt = moe_lib.AdamW(tensors([(n + 259 * i, *kind) for i, kind in enumerate(KINDS)], g), lr=1e-2, bits=bits,
+                        rounding=rounding)
+    for _ in range(2):
+        check_step(opt, rounding)
+        for t in opt.tensors:
+            t["g"].mul_(torch.randn(t["g"].numel(), generator=g, device="cuda").to(t["g"].dtype))
+
+
+@pytest.mark.parametrize("bits,rounding,n", [(32, "even", 24_300_001), (8, "even", 55_000_001), (8, "weyl", 55_000_001)])
+def test_longest_runs(bits, rounding, n, moe_lib, cuda_device):
+    """The longest runs (16 eights of units, 32 with 8-bit states), over a thousand of them in one launch: the
+    step is then counted by a launch of its own, once a call."""
+    g = torch.Generator(device="cuda").manual_seed(bits)
+    opt = moe_lib.AdamW(tensors([(n, "bf16", "bf16", True), (n * 3 // 5, "bf16", "f32", False)], g), lr=1e-2,
+                        bits=bits, rounding=rounding)
+    for _ in range(2):
+        check_step(opt, rounding, every=7)
+
+
+def test_long_runs_beside_short_ones(moe_lib, cuda_device):
+    """Both widths of states in one call, tensors from one element to millions."""
+    g = torch.Generator(device="cuda").manual_seed(11)
+    kinds = [(3_000_001, "bf16", "bf16", True), (1, "f32", "f32", False), (2_000_037, "f32", "bf16", False),
+             (65_536 * 8, "bf16", "f32", True), (300, "bf16", "bf16", False), (16_384 * 2, "f32", "f32", False)]
+    ts = tensors(kinds + kinds, g)
+    for t in ts[:len(kinds)]:
+        codes, scales = torch.zeros(t["p"].numel(), device="cuda"), torch.zeros(-(-t["p"].numel() // O.BLOCK), device="cuda")
+        t.update(m=codes.to(torch.float8_e4m3fn), v=codes.to(torch.float8_e4m3fn), m_scale=scales, v_scale=scales.clone())
+    opt = moe_lib.AdamW(ts, lr=3e-3)
+    for _ in range(2):
+        check_step(opt)
