@@ -258,8 +258,9 @@ __device__ __forceinline__ void advance8(const Step& s, const uint64_t (&g)[4], 
 template <bool kWeyl>
 __device__ __forceinline__ void hold(const uint64_t (&m)[4], const uint64_t (&v)[4], const uint64_t (&root)[4],
                                      uint32_t h0, uint2& cm, uint2& cv, float& sm, float& sv) {
-    // The Weyl word of element and step, or one hash of it: its top bits dither m, those of an odd
-    // multiple v.
+    // The Weyl word of element and step (2^32 over the golden ratio and over its square), or one hash
+    // of it, whose top bits dither m and those of an odd multiple v. The hash is a shift and the two
+    // multipliers of Appleby's 32-bit finaliser (MurmurHash3).
     uint32_t hash[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -359,7 +360,7 @@ __device__ __forceinline__ void run_units(const TensorArg& t, const Step& s, int
     }
     if constexpr (kNarrow) {
         // The scales go out by whole sectors: four bytes at a time from one warp after the other made
-        // the memory fill and rewrite sectors (1.1G weights: 3240 - 3820 us against 2840).
+        // the memory fill and rewrite sectors (1.1G weights, at the time: 3240 - 3820 us against 2740).
         __syncthreads();
         for (int u = threadIdx.x; u < min(count, run * 8); u += kThreads) {
             ms[u] = scales[0][u];
@@ -457,8 +458,10 @@ __device__ __noinline__ void last_unit(const TensorArg& t, const Step& s, int64_
 // vote over all of them.
 // fp32 states, 156M weights with masters: 700 us, 6690 GB/s (99 %); 114 registers and two blocks to
 // an SM, against 720 us at three and 800 at four, whose loads are cut apart. 8-bit states, 1.1G
-// weights: 2800 us, 6350 GB/s (94 %), four fifths of the issue slots taken: the next unit's loads
+// weights: 2800 us, 6350 GB/s (95 %), four fifths of the issue slots taken: the next unit's loads
 // pass under the arithmetic of this one (without: 3400), and blocks start seldom (runs of 8: 3000).
+// The Weyl rule is less arithmetic: 2705 us, 6580 GB/s (98 %), 70 % of the issue slots; 112M bf16
+// weights without masters, bound by issue, 242 us against 285.
 template <bool kNarrow, bool kWeyl>
 __global__ void __launch_bounds__(kThreads, kResident[kNarrow]) adamw_kernel(const __grid_constant__ AdamArgs a) {
     pdl_wait();

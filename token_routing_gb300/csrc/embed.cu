@@ -137,12 +137,14 @@ cudaError_t launch_embed(const moe_embed_config_t& c, const int32_t* ids, const 
 
 // ---------------------------------------------------------------- gradient: sort by token
 // Stable radix sort of (id, token) pairs, least digit first, by ordinary launches: a histogram of
-// every chunk of kChunk pairs for the first digit, then for each digit the chunks' ranks and the
-// scatter, which also counts the next digit's histogram by integer atomics. Left-out tokens
+// every chunk of kChunk pairs for the first digit, then for each digit (with many chunks) a scan of
+// the histogram, and the chunks' ranks and the scatter, which also counts the next digit's histogram
+// by integer atomics. Left-out tokens
 // (padding, ids out of range) take the key V and end up behind all others.
-// Bound by latency: two digits take three launches of 2, 4 and 4 us at up to 4096 tokens, 4, 6 and
-// 6 at 32768. One block for all of it takes 4 us at 777 tokens, 6 at 2048, 10 at 4096 and 45 at
-// 16384 (one SM then ranks and scatters everything): it sorts batches of up to 4096.
+// Bound by latency: two digits take three launches of 2, 4 and 4 us at 4096 tokens; at 32768 they
+// take five, the scans 5 and the scatters 6 us each (by themselves, caches cold). One block for all
+// of it takes 4 us at 777 tokens, 6 at 2048, 10 at 4096 and 45 at 16384 (one SM then ranks and
+// scatters everything): it sorts batches of up to 4096.
 // The sort needs few of the SMs: the other blocks of its launches zero the first rows of a dW that
 // is overwritten, whether or not they get a sum later. (Where dW is added to, bringing dy into the
 // L2 cache meanwhile gained nothing: the sums wait for latencies, not for bytes.)
@@ -164,7 +166,9 @@ constexpr int kPerLane = kChunk / 256;
 constexpr int kMaxBits = 9;          // bits of a digit
 constexpr int kMaxBins = 1 << kMaxBits;
 constexpr int kMaxPasses = 4;        // 31 bits of keys
-// Bytes zeroed beside one launch of the sort: about what the memory takes in its time.
+// Bytes zeroed beside one launch of the sort: about what the memory takes in its time at 16384 to
+// 32768 tokens. A smaller batch's launches are shorter, and the zeros then outlast them; all of the
+// bytes have to be written by the end in any case, by these blocks or by the last launch's.
 constexpr int64_t kZeroOne = 24 << 20, kZeroHist = 32 << 20, kZeroScatter = 44 << 20;
 
 struct SortArgs {
@@ -469,8 +473,9 @@ __global__ void __launch_bounds__(kOneThreads) embed_sort_kernel(SortArgs a, int
 // run it ends with and that begins in it) and an entry in a list, and embed_join_kernel adds them
 // in group order. Every row of dW has one writer and a fixed order of sums.
 // Bound by memory (dy once, the touched rows of dW) and by the latency of gathered rows: 32768 x
-// 2048 bf16 into fp32 rows that are added to, 57 us of 81 in all, 274 MB at 4800 GB/s. Groups of 8
-// leave twice the partial rows (88 us in all), groups of 32 half the blocks (86).
+// 2048 bf16 into fp32 rows that are added to, 51 us by themselves of 79 in all, 272 MB at 5300 GB/s,
+// 54 registers and half of the warps resident. Groups of 8 leave twice the partial rows (88 us in
+// all against 81 at the time), groups of 32 half the blocks (86).
 constexpr int kGroup = 16;
 constexpr int kLong = 16;        // a run over more groups than this is joined by a whole block
 
@@ -607,7 +612,7 @@ __device__ __forceinline__ void join_row(const SumArgs& a, G* dW, uint32_t key, 
 
 // The other blocks zero the rows that get no sum and that the sort's launches have not zeroed: the
 // joins' chain of latencies (8 us) passes beside them. The whole gradient of 16384 x 1024 bf16 into
-// 131072 rows: 61 us, 4950 GB/s of needed traffic (73 %); zeros after the joins: 87.
+// 131072 rows: 59 us, 5080 GB/s of needed traffic (76 %); zeros after the joins: 87.
 template <typename G, int VE, bool kAdd>
 __global__ void __launch_bounds__(256) embed_join_kernel(SumArgs a, G* __restrict__ dW) {
     __shared__ float part[kWarps][32 * VE];

@@ -308,8 +308,8 @@ constexpr int kRows = 8;        // rows handed over and not yet taken
 // same bits from each.
 // Bound by memory: a kept row is read once and written once, about 14 instructions and two
 // exponentials an element lie beside four bytes of bf16. 8192 x 131072 bf16, a fifth left out:
-// 605 us, 6390 GB/s of needed traffic (94 % of the copy rate); log-probabilities of 4096 x 32000
-// fp32: 82 us, 6420 GB/s. On the way: one block a row, read again for the gradient, 1890 us; a CTA
+// 611 us, 6330 GB/s of needed traffic (94 % of the copy rate); log-probabilities of 4096 x 32000
+// fp32: 82 us, 6410 GB/s. On the way: one block a row, read again for the gradient, 1890 us; a CTA
 // a share without the ring, 818; the ring with barriers in the CTA, 699. Shares of two pieces
 // instead of four (clusters twice as large): 760 against 594; 16 warps with two vectors each: 830;
 // pieces of 8 KB: 675.
