@@ -422,6 +422,139 @@ typedef struct {
 MOE_API moe_status_t moe_adamw(const moe_adamw_config_t* cfg, const moe_adamw_tensor_t* tensors, int32_t count,
                                const float* lr, const float* grad_scale, void* state, moe_stream_t stream);
 
+/* Choice of experts from scores: what moe_route's top-k and softmax over the k do not cover. The
+ * scores are a softmax over all experts or sigmoids; a bias for balance enters the choice but not
+ * the weights; experts may stand in groups, of which only the best are open to a token.
+ *   logits [T,E] fp32 (moe_route's `logits`), bias [E] fp32 (nullable: 0)
+ *   s_te = softmax(logits_t / temperature)_e   or   1 / (1 + exp(-logits_te / temperature)),
+ *   c_te = s_te + bias_e; -inf where the logit is -inf or c is NaN,
+ *   worth of a group (E / groups adjacent experts): the largest c in it, or the sum of its two
+ *     largest (group_top 2, one expert alone: its c); the groups_kept of most worth stay open,
+ *   idx [T,k] int32: the k largest c of the open groups, in falling order,
+ *   w [T,k] fp32: scale * s[idx]; renormalise: divided by the sum of the k chosen scores (softmax:
+ *     the softmax over the chosen logits alone; sigmoid: the sum plus 1e-20),
+ *   counts [E] int32: choices of each expert (nullable), balance_loss [1] fp32 =
+ *     mean_e (counts[e] - T k / E)^2 as moe_route's (nullable).
+ * Ties, of experts and of groups, go to the lower id. Without a bias c is compared as the logit
+ * (for groups with group_top 1 too), so that scores which round alike keep their order. idx are
+ * always k different experts of the open groups; one with a logit of -inf is taken only where the
+ * open groups hold fewer than k others, and has weight 0. A softmax over a row that holds NaN or
+ * +inf is NaN: the row's weights are NaN and its experts the first ones. A row of -inf alone has
+ * weights 0. logits are 16-byte aligned. ws (moe_route_scores_workspace_bytes) is needed when counts
+ * or balance_loss is wanted. */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
+typedef struct {
+    int32_t T;             /* tokens, 0 .. 2^27 */
+    int32_t E;             /* experts, 1 .. MOE_MAX_EXPERTS */
+    int32_t k;             /* experts per token, 1 .. min(MOE_MAX_K, E / groups * groups_kept) */
+    int32_t score;         /* moe_score_t */
+    int32_t groups;        /* 1 .. 32, divides E; 1: no groups */
+    int32_t groups_kept;   /* 1 .. groups */
+    int32_t group_top;     /* 1 or 2 */
+    int32_t renormalise;   /* 0/1 */
+    float temperature;     /* > 0, with a finite reciprocal */
+    float scale;           /* finite */
+} moe_score_config_t;
+/* Bytes of `ws` for moe_route_scores; 0 for an invalid cfg. */
+MOE_API size_t moe_route_scores_workspace_bytes(const moe_score_config_t* cfg);
+MOE_API moe_status_t moe_route_scores(const moe_score_config_t* cfg, const float* logits, const float* bias,
+                                      int32_t* idx, float* w, int32_t* counts, float* balance_loss, void* ws,
+                                      moe_stream_t stream);
+/* Gradient of sum(w * dw) in the logits, for the experts that were chosen (the choice itself and the
+ * bias have none): dlogits [T,E] fp32, all of it written. Chosen scores alone have a gradient, but for
+ * a softmax that is not renormalised, where every expert's does; only that one reads logits of experts
+ * that were not chosen. An idx outside [0,E), or an expert that an earlier slot of the token holds, sets
+ * MOE_ERR_DEVICE_BOUNDS and its slot is left out. A chosen logit of -inf has gradient 0 (a softmax over
+ * -inf alone, too). logits and dlogits are 16-byte aligned and do not overlap. */
+MOE_API moe_status_t moe_route_scores_backward(const moe_score_config_t* cfg, const float* logits,
+                                               const int32_t* idx, const float* dw, float* dlogits,
+                                               moe_stream_t stream);
+/* moe_backward for a layer whose idx and w came from moe_route_scores: the same arguments and outputs,
+ * with the gradient of the gate taken through the scores. scores->T, E and k are cfg's; logits [T,E] as
+ * given to moe_route_scores; dlogits [T,E] fp32 is written as moe_route_scores_backward writes it, and
+ * dx, dWg and dbg hold its part. cfg->temperature is not used. Dropped assignments give dw = 0 but still
+ * enter their token's Jacobian. k = E is refused (MOE_ERR_UNSUPPORTED): dense routing wants slot j to be
+ * expert j, and there is nothing to choose. */
+MOE_API moe_status_t moe_backward_scores(const moe_config_t* cfg, const moe_score_config_t* scores,
+                                         const float* logits, float* dlogits, const void* dy, const void* x,
+                                         const void* Wg, const int32_t* idx, const float* w,
+                                         const int32_t* offsets, const int32_t* row_token,
+                                         const int32_t* slot_row, const void* Xp, const void* Gp, const void* H,
+                                         const void* Yp, const void* W1, const void* W2,
+                                         const float* balance_loss, void* dx, float* dWg, void* dW1, float* db1,
+                                         void* dW2, float* db2, float* dbg, float* dw, float* loss, void* ws,
+                                         moe_stream_t stream);
+
+/* Layer norm of rows, and of a residual sum in the same pass.
+ *   s = x + residual (residual null: s = x),  mean = mean(s),  rstd = 1 / sqrt(mean((s - mean)^2) + eps),
+ *   y = (s - mean) rstd gain + bias                                   (gain null: 1; bias null: 0)
+ * x, residual, y, total [T,d] act; gain, bias [d] in param_dtype; total = s, each element rounded once
+ * (wanted iff residual is given); y is of the sum before it is rounded; mean, rstd [T] fp32 (each may be
+ * null). y or total may be x or residual; any other overlap is not allowed. The mean is taken first, the
+ * squares of the differences after it, in fp32 and a fixed order.
+ * Backward, with g = dy gain and h = (s - mean) rstd:
+ *   dx = rstd (g - mean(g) - h mean(g h)) + dtotal                     (dtotal null: 0)
+ *   dgain = sum_t dy h,  dbias = sum_t dy      fp32 [d], each may be null; accumulate: added to them
+ * s [T,d] act is the forward's total (or x), mean and rstd the forward's; dtotal [T,d] act is the gradient
+ * that reaches the sum itself (a residual stream). dx may be dy, s or dtotal; any other overlap is not
+ * allowed. dx may be null where only dgain or dbias is wanted. ws (moe_norm_workspace_bytes) is needed
+ * with dgain or dbias; their sums are fp32 in a fixed order, so results repeat bit for bit.
+ * T = 0 is allowed (dgain and dbias are zeroed unless accumulate). A row that holds NaN or an infinity
+ * gives NaN in its own y and dx only. Arrays of rows, gain, bias, dgain, dbias and ws are 16-byte aligned;
+ * d may be odd. */
+typedef struct {
+    int32_t T;             /* rows, 0 .. 2^30 */
+    int32_t d;             /* row length, 1 .. 2^20 */
+    float eps;             /* finite, >= 0 */
+    int32_t dtype;         /* moe_dtype_t of x, residual, y, total, dy, dx, dtotal */
+    int32_t param_dtype;   /* moe_dtype_t of gain and bias */
+    int32_t accumulate;    /* 0/1: backward adds to dgain and dbias */
+} moe_norm_config_t;
+MOE_API moe_status_t moe_layer_norm(const moe_norm_config_t* cfg, const void* x, const void* residual,
+                                    const void* gain, const void* bias, void* total, void* y, float* mean,
+                                    float* rstd, moe_stream_t stream);
+/* Bytes of `ws` for moe_layer_norm_backward; 0 for an invalid cfg. */
+MOE_API size_t moe_norm_workspace_bytes(const moe_norm_config_t* cfg);
+MOE_API moe_status_t moe_layer_norm_backward(const moe_norm_config_t* cfg, const void* dy, const void* s,
+                                             const void* gain, const float* mean, const float* rstd,
+                                             const void* dtotal, void* dx, float* dgain, float* dbias, void* ws,
+                                             moe_stream_t stream);
+
+/* Orthogonalised updates of weight matrices (Muon), for a stack of `count` matrices [rows, cols], each on
+ * its own (an MoE layer's W1 or W2: one matrix to an expert).
+ *   orth(u): X = u / (|u| + eps) with |u| the root of the sum of squares; `steps` times, with A = X X^T
+ *   (X^T X where rows > cols):  X = a X + (b A + c A A) X   (A on the right where rows > cols).
+ * The singular values go near 1 and the directions stay; a matrix of zeros stays zero.
+ *   moe_orthogonalize: o = orth(g)    o [count,rows,cols] in dtype, g in grad_dtype
+ *   moe_muon:          m = momentum m + g (g times *grad_scale),  u = nesterov ? g + momentum m : m,
+ *                      x = x (1 - lr weight_decay) - lr scale orth(u)
+ * m [count,rows,cols] fp32 (zeroed before the first step); x is the fp32 master if there is one (p is then
+ * x rounded to its type), else p in dtype. precision: MOE_BF16: operands of the products hold 11 bits
+ * (fp16, scaled), sums are fp32, orth(u) is right to about one rounding to bf16; MOE_F32: operands hold two
+ * fp16 parts, 22 bits, and the products three terms, right to a few 1e-6 of the largest elements. An element
+ * that is not finite, or a matrix whose sum of squares is beyond fp32, gives NaN in all of its own matrix
+ * and leaves the others alone.
+ * lr (device fp32, replaces cfg->lr) and grad_scale (device fp32) may be null, as in moe_adamw. p, g, o,
+ * master, m and ws (moe_muon_workspace_bytes) are 16-byte aligned and do not overlap, but o may be g where
+ * their types are the same. count = 0 is allowed. */
+typedef struct {
+    int32_t count;         /* matrices, 0 .. 65535; count * ceil(rows / 256) * ceil(cols / 256) to 2^30 */
+    int32_t rows, cols;    /* 1 .. 65536 each */
+    int32_t steps;         /* 0 .. 100 */
+    double a, b, c;        /* coefficients, magnitudes up to 16 */
+    double lr, momentum, weight_decay, scale, eps;   /* finite; momentum in [0, 1), eps in [1e-12, 1] */
+    int32_t nesterov;      /* 0/1 */
+    int32_t dtype;         /* moe_dtype_t of p, o */
+    int32_t grad_dtype;    /* moe_dtype_t of g */
+    int32_t precision;     /* moe_dtype_t: how exact orth(u) is */
+} moe_muon_config_t;
+/* Bytes of `ws`; 0 for an invalid cfg or count = 0. */
+MOE_API size_t moe_muon_workspace_bytes(const moe_muon_config_t* cfg);
+MOE_API moe_status_t moe_orthogonalize(const moe_muon_config_t* cfg, const void* g, void* o, void* ws,
+                                       moe_stream_t stream);
+MOE_API moe_status_t moe_muon(const moe_muon_config_t* cfg, void* p, const void* g, float* master, float* m,
+                              const float* lr, const float* grad_scale, void* ws, moe_stream_t stream);
+
 /* Synchronises `stream`, then returns and clears the device error word of the current
  * device: MOE_OK, MOE_ERR_DEVICE_TIMEOUT or MOE_ERR_DEVICE_BOUNDS; MOE_ERR_CUDA if the
  * stream reports a CUDA error. */

@@ -26,6 +26,7 @@ MOE_MAX_WINDOW = 4096
 MOE_ADAMW_BLOCK = 256
 MOE_ADAMW_STATE_BYTES = 32
 MOE_ADAMW_ROUND = {"even": 0, "weyl": 1}
+MOE_SCORE = {"softmax": 0, "sigmoid": 1}
 
 
 class MoeConfig(ctypes.Structure):
@@ -67,6 +68,25 @@ class MoeAdamwTensor(ctypes.Structure):
                 ("weight_decay", ctypes.c_float), ("reserved", ctypes.c_int32)]
 
 
+class MoeScoreConfig(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("E", ctypes.c_int32), ("k", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("groups_kept", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("renormalise", ctypes.c_int32), ("temperature", ctypes.c_float), ("scale", ctypes.c_float)]
+
+
+class MoeNormConfig(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("eps", ctypes.c_float), ("dtype", ctypes.c_int32),
+                ("param_dtype", ctypes.c_int32), ("accumulate", ctypes.c_int32)]
+
+
+class MoeMuonConfig(ctypes.Structure):
+    _fields_ = [("count", ctypes.c_int32), ("rows", ctypes.c_int32), ("cols", ctypes.c_int32),
+                ("steps", ctypes.c_int32), ("a", ctypes.c_double), ("b", ctypes.c_double), ("c", ctypes.c_double),
+                ("lr", ctypes.c_double), ("momentum", ctypes.c_double), ("weight_decay", ctypes.c_double),
+                ("scale", ctypes.c_double), ("eps", ctypes.c_double), ("nesterov", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32), ("precision", ctypes.c_int32)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, fn, status):
         self.status = status
@@ -77,6 +97,9 @@ _P = ctypes.c_void_p
 _CFG = ctypes.POINTER(MoeConfig)
 _EMB = ctypes.POINTER(MoeEmbedConfig)
 _POL = ctypes.POINTER(MoePolicyConfig)
+_SCO = ctypes.POINTER(MoeScoreConfig)
+_NRM = ctypes.POINTER(MoeNormConfig)
+_MUO = ctypes.POINTER(MoeMuonConfig)
 _SIGS = {
     "moe_config_init": (ctypes.c_int, [_CFG]),
     "moe_workspace_bytes": (ctypes.c_size_t, [_CFG]),
@@ -106,6 +129,16 @@ _SIGS = {
     "moe_token_logp": (ctypes.c_int, [_POL, _P, _P, _P, _P]),
     "moe_adamw": (ctypes.c_int, [ctypes.POINTER(MoeAdamwConfig), ctypes.POINTER(MoeAdamwTensor), ctypes.c_int32,
                                  _P, _P, _P, _P]),
+    "moe_route_scores_workspace_bytes": (ctypes.c_size_t, [_SCO]),
+    "moe_route_scores": (ctypes.c_int, [_SCO] + [_P] * 8),
+    "moe_route_scores_backward": (ctypes.c_int, [_SCO] + [_P] * 5),
+    "moe_backward_scores": (ctypes.c_int, [_CFG, _SCO] + [_P] * 28),
+    "moe_layer_norm": (ctypes.c_int, [_NRM] + [_P] * 9),
+    "moe_norm_workspace_bytes": (ctypes.c_size_t, [_NRM]),
+    "moe_layer_norm_backward": (ctypes.c_int, [_NRM] + [_P] * 11),
+    "moe_muon_workspace_bytes": (ctypes.c_size_t, [_MUO]),
+    "moe_orthogonalize": (ctypes.c_int, [_MUO] + [_P] * 4),
+    "moe_muon": (ctypes.c_int, [_MUO] + [_P] * 8),
     "moe_trace_begin": (ctypes.c_int, [ctypes.c_int32]),
     "moe_trace_end": (ctypes.c_int32, []),
     "moe_trace_record": (ctypes.c_int, [ctypes.c_int32, ctypes.POINTER(ctypes.c_char_p),

@@ -165,6 +165,13 @@ struct EventSet {
     }
 };
 
+// The gate's gradient through moe_route_scores (moe_backward_scores).
+struct ScoresGrad {
+    const moe_score_config_t* cfg;
+    const float* logits;
+    float* dlogits;
+};
+
 bool use_tc(const moe_config_t& c) { return c.dtype == MOE_BF16 && tc_gemm_supported(c); }
 
 cudaError_t row_gemm(const moe_config_t& c, const RowGemmArgs& a, cudaStream_t s) {
@@ -363,13 +370,12 @@ moe_status_t moe_combine(const moe_config_t* cfg, const void* Yp, const int32_t*
     return cuda_status(launch_combine(*cfg, Yp, slot_row, w, y, (cudaStream_t)stream));
 }
 
-moe_status_t moe_backward(const moe_config_t* cfg, const void* dy, const void* x, const void* Wg,
-                          const int32_t* idx, const float* w, const int32_t* offsets,
-                          const int32_t* row_token, const int32_t* slot_row, const void* Xp,
-                          const void* Gp, const void* H, const void* Yp, const void* W1,
-                          const void* W2, const float* balance_loss, void* dx, float* dWg, void* dW1,
-                          float* db1, void* dW2, float* db2, float* dbg, float* dw, float* loss,
-                          void* ws, moe_stream_t stream) {
+static moe_status_t layer_backward(const moe_config_t* cfg, const ScoresGrad* scores, const void* dy, const void* x,
+                                   const void* Wg, const int32_t* idx, const float* w, const int32_t* offsets,
+                                   const int32_t* row_token, const int32_t* slot_row, const void* Xp,
+                                   const void* Gp, const void* H, const void* Yp, const void* W1, const void* W2,
+                                   const float* balance_loss, void* dx, float* dWg, void* dW1, float* db1, void* dW2,
+                                   float* db2, float* dbg, float* dw, float* loss, void* ws, moe_stream_t stream) {
     moe_status_t st = check_config(cfg);
     if (st != MOE_OK) return st;
     if (!Wg || !offsets || !W1 || !W2 || !dWg || !dW1 || !db1 || !dW2 || !db2 || !ws)
@@ -407,11 +413,22 @@ moe_status_t moe_backward(const moe_config_t* cfg, const void* dy, const void* x
     const bool early_dz = dense_routing(c) || (c.dtype == MOE_BF16 && c.d % 64 == 0 && c.E > 32);
     float* dz_dense = dense_routing(c) ? b.dz : b.soft.dz;
 
+    // With scores the chosen logits' gradients stand in b.dz and all of them in scores->dlogits, both
+    // before the branches part; dWg and dbg follow as they do for dense dz rows, and where every logit
+    // has a gradient dx takes its part after the join.
+
     // combine backward: dYp, dw, loss partials (padding rows of dYp zeroed)
     MOE_TRY(launch_combine_bwd(c, dy, Yp, w, offsets, row_token, slot_row, b.dYp, dwp, b.lossblk, s));
+    if (scores) {
+        dz_dense = scores->dlogits;
+        MOE_TRY(launch_scores_grad(*scores->cfg, scores->logits, idx, dwp, dz_dense, b.dz, s));
+    }
     MOE_TRY(cudaEventRecord(ev.a, s));
     MOE_TRY(cudaStreamWaitEvent(side, ev.a, 0));
-    if (early_dz) {
+    if (scores) {
+        if (loss) MOE_TRY(launch_loss(c, b.lossblk, balance_loss, loss, side));
+        if (early_dz) MOE_TRY(launch_dense_dwg(c, dz_dense, x, dWg, dbg_out, false, b.soft, side));
+    } else if (early_dz) {
         MOE_TRY(launch_router_dz(c, w, dwp, idx, b.dz, dense_routing(c) ? nullptr : dz_dense, b.lossblk,
                                  balance_loss, loss, side));
         MOE_TRY(cudaEventRecord(ev.d, side));
@@ -451,7 +468,11 @@ moe_status_t moe_backward(const moe_config_t* cfg, const void* dy, const void* x
     gx.offsets = offsets; gx.E = c.E; gx.N = c.d; gx.K = c.d_ff; gx.rows_capacity = c.rows_capacity;
     gx.sBe = (long long)c.d_ff * c.d; gx.sBn = 1; gx.sBk = c.d;
     MOE_TRY(row_gemm(c, gx, s));
-    if (early_dz) {
+    if (scores) {
+        MOE_TRY(launch_router_bwd(c, w, dwp, idx, slot_row, Wg, b.dXp, b.dz, dx, nullptr, nullptr, nullptr,
+                                  nullptr, true, s));
+        if (!early_dz) MOE_TRY(launch_dense_dwg(c, dz_dense, x, dWg, dbg_out, false, b.soft, s));
+    } else if (early_dz) {
         // un-permute: dx = sum over kept slots of dXp rows + dz Wg, with dz from the side branch
         MOE_TRY(cudaStreamWaitEvent(s, ev.d, 0));
         MOE_TRY(launch_router_bwd(c, w, dwp, idx, slot_row, Wg, b.dXp, b.dz, dx, nullptr, nullptr, nullptr,
@@ -469,7 +490,38 @@ moe_status_t moe_backward(const moe_config_t* cfg, const void* dy, const void* x
     // join
     MOE_TRY(cudaEventRecord(ev.c, side));
     MOE_TRY(cudaStreamWaitEvent(s, ev.c, 0));
+    if (scores && scores_dense(*scores->cfg)) MOE_TRY(launch_dense_dx(c, dz_dense, Wg, dx, b.soft, s));
     return MOE_OK;
+}
+
+moe_status_t moe_backward(const moe_config_t* cfg, const void* dy, const void* x, const void* Wg,
+                          const int32_t* idx, const float* w, const int32_t* offsets,
+                          const int32_t* row_token, const int32_t* slot_row, const void* Xp,
+                          const void* Gp, const void* H, const void* Yp, const void* W1,
+                          const void* W2, const float* balance_loss, void* dx, float* dWg, void* dW1,
+                          float* db1, void* dW2, float* db2, float* dbg, float* dw, float* loss,
+                          void* ws, moe_stream_t stream) {
+    return layer_backward(cfg, nullptr, dy, x, Wg, idx, w, offsets, row_token, slot_row, Xp, Gp, H, Yp, W1, W2,
+                          balance_loss, dx, dWg, dW1, db1, dW2, db2, dbg, dw, loss, ws, stream);
+}
+
+moe_status_t moe_backward_scores(const moe_config_t* cfg, const moe_score_config_t* scores, const float* logits,
+                                 float* dlogits, const void* dy, const void* x, const void* Wg, const int32_t* idx,
+                                 const float* w, const int32_t* offsets, const int32_t* row_token,
+                                 const int32_t* slot_row, const void* Xp, const void* Gp, const void* H,
+                                 const void* Yp, const void* W1, const void* W2, const float* balance_loss, void* dx,
+                                 float* dWg, void* dW1, float* db1, void* dW2, float* db2, float* dbg, float* dw,
+                                 float* loss, void* ws, moe_stream_t stream) {
+    moe_status_t st = check_config(cfg);
+    if (st == MOE_OK) st = scores_status(scores);
+    if (st != MOE_OK) return st;
+    if (scores->T != cfg->T || scores->E != cfg->E || scores->k != cfg->k) return MOE_ERR_INVALID_ARG;
+    if (dense_routing(*cfg)) return MOE_ERR_UNSUPPORTED;
+    if (cfg->T > 0 && (!logits || !dlogits)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16({logits, dlogits})) return MOE_ERR_INVALID_ARG;
+    const ScoresGrad sg{scores, logits, dlogits};
+    return layer_backward(cfg, &sg, dy, x, Wg, idx, w, offsets, row_token, slot_row, Xp, Gp, H, Yp, W1, W2, balance_loss,
+                          dx, dWg, dW1, db1, dW2, db2, dbg, dw, loss, ws, stream);
 }
 
 moe_status_t moe_coselect(const moe_config_t* cfg, const int32_t* idx, int32_t* H, moe_stream_t stream) {

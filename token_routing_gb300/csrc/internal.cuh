@@ -129,10 +129,21 @@ cudaError_t launch_dense_dwg(const moe_config_t& c, const float* dz, const void*
 cudaError_t launch_soft_balance_bwd(const moe_config_t& c, const float* logits, const float* P, float weight,
                                     const int32_t* win_n, const void* x, const void* Wg, void* dx, float* dWg,
                                     float* dbg, const SoftScratch& s, cudaStream_t st);
+// dx += dz Wg for a dense dz [T, E], after launch_dense_dwg of the same dz on the same scratch.
+cudaError_t launch_dense_dx(const moe_config_t& c, const float* dz, const void* Wg, void* dx, const SoftScratch& s,
+                            cudaStream_t st);
 // Sliding window of soft loads: P (this batch) into ring slot state[0], Pbar = mean of the
 // window's loads, loss on Pbar, state advanced.
 cudaError_t launch_soft_window(const moe_config_t& c, const float* P, float weight, int W, float* ring,
                                int32_t* state, float* Pbar, float* loss, cudaStream_t st);
+
+// scores.cu: choice of experts from scores
+moe_status_t scores_status(const moe_score_config_t* c);
+// Whether every expert's logit has a gradient (softmax that is not renormalised); else the chosen ones'.
+inline bool scores_dense(const moe_score_config_t& c) { return c.score == MOE_SCORE_SOFTMAX && !c.renormalise; }
+// dz (nullable) [T, k]: the chosen logits' gradients; zeros where scores_dense.
+cudaError_t launch_scores_grad(const moe_score_config_t& c, const float* logits, const int32_t* idx, const float* dw,
+                               float* dlogits, float* dz, cudaStream_t s);
 
 // coselect.cu: expert co-selection matrix H [E, E]
 cudaError_t launch_coselect(const moe_config_t& c, const int32_t* idx, int32_t* H, cudaStream_t s);

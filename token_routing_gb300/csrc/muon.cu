@@ -1,0 +1,777 @@
+// Orthogonalised updates of stacks of matrices (Muon): momentum, Newton-Schulz products on CTA pairs
+// (tcgen05.mma.cta_group::2, 256 x 256 x 64 tiles of fp16 operands), and the step on the weights.
+//
+// With A = X X^T (X^T X where there are more rows than columns: the smaller side), one step is
+//   gram:  A                                   symmetric
+//   poly:  B = a I + b A + c A A               symmetric
+//   apply: X = B X   (X B)
+// Of the symmetric two only the tiles on and below the diagonal are computed; each is stored twice, once
+// as it is and once turned.
+//
+// Operands are fp16, not bf16: the tensor cores take both at one rate, and all of the factors are
+// bounded (singular values of X are 1 at most and stay near it), so bf16's range buys nothing and fp16's
+// three more bits make the rounding of one operand 2^-12 of it. X and A are held times 2^11 and B times
+// 2^10, so that what is far smaller than the largest elements keeps its bits too. In MOE_F32 precision an
+// operand is two fp16 planes, x = hi + lo, and a product takes hi hi + hi lo + lo hi.
+#include <cmath>
+
+#include "tc_gemm_common.cuh"
+#include "tc_pair_ptx.cuh"
+
+#include <cuda_fp16.h>
+
+namespace moe {
+
+namespace {
+
+constexpr int kTile = 256, kHalf = 128;              // tile of a pair, rows of a CTA
+constexpr int kPartBytes = kHalf * BK * 2;           // 16 KB: a CTA's rows of A, or its half of B
+constexpr int kStageBytes = 2 * kPartBytes;
+constexpr int kStages = 6;
+constexpr int kEpiWarps = 8;
+constexpr int kGemmThreads = 64 + 32 * kEpiWarps;
+constexpr float kXScale = 2048.f, kAScale = 2048.f, kBScale = 1024.f;
+
+enum Op : int { kGram = 0, kPoly = 1, kApply = 2 };
+
+struct MuonGemm {
+    int count, M, N, K;           // per matrix: out [M, N], reduction K
+    int m_tiles, n_tiles, tiles;  // tiles: of one matrix
+    int terms;                    // products of planes: 1, or 3
+    const __half* aux;            // poly: A [planes][count][M, ld]
+    int ld;
+    float alpha, beta, diag;      // out = alpha acc + beta aux + diag on the diagonal
+    int* err;
+};
+
+// ---- 3D tensors [planes * count, rows, cols]
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* tm, int x, int y, int z,
+                                                 uint32_t mbar_cluster) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(mbar_cluster)
+        : "memory");
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* tm, uint32_t src, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];"
+                 ::"l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(src) : "memory");
+}
+// kind::f16, fp16 operands, fp32 sums.
+__host__ __device__ constexpr uint32_t idesc_fp16(int M, int N, bool a_mn, bool b_mn) {
+    return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
+           ((uint32_t)(M >> 4) << 24);
+}
+
+struct MuonTile {
+    int z, m0, n0;
+};
+// Tile r of a matrix: row-major, or for the symmetric products the tiles on and below the diagonal, one
+// row of tiles after another.
+template <bool SYM>
+__device__ __forceinline__ MuonTile decode_tile(const MuonGemm& p, int tile) {
+    MuonTile t;
+    t.z = tile / p.tiles;
+    const int r = tile - t.z * p.tiles;
+    int i, j;
+    if (SYM) {
+        i = (int)((sqrtf(8.0f * (float)r + 1.0f) - 1.0f) * 0.5f);
+        while (i * (i + 1) / 2 > r) --i;
+        while ((i + 1) * (i + 2) / 2 <= r) ++i;
+        j = r - i * (i + 1) / 2;
+    } else {
+        i = r / p.n_tiles;
+        j = r - i * p.n_tiles;
+    }
+    t.m0 = i * kTile;
+    t.n0 = j * kTile;
+    return t;
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// One epilogue warp's two staging buffers of 32 rows x 64 bytes (64-byte swizzle).
+struct Staging {
+    uint32_t base;
+    int count;
+    __device__ __forceinline__ uint32_t acquire(int lane) {
+        if (lane == 0 && count >= 2) bulk_wait_read1();
+        __syncwarp();
+        return base + (count & 1) * STG_BYTES;
+    }
+    __device__ __forceinline__ void release(int lane, uint32_t buf, const CUtensorMap* tm, int x, int y, int z) {
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_3d(tm, buf, x, y, z);
+            bulk_commit();
+        }
+        ++count;
+    }
+    // h[i]: columns 2i and 2i + 1 of the lane's row
+    __device__ __forceinline__ void store(int lane, const uint32_t (&h)[16], const CUtensorMap* tm, int x, int y, int z) {
+        const uint32_t buf = acquire(lane);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            sts128(sw64_addr(buf, lane, j), make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]));
+        release(lane, buf, tm, x, y, z);
+    }
+    // The box turned: even lanes write the words (rows l, l + 1) of column 2i, odd ones of column 2i + 1.
+    __device__ __forceinline__ void store_turned(int lane, const uint32_t (&h)[16], const CUtensorMap* tm, int x, int y,
+                                                 int z) {
+        const uint32_t buf = acquire(lane);
+        const int odd = lane & 1, word = lane >> 1;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, h[i], 1);
+            const uint32_t v = odd ? __byte_perm(other, h[i], 0x7632) : __byte_perm(h[i], other, 0x5410);
+            const uint32_t addr = sw64_addr(buf, 2 * i + odd, word >> 2) + (word & 3) * 4;
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+        }
+        release(lane, buf, tm, x, y, z);
+    }
+};
+
+// out = alpha P Q + beta aux + diag I on CTA pairs; the pipeline and its barriers are those of the grouped
+// expert GEMMs. Operand planes with SPLIT: lo hi, hi lo, then hi hi into the same sums; the small terms come
+// first, because the sums lose a part of a last bit with every addition, measured by what they hold.
+template <int OP, bool A_MN, bool B_MN, bool SPLIT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
+muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                 const __grid_constant__ CUtensorMap tmO) {
+    constexpr bool SYM = OP != kApply;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* stg_smem = smem + kStages * kStageBytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(stg_smem + kEpiWarps * 2 * STG_BYTES);
+    uint64_t* empty = full + kStages;
+    uint64_t* tfull = empty + kStages;
+    uint64_t* tempty = tfull + 2;
+    uint64_t* drain = tempty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* s_fail = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const bool leader = (rank == 0);
+    const int cluster_id = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) { mbar_init(full + s, 1); mbar_init(empty + s, 1); }
+        for (int b = 0; b < 2; ++b) { mbar_init(tfull + b, 1); mbar_init(tempty + b, 2 * 32 * kEpiWarps); }
+        mbar_init(drain, 1);
+        *s_fail = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 0 && lane == 0) { tma_prefetch_desc(&tmA); tma_prefetch_desc(&tmB); tma_prefetch_desc(&tmO); }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_u32(tmem_slot)), "r"(TMEM_COLS) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    pdl_wait();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    cluster_sync();   // both CTAs' barriers exist before any remote arrive or complete_tx
+    const uint32_t tmem_base = *tmem_slot;
+    const int num_tiles = p.count * p.tiles;
+    const int kblocks = (p.K + BK - 1) / BK, steps = kblocks * p.terms;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t s = 0, ph = 0;
+            long long issued = 0;
+            bool ok = true;
+            for (int tile = cluster_id; tile < num_tiles && ok; tile += nclusters) {
+                const MuonTile t = decode_tile<SYM>(p, tile);
+                const int mr = t.m0 + (int)rank * kHalf, nh = t.n0 + (int)rank * kHalf;
+                int kb = 0, term = 0;
+                for (int q = 0; q < steps; ++q) {
+                    if (!mbar_wait(empty + s, ph ^ 1, p.err)) { ok = false; break; }
+                    const uint32_t sa = smem_u32(smem + s * kStageBytes), sb = sa + kPartBytes;
+                    const uint32_t fb = map_to_rank(smem_u32(full + s), 0);
+                    if (leader) mbar_expect_tx(full + s, 2 * kStageBytes);
+                    const int k0 = kb * BK;
+                    const int za = t.z + (SPLIT && term == 0 ? p.count : 0), zb = t.z + (SPLIT && term == 1 ? p.count : 0);
+                    if (!A_MN) {
+                        tma_load_3d_pair(sa, &tmA, k0, mr, za, fb);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < kHalf / 64; ++j)
+                            tma_load_3d_pair(sa + j * (BK * 128), &tmA, mr + 64 * j, k0, za, fb);
+                    }
+                    if (!B_MN) {
+                        tma_load_3d_pair(sb, &tmB, k0, nh, zb, fb);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < kHalf / 64; ++j)
+                            tma_load_3d_pair(sb + j * (BK * 128), &tmB, nh + 64 * j, k0, zb, fb);
+                    }
+                    ++issued;
+                    if (++s == kStages) { s = 0; ph ^= 1; }
+                    if (++kb == kblocks) { kb = 0; ++term; }
+                }
+            }
+            if (!ok) {
+                *s_fail = 1;
+                // no copy may be in flight when the CTAs leave: the stages issued last, oldest first
+                const long long n = issued < kStages ? issued : kStages;
+                for (long long i = issued - n; i < issued && leader; ++i)
+                    if (!mbar_wait(full + (int)(i % kStages), (uint32_t)(i / kStages) & 1u, p.err)) break;
+            }
+        }
+    } else if (warp == 1) {
+        if (leader && lane == 0) {
+            const uint32_t idesc = idesc_fp16(kTile, BN, A_MN, B_MN);
+            const uint32_t s0 = smem_u32(smem);
+            const uint64_t a_desc0 = A_MN ? make_desc(s0, BK * 128, 1024) : make_desc(s0, 16, 1024);
+            const uint64_t b_desc0 = B_MN ? make_desc(s0 + kPartBytes, BK * 128, 1024) : make_desc(s0 + kPartBytes, 16, 1024);
+            constexpr uint32_t A_KSTEP = (A_MN ? UMMA_K * 128 : UMMA_K * 2) >> 4;
+            constexpr uint32_t B_KSTEP = (B_MN ? UMMA_K * 128 : UMMA_K * 2) >> 4;
+            constexpr uint32_t STAGE_STEP = kStageBytes >> 4;
+            uint32_t s = 0, ph = 0, soff = 0, tl = 0;
+            bool ok = true;
+            for (int tile = cluster_id; tile < num_tiles && ok; tile += nclusters) {
+                const int buf = tl & 1;
+                const uint32_t aph = (tl >> 1) & 1;
+                ++tl;
+                if (!mbar_wait(tempty + buf, aph ^ 1, p.err)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + buf * BN;
+                for (int q = 0; q < steps; ++q) {
+                    if (!mbar_wait(full + s, ph, p.err)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint64_t ad = a_desc0 + soff, bd = b_desc0 + soff;
+#pragma unroll
+                    for (int kk = 0; kk < BK / UMMA_K; ++kk)
+                        mma_pair(d_tmem, ad + kk * A_KSTEP, bd + kk * B_KSTEP, idesc, (q > 0 || kk > 0) ? 1u : 0u);
+                    commit_pair_both(empty + s);
+                    if (++s == kStages) { s = 0; ph ^= 1; soff = 0; } else { soff += STAGE_STEP; }
+                }
+                if (!ok) break;
+                commit_pair_both(tfull + buf);
+            }
+            if (!ok) *s_fail = 1;
+            commit_pair_local(drain);
+            mbar_wait(drain, 0, p.err);
+        }
+    } else {
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        Staging st{smem_u32(stg_smem + (warp - 2) * 2 * STG_BYTES), 0};
+        const uint32_t tempty_leader[2] = {map_to_rank(smem_u32(tempty), 0), map_to_rank(smem_u32(tempty + 1), 0)};
+        uint32_t tl = 0;
+        for (int tile = cluster_id; tile < num_tiles; tile += nclusters) {
+            const MuonTile t = decode_tile<SYM>(p, tile);
+            const int buf = tl & 1;
+            const uint32_t aph = (tl >> 1) & 1;
+            ++tl;
+            const int y = t.m0 + (int)rank * kHalf + quarter * 32;    // the warp's first row
+            const int x0 = t.n0 + half * (BN / 2);                    // its first column
+            const bool turn = SYM && t.m0 != t.n0;
+            if (!mbar_wait(tfull + buf, aph, p.err)) break;
+            tc_fence_after();
+            const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + buf * BN + half * (BN / 2);
+            for (int c = 0; c < BN / 2; c += 32) {
+                const int x = x0 + c;
+                if (x >= p.N || y >= p.M) break;
+                uint32_t acc[32];
+                tmem_ld32(taddr + c, acc);
+                float v[32];
+                if (OP == kPoly) {
+                    // A of the same box: the lane's row, 64 bytes
+                    const bool in = y + lane < p.M;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                    for (int pl = 0; pl < (SPLIT ? 2 : 1); ++pl) {
+                        const __half* src = p.aux + ((size_t)(t.z + pl * p.count) * p.M + (y + lane)) * p.ld + x;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if (in && x + 8 * j < p.ld) {
+                                const uint4 u = __ldg(reinterpret_cast<const uint4*>(src) + j);
+                                const __half2* h = reinterpret_cast<const __half2*>(&u);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const float2 f = __half22float2(h[i]);
+                                    v[8 * j + 2 * i] += f.x;
+                                    v[8 * j + 2 * i + 1] += f.y;
+                                }
+                            }
+                        }
+                    }
+                }
+                tmem_ld_wait_regs(acc);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const float a = p.alpha * __uint_as_float(acc[i]);
+                    if (OP == kPoly) {
+                        v[i] = fmaf(p.beta, v[i], a);
+                        if (!turn && x + i == y + lane) v[i] += p.diag;
+                    } else {
+                        v[i] = a;
+                    }
+                }
+                uint32_t h[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) h[i] = pack_half2(v[2 * i], v[2 * i + 1]);
+                st.store(lane, h, &tmO, x, y, t.z);
+                if (turn) st.store_turned(lane, h, &tmO, y, x, t.z);
+                if (SPLIT) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+                        h[i] = pack_half2(v[2 * i] - f.x, v[2 * i + 1] - f.y);
+                    }
+                    st.store(lane, h, &tmO, x, y, t.z + p.count);
+                    if (turn) st.store_turned(lane, h, &tmO, y, x, t.z + p.count);
+                }
+            }
+            tc_fence_before();
+            if (leader) mbar_arrive(tempty + buf);
+            else mbar_arrive_cluster(tempty_leader[buf]);
+            if (*s_fail) break;
+        }
+        if (lane == 0) bulk_wait_all();
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // all work of both CTAs is done before the pair releases its TMEM
+    tc_fence_after();
+    if (warp == 1) {
+        __syncwarp();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS)
+                     : "memory");
+    }
+}
+
+constexpr size_t kGemmSmem = 1024 + (size_t)kStages * kStageBytes + kEpiWarps * 2 * STG_BYTES + 32 * sizeof(uint64_t);
+static_assert(kGemmSmem <= 227 * 1024, "shared memory per CTA");
+
+// ---------------------------------------------------------------- before the products
+struct MuonPrep {
+    const void* g;
+    float* m;                 // momentum, or null (orthogonalize)
+    const float* grad_scale;
+    float* sums;              // [count, chunks] partial sums of squares
+    __half* X;                // [planes, count, rows, ld]
+    int64_t n, chunk;         // elements of a matrix, of a chunk
+    int chunks, count, rows, cols, ld;
+    float momentum, eps;
+    int nesterov;
+};
+
+constexpr int kPrepThreads = 256;
+
+// V elements of the gradient from element i of a matrix on.
+template <typename G, int V>
+__device__ __forceinline__ void load_v(const G* p, float (&f)[V]) {
+    if constexpr (V == 1) {
+        f[0] = Elem<G>::to_f(*p);
+    } else {
+        static_assert(V == 8, "");
+        if constexpr (sizeof(G) == 2) {
+            load16(p, f);
+        } else {
+            load16(p, f);
+            load16(p + 4, f + 4);
+        }
+    }
+}
+
+// u = g (+ momentum), the momentum written in the first pass.
+template <typename G, int V, bool FIRST>
+__device__ __forceinline__ void update_v(const MuonPrep& a, int64_t at, float gs, float (&u)[V]) {
+    load_v<G, V>(static_cast<const G*>(a.g) + at, u);
+    if (!a.m) return;
+    float m[V];
+    if constexpr (V == 1) {
+        m[0] = a.m[at];
+    } else {
+#pragma unroll
+        for (int q = 0; q < V; q += 4) *reinterpret_cast<float4*>(m + q) = *reinterpret_cast<const float4*>(a.m + at + q);
+    }
+#pragma unroll
+    for (int q = 0; q < V; ++q) {
+        u[q] *= gs;
+        if (FIRST) m[q] = fmaf(a.momentum, m[q], u[q]);
+    }
+    if (FIRST) {
+        if constexpr (V == 1) {
+            a.m[at] = m[0];
+        } else {
+#pragma unroll
+            for (int q = 0; q < V; q += 4) *reinterpret_cast<float4*>(a.m + at + q) = *reinterpret_cast<float4*>(m + q);
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < V; ++q) u[q] = a.nesterov ? fmaf(a.momentum, m[q], u[q]) : m[q];
+}
+
+// First pass: momentum, and the sum of squares of each chunk of a matrix.
+template <typename G, int V>
+__global__ void __launch_bounds__(kPrepThreads) muon_sums_kernel(const MuonPrep a) {
+    __shared__ float s_sum[kPrepThreads / 32];
+    pdl_wait();
+    const float gs = a.grad_scale ? __ldg(a.grad_scale) : 1.f;
+    for (int64_t w = blockIdx.x; w < (int64_t)a.count * a.chunks; w += gridDim.x) {
+        const int64_t z = w / a.chunks, c = w - z * a.chunks;
+        const int64_t end = min(a.n, (c + 1) * a.chunk);
+        float sum = 0.f;
+        for (int64_t i = c * a.chunk + threadIdx.x * V; i < end; i += kPrepThreads * V) {
+            float u[V];
+            update_v<G, V, true>(a, z * a.n + i, gs, u);
+            float part = 0.f;
+#pragma unroll
+            for (int q = 0; q < V; ++q) part = fmaf(u[q], u[q], part);
+            sum += part;
+        }
+        sum = warp_sum(sum);
+        if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = sum;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int i = 1; i < kPrepThreads / 32; ++i) sum += s_sum[i];
+            a.sums[w] = sum;
+        }
+        __syncthreads();
+    }
+}
+
+// Second pass: X = u / (|u| + eps), in fp16 parts.
+template <typename G, int V, bool SPLIT>
+__global__ void __launch_bounds__(kPrepThreads) muon_scale_kernel(const MuonPrep a) {
+    __shared__ float s_scale;
+    pdl_wait();
+    const float gs = a.grad_scale ? __ldg(a.grad_scale) : 1.f;
+    const size_t plane = (size_t)a.count * a.rows * a.ld;
+    for (int64_t w = blockIdx.x; w < (int64_t)a.count * a.chunks; w += gridDim.x) {
+        const int64_t z = w / a.chunks, c = w - z * a.chunks;
+        if (threadIdx.x < 32) {
+            float sum = 0.f;
+            for (int i = threadIdx.x; i < a.chunks; i += 32) sum += a.sums[z * a.chunks + i];
+            sum = warp_sum(sum);
+            const float norm = sqrtf(sum) + a.eps;
+            if (threadIdx.x == 0) s_scale = sum < INFINITY ? kXScale / norm : NAN;
+        }
+        __syncthreads();
+        const float scale = s_scale;
+        const int64_t end = min(a.n, (c + 1) * a.chunk);
+        for (int64_t i = c * a.chunk + threadIdx.x * V; i < end; i += kPrepThreads * V) {
+            float u[V];
+            update_v<G, V, false>(a, z * a.n + i, gs, u);
+            int64_t at;
+            if constexpr (V == 8) {
+                at = z * a.n + i;           // cols % 8 = 0: ld = cols
+            } else {
+                const int r = (int)(i / a.cols);
+                at = (z * a.rows + r) * a.ld + (i - (int64_t)r * a.cols);
+            }
+            __half hi[V], lo[V];
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                const float x = u[q] * scale;
+                hi[q] = __float2half_rn(x);
+                lo[q] = __float2half_rn(x - __half2float(hi[q]));
+            }
+            if constexpr (V == 8) {
+                *reinterpret_cast<uint4*>(a.X + at) = *reinterpret_cast<uint4*>(hi);
+                if (SPLIT) *reinterpret_cast<uint4*>(a.X + plane + at) = *reinterpret_cast<uint4*>(lo);
+            } else {
+                a.X[at] = hi[0];
+                if (SPLIT) a.X[plane + at] = lo[0];
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------- after the products
+struct MuonFinish {
+    const __half* X;
+    void* out;                // o, or p
+    float* master;
+    const float* lr_dev;
+    int64_t n, total;
+    int count, rows, cols, ld;
+    float lr, decay, scale;
+    bool step;                // p is stepped; else o is written
+};
+
+template <typename T, int V, bool SPLIT>
+__global__ void __launch_bounds__(256) muon_finish_kernel(const MuonFinish a) {
+    pdl_wait();
+    const float lr = a.lr_dev ? __ldg(a.lr_dev) : a.lr;
+    const float lose = lr * a.decay, move = lr * a.scale * (1.f / kXScale);
+    const size_t plane = (size_t)a.count * a.rows * a.ld;
+    T* out = static_cast<T*>(a.out);
+    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V; i < a.total; i += (int64_t)gridDim.x * 256 * V) {
+        float x[V];
+        if constexpr (V == 8) {
+            const uint4 h4 = *reinterpret_cast<const uint4*>(a.X + i);
+            const __half* h = reinterpret_cast<const __half*>(&h4);
+#pragma unroll
+            for (int q = 0; q < V; ++q) x[q] = __half2float(h[q]);
+            if (SPLIT) {
+                const uint4 l4 = *reinterpret_cast<const uint4*>(a.X + plane + i);
+                const __half* l = reinterpret_cast<const __half*>(&l4);
+#pragma unroll
+                for (int q = 0; q < V; ++q) x[q] += __half2float(l[q]);
+            }
+        } else {
+            const int64_t row = i / a.cols, at = row * a.ld + (i - row * a.cols);
+            x[0] = __half2float(a.X[at]);
+            if (SPLIT) x[0] += __half2float(a.X[plane + at]);
+        }
+        if (!a.step) {
+#pragma unroll
+            for (int q = 0; q < V; ++q) x[q] *= 1.f / kXScale;
+        } else {
+            float p[V];
+            if (a.master) {
+                if constexpr (V == 8) {
+                    *reinterpret_cast<float4*>(p) = *reinterpret_cast<const float4*>(a.master + i);
+                    *reinterpret_cast<float4*>(p + 4) = *reinterpret_cast<const float4*>(a.master + i + 4);
+                } else {
+                    p[0] = a.master[i];
+                }
+            } else {
+                load_v<T, V>(out + i, p);
+            }
+#pragma unroll
+            for (int q = 0; q < V; ++q) x[q] = fmaf(-move, x[q], fmaf(-lose, p[q], p[q]));
+            if (a.master) {
+                if constexpr (V == 8) {
+                    *reinterpret_cast<float4*>(a.master + i) = *reinterpret_cast<float4*>(x);
+                    *reinterpret_cast<float4*>(a.master + i + 4) = *reinterpret_cast<float4*>(x + 4);
+                } else {
+                    a.master[i] = x[0];
+                }
+            }
+        }
+        if constexpr (V == 8) {
+            if constexpr (sizeof(T) == 2) {
+                store16(out + i, x);
+            } else {
+                store16(out + i, x);
+                store16(out + i + 4, x + 4);
+            }
+        } else {
+            st_f(out + i, x[0]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- host
+moe_status_t check_muon(const moe_muon_config_t* c) {
+    if (!c) return MOE_ERR_INVALID_ARG;
+    if (c->count < 0 || c->rows < 1 || c->cols < 1 || c->steps < 0 || c->steps > 100) return MOE_ERR_INVALID_ARG;
+    for (double v : {c->a, c->b, c->c})
+        if (!(std::fabs(v) <= 16.0)) return MOE_ERR_INVALID_ARG;
+    for (double v : {c->lr, c->weight_decay, c->scale})
+        if (!std::isfinite(v) || !std::isfinite((float)v)) return MOE_ERR_INVALID_ARG;
+    if (!(c->momentum >= 0.0 && c->momentum < 1.0) || !(c->eps >= 1e-12 && c->eps <= 1.0)) return MOE_ERR_INVALID_ARG;
+    if (c->nesterov != 0 && c->nesterov != 1) return MOE_ERR_INVALID_ARG;
+    for (int32_t t : {c->dtype, c->grad_dtype, c->precision})
+        if (t != MOE_F32 && t != MOE_BF16) return MOE_ERR_INVALID_ARG;
+    if (c->count > 65535 || c->rows > 65536 || c->cols > 65536) return MOE_ERR_UNSUPPORTED;
+    const int64_t tiles = (int64_t)ceil_div(c->rows, kTile) * ceil_div(c->cols, kTile);
+    if (c->count * tiles > (1 << 30)) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+
+constexpr int64_t kChunk = 32768;     // elements whose squares one block adds up
+constexpr int kMaxChunks = 1024;      // chunks of a matrix
+
+struct MuonScratch {
+    __half* X[2];
+    __half* A;
+    __half* B;
+    float* sums;
+    int planes, ld, lds, side;        // ld: of X; side, lds: of A and B
+    int64_t chunk;
+    int chunks;
+};
+
+size_t carve_muon(const moe_muon_config_t& c, void* base, MuonScratch* b) {
+    Workspace ws{static_cast<char*>(base), 0};
+    b->planes = c.precision == MOE_F32 ? 2 : 1;
+    b->ld = (int)align_up(c.cols, 8);
+    b->side = std::min(c.rows, c.cols);
+    b->lds = (int)align_up(b->side, 8);
+    const int64_t n = (int64_t)c.rows * c.cols;
+    b->chunk = std::max<int64_t>(kChunk, ((n + kMaxChunks - 1) / kMaxChunks + 7) / 8 * 8);
+    b->chunks = (int)((n + b->chunk - 1) / b->chunk);
+    const size_t all = (size_t)b->planes * c.count;
+    b->sums = ws.take<float>((size_t)c.count * b->chunks + 1);
+    for (__half*& x : b->X) x = ws.take<__half>(all * c.rows * b->ld + 1);
+    b->A = ws.take<__half>(all * b->side * b->lds + 1);
+    b->B = ws.take<__half>(all * b->side * b->lds + 1);
+    return align_up(ws.used, 256);
+}
+
+// fp16 [outer, rows, cols] with rows ld elements apart.
+bool map_3d(CUtensorMap* tm, const void* base, uint64_t cols, uint64_t rows, uint64_t outer, uint64_t ld,
+            uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {cols, rows, outer};
+    cuuint64_t strides[2] = {ld * 2, ld * rows * 2};
+    cuuint32_t box[3] = {box_cols, box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Operand {
+    const __half* base;
+    int rows, cols, ld;
+};
+
+// K-major operands come in boxes of 64 k x 128 rows, MN-major ones of 64 columns x 64 k.
+template <int OP, bool A_MN, bool B_MN>
+cudaError_t launch_gemm(MuonGemm p, int planes, const Operand& a, const Operand& b, const Operand& o, cudaStream_t s) {
+    constexpr bool SYM = OP != kApply;
+    p.m_tiles = ceil_div(p.M, kTile);
+    p.n_tiles = ceil_div(p.N, kTile);
+    p.tiles = SYM ? p.m_tiles * (p.m_tiles + 1) / 2 : p.m_tiles * p.n_tiles;
+    p.terms = planes == 2 ? 3 : 1;
+    p.err = device_error_word();
+    const uint64_t outer = (uint64_t)planes * p.count;
+    CUtensorMap ta, tb, to;
+    if (!map_3d(&ta, a.base, a.cols, a.rows, outer, a.ld, 64, A_MN ? BK : kHalf, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !map_3d(&tb, b.base, b.cols, b.rows, outer, b.ld, 64, B_MN ? BK : kHalf, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !map_3d(&to, o.base, o.cols, o.rows, outer, o.ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+        return cudaErrorInvalidValue;
+    auto kern = planes == 2 ? muon_gemm_kernel<OP, A_MN, B_MN, true> : muon_gemm_kernel<OP, A_MN, B_MN, false>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem);
+    if (e != cudaSuccess) return e;
+    const int clusters = (int)std::min<int64_t>((int64_t)p.count * p.tiles, num_sms() / 2);
+    e = launch_pdl(kern, dim3(2 * clusters), dim3(kGemmThreads), kGemmSmem, s, p, ta, tb, to);
+    count_launch();
+    return e;
+}
+
+template <typename G>
+cudaError_t launch_prep(const MuonPrep& a, bool split, cudaStream_t s) {
+    const int64_t work = (int64_t)a.count * a.chunks;
+    const int grid = (int)std::min<int64_t>(work, (int64_t)num_sms() * 8);
+    cudaError_t e = launch_pdl(a.n % 8 == 0 ? muon_sums_kernel<G, 8> : muon_sums_kernel<G, 1>, dim3(grid),
+                               dim3(kPrepThreads), 0, s, a);
+    count_launch();
+    if (e != cudaSuccess) return e;
+    auto kern = a.cols % 8 == 0 ? (split ? muon_scale_kernel<G, 8, true> : muon_scale_kernel<G, 8, false>)
+                                : (split ? muon_scale_kernel<G, 1, true> : muon_scale_kernel<G, 1, false>);
+    e = launch_pdl(kern, dim3(grid), dim3(kPrepThreads), 0, s, a);
+    count_launch();
+    return e;
+}
+
+template <typename T>
+cudaError_t launch_finish(const MuonFinish& a, bool split, cudaStream_t s) {
+    const int v = a.cols % 8 == 0 ? 8 : 1;
+    auto kern = v == 8 ? (split ? muon_finish_kernel<T, 8, true> : muon_finish_kernel<T, 8, false>)
+                       : (split ? muon_finish_kernel<T, 1, true> : muon_finish_kernel<T, 1, false>);
+    const int64_t need = (a.total + 256 * v - 1) / (256 * v);
+    const cudaError_t e = launch_pdl(kern, dim3((unsigned)std::min<int64_t>(need, (int64_t)num_sms() * 32)), dim3(256),
+                                     0, s, a);
+    count_launch();
+    return e;
+}
+
+cudaError_t launch_muon(const moe_muon_config_t& c, const void* g, float* m, const float* grad_scale, MuonFinish f,
+                        void* ws, cudaStream_t s) {
+    MuonScratch b;
+    carve_muon(c, ws, &b);
+    const bool split = b.planes == 2, tall = c.rows > c.cols;
+    MuonPrep pre{g, m, grad_scale, b.sums, b.X[0], (int64_t)c.rows * c.cols, b.chunk, b.chunks, c.count, c.rows, c.cols,
+                 b.ld, (float)c.momentum, (float)c.eps, c.nesterov};
+    cudaError_t e = c.grad_dtype == MOE_BF16 ? launch_prep<__nv_bfloat16>(pre, split, s)
+                                             : launch_prep<float>(pre, split, s);
+    if (e != cudaSuccess) return e;
+    const Operand A{b.A, b.side, b.side, b.lds}, B{b.B, b.side, b.side, b.lds};
+    int at = 0;
+    for (int k = 0; k < c.steps; ++k, at ^= 1) {
+        const Operand X{b.X[at], c.rows, c.cols, b.ld}, Y{b.X[at ^ 1], c.rows, c.cols, b.ld};
+        MuonGemm p{};
+        p.count = c.count;
+        p.M = p.N = b.side;
+        p.K = std::max(c.rows, c.cols);
+        p.alpha = kAScale / (kXScale * kXScale);
+        e = tall ? launch_gemm<kGram, true, true>(p, b.planes, X, X, A, s)
+                 : launch_gemm<kGram, false, false>(p, b.planes, X, X, A, s);
+        if (e != cudaSuccess) return e;
+        p.K = b.side;
+        p.aux = b.A;
+        p.ld = b.lds;
+        p.alpha = (float)(c.c * kBScale / ((double)kAScale * kAScale));
+        p.beta = (float)(c.b * kBScale / kAScale);
+        p.diag = (float)(c.a * kBScale);
+        e = launch_gemm<kPoly, false, false>(p, b.planes, A, A, B, s);
+        if (e != cudaSuccess) return e;
+        p.M = c.rows;
+        p.N = c.cols;
+        p.alpha = 1.f / kBScale;
+        e = tall ? launch_gemm<kApply, false, false>(p, b.planes, X, B, Y, s)
+                 : launch_gemm<kApply, false, true>(p, b.planes, B, X, Y, s);
+        if (e != cudaSuccess) return e;
+    }
+    f.X = b.X[at];
+    f.n = pre.n;
+    f.total = pre.n * c.count;
+    f.count = c.count;
+    f.rows = c.rows;
+    f.cols = c.cols;
+    f.ld = b.ld;
+    f.lr = (float)c.lr;
+    f.decay = (float)c.weight_decay;
+    f.scale = (float)c.scale;
+    return c.dtype == MOE_BF16 ? launch_finish<__nv_bfloat16>(f, split, s) : launch_finish<float>(f, split, s);
+}
+
+}  // namespace
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" MOE_API size_t moe_muon_workspace_bytes(const moe_muon_config_t* cfg) {
+    if (check_muon(cfg) != MOE_OK || cfg->count == 0) return 0;
+    MuonScratch b;
+    return carve_muon(*cfg, nullptr, &b);
+}
+
+extern "C" MOE_API moe_status_t moe_orthogonalize(const moe_muon_config_t* cfg, const void* g, void* o, void* ws,
+                                                  moe_stream_t stream) {
+    const moe_status_t st = check_muon(cfg);
+    if (st != MOE_OK) return st;
+    if (cfg->count == 0) return MOE_OK;
+    if (!g || !o || !ws || (g == o && cfg->dtype != cfg->grad_dtype)) return MOE_ERR_INVALID_ARG;
+    if (misaligned(g, 16) || misaligned(o, 16) || misaligned(ws, 16)) return MOE_ERR_INVALID_ARG;
+    MuonFinish f{};
+    f.out = o;
+    return launch_muon(*cfg, g, nullptr, nullptr, f, ws, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+extern "C" MOE_API moe_status_t moe_muon(const moe_muon_config_t* cfg, void* p, const void* g, float* master, float* m,
+                                         const float* lr, const float* grad_scale, void* ws, moe_stream_t stream) {
+    const moe_status_t st = check_muon(cfg);
+    if (st != MOE_OK) return st;
+    if (cfg->count == 0) return MOE_OK;
+    if (!p || !g || !m || !ws) return MOE_ERR_INVALID_ARG;
+    if (misaligned(p, 16) || misaligned(g, 16) || misaligned(master, 16) || misaligned(m, 16) || misaligned(ws, 16) ||
+        misaligned(lr, 4) || misaligned(grad_scale, 4))
+        return MOE_ERR_INVALID_ARG;
+    MuonFinish f{};
+    f.out = p;
+    f.master = master;
+    f.lr_dev = lr;
+    f.step = true;
+    return launch_muon(*cfg, g, m, grad_scale, f, ws, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}

@@ -1,0 +1,599 @@
+// Choice of experts from scores (softmax over all experts, or sigmoids), with a bias for balance,
+// expert groups and renormalised weights, and its gradient in the logits.
+#include <cmath>
+
+#include "internal.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kWarps = 8;                 // warps of a block; each takes a token at a time
+constexpr int kThreads = 32 * kWarps;
+constexpr int kCand = 32;                 // candidates that a warp ranks at once, one to a lane
+constexpr float kTiny = 1e-20f;           // added to the sum of the chosen sigmoids
+
+struct ScoreArgs {
+    const float* logits;
+    const float* bias;
+    int32_t* idx;
+    float* w;
+    int32_t* part;        // [blocks, E] choices per block, or null
+    int T, E, k, groups, kept, top, renorm;
+    uint32_t group_mul;   // e / group size = e * group_mul >> 16
+    int lanes_log;        // log2 of the lanes that read one group
+    float inv_hi, inv_lo; // 1 / temperature in two parts
+    float scale;
+};
+
+// z / temperature, by a reciprocal in two parts: within one rounding of the quotient. An infinite z
+// stays what it is (times a low part of zero it would be NaN).
+__device__ __forceinline__ float scaled(float z, float hi, float lo) {
+    return fabsf(z) == INFINITY ? z : fmaf(z, hi, z * lo);
+}
+
+// fp32 in the order of unsigned integers; NaN goes with -inf. Nothing maps to 0, which stands for
+// an expert that is not open to the token.
+__device__ __forceinline__ uint32_t order_key(float f) {
+    if (!(f == f)) f = -INFINITY;
+    const uint32_t u = __float_as_uint(f + 0.0f);     // -0 and 0 tie
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// One token by a warp; expert lane + 32 i is the lane's i-th. CHOICE: experts are compared by score
+// plus bias; else by logit.
+//
+// The k largest of E: the k-th largest of the 32 lanes' maxima bounds them from below, so only the
+// experts at or above it (8 to 12 of 256 for k = 8) are ranked, each by counting those ahead of it.
+template <int V, bool SOFTMAX, bool CHOICE>
+__device__ __forceinline__ void route_token(const ScoreArgs& a, int t, const float (&z)[V], const float (&bias)[V],
+                                            int lane, float* s_score, uint32_t* s_key, uint64_t* s_cand, int* s_hist) {
+    const int E = a.E, k = a.k;
+    uint32_t key[V];
+    float norm_max = 0.f, norm_inv = 1.f;     // softmax: row maximum and 1 / sum
+    float x[V];
+    // a row that holds NaN or +inf has no softmax: its first experts, with NaN weights
+    bool bad = false;
+    if (SOFTMAX) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) bad |= !(z[i] < INFINITY);      // -inf beyond E
+        bad = __any_sync(0xffffffffu, bad);
+    }
+    if (SOFTMAX && (CHOICE || !a.renorm)) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            x[i] = scaled(z[i], a.inv_hi, a.inv_lo);
+            mx = fmaxf(mx, x[i]);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        norm_max = mx == -INFINITY ? 0.f : mx;
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            x[i] = expf(x[i] - norm_max);
+            sum += x[i];
+        }
+        sum = warp_sum(sum);
+        norm_inv = bad ? NAN : sum > 0.f ? 1.0f / sum : 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] *= norm_inv;
+    } else if (!SOFTMAX && CHOICE) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = 1.0f / (1.0f + expf(-scaled(z[i], a.inv_hi, a.inv_lo)));
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = lane + 32 * i;
+        float c = z[i];
+        if (CHOICE) c = z[i] == -INFINITY ? -INFINITY : x[i] + bias[i];
+        key[i] = e < E ? order_key(c) : 0u;
+        if (CHOICE && e < E) s_score[e] = x[i];
+    }
+    if (!CHOICE && SOFTMAX && bad) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) key[i] = min(key[i], 1u);
+    }
+
+    if (a.kept < a.groups) {
+        // worth of each group by 2^lanes_log lanes, each reading every 2^lanes_log-th of its experts
+        // (starting points turned, so that groups of 32 read different banks)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (lane + 32 * i < E) s_key[lane + 32 * i] = key[i];
+        __syncwarp();
+        const int size = E / a.groups, step = 1 << a.lanes_log;
+        const int g = lane >> a.lanes_log, sub = lane & (step - 1);
+        uint32_t m1 = 0, m2 = 0;
+        if (g < a.groups && sub < size) {
+            const int n = (size - sub + step - 1) >> a.lanes_log;
+            int j = g % n;
+            for (int q = 0; q < n; ++q) {
+                const uint32_t v = s_key[g * size + sub + (j << a.lanes_log)];
+                m2 = max(m2, min(m1, v));
+                m1 = max(m1, v);
+                if (++j == n) j = 0;
+            }
+        }
+        for (int o = step >> 1; o > 0; o >>= 1) {
+            const uint32_t n1 = __shfl_xor_sync(0xffffffffu, m1, o), n2 = __shfl_xor_sync(0xffffffffu, m2, o);
+            m2 = max(max(m2, n2), min(m1, n1));
+            m1 = max(m1, n1);
+        }
+        uint32_t worth = m1;
+        if (a.top == 2 && m2) {
+            auto value = [](uint32_t u) { return __uint_as_float((u & 0x80000000u) ? u & 0x7fffffffu : ~u); };
+            worth = order_key(value(m1) + value(m2));
+        }
+        int rank = 0;
+        for (int h = 0; h < a.groups; ++h) {
+            const uint32_t v = __shfl_sync(0xffffffffu, worth, h << a.lanes_log);
+            rank += h < g ? v >= worth : v > worth;
+        }
+        const uint32_t open = __ballot_sync(0xffffffffu, g < a.groups && rank < a.kept);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const uint32_t h = ((uint32_t)(lane + 32 * i) * a.group_mul) >> 16;
+            if (lane + 32 * i < E && !((open >> (h << a.lanes_log)) & 1u)) key[i] = 0;
+        }
+    }
+
+    // a lower bound of the k largest
+    uint32_t top = key[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) top = max(top, key[i]);
+    uint32_t least = 0;
+    for (int j = 0; j < k; ++j) {
+        least = __reduce_max_sync(0xffffffffu, top);
+        const uint32_t at = __ballot_sync(0xffffffffu, top == least);
+        if (lane == __ffs(at) - 1) top = 0;
+    }
+    least = max(least, 1u);
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const bool in = key[i] >= least;
+        const uint32_t at = __ballot_sync(0xffffffffu, in);
+        const int pos = n + __popc(at & ((1u << lane) - 1u));
+        if (in && pos < kCand) s_cand[pos] = (uint64_t)key[i] << 32 | (uint32_t)(lane + 32 * i);
+        n += __popc(at);
+    }
+    __syncwarp();
+    int mine = -1, slot = k;     // the lane's chosen expert and its place
+    if (n <= kCand) {
+        // candidates stand in order of their ids
+        if (lane < n) {
+            const uint32_t own = (uint32_t)(s_cand[lane] >> 32);
+            int rank = 0;
+            for (int j = 0; j < n; ++j) {
+                const uint32_t v = (uint32_t)(s_cand[j] >> 32);
+                rank += j < lane ? v >= own : v > own;
+            }
+            if (rank < k) {
+                slot = rank;
+                mine = (int)(uint32_t)s_cand[lane];
+            }
+        }
+    } else {
+        // many equal keys: one expert after another
+        for (int j = 0; j < k; ++j) {
+            uint32_t best = 0, id = 0xffffffffu;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (key[i] > best) {
+                    best = key[i];
+                    id = (uint32_t)(lane + 32 * i);
+                }
+            const uint32_t most = __reduce_max_sync(0xffffffffu, best);
+            const uint32_t first = __reduce_min_sync(0xffffffffu, best == most ? id : 0xffffffffu);
+            if (lane == j) {
+                mine = (int)first;
+                slot = j;
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if ((uint32_t)(lane + 32 * i) == first) key[i] = 0;
+        }
+    }
+    // weights, by the lanes that hold a chosen expert
+    const bool has = slot < k;
+    float s = 0.f;
+    if (SOFTMAX && a.renorm) {
+        const float zc = has ? scaled(__ldg(a.logits + (size_t)t * E + mine), a.inv_hi, a.inv_lo) : -INFINITY;
+        float mx = zc;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        if (mx == -INFINITY) mx = 0.f;
+        s = expf(zc - mx);
+        const float sum = warp_sum(s);
+        s = bad ? NAN : sum > 0.f ? s / sum : 0.f;
+    } else {
+        if (CHOICE) {
+            if (has) s = s_score[mine];
+        } else if (has) {
+            const float xc = scaled(__ldg(a.logits + (size_t)t * E + mine), a.inv_hi, a.inv_lo);
+            s = SOFTMAX ? expf(xc - norm_max) * norm_inv : 1.0f / (1.0f + expf(-xc));
+        }
+        if (a.renorm) s = s / (warp_sum(s) + kTiny);
+    }
+    if (has) {
+        a.idx[(size_t)t * k + slot] = mine;
+        a.w[(size_t)t * k + slot] = s * a.scale;
+        if (a.part) atomicAdd(s_hist + mine, 1);
+    }
+    __syncwarp();
+}
+
+// balance_loss = mean_e (counts[e] - T k / E)^2, by the whole block: counts differ from their mean by
+// up to T k, whose squares want 64 bits; the sum is of integers (E counts - T k), exact.
+__device__ __forceinline__ void block_balance(const int* s_counts, int T, int E, int k, float* out, double* s_red) {
+    double sq = 0.0;
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+        const double off = (double)s_counts[e] * E - (double)T * k;
+        sq += off * off;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+    if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = sq;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double all = 0.0;
+        for (int w = 0; w < (int)(blockDim.x >> 5); ++w) all += s_red[w];
+        *out = (float)(all / ((double)E * E * E));
+    }
+}
+
+template <int V, bool SOFTMAX, bool CHOICE>
+__global__ void __launch_bounds__(kThreads) route_scores_kernel(const ScoreArgs a, int32_t* counts, float* balance) {
+    __shared__ float s_score[kWarps][32 * V];
+    __shared__ uint32_t s_key[kWarps][32 * V];
+    __shared__ uint64_t s_cand[kWarps][kCand];
+    __shared__ int s_hist[MOE_MAX_EXPERTS];
+    __shared__ double s_red[kWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int nwarps = gridDim.x * kWarps;
+    for (int e = threadIdx.x; e < a.E; e += kThreads) s_hist[e] = 0;
+    __syncthreads();
+    pdl_wait();
+    float bias[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = lane + 32 * i;
+        bias[i] = CHOICE && a.bias && e < a.E ? __ldg(a.bias + e) : 0.f;
+    }
+    int t = blockIdx.x * kWarps + warp;
+    float z[V], next[V];
+    auto fetch = [&](int u, float (&into)[V]) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = lane + 32 * i;
+            into[i] = u < a.T && e < a.E ? __ldg(a.logits + (size_t)u * a.E + e) : -INFINITY;
+        }
+    };
+    fetch(t, z);
+    for (; t < a.T; t += nwarps) {
+        fetch(t + nwarps, next);
+        route_token<V, SOFTMAX, CHOICE>(a, t, z, bias, lane, s_score[warp], s_key[warp], s_cand[warp], s_hist);
+#pragma unroll
+        for (int i = 0; i < V; ++i) z[i] = next[i];
+    }
+    __syncthreads();
+    if (a.part)
+        for (int e = threadIdx.x; e < a.E; e += kThreads) a.part[(size_t)blockIdx.x * a.E + e] = s_hist[e];
+    if (gridDim.x == 1) {      // few tokens: one block has all of the counts
+        if (counts)
+            for (int e = threadIdx.x; e < a.E; e += kThreads) counts[e] = s_hist[e];
+        if (balance) block_balance(s_hist, a.T, a.E, a.k, balance, s_red);
+    }
+}
+
+// counts = sum of the blocks' choices, and the balance loss.
+constexpr int kFinish = 1024;
+__global__ void __launch_bounds__(kFinish) route_counts_kernel(const int32_t* __restrict__ part, int blocks, int T,
+                                                              int E, int k, int32_t* counts, float* balance) {
+    __shared__ int s_sum[kFinish];
+    __shared__ double s_red[kFinish / 32];
+    pdl_wait();
+    const int rows = kFinish / E, row = threadIdx.x / E, e = threadIdx.x - row * E;
+    int sum = 0;
+    if (row < rows) {
+#pragma unroll 8
+        for (int b = row; b < blocks; b += rows) sum += part[(size_t)b * E + e];
+        s_sum[threadIdx.x] = sum;
+    }
+    __syncthreads();
+    if (row == 0) {
+        for (int r = 1; r < rows; ++r) sum += s_sum[r * E + e];
+        if (counts) counts[e] = sum;
+    }
+    __syncthreads();
+    if (row == 0) s_sum[e] = sum;
+    __syncthreads();
+    if (balance) block_balance(s_sum, T, E, k, balance, s_red);
+}
+
+// ---------------------------------------------------------------- gradient
+struct ScoreGradArgs {
+    const float* logits;
+    const int32_t* idx;
+    const float* dw;
+    float* dlogits;
+    float* dz;            // [T, k] gradients of the chosen logits (nullable)
+    int T, E, k, renorm;
+    float inv_hi, inv_lo, scale;
+    int* err;
+};
+
+// The gradients of four tokens' chosen logits, by lanes of eight to a token (slot j = lane % 8). The
+// derivative of a share in its own sum is taken by differences of dw, since one share can be nearly
+// all of the sum. FULL (softmax that is not renormalised): g = dw scale instead, for the Jacobian over
+// all experts. `on` says whether the slot counts.
+template <bool SOFTMAX, bool FULL>
+__device__ __forceinline__ float slot_grad(const ScoreGradArgs& a, int t, int j, int& e, bool& on) {
+    on = t < a.T && j < a.k;
+    const size_t at = (size_t)t * a.k + j;
+    e = on ? a.idx[at] : -1;
+    const float dw = on ? a.dw[at] : 0.f;
+    if (on && (uint32_t)e >= (uint32_t)a.E) {
+        raise_error(a.err, kErrBounds);
+        on = false;
+    }
+    // an expert that an earlier slot holds
+    bool twice = false;
+    for (int i = 0; i < a.k - 1; ++i) {
+        const int o = __shfl_sync(0xffffffffu, e, i, 8);
+        twice |= i < j && o == e;
+    }
+    if (on && twice) {
+        raise_error(a.err, kErrBounds);
+        on = false;
+    }
+    if (FULL) return dw * a.scale;
+    const float z = on ? __ldg(a.logits + (size_t)t * a.E + e) : -INFINITY;
+    const float x = scaled(z, a.inv_hi, a.inv_lo);
+    float s, slope;                 // score, and d score / d x
+    if (SOFTMAX) {
+        float mx = x;
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        if (mx == -INFINITY) mx = 0.f;
+        s = on ? expf(x - mx) : 0.f;
+        slope = s;                  // the part through the sum cancels in the shares
+    } else {
+        const float u = expf(-x);
+        s = on ? 1.0f / (1.0f + u) : 0.f;
+        // s (1 - s), with 1 - s = 1 / (1 + e^x) taken apart so that it does not cancel
+        slope = s * (1.0f / (1.0f + expf(x)));
+    }
+    if (!a.renorm) return on ? dw * a.scale * slope : 0.f;
+    float sum = s;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float tiny = SOFTMAX ? 0.f : kTiny;
+    const float inv = sum + tiny == 0.f ? 0.f : 1.0f / (sum + tiny);
+    const float share = s * inv;
+    float g = dw * (tiny * inv);
+    for (int i = 0; i < a.k; ++i) {
+        const float si = __shfl_sync(0xffffffffu, share, i, 8), di = __shfl_sync(0xffffffffu, dw, i, 8);
+        if (si != 0.f) g = fmaf(si, dw - di, g);
+    }
+    return on ? g * (a.scale * inv) * slope : 0.f;
+}
+
+// Gradient at the chosen experts, zeros elsewhere: a warp holds four tokens' rows of zeros in shared
+// memory, sets their chosen entries, copies the rows out in 16-byte vectors and clears the entries.
+template <bool SOFTMAX>
+__global__ void __launch_bounds__(kThreads) scores_grad_kernel(const ScoreGradArgs a) {
+    extern __shared__ __align__(16) float s_rows[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float* row = s_rows + (size_t)warp * 4 * a.E;
+    for (int i = lane; i < 4 * a.E; i += 32) row[i] = 0.f;
+    __syncwarp();
+    pdl_wait();
+    const int quads = (a.T + 3) / 4, step = gridDim.x * kWarps;
+    for (int q = blockIdx.x * kWarps + warp; q < quads; q += step) {
+        const int t = 4 * q + (lane >> 3);
+        int e;
+        bool on;
+        const float g = slot_grad<SOFTMAX, false>(a, t, lane & 7, e, on);
+        float* at = row + (lane >> 3) * a.E + e;
+        const float dz = scaled(g, a.inv_hi, a.inv_lo);
+        if (on) *at = dz;
+        if (a.dz && t < a.T && (lane & 7) < a.k) a.dz[(size_t)t * a.k + (lane & 7)] = on ? dz : 0.f;
+        __syncwarp();
+        float* out = a.dlogits + (size_t)q * 4 * a.E;
+        if (4 * q + 4 <= a.T) {
+            for (int i = lane; i < a.E; i += 32)
+                reinterpret_cast<float4*>(out)[i] = reinterpret_cast<const float4*>(row)[i];
+        } else {
+            for (int i = lane; i < (a.T - 4 * q) * a.E; i += 32) out[i] = row[i];
+        }
+        __syncwarp();
+        if (on) *at = 0.f;
+        __syncwarp();
+    }
+}
+
+// Softmax over all experts, weights not renormalised: dz_e = p_e (g_e - sum_chosen p g) / temperature.
+template <int V>
+__global__ void __launch_bounds__(kThreads) scores_grad_full_kernel(const ScoreGradArgs a) {
+    __shared__ float s_g[kWarps][32 * V];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float* sg = s_g[warp];
+#pragma unroll
+    for (int i = 0; i < V; ++i) sg[lane + 32 * i] = 0.f;
+    __syncwarp();
+    pdl_wait();
+    for (int t = blockIdx.x * kWarps + warp; t < a.T; t += gridDim.x * kWarps) {
+        float x[V];
+        float mx = -INFINITY;
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = lane + 32 * i;
+            x[i] = e < a.E ? scaled(__ldg(a.logits + (size_t)t * a.E + e), a.inv_hi, a.inv_lo) : -INFINITY;
+            bad |= !(x[i] < INFINITY);
+            mx = fmaxf(mx, x[i]);
+        }
+        int e;
+        bool on;
+        // all four groups of eight lanes work on the same token; the first one's slots are set
+        const float g = slot_grad<true, true>(a, t, lane & 7, e, on);
+        if (on && lane < 8) sg[e] = g;
+        if (a.dz && lane < a.k) a.dz[(size_t)t * a.k + lane] = 0.f;   // all of the gradient is dense
+        __syncwarp();
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        bad = __any_sync(0xffffffffu, bad);
+        if (mx == -INFINITY) mx = 0.f;
+        float sum = 0.f, dot = 0.f;
+        float gi[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            x[i] = expf(x[i] - mx);
+            sum += x[i];
+            gi[i] = sg[lane + 32 * i];
+            dot = fmaf(x[i], gi[i], dot);
+        }
+        sum = warp_sum(sum);
+        dot = warp_sum(dot);
+        const float inv = bad ? NAN : sum > 0.f ? 1.0f / sum : 0.f;
+        dot *= inv;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = lane + 32 * i;
+            if (c < a.E) a.dlogits[(size_t)t * a.E + c] = scaled(x[i] * inv * (gi[i] - dot), a.inv_hi, a.inv_lo);
+        }
+        __syncwarp();
+        if (on && lane < 8) sg[e] = 0.f;
+        __syncwarp();
+    }
+}
+
+// ---------------------------------------------------------------- host
+moe_status_t check_scores(const moe_score_config_t* c) {
+    if (!c) return MOE_ERR_INVALID_ARG;
+    if (c->T < 0 || c->E < 1 || c->E > MOE_MAX_EXPERTS || c->groups < 1 || c->groups > 32 || c->E % c->groups ||
+        c->groups_kept < 1 || c->groups_kept > c->groups || c->k < 1 || c->k > MOE_MAX_K ||
+        c->k > c->E / c->groups * c->groups_kept)
+        return MOE_ERR_INVALID_ARG;
+    if ((c->score != MOE_SCORE_SOFTMAX && c->score != MOE_SCORE_SIGMOID) || (c->group_top != 1 && c->group_top != 2) ||
+        (c->renormalise != 0 && c->renormalise != 1))
+        return MOE_ERR_INVALID_ARG;
+    if (!(c->temperature > 0.0f) || !std::isfinite(c->temperature) || !std::isfinite(1.0f / c->temperature) ||
+        !std::isfinite(c->scale))
+        return MOE_ERR_INVALID_ARG;
+    if (c->T > (1 << 27)) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+
+void reciprocal(float temperature, float* hi, float* lo) {
+    const double inv = 1.0 / (double)temperature;
+    *hi = (float)inv;
+    *lo = (float)(inv - (double)*hi);
+}
+
+// Blocks of the choice: all that the SMs hold at once, or one for few tokens.
+int score_blocks(const moe_score_config_t& c) {
+    const int need = ceil_div(c.T, kWarps);
+    return need <= 4 ? 1 : std::min(need, num_sms() * 6);
+}
+
+template <int V>
+cudaError_t launch_scores(const ScoreArgs& a, bool softmax, bool choice, int blocks, int32_t* counts, float* balance,
+                          cudaStream_t s) {
+    auto kern = softmax ? (choice ? route_scores_kernel<V, true, true> : route_scores_kernel<V, true, false>)
+                        : (choice ? route_scores_kernel<V, false, true> : route_scores_kernel<V, false, false>);
+    const cudaError_t e = launch_pdl(kern, dim3(blocks), dim3(kThreads), 0, s, a, counts, balance);
+    count_launch();
+    return e;
+}
+
+}  // namespace
+
+cudaError_t launch_scores_grad(const moe_score_config_t& c, const float* logits, const int32_t* idx, const float* dw,
+                               float* dlogits, float* dz, cudaStream_t s) {
+    if (c.T == 0) return cudaSuccess;
+    ScoreGradArgs a{logits, idx, dw, dlogits, dz, c.T, c.E, c.k, c.renormalise, 0.f, 0.f, c.scale, device_error_word()};
+    reciprocal(c.temperature, &a.inv_hi, &a.inv_lo);
+    cudaError_t e;
+    if (c.score == MOE_SCORE_SOFTMAX && !c.renormalise) {
+        const int blocks = std::min(ceil_div(c.T, kWarps), num_sms() * 8);
+        const int v = ceil_div(c.E, 32);
+        auto kern = v <= 1 ? scores_grad_full_kernel<1> : v <= 2 ? scores_grad_full_kernel<2>
+                    : v <= 4 ? scores_grad_full_kernel<4> : scores_grad_full_kernel<8>;
+        e = launch_pdl(kern, dim3(blocks), dim3(kThreads), 0, s, a);
+    } else {
+        const int blocks = std::min(ceil_div(c.T, 4 * kWarps), num_sms() * 6);
+        auto kern = c.score == MOE_SCORE_SOFTMAX ? scores_grad_kernel<true> : scores_grad_kernel<false>;
+        e = launch_pdl(kern, dim3(blocks), dim3(kThreads), (size_t)kWarps * 4 * c.E * sizeof(float), s, a);
+    }
+    count_launch();
+    return e;
+}
+
+moe_status_t scores_status(const moe_score_config_t* c) { return check_scores(c); }
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" MOE_API size_t moe_route_scores_workspace_bytes(const moe_score_config_t* cfg) {
+    if (check_scores(cfg) != MOE_OK) return 0;
+    return align_up((size_t)score_blocks(*cfg) * cfg->E * sizeof(int32_t) + 1, 256);
+}
+
+extern "C" MOE_API moe_status_t moe_route_scores(const moe_score_config_t* cfg, const float* logits, const float* bias,
+                                                 int32_t* idx, float* w, int32_t* counts, float* balance_loss,
+                                                 void* ws, moe_stream_t stream) {
+    const moe_status_t st = check_scores(cfg);
+    if (st != MOE_OK) return st;
+    const moe_score_config_t& c = *cfg;
+    if (c.T > 0 && (!logits || !idx || !w)) return MOE_ERR_INVALID_ARG;
+    if ((counts || balance_loss) && !ws) return MOE_ERR_INVALID_ARG;
+    if (misaligned(logits, 16) || misaligned(ws, 16) || misaligned(bias, 4) || misaligned(idx, 4) || misaligned(w, 4) ||
+        misaligned(counts, 4) || misaligned(balance_loss, 4))
+        return MOE_ERR_INVALID_ARG;
+    const bool tally = counts || balance_loss;
+    if (c.T == 0 && !tally) return MOE_OK;
+    cudaStream_t s = (cudaStream_t)stream;
+    const int blocks = score_blocks(c);
+    ScoreArgs a{};
+    a.logits = logits; a.bias = bias; a.idx = idx; a.w = w;
+    a.part = tally ? static_cast<int32_t*>(ws) : nullptr;
+    a.T = c.T; a.E = c.E; a.k = c.k; a.groups = c.groups; a.kept = c.groups_kept; a.top = c.group_top;
+    a.renorm = c.renormalise; a.scale = c.scale;
+    const int size = c.E / c.groups;
+    a.group_mul = (uint32_t)((65536 + size - 1) / size);
+    while ((c.groups << (a.lanes_log + 1)) <= 32) ++a.lanes_log;
+    reciprocal(c.temperature, &a.inv_hi, &a.inv_lo);
+    const bool softmax = c.score == MOE_SCORE_SOFTMAX;
+    const bool choice = bias || (c.groups_kept < c.groups && c.group_top == 2);
+    const int v = ceil_div(c.E, 32);
+    cudaError_t e = v <= 1 ? launch_scores<1>(a, softmax, choice, blocks, counts, balance_loss, s)
+                    : v <= 2 ? launch_scores<2>(a, softmax, choice, blocks, counts, balance_loss, s)
+                    : v <= 4 ? launch_scores<4>(a, softmax, choice, blocks, counts, balance_loss, s)
+                             : launch_scores<8>(a, softmax, choice, blocks, counts, balance_loss, s);
+    if (e == cudaSuccess && tally && blocks > 1) {
+        e = launch_pdl(route_counts_kernel, dim3(1), dim3(kFinish), 0, s, (const int32_t*)a.part, blocks, c.T, c.E, c.k,
+                       counts, balance_loss);
+        count_launch();
+    }
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+extern "C" MOE_API moe_status_t moe_route_scores_backward(const moe_score_config_t* cfg, const float* logits,
+                                                          const int32_t* idx, const float* dw, float* dlogits,
+                                                          moe_stream_t stream) {
+    const moe_status_t st = check_scores(cfg);
+    if (st != MOE_OK) return st;
+    if (cfg->T == 0) return MOE_OK;
+    if (!logits || !idx || !dw || !dlogits) return MOE_ERR_INVALID_ARG;
+    if (misaligned(logits, 16) || misaligned(dlogits, 16) || misaligned(idx, 4) || misaligned(dw, 4))
+        return MOE_ERR_INVALID_ARG;
+    return launch_scores_grad(*cfg, logits, idx, dw, dlogits, nullptr, (cudaStream_t)stream) == cudaSuccess ? MOE_OK
+                                                                                                  : MOE_ERR_CUDA;
+}

@@ -1013,4 +1013,52 @@ cudaError_t launch_dense_dwg(const moe_config_t& c, const float* dz, const void*
     return cudaGetLastError();
 }
 
+namespace {
+
+// dx += dz Wg for rows that are no multiple of a vector: a token to a warp.
+template <typename T>
+__global__ void __launch_bounds__(256) dense_dx_kernel(const float* __restrict__ dz, const T* __restrict__ Wg, int Tn,
+                                                       int E, int d, T* __restrict__ dx) {
+    pdl_wait();
+    __shared__ float s_dz[8][MOE_MAX_EXPERTS];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int t = blockIdx.x * 8 + warp; t < Tn; t += gridDim.x * 8) {
+        for (int e = lane; e < E; e += 32) s_dz[warp][e] = dz[(size_t)t * E + e];
+        __syncwarp();
+        for (int c = lane; c < d; c += 32) {
+            float acc = ld_f(dx + (size_t)t * d + c);
+            for (int e = 0; e < E; ++e) acc = fmaf(s_dz[warp][e], ld_f(Wg + (size_t)e * d + c), acc);
+            st_f(dx + (size_t)t * d + c, acc);
+        }
+        __syncwarp();
+    }
+}
+
+template <typename T>
+cudaError_t dense_dx_t(const moe_config_t& c, const float* dz, const void* Wg, void* dx, cudaStream_t st) {
+    cudaError_t e;
+    if (tiled_ok(c, Wg, dx)) {
+        auto k = soft_dx_tiled_kernel<T>;
+        const size_t sm = dx_tiled_smem<T>(c.E);
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+        if (e != cudaSuccess) return e;
+        e = launch_pdl(k, dim3(ceil_div(c.T, 16), ceil_div(c.d, kTileCols)), dim3(kTileThreads), sm, st, dz,
+                       (const T*)Wg, c.T, c.E, c.d, dx_tiled_ec<T>(c.E), (T*)dx);
+    } else {
+        e = launch_pdl(dense_dx_kernel<T>, dim3(std::min(ceil_div(c.T, 8), num_sms() * 8)), dim3(256), 0, st, dz,
+                       (const T*)Wg, c.T, c.E, c.d, (T*)dx);
+    }
+    count_launch();
+    return e;
+}
+
+}  // namespace
+
+cudaError_t launch_dense_dx(const moe_config_t& c, const float* dz, const void* Wg, void* dx, const SoftScratch& s,
+                            cudaStream_t st) {
+    if (c.T == 0) return cudaSuccess;
+    if (soft_tc_ok(c)) return launch_dzwg_tc(c, Wg, dx, s, st);      // s.dzs holds dz in its parts
+    return c.dtype == MOE_BF16 ? dense_dx_t<__nv_bfloat16>(c, dz, Wg, dx, st) : dense_dx_t<float>(c, dz, Wg, dx, st);
+}
+
 }  // namespace moe

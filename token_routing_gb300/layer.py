@@ -134,6 +134,22 @@ def backward(cfg, dy, x, Wg, W1, W2, b, stream=None, want_dbg=True, want_dw=True
         _s(stream)))
 
 
+def backward_scores(cfg, scores, logits, dlogits, dy, x, Wg, W1, W2, b, stream=None, want_dbg=True, want_dw=True,
+                    want_loss=True):
+    """backward for a layer whose b["idx"] and b["w"] came from route_scores: `scores` is that call's
+    configuration, logits [T, E] its input; dlogits [T, E] fp32 receives the logits' gradient."""
+    f32 = torch.float32
+    for what, t in (("logits", logits), ("dlogits", dlogits)):
+        if t.dtype != f32 or t.shape != (cfg.T, cfg.E) or not t.is_contiguous():
+            raise ValueError(f"{what}: want contiguous {f32} {(cfg.T, cfg.E)}, got {t.dtype} {tuple(t.shape)}")
+    L.check("moe_backward_scores", L.load().moe_backward_scores(
+        ctypes.byref(cfg), ctypes.byref(scores), _p(logits), _p(dlogits), _p(dy), _p(x), _p(Wg), _p(b["idx"]),
+        _p(b["w"]), _p(b["offsets"]), _p(b["row_token"]), _p(b["slot_row"]), _p(b["Xp"]), _p(b["Gp"]), _p(b["H"]),
+        _p(b["Yp"]), _p(W1), _p(W2), _p(b["balance_loss"]), _p(b["dx"]), _p(b["dWg"]), _p(b["dW1"]), _p(b["db1"]),
+        _p(b["dW2"]), _p(b["db2"]), _p(b["dbg"]) if want_dbg else None, _p(b["dw"]) if want_dw else None,
+        _p(b["loss"]) if want_loss else None, _p(b["ws"]), _s(stream)))
+
+
 def coselect(cfg, idx, H, stream=None):
     """Expert co-selection matrix H [E, E] int32 of the routing indices idx [T, k]."""
     L.check("moe_coselect", L.load().moe_coselect(ctypes.byref(cfg), _p(idx), _p(H), _s(stream)))

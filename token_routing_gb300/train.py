@@ -1,5 +1,6 @@
 """Thin torch-facing binding of the training-step calls around the layer: token embedding,
-policy loss and AdamW (the C calls of the same names). The functions check what a tensor's type,
+layer norm, choice of experts from scores, policy loss, AdamW and Muon (the C calls of the same names).
+The functions check what a tensor's type,
 shape and device say, and marshal pointers; nothing is computed here.
 """
 import ctypes
@@ -34,6 +35,15 @@ def _one_gpu(first, *rest):
             return gpu
     on = sorted({t.get_device() for t in (first, *rest) if t is not None})
     raise ValueError(f"tensors on devices {on} (-1: the host): all have to be on one GPU")
+
+
+def _launch(what, gpu, stream, fn, *args):
+    """One C call on tensors of GPU `gpu`, which need not be the current one."""
+    if torch._C._cuda_getDevice() == gpu:
+        L.check(what, fn(*args, _stream(stream, gpu)))
+    else:
+        with torch.cuda.device(gpu):
+            L.check(what, fn(*args, _stream(stream, gpu)))
 
 
 def _want(what, t, dtype, shape, optional=False):
@@ -233,3 +243,197 @@ class AdamW:
     def steps_done(self):
         """Steps that the device has counted (synchronises)."""
         return int(self.state.view(torch.int64)[2])
+
+
+# ---------------------------------------------------------------- choice of experts from scores
+
+def make_score_config(T, E, k, score="softmax", groups=1, groups_kept=None, group_top=1, renormalise=True,
+                      temperature=1.0, scale=1.0):
+    """A moe_score_config_t (the calls check it and raise MoeError). groups_kept: default, all."""
+    if score not in L.MOE_SCORE:
+        raise ValueError(f"score: one of {sorted(L.MOE_SCORE)}")
+    return L.MoeScoreConfig(T=T, E=E, k=k, score=L.MOE_SCORE[score], groups=groups,
+                            groups_kept=groups if groups_kept is None else groups_kept, group_top=group_top,
+                            renormalise=int(bool(renormalise)), temperature=float(temperature), scale=float(scale))
+
+
+def route_scores_workspace_bytes(cfg):
+    return int(L.load().moe_route_scores_workspace_bytes(ctypes.byref(cfg)))
+
+
+def route_scores(cfg, logits, bias, idx, w, counts=None, balance_loss=None, ws=None, stream=None):
+    """idx [T, k] int32 and w [T, k] fp32 from logits [T, E] fp32 (moe_route's `logits`) and bias [E] fp32
+    (or None) by scores, groups and top-k; counts [E] int32 and balance_loss [1] fp32 (each may be None;
+    ws is needed for them)."""
+    T, E, k = cfg.T, cfg.E, cfg.k
+    _want("logits", logits, torch.float32, (T, E))
+    _want("bias", bias, torch.float32, (E,), True)
+    _want("idx", idx, torch.int32, (T, k))
+    _want("w", w, torch.float32, (T, k))
+    _want("counts", counts, torch.int32, (E,), True)
+    _want("balance_loss", balance_loss, torch.float32, (1,), True)
+    if counts is not None or balance_loss is not None:
+        _room("ws", ws, route_scores_workspace_bytes(cfg))
+    gpu = _one_gpu(logits, bias, idx, w, counts, balance_loss, ws)
+    _launch("moe_route_scores", gpu, stream, L.load().moe_route_scores, ctypes.byref(cfg), _ptr(logits), _ptr(bias),
+            _ptr(idx), _ptr(w), _ptr(counts), _ptr(balance_loss), _ptr(ws))
+
+
+def route_scores_backward(cfg, logits, idx, dw, dlogits, stream=None):
+    """dlogits [T, E] = the gradient of sum(w * dw) in the logits."""
+    T, E, k = cfg.T, cfg.E, cfg.k
+    _want("logits", logits, torch.float32, (T, E))
+    _want("idx", idx, torch.int32, (T, k))
+    _want("dw", dw, torch.float32, (T, k))
+    _want("dlogits", dlogits, torch.float32, (T, E))
+    gpu = _one_gpu(logits, idx, dw, dlogits)
+    _launch("moe_route_scores_backward", gpu, stream, L.load().moe_route_scores_backward, ctypes.byref(cfg),
+            _ptr(logits), _ptr(idx), _ptr(dw), _ptr(dlogits))
+
+
+# ---------------------------------------------------------------- layer norm
+
+def make_norm_config(T, d, eps=1e-5, dtype="bf16", param_dtype="f32", accumulate=False):
+    """A moe_norm_config_t (the calls check it and raise MoeError)."""
+    return L.MoeNormConfig(T=T, d=d, eps=float(eps), dtype=MOE_DTYPE[dtype], param_dtype=MOE_DTYPE[param_dtype],
+                           accumulate=int(bool(accumulate)))
+
+
+def norm_workspace_bytes(cfg):
+    return int(L.load().moe_norm_workspace_bytes(ctypes.byref(cfg)))
+
+
+def layer_norm(cfg, x, gain, bias, y, residual=None, total=None, mean=None, rstd=None, stream=None):
+    """y [T, d] = the norm of x + residual, total [T, d] = that sum (both or neither of residual and
+    total); mean, rstd [T] fp32 for the backward pass; gain, bias [d] may be None."""
+    dt, pt, shape = _TORCH[cfg.dtype], _TORCH[cfg.param_dtype], (cfg.T, cfg.d)
+    _want("x", x, dt, shape)
+    _want("gain", gain, pt, (cfg.d,), True)
+    _want("bias", bias, pt, (cfg.d,), True)
+    _want("y", y, dt, shape)
+    _want("residual", residual, dt, shape, total is None)
+    _want("total", total, dt, shape, residual is None)
+    _want("mean", mean, torch.float32, (cfg.T,), True)
+    _want("rstd", rstd, torch.float32, (cfg.T,), True)
+    gpu = _one_gpu(x, gain, bias, y, residual, total, mean, rstd)
+    _launch("moe_layer_norm", gpu, stream, L.load().moe_layer_norm, ctypes.byref(cfg), _ptr(x), _ptr(residual),
+            _ptr(gain), _ptr(bias), _ptr(total), _ptr(y), _ptr(mean), _ptr(rstd))
+
+
+def layer_norm_backward(cfg, dy, s, gain, mean, rstd, dx, dgain, dbias, ws, dtotal=None, stream=None):
+    """dx [T, d] (+ dtotal, the gradient that reaches the sum itself) and dgain, dbias [d] fp32 from dy and
+    the forward's s (its total, or x), mean and rstd. dx, dgain and dbias may each be None."""
+    dt, shape, f32 = _TORCH[cfg.dtype], (cfg.T, cfg.d), torch.float32
+    _want("dy", dy, dt, shape)
+    _want("s", s, dt, shape)
+    _want("gain", gain, _TORCH[cfg.param_dtype], (cfg.d,), True)
+    _want("mean", mean, f32, (cfg.T,))
+    _want("rstd", rstd, f32, (cfg.T,))
+    _want("dtotal", dtotal, dt, shape, True)
+    _want("dx", dx, dt, shape, True)
+    _want("dgain", dgain, f32, (cfg.d,), True)
+    _want("dbias", dbias, f32, (cfg.d,), True)
+    if dgain is not None or dbias is not None:
+        _room("ws", ws, norm_workspace_bytes(cfg))
+    gpu = _one_gpu(dy, s, gain, mean, rstd, dtotal, dx, dgain, dbias, ws)
+    _launch("moe_layer_norm_backward", gpu, stream, L.load().moe_layer_norm_backward, ctypes.byref(cfg), _ptr(dy),
+            _ptr(s), _ptr(gain), _ptr(mean), _ptr(rstd), _ptr(dtotal), _ptr(dx), _ptr(dgain), _ptr(dbias), _ptr(ws))
+
+
+# ---------------------------------------------------------------- orthogonalised updates (Muon)
+
+MUON_COEF = (3.4445, -4.7750, 2.0315)
+
+
+def make_muon_config(count, rows, cols, dtype="bf16", grad_dtype=None, precision=None, steps=5, coef=MUON_COEF,
+                     lr=0.02, momentum=0.95, weight_decay=0.0, scale=None, eps=1e-7, nesterov=True):
+    """A moe_muon_config_t (the calls check it and raise MoeError) for `count` matrices [rows, cols].
+    grad_dtype, precision: default, dtype. scale: default 0.2 sqrt(max(rows, cols)), which makes the
+    update's elements 0.2 lr in size."""
+    a, b, c = coef
+    return L.MoeMuonConfig(count=count, rows=rows, cols=cols, steps=steps, a=a, b=b, c=c, lr=lr, momentum=momentum,
+                           weight_decay=weight_decay,
+                           scale=0.2 * math.sqrt(max(rows, cols)) if scale is None else scale, eps=eps,
+                           nesterov=int(bool(nesterov)), dtype=MOE_DTYPE[dtype], grad_dtype=MOE_DTYPE[grad_dtype or dtype],
+                           precision=MOE_DTYPE[precision or dtype])
+
+
+def muon_workspace_bytes(cfg):
+    return int(L.load().moe_muon_workspace_bytes(ctypes.byref(cfg)))
+
+
+def orthogonalize(cfg, g, o, ws, stream=None):
+    """o [count, rows, cols] = g with the singular values of each matrix brought near 1. o may be g."""
+    shape = (cfg.count, cfg.rows, cfg.cols)
+    _want("g", g, _TORCH[cfg.grad_dtype], shape)
+    _want("o", o, _TORCH[cfg.dtype], shape)
+    _room("ws", ws, muon_workspace_bytes(cfg))
+    gpu = _one_gpu(g, o, ws)
+    _launch("moe_orthogonalize", gpu, stream, L.load().moe_orthogonalize, ctypes.byref(cfg), _ptr(g), _ptr(o), _ptr(ws))
+
+
+class Muon:
+    """moe_muon over a list of weight matrices. `tensors` is a list of dicts:
+
+      p, g           weights and their gradient (bf16 or fp32, contiguous): a matrix [rows, cols], or a
+                     stack of them [count, rows, cols] (an expert layer's W1 or W2), each on its own
+      master         fp32 copy that the step is taken on, or None
+      m              momentum, fp32 (left out: made, zeroed)
+      weight_decay, scale, precision   default: the class's; scale's is 0.2 sqrt(max(rows, cols)),
+                     precision's the weights' own type
+
+    step() takes one step on the current gradients and may be captured into a CUDA graph. The tensors are
+    bound here: refill the gradients in place. One workspace serves all of the tensors, one after another,
+    so two steps of one Muon must not run at once; two Muons have a workspace each."""
+
+    def __init__(self, tensors, lr=0.02, momentum=0.95, weight_decay=0.0, nesterov=True, steps=5, coef=MUON_COEF,
+                 eps=1e-7, scale=None, precision=None):
+        self.tensors = []
+        need, device = 0, "cpu"
+        for t in tensors:
+            t = dict(t)
+            p, g = t["p"], t["g"]
+            for k in ("p", "g"):
+                if t[k].dtype not in _KIND:
+                    raise ValueError(f"{k}: bf16 or fp32, got {t[k].dtype}")
+            if p.dim() not in (2, 3) or g.shape != p.shape or not p.is_contiguous() or not g.is_contiguous():
+                raise ValueError("p and g: contiguous, of one shape [rows, cols] or [count, rows, cols]")
+            if t.get("m") is None:
+                t["m"] = torch.zeros(p.shape, dtype=torch.float32, device=p.device)
+            for k in ("m", "master"):
+                t.setdefault(k, None)
+                if t[k] is not None and (t[k].dtype != torch.float32 or t[k].shape != p.shape or
+                                         not t[k].is_contiguous()):
+                    raise ValueError(f"{k}: want contiguous torch.float32 {tuple(p.shape)}")
+            rows, cols = p.shape[-2:]
+            count = p.shape[0] if p.dim() == 3 else 1
+            cfg = make_muon_config(count, rows, cols, steps=steps, coef=coef, lr=lr, momentum=momentum, eps=eps,
+                                   nesterov=nesterov, weight_decay=float(t.get("weight_decay", weight_decay)),
+                                   scale=t.get("scale", scale))
+            cfg.dtype, cfg.grad_dtype = _KIND[p.dtype], _KIND[g.dtype]
+            own = t.get("precision", precision)
+            cfg.precision = cfg.dtype if own is None else MOE_DTYPE[own]
+            t["cfg"] = cfg
+            if count > 0:
+                size = muon_workspace_bytes(cfg)
+                if size == 0:
+                    L.check("moe_muon", L.MOE_ERR_INVALID_ARG)
+                need, device = max(need, size), p.device
+            self.tensors.append(t)
+        self.ws = torch.empty(need, dtype=torch.uint8, device=device)
+        self.placed = None              # the GPU that the bound arrays have been seen to be on
+
+    def step(self, lr=None, grad_scale=None, stream=None):
+        """One step. lr, grad_scale: fp32 device tensors of one element, read when the step runs (they
+        replace the class's lr; multiply every gradient)."""
+        for what, t in (("lr", lr), ("grad_scale", grad_scale)):
+            if t is not None and (t.dtype != torch.float32 or t.numel() != 1):
+                raise ValueError(f"{what}: one fp32 element")
+        if not self.ws.numel():
+            return                      # nothing but empty stacks
+        if self.placed is None:
+            self.placed = _one_gpu(self.ws, *(t[k] for t in self.tensors for k in ("p", "g", "m", "master")))
+        gpu = _one_gpu(self.ws, lr, grad_scale)
+        for t in self.tensors:
+            _launch("moe_muon", gpu, stream, L.load().moe_muon, ctypes.byref(t["cfg"]), _ptr(t["p"]), _ptr(t["g"]),
+                    _ptr(t["master"]), _ptr(t["m"]), _ptr(lr), _ptr(grad_scale), _ptr(self.ws))
