@@ -30,6 +30,7 @@ constexpr int kStageBytes = 2 * kPartBytes;
 constexpr int kStages = 6;
 constexpr int kEpiWarps = 8;
 constexpr int kGemmThreads = 64 + 32 * kEpiWarps;
+constexpr int kSegment = 2;                          // k-blocks (of 64) to a partial sum, with SPLIT
 constexpr float kXScale = 2048.f, kAScale = 2048.f, kBScale = 1024.f;
 
 enum Op : int { kGram = 0, kPoly = 1, kApply = 2 };
@@ -37,7 +38,6 @@ enum Op : int { kGram = 0, kPoly = 1, kApply = 2 };
 struct MuonGemm {
     int count, M, N, K;           // per matrix: out [M, N], reduction K
     int m_tiles, n_tiles, tiles;  // tiles: of one matrix
-    int terms;                    // products of planes: 1, or 3
     const __half* aux;            // poly: A [planes][count][M, ld]
     int ld;
     float alpha, beta, diag;      // out = alpha acc + beta aux + diag on the diagonal
@@ -135,8 +135,12 @@ struct Staging {
 };
 
 // out = alpha P Q + beta aux + diag I on CTA pairs; the pipeline and its barriers are those of the grouped
-// expert GEMMs. Operand planes with SPLIT: lo hi, hi lo, then hi hi into the same sums; the small terms come
-// first, because the sums lose a part of a last bit with every addition, measured by what they hold.
+// expert GEMMs.
+//
+// SPLIT: the tensor cores cut off their sums at 24 bits with every addition, which over a long K is far more
+// than 22-bit operands leave. So K is taken in segments of kSegment k-blocks; each has a TMEM buffer to
+// itself, lo hi and hi lo before hi hi (what is cut off is measured by what the sum holds), and the epilogue
+// warps add the segments up in registers, rounding to nearest, while the other buffer fills.
 template <int OP, bool A_MN, bool B_MN, bool SPLIT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -179,7 +183,9 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
     cluster_sync();   // both CTAs' barriers exist before any remote arrive or complete_tx
     const uint32_t tmem_base = *tmem_slot;
     const int num_tiles = p.count * p.tiles;
-    const int kblocks = (p.K + BK - 1) / BK, steps = kblocks * p.terms;
+    const int kblocks = (p.K + BK - 1) / BK;
+    const int seg = SPLIT ? kSegment : kblocks;      // k-blocks to an accumulator
+    constexpr int TERMS = SPLIT ? 3 : 1;
 
     if (warp == 0) {
         if (lane == 0) {
@@ -189,8 +195,7 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
             for (int tile = cluster_id; tile < num_tiles && ok; tile += nclusters) {
                 const MuonTile t = decode_tile<SYM>(p, tile);
                 const int mr = t.m0 + (int)rank * kHalf, nh = t.n0 + (int)rank * kHalf;
-                int kb = 0, term = 0;
-                for (int q = 0; q < steps; ++q) {
+                for (int kb = 0, term = 0, first = 0; first < kblocks;) {
                     if (!mbar_wait(empty + s, ph ^ 1, p.err)) { ok = false; break; }
                     const uint32_t sa = smem_u32(smem + s * kStageBytes), sb = sa + kPartBytes;
                     const uint32_t fb = map_to_rank(smem_u32(full + s), 0);
@@ -213,7 +218,13 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
                     }
                     ++issued;
                     if (++s == kStages) { s = 0; ph ^= 1; }
-                    if (++kb == kblocks) { kb = 0; ++term; }
+                    if (++kb == min(first + seg, kblocks)) {
+                        if (++term == TERMS) {
+                            term = 0;
+                            first += seg;
+                        }
+                        kb = first;
+                    }
                 }
             }
             if (!ok) {
@@ -235,13 +246,15 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
             constexpr uint32_t STAGE_STEP = kStageBytes >> 4;
             uint32_t s = 0, ph = 0, soff = 0, tl = 0;
             bool ok = true;
-            for (int tile = cluster_id; tile < num_tiles && ok; tile += nclusters) {
+            for (int tile = cluster_id; tile < num_tiles && ok; tile += nclusters)
+            for (int first = 0; first < kblocks && ok; first += seg) {
                 const int buf = tl & 1;
                 const uint32_t aph = (tl >> 1) & 1;
                 ++tl;
                 if (!mbar_wait(tempty + buf, aph ^ 1, p.err)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + buf * BN;
+                const int steps = TERMS * min(seg, kblocks - first);
                 for (int q = 0; q < steps; ++q) {
                     if (!mbar_wait(full + s, ph, p.err)) { ok = false; break; }
                     tc_fence_after();
@@ -266,20 +279,15 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
         uint32_t tl = 0;
         for (int tile = cluster_id; tile < num_tiles; tile += nclusters) {
             const MuonTile t = decode_tile<SYM>(p, tile);
-            const int buf = tl & 1;
-            const uint32_t aph = (tl >> 1) & 1;
-            ++tl;
             const int y = t.m0 + (int)rank * kHalf + quarter * 32;    // the warp's first row
             const int x0 = t.n0 + half * (BN / 2);                    // its first column
             const bool turn = SYM && t.m0 != t.n0;
-            if (!mbar_wait(tfull + buf, aph, p.err)) break;
-            tc_fence_after();
-            const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + buf * BN + half * (BN / 2);
-            for (int c = 0; c < BN / 2; c += 32) {
+            const uint32_t toff = ((uint32_t)(quarter * 32) << 16) + half * (BN / 2);
+            bool ok = true;
+            // one box of 32 rows x 32 columns from column x0 + c on, out of its sums
+            auto box = [&](int c, const uint32_t (&acc)[32], auto ready) {
                 const int x = x0 + c;
-                if (x >= p.N || y >= p.M) break;
-                uint32_t acc[32];
-                tmem_ld32(taddr + c, acc);
+                if (x >= p.N || y >= p.M) return;
                 float v[32];
                 if (OP == kPoly) {
                     // A of the same box: the lane's row, 64 bytes
@@ -303,7 +311,7 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
                         }
                     }
                 }
-                tmem_ld_wait_regs(acc);
+                ready();
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                     const float a = p.alpha * __uint_as_float(acc[i]);
@@ -328,10 +336,52 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
                     st.store(lane, h, &tmO, x, y, t.z + p.count);
                     if (turn) st.store_turned(lane, h, &tmO, y, x, t.z + p.count);
                 }
+            };
+            auto wait_full = [&]() {
+                const bool got = mbar_wait(tfull + (tl & 1), (tl >> 1) & 1, p.err);
+                tc_fence_after();
+                return got;
+            };
+            auto free_buffer = [&]() {
+                tc_fence_before();
+                if (leader) mbar_arrive(tempty + (tl & 1));
+                else mbar_arrive_cluster(tempty_leader[tl & 1]);
+                ++tl;
+            };
+            if constexpr (SPLIT) {
+                uint32_t sum[BN / 64][32];
+#pragma unroll
+                for (int c = 0; c < BN / 64; ++c)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) sum[c][i] = 0;
+                for (int first = 0; first < kblocks; first += seg) {
+                    if (!wait_full()) { ok = false; break; }
+                    const uint32_t taddr = tmem_base + toff + (tl & 1) * BN;
+#pragma unroll
+                    for (int c = 0; c < BN / 64; ++c) {
+                        uint32_t acc[32];
+                        tmem_ld32(taddr + 32 * c, acc);
+                        tmem_ld_wait_regs(acc);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            sum[c][i] = __float_as_uint(__uint_as_float(sum[c][i]) + __uint_as_float(acc[i]));
+                    }
+                    free_buffer();
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int c = 0; c < BN / 64; ++c) box(32 * c, sum[c], [] {});
+            } else {
+                if (!wait_full()) break;
+                const uint32_t taddr = tmem_base + toff + (tl & 1) * BN;
+                for (int c = 0; c < BN / 2; c += 32) {
+                    if (x0 + c >= p.N || y >= p.M) break;
+                    uint32_t acc[32];
+                    tmem_ld32(taddr + c, acc);
+                    box(c, acc, [&] { tmem_ld_wait_regs(acc); });
+                }
+                free_buffer();
             }
-            tc_fence_before();
-            if (leader) mbar_arrive(tempty + buf);
-            else mbar_arrive_cluster(tempty_leader[buf]);
             if (*s_fail) break;
         }
         if (lane == 0) bulk_wait_all();
@@ -565,6 +615,348 @@ __global__ void __launch_bounds__(256) muon_finish_kernel(const MuonFinish a) {
     }
 }
 
+// ---------------------------------------------------------------- small matrices, in one launch
+// A matrix of 128 at most on its smaller side and 1024 on the other stays in shared memory from the
+// gradient to the update: a cluster of CTAs holds a slice of 128 along the longer side each. Of a step only
+// the Gram matrix concerns all of them: each multiplies its slice with itself, the partial sums stand in
+// fp32 in its shared memory, each CTA adds up a part of the rows over all CTAs, in their order, and
+// writes the fp16 sums into every CTA. B is then computed by each for itself, and B X is each one's own
+// slice. So a step costs three small products and two cluster barriers instead of three launches that
+// read and write global memory.
+//
+// Slices and A lie as the tensor cores read 128-byte swizzled tiles: blocks of 64 columns, each of 128 rows
+// of 128 bytes. One such block is read along either side: as K-major rows, or as MN-major columns, so the
+// products X X^T, X^T X, B X and X B need no copy that is turned.
+constexpr int kSide = 128;
+constexpr int kPlaneBytes = kSide * kSide * 2;       // one fp16 part of a slice, or of A
+constexpr int kSmallThreads = 256;
+constexpr int kMaxCluster = 8;
+constexpr int kBatch = 16;                           // elements in flight to a thread, in and out
+
+struct MuonSmall {
+    MuonPrep pre;
+    MuonFinish fin;
+    int steps, cluster, side;
+    bool g_bf16, p_bf16;
+    float a, b, c;
+    int* err;
+};
+
+// Byte of the 16-byte unit u (0..15) of a row.
+__device__ __forceinline__ uint32_t unit_at(int row, int u) {
+    return (uint32_t)((u >> 3) * (kSide * 128) + row * 128 + (((u & 7) ^ (row & 7)) << 4));
+}
+// fp32 partial sums: row of 32 units of 16 bytes, turned by the row so that rows do not share banks.
+__device__ __forceinline__ uint32_t sum_at(int row, int u) { return (uint32_t)(row * 512 + ((u ^ (row & 31)) << 4)); }
+
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t lo, uint32_t hi) {
+    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(lo), "r"(hi) : "memory");
+}
+__device__ __forceinline__ void fence_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+template <bool SPLIT, bool TALL>
+__global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const MuonSmall a) {
+    constexpr int PL = SPLIT ? 2 : 1;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sX = smem;
+    uint8_t* sA = sX + PL * kPlaneBytes;
+    float* sP = reinterpret_cast<float*>(sA + PL * kPlaneBytes);
+    __shared__ uint64_t s_bar;
+    __shared__ uint32_t s_tmem;
+    __shared__ float s_warp[kSmallThreads / 32];
+    __shared__ float s_sum[kMaxCluster];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int CS = a.cluster, rank = blockIdx.x % CS, z = blockIdx.x / CS;
+    const int rows = a.pre.rows, cols = a.pre.cols;
+    // the slice: rows r0 .. r0 + nr and columns c0 .. c0 + nc of the matrix
+    const int r0 = TALL ? rank * kSide : 0, c0 = TALL ? 0 : rank * kSide;
+    const int nr = min(rows - r0, kSide), nc = min(cols - c0, kSide);
+    const int64_t base = (int64_t)z * a.pre.n;
+
+    if (tid == 0) {
+        mbar_init(&s_bar, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) tmem_alloc(&s_tmem, kSide);
+    cluster_sync();      // every CTA runs before one writes into another
+    pdl_wait();
+
+    // ---- u = g (+ momentum) into sP, and its sum of squares
+    const float gs = a.pre.grad_scale ? __ldg(a.pre.grad_scale) : 1.f;
+    const float mu = a.pre.momentum;
+    float sum = 0.f;
+    for (int e0 = tid; e0 < kSide * kSide; e0 += kSmallThreads * kBatch) {
+        float u[kBatch], m[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int e = e0 + i * kSmallThreads, r = e >> 7, c = e & 127;
+            const int64_t at = base + (int64_t)(r0 + r) * cols + c0 + c;
+            const bool in = r < nr && c < nc;
+            u[i] = !in ? 0.f : a.g_bf16 ? ld_f(static_cast<const __nv_bfloat16*>(a.pre.g) + at)
+                                        : static_cast<const float*>(a.pre.g)[at];
+            m[i] = in && a.pre.m ? a.pre.m[at] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int e = e0 + i * kSmallThreads, r = e >> 7, c = e & 127;
+            if (a.pre.m) {
+                u[i] *= gs;
+                m[i] = fmaf(mu, m[i], u[i]);
+                if (r < nr && c < nc) a.pre.m[base + (int64_t)(r0 + r) * cols + c0 + c] = m[i];
+                u[i] = a.pre.nesterov ? fmaf(mu, m[i], u[i]) : m[i];
+            }
+            sP[e] = u[i];
+            sum = fmaf(u[i], u[i], sum);
+        }
+    }
+    sum = warp_sum(sum);
+    if (lane == 0) s_warp[warp] = sum;
+    __syncthreads();
+    if (tid < CS) {
+        float all = 0.f;
+        for (int w = 0; w < kSmallThreads / 32; ++w) all += s_warp[w];
+        // every CTA's sum into every CTA
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(map_to_rank(smem_u32(s_sum + rank), (uint32_t)tid)), "f"(all)
+                     : "memory");
+    }
+    cluster_sync();
+    float total = 0.f;
+    for (int q = 0; q < CS; ++q) total += s_sum[q];
+    const float scale = total < INFINITY ? kXScale / (sqrtf(total) + a.pre.eps) : NAN;
+    for (int e = tid; e < kSide * kSide / 8; e += kSmallThreads) {
+        const int r = e >> 4, u = e & 15;
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float x0 = sP[r * kSide + 8 * u + 2 * i] * scale, x1 = sP[r * kSide + 8 * u + 2 * i + 1] * scale;
+            hi[i] = pack_half2(x0, x1);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi[i]));
+            lo[i] = pack_half2(x0 - f.x, x1 - f.y);
+        }
+        *reinterpret_cast<uint4*>(sX + unit_at(r, u)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        if (SPLIT) *reinterpret_cast<uint4*>(sX + kPlaneBytes + unit_at(r, u)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    fence_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+
+    // One product of 128 x 128 into TMEM by thread 0, waited for by all. k: length of the reduction.
+    bool ok = true;
+    uint32_t phase = 0;
+    auto product = [&](const uint8_t* pa, bool a_mn, const uint8_t* pb, bool b_mn, int k) {
+        if (tid == 0 && ok) {
+            fence_async_all();
+            const uint32_t idesc = idesc_fp16(kSide, kSide, a_mn, b_mn);
+            bool first = true;
+            for (int term = SPLIT ? 0 : 2; term < 3; ++term) {
+                const uint32_t ba = smem_u32(pa) + (term == 0 ? kPlaneBytes : 0);
+                const uint32_t bb = smem_u32(pb) + (term == 1 ? kPlaneBytes : 0);
+                for (int q = 0; q < (k + 15) / 16; ++q) {
+                    const uint32_t major = (uint32_t)((q >> 2) * (kSide * 128) + (q & 3) * 32), minor = (uint32_t)q * 2048;
+                    const uint64_t da = a_mn ? make_desc(ba + minor, kSide * 128, 1024) : make_desc(ba + major, 16, 1024);
+                    const uint64_t db = b_mn ? make_desc(bb + minor, kSide * 128, 1024) : make_desc(bb + major, 16, 1024);
+                    tc_mma(tmem, da, db, idesc, first ? 0u : 1u);
+                    first = false;
+                }
+            }
+            tc_commit(&s_bar);
+        }
+        if (ok) ok = mbar_wait(&s_bar, phase, a.err);
+        phase ^= 1;
+        tc_fence_after();
+    };
+    // Each thread has a row of the product (TMEM lane) and half of its columns.
+    const int row = (warp & 3) * 32 + lane, half = warp >> 2;
+    const uint32_t taddr = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * 64;
+    // fp16 parts of 8 values to the unit u of the thread's row.
+    auto put8 = [&](uint8_t* to, int u, const float* v) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            hi[i] = pack_half2(v[2 * i], v[2 * i + 1]);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi[i]));
+            lo[i] = pack_half2(v[2 * i] - f.x, v[2 * i + 1] - f.y);
+        }
+        *reinterpret_cast<uint4*>(to + unit_at(row, u)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        if (SPLIT) *reinterpret_cast<uint4*>(to + kPlaneBytes + unit_at(row, u)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    };
+    auto ready = [&]() {     // generic writes of this CTA are there for the next product, and TMEM is read
+        fence_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+    };
+
+    for (int step = 0; step < a.steps; ++step) {
+        // ---- gram
+        product(sX, TALL, sX, TALL, TALL ? nr : nc);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t acc[32];
+            tmem_ld32(taddr + 32 * h, acc);
+            tmem_ld_wait_regs(acc);
+            float v[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(acc[i]) * (kAScale / (kXScale * kXScale));
+            if (CS == 1) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) put8(sA, half * 8 + h * 4 + j, v + 8 * j);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    *reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(sP) + sum_at(row, half * 16 + h * 8 + j)) =
+                        make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            }
+        }
+        if (CS > 1) {
+            tc_fence_before();
+            cluster_sync();      // partial sums of all CTAs are there
+            const int per = (kSide + CS - 1) / CS, lo_row = rank * per, hi_row = min(lo_row + per, kSide);
+            for (int e = tid; e < (hi_row - lo_row) * 32; e += kSmallThreads) {
+                const int r = lo_row + (e >> 5), u = e & 31;
+                const uint32_t from = smem_u32(sP) + sum_at(r, u);
+                float4 part[kMaxCluster];
+#pragma unroll
+                for (int q = 0; q < kMaxCluster; ++q)
+                    if (q < CS) part[q] = ld_cluster(map_to_rank(from, (uint32_t)q));
+                float4 v = part[0];
+#pragma unroll
+                for (int q = 1; q < kMaxCluster; ++q)
+                    if (q < CS) { v.x += part[q].x; v.y += part[q].y; v.z += part[q].z; v.w += part[q].w; }
+                const uint32_t h0 = pack_half2(v.x, v.y), h1 = pack_half2(v.z, v.w);
+                const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
+                const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+                const uint32_t l0 = pack_half2(v.x - f0.x, v.y - f0.y), l1 = pack_half2(v.z - f1.x, v.w - f1.y);
+                const uint32_t to = smem_u32(sA) + unit_at(r, u >> 1) + (u & 1) * 8;
+                for (int q = 0; q < CS; ++q) {
+                    st_cluster(map_to_rank(to, (uint32_t)q), h0, h1);
+                    if (SPLIT) st_cluster(map_to_rank(to + kPlaneBytes, (uint32_t)q), l0, l1);
+                }
+            }
+            fence_async_all();
+            cluster_sync();      // A is whole in every CTA, and every CTA has read its partial sums
+            tc_fence_after();
+            fence_async_all();
+            __syncthreads();
+        } else {
+            ready();
+        }
+        // ---- poly: B = a I + b A + c A A in the place of A
+        product(sA, false, sA, false, a.side);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t acc[32];
+            tmem_ld32(taddr + 32 * h, acc);
+            float v[32];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t at = unit_at(row, half * 8 + h * 4 + j);
+                const uint4 q4 = *reinterpret_cast<const uint4*>(sA + at);
+                const __half2* q = reinterpret_cast<const __half2*>(&q4);
+                uint4 l4 = make_uint4(0, 0, 0, 0);
+                if (SPLIT) l4 = *reinterpret_cast<const uint4*>(sA + kPlaneBytes + at);
+                const __half2* l = reinterpret_cast<const __half2*>(&l4);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = __half22float2(q[i]), g = __half22float2(l[i]);
+                    v[8 * j + 2 * i] = f.x + g.x;
+                    v[8 * j + 2 * i + 1] = f.y + g.y;
+                }
+            }
+            tmem_ld_wait_regs(acc);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                v[i] = fmaf(a.b * (kBScale / kAScale), v[i],
+                            a.c * (kBScale / (kAScale * kAScale)) * __uint_as_float(acc[i]));
+                if (half * 64 + h * 32 + i == row) v[i] += a.a * kBScale;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) put8(sA, half * 8 + h * 4 + j, v + 8 * j);
+        }
+        ready();
+        // ---- apply
+        if (TALL) product(sX, false, sA, false, a.side);
+        else product(sA, false, sX, true, a.side);
+        const bool last = step + 1 == a.steps;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t acc[32];
+            tmem_ld32(taddr + 32 * h, acc);
+            tmem_ld_wait_regs(acc);
+            float v[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(acc[i]) * (1.f / kBScale);
+            if (last) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    *reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(sP) + sum_at(row, half * 16 + h * 8 + j)) =
+                        make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) put8(sX, half * 8 + h * 4 + j, v + 8 * j);
+            }
+        }
+        ready();
+    }
+
+    // ---- o, or the step on the weights
+    const float lr = a.fin.lr_dev ? __ldg(a.fin.lr_dev) : a.fin.lr;
+    const float lose = lr * a.fin.decay, move = lr * a.fin.scale;
+    for (int e0 = tid; e0 < kSide * kSide; e0 += kSmallThreads * kBatch) {
+        float p[kBatch];
+        if (a.fin.step) {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int e = e0 + i * kSmallThreads, r = e >> 7, c = e & 127;
+                const int64_t at = base + (int64_t)(r0 + r) * cols + c0 + c;
+                p[i] = r >= nr || c >= nc ? 0.f : a.fin.master ? a.fin.master[at]
+                       : a.p_bf16 ? ld_f(static_cast<const __nv_bfloat16*>(a.fin.out) + at)
+                                  : static_cast<const float*>(a.fin.out)[at];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int e = e0 + i * kSmallThreads, r = e >> 7, c = e & 127;
+            if (r >= nr || c >= nc) continue;
+            const int64_t at = base + (int64_t)(r0 + r) * cols + c0 + c;
+            float x;
+            if (a.steps) {
+                x = *reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(sP) + sum_at(r, c >> 2) + (c & 3) * 4);
+            } else {
+                const uint32_t b = unit_at(r, c >> 3) + (c & 7) * 2;
+                x = __half2float(*reinterpret_cast<const __half*>(sX + b));
+                if (SPLIT) x += __half2float(*reinterpret_cast<const __half*>(sX + kPlaneBytes + b));
+            }
+            x *= 1.f / kXScale;
+            if (a.fin.step) {
+                x = fmaf(-move, x, fmaf(-lose, p[i], p[i]));
+                if (a.fin.master) a.fin.master[at] = x;
+            }
+            if (a.p_bf16) st_f(static_cast<__nv_bfloat16*>(a.fin.out) + at, x);
+            else static_cast<float*>(a.fin.out)[at] = x;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();      // no CTA leaves while another may still write into it
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kSide);
+    }
+}
+
+constexpr size_t small_smem(bool split) { return 1024 + (split ? 4 : 2) * (size_t)kPlaneBytes + kSide * kSide * 4; }
+static_assert(small_smem(true) <= 227 * 1024 - 1024, "shared memory per CTA");
+
 // ---------------------------------------------------------------- host
 moe_status_t check_muon(const moe_muon_config_t* c) {
     if (!c) return MOE_ERR_INVALID_ARG;
@@ -641,7 +1033,6 @@ cudaError_t launch_gemm(MuonGemm p, int planes, const Operand& a, const Operand&
     p.m_tiles = ceil_div(p.M, kTile);
     p.n_tiles = ceil_div(p.N, kTile);
     p.tiles = SYM ? p.m_tiles * (p.m_tiles + 1) / 2 : p.m_tiles * p.n_tiles;
-    p.terms = planes == 2 ? 3 : 1;
     p.err = device_error_word();
     const uint64_t outer = (uint64_t)planes * p.count;
     CUtensorMap ta, tb, to;
@@ -685,6 +1076,50 @@ cudaError_t launch_finish(const MuonFinish& a, bool split, cudaStream_t s) {
     return e;
 }
 
+// Whether a matrix fits a cluster of CTAs that keep it in shared memory. Measured against the tiled products
+// at the border, 128 x 1024 fp32, one matrix: see there.
+bool small_matrix(const moe_muon_config_t& c) {
+    return std::min(c.rows, c.cols) <= kSide && std::max(c.rows, c.cols) <= kSide * kMaxCluster;
+}
+
+cudaError_t launch_small(const moe_muon_config_t& c, const MuonPrep& pre, const MuonFinish& fin, bool split,
+                         cudaStream_t s) {
+    MuonSmall a{};
+    a.pre = pre;
+    a.fin = fin;
+    a.steps = c.steps;
+    a.side = std::min(c.rows, c.cols);
+    a.cluster = ceil_div(std::max(c.rows, c.cols), kSide);
+    a.g_bf16 = c.grad_dtype == MOE_BF16;
+    a.p_bf16 = c.dtype == MOE_BF16;
+    a.a = (float)c.a;
+    a.b = (float)c.b;
+    a.c = (float)c.c;
+    a.err = device_error_word();
+    const bool tall = c.rows > c.cols;
+    auto kern = split ? (tall ? muon_small_kernel<true, true> : muon_small_kernel<true, false>)
+                      : (tall ? muon_small_kernel<false, true> : muon_small_kernel<false, false>);
+    const size_t smem = small_smem(split);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(c.count * a.cluster));
+    cfg.blockDim = dim3(kSmallThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)a.cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    e = launch_ex(cfg, kern, a);
+    count_launch();
+    return e;
+}
+
 cudaError_t launch_muon(const moe_muon_config_t& c, const void* g, float* m, const float* grad_scale, MuonFinish f,
                         void* ws, cudaStream_t s) {
     MuonScratch b;
@@ -692,6 +1127,16 @@ cudaError_t launch_muon(const moe_muon_config_t& c, const void* g, float* m, con
     const bool split = b.planes == 2, tall = c.rows > c.cols;
     MuonPrep pre{g, m, grad_scale, b.sums, b.X[0], (int64_t)c.rows * c.cols, b.chunk, b.chunks, c.count, c.rows, c.cols,
                  b.ld, (float)c.momentum, (float)c.eps, c.nesterov};
+    f.n = pre.n;
+    f.total = pre.n * c.count;
+    f.count = c.count;
+    f.rows = c.rows;
+    f.cols = c.cols;
+    f.ld = b.ld;
+    f.lr = (float)c.lr;
+    f.decay = (float)c.weight_decay;
+    f.scale = (float)c.scale;
+    if (small_matrix(c)) return launch_small(c, pre, f, split, s);
     cudaError_t e = c.grad_dtype == MOE_BF16 ? launch_prep<__nv_bfloat16>(pre, split, s)
                                              : launch_prep<float>(pre, split, s);
     if (e != cudaSuccess) return e;
@@ -723,15 +1168,6 @@ cudaError_t launch_muon(const moe_muon_config_t& c, const void* g, float* m, con
         if (e != cudaSuccess) return e;
     }
     f.X = b.X[at];
-    f.n = pre.n;
-    f.total = pre.n * c.count;
-    f.count = c.count;
-    f.rows = c.rows;
-    f.cols = c.cols;
-    f.ld = b.ld;
-    f.lr = (float)c.lr;
-    f.decay = (float)c.weight_decay;
-    f.scale = (float)c.scale;
     return c.dtype == MOE_BF16 ? launch_finish<__nv_bfloat16>(f, split, s) : launch_finish<float>(f, split, s);
 }
 
