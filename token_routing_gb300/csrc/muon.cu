@@ -14,6 +14,7 @@
 // 2^10, so that what is far smaller than the largest elements keeps its bits too. In MOE_F32 precision an
 // operand is two fp16 planes, x = hi + lo, and a product takes hi hi + hi lo + lo hi.
 #include <cmath>
+#include <type_traits>
 
 #include "tc_gemm_common.cuh"
 #include "tc_pair_ptx.cuh"
@@ -618,47 +619,92 @@ __global__ void __launch_bounds__(256) muon_finish_kernel(const MuonFinish a) {
 // ---------------------------------------------------------------- small matrices, in one launch
 // A matrix of 128 at most on its smaller side and 1024 on the other stays in shared memory from the
 // gradient to the update: a cluster of CTAs holds a slice of 128 along the longer side each. Of a step only
-// the Gram matrix concerns all of them: each multiplies its slice with itself, the partial sums stand in
-// fp32 in its shared memory, each CTA adds up a part of the rows over all CTAs, in their order, and
-// writes the fp16 sums into every CTA. B is then computed by each for itself, and B X is each one's own
-// slice. So a step costs three small products and two cluster barriers instead of three launches that
-// read and write global memory.
+// the Gram matrix concerns all of them: each multiplies its slice with itself and sends every CTA its part of
+// the rows of the fp32 sums; each adds up its rows over all CTAs, in their order, and sends them, in fp16
+// parts, to all. B is then computed by each for itself, and B X is each one's own slice.
 //
 // Slices and A lie as the tensor cores read 128-byte swizzled tiles: blocks of 64 columns, each of 128 rows
 // of 128 bytes. One such block is read along either side: as K-major rows, or as MN-major columns, so the
-// products X X^T, X^T X, B X and X B need no copy that is turned.
+// products X X^T, X^T X, B X and X B need no copy that is turned. The fp32 sums lie in four such blocks (of 32
+// columns), so that the rows of one CTA take the same bytes as fp32 sums and as fp16 parts: a CTA that sends
+// its rows of A overwrites only what it has received.
+//
+// The exchanges wait for no cluster barrier (one that they arrive on is waited for a product later, before B
+// takes the place of A, which copies may still read until then). Sums arrive in a buffer of their own, which is read before the rows
+// of A that it makes are sent, and no CTA sends sums again before it has all rows of A; rows of A arrive where
+// their sums stood, which the sender has.
 constexpr int kSide = 128;
 constexpr int kPlaneBytes = kSide * kSide * 2;       // one fp16 part of a slice, or of A
+constexpr int kBlockBytes = kSide * 128;             // 128 rows of 128 bytes
 constexpr int kSmallThreads = 256;
 constexpr int kMaxCluster = 8;
-constexpr int kBatch = 16;                           // elements in flight to a thread, in and out
+constexpr int kUnits = kSide * kSide / 8 / kSmallThreads;   // units of 8 elements to a thread
+constexpr int kRecvBytes = 68608;                    // sums of n CTAs' rows: n ceil(128 / n) 512, at most for n = 7
 
 struct MuonSmall {
     MuonPrep pre;
     MuonFinish fin;
     int steps, cluster, side;
-    bool g_bf16, p_bf16;
+    bool g_bf16, p_bf16, vec;     // vec: rows are whole units of 8 elements
     float a, b, c;
     int* err;
 };
 
-// Byte of the 16-byte unit u (0..15) of a row.
+// Byte of the 16-byte unit u of a row: fp16 parts have 16, fp32 sums 32.
 __device__ __forceinline__ uint32_t unit_at(int row, int u) {
-    return (uint32_t)((u >> 3) * (kSide * 128) + row * 128 + (((u & 7) ^ (row & 7)) << 4));
+    return (uint32_t)((u >> 3) * kBlockBytes + row * 128 + (((u & 7) ^ (row & 7)) << 4));
 }
-// fp32 partial sums: row of 32 units of 16 bytes, turned by the row so that rows do not share banks.
-__device__ __forceinline__ uint32_t sum_at(int row, int u) { return (uint32_t)(row * 512 + ((u ^ (row & 31)) << 4)); }
-
-__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr) : "memory");
-    return v;
+// `bytes` of this CTA's shared memory to another's, counted on a barrier there.
+__device__ __forceinline__ void send(uint32_t to, uint32_t from, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(to), "r"(from), "r"(bytes), "r"(bar) : "memory");
 }
-__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t lo, uint32_t hi) {
-    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(lo), "r"(hi) : "memory");
+// 8 elements at p (fp32 or bf16) of which the first n exist.
+__device__ __forceinline__ void load_unit(const void* p, int64_t at, bool bf16, bool vec, int n, float (&f)[8]) {
+    if (vec && n == 8) {
+        if (bf16) {
+            const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at);
+            unpack16<__nv_bfloat16>(u, f);
+        } else {
+            *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+            *reinterpret_cast<float4*>(f + 4) = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at + 4);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            f[i] = i >= n ? 0.f : bf16 ? Elem<__nv_bfloat16>::to_f(static_cast<const __nv_bfloat16*>(p)[at + i])
+                                       : static_cast<const float*>(p)[at + i];
+    }
 }
-__device__ __forceinline__ void fence_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+__device__ __forceinline__ void store_unit(void* p, int64_t at, bool bf16, bool vec, int n, const float (&f)[8]) {
+    if (vec && n == 8) {
+        if (bf16) {
+            store16(static_cast<__nv_bfloat16*>(p) + at, f);
+        } else {
+            store16(static_cast<float*>(p) + at, f);
+            store16(static_cast<float*>(p) + at + 4, f + 4);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) {
+                if (bf16) st_f(static_cast<__nv_bfloat16*>(p) + at + i, f[i]);
+                else static_cast<float*>(p)[at + i] = f[i];
+            }
+    }
+}
+// 8 values in fp16 parts.
+__device__ __forceinline__ void split8(const float* v, uint4& hi, uint4& lo) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        h[i] = pack_half2(v[2 * i], v[2 * i + 1]);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+        l[i] = pack_half2(v[2 * i] - f.x, v[2 * i + 1] - f.y);
+    }
+    hi = make_uint4(h[0], h[1], h[2], h[3]);
+    lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
 
 template <bool SPLIT, bool TALL>
 __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const MuonSmall a) {
@@ -666,56 +712,67 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sX = smem;
-    uint8_t* sA = sX + PL * kPlaneBytes;
-    float* sP = reinterpret_cast<float*>(sA + PL * kPlaneBytes);
-    __shared__ uint64_t s_bar;
+    uint8_t* sA = sX + PL * kPlaneBytes;          // fp32 sums, A, B, and the result
+    uint8_t* sR = sA + 4 * kBlockBytes;           // sums of the CTA's rows from the others
+    __shared__ uint64_t s_bar, s_sums, s_rows;    // products; sums, rows of A that have arrived
     __shared__ uint32_t s_tmem;
     __shared__ float s_warp[kSmallThreads / 32];
-    __shared__ float s_sum[kMaxCluster];
+    __shared__ float s_sq[kMaxCluster];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int CS = a.cluster, rank = blockIdx.x % CS, z = blockIdx.x / CS;
     const int rows = a.pre.rows, cols = a.pre.cols;
     // the slice: rows r0 .. r0 + nr and columns c0 .. c0 + nc of the matrix
     const int r0 = TALL ? rank * kSide : 0, c0 = TALL ? 0 : rank * kSide;
     const int nr = min(rows - r0, kSide), nc = min(cols - c0, kSide);
-    const int64_t base = (int64_t)z * a.pre.n;
+    const int64_t base = (int64_t)z * a.pre.n + (int64_t)r0 * cols + c0;
 
     if (tid == 0) {
         mbar_init(&s_bar, 1);
+        mbar_init(&s_sums, 1);
+        mbar_init(&s_rows, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     if (warp == 0) tmem_alloc(&s_tmem, kSide);
-    cluster_sync();      // every CTA runs before one writes into another
+    cluster_sync();      // every CTA runs, with its barriers, before one writes into another
     pdl_wait();
 
-    // ---- u = g (+ momentum) into sP, and its sum of squares
+    // ---- u = g (+ momentum) in registers, and its sum of squares
     const float gs = a.pre.grad_scale ? __ldg(a.pre.grad_scale) : 1.f;
     const float mu = a.pre.momentum;
+    float u[kUnits][8];
     float sum = 0.f;
-    for (int e0 = tid; e0 < kSide * kSide; e0 += kSmallThreads * kBatch) {
-        float u[kBatch], m[kBatch];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int e = e0 + i * kSmallThreads, r = e >> 7, c = e & 127;
-            const int64_t at = base + (int64_t)(r0 + r) * cols + c0 + c;
-            const bool in = r < nr && c < nc;
-            u[i] = !in ? 0.f : a.g_bf16 ? ld_f(static_cast<const __nv_bfloat16*>(a.pre.g) + at)
-                                        : static_cast<const float*>(a.pre.g)[at];
-            m[i] = in && a.pre.m ? a.pre.m[at] : 0.f;
-        }
+    for (int i = 0; i < kUnits; ++i) {
+        const int e = tid + i * kSmallThreads, r = e >> 4, c = (e & 15) * 8;
+        load_unit(a.pre.g, base + (int64_t)r * cols + c, a.g_bf16, a.vec, r < nr ? min(nc - c, 8) : 0, u[i]);
+    }
+    if (a.pre.m) {
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int e = e0 + i * kSmallThreads, r = e >> 7, c = e & 127;
-            if (a.pre.m) {
-                u[i] *= gs;
-                m[i] = fmaf(mu, m[i], u[i]);
-                if (r < nr && c < nc) a.pre.m[base + (int64_t)(r0 + r) * cols + c0 + c] = m[i];
-                u[i] = a.pre.nesterov ? fmaf(mu, m[i], u[i]) : m[i];
+        for (int h = 0; h < kUnits; h += kUnits / 2) {
+            float m[kUnits / 2][8];
+#pragma unroll
+            for (int i = 0; i < kUnits / 2; ++i) {
+                const int e = tid + (h + i) * kSmallThreads, r = e >> 4, c = (e & 15) * 8;
+                load_unit(a.pre.m, base + (int64_t)r * cols + c, false, a.vec, r < nr ? min(nc - c, 8) : 0, m[i]);
             }
-            sP[e] = u[i];
-            sum = fmaf(u[i], u[i], sum);
+#pragma unroll
+            for (int i = 0; i < kUnits / 2; ++i) {
+                const int e = tid + (h + i) * kSmallThreads, r = e >> 4, c = (e & 15) * 8;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const float g = u[h + i][q] * gs;
+                    m[i][q] = fmaf(mu, m[i][q], g);
+                    u[h + i][q] = a.pre.nesterov ? fmaf(mu, m[i][q], g) : m[i][q];
+                }
+                if (r < nr) store_unit(a.pre.m, base + (int64_t)r * cols + c, false, a.vec, min(nc - c, 8), m[i]);
+            }
         }
     }
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) sum = fmaf(u[i][q], u[i][q], sum);
     sum = warp_sum(sum);
     if (lane == 0) s_warp[warp] = sum;
     __syncthreads();
@@ -723,25 +780,22 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
         float all = 0.f;
         for (int w = 0; w < kSmallThreads / 32; ++w) all += s_warp[w];
         // every CTA's sum into every CTA
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(map_to_rank(smem_u32(s_sum + rank), (uint32_t)tid)), "f"(all)
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(map_to_rank(smem_u32(s_sq + rank), (uint32_t)tid)), "f"(all)
                      : "memory");
     }
     cluster_sync();
     float total = 0.f;
-    for (int q = 0; q < CS; ++q) total += s_sum[q];
+    for (int q = 0; q < CS; ++q) total += s_sq[q];
     const float scale = total < INFINITY ? kXScale / (sqrtf(total) + a.pre.eps) : NAN;
-    for (int e = tid; e < kSide * kSide / 8; e += kSmallThreads) {
-        const int r = e >> 4, u = e & 15;
-        uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float x0 = sP[r * kSide + 8 * u + 2 * i] * scale, x1 = sP[r * kSide + 8 * u + 2 * i + 1] * scale;
-            hi[i] = pack_half2(x0, x1);
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi[i]));
-            lo[i] = pack_half2(x0 - f.x, x1 - f.y);
-        }
-        *reinterpret_cast<uint4*>(sX + unit_at(r, u)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        if (SPLIT) *reinterpret_cast<uint4*>(sX + kPlaneBytes + unit_at(r, u)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    for (int i = 0; i < kUnits; ++i) {
+        const int e = tid + i * kSmallThreads, r = e >> 4;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) u[i][q] *= scale;
+        uint4 hi, lo;
+        split8(u[i], hi, lo);
+        *reinterpret_cast<uint4*>(sX + unit_at(r, e & 15)) = hi;
+        if (SPLIT) *reinterpret_cast<uint4*>(sX + kPlaneBytes + unit_at(r, e & 15)) = lo;
     }
     fence_async_smem();
     tc_fence_before();
@@ -749,23 +803,26 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
     tc_fence_after();
     const uint32_t tmem = s_tmem;
 
-    // One product of 128 x 128 into TMEM by thread 0, waited for by all. k: length of the reduction.
+    // One product of 128 x 128 into TMEM by thread 0, waited for by all. k: length of the reduction. A K step of
+    // 16 is 32 bytes of a K-major row (a block holds four), or 16 rows of an MN-major block; both are constants
+    // in the unrolled loop, since the issuing thread's own instructions are what a small product waits for.
     bool ok = true;
     uint32_t phase = 0;
-    auto product = [&](const uint8_t* pa, bool a_mn, const uint8_t* pb, bool b_mn, int k) {
+    auto product = [&](const uint8_t* pa, auto a_mn, const uint8_t* pb, auto b_mn, int k) {
+        constexpr bool AMN = decltype(a_mn)::value, BMN = decltype(b_mn)::value;
         if (tid == 0 && ok) {
-            fence_async_all();
-            const uint32_t idesc = idesc_fp16(kSide, kSide, a_mn, b_mn);
-            bool first = true;
+            constexpr uint32_t idesc = idesc_fp16(kSide, kSide, AMN, BMN);
+            const uint64_t da = make_desc(smem_u32(pa), AMN ? kBlockBytes : 16, 1024);
+            const uint64_t db = make_desc(smem_u32(pb), BMN ? kBlockBytes : 16, 1024);
+            const int n = (k + 15) / 16;
+#pragma unroll
             for (int term = SPLIT ? 0 : 2; term < 3; ++term) {
-                const uint32_t ba = smem_u32(pa) + (term == 0 ? kPlaneBytes : 0);
-                const uint32_t bb = smem_u32(pb) + (term == 1 ? kPlaneBytes : 0);
-                for (int q = 0; q < (k + 15) / 16; ++q) {
-                    const uint32_t major = (uint32_t)((q >> 2) * (kSide * 128) + (q & 3) * 32), minor = (uint32_t)q * 2048;
-                    const uint64_t da = a_mn ? make_desc(ba + minor, kSide * 128, 1024) : make_desc(ba + major, 16, 1024);
-                    const uint64_t db = b_mn ? make_desc(bb + minor, kSide * 128, 1024) : make_desc(bb + major, 16, 1024);
-                    tc_mma(tmem, da, db, idesc, first ? 0u : 1u);
-                    first = false;
+                const uint64_t ta = da + (term == 0 ? kPlaneBytes >> 4 : 0), tb = db + (term == 1 ? kPlaneBytes >> 4 : 0);
+#pragma unroll
+                for (int q = 0; q < kSide / 16; ++q) {
+                    const uint32_t major = ((q >> 2) * kBlockBytes + (q & 3) * 32) >> 4, minor = (q * 16 * 128) >> 4;
+                    if (q < n) tc_mma(tmem, ta + (AMN ? minor : major), tb + (BMN ? minor : major), idesc,
+                                      term == (SPLIT ? 0 : 2) && q == 0 ? 0u : 1u);
                 }
             }
             tc_commit(&s_bar);
@@ -774,31 +831,30 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
         phase ^= 1;
         tc_fence_after();
     };
+    constexpr std::integral_constant<bool, TALL> tall{};
+    constexpr std::false_type major{};
+    constexpr std::true_type minor{};
     // Each thread has a row of the product (TMEM lane) and half of its columns.
     const int row = (warp & 3) * 32 + lane, half = warp >> 2;
     const uint32_t taddr = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * 64;
-    // fp16 parts of 8 values to the unit u of the thread's row.
-    auto put8 = [&](uint8_t* to, int u, const float* v) {
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            hi[i] = pack_half2(v[2 * i], v[2 * i + 1]);
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi[i]));
-            lo[i] = pack_half2(v[2 * i] - f.x, v[2 * i + 1] - f.y);
-        }
-        *reinterpret_cast<uint4*>(to + unit_at(row, u)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        if (SPLIT) *reinterpret_cast<uint4*>(to + kPlaneBytes + unit_at(row, u)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    auto put8 = [&](uint8_t* to, int unit, const float* v) {
+        uint4 hi, lo;
+        split8(v, hi, lo);
+        *reinterpret_cast<uint4*>(to + unit_at(row, unit)) = hi;
+        if (SPLIT) *reinterpret_cast<uint4*>(to + kPlaneBytes + unit_at(row, unit)) = lo;
     };
-    auto ready = [&]() {     // generic writes of this CTA are there for the next product, and TMEM is read
+    auto ready = [&]() {     // this CTA's writes are there for the next product or copy, and TMEM is read
         fence_async_smem();
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
     };
+    const int per = (kSide + CS - 1) / CS;                               // rows of A that a CTA adds up
+    const int own0 = min(rank * per, kSide), own = min(own0 + per, kSide) - own0;
 
     for (int step = 0; step < a.steps; ++step) {
         // ---- gram
-        product(sX, TALL, sX, TALL, TALL ? nr : nc);
+        product(sX, tall, sX, tall, TALL ? nr : nc);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             uint32_t acc[32];
@@ -813,45 +869,68 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    *reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(sP) + sum_at(row, half * 16 + h * 8 + j)) =
+                    *reinterpret_cast<float4*>(sA + unit_at(row, half * 16 + h * 8 + j)) =
                         make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
             }
         }
+        ready();
         if (CS > 1) {
-            tc_fence_before();
-            cluster_sync();      // partial sums of all CTAs are there
-            const int per = (kSide + CS - 1) / CS, lo_row = rank * per, hi_row = min(lo_row + per, kSide);
-            for (int e = tid; e < (hi_row - lo_row) * 32; e += kSmallThreads) {
-                const int r = lo_row + (e >> 5), u = e & 31;
-                const uint32_t from = smem_u32(sP) + sum_at(r, u);
-                float4 part[kMaxCluster];
+            // the others' rows of the sums to them: lane = 4 * CTA + block
+            const int q = lane >> 2, k = lane & 3;
+            const int q0 = min(q * per, kSide), nq = min(q0 + per, kSide) - q0;
+            if (warp == 0 && ok && q < CS && q != rank && nq > 0)
+                send(map_to_rank(smem_u32(sR) + (uint32_t)((rank * 4 + k) * nq * 128), (uint32_t)q),
+                     smem_u32(sA) + (uint32_t)(k * kBlockBytes + q0 * 128), (uint32_t)nq * 128,
+                     map_to_rank(smem_u32(&s_sums), (uint32_t)q));
+            if (tid == 0) mbar_expect_tx(&s_sums, (uint32_t)((CS - 1) * own * 512));
+            if (ok) ok = mbar_wait(&s_sums, (uint32_t)step & 1u, a.err);
+            // a thread adds up one unit of 8 values, or up to four (two CTAs: 64 rows of 16 units each)
+            constexpr int MOST = kSide / 2 * (kSide / 8) / kSmallThreads;
+            float v[MOST][8];
 #pragma unroll
-                for (int q = 0; q < kMaxCluster; ++q)
-                    if (q < CS) part[q] = ld_cluster(map_to_rank(from, (uint32_t)q));
-                float4 v = part[0];
+            for (int i = 0; i < MOST; ++i) {
+                const int e = tid + i * kSmallThreads, r = own0 + (e >> 4), c = e & 15;
 #pragma unroll
-                for (int q = 1; q < kMaxCluster; ++q)
-                    if (q < CS) { v.x += part[q].x; v.y += part[q].y; v.z += part[q].z; v.w += part[q].w; }
-                const uint32_t h0 = pack_half2(v.x, v.y), h1 = pack_half2(v.z, v.w);
-                const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
-                const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
-                const uint32_t l0 = pack_half2(v.x - f0.x, v.y - f0.y), l1 = pack_half2(v.z - f1.x, v.w - f1.y);
-                const uint32_t to = smem_u32(sA) + unit_at(r, u >> 1) + (u & 1) * 8;
-                for (int q = 0; q < CS; ++q) {
-                    st_cluster(map_to_rank(to, (uint32_t)q), h0, h1);
-                    if (SPLIT) st_cluster(map_to_rank(to + kPlaneBytes, (uint32_t)q), l0, l1);
+                for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+                for (int o = 0; o < CS && (e >> 4) < own; ++o) {
+                    // fp32 units 2 c and 2 c + 1 of the row
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        const int unit = 2 * c + w;
+                        const uint8_t* from = o == rank ? sA + unit_at(r, unit)
+                                                        : sR + (o * 4 + (unit >> 3)) * own * 128 + (r - own0) * 128 +
+                                                              (((unit & 7) ^ (r & 7)) << 4);
+                        const float4 f = *reinterpret_cast<const float4*>(from);
+                        v[i][4 * w] += f.x; v[i][4 * w + 1] += f.y; v[i][4 * w + 2] += f.z; v[i][4 * w + 3] += f.w;
+                    }
                 }
             }
-            fence_async_all();
-            cluster_sync();      // A is whole in every CTA, and every CTA has read its partial sums
-            tc_fence_after();
-            fence_async_all();
+            __syncthreads();      // the sums of the CTA's own rows are read: its rows of A take their place
+#pragma unroll
+            for (int i = 0; i < MOST; ++i) {
+                const int e = tid + i * kSmallThreads, r = own0 + (e >> 4), c = e & 15;
+                if ((e >> 4) < own) {
+                    uint4 hi, lo;
+                    split8(v[i], hi, lo);
+                    *reinterpret_cast<uint4*>(sA + unit_at(r, c)) = hi;
+                    if (SPLIT) *reinterpret_cast<uint4*>(sA + kPlaneBytes + unit_at(r, c)) = lo;
+                }
+            }
+            fence_async_smem();
             __syncthreads();
-        } else {
-            ready();
+            // the CTA's rows of A to the others
+            if (warp == 0 && ok && q < CS && q != rank && k < 2 * PL && own > 0) {
+                const uint32_t at = smem_u32(sA) + (uint32_t)(k * kBlockBytes + own0 * 128);
+                send(map_to_rank(at, (uint32_t)q), at, (uint32_t)own * 128, map_to_rank(smem_u32(&s_rows), (uint32_t)q));
+            }
+            if (tid == 0) mbar_expect_tx(&s_rows, (uint32_t)((kSide - own) * 128 * 2 * PL));
+            if (ok) ok = mbar_wait(&s_rows, (uint32_t)step & 1u, a.err);
+            asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
         }
         // ---- poly: B = a I + b A + c A A in the place of A
-        product(sA, false, sA, false, a.side);
+        product(sA, major, sA, major, a.side);
+        // every CTA has its rows of A, so none of this one's are still being read by a copy
+        if (CS > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             uint32_t acc[32];
@@ -884,8 +963,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
         }
         ready();
         // ---- apply
-        if (TALL) product(sX, false, sA, false, a.side);
-        else product(sA, false, sX, true, a.side);
+        if constexpr (TALL) product(sX, major, sA, major, a.side);
+        else product(sA, major, sX, minor, a.side);
         const bool last = step + 1 == a.steps;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -898,7 +977,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
             if (last) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    *reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(sP) + sum_at(row, half * 16 + h * 8 + j)) =
+                    *reinterpret_cast<float4*>(sA + unit_at(row, half * 16 + h * 8 + j)) =
                         make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
             } else {
 #pragma unroll
@@ -911,38 +990,38 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
     // ---- o, or the step on the weights
     const float lr = a.fin.lr_dev ? __ldg(a.fin.lr_dev) : a.fin.lr;
     const float lose = lr * a.fin.decay, move = lr * a.fin.scale;
-    for (int e0 = tid; e0 < kSide * kSide; e0 += kSmallThreads * kBatch) {
-        float p[kBatch];
-        if (a.fin.step) {
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int e = e0 + i * kSmallThreads, r = e >> 7, c = e & 127;
-                const int64_t at = base + (int64_t)(r0 + r) * cols + c0 + c;
-                p[i] = r >= nr || c >= nc ? 0.f : a.fin.master ? a.fin.master[at]
-                       : a.p_bf16 ? ld_f(static_cast<const __nv_bfloat16*>(a.fin.out) + at)
-                                  : static_cast<const float*>(a.fin.out)[at];
-            }
+    for (int h = 0; h < kUnits; h += kUnits / 2) {
+        float p[kUnits / 2][8];
+#pragma unroll
+        for (int i = 0; i < kUnits / 2; ++i) {
+            const int e = tid + (h + i) * kSmallThreads, r = e >> 4, c = (e & 15) * 8;
+            if (a.fin.step)
+                load_unit(a.fin.master ? (const void*)a.fin.master : a.fin.out, base + (int64_t)r * cols + c,
+                          !a.fin.master && a.p_bf16, a.vec, r < nr ? min(nc - c, 8) : 0, p[i]);
         }
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int e = e0 + i * kSmallThreads, r = e >> 7, c = e & 127;
-            if (r >= nr || c >= nc) continue;
-            const int64_t at = base + (int64_t)(r0 + r) * cols + c0 + c;
-            float x;
+        for (int i = 0; i < kUnits / 2; ++i) {
+            const int e = tid + (h + i) * kSmallThreads, r = e >> 4, c = (e & 15) * 8, n = min(nc - c, 8);
+            if (r >= nr || n <= 0) continue;
+            const int64_t at = base + (int64_t)r * cols + c;
+            float x[8];
             if (a.steps) {
-                x = *reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(sP) + sum_at(r, c >> 2) + (c & 3) * 4);
+                *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(sA + unit_at(r, 2 * (e & 15)));
+                *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(sA + unit_at(r, 2 * (e & 15) + 1));
             } else {
-                const uint32_t b = unit_at(r, c >> 3) + (c & 7) * 2;
-                x = __half2float(*reinterpret_cast<const __half*>(sX + b));
-                if (SPLIT) x += __half2float(*reinterpret_cast<const __half*>(sX + kPlaneBytes + b));
+                const __half* hi = reinterpret_cast<const __half*>(sX + unit_at(r, e & 15));
+                const __half* lo = reinterpret_cast<const __half*>(sX + kPlaneBytes + unit_at(r, e & 15));
+#pragma unroll
+                for (int q = 0; q < 8; ++q) x[q] = __half2float(hi[q]) + (SPLIT ? __half2float(lo[q]) : 0.f);
             }
-            x *= 1.f / kXScale;
-            if (a.fin.step) {
-                x = fmaf(-move, x, fmaf(-lose, p[i], p[i]));
-                if (a.fin.master) a.fin.master[at] = x;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                x[q] *= 1.f / kXScale;
+                if (a.fin.step) x[q] = fmaf(-move, x[q], fmaf(-lose, p[i][q], p[i][q]));
             }
-            if (a.p_bf16) st_f(static_cast<__nv_bfloat16*>(a.fin.out) + at, x);
-            else static_cast<float*>(a.fin.out)[at] = x;
+            if (a.fin.master) store_unit(a.fin.master, at, false, a.vec, n, x);
+            store_unit(a.fin.out, at, a.p_bf16, a.vec, n, x);
         }
     }
     tc_fence_before();
@@ -954,7 +1033,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
     }
 }
 
-constexpr size_t small_smem(bool split) { return 1024 + (split ? 4 : 2) * (size_t)kPlaneBytes + kSide * kSide * 4; }
+constexpr size_t small_smem(bool split) { return 1024 + (split ? 2 : 1) * (size_t)kPlaneBytes + 4 * kBlockBytes + kRecvBytes; }
 static_assert(small_smem(true) <= 227 * 1024 - 1024, "shared memory per CTA");
 
 // ---------------------------------------------------------------- host
@@ -1092,6 +1171,7 @@ cudaError_t launch_small(const moe_muon_config_t& c, const MuonPrep& pre, const 
     a.cluster = ceil_div(std::max(c.rows, c.cols), kSide);
     a.g_bf16 = c.grad_dtype == MOE_BF16;
     a.p_bf16 = c.dtype == MOE_BF16;
+    a.vec = c.cols % 8 == 0;
     a.a = (float)c.a;
     a.b = (float)c.b;
     a.c = (float)c.c;

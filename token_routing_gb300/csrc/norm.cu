@@ -2,6 +2,7 @@
 #include <cmath>
 
 #include "internal.cuh"
+#include "tc_ptx.cuh"
 
 namespace moe {
 
@@ -59,6 +60,111 @@ __device__ __forceinline__ void load_params(const void* p, bool f32, int c, floa
     }
 }
 
+// NE elements of a row as a thread holds them: chunks `lane`, lane + tpr, ... of the row's nvec; beyond
+// them zero. FULL: the row is just that many chunks. Arithmetic is on packed fp32 pairs.
+template <typename T, int VE, int NE, bool FULL>
+struct Part {
+    static constexpr int NC = NE / VE, NP = NE / 2;
+    Chunk<T, VE> c[NC];
+    __device__ __forceinline__ void load(const T* row, int lane, int tpr, int nvec, bool live) {
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int at = lane + i * tpr;
+            c[i].zero();
+            if (live && (FULL || at < nvec)) c[i].load(row + (int64_t)at * VE);
+        }
+    }
+    __device__ __forceinline__ void pairs(uint64_t (&p)[NP]) const {
+        if constexpr (VE == 1) {
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                float a[1], b[1];
+                c[2 * i].get(a);
+                c[2 * i + 1].get(b);
+                p[i] = pk2(a[0], b[0]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                const uint32_t* w = reinterpret_cast<const uint32_t*>(&c[i].u);
+#pragma unroll
+                for (int k = 0; k < VE / 2; ++k) {
+                    if constexpr (sizeof(T) == 2)
+                        p[i * (VE / 2) + k] = pk2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
+                    else
+                        p[i * (VE / 2) + k] = pk2(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
+                }
+            }
+        }
+    }
+    static __device__ __forceinline__ void store(T* row, int lane, int tpr, int nvec, const uint64_t (&p)[NP]) {
+        if constexpr (VE == 1) {
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                float f[2];
+                upk2(p[i], f[0], f[1]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int at = lane + (2 * i + k) * tpr;
+                    if (FULL || at < nvec) st_f(row + at, f[k]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                const int at = lane + i * tpr;
+                Chunk<T, VE> o;
+                uint32_t* w = reinterpret_cast<uint32_t*>(&o.u);
+#pragma unroll
+                for (int k = 0; k < VE / 2; ++k) {
+                    float lo, hi;
+                    upk2(p[i * (VE / 2) + k], lo, hi);
+                    if constexpr (sizeof(T) == 2) {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+                        w[k] = *reinterpret_cast<const uint32_t*>(&h);
+                    } else {
+                        w[2 * k] = __float_as_uint(lo);
+                        w[2 * k + 1] = __float_as_uint(hi);
+                    }
+                }
+                if (FULL || at < nvec) *reinterpret_cast<typename Chunk<T, VE>::R*>(row + (int64_t)at * VE) = o.u;
+            }
+        }
+    }
+    // Zeros in the pairs of chunks that the row does not have.
+    static __device__ __forceinline__ void cut(int lane, int tpr, int nvec, uint64_t (&p)[NP]) {
+        if constexpr (!FULL) {
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                if constexpr (VE == 1) {
+                    float lo, hi;
+                    upk2(p[i], lo, hi);
+                    p[i] = pk2(lane + 2 * i * tpr < nvec ? lo : 0.f, lane + (2 * i + 1) * tpr < nvec ? hi : 0.f);
+                } else if (lane + i / (VE / 2) * tpr >= nvec) {
+                    p[i] = 0;
+                }
+            }
+        }
+    }
+    // The parameters of the thread's columns.
+    static __device__ __forceinline__ void params(const void* v, bool f32, float none, int lane, int tpr, int nvec,
+                                                  uint64_t (&p)[NP]) {
+        float f[NE];
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int at = lane + i * tpr;
+            float one[VE];
+#pragma unroll
+            for (int k = 0; k < VE; ++k) one[k] = none;
+            if (FULL || at < nvec) load_params<VE>(v, f32, at * VE, none, one);
+#pragma unroll
+            for (int k = 0; k < VE; ++k) f[i * VE + k] = one[k];
+        }
+#pragma unroll
+        for (int i = 0; i < NP; ++i) p[i] = pk2(f[2 * i], f[2 * i + 1]);
+    }
+};
+
 // Widest vector (elements, up to 16 bytes) that divides rows of d elements of es bytes.
 int row_vec(int d, int es) {
     int v = 16 / es;
@@ -66,30 +172,45 @@ int row_vec(int d, int es) {
     return v;
 }
 
-// Sum over the `tpr` threads of a row (32 or more, a power of two; a block holds whole rows). `red`
-// is free again after the next row_sum on another buffer.
-__device__ __forceinline__ float row_sum(float v, int tpr, float* red) {
+// Sums over the `tpr` threads of a row (32 or more, a power of two; a block holds whole rows, `own` is the
+// row's number in it). `red` (a value to each warp) is free again after the next sum on another buffer.
+__device__ __forceinline__ void row_sync(int tpr, int own) {
+    asm volatile("bar.sync %0, %1;" ::"r"(own + 1), "r"(tpr) : "memory");
+}
+__device__ __forceinline__ float row_sum(float v, int tpr, int own, float* red) {
     v = warp_sum(v);
     if (tpr == 32) return v;
     const int warp = threadIdx.x >> 5, n = tpr >> 5;
     if ((threadIdx.x & 31) == 0) red[warp] = v;
-    __syncthreads();
-    const float* at = red + warp / n * n;
+    row_sync(tpr, own);
+    const float* at = red + own * n;
     float s = at[0];
     for (int i = 1; i < n; ++i) s += at[i];
     return s;
 }
-__device__ __forceinline__ float2 row_sum2(float2 v, int tpr, float2* red) {
-    v.x = warp_sum(v.x);
-    v.y = warp_sum(v.y);
+__device__ __forceinline__ float2 row_sum2(float2 v, int tpr, int own, float2* red) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+        v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    }
     if (tpr == 32) return v;
     const int warp = threadIdx.x >> 5, n = tpr >> 5;
     if ((threadIdx.x & 31) == 0) red[warp] = v;
-    __syncthreads();
-    const float2* at = red + warp / n * n;
+    row_sync(tpr, own);
+    const float2* at = red + own * n;
     float2 s = at[0];
     for (int i = 1; i < n; ++i) { s.x += at[i].x; s.y += at[i].y; }
     return s;
+}
+template <int N>
+__device__ __forceinline__ float pair_sum(const uint64_t (&p)[N]) {
+    uint64_t s = p[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) s = add2(s, p[i]);
+    float lo, hi;
+    upk2(s, lo, hi);
+    return lo + hi;
 }
 
 struct NormArgs {
@@ -107,77 +228,63 @@ struct NormArgs {
 };
 
 // A row to `tpr` threads, in registers between the reading and the writing: the mean, then the squares
-// of the differences, then the output. NV vectors of VE elements a thread.
-constexpr int kMaxRow = 512;      // threads to a row at most: 128 registers each
-template <typename T, int VE, int NV>
+// of the differences, then the output; gain and bias stay in registers from row to row, and the next row is
+// on its way while one is worked on. Bound by memory.
+constexpr int kMaxRow = 512;      // threads to a row at most
+constexpr int kNormThreads = 640; // threads on an SM that launches count on
+template <typename T, int VE, int NE, bool FULL, bool RES>
 __global__ void __launch_bounds__(kMaxRow) norm_kernel(const NormArgs a) {
-    __shared__ float s_red[2][32];
+    using P = Part<T, VE, NE, FULL>;
+    constexpr int NP = NE / 2;
+    constexpr bool AHEAD = NE * (int)sizeof(T) <= 32;       // longer parts have no registers left for it
+    __shared__ float s_red[2][kMaxRow / 32];
     pdl_wait();
-    const int rows = blockDim.x / a.tpr, lane = threadIdx.x & (a.tpr - 1), nvec = a.d / VE;
+    const int own = threadIdx.x / a.tpr, lane = threadIdx.x - own * a.tpr, rows = blockDim.x / a.tpr, nvec = a.d / VE;
     const T* x = static_cast<const T*>(a.x);
     const T* r = static_cast<const T*>(a.r);
-    for (int64_t t0 = (int64_t)blockIdx.x * rows; t0 < a.T; t0 += (int64_t)gridDim.x * rows) {
-        const int64_t t = t0 + threadIdx.x / a.tpr;
-        const bool live = t < a.T;
-        const int64_t base = t * a.d;
-        Chunk<T, VE> cx[NV], cr[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = lane + i * a.tpr;
-            cx[i].zero();
-            cr[i].zero();
-            if (live && c < nvec) {
-                cx[i].load(x + base + (int64_t)c * VE);
-                if (r) cr[i].load(r + base + (int64_t)c * VE);
-            }
+    uint64_t gain[NP], bias[NP];
+    P::params(a.gain, a.p32, 1.f, lane, a.tpr, nvec, gain);
+    P::params(a.bias, a.p32, 0.f, lane, a.tpr, nvec, bias);
+    const int64_t step = (int64_t)gridDim.x * rows;
+    int64_t t = (int64_t)blockIdx.x * rows + own;
+    P px, pr;
+    if (AHEAD) {
+        px.load(x + t * a.d, lane, a.tpr, nvec, t < a.T);
+        if (RES) pr.load(r + t * a.d, lane, a.tpr, nvec, t < a.T);
+    }
+    for (; t < a.T; t += step) {
+        if (!AHEAD) {
+            px.load(x + t * a.d, lane, a.tpr, nvec, true);
+            if (RES) pr.load(r + t * a.d, lane, a.tpr, nvec, true);
         }
-        float v[NV][VE];
-        float sum = 0.f;
+        uint64_t v[NP];
+        px.pairs(v);
+        if (RES) {
+            uint64_t q[NP];
+            pr.pairs(q);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            cx[i].get(v[i]);
-            if (r) {
-                float q[VE];
-                cr[i].get(q);
-#pragma unroll
-                for (int k = 0; k < VE; ++k) v[i][k] += q[k];
-                const int c = lane + i * a.tpr;
-                if (live && c < nvec) Chunk<T, VE>::store(static_cast<T*>(a.total) + base + (int64_t)c * VE, v[i]);
-            }
-#pragma unroll
-            for (int k = 0; k < VE; ++k) sum += v[i][k];
+            for (int i = 0; i < NP; ++i) v[i] = add2(v[i], q[i]);
         }
-        const float mean = row_sum(sum, a.tpr, s_red[0]) * a.inv_d;
-        float sq = 0.f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (lane + i * a.tpr < nvec) {
-#pragma unroll
-                for (int k = 0; k < VE; ++k) {
-                    v[i][k] -= mean;
-                    sq = fmaf(v[i][k], v[i][k], sq);
-                }
-            }
+        if (AHEAD) {
+            px.load(x + (t + step) * a.d, lane, a.tpr, nvec, t + step < a.T);
+            if (RES) pr.load(r + (t + step) * a.d, lane, a.tpr, nvec, t + step < a.T);
         }
-        const float var = row_sum(sq, a.tpr, s_red[1]) * a.inv_d;
+        if (RES) P::store(static_cast<T*>(a.total) + t * a.d, lane, a.tpr, nvec, v);
+        const float mean = row_sum(pair_sum(v), a.tpr, own, s_red[0]) * a.inv_d;
+        uint64_t sq[NP];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) v[i] = add2(v[i], splat2(-mean));
+        P::cut(lane, a.tpr, nvec, v);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) sq[i] = mul2(v[i], v[i]);
+        const float var = row_sum(pair_sum(sq), a.tpr, own, s_red[1]) * a.inv_d;
         const float rstd = 1.0f / sqrtf(var + a.eps);
-        if (live) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = lane + i * a.tpr;
-                if (c < nvec) {
-                    float g[VE], b[VE];
-                    load_params<VE>(a.gain, a.p32, c * VE, 1.f, g);
-                    load_params<VE>(a.bias, a.p32, c * VE, 0.f, b);
-#pragma unroll
-                    for (int k = 0; k < VE; ++k) v[i][k] = fmaf(v[i][k] * rstd, g[k], b[k]);
-                    Chunk<T, VE>::store(static_cast<T*>(a.y) + base + (int64_t)c * VE, v[i]);
-                }
-            }
-            if (lane == 0) {
-                if (a.mean) a.mean[t] = mean;
-                if (a.rstd) a.rstd[t] = rstd;
-            }
+        for (int i = 0; i < NP; ++i) v[i] = fma2(mul2(v[i], splat2(rstd)), gain[i], bias[i]);
+        P::store(static_cast<T*>(a.y) + t * a.d, lane, a.tpr, nvec, v);
+        if (lane == 0) {
+            if (a.mean) a.mean[t] = mean;
+            if (a.rstd) a.rstd[t] = rstd;
         }
     }
 }
@@ -212,7 +319,7 @@ __global__ void __launch_bounds__(kLong) norm_long_kernel(const NormArgs a) {
             for (int k = 0; k < VE; ++k) part += v[k];
             sum += part;
         }
-        const float mean = row_sum(sum, kLong, s_red[0]) * a.inv_d;
+        const float mean = row_sum(sum, kLong, 0, s_red[0]) * a.inv_d;
         float sq = 0.f;
         for (int c = threadIdx.x; c < nvec; c += kLong) {
             element(c, v);
@@ -221,7 +328,7 @@ __global__ void __launch_bounds__(kLong) norm_long_kernel(const NormArgs a) {
             for (int k = 0; k < VE; ++k) part = fmaf(v[k] - mean, v[k] - mean, part);
             sq += part;
         }
-        const float var = row_sum(sq, kLong, s_red[1]) * a.inv_d;
+        const float var = row_sum(sq, kLong, 0, s_red[1]) * a.inv_d;
         const float rstd = 1.0f / sqrtf(var + a.eps);
         for (int c = threadIdx.x; c < nvec; c += kLong) {
             element(c, v);                    // read before y or total, which may be x or r, is written
@@ -253,82 +360,158 @@ struct NormGradArgs {
     int T, d, tpr;
     bool p32;
     float inv_d;
+    int stages, array_bytes;   // of the ring: a stage holds 2 arrays, or 3 with dtotal
+    int* err;
 };
 
 // A row to `tpr` threads, as in the forward pass. A thread keeps its columns from row to row, so it adds
-// up dgain and dbias in registers; a block's rows join in shared memory at the end.
-template <typename T, int VE, int NV>
-__global__ void __launch_bounds__(kMaxRow) norm_grad_kernel(const NormGradArgs a) {
-    __shared__ float2 s_red[2][32];
-    extern __shared__ float s_part[];     // [d] (blocks of more than one row)
+// up dgain and dbias in registers; a block's rows join in shared memory at the end. One block to an SM: its
+// partial sums are what the joining kernel reads.
+//
+// Bound by memory, and registers are full of sums, so rows come ahead through a ring in shared memory: the
+// rows that a block works on at once are adjacent, so a stage is one bulk copy each of dy, s and dtotal, up to
+// 150 KB in flight. A copy starts on a 16-byte boundary: it takes in what lies before and behind odd rows,
+// but for the end of the last one, whose odd bytes a thread fetches.
+constexpr int kGradThreads = 512;
+constexpr int kMaxStages = 6;
+constexpr int kRingBytes = 180 * 1024;
+constexpr int kGradSmem = 200 * 1024;
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(dst), "l"(src), "r"(bytes), "r"(tc::smem_u32(bar)) : "memory");
+}
+
+template <typename T, int VE, int NE, bool FULL>
+__global__ void __launch_bounds__(kGradThreads, 1) norm_grad_kernel(const NormGradArgs a) {
+    using P = Part<T, VE, NE, FULL>;
+    constexpr int NP = NE / 2;
+    __shared__ float2 s_red[2][kGradThreads / 32];
+    __shared__ uint64_t s_full[kMaxStages], s_empty[kMaxStages];
+    extern __shared__ __align__(128) uint8_t s_ring[];
+    const int own = threadIdx.x / a.tpr, lane = threadIdx.x - own * a.tpr, rows = kGradThreads / a.tpr, nvec = a.d / VE;
+    const int arrays = a.dtotal && a.dx ? 3 : 2;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < a.stages; ++i) {
+            tc::mbar_init(s_full + i, 1);
+            tc::mbar_init(s_empty + i, kGradThreads / 32);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    __syncthreads();
     pdl_wait();
-    const int rows = blockDim.x / a.tpr, lane = threadIdx.x & (a.tpr - 1), nvec = a.d / VE;
-    const int own = threadIdx.x / a.tpr;
-    float dg[NV][VE], db[NV][VE];
+    const int64_t row_bytes = (int64_t)a.d * sizeof(T);
+    const int64_t sets = ((int64_t)a.T + rows - 1) / rows;
+    // Set `set` (rows set * rows on) into a stage; where its bytes start in the stage's arrays.
+    auto first_byte = [&](int64_t set) { return set * rows * row_bytes; };
+    auto fill = [&](int64_t set, int stage) {
+        const int64_t all = (int64_t)a.T * row_bytes, from = first_byte(set) & ~(int64_t)15;
+        const int64_t end = min((set + 1) * rows * row_bytes, all);
+        const int64_t upto = min((end + 15) & ~(int64_t)15, all & ~(int64_t)15);    // not past the array
+        const uint32_t bytes = (uint32_t)(upto - from);
+        const char* src[3] = {static_cast<const char*>(a.dy), static_cast<const char*>(a.s), static_cast<const char*>(a.dtotal)};
+        uint8_t* dst = s_ring + (size_t)stage * arrays * a.array_bytes;
+        for (int i = 0; i < arrays; ++i)
+            for (int64_t q = upto; q < end; q += sizeof(T))
+                *reinterpret_cast<T*>(dst + i * a.array_bytes + (q - from)) = *reinterpret_cast<const T*>(src[i] + q);
+        // (the arrive makes the bytes stored above visible to whom waits)
+        tc::mbar_expect_tx(s_full + stage, bytes * arrays);
+        if (bytes)
+            for (int i = 0; i < arrays; ++i)
+                bulk_load(tc::smem_u32(dst + i * a.array_bytes), src[i] + from, bytes, s_full + stage);
+    };
+    uint64_t gain[NP], dg[NP], db[NP];
+    P::params(a.gain, a.p32, 1.f, lane, a.tpr, nvec, gain);
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int k = 0; k < VE; ++k) dg[i][k] = db[i][k] = 0.f;
-    int flip = 0;
-    for (int64_t t0 = (int64_t)blockIdx.x * rows; t0 < a.T; t0 += (int64_t)gridDim.x * rows) {
-        const int64_t t = t0 + own;
+    for (int i = 0; i < NP; ++i) dg[i] = db[i] = 0;
+    if (threadIdx.x == 0)
+        for (int i = 0; i < a.stages; ++i)
+            if (blockIdx.x + (int64_t)i * gridDim.x < sets) fill(blockIdx.x + (int64_t)i * gridDim.x, i);
+    int flip = 0, stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    float mean = 0.f, rstd = 0.f;
+    if ((int64_t)blockIdx.x * rows + own < a.T) {
+        mean = __ldg(a.mean + (int64_t)blockIdx.x * rows + own);
+        rstd = __ldg(a.rstd + (int64_t)blockIdx.x * rows + own);
+    }
+    for (int64_t set = blockIdx.x; set < sets; set += gridDim.x) {
+        const int64_t t = set * rows + own;
         const bool live = t < a.T;
-        const int64_t base = t * a.d;
-        Chunk<T, VE> cd[NV], cs[NV], ct[NV];
+        if (ok) ok = tc::mbar_wait(s_full + stage, phase, a.err);
+        const uint8_t* at = s_ring + (size_t)stage * arrays * a.array_bytes + (first_byte(set) & 15) + own * row_bytes;
+        uint64_t g[NP], h[NP];
+        {
+            P py, ps;
+            py.load(reinterpret_cast<const T*>(at), lane, a.tpr, nvec, live);
+            ps.load(reinterpret_cast<const T*>(at + a.array_bytes), lane, a.tpr, nvec, live);
+            py.pairs(g);
+            ps.pairs(h);
+        }
+        const float rs = rstd;
+        const uint64_t off = splat2(-mean);
+        const int64_t next = t + (int64_t)gridDim.x * rows;
+        if (next < a.T) {
+            mean = __ldg(a.mean + next);
+            rstd = __ldg(a.rstd + next);
+        }
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = lane + i * a.tpr;
-            cd[i].zero();
-            cs[i].zero();
-            ct[i].zero();
-            if (live && c < nvec) {
-                cd[i].load(static_cast<const T*>(a.dy) + base + (int64_t)c * VE);
-                cs[i].load(static_cast<const T*>(a.s) + base + (int64_t)c * VE);
-                if (a.dtotal) ct[i].load(static_cast<const T*>(a.dtotal) + base + (int64_t)c * VE);
+        for (int i = 0; i < NP; ++i) h[i] = mul2(add2(h[i], off), splat2(rs));
+        P::cut(lane, a.tpr, nvec, h);
+        if (!live) {
+#pragma unroll
+            for (int i = 0; i < NP; ++i) h[i] = 0;      // (g is zero)
+        }
+        uint64_t s1 = 0, s2 = 0;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            dg[i] = fma2(g[i], h[i], dg[i]);
+            db[i] = add2(db[i], g[i]);
+            g[i] = mul2(g[i], gain[i]);
+            s1 = add2(s1, g[i]);
+            s2 = fma2(g[i], h[i], s2);
+        }
+        if (a.dx) {
+            float2 lo, hi;
+            upk2(s1, lo.x, hi.x);
+            upk2(s2, lo.y, hi.y);
+            const float2 all = row_sum2(make_float2(lo.x + hi.x, lo.y + hi.y), a.tpr, own, s_red[flip]);
+            flip ^= 1;
+            const uint64_t c1 = splat2(-all.x * a.inv_d), c2 = splat2(-all.y * a.inv_d);
+#pragma unroll
+            for (int i = 0; i < NP; ++i) g[i] = mul2(splat2(rs), add2(g[i], fma2(h[i], c2, c1)));
+            if (arrays == 3) {
+                P pt;
+                uint64_t q[NP];
+                pt.load(reinterpret_cast<const T*>(at + 2 * a.array_bytes), lane, a.tpr, nvec, live);
+                pt.pairs(q);
+#pragma unroll
+                for (int i = 0; i < NP; ++i) g[i] = add2(g[i], q[i]);
             }
         }
-        const float mean = live ? __ldg(a.mean + t) : 0.f, rstd = live ? __ldg(a.rstd + t) : 0.f;
-        float g[NV][VE], h[NV][VE];
-        float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = lane + i * a.tpr;
-            float w[VE];
-            cd[i].get(g[i]);
-            cs[i].get(h[i]);
-            if (c < nvec) load_params<VE>(a.gain, a.p32, c * VE, 1.f, w);
-#pragma unroll
-            for (int k = 0; k < VE; ++k) {
-                if (!live || c >= nvec) {
-                    g[i][k] = h[i][k] = 0.f;
-                    continue;
+        // the stage is read: thread 0 fills it again when all warps say so
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) tc::mbar_arrive(s_empty + stage);
+        if (a.dx && live) P::store(static_cast<T*>(a.dx) + t * a.d, lane, a.tpr, nvec, g);
+        if (threadIdx.x == 0 && ok) {
+            const int64_t more = set + (int64_t)a.stages * gridDim.x;
+            if (more < sets) {
+                ok = tc::mbar_wait(s_empty + stage, phase, a.err);
+                if (ok) {
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    fill(more, stage);
                 }
-                h[i][k] = (h[i][k] - mean) * rstd;
-                dg[i][k] = fmaf(g[i][k], h[i][k], dg[i][k]);
-                db[i][k] += g[i][k];
-                g[i][k] *= w[k];
-                sum.x += g[i][k];
-                sum.y = fmaf(g[i][k], h[i][k], sum.y);
             }
         }
-        if (!a.dx) continue;
-        const float2 all = row_sum2(sum, a.tpr, s_red[flip]);
-        flip ^= 1;
-        const float c1 = all.x * a.inv_d, c2 = all.y * a.inv_d;
-        if (live) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = lane + i * a.tpr;
-                if (c < nvec) {
-                    float q[VE];
-                    ct[i].get(q);
-#pragma unroll
-                    for (int k = 0; k < VE; ++k) q[k] = fmaf(rstd, g[i][k] - fmaf(h[i][k], c2, c1), q[k]);
-                    Chunk<T, VE>::store(static_cast<T*>(a.dx) + base + (int64_t)c * VE, q);
-                }
-            }
+        if (++stage == a.stages) {
+            stage = 0;
+            phase ^= 1;
         }
     }
+    if (!ok && threadIdx.x == 0)      // no copy may be in flight when the block leaves
+        for (int i = 0; i < a.stages; ++i) tc::mbar_wait(s_full + i, phase, a.err);
+    float* s_part = reinterpret_cast<float*>(s_ring);      // [d]: the ring has been read
+    __syncthreads();
     if (!a.part) return;
     // the block's rows one after another, dgain then dbias
     for (int which = 0; which < 2; ++which) {
@@ -336,17 +519,18 @@ __global__ void __launch_bounds__(kMaxRow) norm_grad_kernel(const NormGradArgs a
         for (int q = 0; q < rows; ++q) {
             if (own == q) {
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int c = lane + i * a.tpr;
-                    if (c >= nvec) continue;
+                for (int i = 0; i < NP; ++i) {
+                    float f[2];
+                    upk2(which ? db[i] : dg[i], f[0], f[1]);
 #pragma unroll
-                    for (int k = 0; k < VE; ++k) {
-                        float v = which ? db[i][k] : dg[i][k];
+                    for (int k = 0; k < 2; ++k) {
+                        const int e = 2 * i + k, at = lane + e / VE * a.tpr, c = at * VE + e % VE;
+                        if (!FULL && at >= nvec) continue;
                         if (rows > 1) {
-                            if (q > 0) v += s_part[c * VE + k];
-                            s_part[c * VE + k] = v;
+                            if (q > 0) f[k] += s_part[c];
+                            s_part[c] = f[k];
                         }
-                        if (q + 1 == rows) out[c * VE + k] = v;
+                        if (q + 1 == rows) out[c] = f[k];
                     }
                 }
             }
@@ -392,7 +576,7 @@ __global__ void __launch_bounds__(kLong) norm_grad_long_kernel(const NormGradArg
             sum.x += part.x;
             sum.y += part.y;
         }
-        const float2 all = row_sum2(sum, kLong, s_red[flip]);
+        const float2 all = row_sum2(sum, kLong, 0, s_red[flip]);
         flip ^= 1;
         const float c1 = all.x * a.inv_d, c2 = all.y * a.inv_d;
         for (int c = threadIdx.x; c < nvec; c += kLong) {
@@ -441,9 +625,9 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const NormGradArgs a)
     }
 }
 
-// dgain and dbias from the blocks' sums: 32 columns to a block, its warps take every eighth partial
-// row, then join in order.
-constexpr int kJoinWarps = 8;
+// dgain and dbias from the blocks' sums: 32 columns to a block, its 32 warps take every 32nd partial row,
+// then join in order.
+constexpr int kJoinWarps = 32;
 __global__ void __launch_bounds__(32 * kJoinWarps) norm_join_kernel(const float* __restrict__ part, int blocks, int d,
                                                                    int accumulate, float* dgain, float* dbias) {
     __shared__ float s_sum[kJoinWarps][32];
@@ -454,12 +638,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) norm_join_kernel(const float*
     const float* in = part + (size_t)blockIdx.y * blocks * d;
     float v = 0.f;
     if (c < d) {
-#pragma unroll 4
+#pragma unroll 8
         for (int b = warp; b < blocks; b += kJoinWarps) v += in[(size_t)b * d + c];
     }
     s_sum[warp][lane] = v;
     __syncthreads();
     if (warp == 0 && c < d) {
+#pragma unroll
         for (int w = 1; w < kJoinWarps; ++w) v += s_sum[w][lane];
         out[c] = accumulate ? out[c] + v : v;
     }
@@ -478,49 +663,69 @@ moe_status_t check_norm(const moe_norm_config_t* c) {
 
 bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
-// How a row is shared out: vector, threads to a row and elements to a thread (8, 16 or 32; 0: too long for
-// registers).
+// How a row is shared out: vector, threads to a row and bytes of it to a thread (16, 32 or 64; 0: too long
+// for registers). 32 bytes to a thread, and the next row's 32 in flight, keep the registers of a block of 512
+// threads; below 256 elements a warp takes 16 or 32 bytes a lane, and beyond 512 threads 64.
 struct Shape {
-    int ve, tpr, ne, block;
+    int ve, tpr, bytes;
 };
 Shape norm_shape(const moe_norm_config_t& c) {
     Shape s;
-    s.ve = row_vec(c.d, c.dtype == MOE_BF16 ? 2 : 4);
+    const int es = c.dtype == MOE_BF16 ? 2 : 4;
+    const int64_t row = (int64_t)c.d * es;
+    s.ve = row_vec(c.d, es);
     s.tpr = 32;
-    while (s.tpr < kMaxRow && s.tpr * 16 < c.d) s.tpr *= 2;
-    s.ne = c.d <= s.tpr * 8 ? 8 : c.d <= s.tpr * 16 ? 16 : c.d <= s.tpr * 32 ? 32 : 0;
-    s.block = std::max(s.tpr, 128);
+    while (s.tpr < kMaxRow && s.tpr * 32 < row) s.tpr *= 2;
+    s.bytes = row <= s.tpr * 16 ? 16 : row <= s.tpr * 32 ? 32 : row <= s.tpr * 64 ? 64 : 0;
     return s;
+}
+
+template <typename T, int VE, int NE, bool FULL>
+cudaError_t launch_norm_ne(const moe_norm_config_t& c, const NormArgs& a, cudaStream_t s) {
+    const int block = std::max(a.tpr, 128), tiles = ceil_div(c.T, block / a.tpr);
+    auto kern = a.r ? norm_kernel<T, VE, NE, FULL, true> : norm_kernel<T, VE, NE, FULL, false>;
+    // blocks of 512 threads together, by registers (see norm_shape)
+    const int grid = std::min(tiles, num_sms() * (kNormThreads / block));
+    return launch_pdl(kern, dim3(grid), dim3(block), 0, s, a);
 }
 
 template <typename T, int VE>
 cudaError_t launch_norm(const moe_norm_config_t& c, NormArgs a, const Shape& sh, cudaStream_t s) {
+    constexpr int ES = (int)sizeof(T);
     a.tpr = sh.tpr;
     cudaError_t e;
-    if (sh.ne == 0) {
-        e = launch_pdl(norm_long_kernel<T, VE>, dim3(std::min(c.T, num_sms() * 2)), dim3(kLong), 0, s, a);
-    } else {
-        auto kern = sh.ne == 8 ? norm_kernel<T, VE, 8 / VE> : sh.ne == 16 ? norm_kernel<T, VE, 16 / VE>
-                                                            : norm_kernel<T, VE, 32 / VE>;
-        const int tiles = ceil_div(c.T, sh.block / sh.tpr);
-        e = launch_pdl(kern, dim3(std::min(tiles, num_sms() * 64)), dim3(sh.block), 0, s, a);
-    }
+    const bool full = VE > 1 && (int64_t)c.d * ES == (int64_t)sh.tpr * sh.bytes;
+    if (sh.bytes == 0) e = launch_pdl(norm_long_kernel<T, VE>, dim3(std::min(c.T, num_sms() * 2)), dim3(kLong), 0, s, a);
+    else if (sh.bytes == 16) e = full ? launch_norm_ne<T, VE, 16 / ES, VE != 1>(c, a, s) : launch_norm_ne<T, VE, 16 / ES, false>(c, a, s);
+    else if (sh.bytes == 32) e = full ? launch_norm_ne<T, VE, 32 / ES, VE != 1>(c, a, s) : launch_norm_ne<T, VE, 32 / ES, false>(c, a, s);
+    else e = full ? launch_norm_ne<T, VE, 64 / ES, VE != 1>(c, a, s) : launch_norm_ne<T, VE, 64 / ES, false>(c, a, s);
     count_launch();
     return e;
 }
 
 // Blocks whose partial sums norm_join_kernel adds up.
 int grad_blocks(const moe_norm_config_t& c, const Shape& sh) {
-    if (sh.ne == 0) return std::max(1, std::min(c.T, 16));
-    return std::max(1, std::min(ceil_div(c.T, sh.block / sh.tpr), num_sms() * (sh.block >= 512 ? 1 : 512 / sh.block)));
+    if (sh.bytes == 0) return std::max(1, std::min(c.T, 16));
+    return std::max(1, std::min(ceil_div(c.T, kGradThreads / sh.tpr), num_sms()));
+}
+
+template <typename T, int VE, int NE, bool FULL>
+cudaError_t launch_grad_ne(const moe_norm_config_t& c, const NormGradArgs& a, int blocks, cudaStream_t s) {
+    auto kern = norm_grad_kernel<T, VE, NE, FULL>;
+    const size_t ring = (size_t)a.stages * (a.dtotal && a.dx ? 3 : 2) * a.array_bytes;
+    const size_t smem = std::max(ring, (size_t)c.d * sizeof(float));
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kGradSmem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3(blocks), dim3(kGradThreads), smem, s, a);
 }
 
 template <typename T, int VE>
 cudaError_t launch_norm_grad(const moe_norm_config_t& c, NormGradArgs a, const Shape& sh, cudaStream_t s) {
+    constexpr int ES = (int)sizeof(T);
     a.tpr = sh.tpr;
     const int blocks = grad_blocks(c, sh);
     cudaError_t e = cudaSuccess;
-    if (sh.ne == 0) {
+    if (sh.bytes == 0) {
         if (a.part) {
             e = launch_pdl(norm_columns_kernel<T, VE>, dim3(ceil_div(c.d / VE, 256), blocks), dim3(256), 0, s, a);
             count_launch();
@@ -531,10 +736,16 @@ cudaError_t launch_norm_grad(const moe_norm_config_t& c, NormGradArgs a, const S
         }
         return e;
     }
-    auto kern = sh.ne == 8 ? norm_grad_kernel<T, VE, 8 / VE> : sh.ne == 16 ? norm_grad_kernel<T, VE, 16 / VE>
-                                                             : norm_grad_kernel<T, VE, 32 / VE>;
-    const size_t smem = sh.block > sh.tpr ? (size_t)c.d * sizeof(float) : 0;
-    e = launch_pdl(kern, dim3(blocks), dim3(sh.block), smem, s, a);
+    // a set of rows with what a copy takes in beside it, and as many stages as fit (2 at least: rows are 32 KB
+    // at most, arrays 3)
+    a.array_bytes = (int)align_up((size_t)(kGradThreads / sh.tpr) * c.d * ES + 32, 128);
+    const int stage_bytes = (a.dtotal && a.dx ? 3 : 2) * a.array_bytes;
+    a.stages = std::max(2, std::min(kMaxStages, kRingBytes / stage_bytes));
+    a.err = device_error_word();
+    const bool full = VE > 1 && (int64_t)c.d * ES == (int64_t)sh.tpr * sh.bytes;
+    if (sh.bytes == 16) e = full ? launch_grad_ne<T, VE, 16 / ES, VE != 1>(c, a, blocks, s) : launch_grad_ne<T, VE, 16 / ES, false>(c, a, blocks, s);
+    else if (sh.bytes == 32) e = full ? launch_grad_ne<T, VE, 32 / ES, VE != 1>(c, a, blocks, s) : launch_grad_ne<T, VE, 32 / ES, false>(c, a, blocks, s);
+    else e = full ? launch_grad_ne<T, VE, 64 / ES, VE != 1>(c, a, blocks, s) : launch_grad_ne<T, VE, 64 / ES, false>(c, a, blocks, s);
     count_launch();
     return e;
 }
@@ -598,7 +809,7 @@ extern "C" MOE_API moe_status_t moe_layer_norm_backward(const moe_norm_config_t*
     }
     const Shape sh = norm_shape(c);
     const NormGradArgs a{dy, x, gain, mean, rstd, dtotal, dx, sums ? static_cast<float*>(ws) : nullptr, c.T, c.d, sh.tpr,
-                         c.param_dtype == MOE_F32, 1.0f / (float)c.d};
+                         c.param_dtype == MOE_F32, 1.0f / (float)c.d, 0, 0, nullptr};
     cudaError_t e = c.dtype == MOE_BF16 ? MOE_NORM_VE(__nv_bfloat16, launch_norm_grad, c, a, sh, s)
                                         : MOE_NORM_VE(float, launch_norm_grad, c, a, sh, s);
     if (e == cudaSuccess && sums) {
