@@ -66,7 +66,7 @@ template <typename T, int VE, int NE, bool FULL>
 struct Part {
     static constexpr int NC = NE / VE, NP = NE / 2;
     Chunk<T, VE> c[NC];
-    __device__ __forceinline__ void load(const T* row, int lane, int tpr, int nvec, bool live) {
+    __device__ __forceinline__ void load(const T* row, int lane, int tpr, int nvec, bool live = true) {
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int at = lane + i * tpr;
@@ -173,13 +173,17 @@ int row_vec(int d, int es) {
 }
 
 // Sums over the `tpr` threads of a row (32 or more, a power of two; a block holds whole rows, `own` is the
-// row's number in it). `red` (a value to each warp) is free again after the next sum on another buffer.
+// row's number in it). `red` (a value to each warp) is free again after the next sum on another buffer. The row's
+// threads meet.
 __device__ __forceinline__ void row_sync(int tpr, int own) {
     asm volatile("bar.sync %0, %1;" ::"r"(own + 1), "r"(tpr) : "memory");
 }
 __device__ __forceinline__ float row_sum(float v, int tpr, int own, float* red) {
     v = warp_sum(v);
-    if (tpr == 32) return v;
+    if (tpr == 32) {
+        __syncwarp();
+        return v;
+    }
     const int warp = threadIdx.x >> 5, n = tpr >> 5;
     if ((threadIdx.x & 31) == 0) red[warp] = v;
     row_sync(tpr, own);
@@ -194,7 +198,10 @@ __device__ __forceinline__ float2 row_sum2(float2 v, int tpr, int own, float2* r
         v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
         v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
     }
-    if (tpr == 32) return v;
+    if (tpr == 32) {
+        __syncwarp();
+        return v;
+    }
     const int warp = threadIdx.x >> 5, n = tpr >> 5;
     if ((threadIdx.x & 31) == 0) red[warp] = v;
     row_sync(tpr, own);
@@ -213,6 +220,121 @@ __device__ __forceinline__ float pair_sum(const uint64_t (&p)[N]) {
     return lo + hi;
 }
 
+// ---------------------------------------------------------------- rows through shared memory
+// A ring of stages in shared memory, which rows reach by bulk copies: up to 180 KB are in flight to an SM
+// whatever the registers hold. A stage holds `per` adjacent rows of each of up to three arrays. A copy starts on
+// a 16-byte boundary: it takes in what lies before and behind odd rows, but for the end of the last one, whose
+// odd bytes a thread fetches.
+//
+// The forward pass has a ring to each row's group of threads, which wait for no other row; the gradient one to
+// the block, whose rows are one copy. Both ways measured: forward 16384 x 1024 bf16 with a residual 25.1 us and
+// 28, gradient 32768 x 2048 98 us and 89 (DRAM is read in pieces of 4 KB and 16).
+constexpr int kRingThreads = 512;         // threads of a block; one block to an SM
+constexpr int kMaxStages = 6;
+constexpr int kRingBytes = 180 * 1024;
+constexpr int kRingSmem = 200 * 1024;     // two stages of three rows of 32 KB
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(dst), "l"(src), "r"(bytes), "r"(tc::smem_u32(bar)) : "memory");
+}
+
+struct RingArgs {
+    int stages, array_bytes, arrays, per;
+    int* err;
+};
+
+// Arrays are named at each call, so that they stay in constant memory.
+template <typename T>
+struct Ring {
+    uint8_t* base;            // the stages
+    uint64_t* full;           // and their barriers
+    int tile, step, tiles;    // tiles of `per` rows: the current one, to the next, all
+    int row_bytes, stage;
+    uint32_t phase;
+    bool ok, lead;
+
+    // By all threads, before the first global access: `rings` to a block, this one `own`, filled by thread `lead_`.
+    __device__ __forceinline__ void init(const RingArgs& a, int T_, int d, int rings, int own, bool lead_, uint8_t* smem,
+                                         uint64_t* bars) {
+        row_bytes = d * (int)sizeof(T);
+        tiles = (T_ + a.per - 1) / a.per;
+        tile = blockIdx.x * rings + own;
+        step = gridDim.x * rings;
+        base = smem + (size_t)own * a.stages * a.arrays * a.array_bytes;
+        full = bars + own * kMaxStages;
+        stage = 0;
+        phase = 0;
+        ok = true;
+        lead = lead_;
+        if (lead) {
+            for (int i = 0; i < a.stages; ++i) tc::mbar_init(full + i, 1);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        __syncthreads();
+    }
+    __device__ __forceinline__ void tail(const char* src, uint32_t dst, int64_t from, int64_t upto, int64_t end) {
+        for (int64_t q = upto; q < end; q += sizeof(T)) {
+            if constexpr (sizeof(T) == 2)
+                asm volatile("st.shared.b16 [%0], %1;" ::"r"(dst + (uint32_t)(q - from)),
+                             "h"(*reinterpret_cast<const uint16_t*>(src + q)) : "memory");
+            else
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + (uint32_t)(q - from)),
+                             "r"(*reinterpret_cast<const uint32_t*>(src + q)) : "memory");
+        }
+    }
+    // Tile `t` into stage `to`, by the leading thread.
+    __device__ __forceinline__ void fill(const RingArgs& a, int T_, const void* p0, const void* p1, const void* p2, int t, int to) {
+        const int64_t all = (int64_t)T_ * row_bytes, begin = (int64_t)t * a.per * row_bytes, from = begin & ~(int64_t)15;
+        const int64_t end = min(begin + (int64_t)a.per * row_bytes, all);
+        const int64_t upto = min((end + 15) & ~(int64_t)15, all & ~(int64_t)15);    // not past the array
+        const uint32_t bytes = (uint32_t)(upto - from);
+        const uint32_t dst = tc::smem_u32(base) + (uint32_t)(to * a.arrays * a.array_bytes);
+        const char *src0 = static_cast<const char*>(p0), *src1 = static_cast<const char*>(p1), *src2 = static_cast<const char*>(p2);
+        if (upto < end) {
+            tail(src0, dst, from, upto, end);
+            if (a.arrays > 1) tail(src1, dst + a.array_bytes, from, upto, end);
+            if (a.arrays > 2) tail(src2, dst + 2 * a.array_bytes, from, upto, end);
+        }
+        // (the arrive makes the bytes stored above visible to whom waits)
+        tc::mbar_expect_tx(full + to, bytes * a.arrays);
+        if (bytes) {
+            bulk_load(dst, src0 + from, bytes, full + to);
+            if (a.arrays > 1) bulk_load(dst + a.array_bytes, src1 + from, bytes, full + to);
+            if (a.arrays > 2) bulk_load(dst + 2 * a.array_bytes, src2 + from, bytes, full + to);
+        }
+    }
+    __device__ __forceinline__ void start(const RingArgs& a, int T_, const void* p0, const void* p1, const void* p2) {
+        if (lead)
+            for (int i = 0; i < a.stages; ++i)
+                if (tile + i * step < tiles) fill(a, T_, p0, p1, p2, tile + i * step, i);
+    }
+    // The tile's first row in the first array (the others array_bytes apart), once it is there.
+    __device__ __forceinline__ const uint8_t* wait(const RingArgs& a) {
+        if (ok) ok = tc::mbar_wait(full + stage, phase, a.err);
+        return base + stage * a.arrays * a.array_bytes + (((uint32_t)tile * (uint32_t)a.per * (uint32_t)row_bytes) & 15u);
+    }
+    // All of the ring's threads have read the stage (and met since): it is filled again.
+    __device__ __forceinline__ void refill(const RingArgs& a, int T_, const void* p0, const void* p1, const void* p2) {
+        if (lead && ok && tile + a.stages * step < tiles) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            fill(a, T_, p0, p1, p2, tile + a.stages * step, stage);
+        }
+    }
+    __device__ __forceinline__ void next(const RingArgs& a) {
+        tile += step;
+        if (++stage == a.stages) {
+            stage = 0;
+            phase ^= 1;
+        }
+    }
+    // After the last tile: no copy may be in flight when the block leaves.
+    __device__ __forceinline__ void finish(const RingArgs& a) {
+        if (!ok && lead)
+            for (int i = 0; i < a.stages; ++i) tc::mbar_wait(full + i, phase, a.err);
+    }
+};
+
 struct NormArgs {
     const void* x;
     const void* r;
@@ -228,65 +350,59 @@ struct NormArgs {
 };
 
 // A row to `tpr` threads, in registers between the reading and the writing: the mean, then the squares
-// of the differences, then the output; gain and bias stay in registers from row to row, and the next row is
-// on its way while one is worked on. Bound by memory.
-constexpr int kMaxRow = 512;      // threads to a row at most
-constexpr int kNormThreads = 640; // threads on an SM that launches count on
+// of the differences, then the output; gain and bias stay in registers from row to row. Bound by memory.
+constexpr int kMaxRow = kRingThreads;      // threads to a row at most
 template <typename T, int VE, int NE, bool FULL, bool RES>
-__global__ void __launch_bounds__(kMaxRow) norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kRingThreads, 1) norm_kernel(const NormArgs a, const RingArgs ra) {
     using P = Part<T, VE, NE, FULL>;
     constexpr int NP = NE / 2;
-    constexpr bool AHEAD = NE * (int)sizeof(T) <= 32;       // longer parts have no registers left for it
-    __shared__ float s_red[2][kMaxRow / 32];
+    __shared__ float s_red[2][kRingThreads / 32];
+    __shared__ uint64_t s_full[kRingThreads / 32 * kMaxStages];
+    extern __shared__ __align__(128) uint8_t s_ring[];
+    const int own = threadIdx.x / a.tpr, lane = threadIdx.x - own * a.tpr, nvec = a.d / VE;
+    Ring<T> ring;
+    ring.init(ra, a.T, a.d, kRingThreads / a.tpr, own, lane == 0, s_ring, s_full);
     pdl_wait();
-    const int own = threadIdx.x / a.tpr, lane = threadIdx.x - own * a.tpr, rows = blockDim.x / a.tpr, nvec = a.d / VE;
-    const T* x = static_cast<const T*>(a.x);
-    const T* r = static_cast<const T*>(a.r);
+    ring.start(ra, a.T, a.x, a.r, nullptr);
     uint64_t gain[NP], bias[NP];
     P::params(a.gain, a.p32, 1.f, lane, a.tpr, nvec, gain);
     P::params(a.bias, a.p32, 0.f, lane, a.tpr, nvec, bias);
-    const int64_t step = (int64_t)gridDim.x * rows;
-    int64_t t = (int64_t)blockIdx.x * rows + own;
-    P px, pr;
-    if (AHEAD) {
-        px.load(x + t * a.d, lane, a.tpr, nvec, t < a.T);
-        if (RES) pr.load(r + t * a.d, lane, a.tpr, nvec, t < a.T);
-    }
-    for (; t < a.T; t += step) {
-        if (!AHEAD) {
-            px.load(x + t * a.d, lane, a.tpr, nvec, true);
-            if (RES) pr.load(r + t * a.d, lane, a.tpr, nvec, true);
-        }
-        uint64_t v[NP];
-        px.pairs(v);
-        if (RES) {
-            uint64_t q[NP];
-            pr.pairs(q);
+    for (; ring.tile < ring.tiles; ring.next(ra)) {
+        const uint8_t* at = ring.wait(ra);
+        const int t0 = ring.tile * ra.per, t1 = min(t0 + ra.per, a.T);
+        for (int t = t0; t < t1; ++t, at += ring.row_bytes) {
+            uint64_t v[NP];
+            P part;
+            part.load(reinterpret_cast<const T*>(at), lane, a.tpr, nvec);
+            part.pairs(v);
+            if (RES) {
+                uint64_t w[NP];
+                part.load(reinterpret_cast<const T*>(at + ra.array_bytes), lane, a.tpr, nvec);
+                part.pairs(w);
 #pragma unroll
-            for (int i = 0; i < NP; ++i) v[i] = add2(v[i], q[i]);
-        }
-        if (AHEAD) {
-            px.load(x + (t + step) * a.d, lane, a.tpr, nvec, t + step < a.T);
-            if (RES) pr.load(r + (t + step) * a.d, lane, a.tpr, nvec, t + step < a.T);
-        }
-        if (RES) P::store(static_cast<T*>(a.total) + t * a.d, lane, a.tpr, nvec, v);
-        const float mean = row_sum(pair_sum(v), a.tpr, own, s_red[0]) * a.inv_d;
-        uint64_t sq[NP];
+                for (int i = 0; i < NP; ++i) v[i] = add2(v[i], w[i]);
+            }
+            const float mean = row_sum(pair_sum(v), a.tpr, own, s_red[0]) * a.inv_d;
+            if (t + 1 == t1) ring.refill(ra, a.T, a.x, a.r, nullptr);
+            if (RES) P::store(static_cast<T*>(a.total) + (int64_t)t * a.d, lane, a.tpr, nvec, v);
+            uint64_t sq[NP];
 #pragma unroll
-        for (int i = 0; i < NP; ++i) v[i] = add2(v[i], splat2(-mean));
-        P::cut(lane, a.tpr, nvec, v);
+            for (int i = 0; i < NP; ++i) v[i] = add2(v[i], splat2(-mean));
+            P::cut(lane, a.tpr, nvec, v);
 #pragma unroll
-        for (int i = 0; i < NP; ++i) sq[i] = mul2(v[i], v[i]);
-        const float var = row_sum(pair_sum(sq), a.tpr, own, s_red[1]) * a.inv_d;
-        const float rstd = 1.0f / sqrtf(var + a.eps);
+            for (int i = 0; i < NP; ++i) sq[i] = mul2(v[i], v[i]);
+            const float var = row_sum(pair_sum(sq), a.tpr, own, s_red[1]) * a.inv_d;
+            const float rstd = 1.0f / sqrtf(var + a.eps);
 #pragma unroll
-        for (int i = 0; i < NP; ++i) v[i] = fma2(mul2(v[i], splat2(rstd)), gain[i], bias[i]);
-        P::store(static_cast<T*>(a.y) + t * a.d, lane, a.tpr, nvec, v);
-        if (lane == 0) {
-            if (a.mean) a.mean[t] = mean;
-            if (a.rstd) a.rstd[t] = rstd;
+            for (int i = 0; i < NP; ++i) v[i] = fma2(mul2(v[i], splat2(rstd)), gain[i], bias[i]);
+            P::store(static_cast<T*>(a.y) + (int64_t)t * a.d, lane, a.tpr, nvec, v);
+            if (lane == 0) {
+                if (a.mean) a.mean[t] = mean;
+                if (a.rstd) a.rstd[t] = rstd;
+            }
         }
     }
+    ring.finish(ra);
 }
 
 // Rows too long for registers: a block to a row, three passes over it (the later ones from L2).
@@ -368,33 +484,21 @@ struct NormGradArgs {
 // up dgain and dbias in registers; a block's rows join in shared memory at the end. One block to an SM: its
 // partial sums are what the joining kernel reads.
 //
-// Bound by memory, and registers are full of sums, so rows come ahead through a ring in shared memory: the
-// rows that a block works on at once are adjacent, so a stage is one bulk copy each of dy, s and dtotal, up to
-// 150 KB in flight. A copy starts on a 16-byte boundary: it takes in what lies before and behind odd rows,
-// but for the end of the last one, whose odd bytes a thread fetches.
-constexpr int kGradThreads = 512;
-constexpr int kMaxStages = 6;
-constexpr int kRingBytes = 180 * 1024;
-constexpr int kGradSmem = 200 * 1024;
-
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                 ::"r"(dst), "l"(src), "r"(bytes), "r"(tc::smem_u32(bar)) : "memory");
-}
-
+// Bound by memory, with registers full of sums. Rows come through one ring to the block, as in Ring, but written
+// out: through that struct this kernel takes 95 us where it takes 89 (32768 x 2048 bf16).
 template <typename T, int VE, int NE, bool FULL>
-__global__ void __launch_bounds__(kGradThreads, 1) norm_grad_kernel(const NormGradArgs a) {
+__global__ void __launch_bounds__(kRingThreads, 1) norm_grad_kernel(const NormGradArgs a) {
     using P = Part<T, VE, NE, FULL>;
     constexpr int NP = NE / 2;
-    __shared__ float2 s_red[2][kGradThreads / 32];
+    __shared__ float2 s_red[2][kRingThreads / 32];
     __shared__ uint64_t s_full[kMaxStages], s_empty[kMaxStages];
     extern __shared__ __align__(128) uint8_t s_ring[];
-    const int own = threadIdx.x / a.tpr, lane = threadIdx.x - own * a.tpr, rows = kGradThreads / a.tpr, nvec = a.d / VE;
+    const int own = threadIdx.x / a.tpr, lane = threadIdx.x - own * a.tpr, rows = kRingThreads / a.tpr, nvec = a.d / VE;
     const int arrays = a.dtotal && a.dx ? 3 : 2;
     if (threadIdx.x == 0) {
         for (int i = 0; i < a.stages; ++i) {
             tc::mbar_init(s_full + i, 1);
-            tc::mbar_init(s_empty + i, kGradThreads / 32);
+            tc::mbar_init(s_empty + i, kRingThreads / 32);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
@@ -680,13 +784,28 @@ Shape norm_shape(const moe_norm_config_t& c) {
     return s;
 }
 
+// The forward pass: adjacent rows to a copy, 2 KB of short ones, but not so many that groups of threads have none.
+int rows_per_copy(const moe_norm_config_t& c, const Shape& sh) {
+    const int row = c.d * (c.dtype == MOE_BF16 ? 2 : 4), groups = num_sms() * (kRingThreads / sh.tpr);
+    return std::max(1, std::min(2048 / row, c.T / groups));
+}
+
 template <typename T, int VE, int NE, bool FULL>
-cudaError_t launch_norm_ne(const moe_norm_config_t& c, const NormArgs& a, cudaStream_t s) {
-    const int block = std::max(a.tpr, 128), tiles = ceil_div(c.T, block / a.tpr);
+cudaError_t launch_norm_ne(const moe_norm_config_t& c, const NormArgs& a, const Shape& sh, cudaStream_t s) {
+    // as many stages as fit (2 at least)
+    const int groups = kRingThreads / sh.tpr;
+    RingArgs r;
+    r.arrays = a.r ? 2 : 1;
+    r.per = rows_per_copy(c, sh);
+    r.array_bytes = (int)align_up((size_t)r.per * c.d * sizeof(T) + 32, 128);
+    r.stages = std::max(2, std::min(kMaxStages, kRingBytes / (groups * r.arrays * r.array_bytes)));
+    r.err = device_error_word();
+    const size_t bytes = (size_t)groups * r.stages * r.arrays * r.array_bytes;
+    const int blocks = std::min(ceil_div(ceil_div(c.T, r.per), groups), num_sms());
     auto kern = a.r ? norm_kernel<T, VE, NE, FULL, true> : norm_kernel<T, VE, NE, FULL, false>;
-    // blocks of 512 threads together, by registers (see norm_shape)
-    const int grid = std::min(tiles, num_sms() * (kNormThreads / block));
-    return launch_pdl(kern, dim3(grid), dim3(block), 0, s, a);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3(blocks), dim3(kRingThreads), bytes, s, a, r);
 }
 
 template <typename T, int VE>
@@ -694,39 +813,43 @@ cudaError_t launch_norm(const moe_norm_config_t& c, NormArgs a, const Shape& sh,
     constexpr int ES = (int)sizeof(T);
     a.tpr = sh.tpr;
     cudaError_t e;
-    const bool full = VE > 1 && (int64_t)c.d * ES == (int64_t)sh.tpr * sh.bytes;
+    constexpr bool WIDE = VE * ES == 16;      // (rows of other vectors are never taken as whole)
+    const bool full = WIDE && (int64_t)c.d * ES == (int64_t)sh.tpr * sh.bytes;
     if (sh.bytes == 0) e = launch_pdl(norm_long_kernel<T, VE>, dim3(std::min(c.T, num_sms() * 2)), dim3(kLong), 0, s, a);
-    else if (sh.bytes == 16) e = full ? launch_norm_ne<T, VE, 16 / ES, VE != 1>(c, a, s) : launch_norm_ne<T, VE, 16 / ES, false>(c, a, s);
-    else if (sh.bytes == 32) e = full ? launch_norm_ne<T, VE, 32 / ES, VE != 1>(c, a, s) : launch_norm_ne<T, VE, 32 / ES, false>(c, a, s);
-    else e = full ? launch_norm_ne<T, VE, 64 / ES, VE != 1>(c, a, s) : launch_norm_ne<T, VE, 64 / ES, false>(c, a, s);
+    else if (sh.bytes == 16) e = full ? launch_norm_ne<T, VE, 16 / ES, WIDE>(c, a, sh, s) : launch_norm_ne<T, VE, 16 / ES, false>(c, a, sh, s);
+    else if (sh.bytes == 32) e = full ? launch_norm_ne<T, VE, 32 / ES, WIDE>(c, a, sh, s) : launch_norm_ne<T, VE, 32 / ES, false>(c, a, sh, s);
+    else e = full ? launch_norm_ne<T, VE, 64 / ES, WIDE>(c, a, sh, s) : launch_norm_ne<T, VE, 64 / ES, false>(c, a, sh, s);
     count_launch();
     return e;
 }
 
 // Blocks whose partial sums norm_join_kernel adds up.
 int grad_blocks(const moe_norm_config_t& c, const Shape& sh) {
-    if (sh.bytes == 0) return std::max(1, std::min(c.T, 16));
-    return std::max(1, std::min(ceil_div(c.T, kGradThreads / sh.tpr), num_sms()));
+    return std::max(1, sh.bytes == 0 ? std::min(c.T, 16) : std::min(ceil_div(c.T, kRingThreads / sh.tpr), num_sms()));
 }
 
 template <typename T, int VE, int NE, bool FULL>
-cudaError_t launch_grad_ne(const moe_norm_config_t& c, const NormGradArgs& a, int blocks, cudaStream_t s) {
+cudaError_t launch_grad_ne(const moe_norm_config_t& c, const NormGradArgs& a, const Shape& sh, cudaStream_t s) {
     auto kern = norm_grad_kernel<T, VE, NE, FULL>;
-    const size_t ring = (size_t)a.stages * (a.dtotal && a.dx ? 3 : 2) * a.array_bytes;
-    const size_t smem = std::max(ring, (size_t)c.d * sizeof(float));
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kGradSmem);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(blocks), dim3(kGradThreads), smem, s, a);
+    const size_t ring = (size_t)a.stages * (a.dtotal && a.dx ? 3 : 2) * a.array_bytes;
+    return launch_pdl(kern, dim3(grad_blocks(c, sh)), dim3(kRingThreads), std::max(ring, (size_t)c.d * sizeof(float)), s, a);
 }
 
 template <typename T, int VE>
 cudaError_t launch_norm_grad(const moe_norm_config_t& c, NormGradArgs a, const Shape& sh, cudaStream_t s) {
     constexpr int ES = (int)sizeof(T);
     a.tpr = sh.tpr;
-    const int blocks = grad_blocks(c, sh);
+    // the rows that a block works on at once with what a copy takes in beside them, and as many stages as fit (2
+    // at least: rows are 32 KB at most, arrays 3)
+    a.array_bytes = (int)align_up((size_t)(kRingThreads / sh.tpr) * c.d * ES + 32, 128);
+    a.stages = std::max(2, std::min(kMaxStages, kRingBytes / ((a.dtotal && a.dx ? 3 : 2) * a.array_bytes)));
+    a.err = device_error_word();
     cudaError_t e = cudaSuccess;
     if (sh.bytes == 0) {
         if (a.part) {
+            const int blocks = grad_blocks(c, sh);
             e = launch_pdl(norm_columns_kernel<T, VE>, dim3(ceil_div(c.d / VE, 256), blocks), dim3(256), 0, s, a);
             count_launch();
         }
@@ -736,16 +859,11 @@ cudaError_t launch_norm_grad(const moe_norm_config_t& c, NormGradArgs a, const S
         }
         return e;
     }
-    // a set of rows with what a copy takes in beside it, and as many stages as fit (2 at least: rows are 32 KB
-    // at most, arrays 3)
-    a.array_bytes = (int)align_up((size_t)(kGradThreads / sh.tpr) * c.d * ES + 32, 128);
-    const int stage_bytes = (a.dtotal && a.dx ? 3 : 2) * a.array_bytes;
-    a.stages = std::max(2, std::min(kMaxStages, kRingBytes / stage_bytes));
-    a.err = device_error_word();
-    const bool full = VE > 1 && (int64_t)c.d * ES == (int64_t)sh.tpr * sh.bytes;
-    if (sh.bytes == 16) e = full ? launch_grad_ne<T, VE, 16 / ES, VE != 1>(c, a, blocks, s) : launch_grad_ne<T, VE, 16 / ES, false>(c, a, blocks, s);
-    else if (sh.bytes == 32) e = full ? launch_grad_ne<T, VE, 32 / ES, VE != 1>(c, a, blocks, s) : launch_grad_ne<T, VE, 32 / ES, false>(c, a, blocks, s);
-    else e = full ? launch_grad_ne<T, VE, 64 / ES, VE != 1>(c, a, blocks, s) : launch_grad_ne<T, VE, 64 / ES, false>(c, a, blocks, s);
+    constexpr bool WIDE = VE * ES == 16;      // (rows of other vectors are never taken as whole)
+    const bool full = WIDE && (int64_t)c.d * ES == (int64_t)sh.tpr * sh.bytes;
+    if (sh.bytes == 16) e = full ? launch_grad_ne<T, VE, 16 / ES, WIDE>(c, a, sh, s) : launch_grad_ne<T, VE, 16 / ES, false>(c, a, sh, s);
+    else if (sh.bytes == 32) e = full ? launch_grad_ne<T, VE, 32 / ES, WIDE>(c, a, sh, s) : launch_grad_ne<T, VE, 32 / ES, false>(c, a, sh, s);
+    else e = full ? launch_grad_ne<T, VE, 64 / ES, WIDE>(c, a, sh, s) : launch_grad_ne<T, VE, 64 / ES, false>(c, a, sh, s);
     count_launch();
     return e;
 }

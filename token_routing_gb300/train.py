@@ -37,13 +37,46 @@ def _one_gpu(first, *rest):
     raise ValueError(f"tensors on devices {on} (-1: the host): all have to be on one GPU")
 
 
-def _launch(what, gpu, stream, fn, *args):
+def _arg(what, t, dtype, shape, gpu):
+    """The address of a contiguous tensor of this type and shape on GPU `gpu`; others are refused, as the C
+    call sees only the address. One pass over what the tensor says: small calls are as long as their checks."""
+    if t is not None and t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == gpu:
+        return t.data_ptr()
+    _want(what, t, dtype, shape)
+    raise ValueError(f"{what} is on device {t.get_device()}, another tensor on {gpu} (-1: the host): all have to be "
+                     "on one GPU")
+
+
+def _opt(what, t, dtype, shape, gpu):
+    return None if t is None else _arg(what, t, dtype, shape, gpu)
+
+
+def _work(ws, need, gpu):
+    """The address of a workspace of `need` bytes on GPU `gpu`."""
+    if ws is None or ws.nbytes < need or not ws.is_contiguous():
+        raise ValueError(f"ws: {need} contiguous bytes are needed")
+    if ws.get_device() != gpu:
+        raise ValueError(f"ws is on device {ws.get_device()}, other tensors on {gpu}: all have to be on one GPU")
+    return ws.data_ptr()
+
+
+_CALLS = {}
+
+
+def _launch(what, gpu, stream, *args):
     """One C call on tensors of GPU `gpu`, which need not be the current one."""
+    if gpu < 0:
+        raise ValueError("tensors on the host: all have to be on one GPU")
+    fn = _CALLS.get(what)
+    if fn is None:
+        fn = _CALLS[what] = getattr(L.load(), what)
     if torch._C._cuda_getDevice() == gpu:
-        L.check(what, fn(*args, _stream(stream, gpu)))
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(gpu) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(gpu):
-            L.check(what, fn(*args, _stream(stream, gpu)))
+            status = fn(*args, _stream(stream, gpu))
+    if status:
+        raise L.MoeError(what, status)
 
 
 def _want(what, t, dtype, shape, optional=False):
@@ -265,30 +298,21 @@ def route_scores(cfg, logits, bias, idx, w, counts=None, balance_loss=None, ws=N
     """idx [T, k] int32 and w [T, k] fp32 from logits [T, E] fp32 (moe_route's `logits`) and bias [E] fp32
     (or None) by scores, groups and top-k; counts [E] int32 and balance_loss [1] fp32 (each may be None;
     ws is needed for them)."""
-    T, E, k = cfg.T, cfg.E, cfg.k
-    _want("logits", logits, torch.float32, (T, E))
-    _want("bias", bias, torch.float32, (E,), True)
-    _want("idx", idx, torch.int32, (T, k))
-    _want("w", w, torch.float32, (T, k))
-    _want("counts", counts, torch.int32, (E,), True)
-    _want("balance_loss", balance_loss, torch.float32, (1,), True)
-    if counts is not None or balance_loss is not None:
-        _room("ws", ws, route_scores_workspace_bytes(cfg))
-    gpu = _one_gpu(logits, bias, idx, w, counts, balance_loss, ws)
-    _launch("moe_route_scores", gpu, stream, L.load().moe_route_scores, ctypes.byref(cfg), _ptr(logits), _ptr(bias),
-            _ptr(idx), _ptr(w), _ptr(counts), _ptr(balance_loss), _ptr(ws))
+    T, E, k, f32, i32, gpu = cfg.T, cfg.E, cfg.k, torch.float32, torch.int32, logits.get_device()
+    args = (_arg("logits", logits, f32, (T, E), gpu), _opt("bias", bias, f32, (E,), gpu),
+            _arg("idx", idx, i32, (T, k), gpu), _arg("w", w, f32, (T, k), gpu), _opt("counts", counts, i32, (E,), gpu),
+            _opt("balance_loss", balance_loss, f32, (1,), gpu))
+    tally = counts is not None or balance_loss is not None
+    at = _work(ws, route_scores_workspace_bytes(cfg), gpu) if tally else None
+    _launch("moe_route_scores", gpu, stream, ctypes.byref(cfg), *args, at)
 
 
 def route_scores_backward(cfg, logits, idx, dw, dlogits, stream=None):
     """dlogits [T, E] = the gradient of sum(w * dw) in the logits."""
-    T, E, k = cfg.T, cfg.E, cfg.k
-    _want("logits", logits, torch.float32, (T, E))
-    _want("idx", idx, torch.int32, (T, k))
-    _want("dw", dw, torch.float32, (T, k))
-    _want("dlogits", dlogits, torch.float32, (T, E))
-    gpu = _one_gpu(logits, idx, dw, dlogits)
-    _launch("moe_route_scores_backward", gpu, stream, L.load().moe_route_scores_backward, ctypes.byref(cfg),
-            _ptr(logits), _ptr(idx), _ptr(dw), _ptr(dlogits))
+    T, E, k, f32, gpu = cfg.T, cfg.E, cfg.k, torch.float32, logits.get_device()
+    _launch("moe_route_scores_backward", gpu, stream, ctypes.byref(cfg), _arg("logits", logits, f32, (T, E), gpu),
+            _arg("idx", idx, torch.int32, (T, k), gpu), _arg("dw", dw, f32, (T, k), gpu),
+            _arg("dlogits", dlogits, f32, (T, E), gpu))
 
 
 # ---------------------------------------------------------------- layer norm
@@ -306,38 +330,27 @@ def norm_workspace_bytes(cfg):
 def layer_norm(cfg, x, gain, bias, y, residual=None, total=None, mean=None, rstd=None, stream=None):
     """y [T, d] = the norm of x + residual, total [T, d] = that sum (both or neither of residual and
     total); mean, rstd [T] fp32 for the backward pass; gain, bias [d] may be None."""
-    dt, pt, shape = _TORCH[cfg.dtype], _TORCH[cfg.param_dtype], (cfg.T, cfg.d)
-    _want("x", x, dt, shape)
-    _want("gain", gain, pt, (cfg.d,), True)
-    _want("bias", bias, pt, (cfg.d,), True)
-    _want("y", y, dt, shape)
-    _want("residual", residual, dt, shape, total is None)
-    _want("total", total, dt, shape, residual is None)
-    _want("mean", mean, torch.float32, (cfg.T,), True)
-    _want("rstd", rstd, torch.float32, (cfg.T,), True)
-    gpu = _one_gpu(x, gain, bias, y, residual, total, mean, rstd)
-    _launch("moe_layer_norm", gpu, stream, L.load().moe_layer_norm, ctypes.byref(cfg), _ptr(x), _ptr(residual),
-            _ptr(gain), _ptr(bias), _ptr(total), _ptr(y), _ptr(mean), _ptr(rstd))
+    T, d, dt, pt, f32, gpu = cfg.T, cfg.d, _TORCH[cfg.dtype], _TORCH[cfg.param_dtype], torch.float32, x.get_device()
+    shape, row, col = (T, d), (d,), (T,)
+    both = residual is not None or total is not None
+    _launch("moe_layer_norm", gpu, stream, ctypes.byref(cfg), _arg("x", x, dt, shape, gpu),
+            _arg("residual", residual, dt, shape, gpu) if both else None, _opt("gain", gain, pt, row, gpu),
+            _opt("bias", bias, pt, row, gpu), _arg("total", total, dt, shape, gpu) if both else None,
+            _arg("y", y, dt, shape, gpu), _opt("mean", mean, f32, col, gpu), _opt("rstd", rstd, f32, col, gpu))
 
 
 def layer_norm_backward(cfg, dy, s, gain, mean, rstd, dx, dgain, dbias, ws, dtotal=None, stream=None):
     """dx [T, d] (+ dtotal, the gradient that reaches the sum itself) and dgain, dbias [d] fp32 from dy and
     the forward's s (its total, or x), mean and rstd. dx, dgain and dbias may each be None."""
-    dt, shape, f32 = _TORCH[cfg.dtype], (cfg.T, cfg.d), torch.float32
-    _want("dy", dy, dt, shape)
-    _want("s", s, dt, shape)
-    _want("gain", gain, _TORCH[cfg.param_dtype], (cfg.d,), True)
-    _want("mean", mean, f32, (cfg.T,))
-    _want("rstd", rstd, f32, (cfg.T,))
-    _want("dtotal", dtotal, dt, shape, True)
-    _want("dx", dx, dt, shape, True)
-    _want("dgain", dgain, f32, (cfg.d,), True)
-    _want("dbias", dbias, f32, (cfg.d,), True)
-    if dgain is not None or dbias is not None:
-        _room("ws", ws, norm_workspace_bytes(cfg))
-    gpu = _one_gpu(dy, s, gain, mean, rstd, dtotal, dx, dgain, dbias, ws)
-    _launch("moe_layer_norm_backward", gpu, stream, L.load().moe_layer_norm_backward, ctypes.byref(cfg), _ptr(dy),
-            _ptr(s), _ptr(gain), _ptr(mean), _ptr(rstd), _ptr(dtotal), _ptr(dx), _ptr(dgain), _ptr(dbias), _ptr(ws))
+    T, d, dt, f32, gpu = cfg.T, cfg.d, _TORCH[cfg.dtype], torch.float32, dy.get_device()
+    shape, row, col = (T, d), (d,), (T,)
+    args = (_arg("dy", dy, dt, shape, gpu), _arg("s", s, dt, shape, gpu),
+            _opt("gain", gain, _TORCH[cfg.param_dtype], row, gpu), _arg("mean", mean, f32, col, gpu),
+            _arg("rstd", rstd, f32, col, gpu), _opt("dtotal", dtotal, dt, shape, gpu), _opt("dx", dx, dt, shape, gpu),
+            _opt("dgain", dgain, f32, row, gpu), _opt("dbias", dbias, f32, row, gpu))
+    sums = dgain is not None or dbias is not None
+    _launch("moe_layer_norm_backward", gpu, stream, ctypes.byref(cfg), *args,
+            _work(ws, norm_workspace_bytes(cfg), gpu) if sums else None)
 
 
 # ---------------------------------------------------------------- orthogonalised updates (Muon)
@@ -364,12 +377,9 @@ def muon_workspace_bytes(cfg):
 
 def orthogonalize(cfg, g, o, ws, stream=None):
     """o [count, rows, cols] = g with the singular values of each matrix brought near 1. o may be g."""
-    shape = (cfg.count, cfg.rows, cfg.cols)
-    _want("g", g, _TORCH[cfg.grad_dtype], shape)
-    _want("o", o, _TORCH[cfg.dtype], shape)
-    _room("ws", ws, muon_workspace_bytes(cfg))
-    gpu = _one_gpu(g, o, ws)
-    _launch("moe_orthogonalize", gpu, stream, L.load().moe_orthogonalize, ctypes.byref(cfg), _ptr(g), _ptr(o), _ptr(ws))
+    shape, gpu = (cfg.count, cfg.rows, cfg.cols), g.get_device()
+    _launch("moe_orthogonalize", gpu, stream, ctypes.byref(cfg), _arg("g", g, _TORCH[cfg.grad_dtype], shape, gpu),
+            _arg("o", o, _TORCH[cfg.dtype], shape, gpu), _work(ws, muon_workspace_bytes(cfg), gpu))
 
 
 class Muon:
@@ -435,5 +445,5 @@ class Muon:
             self.placed = _one_gpu(self.ws, *(t[k] for t in self.tensors for k in ("p", "g", "m", "master")))
         gpu = _one_gpu(self.ws, lr, grad_scale)
         for t in self.tensors:
-            _launch("moe_muon", gpu, stream, L.load().moe_muon, ctypes.byref(t["cfg"]), _ptr(t["p"]), _ptr(t["g"]),
+            _launch("moe_muon", gpu, stream, ctypes.byref(t["cfg"]), _ptr(t["p"]), _ptr(t["g"]),
                     _ptr(t["master"]), _ptr(t["m"]), _ptr(lr), _ptr(grad_scale), _ptr(self.ws))
