@@ -434,38 +434,58 @@ __device__ __forceinline__ void load_v(const G* p, float (&f)[V]) {
     }
 }
 
-// u = g (+ momentum), the momentum written in the first pass.
-template <typename G, int V, bool FIRST>
-__device__ __forceinline__ void update_v(const MuonPrep& a, int64_t at, float gs, float (&u)[V]) {
-    load_v<G, V>(static_cast<const G*>(a.g) + at, u);
-    if (!a.m) return;
-    float m[V];
-    if constexpr (V == 1) {
-        m[0] = a.m[at];
-    } else {
-#pragma unroll
-        for (int q = 0; q < V; q += 4) *reinterpret_cast<float4*>(m + q) = *reinterpret_cast<const float4*>(a.m + at + q);
-    }
-#pragma unroll
-    for (int q = 0; q < V; ++q) {
-        u[q] *= gs;
-        if (FIRST) m[q] = fmaf(a.momentum, m[q], u[q]);
-    }
-    if (FIRST) {
+// The gradient and momentum of V elements, and u = g (+ momentum); the first pass writes the momentum.
+template <typename G, int V, bool MOMENTUM>
+struct Update {
+    static constexpr int NG = V == 1 ? 1 : V * (int)sizeof(G) / 16;
+    G one;                    // V = 1
+    uint4 g[NG];              // V = 8, as it is in memory
+    float m[MOMENTUM ? V : 1];
+    __device__ __forceinline__ void load(const MuonPrep& a, int64_t at) {
+        const G* p = static_cast<const G*>(a.g) + at;
         if constexpr (V == 1) {
-            a.m[at] = m[0];
+            one = *p;
+            if (MOMENTUM) m[0] = a.m[at];
         } else {
 #pragma unroll
-            for (int q = 0; q < V; q += 4) *reinterpret_cast<float4*>(a.m + at + q) = *reinterpret_cast<float4*>(m + q);
+            for (int q = 0; q < NG; ++q) g[q] = __ldg(reinterpret_cast<const uint4*>(p) + q);
+            if constexpr (MOMENTUM) {
+#pragma unroll
+                for (int q = 0; q < V; q += 4) *reinterpret_cast<float4*>(m + q) = *reinterpret_cast<const float4*>(a.m + at + q);
+            }
         }
     }
+    template <bool FIRST>
+    __device__ __forceinline__ void step(const MuonPrep& a, int64_t at, float gs, float (&u)[V]) {
+        if constexpr (V == 1) {
+            u[0] = Elem<G>::to_f(one);
+        } else {
 #pragma unroll
-    for (int q = 0; q < V; ++q) u[q] = a.nesterov ? fmaf(a.momentum, m[q], u[q]) : m[q];
-}
+            for (int q = 0; q < NG; ++q) unpack16<G>(g[q], u + q * (16 / (int)sizeof(G)));
+        }
+        if constexpr (MOMENTUM) {
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                u[q] *= gs;
+                if (FIRST) m[q] = fmaf(a.momentum, m[q], u[q]);
+            }
+            if constexpr (FIRST && V == 1) a.m[at] = m[0];
+            if constexpr (FIRST && V > 1) {
+#pragma unroll
+                for (int q = 0; q < V; q += 4) *reinterpret_cast<float4*>(a.m + at + q) = *reinterpret_cast<float4*>(m + q);
+            }
+#pragma unroll
+            for (int q = 0; q < V; ++q) u[q] = a.nesterov ? fmaf(a.momentum, m[q], u[q]) : m[q];
+        }
+    }
+};
+// Vectors that a thread has in flight. (One, with 2048 threads to an SM, read 4 TB/s.)
+template <bool MOMENTUM> constexpr int kAhead = MOMENTUM ? 2 : 4;
 
 // First pass: momentum, and the sum of squares of each chunk of a matrix.
-template <typename G, int V>
-__global__ void __launch_bounds__(kPrepThreads) muon_sums_kernel(const MuonPrep a) {
+template <typename G, int V, bool MOMENTUM>
+__global__ void __launch_bounds__(kPrepThreads, 4) muon_sums_kernel(const MuonPrep a) {
+    constexpr int U = kAhead<MOMENTUM>;
     __shared__ float s_sum[kPrepThreads / 32];
     pdl_wait();
     const float gs = a.grad_scale ? __ldg(a.grad_scale) : 1.f;
@@ -473,13 +493,21 @@ __global__ void __launch_bounds__(kPrepThreads) muon_sums_kernel(const MuonPrep 
         const int64_t z = w / a.chunks, c = w - z * a.chunks;
         const int64_t end = min(a.n, (c + 1) * a.chunk);
         float sum = 0.f;
-        for (int64_t i = c * a.chunk + threadIdx.x * V; i < end; i += kPrepThreads * V) {
-            float u[V];
-            update_v<G, V, true>(a, z * a.n + i, gs, u);
-            float part = 0.f;
+        for (int64_t i = c * a.chunk + threadIdx.x * V; i < end; i += kPrepThreads * V * U) {
+            Update<G, V, MOMENTUM> x[U];
 #pragma unroll
-            for (int q = 0; q < V; ++q) part = fmaf(u[q], u[q], part);
-            sum += part;
+            for (int k = 0; k < U; ++k)
+                if (i + k * kPrepThreads * V < end) x[k].load(a, z * a.n + i + k * kPrepThreads * V);
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                if (i + k * kPrepThreads * V >= end) break;
+                float u[V];
+                x[k].template step<true>(a, z * a.n + i + k * kPrepThreads * V, gs, u);
+                float part = 0.f;
+#pragma unroll
+                for (int q = 0; q < V; ++q) part = fmaf(u[q], u[q], part);
+                sum += part;
+            }
         }
         sum = warp_sum(sum);
         if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = sum;
@@ -493,8 +521,9 @@ __global__ void __launch_bounds__(kPrepThreads) muon_sums_kernel(const MuonPrep 
 }
 
 // Second pass: X = u / (|u| + eps), in fp16 parts.
-template <typename G, int V, bool SPLIT>
-__global__ void __launch_bounds__(kPrepThreads) muon_scale_kernel(const MuonPrep a) {
+template <typename G, int V, bool SPLIT, bool MOMENTUM>
+__global__ void __launch_bounds__(kPrepThreads, 4) muon_scale_kernel(const MuonPrep a) {
+    constexpr int U = kAhead<MOMENTUM>;
     __shared__ float s_scale;
     pdl_wait();
     const float gs = a.grad_scale ? __ldg(a.grad_scale) : 1.f;
@@ -511,29 +540,38 @@ __global__ void __launch_bounds__(kPrepThreads) muon_scale_kernel(const MuonPrep
         __syncthreads();
         const float scale = s_scale;
         const int64_t end = min(a.n, (c + 1) * a.chunk);
-        for (int64_t i = c * a.chunk + threadIdx.x * V; i < end; i += kPrepThreads * V) {
-            float u[V];
-            update_v<G, V, false>(a, z * a.n + i, gs, u);
-            int64_t at;
-            if constexpr (V == 8) {
-                at = z * a.n + i;           // cols % 8 = 0: ld = cols
-            } else {
-                const int r = (int)(i / a.cols);
-                at = (z * a.rows + r) * a.ld + (i - (int64_t)r * a.cols);
-            }
-            __half hi[V], lo[V];
+        for (int64_t i0 = c * a.chunk + threadIdx.x * V; i0 < end; i0 += kPrepThreads * V * U) {
+            Update<G, V, MOMENTUM> x[U];
 #pragma unroll
-            for (int q = 0; q < V; ++q) {
-                const float x = u[q] * scale;
-                hi[q] = __float2half_rn(x);
-                lo[q] = __float2half_rn(x - __half2float(hi[q]));
-            }
-            if constexpr (V == 8) {
-                *reinterpret_cast<uint4*>(a.X + at) = *reinterpret_cast<uint4*>(hi);
-                if (SPLIT) *reinterpret_cast<uint4*>(a.X + plane + at) = *reinterpret_cast<uint4*>(lo);
-            } else {
-                a.X[at] = hi[0];
-                if (SPLIT) a.X[plane + at] = lo[0];
+            for (int k = 0; k < U; ++k)
+                if (i0 + k * kPrepThreads * V < end) x[k].load(a, z * a.n + i0 + k * kPrepThreads * V);
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const int64_t i = i0 + k * kPrepThreads * V;
+                if (i >= end) break;
+                float u[V];
+                x[k].template step<false>(a, z * a.n + i, gs, u);
+                int64_t at;
+                if constexpr (V == 8) {
+                    at = z * a.n + i;           // cols % 8 = 0: ld = cols
+                } else {
+                    const int r = (int)(i / a.cols);
+                    at = (z * a.rows + r) * a.ld + (i - (int64_t)r * a.cols);
+                }
+                __half hi[V], lo[V];
+#pragma unroll
+                for (int q = 0; q < V; ++q) {
+                    const float y = u[q] * scale;
+                    hi[q] = __float2half_rn(y);
+                    lo[q] = __float2half_rn(y - __half2float(hi[q]));
+                }
+                if constexpr (V == 8) {
+                    *reinterpret_cast<uint4*>(a.X + at) = *reinterpret_cast<uint4*>(hi);
+                    if (SPLIT) *reinterpret_cast<uint4*>(a.X + plane + at) = *reinterpret_cast<uint4*>(lo);
+                } else {
+                    a.X[at] = hi[0];
+                    if (SPLIT) a.X[plane + at] = lo[0];
+                }
             }
         }
         __syncthreads();
@@ -1128,16 +1166,16 @@ cudaError_t launch_gemm(MuonGemm p, int planes, const Operand& a, const Operand&
     return e;
 }
 
-template <typename G>
+template <typename G, bool MOMENTUM>
 cudaError_t launch_prep(const MuonPrep& a, bool split, cudaStream_t s) {
     const int64_t work = (int64_t)a.count * a.chunks;
-    const int grid = (int)std::min<int64_t>(work, (int64_t)num_sms() * 8);
-    cudaError_t e = launch_pdl(a.n % 8 == 0 ? muon_sums_kernel<G, 8> : muon_sums_kernel<G, 1>, dim3(grid),
-                               dim3(kPrepThreads), 0, s, a);
+    const int grid = (int)std::min<int64_t>(work, (int64_t)num_sms() * 4);
+    cudaError_t e = launch_pdl(a.n % 8 == 0 ? muon_sums_kernel<G, 8, MOMENTUM> : muon_sums_kernel<G, 1, MOMENTUM>,
+                               dim3(grid), dim3(kPrepThreads), 0, s, a);
     count_launch();
     if (e != cudaSuccess) return e;
-    auto kern = a.cols % 8 == 0 ? (split ? muon_scale_kernel<G, 8, true> : muon_scale_kernel<G, 8, false>)
-                                : (split ? muon_scale_kernel<G, 1, true> : muon_scale_kernel<G, 1, false>);
+    auto kern = a.cols % 8 == 0 ? (split ? muon_scale_kernel<G, 8, true, MOMENTUM> : muon_scale_kernel<G, 8, false, MOMENTUM>)
+                                : (split ? muon_scale_kernel<G, 1, true, MOMENTUM> : muon_scale_kernel<G, 1, false, MOMENTUM>);
     e = launch_pdl(kern, dim3(grid), dim3(kPrepThreads), 0, s, a);
     count_launch();
     return e;
@@ -1217,8 +1255,9 @@ cudaError_t launch_muon(const moe_muon_config_t& c, const void* g, float* m, con
     f.decay = (float)c.weight_decay;
     f.scale = (float)c.scale;
     if (small_matrix(c)) return launch_small(c, pre, f, split, s);
-    cudaError_t e = c.grad_dtype == MOE_BF16 ? launch_prep<__nv_bfloat16>(pre, split, s)
-                                             : launch_prep<float>(pre, split, s);
+    cudaError_t e = c.grad_dtype == MOE_BF16
+                        ? (m ? launch_prep<__nv_bfloat16, true>(pre, split, s) : launch_prep<__nv_bfloat16, false>(pre, split, s))
+                        : (m ? launch_prep<float, true>(pre, split, s) : launch_prep<float, false>(pre, split, s));
     if (e != cudaSuccess) return e;
     const Operand A{b.A, b.side, b.side, b.lds}, B{b.B, b.side, b.side, b.lds};
     int at = 0;
