@@ -71,7 +71,8 @@ def orthogonalize(moe, g, dtype, precision=None, steps=5, coef=COEF):
 
 
 SHAPES = [(1, 1, 1), (3, 1, 7), (2, 9, 1), (5, 45, 37), (2, 37, 45), (4, 64, 64), (1, 128, 200), (2, 130, 257),
-          (2, 257, 130), (1, 300, 520), (3, 256, 256), (1, 16, 1000), (1, 1000, 24), (1, 520, 512), (2, 513, 300)]
+          (2, 257, 130), (1, 300, 520), (3, 256, 256), (1, 16, 1000), (1, 1000, 24), (1, 520, 512), (2, 513, 300),
+          (1, 257, 2048), (1, 2500, 130), (13, 600, 640), (7, 640, 520)]       # pairs share tiles by k-blocks
 
 
 @pytest.mark.parametrize("shape", SHAPES)

@@ -42,6 +42,9 @@ struct MuonGemm {
     const __half* aux;            // poly: A [planes][count][M, ld]
     int ld;
     float alpha, beta, diag;      // out = alpha acc + beta aux + diag on the diagonal
+    const __nv_bfloat16* p;       // the last product, with bf16 output: weights [count, M, N] that it steps (null: o)
+    const float* lr_dev;
+    float lr, decay, scale;       // scale includes 1 / kXScale
     int* err;
 };
 
@@ -135,6 +138,10 @@ struct Staging {
     }
 };
 
+// What the product's epilogue makes of X: fp16 parts for the next step, or, where rows are whole 16-byte units,
+// the bf16 result itself, o or stepped weights (128 x 1024 x 4096: NNN).
+enum Out : int { kParts = 0, kResult = 1 };
+
 // out = alpha P Q + beta aux + diag I on CTA pairs; the pipeline and its barriers are those of the grouped
 // expert GEMMs.
 //
@@ -142,7 +149,7 @@ struct Staging {
 // than 22-bit operands leave. So K is taken in segments of kSegment k-blocks; each has a TMEM buffer to
 // itself, lo hi and hi lo before hi hi (what is cut off is measured by what the sum holds), and the epilogue
 // warps add the segments up in registers, rounding to nearest, while the other buffer fills.
-template <int OP, bool A_MN, bool B_MN, bool SPLIT>
+template <int OP, bool A_MN, bool B_MN, bool SPLIT, int OUT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                  const __grid_constant__ CUtensorMap tmO) {
@@ -275,6 +282,7 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
         }
     } else {
         const int quarter = warp & 3, half = (warp - 2) >> 2;
+        const float lr = OUT == kResult && p.lr_dev ? __ldg(p.lr_dev) : p.lr, lose = lr * p.decay, move = lr * p.scale;
         Staging st{smem_u32(stg_smem + (warp - 2) * 2 * STG_BYTES), 0};
         const uint32_t tempty_leader[2] = {map_to_rank(smem_u32(tempty), 0), map_to_rank(smem_u32(tempty + 1), 0)};
         uint32_t tl = 0;
@@ -285,6 +293,15 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
             const bool turn = SYM && t.m0 != t.n0;
             const uint32_t toff = ((uint32_t)(quarter * 32) << 16) + half * (BN / 2);
             bool ok = true;
+            // (stepped weights) the box's: the lane's row, 64 bytes, fetched a box ahead
+            uint4 ahead[4];
+            auto fetch = [&](int c) {
+                const __nv_bfloat16* src = p.p + ((size_t)t.z * p.M + (y + lane)) * p.N + x0 + c;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (y + lane < p.M && x0 + c + 8 * j < p.N) ahead[j] = __ldcg(reinterpret_cast<const uint4*>(src) + j);
+            };
+            if (OUT == kResult && p.p) fetch(0);
             // one box of 32 rows x 32 columns from column x0 + c on, out of its sums
             auto box = [&](int c, const uint32_t (&acc)[32], auto ready) {
                 const int x = x0 + c;
@@ -324,6 +341,23 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
                     }
                 }
                 uint32_t h[16];
+                if (OUT == kResult) {
+                    if (p.p) {
+                        float w[32];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) unpack8(ahead[j], w + 8 * j);
+                        if (c + 32 < BN / 2) fetch(c + 32);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = fmaf(-move, v[i], fmaf(-lose, w[i], w[i]));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                        h[i] = *reinterpret_cast<const uint32_t*>(&b);
+                    }
+                    st.store(lane, h, &tmO, x, y, t.z);
+                    return;
+                }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) h[i] = pack_half2(v[2 * i], v[2 * i + 1]);
                 st.store(lane, h, &tmO, x, y, t.z);
@@ -1124,28 +1158,30 @@ size_t carve_muon(const moe_muon_config_t& c, void* base, MuonScratch* b) {
     return align_up(ws.used, 256);
 }
 
-// fp16 [outer, rows, cols] with rows ld elements apart.
+// 16-bit elements [outer, rows, cols] with rows ld elements apart.
 bool map_3d(CUtensorMap* tm, const void* base, uint64_t cols, uint64_t rows, uint64_t outer, uint64_t ld,
-            uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+            uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle,
+            CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_FLOAT16) {
     auto fn = encode_fn();
     if (!fn) return false;
     cuuint64_t dims[3] = {cols, rows, outer};
     cuuint64_t strides[2] = {ld * 2, ld * rows * 2};
     cuuint32_t box[3] = {box_cols, box_rows, 1};
     cuuint32_t estr[3] = {1, 1, 1};
-    return fn(tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+    return fn(tm, type, 3, const_cast<void*>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 struct Operand {
-    const __half* base;
+    const void* base;
     int rows, cols, ld;
 };
 
 // K-major operands come in boxes of 64 k x 128 rows, MN-major ones of 64 columns x 64 k.
 template <int OP, bool A_MN, bool B_MN>
-cudaError_t launch_gemm(MuonGemm p, int planes, const Operand& a, const Operand& b, const Operand& o, cudaStream_t s) {
+cudaError_t launch_gemm(MuonGemm p, int planes, const Operand& a, const Operand& b, const Operand& o, cudaStream_t s,
+                        int out = kParts) {
     constexpr bool SYM = OP != kApply;
     p.m_tiles = ceil_div(p.M, kTile);
     p.n_tiles = ceil_div(p.N, kTile);
@@ -1155,9 +1191,12 @@ cudaError_t launch_gemm(MuonGemm p, int planes, const Operand& a, const Operand&
     CUtensorMap ta, tb, to;
     if (!map_3d(&ta, a.base, a.cols, a.rows, outer, a.ld, 64, A_MN ? BK : kHalf, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !map_3d(&tb, b.base, b.cols, b.rows, outer, b.ld, 64, B_MN ? BK : kHalf, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !map_3d(&to, o.base, o.cols, o.rows, outer, o.ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+        !map_3d(&to, o.base, o.cols, o.rows, outer, o.ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B,
+                out == kResult ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16))
         return cudaErrorInvalidValue;
-    auto kern = planes == 2 ? muon_gemm_kernel<OP, A_MN, B_MN, true> : muon_gemm_kernel<OP, A_MN, B_MN, false>;
+    auto kern = planes == 2 ? muon_gemm_kernel<OP, A_MN, B_MN, true, kParts> : muon_gemm_kernel<OP, A_MN, B_MN, false, kParts>;
+    if constexpr (OP == kApply)
+        if (out == kResult) kern = muon_gemm_kernel<OP, A_MN, B_MN, false, kResult>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem);
     if (e != cudaSuccess) return e;
     const int clusters = (int)std::min<int64_t>((int64_t)p.count * p.tiles, num_sms() / 2);
@@ -1260,9 +1299,13 @@ cudaError_t launch_muon(const moe_muon_config_t& c, const void* g, float* m, con
                         : (m ? launch_prep<float, true>(pre, split, s) : launch_prep<float, false>(pre, split, s));
     if (e != cudaSuccess) return e;
     const Operand A{b.A, b.side, b.side, b.lds}, B{b.B, b.side, b.side, b.lds};
+    // the last product writes the result where that is bf16, in rows of whole 16-byte units
+    const bool direct = !split && c.dtype == MOE_BF16 && !f.master && c.cols % 8 == 0;
     int at = 0;
     for (int k = 0; k < c.steps; ++k, at ^= 1) {
-        const Operand X{b.X[at], c.rows, c.cols, b.ld}, Y{b.X[at ^ 1], c.rows, c.cols, b.ld};
+        const bool result = direct && k + 1 == c.steps;
+        const Operand X{b.X[at], c.rows, c.cols, b.ld};
+        const Operand Y{result ? f.out : b.X[at ^ 1], c.rows, c.cols, result ? c.cols : b.ld};
         MuonGemm p{};
         p.count = c.count;
         p.M = p.N = b.side;
@@ -1282,9 +1325,19 @@ cudaError_t launch_muon(const moe_muon_config_t& c, const void* g, float* m, con
         p.M = c.rows;
         p.N = c.cols;
         p.alpha = 1.f / kBScale;
-        e = tall ? launch_gemm<kApply, false, false>(p, b.planes, X, B, Y, s)
-                 : launch_gemm<kApply, false, true>(p, b.planes, B, X, Y, s);
+        if (result) {
+            p.p = f.step ? static_cast<const __nv_bfloat16*>(f.out) : nullptr;
+            if (!f.step) p.alpha /= kXScale;
+            p.lr_dev = f.lr_dev;
+            p.lr = f.lr;
+            p.decay = f.decay;
+            p.scale = f.scale / kXScale;
+        }
+        const int out = result ? kResult : kParts;
+        e = tall ? launch_gemm<kApply, false, false>(p, b.planes, X, B, Y, s, out)
+                 : launch_gemm<kApply, false, true>(p, b.planes, B, X, Y, s, out);
         if (e != cudaSuccess) return e;
+        if (result) return cudaSuccess;
     }
     f.X = b.X[at];
     return c.dtype == MOE_BF16 ? launch_finish<__nv_bfloat16>(f, split, s) : launch_finish<float>(f, split, s);
