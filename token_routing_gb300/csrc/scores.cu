@@ -51,7 +51,7 @@ __device__ __forceinline__ float warp_max(float v) {
 // ahead of it; a reduction over the warp is one instruction.
 template <int V, bool SOFTMAX, bool CHOICE, bool FULL>
 __device__ __forceinline__ void route_token(const ScoreArgs& a, int t, const float (&z)[V], const float (&bias)[V],
-                                            int lane, float* s_row, float* s_val, int* s_id, int* s_hist) {
+                                            int lane, float* s_row, float2* s_cand, int* s_hist) {
     const int E = a.E, k = a.k;
     const float inf = INFINITY;
     // a row that holds NaN or +inf has no softmax: its first experts, with NaN weights
@@ -93,74 +93,67 @@ __device__ __forceinline__ void route_token(const ScoreArgs& a, int t, const flo
 #pragma unroll
         for (int i = 0; i < V; ++i) c[i] = rcp_approx(1.0f + ex2_approx(-z[i] * a.to_log2));
     }
-    uint32_t open = 0;                        // bit i: the lane's i-th expert may be taken
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         // a logit of -inf, or a NaN, counts as -inf (fmaxf drops a NaN)
         c[i] = fmaxf(CHOICE ? (z[i] == -inf ? -inf : c[i] + bias[i]) : z[i], -inf);
         if (SOFTMAX && bad) c[i] = -inf;
-        if (FULL || lane + 32 * i < E) open |= 1u << i;
     }
 
+    uint32_t shut = 0;                        // bit h << log: group h is not kept
+    const int log = FULL && a.groups == V ? (V == 8 ? 2 : V == 4 ? 3 : V == 2 ? 4 : 5) : a.lanes_log;
     if (a.kept < a.groups) {
-        uint32_t shut = 0;                    // bit g: group g is not kept
+        // 2^log lanes to a group, each reading every 2^log-th of its experts; a row of 32 is 33 words apart, so
+        // that groups of 32 are read from different banks
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (FULL || lane + 32 * i < E) s_row[lane + 33 * i] = c[i];
+        __syncwarp();
+        float m1 = -inf, m2 = -inf;
+        auto see = [&](float v) {
+            m2 = fmaxf(m2, fminf(m1, v));
+            m1 = fmaxf(m1, v);
+        };
+        auto worth_of = [&](int size) { return a.top == 2 && size > 1 ? fmaxf(m1 + m2, -inf) : m1; };
+        auto join = [&](int o) {
+            const float n1 = __shfl_xor_sync(0xffffffffu, m1, o), n2 = __shfl_xor_sync(0xffffffffu, m2, o);
+            m2 = fmaxf(fmaxf(m2, n2), fminf(m1, n1));
+            m1 = fmaxf(m1, n1);
+        };
+        int rank = 0;
+        const int g = lane >> log, sub = lane & ((1 << log) - 1);
         if (FULL && a.groups == V) {
-            // groups of 32: the i-th expert of every lane
-            float mine = -inf;
-            float worth[V];
+            // groups of 32, a register of every lane each: the same with all numbers known
+            const float* row = s_row + g * 33 + sub;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                worth[i] = warp_max(c[i]);
-                if (a.top == 2) {
-                    const uint32_t at = __ballot_sync(0xffffffffu, c[i] == worth[i]);
-                    worth[i] += warp_max(lane == __ffs(at) - 1 ? -inf : c[i]);
-                    worth[i] = fmaxf(worth[i], -inf);
-                }
-                if (lane == i) mine = worth[i];
+            for (int j = 0; j < V; ++j) see(row[j * (32 / V)]);
+#pragma unroll
+            for (int o = 16 / V; o > 0; o >>= 1) join(o);
+            const float worth = worth_of(32);
+#pragma unroll
+            for (int h = 0; h < V; ++h) {
+                const float v = __shfl_sync(0xffffffffu, worth, h * (32 / V));
+                if (v > worth || (v == worth && h < g)) ++rank;
             }
-            int rank = 0;
-#pragma unroll
-            for (int i = 0; i < V; ++i) rank += (worth[i] > mine || (worth[i] == mine && i < lane)) ? 1 : 0;
-            shut = __ballot_sync(0xffffffffu, lane >= V || rank >= a.kept);
+            shut = __ballot_sync(0xffffffffu, rank >= a.kept);
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                if ((shut >> i) & 1u) c[i] = -inf;
-            open &= ~shut;
+                if ((shut >> (i * (32 / V))) & 1u) c[i] = -inf;
         } else {
-            // 2^lanes_log lanes to a group, each reading every 2^lanes_log-th of its experts; a row of 32 is
-            // 33 words apart, so that groups of 32 are read from different banks
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (FULL || lane + 32 * i < E) s_row[lane + 33 * i] = c[i];
-            __syncwarp();
-            const int size = E / a.groups, step = 1 << a.lanes_log;
-            const int g = lane >> a.lanes_log, sub = lane & (step - 1);
-            float m1 = -inf, m2 = -inf;
+            const int size = E / a.groups, step = 1 << log;
             if (g < a.groups)
-                for (int e = g * size + sub; e < (g + 1) * size; e += step) {
-                    const float v = s_row[e + (e >> 5)];
-                    m2 = fmaxf(m2, fminf(m1, v));
-                    m1 = fmaxf(m1, v);
-                }
-            for (int o = step >> 1; o > 0; o >>= 1) {
-                const float n1 = __shfl_xor_sync(0xffffffffu, m1, o), n2 = __shfl_xor_sync(0xffffffffu, m2, o);
-                m2 = fmaxf(fmaxf(m2, n2), fminf(m1, n1));
-                m1 = fmaxf(m1, n1);
-            }
-            const float worth = a.top == 2 && size > 1 ? fmaxf(m1 + m2, -inf) : m1;
-            int rank = 0;
+                for (int e = g * size + sub; e < (g + 1) * size; e += step) see(s_row[e + (e >> 5)]);
+            for (int o = step >> 1; o > 0; o >>= 1) join(o);
+            const float worth = worth_of(size);
             for (int h = 0; h < a.groups; ++h) {
-                const float v = __shfl_sync(0xffffffffu, worth, h << a.lanes_log);
-                rank += (v > worth || (v == worth && h < g)) ? 1 : 0;
+                const float v = __shfl_sync(0xffffffffu, worth, h << log);
+                if (v > worth || (v == worth && h < g)) ++rank;
             }
             shut = __ballot_sync(0xffffffffu, g >= a.groups || rank >= a.kept);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const uint32_t h = ((uint32_t)(lane + 32 * i) * a.group_mul) >> 16;
-                if ((FULL || lane + 32 * i < E) && ((shut >> (h << a.lanes_log)) & 1u)) {
-                    c[i] = -inf;
-                    open &= ~(1u << i);
-                }
+                if ((FULL || lane + 32 * i < E) && ((shut >> (h << log)) & 1u)) c[i] = -inf;
             }
         }
     }
@@ -170,40 +163,48 @@ __device__ __forceinline__ void route_token(const ScoreArgs& a, int t, const flo
 #pragma unroll
     for (int i = 1; i < V; ++i) top = fmaxf(top, c[i]);
     float least = -inf;
-    for (int j = 0; j < k; ++j) {
+#pragma unroll
+    for (int j = 0; j < MOE_MAX_K; ++j) {
+        if (j >= k) break;
         least = warp_max(top);
         if (top == least) top = -inf;
     }
-    int n = 0;
+    // experts at or above it, in order of their ids (an expert that is shut stands at -inf, like a masked one)
+    int n = kCand + 1;
+    if (least > -inf) {
+        n = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const bool in = c[i] >= least && ((open >> i) & 1u);
-        const uint32_t at = __ballot_sync(0xffffffffu, in);
-        const int pos = n + __popc(at & ((1u << lane) - 1u));
-        if (in && pos < kCand) {
-            s_val[pos] = c[i];
-            s_id[pos] = lane + 32 * i;
+        for (int i = 0; i < V; ++i) {
+            const uint32_t at = __ballot_sync(0xffffffffu, c[i] >= least);
+            if (c[i] >= least) s_cand[n + __popc(at & ((1u << lane) - 1u))] = make_float2(c[i], __int_as_float(lane + 32 * i));
+            n += __popc(at);
         }
-        n += __popc(at);
     }
     __syncwarp();
     int mine = -1, slot = k;     // the lane's chosen expert and its place
     if (n <= kCand) {
-        // candidates stand in order of their ids; what follows the last one counts for nothing
-        const float own = lane < n ? s_val[lane] : inf;
+        // what follows the last candidate counts for nothing
+        const float2 own = s_cand[lane];
         int rank = 0;
         for (int j = 0; j < n; j += 4) {
-            const float4 v4 = *reinterpret_cast<const float4*>(s_val + j);
-            const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+            const float4 v01 = *reinterpret_cast<const float4*>(s_cand + j), v23 = *reinterpret_cast<const float4*>(s_cand + j + 2);
+            const float v[4] = {v01.x, v01.z, v23.x, v23.z};
 #pragma unroll
-            for (int q = 0; q < 4; ++q) rank += (j + q < n && (v[q] > own || (v[q] == own && j + q < lane))) ? 1 : 0;
+            for (int q = 0; q < 4; ++q)
+                if (j + q < n && (v[q] > own.x || (v[q] == own.x && j + q < lane))) ++rank;
         }
         if (lane < n && rank < k) {
             slot = rank;
-            mine = s_id[lane];
+            mine = __float_as_int(own.y);
         }
     } else {
-        // many equal values: one expert after another
+        // many equal values, or fewer than k above -inf: one expert after another
+        uint32_t open = 0;       // bit i: the lane's i-th expert may be taken
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const uint32_t h = ((uint32_t)(lane + 32 * i) * a.group_mul) >> 16;
+            if ((FULL || lane + 32 * i < E) && !((shut >> (h << log)) & 1u)) open |= 1u << i;
+        }
         for (int j = 0; j < k; ++j) {
             float best = -inf;
             uint32_t id = 0xffffffffu;
@@ -271,8 +272,7 @@ template <int V, bool SOFTMAX, bool CHOICE, bool FULL>
 __global__ void __launch_bounds__(kThreads, kScoreBlocks) route_scores_kernel(const ScoreArgs a, int32_t* counts,
                                                                              float* balance) {
     __shared__ float s_row[kWarps][33 * V];
-    __shared__ __align__(16) float s_val[kWarps][kCand];
-    __shared__ int s_id[kWarps][kCand];
+    __shared__ __align__(16) float2 s_cand[kWarps][32 * V];      // (all may tie)
     __shared__ int s_hist[MOE_MAX_EXPERTS];
     __shared__ double s_red[kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, kScoreBlocks) route_scores_kernel(co
     if (t < a.T) fetch(t, z);
     for (; t < a.T; t += nwarps) {
         fetch(t + nwarps, next);
-        route_token<V, SOFTMAX, CHOICE, FULL>(a, t, z, bias, lane, s_row[warp], s_val[warp], s_id[warp], s_hist);
+        route_token<V, SOFTMAX, CHOICE, FULL>(a, t, z, bias, lane, s_row[warp], s_cand[warp], s_hist);
 #pragma unroll
         for (int i = 0; i < V; ++i) z[i] = next[i];
     }
