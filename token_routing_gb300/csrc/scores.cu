@@ -361,92 +361,108 @@ struct ScoreGradArgs {
     int* err;
 };
 
-// The gradients of four tokens' chosen logits, by lanes of eight to a token (slot j = lane % 8). The
-// derivative of a share in its own sum is taken by differences of dw, since one share can be nearly
-// all of the sum. FULL (softmax that is not renormalised): g = dw scale instead, for the Jacobian over
-// all experts. `on` says whether the slot counts.
-template <bool SOFTMAX, bool FULL>
-__device__ __forceinline__ float slot_grad(const ScoreGradArgs& a, int t, int j, int& e, bool& on) {
-    on = t < a.T && j < a.k;
-    const size_t at = (size_t)t * a.k + j;
-    e = on ? a.idx[at] : -1;
-    const float dw = on ? a.dw[at] : 0.f;
-    if (on && (uint32_t)e >= (uint32_t)a.E) {
-        raise_error(a.err, kErrBounds);
-        on = false;
+// Slot j = lane % 8 of a token: its expert, whether it counts, the weight's gradient.
+struct Slot {
+    int e;
+    bool on;
+    float dw;
+    __device__ __forceinline__ void load(const ScoreGradArgs& a, int t, int j) {
+        on = t < a.T && j < a.k;
+        const size_t at = (size_t)t * a.k + j;
+        e = on ? __ldg(a.idx + at) : -1;
+        dw = on ? __ldg(a.dw + at) : 0.f;
     }
-    // an expert that an earlier slot holds
-    bool twice = false;
-    for (int i = 0; i < a.k - 1; ++i) {
-        const int o = __shfl_sync(0xffffffffu, e, i, 8);
-        twice |= i < j && o == e;
+    // Experts out of range, or that an earlier slot of the token holds, are left out.
+    __device__ __forceinline__ void check(const ScoreGradArgs& a, int j) {
+        bool bad = on && (uint32_t)e >= (uint32_t)a.E;
+        for (int i = 0; i < a.k - 1; ++i) {
+            const int o = __shfl_sync(0xffffffffu, e, i, 8);
+            bad |= on && i < j && o == e;
+        }
+        if (bad) {
+            raise_error(a.err, kErrBounds);
+            on = false;
+        }
     }
-    if (on && twice) {
-        raise_error(a.err, kErrBounds);
-        on = false;
-    }
-    if (FULL) return dw * a.scale;
-    const float z = on ? __ldg(a.logits + (size_t)t * a.E + e) : -INFINITY;
+};
+
+// The gradient of the slot's logit z, by lanes of eight to a token. The derivative of a share in its own sum is
+// taken by differences of dw, since one share can be nearly all of the sum.
+template <bool SOFTMAX>
+__device__ __forceinline__ float slot_grad(const ScoreGradArgs& a, const Slot& s, float z) {
     const float x = scaled(z, a.inv_hi, a.inv_lo);
-    float s, slope;                 // score, and d score / d x
+    float score, slope;             // slope: d score / d x
     if (SOFTMAX) {
-        float mx = x;
+        float mx = s.on ? x : -INFINITY;
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         if (mx == -INFINITY) mx = 0.f;
-        s = on ? expf(x - mx) : 0.f;
-        slope = s;                  // the part through the sum cancels in the shares
+        score = s.on ? expf(x - mx) : 0.f;
+        slope = score;              // the part through the sum cancels in the shares
     } else {
-        const float u = expf(-x);
-        s = on ? 1.0f / (1.0f + u) : 0.f;
+        score = s.on ? 1.0f / (1.0f + expf(-x)) : 0.f;
         // s (1 - s), with 1 - s = 1 / (1 + e^x) taken apart so that it does not cancel
-        slope = s * (1.0f / (1.0f + expf(x)));
+        slope = score * (1.0f / (1.0f + expf(x)));
     }
-    if (!a.renorm) return on ? dw * a.scale * slope : 0.f;
-    float sum = s;
+    if (!a.renorm) return s.on ? s.dw * a.scale * slope : 0.f;
+    float sum = score;
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const float tiny = SOFTMAX ? 0.f : kTiny;
     const float inv = sum + tiny == 0.f ? 0.f : 1.0f / (sum + tiny);
-    const float share = s * inv;
-    float g = dw * (tiny * inv);
+    const float share = score * inv;
+    float g = s.dw * (tiny * inv);
     for (int i = 0; i < a.k; ++i) {
-        const float si = __shfl_sync(0xffffffffu, share, i, 8), di = __shfl_sync(0xffffffffu, dw, i, 8);
-        if (si != 0.f) g = fmaf(si, dw - di, g);
+        const float si = __shfl_sync(0xffffffffu, share, i, 8), di = __shfl_sync(0xffffffffu, s.dw, i, 8);
+        if (si != 0.f) g = fmaf(si, s.dw - di, g);
     }
-    return on ? g * (a.scale * inv) * slope : 0.f;
+    return s.on ? g * (a.scale * inv) * slope : 0.f;
 }
 
-// Gradient at the chosen experts, zeros elsewhere: a warp holds four tokens' rows of zeros in shared
-// memory, sets their chosen entries, copies the rows out in 16-byte vectors and clears the entries.
+// Gradient at the chosen experts, zeros elsewhere: a warp holds rows of zeros in shared memory, four tokens' at a
+// time, sets their chosen entries, copies the rows out in 16-byte vectors and clears the entries. What it waits
+// for is one load after another (idx, then that logit), so kQuads times four tokens go together.
+constexpr int kQuads = 1;
+constexpr int kGradWarps = 4;
 template <bool SOFTMAX>
-__global__ void __launch_bounds__(kThreads) scores_grad_kernel(const ScoreGradArgs a) {
+__global__ void __launch_bounds__(32 * kGradWarps) scores_grad_kernel(const ScoreGradArgs a) {
     extern __shared__ __align__(16) float s_rows[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float* row = s_rows + (size_t)warp * 4 * a.E;
-    for (int i = lane; i < 4 * a.E; i += 32) row[i] = 0.f;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane & 7;
+    float* row = s_rows + (size_t)warp * kQuads * 4 * a.E;
+    for (int i = lane; i < kQuads * 4 * a.E; i += 32) row[i] = 0.f;
     __syncwarp();
     pdl_wait();
-    const int quads = (a.T + 3) / 4, step = gridDim.x * kWarps;
-    for (int q = blockIdx.x * kWarps + warp; q < quads; q += step) {
-        const int t = 4 * q + (lane >> 3);
-        int e;
-        bool on;
-        const float g = slot_grad<SOFTMAX, false>(a, t, lane & 7, e, on);
-        float* at = row + (lane >> 3) * a.E + e;
-        const float dz = scaled(g, a.inv_hi, a.inv_lo);
-        if (on) *at = dz;
-        if (a.dz && t < a.T && (lane & 7) < a.k) a.dz[(size_t)t * a.k + (lane & 7)] = on ? dz : 0.f;
-        __syncwarp();
-        float* out = a.dlogits + (size_t)q * 4 * a.E;
-        if (4 * q + 4 <= a.T) {
-            for (int i = lane; i < a.E; i += 32)
-                reinterpret_cast<float4*>(out)[i] = reinterpret_cast<const float4*>(row)[i];
-        } else {
-            for (int i = lane; i < (a.T - 4 * q) * a.E; i += 32) out[i] = row[i];
+    const int sets = (a.T + 4 * kQuads - 1) / (4 * kQuads), step = gridDim.x * kGradWarps;
+    for (int q = blockIdx.x * kGradWarps + warp; q < sets; q += step) {
+        const int t0 = q * 4 * kQuads;
+        Slot s[kQuads];
+        float z[kQuads];
+#pragma unroll
+        for (int u = 0; u < kQuads; ++u) s[u].load(a, t0 + 4 * u + (lane >> 3), j);
+#pragma unroll
+        for (int u = 0; u < kQuads; ++u) {
+            s[u].check(a, j);
+            z[u] = s[u].on ? __ldg(a.logits + (size_t)(t0 + 4 * u + (lane >> 3)) * a.E + s[u].e) : -INFINITY;
+        }
+#pragma unroll
+        for (int u = 0; u < kQuads; ++u) {
+            const int t = t0 + 4 * u + (lane >> 3);
+            const float dz = scaled(slot_grad<SOFTMAX>(a, s[u], z[u]), a.inv_hi, a.inv_lo);
+            if (s[u].on) row[(4 * u + (lane >> 3)) * a.E + s[u].e] = dz;
+            if (a.dz && t < a.T && j < a.k) a.dz[(size_t)t * a.k + j] = s[u].on ? dz : 0.f;
         }
         __syncwarp();
-        if (on) *at = 0.f;
+        float* out = a.dlogits + (size_t)t0 * a.E;
+        if (t0 + 4 * kQuads <= a.T) {
+            for (int i = lane; i < kQuads * a.E; i += 32)
+                reinterpret_cast<float4*>(out)[i] = reinterpret_cast<const float4*>(row)[i];
+        } else {
+            for (int i = lane; i < (a.T - t0) * a.E; i += 32) out[i] = row[i];
+        }
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < kQuads; ++u)
+            if (s[u].on) row[(4 * u + (lane >> 3)) * a.E + s[u].e] = 0.f;
         __syncwarp();
     }
 }
@@ -472,11 +488,13 @@ __global__ void __launch_bounds__(kThreads) scores_grad_full_kernel(const ScoreG
             bad |= !(x[i] < INFINITY);
             mx = fmaxf(mx, x[i]);
         }
-        int e;
-        bool on;
         // all four groups of eight lanes work on the same token; the first one's slots are set
-        const float g = slot_grad<true, true>(a, t, lane & 7, e, on);
-        if (on && lane < 8) sg[e] = g;
+        Slot slot;
+        slot.load(a, t, lane & 7);
+        slot.check(a, lane & 7);
+        const bool on = slot.on && lane < 8;
+        const int e = slot.e;
+        if (on) sg[e] = slot.dw * a.scale;
         if (a.dz && lane < a.k) a.dz[(size_t)t * a.k + lane] = 0.f;   // all of the gradient is dense
         __syncwarp();
 #pragma unroll
@@ -502,7 +520,7 @@ __global__ void __launch_bounds__(kThreads) scores_grad_full_kernel(const ScoreG
             if (c < a.E) a.dlogits[(size_t)t * a.E + c] = scaled(x[i] * inv * (gi[i] - dot), a.inv_hi, a.inv_lo);
         }
         __syncwarp();
-        if (on && lane < 8) sg[e] = 0.f;
+        if (on) sg[e] = 0.f;
         __syncwarp();
     }
 }
@@ -582,9 +600,9 @@ cudaError_t launch_scores_grad(const moe_score_config_t& c, const float* logits,
                     : v <= 4 ? scores_grad_full_kernel<4> : scores_grad_full_kernel<8>;
         e = launch_pdl(kern, dim3(blocks), dim3(kThreads), 0, s, a);
     } else {
-        const int blocks = std::min(ceil_div(c.T, 4 * kWarps), num_sms() * 6);
+        const int blocks = std::min(ceil_div(c.T, 4 * kQuads * kGradWarps), num_sms() * 12);
         auto kern = c.score == MOE_SCORE_SOFTMAX ? scores_grad_kernel<true> : scores_grad_kernel<false>;
-        e = launch_pdl(kern, dim3(blocks), dim3(kThreads), (size_t)kWarps * 4 * c.E * sizeof(float), s, a);
+        e = launch_pdl(kern, dim3(blocks), dim3(32 * kGradWarps), (size_t)kGradWarps * kQuads * 4 * c.E * sizeof(float), s, a);
     }
     count_launch();
     return e;

@@ -51,6 +51,16 @@ def _opt(what, t, dtype, shape, gpu):
     return None if t is None else _arg(what, t, dtype, shape, gpu)
 
 
+def _bytes(what, cfg, key):
+    """The C call's answer for this configuration, asked for once while the fields that it depends on stay."""
+    got = cfg.__dict__.get("_bytes")
+    if got is None or got[0] != key:
+        got = key, int(getattr(L.load(), what)(ctypes.byref(cfg)))
+        if got[1]:                      # 0: the configuration is refused, as the call will be
+            cfg._bytes = got
+    return got[1]
+
+
 def _work(ws, need, gpu):
     """The address of a workspace of `need` bytes on GPU `gpu`."""
     if ws is None or ws.nbytes < need or not ws.is_contiguous():
@@ -303,7 +313,7 @@ def route_scores(cfg, logits, bias, idx, w, counts=None, balance_loss=None, ws=N
             _arg("idx", idx, i32, (T, k), gpu), _arg("w", w, f32, (T, k), gpu), _opt("counts", counts, i32, (E,), gpu),
             _opt("balance_loss", balance_loss, f32, (1,), gpu))
     tally = counts is not None or balance_loss is not None
-    at = _work(ws, route_scores_workspace_bytes(cfg), gpu) if tally else None
+    at = _work(ws, _bytes("moe_route_scores_workspace_bytes", cfg, (T, E)), gpu) if tally else None
     _launch("moe_route_scores", gpu, stream, ctypes.byref(cfg), *args, at)
 
 
@@ -350,7 +360,7 @@ def layer_norm_backward(cfg, dy, s, gain, mean, rstd, dx, dgain, dbias, ws, dtot
             _opt("dgain", dgain, f32, row, gpu), _opt("dbias", dbias, f32, row, gpu))
     sums = dgain is not None or dbias is not None
     _launch("moe_layer_norm_backward", gpu, stream, ctypes.byref(cfg), *args,
-            _work(ws, norm_workspace_bytes(cfg), gpu) if sums else None)
+            _work(ws, _bytes("moe_norm_workspace_bytes", cfg, (T, d, dt)), gpu) if sums else None)
 
 
 # ---------------------------------------------------------------- orthogonalised updates (Muon)
