@@ -6,7 +6,7 @@
 //   poly:  B = a I + b A + c A A               symmetric
 //   apply: X = B X   (X B)
 // Of the symmetric two only the tiles on and below the diagonal are computed; each is stored twice, once
-// as it is and once turned.
+// as it is and once turned. On the diagonal both operands are the same rows, which are loaded once.
 //
 // Operands are fp16, not bf16: the tensor cores take both at one rate, and all of the factors are
 // bounded (singular values of X are 1 at most and stay near it), so bf16's range buys nothing and fp16's
@@ -203,11 +203,12 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
             for (int tile = cluster_id; tile < num_tiles && ok; tile += nclusters) {
                 const MuonTile t = decode_tile<SYM>(p, tile);
                 const int mr = t.m0 + (int)rank * kHalf, nh = t.n0 + (int)rank * kHalf;
+                const bool same = SYM && !SPLIT && t.m0 == t.n0;
                 for (int kb = 0, term = 0, first = 0; first < kblocks;) {
                     if (!mbar_wait(empty + s, ph ^ 1, p.err)) { ok = false; break; }
                     const uint32_t sa = smem_u32(smem + s * kStageBytes), sb = sa + kPartBytes;
                     const uint32_t fb = map_to_rank(smem_u32(full + s), 0);
-                    if (leader) mbar_expect_tx(full + s, 2 * kStageBytes);
+                    if (leader) mbar_expect_tx(full + s, same ? 2 * kPartBytes : 2 * kStageBytes);
                     const int k0 = kb * BK;
                     const int za = t.z + (SPLIT && term == 0 ? p.count : 0), zb = t.z + (SPLIT && term == 1 ? p.count : 0);
                     if (!A_MN) {
@@ -217,7 +218,8 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
                         for (int j = 0; j < kHalf / 64; ++j)
                             tma_load_3d_pair(sa + j * (BK * 128), &tmA, mr + 64 * j, k0, za, fb);
                     }
-                    if (!B_MN) {
+                    if (same) {
+                    } else if (!B_MN) {
                         tma_load_3d_pair(sb, &tmB, k0, nh, zb, fb);
                     } else {
 #pragma unroll
@@ -262,11 +264,13 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
                 if (!mbar_wait(tempty + buf, aph ^ 1, p.err)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + buf * BN;
+                const MuonTile t = decode_tile<SYM>(p, tile);
+                const uint64_t b_desc = SYM && !SPLIT && t.m0 == t.n0 ? a_desc0 : b_desc0;
                 const int steps = TERMS * min(seg, kblocks - first);
                 for (int q = 0; q < steps; ++q) {
                     if (!mbar_wait(full + s, ph, p.err)) { ok = false; break; }
                     tc_fence_after();
-                    const uint64_t ad = a_desc0 + soff, bd = b_desc0 + soff;
+                    const uint64_t ad = a_desc0 + soff, bd = b_desc + soff;
 #pragma unroll
                     for (int kk = 0; kk < BK / UMMA_K; ++kk)
                         mma_pair(d_tmem, ad + kk * A_KSTEP, bd + kk * B_KSTEP, idesc, (q > 0 || kk > 0) ? 1u : 0u);
