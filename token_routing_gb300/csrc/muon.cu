@@ -39,11 +39,10 @@ enum Op : int { kGram = 0, kPoly = 1, kApply = 2 };
 struct MuonGemm {
     int count, M, N, K;           // per matrix: out [M, N], reduction K
     int m_tiles, n_tiles, tiles;  // tiles: of one matrix
-    const __half* aux;            // poly: A [planes][count][M, ld]
-    int ld;
-    float alpha, beta, diag;      // out = alpha acc + beta aux + diag on the diagonal
-    const __nv_bfloat16* p;       // the last product, with bf16 output: weights [count, M, N] that it steps (null: o)
-    const float* lr_dev;
+    const uint16_t* side;         // [planes][count][M, ld]: poly: A; last product with bf16 output: the weights that it
+    int ld;                       // steps (null: o is written)
+    float alpha, beta, diag;      // out = alpha acc + beta side + diag on the diagonal
+    const float* lr_dev;          // (last product)
     float lr, decay, scale;       // scale includes 1 / kXScale
     int* err;
 };
@@ -114,6 +113,16 @@ struct Staging {
         }
         ++count;
     }
+    // 16-byte units that were read in order (lane l: unit l & 3 of rows l / 4 + 8 i) to the lane's own row.
+    __device__ __forceinline__ void to_rows(int lane, uint4 (&r)[4]) {
+        const uint32_t buf = acquire(lane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sts128(sw64_addr(buf, (lane >> 2) + 8 * i, lane & 3), r[i]);
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r[j] = lds128(sw64_addr(buf, lane, j));
+        __syncwarp();
+    }
     // h[i]: columns 2i and 2i + 1 of the lane's row
     __device__ __forceinline__ void store(int lane, const uint32_t (&h)[16], const CUtensorMap* tm, int x, int y, int z) {
         const uint32_t buf = acquire(lane);
@@ -142,7 +151,7 @@ struct Staging {
 // the bf16 result itself, o or stepped weights (128 x 1024 x 4096: NNN).
 enum Out : int { kParts = 0, kResult = 1 };
 
-// out = alpha P Q + beta aux + diag I on CTA pairs; the pipeline and its barriers are those of the grouped
+// out = alpha P Q + beta side + diag I on CTA pairs; the pipeline and its barriers are those of the grouped
 // expert GEMMs.
 //
 // SPLIT: the tensor cores cut off their sums at 24 bits with every addition, which over a long K is far more
@@ -297,40 +306,47 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
             const bool turn = SYM && t.m0 != t.n0;
             const uint32_t toff = ((uint32_t)(quarter * 32) << 16) + half * (BN / 2);
             bool ok = true;
-            // (stepped weights) the box's: the lane's row, 64 bytes, fetched a box ahead
-            uint4 ahead[4];
-            auto fetch = [&](int c) {
-                const __nv_bfloat16* src = p.p + ((size_t)t.z * p.M + (y + lane)) * p.N + x0 + c;
+            // The side input of a box, fetched a box ahead, in whole sectors (a row of it to a lane took a read of
+            // 32 lines for every 16 bytes: stepping weights in the last product then took longer than apart from it).
+            const bool sided = OP == kPoly || (OUT == kResult && p.side);
+            auto fetch = [&](int c, int part, uint4 (&to)[4]) {
+                const int row = y + (lane >> 2), col = x0 + c + (lane & 3) * 8;
+                const uint16_t* src = p.side + ((size_t)(t.z + part * p.count) * p.M + row) * p.ld + col;
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (y + lane < p.M && x0 + c + 8 * j < p.N) ahead[j] = __ldcg(reinterpret_cast<const uint4*>(src) + j);
+                for (int i = 0; i < 4; ++i) {
+                    to[i] = make_uint4(0, 0, 0, 0);
+                    if (row + 8 * i < p.M && col < p.ld) to[i] = __ldcg(reinterpret_cast<const uint4*>(src + (size_t)8 * i * p.ld));
+                }
             };
-            if (OUT == kResult && p.p) fetch(0);
+            uint4 ahead[4];
+            if (sided) fetch(0, 0, ahead);
             // one box of 32 rows x 32 columns from column x0 + c on, out of its sums
             auto box = [&](int c, const uint32_t (&acc)[32], auto ready) {
                 const int x = x0 + c;
                 if (x >= p.N || y >= p.M) return;
                 float v[32];
+                uint4 own[4];
+                if (sided) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) own[i] = ahead[i];
+                    if (c + 32 < BN / 2) fetch(c + 32, 0, ahead);
+                    st.to_rows(lane, own);
+                }
                 if (OP == kPoly) {
-                    // A of the same box: the lane's row, 64 bytes
-                    const bool in = y + lane < p.M;
+                    auto add = [&](bool first) {
+                        const __half2* h = reinterpret_cast<const __half2*>(own);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = 0.f;
-                    for (int pl = 0; pl < (SPLIT ? 2 : 1); ++pl) {
-                        const __half* src = p.aux + ((size_t)(t.z + pl * p.count) * p.M + (y + lane)) * p.ld + x;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            if (in && x + 8 * j < p.ld) {
-                                const uint4 u = __ldg(reinterpret_cast<const uint4*>(src) + j);
-                                const __half2* h = reinterpret_cast<const __half2*>(&u);
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const float2 f = __half22float2(h[i]);
-                                    v[8 * j + 2 * i] += f.x;
-                                    v[8 * j + 2 * i + 1] += f.y;
-                                }
-                            }
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 f = __half22float2(h[i]);
+                            v[2 * i] = first ? f.x : v[2 * i] + f.x;
+                            v[2 * i + 1] = first ? f.y : v[2 * i + 1] + f.y;
                         }
+                    };
+                    add(true);
+                    if (SPLIT) {
+                        fetch(c, 1, own);
+                        st.to_rows(lane, own);
+                        add(false);
                     }
                 }
                 ready();
@@ -346,11 +362,10 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
                 }
                 uint32_t h[16];
                 if (OUT == kResult) {
-                    if (p.p) {
+                    if (p.side) {
                         float w[32];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) unpack8(ahead[j], w + 8 * j);
-                        if (c + 32 < BN / 2) fetch(c + 32);
+                        for (int j = 0; j < 4; ++j) unpack8(own[j], w + 8 * j);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = fmaf(-move, v[i], fmaf(-lose, w[i], w[i]));
                     }
@@ -1319,7 +1334,7 @@ cudaError_t launch_muon(const moe_muon_config_t& c, const void* g, float* m, con
                  : launch_gemm<kGram, false, false>(p, b.planes, X, X, A, s);
         if (e != cudaSuccess) return e;
         p.K = b.side;
-        p.aux = b.A;
+        p.side = reinterpret_cast<const uint16_t*>(b.A);
         p.ld = b.lds;
         p.alpha = (float)(c.c * kBScale / ((double)kAScale * kAScale));
         p.beta = (float)(c.b * kBScale / kAScale);
@@ -1329,8 +1344,10 @@ cudaError_t launch_muon(const moe_muon_config_t& c, const void* g, float* m, con
         p.M = c.rows;
         p.N = c.cols;
         p.alpha = 1.f / kBScale;
+        p.side = nullptr;
         if (result) {
-            p.p = f.step ? static_cast<const __nv_bfloat16*>(f.out) : nullptr;
+            p.side = f.step ? static_cast<const uint16_t*>(f.out) : nullptr;
+            p.ld = c.cols;
             if (!f.step) p.alpha /= kXScale;
             p.lr_dev = f.lr_dev;
             p.lr = f.lr;

@@ -19,7 +19,7 @@ struct ScoreArgs {
     const float* bias;
     int32_t* idx;
     float* w;
-    int32_t* part;        // [blocks, E] choices per block, or null
+    int32_t* part;        // [blocks, 32 V] choices per block, zeros beyond E; or null
     int T, E, k, groups, kept, top, renorm;
     uint32_t group_mul;   // e / group size = e * group_mul >> 16
     int lanes_log;        // log2 of the lanes that read one group
@@ -249,6 +249,9 @@ __device__ __forceinline__ void route_token(const ScoreArgs& a, int t, const flo
     __syncwarp();
 }
 
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 // balance_loss = mean_e (counts[e] - T k / E)^2, by the whole block: counts differ from their mean by
 // up to T k, whose squares want 64 bits; the sum is of integers (E counts - T k), exact.
 __device__ __forceinline__ void block_balance(const int* s_counts, int T, int E, int k, float* out, double* s_red) {
@@ -302,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, kScoreBlocks) route_scores_kernel(co
     }
     __syncthreads();
     if (a.part)
-        for (int e = threadIdx.x; e < a.E; e += kThreads) a.part[(size_t)blockIdx.x * a.E + e] = s_hist[e];
+        for (int e = threadIdx.x; e < 32 * V; e += kThreads) a.part[(size_t)blockIdx.x * (32 * V) + e] = e < a.E ? s_hist[e] : 0;
     if (gridDim.x == 1) {      // few tokens: one block has all of the counts
         if (counts)
             for (int e = threadIdx.x; e < a.E; e += kThreads) counts[e] = s_hist[e];
@@ -310,42 +313,55 @@ __global__ void __launch_bounds__(kThreads, kScoreBlocks) route_scores_kernel(co
     }
 }
 
-// counts = sum of the blocks' choices, and the balance loss: a cluster of CTAs, 32 experts each, whose
-// warps take every 32nd block's row. One block over all experts read 900 rows in 20 us; this reads 600 in 3.
+// counts = sum of the blocks' choices, and the balance loss: a cluster of CTAs, 32 experts each. A warp reads four
+// rows of the partial counts at once, and all of a thread's rows are in flight together: one latency, not one for
+// each of the 600 rows (7 us in that form, of which 3 were the rows).
 constexpr int kFinish = 1024;
-__global__ void __launch_bounds__(kFinish) route_counts_kernel(const int32_t* __restrict__ part, int blocks, int T,
+__global__ void __launch_bounds__(kFinish) route_counts_kernel(const int32_t* __restrict__ part, int parts, int T,
                                                               int E, int k, int32_t* counts, float* balance) {
-    __shared__ int s_sum[kFinish / 32][32];
+    __shared__ int s_sum[kFinish / 8][33];
     __shared__ double s_sq[MOE_MAX_EXPERTS / 32];
     pdl_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = blockIdx.x * 32 + lane;
-    int sum = 0;
-    if (e < E) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int4* rows = reinterpret_cast<const int4*>(part + blockIdx.x * 32) + (lane & 7);
+    const int stride = gridDim.x * 8;      // of a row, in int4
+    int4 sum = make_int4(0, 0, 0, 0);
 #pragma unroll 8
-        for (int b = warp; b < blocks; b += kFinish / 32) sum += part[(size_t)b * E + e];
+    for (int b = threadIdx.x >> 3; b < parts; b += kFinish / 8) {
+        const int4 v = __ldg(rows + (size_t)b * stride);
+        sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
     }
-    s_sum[warp][lane] = sum;
-    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");   // all CTAs run
-    if (warp == 0) {
+    int* to = &s_sum[threadIdx.x >> 3][(lane & 7) * 4];
+    to[0] = sum.x; to[1] = sum.y; to[2] = sum.z; to[3] = sum.w;
+    __syncthreads();
+    int all = 0;                           // warp w: rows w, w + 32, w + 64, w + 96 of the sums
 #pragma unroll
-        for (int w = 1; w < kFinish / 32; ++w) sum += s_sum[w][lane];
-        if (counts && e < E) counts[e] = sum;
-        double sq = e < E ? (double)sum * E - (double)T * k : 0.0;
+    for (int r = 0; r < 4; ++r) all += s_sum[warp + 32 * r][lane];
+    __syncthreads();
+    s_sum[warp][lane] = all;
+    cluster_barrier();                     // (all CTAs run, too)
+    if (warp == 0) {
+        const int e = blockIdx.x * 32 + lane;
+        all = 0;
+#pragma unroll
+        for (int w = 0; w < 32; ++w) all += s_sum[w][lane];
+        if (counts && e < E) counts[e] = all;
+        double sq = e < E ? (double)all * E - (double)T * k : 0.0;
         sq *= sq;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
         if (lane == 0) {
-            uint32_t to;
+            uint32_t at;
             asm volatile("mapa.shared::cluster.u32 %0, %1, 0;"
-                         : "=r"(to) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(s_sq + blockIdx.x))));
-            asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(to), "d"(sq) : "memory");
+                         : "=r"(at) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(s_sq + blockIdx.x))));
+            asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(at), "d"(sq) : "memory");
         }
     }
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_barrier();
     if (balance && blockIdx.x == 0 && threadIdx.x == 0) {
-        double all = 0.0;
-        for (int b = 0; b < (int)gridDim.x; ++b) all += s_sq[b];
-        *balance = (float)(all / ((double)E * E * E));
+        double total = 0.0;
+        for (int b = 0; b < (int)gridDim.x; ++b) total += s_sq[b];
+        *balance = (float)(total / ((double)E * E * E));
     }
 }
 
@@ -555,6 +571,8 @@ int score_blocks(const moe_score_config_t& c) {
     const int need = ceil_div(c.T, kWarps);
     return need <= 4 ? 1 : std::min(need, num_sms() * kScoreBlocks);
 }
+// Registers to a lane that hold a token's experts (1, 2, 4 or 8).
+int score_width(const moe_score_config_t& c) { return c.E > 128 ? 8 : c.E > 64 ? 4 : c.E > 32 ? 2 : 1; }
 
 template <int V, bool FULL>
 cudaError_t launch_scores(const ScoreArgs& a, bool softmax, bool choice, int blocks, int32_t* counts, float* balance,
@@ -566,10 +584,10 @@ cudaError_t launch_scores(const ScoreArgs& a, bool softmax, bool choice, int blo
     return e;
 }
 
-cudaError_t launch_counts(const moe_score_config_t& c, const int32_t* part, int blocks, int32_t* counts, float* balance,
+cudaError_t launch_counts(const moe_score_config_t& c, const int32_t* part, int parts, int32_t* counts, float* balance,
                           cudaStream_t s) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)ceil_div(c.E, 32));
+    cfg.gridDim = dim3((unsigned)score_width(c));
     cfg.blockDim = dim3(kFinish);
     cfg.stream = s;
     cudaLaunchAttribute at[2];
@@ -580,7 +598,7 @@ cudaError_t launch_counts(const moe_score_config_t& c, const int32_t* part, int 
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    const cudaError_t e = launch_ex(cfg, route_counts_kernel, part, blocks, c.T, c.E, c.k, counts, balance);
+    const cudaError_t e = launch_ex(cfg, route_counts_kernel, part, parts, c.T, c.E, c.k, counts, balance);
     count_launch();
     return e;
 }
@@ -616,7 +634,7 @@ using namespace moe;
 
 extern "C" MOE_API size_t moe_route_scores_workspace_bytes(const moe_score_config_t* cfg) {
     if (check_scores(cfg) != MOE_OK) return 0;
-    return align_up((size_t)score_blocks(*cfg) * cfg->E * sizeof(int32_t) + 1, 256);
+    return align_up((size_t)score_blocks(*cfg) * score_width(*cfg) * 32 * sizeof(int32_t), 256);
 }
 
 extern "C" MOE_API moe_status_t moe_route_scores(const moe_score_config_t* cfg, const float* logits, const float* bias,
