@@ -127,7 +127,7 @@ def norm_backward(dy, x, gain, mean, rstd):
 
 def orth(u, steps=5, coef=(3.4445, -4.7750, 2.0315), eps=1e-7, held=None):
     """Newton-Schulz steps on one matrix. `held(x, what)` is what storage makes of an operand ("X", "A",
-    "B"); `held(x, "sum")` of a product."""
+    "B" without its diagonal); `held(x, ("sum", K))` of a product of length K."""
     a, b, c = coef
     keep = held or (lambda x, what: x)
     tall = u.shape[0] > u.shape[1]
@@ -135,8 +135,10 @@ def orth(u, steps=5, coef=(3.4445, -4.7750, 2.0315), eps=1e-7, held=None):
     eye = np.eye(min(u.shape))
     for _ in range(steps):
         A = keep(keep(x.T @ x if tall else x @ x.T, ("sum", max(u.shape))), "A")
-        B = keep(a * eye + b * A + c * keep(A @ A, ("sum", min(u.shape))), "B")
-        x = keep(keep(x @ B if tall else B @ x, ("sum", min(u.shape))), "X")
+        B = a * eye + b * A + c * keep(A @ A, ("sum", min(u.shape)))
+        D = np.diag(np.diag(B))
+        B = keep(B - D, "B")
+        x = keep(keep(x @ B if tall else B @ x, ("sum", min(u.shape))) + (x @ D if tall else D @ x), "X")
     return x
 
 

@@ -3,14 +3,10 @@
 The kernels round X, A and B to fp16 (one number, or two) at each step; the oracle takes the same
 roundings at the same places in 64 bits, and its distance from the exact result is the size of error
 that they make. A second set of roundings of that size is off by as much, so a kernel that rounds at
-those places only stays within twice the distance in the Frobenius norm; one element within eight of
-its root mean square (independent errors: eight standard deviations). The output's own rounding is added.
-
-Two of a step's roundings stay with an element instead of spreading over the matrix: its own in X, and that
-of the diagonal of B, which multiplies it. Each is up to half a step, 2^-11 of the element (2^-22 in two
-parts), so an element may be off by 2 steps times that, and by one such rounding with no steps: an element of
-0.0304 by 0.0304 2^-11 = 1.5e-5, which is more than eight times the root mean square over a matrix whose
-elements are 0.0085 on average.
+those places only stays within twice the distance in the Frobenius norm, and in one element within twice the
+largest distance of any (elements are not alike: those along a strong direction are large in the first steps,
+and so are their roundings, which stay with them; for 1 x 257 x 2048 the oracle's own largest is ten times its
+root mean square). The output's own rounding is added.
 """
 import numpy as np
 import pytest
@@ -37,14 +33,14 @@ def make(count, rows, cols, dtype, seed=0, size=1e-3):
 
 
 def expected(u, precision, steps=5, coef=COEF):
-    """(exact, size of the error in the Frobenius norm, and of one element) for one matrix."""
+    """(exact, size of the error in the Frobenius norm, and of the element that it is largest in) for one matrix."""
     ref = O.orth(u, steps, coef)
     off = O.orth(u, steps, coef, held=O.fp16_planes(1 if precision == "bf16" else 2)) - ref
     fro = np.sqrt((off * off).sum())
     # the scale's own rounding and that of the sums before it: 2^-20 of X, which a step leaves or shrinks,
     # but for small singular values, which grow with it
     own = 2.0 ** -20 * np.sqrt((ref * ref).sum())
-    return ref, fro + own, (fro + own) / np.sqrt(ref.size)
+    return ref, fro + own, np.abs(off).max() + 2.0 ** -20 * np.abs(ref).max()
 
 
 def compare(got, u, precision, dtype, steps=5, coef=COEF, scale=1.0, base=None):
@@ -55,8 +51,7 @@ def compare(got, u, precision, dtype, steps=5, coef=COEF, scale=1.0, base=None):
         err = np.abs(got[i] - want)
         out = HALF[dtype] * np.abs(want) * 1.01 + (0 if base is None else 4 * 2.0 ** -24 * np.abs(base[i]))
         assert np.sqrt((np.maximum(err - out, 0) ** 2).sum()) <= 2 * scale * fro, (i, err.max(), fro)
-        own = scale * np.abs(ref) * max(1, 2 * steps) * (2.0 ** -11 if precision == "bf16" else 2.0 ** -22)
-        assert (err <= out + own + 8 * scale * one + 2.0 ** -40).all(), (i, err.max(), one)
+        assert (err <= out + 2 * scale * one + 2.0 ** -40).all(), (i, err.max(), one)
 
 
 def orthogonalize(moe, g, dtype, precision=None, steps=5, coef=COEF):
@@ -72,7 +67,7 @@ def orthogonalize(moe, g, dtype, precision=None, steps=5, coef=COEF):
 
 SHAPES = [(1, 1, 1), (3, 1, 7), (2, 9, 1), (5, 45, 37), (2, 37, 45), (4, 64, 64), (1, 128, 200), (2, 130, 257),
           (2, 257, 130), (1, 300, 520), (3, 256, 256), (1, 16, 1000), (1, 1000, 24), (1, 520, 512), (2, 513, 300),
-          (1, 257, 2048), (1, 2500, 130), (13, 600, 640), (7, 640, 520)]       # pairs share tiles by k-blocks
+          (1, 257, 2048), (1, 2500, 130), (13, 600, 640), (7, 640, 520), (2, 35, 1500)]
 
 
 @pytest.mark.parametrize("shape", SHAPES)

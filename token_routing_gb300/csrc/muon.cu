@@ -13,6 +13,11 @@
 // three more bits make the rounding of one operand 2^-12 of it. X and A are held times 2^11 and B times
 // 2^10, so that what is far smaller than the largest elements keeps its bits too. In MOE_F32 precision an
 // operand is two fp16 planes, x = hi + lo, and a product takes hi hi + hi lo + lo hi.
+//
+// The diagonal of B, which is near a = 3.4 where the rest is small, is not rounded with it: it stays in fp32 and
+// multiplies X in the epilogue of the product, B X = (B - D) X + D X. (Rounded, it is off by up to 2^-12 in one
+// direction in all rows alike: 2.7e-3 of the result for 35 x 3195 instead of 1.3e-3, simulated. And most of a
+// product goes past the tensor cores' sums, which cut off.)
 #include <cmath>
 #include <type_traits>
 
@@ -39,9 +44,13 @@ enum Op : int { kGram = 0, kPoly = 1, kApply = 2 };
 struct MuonGemm {
     int count, M, N, K;           // per matrix: out [M, N], reduction K
     int m_tiles, n_tiles, tiles;  // tiles: of one matrix
-    const uint16_t* side;         // [planes][count][M, ld]: poly: A; last product with bf16 output: the weights that it
-    int ld;                       // steps (null: o is written)
-    float alpha, beta, diag;      // out = alpha acc + beta side + diag on the diagonal
+    const uint16_t* side;         // [planes][count][M, ld]: poly: A; apply: X
+    int ld;
+    float* diag;                  // [count][dstride]: poly writes B's diagonal, apply reads it
+    int dstride;
+    const uint16_t* weights;      // last product with bf16 output: what it steps [count, M, N] (null: o is written)
+    float gain;                   // last product: o = gain X
+    float alpha, beta, a;         // poly: B = alpha acc + beta side + a I; others: alpha acc (+ D X)
     const float* lr_dev;          // (last product)
     float lr, decay, scale;       // scale includes 1 / kXScale
     int* err;
@@ -151,18 +160,19 @@ struct Staging {
 // the bf16 result itself, o or stepped weights (128 x 1024 x 4096: NNN).
 enum Out : int { kParts = 0, kResult = 1 };
 
-// out = alpha P Q + beta side + diag I on CTA pairs; the pipeline and its barriers are those of the grouped
+// out = alpha P Q + beta side + a I on CTA pairs; the pipeline and its barriers are those of the grouped
 // expert GEMMs.
 //
 // SPLIT: the tensor cores cut off their sums at 24 bits with every addition, which over a long K is far more
-// than 22-bit operands leave. So K is taken in segments of kSegment k-blocks; each has a TMEM buffer to
+// than 22-bit operands leave. So K is taken in segments of kSegment k-blocks (2048 x 1024: 3.5e-6 of the result
+// in 533 us, with one k-block 2.0e-6 in 655, plain fp32 products 3.3e-6); each has a TMEM buffer to
 // itself, lo hi and hi lo before hi hi (what is cut off is measured by what the sum holds), and the epilogue
 // warps add the segments up in registers, rounding to nearest, while the other buffer fills.
 template <int OP, bool A_MN, bool B_MN, bool SPLIT, int OUT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                  const __grid_constant__ CUtensorMap tmO) {
-    constexpr bool SYM = OP != kApply;
+    constexpr bool SYM = OP != kApply, SIDED = OP != kGram, TALL = OP == kApply && !B_MN;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* stg_smem = smem + kStages * kStageBytes;
@@ -308,31 +318,31 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
             bool ok = true;
             // The side input of a box, fetched a box ahead, in whole sectors (a row of it to a lane took a read of
             // 32 lines for every 16 bytes: stepping weights in the last product then took longer than apart from it).
-            const bool sided = OP == kPoly || (OUT == kResult && p.side);
-            auto fetch = [&](int c, int part, uint4 (&to)[4]) {
+            auto fetch = [&](const uint16_t* from, int ld, int c, int part, uint4 (&to)[4]) {
                 const int row = y + (lane >> 2), col = x0 + c + (lane & 3) * 8;
-                const uint16_t* src = p.side + ((size_t)(t.z + part * p.count) * p.M + row) * p.ld + col;
+                const uint16_t* src = from + ((size_t)(t.z + part * p.count) * p.M + row) * ld + col;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     to[i] = make_uint4(0, 0, 0, 0);
-                    if (row + 8 * i < p.M && col < p.ld) to[i] = __ldcg(reinterpret_cast<const uint4*>(src + (size_t)8 * i * p.ld));
+                    if (row + 8 * i < p.M && col < ld) to[i] = __ldcg(reinterpret_cast<const uint4*>(src + (size_t)8 * i * ld));
                 }
             };
-            uint4 ahead[4];
-            if (sided) fetch(0, 0, ahead);
+            uint4 ahead[4], weights[4];
+            if (SIDED) fetch(p.side, p.ld, 0, 0, ahead);
+            if (OUT == kResult && p.weights) fetch(p.weights, p.N, 0, 0, weights);
+            float drow = 0.f;              // D of the lane's row (X times it on the left)
+            if (OP == kApply && !TALL && y + lane < p.M) drow = __ldg(p.diag + (size_t)t.z * p.dstride + y + lane);
             // one box of 32 rows x 32 columns from column x0 + c on, out of its sums
             auto box = [&](int c, const uint32_t (&acc)[32], auto ready) {
                 const int x = x0 + c;
                 if (x >= p.N || y >= p.M) return;
                 float v[32];
                 uint4 own[4];
-                if (sided) {
+                if (SIDED) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) own[i] = ahead[i];
-                    if (c + 32 < BN / 2) fetch(c + 32, 0, ahead);
+                    if (c + 32 < BN / 2) fetch(p.side, p.ld, c + 32, 0, ahead);
                     st.to_rows(lane, own);
-                }
-                if (OP == kPoly) {
                     auto add = [&](bool first) {
                         const __half2* h = reinterpret_cast<const __half2*>(own);
 #pragma unroll
@@ -344,30 +354,52 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
                     };
                     add(true);
                     if (SPLIT) {
-                        fetch(c, 1, own);
+                        fetch(p.side, p.ld, c, 1, own);
                         st.to_rows(lane, own);
                         add(false);
                     }
                 }
                 ready();
+                if (OP == kGram) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const float a = p.alpha * __uint_as_float(acc[i]);
-                    if (OP == kPoly) {
-                        v[i] = fmaf(p.beta, v[i], a);
-                        if (!turn && x + i == y + lane) v[i] += p.diag;
-                    } else {
-                        v[i] = a;
+                    for (int i = 0; i < 32; ++i) v[i] = p.alpha * __uint_as_float(acc[i]);
+                } else if (OP == kPoly) {
+                    float d = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        v[i] = fmaf(p.beta, v[i], p.alpha * __uint_as_float(acc[i]));
+                        if (x == y && i == lane) {       // (a box on the diagonal)
+                            d = v[i];
+                            v[i] = 0.f;
+                        }
+                    }
+                    if (x == y && y + lane < p.M) p.diag[(size_t)t.z * p.dstride + y + lane] = fmaf(d, 1.f / kBScale, p.a);
+                } else {
+                    const float4* dcol = reinterpret_cast<const float4*>(p.diag + (size_t)t.z * p.dstride + x);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 d = TALL ? __ldg(dcol + i / 4) : make_float4(drow, drow, drow, drow);
+                        v[i] = fmaf(d.x, v[i], p.alpha * __uint_as_float(acc[i]));
+                        v[i + 1] = fmaf(d.y, v[i + 1], p.alpha * __uint_as_float(acc[i + 1]));
+                        v[i + 2] = fmaf(d.z, v[i + 2], p.alpha * __uint_as_float(acc[i + 2]));
+                        v[i + 3] = fmaf(d.w, v[i + 3], p.alpha * __uint_as_float(acc[i + 3]));
                     }
                 }
                 uint32_t h[16];
                 if (OUT == kResult) {
-                    if (p.side) {
+                    if (p.weights) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) own[i] = weights[i];
+                        if (c + 32 < BN / 2) fetch(p.weights, p.N, c + 32, 0, weights);
+                        st.to_rows(lane, own);
                         float w[32];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) unpack8(own[j], w + 8 * j);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = fmaf(-move, v[i], fmaf(-lose, w[i], w[i]));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] *= p.gain;
                     }
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
@@ -800,6 +832,10 @@ __device__ __forceinline__ void split8(const float* v, uint4& hi, uint4& lo) {
 template <bool SPLIT, bool TALL>
 __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const MuonSmall a) {
     constexpr int PL = SPLIT ? 2 : 1;
+    // With two parts K steps go to four sums in turn, which the epilogue adds up rounding to nearest: the tensor
+    // cores cut off with every addition (128 x 1024: 1.3e-6 of the result, as plain fp32 products; with two sums
+    // 2.0e-6, with one 3.6e-6, in 1 and 9% less time).
+    constexpr int SUMS = SPLIT ? 4 : 1;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sX = smem;
@@ -808,6 +844,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
     __shared__ uint64_t s_bar, s_sums, s_rows;    // products; sums, rows of A that have arrived
     __shared__ uint32_t s_tmem;
     __shared__ float s_warp[kSmallThreads / 32];
+    __shared__ __align__(16) float s_diag[kSide]; // of B
     __shared__ float s_sq[kMaxCluster];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int CS = a.cluster, rank = blockIdx.x % CS, z = blockIdx.x / CS;
@@ -824,7 +861,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
-    if (warp == 0) tmem_alloc(&s_tmem, kSide);
+    if (warp == 0) tmem_alloc(&s_tmem, SUMS * kSide);
     cluster_sync();      // every CTA runs, with its barriers, before one writes into another
     pdl_wait();
 
@@ -912,8 +949,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
 #pragma unroll
                 for (int q = 0; q < kSide / 16; ++q) {
                     const uint32_t major = ((q >> 2) * kBlockBytes + (q & 3) * 32) >> 4, minor = (q * 16 * 128) >> 4;
-                    if (q < n) tc_mma(tmem, ta + (AMN ? minor : major), tb + (BMN ? minor : major), idesc,
-                                      term == (SPLIT ? 0 : 2) && q == 0 ? 0u : 1u);
+                    if (q < n) tc_mma(tmem + q % SUMS * kSide, ta + (AMN ? minor : major), tb + (BMN ? minor : major), idesc,
+                                      term == (SPLIT ? 0 : 2) && q < SUMS ? 0u : 1u);
                 }
             }
             tc_commit(&s_bar);
@@ -934,6 +971,36 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
         *reinterpret_cast<uint4*>(to + unit_at(row, unit)) = hi;
         if (SPLIT) *reinterpret_cast<uint4*>(to + kPlaneBytes + unit_at(row, unit)) = lo;
     };
+    // 32 columns of the product, from column 32 h of the thread's half on; k: the reduction's length.
+    auto sums = [&](int h, int k, float (&v)[32]) {
+        uint32_t acc[32];
+        tmem_ld32(taddr + 32 * h, acc);
+        tmem_ld_wait_regs(acc);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(acc[i]);
+#pragma unroll
+        for (int m = 1; m < SUMS; ++m) {
+            if (16 * m >= k) break;
+            tmem_ld32(taddr + m * kSide + 32 * h, acc);
+            tmem_ld_wait_regs(acc);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] += __uint_as_float(acc[i]);
+        }
+    };
+    // 8 fp16 values (in parts) of the thread's row.
+    auto get8 = [&](const uint8_t* from, int unit, float* v) {
+        const uint4 q4 = *reinterpret_cast<const uint4*>(from + unit_at(row, unit));
+        const __half2* q = reinterpret_cast<const __half2*>(&q4);
+        uint4 l4 = make_uint4(0, 0, 0, 0);
+        if (SPLIT) l4 = *reinterpret_cast<const uint4*>(from + kPlaneBytes + unit_at(row, unit));
+        const __half2* l = reinterpret_cast<const __half2*>(&l4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(q[i]), g = __half22float2(l[i]);
+            v[2 * i] = SPLIT ? f.x + g.x : f.x;
+            v[2 * i + 1] = SPLIT ? f.y + g.y : f.y;
+        }
+    };
     auto ready = [&]() {     // this CTA's writes are there for the next product or copy, and TMEM is read
         fence_async_smem();
         tc_fence_before();
@@ -948,12 +1015,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
         product(sX, tall, sX, tall, TALL ? nr : nc);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            uint32_t acc[32];
-            tmem_ld32(taddr + 32 * h, acc);
-            tmem_ld_wait_regs(acc);
             float v[32];
+            sums(h, TALL ? nr : nc, v);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(acc[i]) * (kAScale / (kXScale * kXScale));
+            for (int i = 0; i < 32; ++i) v[i] *= kAScale / (kXScale * kXScale);
             if (CS == 1) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) put8(sA, half * 8 + h * 4 + j, v + 8 * j);
@@ -1024,30 +1089,17 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
         if (CS > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            uint32_t acc[32];
-            tmem_ld32(taddr + 32 * h, acc);
-            float v[32];
+            float v[32], w[32];
+            sums(h, a.side, v);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t at = unit_at(row, half * 8 + h * 4 + j);
-                const uint4 q4 = *reinterpret_cast<const uint4*>(sA + at);
-                const __half2* q = reinterpret_cast<const __half2*>(&q4);
-                uint4 l4 = make_uint4(0, 0, 0, 0);
-                if (SPLIT) l4 = *reinterpret_cast<const uint4*>(sA + kPlaneBytes + at);
-                const __half2* l = reinterpret_cast<const __half2*>(&l4);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 f = __half22float2(q[i]), g = __half22float2(l[i]);
-                    v[8 * j + 2 * i] = f.x + g.x;
-                    v[8 * j + 2 * i + 1] = f.y + g.y;
-                }
-            }
-            tmem_ld_wait_regs(acc);
+            for (int j = 0; j < 4; ++j) get8(sA, half * 8 + h * 4 + j, w + 8 * j);
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-                v[i] = fmaf(a.b * (kBScale / kAScale), v[i],
-                            a.c * (kBScale / (kAScale * kAScale)) * __uint_as_float(acc[i]));
-                if (half * 64 + h * 32 + i == row) v[i] += a.a * kBScale;
+                v[i] = fmaf(a.b * (kBScale / kAScale), w[i], a.c * (kBScale / (kAScale * kAScale)) * v[i]);
+                if (half * 64 + h * 32 + i == row) {
+                    s_diag[row] = fmaf(v[i], 1.f / kBScale, a.a);
+                    v[i] = 0.f;
+                }
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) put8(sA, half * 8 + h * 4 + j, v + 8 * j);
@@ -1057,14 +1109,22 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
         if constexpr (TALL) product(sX, major, sA, major, a.side);
         else product(sA, major, sX, minor, a.side);
         const bool last = step + 1 == a.steps;
+        const float drow = s_diag[row];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            uint32_t acc[32];
-            tmem_ld32(taddr + 32 * h, acc);
-            tmem_ld_wait_regs(acc);
-            float v[32];
+            float v[32], w[32];
+            sums(h, a.side, v);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(acc[i]) * (1.f / kBScale);
+            for (int j = 0; j < 4; ++j) get8(sX, half * 8 + h * 4 + j, w + 8 * j);
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+                float4 d = make_float4(drow, drow, drow, drow);
+                if (TALL) d = *reinterpret_cast<const float4*>(s_diag + half * 64 + h * 32 + i);
+                v[i] = fmaf(d.x, w[i], v[i] * (1.f / kBScale));
+                v[i + 1] = fmaf(d.y, w[i + 1], v[i + 1] * (1.f / kBScale));
+                v[i + 2] = fmaf(d.z, w[i + 2], v[i + 2] * (1.f / kBScale));
+                v[i + 3] = fmaf(d.w, w[i + 3], v[i + 3] * (1.f / kBScale));
+            }
             if (last) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
@@ -1120,7 +1180,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
     cluster_sync();      // no CTA leaves while another may still write into it
     if (warp == 0) {
         tc_fence_after();
-        tmem_dealloc(tmem, kSide);
+        tmem_dealloc(tmem, SUMS * kSide);
     }
 }
 
@@ -1154,8 +1214,10 @@ struct MuonScratch {
     __half* X[2];
     __half* A;
     __half* B;
+    float* diag;
     float* sums;
     int planes, ld, lds, side;        // ld: of X; side, lds: of A and B
+    int dstride;
     int64_t chunk;
     int chunks;
 };
@@ -1172,6 +1234,8 @@ size_t carve_muon(const moe_muon_config_t& c, void* base, MuonScratch* b) {
     const size_t all = (size_t)b->planes * c.count;
     b->sums = ws.take<float>((size_t)c.count * b->chunks + 1);
     for (__half*& x : b->X) x = ws.take<__half>(all * c.rows * b->ld + 1);
+    b->dstride = (int)align_up(b->side, 32);
+    b->diag = ws.take<float>((size_t)c.count * b->dstride + kTile);
     b->A = ws.take<__half>(all * b->side * b->lds + 1);
     b->B = ws.take<__half>(all * b->side * b->lds + 1);
     return align_up(ws.used, 256);
@@ -1335,20 +1399,22 @@ cudaError_t launch_muon(const moe_muon_config_t& c, const void* g, float* m, con
         if (e != cudaSuccess) return e;
         p.K = b.side;
         p.side = reinterpret_cast<const uint16_t*>(b.A);
+        p.diag = b.diag;
+        p.dstride = b.dstride;
         p.ld = b.lds;
         p.alpha = (float)(c.c * kBScale / ((double)kAScale * kAScale));
         p.beta = (float)(c.b * kBScale / kAScale);
-        p.diag = (float)(c.a * kBScale);
+        p.a = (float)c.a;
         e = launch_gemm<kPoly, false, false>(p, b.planes, A, A, B, s);
         if (e != cudaSuccess) return e;
         p.M = c.rows;
         p.N = c.cols;
         p.alpha = 1.f / kBScale;
-        p.side = nullptr;
+        p.side = reinterpret_cast<const uint16_t*>(b.X[at]);
+        p.ld = b.ld;
         if (result) {
-            p.side = f.step ? static_cast<const uint16_t*>(f.out) : nullptr;
-            p.ld = c.cols;
-            if (!f.step) p.alpha /= kXScale;
+            p.weights = f.step ? static_cast<const uint16_t*>(f.out) : nullptr;
+            p.gain = 1.f / kXScale;
             p.lr_dev = f.lr_dev;
             p.lr = f.lr;
             p.decay = f.decay;
