@@ -424,7 +424,8 @@ MOE_API moe_status_t moe_adamw(const moe_adamw_config_t* cfg, const moe_adamw_te
 
 /* Choice of experts from scores: what moe_route's top-k and softmax over the k do not cover. The
  * scores are a softmax over all experts or sigmoids; a bias for balance enters the choice but not
- * the weights; experts may stand in groups, of which only the best are open to a token.
+ * the weights; experts may stand in groups, of which only the best are open to a token. What is
+ * compared is within 2^-21 of the exact value; weights are rounded as fp32 operations are.
  *   logits [T,E] fp32 (moe_route's `logits`), bias [E] fp32 (nullable: 0)
  *   s_te = softmax(logits_t / temperature)_e   or   1 / (1 + exp(-logits_te / temperature)),
  *   c_te = s_te + bias_e; -inf where the logit is -inf or c is NaN,
@@ -500,7 +501,7 @@ MOE_API moe_status_t moe_backward_scores(const moe_config_t* cfg, const moe_scor
  * allowed. dx may be null where only dgain or dbias is wanted. ws (moe_norm_workspace_bytes) is needed
  * with dgain or dbias; their sums are fp32 in a fixed order, so results repeat bit for bit.
  * T = 0 is allowed (dgain and dbias are zeroed unless accumulate). A row that holds NaN or an infinity
- * gives NaN in its own y and dx only. Arrays of rows, gain, bias, dgain, dbias and ws are 16-byte aligned;
+ * gives NaN in its own y and dx, and in dgain and dbias. Arrays of rows, gain, bias, dgain, dbias and ws are 16-byte aligned;
  * d may be odd. */
 typedef struct {
     int32_t T;             /* rows, 0 .. 2^30 */
@@ -529,9 +530,9 @@ MOE_API moe_status_t moe_layer_norm_backward(const moe_norm_config_t* cfg, const
  *   moe_muon:          m = momentum m + g (g times *grad_scale),  u = nesterov ? g + momentum m : m,
  *                      x = x (1 - lr weight_decay) - lr scale orth(u)
  * m [count,rows,cols] fp32 (zeroed before the first step); x is the fp32 master if there is one (p is then
- * x rounded to its type), else p in dtype. precision: MOE_BF16: operands of the products hold 11 bits
- * (fp16, scaled), sums are fp32, orth(u) is right to about one rounding to bf16; MOE_F32: operands hold two
- * fp16 parts, 22 bits, and the products three terms, right to a few 1e-6 of the largest elements. An element
+ * x rounded to its type), else p in dtype. precision: MOE_BF16: operands of the products hold 11 bits (fp16,
+ * scaled), sums are fp32; orth(u) is off by 1e-3 of its size (root mean square), half of a rounding to bf16;
+ * MOE_F32: operands hold two fp16 parts, 22 bits; off by 1e-6 to 4e-6, as fp32 products are. An element
  * that is not finite, or a matrix whose sum of squares is beyond fp32, gives NaN in all of its own matrix
  * and leaves the others alone.
  * lr (device fp32, replaces cfg->lr) and grad_scale (device fp32) may be null, as in moe_adamw. p, g, o,

@@ -199,10 +199,11 @@ def test_matrix_and_stack(moe_lib, cuda_device):
     moe.get_error()
 
 
-def test_graph_and_two_streams(moe_lib, cuda_device):
+@pytest.mark.parametrize("shape", [(2, 256, 320), (3, 100, 700), (3, 40, 33)])
+def test_graph_and_two_streams(shape, moe_lib, cuda_device):
     """A captured step, replayed while another optimiser steps on its own stream."""
     moe = moe_lib
-    made = [[make(2, 256, 320, "bf16", seed=i, size=0.02).cuda(), make(2, 256, 320, "bf16", seed=10 + i).cuda()] for i in range(2)]
+    made = [[make(*shape, "bf16", seed=i, size=0.02).cuda(), make(*shape, "bf16", seed=10 + i).cuda()] for i in range(2)]
     want = []
     for p, g in made:
         q = p.clone()

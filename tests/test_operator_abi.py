@@ -51,9 +51,10 @@ def test_scores_refuse_arrays(moe_lib):
             assert lib.moe_route_scores(ref(c), *args, None) == BAD
     for i in range(4):
         for p in (None, ctypes.c_void_p(257)):
-            args = [P] * 4
+            args = [P, P, P, R]
             args[i] = p
             assert lib.moe_route_scores_backward(ref(c), *args, None) == BAD
+    assert lib.moe_route_scores_backward(ref(c), P, P, P, P, None) == BAD       # dlogits in place of logits
     assert lib.moe_route_scores(None, P, P, P, P, P, P, P, None) == BAD
     c = scores_cfg(moe_lib, T=0)
     assert lib.moe_route_scores(ref(c), None, None, None, None, None, None, None, None) == 0
@@ -63,7 +64,7 @@ def test_scores_refuse_arrays(moe_lib):
 def test_backward_scores_refuses(moe_lib):
     moe, lib = moe_lib, moe_lib.load()
     c = moe.make_config(10, 64, 16, 4, 64)
-    good = [P] * 27 + [None]
+    good = [P, R] + [P] * 25 + [None]
 
     def call(c, s, args=good):
         return lib.moe_backward_scores(ref(c), s if s is None else ref(s), *args)
@@ -75,6 +76,7 @@ def test_backward_scores_refuses(moe_lib):
             args = list(good)
             args[i] = p
             assert call(c, scores_cfg(moe), args) == BAD
+    assert call(c, scores_cfg(moe), [P] * 27 + [None]) == BAD                   # dlogits in place of logits
     dense = moe.make_config(10, 64, 4, 4, 64)
     assert call(dense, put(moe.make_score_config(10, 4, 4))) == NOT
 
@@ -154,6 +156,8 @@ def test_muon_refuses_arrays(moe_lib):
         if i in (0, 1, 3, 6):                           # master, lr and grad_scale may be missing
             args[i] = None
             assert lib.moe_muon(ref(c), *args, None) == BAD
+    assert 0 < moe_lib.muon_workspace_bytes(moe_lib.make_muon_config(1000, 128, 1024)) < 4096
+    assert moe_lib.muon_workspace_bytes(moe_lib.make_muon_config(2, 129, 1024)) > 4 * 129 * 1024 * 2
     c.grad_dtype = moe_lib.MOE_F32
     assert lib.moe_orthogonalize(ref(c), P, P, R, None) == BAD      # in place, but of another type
     c.count = 0

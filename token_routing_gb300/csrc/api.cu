@@ -1,7 +1,7 @@
 // C ABI of the MoE layer library: argument validation, workspace layout and the order of
 // kernel launches for each entry point. The arithmetic lives in router_tc.cu / router.cu,
-// dispatch.cu, gemm_tc_pair.cu / gemm_tc.cu / gemm_simt.cu, combine.cu, soft_balance.cu and
-// coselect.cu.
+// dispatch.cu, gemm_tc_pair.cu / gemm_tc.cu / gemm_simt.cu, combine.cu, soft_balance.cu,
+// scores.cu and coselect.cu.
 #include <climits>
 #include <cmath>
 #include <initializer_list>
@@ -517,7 +517,7 @@ moe_status_t moe_backward_scores(const moe_config_t* cfg, const moe_score_config
     if (st != MOE_OK) return st;
     if (scores->T != cfg->T || scores->E != cfg->E || scores->k != cfg->k) return MOE_ERR_INVALID_ARG;
     if (dense_routing(*cfg)) return MOE_ERR_UNSUPPORTED;
-    if (cfg->T > 0 && (!logits || !dlogits)) return MOE_ERR_INVALID_ARG;
+    if (cfg->T > 0 && (!logits || !dlogits || logits == dlogits)) return MOE_ERR_INVALID_ARG;
     if (!aligned16({logits, dlogits})) return MOE_ERR_INVALID_ARG;
     const ScoresGrad sg{scores, logits, dlogits};
     return layer_backward(cfg, &sg, dy, x, Wg, idx, w, offsets, row_token, slot_row, Xp, Gp, H, Yp, W1, W2, balance_loss,
