@@ -759,7 +759,7 @@ __global__ void __launch_bounds__(256) muon_finish_kernel(const MuonFinish a) {
 constexpr int kSide = 128;
 constexpr int kPlaneBytes = kSide * kSide * 2;       // one fp16 part of a slice, or of A
 constexpr int kBlockBytes = kSide * 128;             // 128 rows of 128 bytes
-constexpr int kSmallThreads = 256;
+constexpr int kSmallThreads = 512;
 constexpr int kMaxCluster = 8;
 constexpr int kUnits = kSide * kSide / 8 / kSmallThreads;   // units of 8 elements to a thread
 constexpr int kRecvBytes = 68608;                    // sums of n CTAs' rows: n ceil(128 / n) 512, at most for n = 7
@@ -962,26 +962,26 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
     constexpr std::integral_constant<bool, TALL> tall{};
     constexpr std::false_type major{};
     constexpr std::true_type minor{};
-    // Each thread has a row of the product (TMEM lane) and half of its columns.
-    const int row = (warp & 3) * 32 + lane, half = warp >> 2;
-    const uint32_t taddr = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * 64;
+    // Each thread has a row of the product (TMEM lane) and 32 of its columns.
+    const int row = (warp & 3) * 32 + lane, part = warp >> 2;
+    const uint32_t taddr = tmem + ((uint32_t)((warp & 3) * 32) << 16) + part * 32;
     auto put8 = [&](uint8_t* to, int unit, const float* v) {
         uint4 hi, lo;
         split8(v, hi, lo);
         *reinterpret_cast<uint4*>(to + unit_at(row, unit)) = hi;
         if (SPLIT) *reinterpret_cast<uint4*>(to + kPlaneBytes + unit_at(row, unit)) = lo;
     };
-    // 32 columns of the product, from column 32 h of the thread's half on; k: the reduction's length.
-    auto sums = [&](int h, int k, float (&v)[32]) {
+    // The thread's columns of the product; k: the reduction's length.
+    auto sums = [&](int k, float (&v)[32]) {
         uint32_t acc[32];
-        tmem_ld32(taddr + 32 * h, acc);
+        tmem_ld32(taddr, acc);
         tmem_ld_wait_regs(acc);
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(acc[i]);
 #pragma unroll
         for (int m = 1; m < SUMS; ++m) {
             if (16 * m >= k) break;
-            tmem_ld32(taddr + m * kSide + 32 * h, acc);
+            tmem_ld32(taddr + m * kSide, acc);
             tmem_ld_wait_regs(acc);
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] += __uint_as_float(acc[i]);
@@ -1013,19 +1013,18 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
     for (int step = 0; step < a.steps; ++step) {
         // ---- gram
         product(sX, tall, sX, tall, TALL ? nr : nc);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        {
             float v[32];
-            sums(h, TALL ? nr : nc, v);
+            sums(TALL ? nr : nc, v);
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] *= kAScale / (kXScale * kXScale);
             if (CS == 1) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) put8(sA, half * 8 + h * 4 + j, v + 8 * j);
+                for (int j = 0; j < 4; ++j) put8(sA, part * 4 + j, v + 8 * j);
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    *reinterpret_cast<float4*>(sA + unit_at(row, half * 16 + h * 8 + j)) =
+                    *reinterpret_cast<float4*>(sA + unit_at(row, part * 8 + j)) =
                         make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
             }
         }
@@ -1040,7 +1039,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
                      map_to_rank(smem_u32(&s_sums), (uint32_t)q));
             if (tid == 0) mbar_expect_tx(&s_sums, (uint32_t)((CS - 1) * own * 512));
             if (ok) ok = mbar_wait(&s_sums, (uint32_t)step & 1u, a.err);
-            // a thread adds up one unit of 8 values, or up to four (two CTAs: 64 rows of 16 units each)
+            // a thread adds up one unit of 8 values, or two (two CTAs: 64 rows of 16 units each)
             constexpr int MOST = kSide / 2 * (kSide / 8) / kSmallThreads;
             float v[MOST][8];
 #pragma unroll
@@ -1087,22 +1086,21 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
         product(sA, major, sA, major, a.side);
         // every CTA has its rows of A, so none of this one's are still being read by a copy
         if (CS > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        {
             float v[32], w[32];
-            sums(h, a.side, v);
+            sums(a.side, v);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) get8(sA, half * 8 + h * 4 + j, w + 8 * j);
+            for (int j = 0; j < 4; ++j) get8(sA, part * 4 + j, w + 8 * j);
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
                 v[i] = fmaf(a.b * (kBScale / kAScale), w[i], a.c * (kBScale / (kAScale * kAScale)) * v[i]);
-                if (half * 64 + h * 32 + i == row) {
+                if (part * 32 + i == row) {
                     s_diag[row] = fmaf(v[i], 1.f / kBScale, a.a);
                     v[i] = 0.f;
                 }
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) put8(sA, half * 8 + h * 4 + j, v + 8 * j);
+            for (int j = 0; j < 4; ++j) put8(sA, part * 4 + j, v + 8 * j);
         }
         ready();
         // ---- apply
@@ -1110,16 +1108,15 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
         else product(sA, major, sX, minor, a.side);
         const bool last = step + 1 == a.steps;
         const float drow = s_diag[row];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        {
             float v[32], w[32];
-            sums(h, a.side, v);
+            sums(a.side, v);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) get8(sX, half * 8 + h * 4 + j, w + 8 * j);
+            for (int j = 0; j < 4; ++j) get8(sX, part * 4 + j, w + 8 * j);
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
                 float4 d = make_float4(drow, drow, drow, drow);
-                if (TALL) d = *reinterpret_cast<const float4*>(s_diag + half * 64 + h * 32 + i);
+                if (TALL) d = *reinterpret_cast<const float4*>(s_diag + part * 32 + i);
                 v[i] = fmaf(d.x, w[i], v[i] * (1.f / kBScale));
                 v[i + 1] = fmaf(d.y, w[i + 1], v[i + 1] * (1.f / kBScale));
                 v[i + 2] = fmaf(d.z, w[i + 2], v[i + 2] * (1.f / kBScale));
@@ -1128,11 +1125,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
             if (last) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    *reinterpret_cast<float4*>(sA + unit_at(row, half * 16 + h * 8 + j)) =
+                    *reinterpret_cast<float4*>(sA + unit_at(row, part * 8 + j)) =
                         make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
             } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) put8(sX, half * 8 + h * 4 + j, v + 8 * j);
+                for (int j = 0; j < 4; ++j) put8(sX, part * 4 + j, v + 8 * j);
             }
         }
         ready();
