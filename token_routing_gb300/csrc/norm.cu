@@ -769,7 +769,9 @@ bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t
 
 // How a row is shared out: vector, threads to a row and bytes of it to a thread (16, 32 or 64; 0: too long
 // for registers). 32 bytes to a thread, and the next row's 32 in flight, keep the registers of a block of 512
-// threads; below 256 elements a warp takes 16 or 32 bytes a lane, and beyond 512 threads 64.
+// threads; below 256 elements a warp takes 16 or 32 bytes a lane, and beyond 512 threads 64. Measured with 16, 32
+// and 64 bytes to a thread: forward, 16384 rows of 1024 bf16 with a residual, 38, 25 and 41 us; the gradient of
+// 32768 rows of 2048 bf16 123, 89 and 267 us; of 2047 rows of 1023 fp32 13.0, 13.7 and 21.2 us.
 struct Shape {
     int ve, tpr, bytes;
 };
