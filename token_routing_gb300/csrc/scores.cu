@@ -41,19 +41,22 @@ __device__ __forceinline__ float warp_max(float v) {
     return r;
 }
 
-// One token by a warp; expert lane + 32 i is the lane's i-th. CHOICE: experts are compared by score plus
-// bias; else by logit. FULL: E = 32 V. Scores of all experts serve the comparison only and are within 2^-21
-// (hardware exponential and reciprocal); weights are computed anew, in full precision, from the chosen logits.
+// One token by a warp, up to its list of chosen experts. CHOICE: experts are compared by score plus bias; else by
+// logit. FULL: E = 32 V, and a lane has V experts side by side, so that a group is a lane or more and needs no
+// exchange but shuffles; else expert lane + 32 i is the lane's i-th. Scores of all experts serve the comparison
+// only and are within 2^-21 (hardware exponential and reciprocal); weights are computed anew, in full precision,
+// from the chosen logits.
 //
-// Bound by instructions: 32768 tokens of 256 experts in groups are 34 MB, 5 us at the copy rate, and take 28
-// (27 of them issuing: some 600 warp instructions a token). What keeps them few: the k-th largest of the 32 lanes' maxima bounds the k largest
-// from below, so only experts at or above it (8 to 12 of 256 for k = 8) are ranked, each by counting those
-// ahead of it; a reduction over the warp is one instruction.
+// Bound by instructions: 32768 tokens of 256 experts in groups are 34 MB, 5 us at the copy rate. What keeps them
+// few: the k-th largest of the 32 lanes' maxima bounds the k largest from below, so only experts at or above it (8
+// to 14 of 256 for k = 8) are ranked, each by counting those ahead of it; a reduction over the warp is one
+// instruction; weights are left to route_weights, for four tokens at once.
 template <int V, bool SOFTMAX, bool CHOICE, bool FULL>
-__device__ __forceinline__ void route_token(const ScoreArgs& a, int t, const float (&z)[V], const float (&bias)[V],
-                                            int lane, float* s_row, float2* s_cand, int* s_hist) {
+__device__ __forceinline__ void route_token(const ScoreArgs& a, const float (&z)[V], const float (&bias)[V], int lane,
+                                            float* s_row, float* s_val, int* s_id, int* pick, float2* norm) {
     const int E = a.E, k = a.k;
     const float inf = INFINITY;
+    auto id_of = [&](int i) { return FULL ? lane * V + i : lane + 32 * i; };
     // a row that holds NaN or +inf has no softmax: its first experts, with NaN weights
     bool bad = false;
     if (SOFTMAX) {
@@ -93,22 +96,19 @@ __device__ __forceinline__ void route_token(const ScoreArgs& a, int t, const flo
 #pragma unroll
         for (int i = 0; i < V; ++i) c[i] = rcp_approx(1.0f + ex2_approx(-z[i] * a.to_log2));
     }
+    if (SOFTMAX && lane == 0) *norm = make_float2(row_max, bad ? NAN : row_inv);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         // a logit of -inf, or a NaN, counts as -inf (fmaxf drops a NaN)
-        c[i] = fmaxf(CHOICE ? (z[i] == -inf ? -inf : c[i] + bias[i]) : z[i], -inf);
+        c[i] = CHOICE ? (z[i] > -inf ? c[i] + bias[i] : -inf) : fmaxf(z[i], -inf);
         if (SOFTMAX && bad) c[i] = -inf;
     }
 
     uint32_t shut = 0;                        // bit h << log: group h is not kept
-    const int log = FULL && a.groups == V ? (V == 8 ? 2 : V == 4 ? 3 : V == 2 ? 4 : 5) : a.lanes_log;
+    float top = -inf;                         // the lane's largest that is not shut
+    const int log = a.lanes_log;
     if (a.kept < a.groups) {
-        // 2^log lanes to a group, each reading every 2^log-th of its experts; a row of 32 is 33 words apart, so
-        // that groups of 32 are read from different banks
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (FULL || lane + 32 * i < E) s_row[lane + 33 * i] = c[i];
-        __syncwarp();
+        // 2^log lanes to a group
         float m1 = -inf, m2 = -inf;
         auto see = [&](float v) {
             m2 = fmaxf(m2, fminf(m1, v));
@@ -120,31 +120,48 @@ __device__ __forceinline__ void route_token(const ScoreArgs& a, int t, const flo
             m2 = fmaxf(fmaxf(m2, n2), fminf(m1, n1));
             m1 = fmaxf(m1, n1);
         };
-        int rank = 0;
-        const int g = lane >> log, sub = lane & ((1 << log) - 1);
-        if (FULL && a.groups == V) {
-            // groups of 32, a register of every lane each: the same with all numbers known
-            const float* row = s_row + g * 33 + sub;
+        if (FULL) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) see(row[j * (32 / V)]);
+            for (int i = 0; i < V; ++i) see(c[i]);
+            top = m1;
+            // a group's rank is counted by its lanes together, each against every 2^log-th group
+            auto rank_of = [&](int groups, int lg) {
+                const int step = 1 << lg, g = lane >> lg, sub = lane & (step - 1);
 #pragma unroll
-            for (int o = 16 / V; o > 0; o >>= 1) join(o);
-            const float worth = worth_of(32);
+                for (int o = step >> 1; o > 0; o >>= 1) join(o);
+                const float worth = worth_of(V << lg);
+                int rank = 0;
 #pragma unroll
-            for (int h = 0; h < V; ++h) {
-                const float v = __shfl_sync(0xffffffffu, worth, h * (32 / V));
-                if (v > worth || (v == worth && h < g)) ++rank;
-            }
-            shut = __ballot_sync(0xffffffffu, rank >= a.kept);
+                for (int first = 0; first < groups; first += step) {
+                    const int h = first + sub;
+                    const float v = __shfl_sync(0xffffffffu, worth, h << lg);
+                    if (h < groups && (v > worth || (v == worth && h < g))) ++rank;
+                }
+#pragma unroll
+                for (int o = step >> 1; o > 0; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+                return rank;
+            };
+            // (groups of 32 in a full row: with all numbers known)
+            const bool mine = (a.groups == V ? rank_of(V, V == 8 ? 2 : V == 4 ? 3 : V == 2 ? 4 : 5)
+                                             : rank_of(a.groups, log)) >= a.kept;
+            shut = __ballot_sync(0xffffffffu, mine);
+            if (mine) top = -inf;
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                if ((shut >> (i * (32 / V))) & 1u) c[i] = -inf;
+                if (mine) c[i] = -inf;
         } else {
-            const int size = E / a.groups, step = 1 << log;
+            // a lane reads every 2^log-th of a group's experts; a row of 32 is 33 words apart, so that groups of 32
+            // are read from different banks
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (lane + 32 * i < E) s_row[lane + 33 * i] = c[i];
+            __syncwarp();
+            const int size = E / a.groups, step = 1 << log, g = lane >> log, sub = lane & (step - 1);
             if (g < a.groups)
                 for (int e = g * size + sub; e < (g + 1) * size; e += step) see(s_row[e + (e >> 5)]);
             for (int o = step >> 1; o > 0; o >>= 1) join(o);
             const float worth = worth_of(size);
+            int rank = 0;
             for (int h = 0; h < a.groups; ++h) {
                 const float v = __shfl_sync(0xffffffffu, worth, h << log);
                 if (v > worth || (v == worth && h < g)) ++rank;
@@ -153,15 +170,16 @@ __device__ __forceinline__ void route_token(const ScoreArgs& a, int t, const flo
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const uint32_t h = ((uint32_t)(lane + 32 * i) * a.group_mul) >> 16;
-                if ((FULL || lane + 32 * i < E) && ((shut >> (h << log)) & 1u)) c[i] = -inf;
+                if (lane + 32 * i < E && ((shut >> (h << log)) & 1u)) c[i] = -inf;
+                top = fmaxf(top, c[i]);
             }
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) top = fmaxf(top, c[i]);
     }
 
     // a lower bound of the k largest (lanes that tie fall out together, which only lowers it)
-    float top = c[0];
-#pragma unroll
-    for (int i = 1; i < V; ++i) top = fmaxf(top, c[i]);
     float least = -inf;
 #pragma unroll
     for (int j = 0; j < MOE_MAX_K; ++j) {
@@ -172,37 +190,56 @@ __device__ __forceinline__ void route_token(const ScoreArgs& a, int t, const flo
     // experts at or above it, in order of their ids (an expert that is shut stands at -inf, like a masked one)
     int n = kCand + 1;
     if (least > -inf) {
-        n = 0;
+        if (FULL) {
+            int own = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const uint32_t at = __ballot_sync(0xffffffffu, c[i] >= least);
-            if (c[i] >= least) s_cand[n + __popc(at & ((1u << lane) - 1u))] = make_float2(c[i], __int_as_float(lane + 32 * i));
-            n += __popc(at);
+            for (int i = 0; i < V; ++i) own += c[i] >= least;
+            int at = own;
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const int v = __shfl_up_sync(0xffffffffu, at, o);
+                if (lane >= o) at += v;
+            }
+            n = __shfl_sync(0xffffffffu, at, 31);
+            at -= own;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (c[i] >= least) {
+                    s_val[at] = c[i];
+                    s_id[at++] = lane * V + i;
+                }
+        } else {
+            n = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const uint32_t at = __ballot_sync(0xffffffffu, c[i] >= least);
+                if (c[i] >= least) {
+                    const int to = n + __popc(at & ((1u << lane) - 1u));
+                    s_val[to] = c[i];
+                    s_id[to] = lane + 32 * i;
+                }
+                n += __popc(at);
+            }
         }
+        if (lane < 4) s_val[n + lane] = -inf;       // ranks are counted in fours
     }
     __syncwarp();
-    int mine = -1, slot = k;     // the lane's chosen expert and its place
     if (n <= kCand) {
-        // what follows the last candidate counts for nothing
-        const float2 own = s_cand[lane];
+        const float own = s_val[lane];              // (counts for nothing behind the last)
         int rank = 0;
         for (int j = 0; j < n; j += 4) {
-            const float4 v01 = *reinterpret_cast<const float4*>(s_cand + j), v23 = *reinterpret_cast<const float4*>(s_cand + j + 2);
-            const float v[4] = {v01.x, v01.z, v23.x, v23.z};
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (j + q < n && (v[q] > own.x || (v[q] == own.x && j + q < lane))) ++rank;
+            const float4 v = *reinterpret_cast<const float4*>(s_val + j);
+            rank += (v.x > own) + (v.y > own) + (v.z > own) + (v.w > own);
         }
-        if (lane < n && rank < k) {
-            slot = rank;
-            mine = __float_as_int(own.y);
-        }
+        if (__popc(__reduce_or_sync(0xffffffffu, lane < n ? 1u << rank : 0u)) != n)      // equal ones: the first is ahead
+            for (int j = 0; j < n; ++j) rank += j < lane && s_val[j] == own;
+        if (lane < n && rank < k) pick[rank] = s_id[lane];
     } else {
         // many equal values, or fewer than k above -inf: one expert after another
         uint32_t open = 0;       // bit i: the lane's i-th expert may be taken
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const uint32_t h = ((uint32_t)(lane + 32 * i) * a.group_mul) >> 16;
+            const uint32_t h = ((uint32_t)id_of(i) * a.group_mul) >> 16;
             if ((FULL || lane + 32 * i < E) && !((shut >> (h << log)) & 1u)) open |= 1u << i;
         }
         for (int j = 0; j < k; ++j) {
@@ -212,38 +249,50 @@ __device__ __forceinline__ void route_token(const ScoreArgs& a, int t, const flo
             for (int i = 0; i < V; ++i)
                 if (((open >> i) & 1u) && (c[i] > best || id == 0xffffffffu)) {
                     best = c[i];
-                    id = (uint32_t)(lane + 32 * i);
+                    id = (uint32_t)id_of(i);
                 }
             const float most = warp_max(best);
             const uint32_t first = __reduce_min_sync(0xffffffffu, best == most ? id : 0xffffffffu);
-            if (lane == j) {
-                mine = (int)first;
-                slot = j;
-            }
+            if (lane == j) pick[j] = (int)first;
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                if ((uint32_t)(lane + 32 * i) == first) open &= ~(1u << i);
+                if ((uint32_t)id_of(i) == first) open &= ~(1u << i);
         }
     }
-    // weights, by the lanes that hold a chosen expert
-    const bool has = slot < k;
-    const float zc = has ? __ldg(a.logits + (size_t)t * E + mine) : -inf;
+    __syncwarp();
+}
+
+// Weights of up to four tokens t, t + step, ..., eight lanes to each.
+template <bool SOFTMAX>
+__device__ __forceinline__ void route_weights(const ScoreArgs& a, int t, int step, int tokens, int lane, const int* pick,
+                                              const float2* norm, int* s_hist) {
+    const int j = lane >> 3, slot = lane & 7;
+    const bool has = j < tokens && slot < a.k;
+    const size_t row = (size_t)t + (size_t)j * step;
+    const int mine = has ? pick[lane] : 0;
+    const float zc = has ? __ldg(a.logits + row * a.E + mine) : -INFINITY;
+    const float2 whole = SOFTMAX && has ? norm[j] : make_float2(0.f, 1.f);      // row maximum, 1 / sum or NaN
     float s = 0.f;
     if (SOFTMAX && a.renorm) {
-        float mx = warp_max(fmaxf(zc, -inf));
-        if (mx == -inf) mx = 0.f;
+        float mx = fmaxf(zc, -INFINITY);
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        if (mx == -INFINITY) mx = 0.f;
         s = has ? expf(scaled(zc - mx, a.inv_hi, a.inv_lo)) : 0.f;
-        const float sum = warp_sum(s);
-        s = sum > 0.f ? s / sum : 0.f;
-    } else {
-        if (has) s = SOFTMAX ? expf(scaled(zc - row_max, a.inv_hi, a.inv_lo)) * row_inv
-                             : 1.0f / (1.0f + expf(-scaled(zc, a.inv_hi, a.inv_lo)));
-        if (a.renorm) s = s / (warp_sum(s) + kTiny);
+    } else if (has) {
+        s = SOFTMAX ? expf(scaled(zc - whole.x, a.inv_hi, a.inv_lo)) : 1.0f / (1.0f + expf(-scaled(zc, a.inv_hi, a.inv_lo)));
     }
-    if (SOFTMAX && bad) s = NAN;
+    if (a.renorm) {
+        float sum = s;
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        s = SOFTMAX ? (sum > 0.f ? s / sum : 0.f) : s / (sum + kTiny);
+    }
+    if (SOFTMAX) s *= whole.y;
     if (has) {
-        a.idx[(size_t)t * k + slot] = mine;
-        a.w[(size_t)t * k + slot] = s * a.scale;
+        const size_t at = row * a.k + slot;
+        a.idx[at] = mine;
+        a.w[at] = s * a.scale;
         if (a.part) atomicAdd(s_hist + mine, 1);
     }
     __syncwarp();
@@ -274,8 +323,11 @@ __device__ __forceinline__ void block_balance(const int* s_counts, int T, int E,
 template <int V, bool SOFTMAX, bool CHOICE, bool FULL>
 __global__ void __launch_bounds__(kThreads, kScoreBlocks) route_scores_kernel(const ScoreArgs a, int32_t* counts,
                                                                              float* balance) {
-    __shared__ float s_row[kWarps][33 * V];
-    __shared__ __align__(16) float2 s_cand[kWarps][32 * V];      // (all may tie)
+    __shared__ float s_row[FULL ? 1 : kWarps][FULL ? 1 : 33 * V];
+    __shared__ __align__(16) float s_val[kWarps][32 * V + 4];    // (all may tie)
+    __shared__ int s_id[kWarps][32 * V];
+    __shared__ int s_pick[kWarps][4 * MOE_MAX_K];
+    __shared__ float2 s_norm[kWarps][4];
     __shared__ int s_hist[MOE_MAX_EXPERTS];
     __shared__ double s_red[kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -286,20 +338,37 @@ __global__ void __launch_bounds__(kThreads, kScoreBlocks) route_scores_kernel(co
     float bias[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int e = lane + 32 * i;
-        bias[i] = CHOICE && a.bias && e < a.E ? __ldg(a.bias + e) : 0.f;
+        const int e = FULL ? lane * V + i : lane + 32 * i;
+        bias[i] = CHOICE && a.bias && e < a.E ? fmaxf(__ldg(a.bias + e), -INFINITY) : 0.f;     // (a NaN: never chosen)
     }
     int t = blockIdx.x * kWarps + warp;
     float z[V], next[V];
     auto fetch = [&](int u, float (&into)[V]) {
-        const float* p = a.logits + (size_t)min(u, a.T - 1) * a.E + lane;     // (behind the last token: not used)
+        const float* p = a.logits + (size_t)min(u, a.T - 1) * a.E;     // (behind the last token: not used)
+        if constexpr (FULL && V >= 4) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) into[i] = FULL || lane + 32 * i < a.E ? __ldg(p + 32 * i) : -INFINITY;
+            for (int i = 0; i < V; i += 4) {
+                const float4 v = __ldg(reinterpret_cast<const float4*>(p + lane * V + i));
+                into[i] = v.x; into[i + 1] = v.y; into[i + 2] = v.z; into[i + 3] = v.w;
+            }
+        } else if constexpr (FULL && V == 2) {
+            const float2 v = __ldg(reinterpret_cast<const float2*>(p + lane * V));
+            into[0] = v.x; into[1] = v.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) into[i] = FULL || lane + 32 * i < a.E ? __ldg(p + lane + 32 * i) : -INFINITY;
+        }
     };
     if (t < a.T) fetch(t, z);
-    for (; t < a.T; t += nwarps) {
+    for (int done = 0; t < a.T; t += nwarps) {
         fetch(t + nwarps, next);
-        route_token<V, SOFTMAX, CHOICE, FULL>(a, t, z, bias, lane, s_row[warp], s_cand[warp], s_hist);
+        route_token<V, SOFTMAX, CHOICE, FULL>(a, z, bias, lane, s_row[FULL ? 0 : warp], s_val[warp], s_id[warp],
+                                              s_pick[warp] + done * MOE_MAX_K, s_norm[warp] + done);
+        ++done;
+        if (done == 4 || t + nwarps >= a.T) {
+            route_weights<SOFTMAX>(a, t - (done - 1) * nwarps, nwarps, done, lane, s_pick[warp], s_norm[warp], s_hist);
+            done = 0;
+        }
 #pragma unroll
         for (int i = 0; i < V; ++i) z[i] = next[i];
     }
