@@ -105,6 +105,7 @@ __device__ __forceinline__ void route_token(const ScoreArgs& a, const float (&z)
     }
 
     uint32_t shut = 0;                        // bit h << log: group h is not kept
+    bool out = false;                         // FULL: the lane's group is not
     float top = -inf;                         // the lane's largest that is not shut
     const int log = a.lanes_log;
     if (a.kept < a.groups) {
@@ -145,10 +146,8 @@ __device__ __forceinline__ void route_token(const ScoreArgs& a, const float (&z)
             const bool mine = (a.groups == V ? rank_of(V, V == 8 ? 2 : V == 4 ? 3 : V == 2 ? 4 : 5)
                                              : rank_of(a.groups, log)) >= a.kept;
             shut = __ballot_sync(0xffffffffu, mine);
+            out = mine;
             if (mine) top = -inf;
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (mine) c[i] = -inf;
         } else {
             // a lane reads every 2^log-th of a group's experts; a row of 32 is 33 words apart, so that groups of 32
             // are read from different banks
@@ -187,24 +186,27 @@ __device__ __forceinline__ void route_token(const ScoreArgs& a, const float (&z)
         least = warp_max(top);
         if (top == least) top = -inf;
     }
-    // experts at or above it, in order of their ids (an expert that is shut stands at -inf, like a masked one)
+    // experts at or above it, in order of their ids
     int n = kCand + 1;
     if (least > -inf) {
         if (FULL) {
+            const float bar = out ? NAN : least;       // (no comparison holds)
             int own = 0;
 #pragma unroll
-            for (int i = 0; i < V; ++i) own += c[i] >= least;
-            int at = own;
-#pragma unroll
-            for (int o = 1; o < 32; o *= 2) {
-                const int v = __shfl_up_sync(0xffffffffu, at, o);
-                if (lane >= o) at += v;
+            for (int i = 0; i < V; ++i) own += c[i] >= bar;
+            // places of a lane's own: the lanes before it, by the bits of their counts (a scan: 25.2 us for 24.7)
+            const uint32_t before = (1u << lane) - 1u;
+            const uint32_t b0 = __ballot_sync(0xffffffffu, own & 1), b1 = __ballot_sync(0xffffffffu, own & 2),
+                           b2 = __ballot_sync(0xffffffffu, own & 4), b3 = __ballot_sync(0xffffffffu, own & 8);
+            int at = __popc(b0 & before) + 2 * __popc(b1 & before);
+            n = __popc(b0) + 2 * __popc(b1);
+            if (b2 | b3) {
+                at += 4 * __popc(b2 & before) + 8 * __popc(b3 & before);
+                n += 4 * __popc(b2) + 8 * __popc(b3);
             }
-            n = __shfl_sync(0xffffffffu, at, 31);
-            at -= own;
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                if (c[i] >= least) {
+                if (c[i] >= bar) {
                     s_val[at] = c[i];
                     s_id[at++] = lane * V + i;
                 }
