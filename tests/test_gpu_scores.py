@@ -140,6 +140,27 @@ def test_masked_experts(kind, with_bias, moe_lib, cuda_device):
 
 
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups", [(E, g) for E in (32, 64, 128, 256) for g in (2, 4, 8, 16, 32)])
+def test_groups_of_whole_rows(E, groups, kind, moe_lib, cuda_device):
+    """Rows of whole registers, groups of one expert to half a row: random values, equal ones, masked ones."""
+    kept = max(1, groups // 4)
+    k = min(8, E // groups * kept)
+    z, bias = make(211, E, seed=E + groups)
+    for top in (1, 2):
+        check(moe_lib, z, bias, kind, k, groups, kept, top, renorm=k > 1)
+    g = torch.Generator().manual_seed(E * groups)
+    few = torch.randint(0, 9, (211, E), generator=g).float()       # whole numbers tie exactly on both sides
+    check(moe_lib, few, None, kind, k, groups, kept, 1, renorm=k > 1, all_rows=True)
+    few[torch.rand(211, E, generator=g) < 0.9] = float("-inf")     # open groups with fewer than k, or none
+    few[:5] = float("-inf")
+    _, _, idx, w, _, _ = run(moe_lib, few, None, kind, k, groups, kept, 1)
+    want, _, _ = O.choose(f64(few), None, kind, k, groups, kept, 1)
+    got = idx.cpu().numpy().astype(np.int64)
+    assert (got == want).all()
+    assert (f64(w)[np.isneginf(np.take_along_axis(f64(few), got, axis=1))] == 0).all()
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("groups,kept,top", GROUPS)
 def test_rows_that_are_not_finite(kind, groups, kept, top, moe_lib, cuda_device):
     z, bias = make(64, 64, seed=8)
@@ -276,3 +297,17 @@ def test_other_stream_and_graph(moe_lib, cuda_device):
         assert torch.equal(a, b)
     assert int(n.sum()) == 2000
     moe.get_error()
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [100, 128])
+def test_bias_that_is_not_finite(E, kind, moe_lib, cuda_device):
+    """A bias of NaN counts as one of -inf; one of +inf is chosen first, unless its logit is -inf."""
+    z, bias = make(77, E, seed=12)
+    bias[3], bias[40], z[5, 40] = float("nan"), float("inf"), float("-inf")
+    _, _, idx, w, _, _ = run(moe_lib, z, bias, kind, 8)
+    bias[3] = float("-inf")
+    _, _, i2, w2, _, _ = run(moe_lib, z, bias, kind, 8)
+    assert torch.equal(idx, i2) and torch.equal(w, w2)
+    got = idx.cpu().numpy()
+    assert (got != 3).all() and (np.delete(got[:, 0], 5) == 40).all() and (got[5] != 40).all()

@@ -49,9 +49,10 @@ __device__ __forceinline__ float warp_max(float v) {
 //
 // Bound by instructions: 32768 tokens of 256 experts in groups are 34 MB, 5 us at the copy rate, and take 22 us,
 // 518 warp instructions a token in 75% of the issue slots (700 with every 32nd expert to a lane, groups exchanged
-// through shared memory and each token's weights by themselves: 29 us). What keeps them few: the k-th largest of the 32 lanes' maxima bounds the k largest from below, so only experts at or above it (8
-// to 14 of 256 for k = 8) are ranked, each by counting those ahead of it; a reduction over the warp is one
-// instruction; weights are left to route_weights, for four tokens at once.
+// through shared memory and each token's weights by themselves: 29 us). What keeps them few: the k-th largest of the
+// 32 lanes' maxima bounds the k largest from below, so only experts at or above it (8 to 14 of 256 for k = 8) are
+// ranked, each by counting those ahead of it; a reduction over the warp is one instruction; weights are left to
+// route_weights, for four tokens at once.
 template <int V, bool SOFTMAX, bool CHOICE, bool FULL>
 __device__ __forceinline__ void route_token(const ScoreArgs& a, const float (&z)[V], const float (&bias)[V], int lane,
                                             float* s_row, float* s_val, int* s_id, int* pick, float2* norm) {
