@@ -508,51 +508,30 @@ __device__ __forceinline__ float slot_grad(const ScoreGradArgs& a, const Slot& s
     return s.on ? g * (a.scale * inv) * slope : 0.f;
 }
 
-// Gradient at the chosen experts, zeros elsewhere: a warp holds rows of zeros in shared memory, four tokens' at a
-// time, sets their chosen entries, copies the rows out in 16-byte vectors and clears the entries. What it waits
-// for is one load after another (idx, then that logit), so kQuads times four tokens go together.
-constexpr int kQuads = 1;
-constexpr int kGradWarps = 4;
+// Gradient at the chosen experts, zeros elsewhere, by a warp for four tokens at a time: zeros go out while idx and
+// then its logits are on their way, and the chosen entries after them (the lines are still in L2).
+constexpr int kGradWarps = 4, kGradBlocks = 12;
 template <bool SOFTMAX>
-__global__ void __launch_bounds__(32 * kGradWarps) scores_grad_kernel(const ScoreGradArgs a) {
-    extern __shared__ __align__(16) float s_rows[];
+__global__ void __launch_bounds__(32 * kGradWarps, kGradBlocks) scores_grad_kernel(const ScoreGradArgs a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane & 7;
-    float* row = s_rows + (size_t)warp * kQuads * 4 * a.E;
-    for (int i = lane; i < kQuads * 4 * a.E; i += 32) row[i] = 0.f;
-    __syncwarp();
     pdl_wait();
-    const int sets = (a.T + 4 * kQuads - 1) / (4 * kQuads), step = gridDim.x * kGradWarps;
-    for (int q = blockIdx.x * kGradWarps + warp; q < sets; q += step) {
-        const int t0 = q * 4 * kQuads;
-        Slot s[kQuads];
-        float z[kQuads];
-#pragma unroll
-        for (int u = 0; u < kQuads; ++u) s[u].load(a, t0 + 4 * u + (lane >> 3), j);
-#pragma unroll
-        for (int u = 0; u < kQuads; ++u) {
-            s[u].check(a, j);
-            z[u] = s[u].on ? __ldg(a.logits + (size_t)(t0 + 4 * u + (lane >> 3)) * a.E + s[u].e) : -INFINITY;
-        }
-#pragma unroll
-        for (int u = 0; u < kQuads; ++u) {
-            const int t = t0 + 4 * u + (lane >> 3);
-            const float dz = scaled(slot_grad<SOFTMAX>(a, s[u], z[u]), a.inv_hi, a.inv_lo);
-            if (s[u].on) row[(4 * u + (lane >> 3)) * a.E + s[u].e] = dz;
-            if (a.dz && t < a.T && j < a.k) a.dz[(size_t)t * a.k + j] = s[u].on ? dz : 0.f;
-        }
-        __syncwarp();
-        float* out = a.dlogits + (size_t)t0 * a.E;
-        if (t0 + 4 * kQuads <= a.T) {
-            for (int i = lane; i < kQuads * a.E; i += 32)
-                reinterpret_cast<float4*>(out)[i] = reinterpret_cast<const float4*>(row)[i];
+    const int quads = (a.T + 3) / 4, step = gridDim.x * kGradWarps;
+    for (int q = blockIdx.x * kGradWarps + warp; q < quads; q += step) {
+        const int t = 4 * q + (lane >> 3);
+        Slot s;
+        s.load(a, t, j);
+        float* out = a.dlogits + (size_t)4 * q * a.E;
+        if (4 * q + 4 <= a.T) {
+            for (int i = lane; i < a.E; i += 32) reinterpret_cast<float4*>(out)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         } else {
-            for (int i = lane; i < (a.T - t0) * a.E; i += 32) out[i] = row[i];
+            for (int i = lane; i < (a.T - 4 * q) * a.E; i += 32) out[i] = 0.f;
         }
-        __syncwarp();
-#pragma unroll
-        for (int u = 0; u < kQuads; ++u)
-            if (s[u].on) row[(4 * u + (lane >> 3)) * a.E + s[u].e] = 0.f;
-        __syncwarp();
+        s.check(a, j);
+        const float z = s.on ? __ldg(a.logits + (size_t)t * a.E + s.e) : -INFINITY;
+        const float dz = scaled(slot_grad<SOFTMAX>(a, s, z), a.inv_hi, a.inv_lo);
+        __syncwarp();                    // the zeros come first
+        if (s.on) a.dlogits[(size_t)t * a.E + s.e] = dz;
+        if (a.dz && t < a.T && j < a.k) a.dz[(size_t)t * a.k + j] = s.on ? dz : 0.f;
     }
 }
 
@@ -691,9 +670,9 @@ cudaError_t launch_scores_grad(const moe_score_config_t& c, const float* logits,
                     : v <= 4 ? scores_grad_full_kernel<4> : scores_grad_full_kernel<8>;
         e = launch_pdl(kern, dim3(blocks), dim3(kThreads), 0, s, a);
     } else {
-        const int blocks = std::min(ceil_div(c.T, 4 * kQuads * kGradWarps), num_sms() * 12);
+        const int blocks = std::min(ceil_div(c.T, 4 * kGradWarps), num_sms() * kGradBlocks);
         auto kern = c.score == MOE_SCORE_SOFTMAX ? scores_grad_kernel<true> : scores_grad_kernel<false>;
-        e = launch_pdl(kern, dim3(blocks), dim3(32 * kGradWarps), (size_t)kGradWarps * kQuads * 4 * c.E * sizeof(float), s, a);
+        e = launch_pdl(kern, dim3(blocks), dim3(32 * kGradWarps), 0, s, a);
     }
     count_launch();
     return e;
