@@ -1,12 +1,13 @@
 // Orthogonalised updates of stacks of matrices (Muon): momentum, Newton-Schulz products on CTA pairs
-// (tcgen05.mma.cta_group::2, 256 x 256 x 64 tiles of fp16 operands), and the step on the weights.
+// (tcgen05.mma.cta_group::2, tiles of 256 rows, 64 to 256 columns and 64 k of fp16 operands), and the step on the
+// weights.
 //
 // With A = X X^T (X^T X where there are more rows than columns: the smaller side), one step is
 //   gram:  A                                   symmetric
 //   poly:  B = a I + b A + c A A               symmetric
 //   apply: X = B X   (X B)
 // Of the symmetric two only the tiles on and below the diagonal are computed; each is stored twice, once
-// as it is and once turned. On the diagonal both operands are the same rows, which are loaded once.
+// as it is and once turned. Where both operands of a square tile are the same rows, they are loaded once.
 //
 // Operands are fp16, not bf16: the tensor cores take both at one rate, and all of the factors are
 // bounded (singular values of X are 1 at most and stay near it), so bf16's range buys nothing and fp16's
@@ -31,9 +32,10 @@ namespace moe {
 namespace {
 
 constexpr int kTile = 256, kHalf = 128;              // tile of a pair, rows of a CTA
-constexpr int kPartBytes = kHalf * BK * 2;           // 16 KB: a CTA's rows of A, or its half of B
-constexpr int kStageBytes = 2 * kPartBytes;
-constexpr int kStages = 6;
+constexpr int kPartBytes = kHalf * BK * 2;           // 16 KB: a CTA's rows of A
+constexpr int kRingBytes = 12 * kPartBytes;          // the stages
+// A stage holds a k-block of the CTA's rows of A and of its half of B's nt columns, in one part or two.
+constexpr int stage_bytes(int nt, bool split) { return (split ? 2 : 1) * (kPartBytes + nt / 2 * BK * 2); }
 constexpr int kEpiWarps = 8;
 constexpr int kGemmThreads = 64 + 32 * kEpiWarps;
 constexpr int kSegment = 2;                          // k-blocks (of 64) to a partial sum, with SPLIT
@@ -43,7 +45,7 @@ enum Op : int { kGram = 0, kPoly = 1, kApply = 2 };
 
 struct MuonGemm {
     int count, M, N, K;           // per matrix: out [M, N], reduction K
-    int m_tiles, n_tiles, tiles;  // tiles: of one matrix
+    int n_tiles, tiles;           // of a row of tiles; of one matrix
     const uint16_t* side;         // [planes][count][M, ld]: poly: A; apply: X
     int ld;
     float* diag;                  // [count][dstride]: poly writes B's diagonal, apply reads it
@@ -79,23 +81,25 @@ struct MuonTile {
 };
 // Tile r of a matrix: row-major, or for the symmetric products the tiles on and below the diagonal, one
 // row of tiles after another.
-template <bool SYM>
+template <bool SYM, int NT>
 __device__ __forceinline__ MuonTile decode_tile(const MuonGemm& p, int tile) {
+    constexpr int R = kTile / NT;      // tiles to a square
     MuonTile t;
     t.z = tile / p.tiles;
     const int r = tile - t.z * p.tiles;
     int i, j;
     if (SYM) {
-        i = (int)((sqrtf(8.0f * (float)r + 1.0f) - 1.0f) * 0.5f);
-        while (i * (i + 1) / 2 > r) --i;
-        while ((i + 1) * (i + 2) / 2 <= r) ++i;
-        j = r - i * (i + 1) / 2;
+        const int q = r / R;
+        i = (int)((sqrtf(8.0f * (float)q + 1.0f) - 1.0f) * 0.5f);
+        while (i * (i + 1) / 2 > q) --i;
+        while ((i + 1) * (i + 2) / 2 <= q) ++i;
+        j = r - R * (i * (i + 1) / 2);
     } else {
         i = r / p.n_tiles;
         j = r - i * p.n_tiles;
     }
     t.m0 = i * kTile;
-    t.n0 = j * kTile;
+    t.n0 = j * NT;
     return t;
 }
 
@@ -164,21 +168,25 @@ enum Out : int { kParts = 0, kResult = 1 };
 // expert GEMMs.
 //
 // SPLIT: the tensor cores cut off their sums at 24 bits with every addition, which over a long K is far more
-// than 22-bit operands leave. So K is taken in segments of kSegment k-blocks (2048 x 1024: 3.5e-6 of the result
-// in 533 us, with one k-block 2.0e-6 in 655, plain fp32 products 3.3e-6); each has a TMEM buffer to
-// itself, lo hi and hi lo before hi hi (what is cut off is measured by what the sum holds), and the epilogue
-// warps add the segments up in registers, rounding to nearest, while the other buffer fills.
-template <int OP, bool A_MN, bool B_MN, bool SPLIT, int OUT>
+// than 22-bit operands leave. So K is taken in segments, of kSegment k-blocks in the widest tiles (4 x 2048 x 1024:
+// 722 us, with one 892) and of one in the others, which do not fill the tensor cores (416 x 768: 2.2e-6 of the
+// result, where segments of two left 3.7e-6; plain fp32 products 2.2e-6). Each segment has a TMEM buffer to itself, lo hi
+// and hi lo before hi hi (what is cut off is measured by what the sum holds: one k-block's three products after
+// the other's, 4.5e-6), and the epilogue warps add the segments up in registers, rounding to nearest, while the
+// other buffer fills. A stage has all four parts of its k-block (loaded for each product anew, 6 in place of 4:
+// 1024 x 4096 682 us and 608 with tiles alike).
+template <int OP, bool A_MN, bool B_MN, bool SPLIT, int OUT, int NT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                  const __grid_constant__ CUtensorMap tmO) {
     constexpr bool SYM = OP != kApply, SIDED = OP != kGram, TALL = OP == kApply && !B_MN;
+    constexpr int PL = SPLIT ? 2 : 1, B_BYTES = NT / 2 * BK * 2, STAGE = stage_bytes(NT, SPLIT), STAGES = kRingBytes / STAGE;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* stg_smem = smem + kStages * kStageBytes;
+    uint8_t* stg_smem = smem + kRingBytes;
     uint64_t* full = reinterpret_cast<uint64_t*>(stg_smem + kEpiWarps * 2 * STG_BYTES);
-    uint64_t* empty = full + kStages;
-    uint64_t* tfull = empty + kStages;
+    uint64_t* empty = full + STAGES;
+    uint64_t* tfull = empty + STAGES;
     uint64_t* tempty = tfull + 2;
     uint64_t* drain = tempty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -190,7 +198,7 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
     const int cluster_id = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) { mbar_init(full + s, 1); mbar_init(empty + s, 1); }
+        for (int s = 0; s < STAGES; ++s) { mbar_init(full + s, 1); mbar_init(empty + s, 1); }
         for (int b = 0; b < 2; ++b) { mbar_init(tfull + b, 1); mbar_init(tempty + b, 2 * 32 * kEpiWarps); }
         mbar_init(drain, 1);
         *s_fail = 0;
@@ -211,8 +219,7 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
     const uint32_t tmem_base = *tmem_slot;
     const int num_tiles = p.count * p.tiles;
     const int kblocks = (p.K + BK - 1) / BK;
-    const int seg = SPLIT ? kSegment : kblocks;      // k-blocks to an accumulator
-    constexpr int TERMS = SPLIT ? 3 : 1;
+    const int seg = SPLIT ? (NT == kTile ? kSegment : 1) : kblocks;      // k-blocks to an accumulator
 
     if (warp == 0) {
         if (lane == 0) {
@@ -220,59 +227,56 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
             long long issued = 0;
             bool ok = true;
             for (int tile = cluster_id; tile < num_tiles && ok; tile += nclusters) {
-                const MuonTile t = decode_tile<SYM>(p, tile);
-                const int mr = t.m0 + (int)rank * kHalf, nh = t.n0 + (int)rank * kHalf;
-                const bool same = SYM && !SPLIT && t.m0 == t.n0;
-                for (int kb = 0, term = 0, first = 0; first < kblocks;) {
+                const MuonTile t = decode_tile<SYM, NT>(p, tile);
+                const int mr = t.m0 + (int)rank * kHalf, nh = t.n0 + (int)rank * (NT / 2);
+                const bool same = SYM && !SPLIT && NT == kTile && t.m0 == t.n0;
+                for (int kb = 0; kb < kblocks; ++kb) {
                     if (!mbar_wait(empty + s, ph ^ 1, p.err)) { ok = false; break; }
-                    const uint32_t sa = smem_u32(smem + s * kStageBytes), sb = sa + kPartBytes;
+                    const uint32_t sa = smem_u32(smem + s * STAGE), sb = sa + PL * kPartBytes;
                     const uint32_t fb = map_to_rank(smem_u32(full + s), 0);
-                    if (leader) mbar_expect_tx(full + s, same ? 2 * kPartBytes : 2 * kStageBytes);
+                    if (leader) mbar_expect_tx(full + s, same ? 2 * kPartBytes : 2 * STAGE);
                     const int k0 = kb * BK;
-                    const int za = t.z + (SPLIT && term == 0 ? p.count : 0), zb = t.z + (SPLIT && term == 1 ? p.count : 0);
-                    if (!A_MN) {
-                        tma_load_3d_pair(sa, &tmA, k0, mr, za, fb);
-                    } else {
 #pragma unroll
-                        for (int j = 0; j < kHalf / 64; ++j)
-                            tma_load_3d_pair(sa + j * (BK * 128), &tmA, mr + 64 * j, k0, za, fb);
-                    }
-                    if (same) {
-                    } else if (!B_MN) {
-                        tma_load_3d_pair(sb, &tmB, k0, nh, zb, fb);
-                    } else {
+                    for (int part = 0; part < PL; ++part) {
+                        const int z = t.z + part * p.count;
+                        if (!A_MN) {
+                            tma_load_3d_pair(sa + part * kPartBytes, &tmA, k0, mr, z, fb);
+                        } else {
 #pragma unroll
-                        for (int j = 0; j < kHalf / 64; ++j)
-                            tma_load_3d_pair(sb + j * (BK * 128), &tmB, nh + 64 * j, k0, zb, fb);
+                            for (int j = 0; j < kHalf / 64; ++j)
+                                tma_load_3d_pair(sa + part * kPartBytes + j * (BK * 128), &tmA, mr + 64 * j, k0, z, fb);
+                        }
+                        if (same) {
+                        } else if (!B_MN) {
+                            tma_load_3d_pair(sb + part * B_BYTES, &tmB, k0, nh, z, fb);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < NT / 128; ++j)
+                                tma_load_3d_pair(sb + part * B_BYTES + j * (BK * 128), &tmB, nh + 64 * j, k0, z, fb);
+                        }
                     }
                     ++issued;
-                    if (++s == kStages) { s = 0; ph ^= 1; }
-                    if (++kb == min(first + seg, kblocks)) {
-                        if (++term == TERMS) {
-                            term = 0;
-                            first += seg;
-                        }
-                        kb = first;
-                    }
+                    if (++s == STAGES) { s = 0; ph ^= 1; }
                 }
             }
             if (!ok) {
                 *s_fail = 1;
                 // no copy may be in flight when the CTAs leave: the stages issued last, oldest first
-                const long long n = issued < kStages ? issued : kStages;
+                const long long n = issued < STAGES ? issued : STAGES;
                 for (long long i = issued - n; i < issued && leader; ++i)
-                    if (!mbar_wait(full + (int)(i % kStages), (uint32_t)(i / kStages) & 1u, p.err)) break;
+                    if (!mbar_wait(full + (int)(i % STAGES), (uint32_t)(i / STAGES) & 1u, p.err)) break;
             }
         }
     } else if (warp == 1) {
         if (leader && lane == 0) {
-            const uint32_t idesc = idesc_fp16(kTile, BN, A_MN, B_MN);
+            const uint32_t idesc = idesc_fp16(kTile, NT, A_MN, B_MN);
             const uint32_t s0 = smem_u32(smem);
             const uint64_t a_desc0 = A_MN ? make_desc(s0, BK * 128, 1024) : make_desc(s0, 16, 1024);
-            const uint64_t b_desc0 = B_MN ? make_desc(s0 + kPartBytes, BK * 128, 1024) : make_desc(s0 + kPartBytes, 16, 1024);
+            const uint32_t b0 = s0 + PL * kPartBytes;
+            const uint64_t b_desc0 = B_MN ? make_desc(b0, BK * 128, 1024) : make_desc(b0, 16, 1024);
             constexpr uint32_t A_KSTEP = (A_MN ? UMMA_K * 128 : UMMA_K * 2) >> 4;
             constexpr uint32_t B_KSTEP = (B_MN ? UMMA_K * 128 : UMMA_K * 2) >> 4;
-            constexpr uint32_t STAGE_STEP = kStageBytes >> 4;
+            constexpr uint32_t STAGE_STEP = STAGE >> 4;
             uint32_t s = 0, ph = 0, soff = 0, tl = 0;
             bool ok = true;
             for (int tile = cluster_id; tile < num_tiles && ok; tile += nclusters)
@@ -282,19 +286,44 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
                 ++tl;
                 if (!mbar_wait(tempty + buf, aph ^ 1, p.err)) { ok = false; break; }
                 tc_fence_after();
-                const uint32_t d_tmem = tmem_base + buf * BN;
-                const MuonTile t = decode_tile<SYM>(p, tile);
-                const uint64_t b_desc = SYM && !SPLIT && t.m0 == t.n0 ? a_desc0 : b_desc0;
-                const int steps = TERMS * min(seg, kblocks - first);
-                for (int q = 0; q < steps; ++q) {
-                    if (!mbar_wait(full + s, ph, p.err)) { ok = false; break; }
-                    tc_fence_after();
-                    const uint64_t ad = a_desc0 + soff, bd = b_desc + soff;
+                const uint32_t d_tmem = tmem_base + buf * NT;
+                const MuonTile t = decode_tile<SYM, NT>(p, tile);
+                const uint64_t b_desc = SYM && !SPLIT && NT == kTile && t.m0 == t.n0 ? a_desc0 : b_desc0;
+                const int steps = min(seg, kblocks - first);
+                // one part of A times one of B, of the k-block in the stage at `off`
+                auto product = [&](uint32_t off, int term, bool add) {      // term: lo hi, hi lo, hi hi
+                    const uint64_t ad = a_desc0 + off + (term == 0 ? kPartBytes >> 4 : 0);
+                    const uint64_t bd = b_desc + off + (term == 1 ? B_BYTES >> 4 : 0);
 #pragma unroll
                     for (int kk = 0; kk < BK / UMMA_K; ++kk)
-                        mma_pair(d_tmem, ad + kk * A_KSTEP, bd + kk * B_KSTEP, idesc, (q > 0 || kk > 0) ? 1u : 0u);
-                    commit_pair_both(empty + s);
-                    if (++s == kStages) { s = 0; ph ^= 1; soff = 0; } else { soff += STAGE_STEP; }
+                        mma_pair(d_tmem, ad + kk * A_KSTEP, bd + kk * B_KSTEP, idesc, add || kk > 0 ? 1u : 0u);
+                };
+                auto forward = [&]() {
+                    if (++s == STAGES) { s = 0; ph ^= 1; soff = 0; } else { soff += STAGE_STEP; }
+                };
+                if constexpr (SPLIT) {
+                    const uint32_t s0 = s, soff0 = soff;
+                    for (int q = 0; q < steps; ++q) {
+                        if (!mbar_wait(full + s, ph, p.err)) { ok = false; break; }
+                        tc_fence_after();
+                        product(soff, 0, q > 0);
+                        product(soff, 1, true);
+                        forward();
+                    }
+                    uint32_t back = s0, boff = soff0;
+                    for (int q = 0; q < steps && ok; ++q) {
+                        product(boff, 2, true);
+                        commit_pair_both(empty + back);
+                        if (++back == STAGES) { back = 0; boff = 0; } else { boff += STAGE_STEP; }
+                    }
+                } else {
+                    for (int q = 0; q < steps; ++q) {
+                        if (!mbar_wait(full + s, ph, p.err)) { ok = false; break; }
+                        tc_fence_after();
+                        product(soff, 2, q > 0);
+                        commit_pair_both(empty + s);
+                        forward();
+                    }
                 }
                 if (!ok) break;
                 commit_pair_both(tfull + buf);
@@ -310,11 +339,11 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
         const uint32_t tempty_leader[2] = {map_to_rank(smem_u32(tempty), 0), map_to_rank(smem_u32(tempty + 1), 0)};
         uint32_t tl = 0;
         for (int tile = cluster_id; tile < num_tiles; tile += nclusters) {
-            const MuonTile t = decode_tile<SYM>(p, tile);
+            const MuonTile t = decode_tile<SYM, NT>(p, tile);
             const int y = t.m0 + (int)rank * kHalf + quarter * 32;    // the warp's first row
-            const int x0 = t.n0 + half * (BN / 2);                    // its first column
-            const bool turn = SYM && t.m0 != t.n0;
-            const uint32_t toff = ((uint32_t)(quarter * 32) << 16) + half * (BN / 2);
+            const int x0 = t.n0 + half * (NT / 2);                    // its first column
+            const bool turn = SYM && t.n0 < t.m0;
+            const uint32_t toff = ((uint32_t)(quarter * 32) << 16) + half * (NT / 2);
             bool ok = true;
             // The side input of a box, fetched a box ahead, in whole sectors (a row of it to a lane took a read of
             // 32 lines for every 16 bytes: stepping weights in the last product then took longer than apart from it).
@@ -341,7 +370,7 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
                 if (SIDED) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) own[i] = ahead[i];
-                    if (c + 32 < BN / 2) fetch(p.side, p.ld, c + 32, 0, ahead);
+                    if (c + 32 < NT / 2) fetch(p.side, p.ld, c + 32, 0, ahead);
                     st.to_rows(lane, own);
                     auto add = [&](bool first) {
                         const __half2* h = reinterpret_cast<const __half2*>(own);
@@ -390,7 +419,7 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
                     if (p.weights) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) own[i] = weights[i];
-                        if (c + 32 < BN / 2) fetch(p.weights, p.N, c + 32, 0, weights);
+                        if (c + 32 < NT / 2) fetch(p.weights, p.N, c + 32, 0, weights);
                         st.to_rows(lane, own);
                         float w[32];
 #pragma unroll
@@ -435,16 +464,16 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
                 ++tl;
             };
             if constexpr (SPLIT) {
-                uint32_t sum[BN / 64][32];
+                uint32_t sum[NT / 64][32];
 #pragma unroll
-                for (int c = 0; c < BN / 64; ++c)
+                for (int c = 0; c < NT / 64; ++c)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) sum[c][i] = 0;
                 for (int first = 0; first < kblocks; first += seg) {
                     if (!wait_full()) { ok = false; break; }
-                    const uint32_t taddr = tmem_base + toff + (tl & 1) * BN;
+                    const uint32_t taddr = tmem_base + toff + (tl & 1) * NT;
 #pragma unroll
-                    for (int c = 0; c < BN / 64; ++c) {
+                    for (int c = 0; c < NT / 64; ++c) {
                         uint32_t acc[32];
                         tmem_ld32(taddr + 32 * c, acc);
                         tmem_ld_wait_regs(acc);
@@ -456,11 +485,11 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
                 }
                 if (!ok) break;
 #pragma unroll
-                for (int c = 0; c < BN / 64; ++c) box(32 * c, sum[c], [] {});
+                for (int c = 0; c < NT / 64; ++c) box(32 * c, sum[c], [] {});
             } else {
                 if (!wait_full()) break;
-                const uint32_t taddr = tmem_base + toff + (tl & 1) * BN;
-                for (int c = 0; c < BN / 2; c += 32) {
+                const uint32_t taddr = tmem_base + toff + (tl & 1) * NT;
+                for (int c = 0; c < NT / 2; c += 32) {
                     if (x0 + c >= p.N || y >= p.M) break;
                     uint32_t acc[32];
                     tmem_ld32(taddr + c, acc);
@@ -485,7 +514,7 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
     }
 }
 
-constexpr size_t kGemmSmem = 1024 + (size_t)kStages * kStageBytes + kEpiWarps * 2 * STG_BYTES + 32 * sizeof(uint64_t);
+constexpr size_t kGemmSmem = 1024 + (size_t)kRingBytes + kEpiWarps * 2 * STG_BYTES + 32 * sizeof(uint64_t);
 static_assert(kGemmSmem <= 227 * 1024, "shared memory per CTA");
 
 // ---------------------------------------------------------------- before the products
@@ -1264,31 +1293,54 @@ struct Operand {
     int rows, cols, ld;
 };
 
-// K-major operands come in boxes of 64 k x 128 rows, MN-major ones of 64 columns x 64 k.
-template <int OP, bool A_MN, bool B_MN>
-cudaError_t launch_gemm(MuonGemm p, int planes, const Operand& a, const Operand& b, const Operand& o, cudaStream_t s,
-                        int out = kParts) {
-    constexpr bool SYM = OP != kApply;
-    p.m_tiles = ceil_div(p.M, kTile);
-    p.n_tiles = ceil_div(p.N, kTile);
-    p.tiles = SYM ? p.m_tiles * (p.m_tiles + 1) / 2 : p.m_tiles * p.n_tiles;
-    p.err = device_error_word();
+// K-major operands come in boxes of 64 k x 128 rows (B: half a tile's columns), MN-major ones of 64 columns x 64 k.
+template <int OP, bool A_MN, bool B_MN, int NT>
+cudaError_t launch_gemm_as(MuonGemm p, int planes, const Operand& a, const Operand& b, const Operand& o, int out,
+                           cudaStream_t s) {
     const uint64_t outer = (uint64_t)planes * p.count;
     CUtensorMap ta, tb, to;
     if (!map_3d(&ta, a.base, a.cols, a.rows, outer, a.ld, 64, A_MN ? BK : kHalf, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !map_3d(&tb, b.base, b.cols, b.rows, outer, b.ld, 64, B_MN ? BK : kHalf, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !map_3d(&tb, b.base, b.cols, b.rows, outer, b.ld, 64, B_MN ? BK : NT / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !map_3d(&to, o.base, o.cols, o.rows, outer, o.ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B,
                 out == kResult ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16))
         return cudaErrorInvalidValue;
-    auto kern = planes == 2 ? muon_gemm_kernel<OP, A_MN, B_MN, true, kParts> : muon_gemm_kernel<OP, A_MN, B_MN, false, kParts>;
+    auto kern = planes == 2 ? muon_gemm_kernel<OP, A_MN, B_MN, true, kParts, NT>
+                            : muon_gemm_kernel<OP, A_MN, B_MN, false, kParts, NT>;
     if constexpr (OP == kApply)
-        if (out == kResult) kern = muon_gemm_kernel<OP, A_MN, B_MN, false, kResult>;
+        if (out == kResult) kern = muon_gemm_kernel<OP, A_MN, B_MN, false, kResult, NT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem);
     if (e != cudaSuccess) return e;
     const int clusters = (int)std::min<int64_t>((int64_t)p.count * p.tiles, num_sms() / 2);
     e = launch_pdl(kern, dim3(2 * clusters), dim3(kGemmThreads), kGemmSmem, s, p, ta, tb, to);
     count_launch();
     return e;
+}
+
+// Tiles of a matrix, nt columns wide.
+int tiles_of(const MuonGemm& p, bool sym, int nt) {
+    const int m = ceil_div(p.M, kTile), n = ceil_div(p.N, nt);
+    return sym ? kTile / nt * (m * (m - 1) / 2) + n : m * n;
+}
+
+// Tiles are as narrow as they may be (256, 128 or 64 columns; 128 where B is MN-major, which comes in boxes of 64)
+// without a further round of tiles over the pairs: a product of few tiles waits for its longest one (polynomial of
+// 1024 x 1024 in two parts: 34.7 us, 26.5 and 22.4), but a tile of half the columns takes 0.6 to 0.85 of the time
+// (4 x 2048 x 1024, two rounds for one: gram 42 us and 67, polynomial 37 and 45).
+template <int OP, bool A_MN, bool B_MN>
+cudaError_t launch_gemm(MuonGemm p, int planes, const Operand& a, const Operand& b, const Operand& o, cudaStream_t s,
+                        int out = kParts) {
+    constexpr bool SYM = OP != kApply;
+    constexpr int LEAST = B_MN ? 128 : 64;
+    auto rounds = [&](int w) { return ((int64_t)p.count * tiles_of(p, SYM, w) + num_sms() / 2 - 1) / (num_sms() / 2); };
+    int nt = kTile;
+    while (nt > LEAST && rounds(nt / 2) <= rounds(nt)) nt /= 2;
+    p.n_tiles = ceil_div(p.N, nt);
+    p.tiles = tiles_of(p, SYM, nt);
+    p.err = device_error_word();
+    if (nt == 256) return launch_gemm_as<OP, A_MN, B_MN, 256>(p, planes, a, b, o, out, s);
+    if (nt == 128) return launch_gemm_as<OP, A_MN, B_MN, 128>(p, planes, a, b, o, out, s);
+    if constexpr (LEAST == 64) return launch_gemm_as<OP, A_MN, B_MN, 64>(p, planes, a, b, o, out, s);
+    return cudaErrorInvalidValue;
 }
 
 template <typename G, bool MOMENTUM>
