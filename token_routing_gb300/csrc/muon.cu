@@ -174,7 +174,7 @@ enum Out : int { kParts = 0, kResult = 1 };
 // and hi lo before hi hi (what is cut off is measured by what the sum holds: one k-block's three products after
 // the other's, 4.5e-6), and the epilogue warps add the segments up in registers, rounding to nearest, while the
 // other buffer fills. A stage has all four parts of its k-block (loaded for each product anew, 6 in place of 4:
-// 1024 x 4096 682 us and 608 with tiles alike).
+// 1024 x 4096 in tiles of 64 columns 701 us, so 608).
 template <int OP, bool A_MN, bool B_MN, bool SPLIT, int OUT, int NT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
