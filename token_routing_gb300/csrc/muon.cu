@@ -173,7 +173,7 @@ enum Out : int { kParts = 0, kResult = 1 };
 // result, where segments of two left 3.7e-6; plain fp32 products 2.2e-6). Each segment has a TMEM buffer to itself, lo hi
 // and hi lo before hi hi (what is cut off is measured by what the sum holds: one k-block's three products after
 // the other's, 4.5e-6), and the epilogue warps add the segments up in registers, rounding to nearest, while the
-// other buffer fills. A stage has all four parts of its k-block (loaded for each product anew, 6 in place of 4:
+// next buffer fills. A stage has all four parts of its k-block (loaded for each product anew, 6 in place of 4:
 // 1024 x 4096 in tiles of 64 columns 701 us, so 608).
 template <int OP, bool A_MN, bool B_MN, bool SPLIT, int OUT, int NT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
@@ -181,14 +181,15 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
                  const __grid_constant__ CUtensorMap tmO) {
     constexpr bool SYM = OP != kApply, SIDED = OP != kGram, TALL = OP == kApply && !B_MN;
     constexpr int PL = SPLIT ? 2 : 1, B_BYTES = NT / 2 * BK * 2, STAGE = stage_bytes(NT, SPLIT), STAGES = kRingBytes / STAGE;
+    constexpr int BUFS = NT == kTile ? 2 : 4;      // sums in TMEM (1024 x 1024 in two parts: 295 us with 2, 263 with 4)
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* stg_smem = smem + kRingBytes;
     uint64_t* full = reinterpret_cast<uint64_t*>(stg_smem + kEpiWarps * 2 * STG_BYTES);
     uint64_t* empty = full + STAGES;
     uint64_t* tfull = empty + STAGES;
-    uint64_t* tempty = tfull + 2;
-    uint64_t* drain = tempty + 2;
+    uint64_t* tempty = tfull + BUFS;
+    uint64_t* drain = tempty + BUFS;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* s_fail = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -199,7 +200,7 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) { mbar_init(full + s, 1); mbar_init(empty + s, 1); }
-        for (int b = 0; b < 2; ++b) { mbar_init(tfull + b, 1); mbar_init(tempty + b, 2 * 32 * kEpiWarps); }
+        for (int b = 0; b < BUFS; ++b) { mbar_init(tfull + b, 1); mbar_init(tempty + b, 2 * 32 * kEpiWarps); }
         mbar_init(drain, 1);
         *s_fail = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -281,8 +282,8 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
             bool ok = true;
             for (int tile = cluster_id; tile < num_tiles && ok; tile += nclusters)
             for (int first = 0; first < kblocks && ok; first += seg) {
-                const int buf = tl & 1;
-                const uint32_t aph = (tl >> 1) & 1;
+                const int buf = tl % BUFS;
+                const uint32_t aph = (tl / BUFS) & 1;
                 ++tl;
                 if (!mbar_wait(tempty + buf, aph ^ 1, p.err)) { ok = false; break; }
                 tc_fence_after();
@@ -302,7 +303,7 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
                     if (++s == STAGES) { s = 0; ph ^= 1; soff = 0; } else { soff += STAGE_STEP; }
                 };
                 if constexpr (SPLIT) {
-                    const uint32_t s0 = s, soff0 = soff;
+                    uint32_t back = s, boff = soff;       // the segment's first stage
                     for (int q = 0; q < steps; ++q) {
                         if (!mbar_wait(full + s, ph, p.err)) { ok = false; break; }
                         tc_fence_after();
@@ -310,7 +311,6 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
                         product(soff, 1, true);
                         forward();
                     }
-                    uint32_t back = s0, boff = soff0;
                     for (int q = 0; q < steps && ok; ++q) {
                         product(boff, 2, true);
                         commit_pair_both(empty + back);
@@ -336,7 +336,7 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
         const int quarter = warp & 3, half = (warp - 2) >> 2;
         const float lr = OUT == kResult && p.lr_dev ? __ldg(p.lr_dev) : p.lr, lose = lr * p.decay, move = lr * p.scale;
         Staging st{smem_u32(stg_smem + (warp - 2) * 2 * STG_BYTES), 0};
-        const uint32_t tempty_leader[2] = {map_to_rank(smem_u32(tempty), 0), map_to_rank(smem_u32(tempty + 1), 0)};
+        const uint32_t tempty_leader = map_to_rank(smem_u32(tempty), 0);
         uint32_t tl = 0;
         for (int tile = cluster_id; tile < num_tiles; tile += nclusters) {
             const MuonTile t = decode_tile<SYM, NT>(p, tile);
@@ -453,14 +453,14 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
                 }
             };
             auto wait_full = [&]() {
-                const bool got = mbar_wait(tfull + (tl & 1), (tl >> 1) & 1, p.err);
+                const bool got = mbar_wait(tfull + tl % BUFS, (tl / BUFS) & 1, p.err);
                 tc_fence_after();
                 return got;
             };
             auto free_buffer = [&]() {
                 tc_fence_before();
-                if (leader) mbar_arrive(tempty + (tl & 1));
-                else mbar_arrive_cluster(tempty_leader[tl & 1]);
+                if (leader) mbar_arrive(tempty + tl % BUFS);
+                else mbar_arrive_cluster(tempty_leader + tl % BUFS * 8);
                 ++tl;
             };
             if constexpr (SPLIT) {
@@ -471,7 +471,7 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
                     for (int i = 0; i < 32; ++i) sum[c][i] = 0;
                 for (int first = 0; first < kblocks; first += seg) {
                     if (!wait_full()) { ok = false; break; }
-                    const uint32_t taddr = tmem_base + toff + (tl & 1) * NT;
+                    const uint32_t taddr = tmem_base + toff + tl % BUFS * NT;
 #pragma unroll
                     for (int c = 0; c < NT / 64; ++c) {
                         uint32_t acc[32];
@@ -488,7 +488,7 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
                 for (int c = 0; c < NT / 64; ++c) box(32 * c, sum[c], [] {});
             } else {
                 if (!wait_full()) break;
-                const uint32_t taddr = tmem_base + toff + (tl & 1) * NT;
+                const uint32_t taddr = tmem_base + toff + tl % BUFS * NT;
                 for (int c = 0; c < NT / 2; c += 32) {
                     if (x0 + c >= p.N || y >= p.M) break;
                     uint32_t acc[32];
@@ -1324,7 +1324,7 @@ int tiles_of(const MuonGemm& p, bool sym, int nt) {
 
 // Tiles are as narrow as they may be (256, 128 or 64 columns; 128 where B is MN-major, which comes in boxes of 64)
 // without a further round of tiles over the pairs: a product of few tiles waits for its longest one (polynomial of
-// 1024 x 1024 in two parts: 34.7 us, 26.5 and 22.4), but a tile of half the columns takes 0.6 to 0.85 of the time
+// 1024 x 1024 in two parts: 34.7 us, 26.5 and 20.4), but a tile of half the columns takes 0.6 to 0.85 of the time
 // (4 x 2048 x 1024, two rounds for one: gram 42 us and 67, polynomial 37 and 45).
 template <int OP, bool A_MN, bool B_MN>
 cudaError_t launch_gemm(MuonGemm p, int planes, const Operand& a, const Operand& b, const Operand& o, cudaStream_t s,
