@@ -231,3 +231,14 @@ def test_graph_and_two_streams(shape, moe_lib, cuda_device):
     for opt, (p, m) in zip((a, b), want):
         assert torch.equal(opt.tensors[0]["p"], p) and torch.equal(opt.tensors[0]["m"], m)
     moe.get_error()
+
+
+@pytest.mark.parametrize("shape", [(1, 300, 704), (3, 704, 336), (30, 520, 304), (40, 300, 600), (40, 600, 304)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_tiles_of_every_width(shape, dtype, moe_lib, cuda_device):
+    """Few matrices, whose tiles are narrow, and many, whose tiles are wide; four of them are looked at."""
+    g = make(*shape, dtype).cuda()
+    _, _, o = orthogonalize(moe_lib, g, dtype)
+    pick = sorted({0, shape[0] // 2, max(0, shape[0] - 2), shape[0] - 1})
+    compare(f64(o)[pick], f64(g)[pick], dtype, dtype)
+    assert torch.isfinite(o.float()).all()
