@@ -228,7 +228,7 @@ __device__ __forceinline__ float pair_sum(const uint64_t (&p)[N]) {
 //
 // The forward pass has a ring to each row's group of threads, which wait for no other row; the gradient one to
 // the block, whose rows are one copy. Both ways measured: forward 16384 x 1024 bf16 with a residual 25.1 us and
-// 28, gradient 32768 x 2048 98 us and 89 (DRAM is read in pieces of 4 KB and 16).
+// 28, gradient 32768 x 2048 98 us and 89, before its sums joined at once (DRAM is read in pieces of 4 KB and 16).
 constexpr int kRingThreads = 512;         // threads of a block; one block to an SM
 constexpr int kMaxStages = 6;
 constexpr int kRingBytes = 180 * 1024;
@@ -485,7 +485,7 @@ struct NormGradArgs {
 // partial sums are what the joining kernel reads.
 //
 // Bound by memory, with registers full of sums. Rows come through one ring to the block, as in Ring, but written
-// out: through that struct this kernel takes 95 us where it takes 89 (32768 x 2048 bf16).
+// out: through that struct this kernel took 95 us where it took 89 (32768 x 2048 bf16).
 template <typename T, int VE, int NE, bool FULL>
 __global__ void __launch_bounds__(kRingThreads, 1) norm_grad_kernel(const NormGradArgs a) {
     using P = Part<T, VE, NE, FULL>;
@@ -614,32 +614,35 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_grad_kernel(const NormGr
     }
     if (!ok && threadIdx.x == 0)      // no copy may be in flight when the block leaves
         for (int i = 0; i < a.stages; ++i) tc::mbar_wait(s_full + i, phase, a.err);
-    float* s_part = reinterpret_cast<float*>(s_ring);      // [d]: the ring has been read
-    __syncthreads();
     if (!a.part) return;
-    // the block's rows one after another, dgain then dbias
+    // the block's rows join in their order, through the ring's memory [2, rows, d] (one after another, with a
+    // wait for each: 32768 x 2048 bf16 89.1 us, so 84.8; 2047 x 1023 fp32 13.7 us, so 11.8)
+    float* s_part = reinterpret_cast<float*>(s_ring);
+    __syncthreads();
+#pragma unroll
     for (int which = 0; which < 2; ++which) {
-        float* out = a.part + ((size_t)which * gridDim.x + blockIdx.x) * a.d;
-        for (int q = 0; q < rows; ++q) {
-            if (own == q) {
+        float* out = rows > 1 ? s_part + (which * rows + own) * a.d : a.part + ((size_t)which * gridDim.x + blockIdx.x) * a.d;
 #pragma unroll
-                for (int i = 0; i < NP; ++i) {
-                    float f[2];
-                    upk2(which ? db[i] : dg[i], f[0], f[1]);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int e = 2 * i + k, at = lane + e / VE * a.tpr, c = at * VE + e % VE;
-                        if (!FULL && at >= nvec) continue;
-                        if (rows > 1) {
-                            if (q > 0) f[k] += s_part[c];
-                            s_part[c] = f[k];
-                        }
-                        if (q + 1 == rows) out[c] = f[k];
-                    }
-                }
+        for (int i = 0; i < NP; ++i) {
+            float f[2];
+            upk2(which ? db[i] : dg[i], f[0], f[1]);
+            const int at = lane + 2 * i / VE * a.tpr, c = at * VE + 2 * i % VE;
+            if constexpr (VE > 1) {
+                if (FULL || at < nvec) *reinterpret_cast<float2*>(out + c) = make_float2(f[0], f[1]);
+            } else {
+                if (FULL || at < nvec) out[c] = f[0];
+                if (FULL || at + a.tpr < nvec) out[c + a.tpr] = f[1];
             }
-            if (rows > 1) __syncthreads();
         }
+    }
+    if (rows == 1) return;
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * a.d; i += kRingThreads) {
+        const int which = i >= a.d, c = i - which * a.d;
+        const float* in = s_part + which * rows * a.d + c;
+        float f = in[0];
+        for (int q = 1; q < rows; ++q) f += in[q * a.d];
+        a.part[((size_t)which * gridDim.x + blockIdx.x) * a.d + c] = f;
     }
 }
 
@@ -836,7 +839,8 @@ cudaError_t launch_grad_ne(const moe_norm_config_t& c, const NormGradArgs& a, co
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
     if (e != cudaSuccess) return e;
     const size_t ring = (size_t)a.stages * (a.dtotal && a.dx ? 3 : 2) * a.array_bytes;
-    return launch_pdl(kern, dim3(grad_blocks(c, sh)), dim3(kRingThreads), std::max(ring, (size_t)c.d * sizeof(float)), s, a);
+    const size_t sums = 2 * (size_t)(kRingThreads / sh.tpr) * c.d * sizeof(float);
+    return launch_pdl(kern, dim3(grad_blocks(c, sh)), dim3(kRingThreads), std::max(ring, sums), s, a);
 }
 
 template <typename T, int VE>
