@@ -772,20 +772,27 @@ bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t
 
 // How a row is shared out: vector, threads to a row and bytes of it to a thread (16, 32 or 64; 0: too long
 // for registers). 32 bytes to a thread, and the next row's 32 in flight, keep the registers of a block of 512
-// threads; below 256 elements a warp takes 16 or 32 bytes a lane, and beyond 512 threads 64. Measured with 16, 32
-// and 64 bytes to a thread: forward, 16384 rows of 1024 bf16 with a residual, 38, 25 and 41 us; the gradient of
-// 32768 rows of 2048 bf16 123, 89 and 267 us; of 2047 rows of 1023 fp32 13.0, 13.7 and 21.2 us.
+// threads; below 256 elements a warp takes 16 or 32 bytes a lane, and beyond 512 threads 64 of fp32. Measured with
+// 16, 32 and 64 bytes to a thread: forward, 16384 rows of 1024 bf16 with a residual, 38, 25 and 41 us; the gradient
+// of 32768 rows of 2048 bf16 123, 89 and 267 us; of 2047 rows of 1023 fp32 13.0, 13.7 and 21.2 us. 64 bytes of bf16
+// are 32 elements, which spill: 3198 rows of 8195 forward 152 us and by the kernels for long rows 89, gradient 304
+// and 133, 1600 rows of 16384 64 and 58, 95 and 97.
+// The forward pass takes rows of single elements (odd ones) 8 to a thread at most: 16 spill, too (25625 rows of
+// 1023 bf16 101 us, so 72; 3200 rows of 8191 fp32 121, long rows 93).
 struct Shape {
     int ve, tpr, bytes;
 };
-Shape norm_shape(const moe_norm_config_t& c) {
+Shape norm_shape(const moe_norm_config_t& c, bool grad) {
     Shape s;
     const int es = c.dtype == MOE_BF16 ? 2 : 4;
     const int64_t row = (int64_t)c.d * es;
     s.ve = row_vec(c.d, es);
+    const bool few = s.ve == 1 && !grad;
+    const int each = few ? 8 * es : 32, most = es == 2 || few ? each : 64;
     s.tpr = 32;
-    while (s.tpr < kMaxRow && s.tpr * 32 < row) s.tpr *= 2;
+    while (s.tpr < kMaxRow && s.tpr * each < row) s.tpr *= 2;
     s.bytes = row <= s.tpr * 16 ? 16 : row <= s.tpr * 32 ? 32 : row <= s.tpr * 64 ? 64 : 0;
+    if (s.bytes > most) s.bytes = 0;
     return s;
 }
 
@@ -817,20 +824,24 @@ template <typename T, int VE>
 cudaError_t launch_norm(const moe_norm_config_t& c, NormArgs a, const Shape& sh, cudaStream_t s) {
     constexpr int ES = (int)sizeof(T);
     a.tpr = sh.tpr;
-    cudaError_t e;
+    cudaError_t e = cudaErrorInvalidValue;
     constexpr bool WIDE = VE * ES == 16;      // (rows of other vectors are never taken as whole)
     const bool full = WIDE && (int64_t)c.d * ES == (int64_t)sh.tpr * sh.bytes;
     if (sh.bytes == 0) e = launch_pdl(norm_long_kernel<T, VE>, dim3(std::min(c.T, num_sms() * 2)), dim3(kLong), 0, s, a);
     else if (sh.bytes == 16) e = full ? launch_norm_ne<T, VE, 16 / ES, WIDE>(c, a, sh, s) : launch_norm_ne<T, VE, 16 / ES, false>(c, a, sh, s);
-    else if (sh.bytes == 32) e = full ? launch_norm_ne<T, VE, 32 / ES, WIDE>(c, a, sh, s) : launch_norm_ne<T, VE, 32 / ES, false>(c, a, sh, s);
-    else e = full ? launch_norm_ne<T, VE, 64 / ES, WIDE>(c, a, sh, s) : launch_norm_ne<T, VE, 64 / ES, false>(c, a, sh, s);
+    if constexpr (VE > 1 || ES == 4)
+        if (sh.bytes == 32) e = full ? launch_norm_ne<T, VE, 32 / ES, WIDE>(c, a, sh, s) : launch_norm_ne<T, VE, 32 / ES, false>(c, a, sh, s);
+    if constexpr (VE > 1 && ES == 4)
+        if (sh.bytes == 64) e = full ? launch_norm_ne<T, VE, 64 / ES, WIDE>(c, a, sh, s) : launch_norm_ne<T, VE, 64 / ES, false>(c, a, sh, s);
     count_launch();
     return e;
 }
 
-// Blocks whose partial sums norm_join_kernel adds up.
+// Blocks whose partial sums norm_join_kernel adds up; for long rows slices of the rows, four blocks to an SM in all
+// (16 slices: 2133 rows of 12288 fp32 172 us, so 137).
 int grad_blocks(const moe_norm_config_t& c, const Shape& sh) {
-    return std::max(1, sh.bytes == 0 ? std::min(c.T, 16) : std::min(ceil_div(c.T, kRingThreads / sh.tpr), num_sms()));
+    const int slices = std::max(1, num_sms() * 4 / ceil_div(c.d / sh.ve, 256));
+    return std::max(1, sh.bytes == 0 ? std::min(c.T, slices) : std::min(ceil_div(c.T, kRingThreads / sh.tpr), num_sms()));
 }
 
 template <typename T, int VE, int NE, bool FULL>
@@ -869,7 +880,8 @@ cudaError_t launch_norm_grad(const moe_norm_config_t& c, NormGradArgs a, const S
     const bool full = WIDE && (int64_t)c.d * ES == (int64_t)sh.tpr * sh.bytes;
     if (sh.bytes == 16) e = full ? launch_grad_ne<T, VE, 16 / ES, WIDE>(c, a, sh, s) : launch_grad_ne<T, VE, 16 / ES, false>(c, a, sh, s);
     else if (sh.bytes == 32) e = full ? launch_grad_ne<T, VE, 32 / ES, WIDE>(c, a, sh, s) : launch_grad_ne<T, VE, 32 / ES, false>(c, a, sh, s);
-    else e = full ? launch_grad_ne<T, VE, 64 / ES, WIDE>(c, a, sh, s) : launch_grad_ne<T, VE, 64 / ES, false>(c, a, sh, s);
+    if constexpr (ES == 4)
+        if (sh.bytes == 64) e = full ? launch_grad_ne<T, VE, 64 / ES, WIDE>(c, a, sh, s) : launch_grad_ne<T, VE, 64 / ES, false>(c, a, sh, s);
     count_launch();
     return e;
 }
@@ -898,7 +910,7 @@ extern "C" MOE_API moe_status_t moe_layer_norm(const moe_norm_config_t* cfg, con
     if (misaligned(mean, 4) || misaligned(rstd, 4)) return MOE_ERR_INVALID_ARG;
     if (total && total == y) return MOE_ERR_INVALID_ARG;
     if (c.T == 0) return MOE_OK;
-    const Shape sh = norm_shape(c);
+    const Shape sh = norm_shape(c, false);
     const NormArgs a{x, residual, gain, bias, total, y, mean, rstd, c.T, c.d, sh.tpr, c.param_dtype == MOE_F32, c.eps,
                      1.0f / (float)c.d};
     cudaStream_t s = (cudaStream_t)stream;
@@ -909,7 +921,7 @@ extern "C" MOE_API moe_status_t moe_layer_norm(const moe_norm_config_t* cfg, con
 
 extern "C" MOE_API size_t moe_norm_workspace_bytes(const moe_norm_config_t* cfg) {
     if (check_norm(cfg) != MOE_OK) return 0;
-    return align_up(2 * (size_t)grad_blocks(*cfg, norm_shape(*cfg)) * cfg->d * sizeof(float), 256);
+    return align_up(2 * (size_t)grad_blocks(*cfg, norm_shape(*cfg, true)) * cfg->d * sizeof(float), 256);
 }
 
 extern "C" MOE_API moe_status_t moe_layer_norm_backward(const moe_norm_config_t* cfg, const void* dy, const void* x,
@@ -931,7 +943,7 @@ extern "C" MOE_API moe_status_t moe_layer_norm_backward(const moe_norm_config_t*
             if (p && launch_fill(p, (long long)c.d, 0.f, s) != cudaSuccess) return MOE_ERR_CUDA;
         return MOE_OK;
     }
-    const Shape sh = norm_shape(c);
+    const Shape sh = norm_shape(c, true);
     const NormGradArgs a{dy, x, gain, mean, rstd, dtotal, dx, sums ? static_cast<float*>(ws) : nullptr, c.T, c.d, sh.tpr,
                          c.param_dtype == MOE_F32, 1.0f / (float)c.d, 0, 0, nullptr};
     cudaError_t e = c.dtype == MOE_BF16 ? MOE_NORM_VE(__nv_bfloat16, launch_norm_grad, c, a, sh, s)
