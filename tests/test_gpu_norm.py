@@ -50,10 +50,17 @@ def check_forward(moe, T, d, dtype, params, residual, eps=1e-5, plain=False, off
     dm = N * np.abs(s).mean(axis=1) + 2 * U * np.abs(rm)
     var = 1 / (rr * rr)                                   # eps and all: the smallest it can be off
     rv = N + 8 * U + dm * dm / var
+    # x + residual is rounded to fp32: element i by U |s_i|, and with it the mean by up to U mean|s|, so s_i - mean by
+    # own_i = U (|s_i| + mean|s|). The mean of the squares of e_i = s_i - mean changes by mean(2 e_i own_i + own_i^2), at
+    # most 2 sqrt(mean e^2) sqrt(mean own^2) + mean own^2 (Cauchy), relative to var >= mean e^2 by 2 q + q^2 with
+    # q = sqrt(mean own^2 / var).
+    own = U * (np.abs(s) + np.abs(s).mean(axis=1, keepdims=True)) if residual else np.zeros_like(s)
+    q = np.sqrt((own * own).mean(axis=1) / var)
+    rv = rv + 2 * q + q * q
     close(f64(mean), rm, dm)
     close(f64(rstd), rr, rr * (rv / 2 + 4 * U))
     h = np.abs(s - rm[:, None]) * rr[:, None]
-    tol = np.abs(gn) * (h * (rv[:, None] / 2 + 6 * U) + (rr * dm)[:, None]) + 2 * U * np.abs(bn) + HALF[dtype] * np.abs(ref)
+    tol = np.abs(gn) * (h * (rv[:, None] / 2 + 6 * U) + (rr * dm)[:, None] + rr[:, None] * own) + 2 * U * np.abs(bn) + HALF[dtype] * np.abs(ref)
     close(f64(y), ref, tol * 1.01 + 1e-30)
     if residual:
         close(f64(total), s, (HALF[dtype] + U) * np.abs(s))
@@ -270,3 +277,16 @@ def test_other_stream_and_graph(moe_lib, cuda_device):
     for a, b in zip(got, (y, total, mean, rstd, dx, dg, db)):
         assert torch.equal(a, b)
     moe.get_error()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [2, 8, 12, 33, 63, 64, 65, 96, 127, 128])
+def test_short_rows(d, dtype, moe_lib, cuda_device):
+    """Several rows to a warp: fewer rows than a warp takes, ragged ends, many copies of rows; in place."""
+    for T in (1, 3, 31, 1001, 40003):
+        check_forward(moe_lib, T, d, dtype, "f32", False)
+        c, x, r, gain, bias, y, total, _, _ = check_forward(moe_lib, T, d, dtype, "f32", True)
+        moe_lib.layer_norm(c, x, gain, bias, r, residual=r, total=x)
+        assert torch.equal(x, total) and torch.equal(r, y)
+    check_backward(moe_lib, 1001, d, dtype, "f32", True)
+    check_backward(moe_lib, 31, d, dtype, "f32", False)

@@ -172,13 +172,19 @@ int row_vec(int d, int es) {
     return v;
 }
 
-// Sums over the `tpr` threads of a row (32 or more, a power of two; a block holds whole rows, `own` is the
-// row's number in it). `red` (a value to each warp) is free again after the next sum on another buffer. The row's
+// Sums over the `tpr` threads of a row (a power of two; a block holds whole rows, `own` is the number of the row, or
+// of the warp whose rows are shorter, in it). `red` (a value to each warp) is free again after the next sum on another buffer. The row's
 // threads meet.
 __device__ __forceinline__ void row_sync(int tpr, int own) {
     asm volatile("bar.sync %0, %1;" ::"r"(own + 1), "r"(tpr) : "memory");
 }
+template <bool SHORT = false>
 __device__ __forceinline__ float row_sum(float v, int tpr, int own, float* red) {
+    if (SHORT) {                 // (tpr < 32)
+        for (int o = tpr >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        __syncwarp();
+        return v;
+    }
     v = warp_sum(v);
     if (tpr == 32) {
         __syncwarp();
@@ -192,7 +198,16 @@ __device__ __forceinline__ float row_sum(float v, int tpr, int own, float* red) 
     for (int i = 1; i < n; ++i) s += at[i];
     return s;
 }
+template <bool SHORT = false>
 __device__ __forceinline__ float2 row_sum2(float2 v, int tpr, int own, float2* red) {
+    if (SHORT) {                 // (tpr < 32)
+        for (int o = tpr >> 1; o > 0; o >>= 1) {
+            v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+            v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+        }
+        __syncwarp();
+        return v;
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
@@ -352,16 +367,18 @@ struct NormArgs {
 // A row to `tpr` threads, in registers between the reading and the writing: the mean, then the squares
 // of the differences, then the output; gain and bias stay in registers from row to row. Bound by memory.
 constexpr int kMaxRow = kRingThreads;      // threads to a row at most
-template <typename T, int VE, int NE, bool FULL, bool RES>
+template <typename T, int VE, int NE, bool FULL, bool RES, bool SHORT>
 __global__ void __launch_bounds__(kRingThreads, 1) norm_kernel(const NormArgs a, const RingArgs ra) {
     using P = Part<T, VE, NE, FULL>;
     constexpr int NP = NE / 2;
     __shared__ float s_red[2][kRingThreads / 32];
     __shared__ uint64_t s_full[kRingThreads / 32 * kMaxStages];
     extern __shared__ __align__(128) uint8_t s_ring[];
-    const int own = threadIdx.x / a.tpr, lane = threadIdx.x - own * a.tpr, nvec = a.d / VE;
+    // SHORT: a warp takes 32 / tpr rows at once, from one ring
+    const int unit = SHORT ? 32 : a.tpr, own = threadIdx.x / unit, in = threadIdx.x - own * unit, nvec = a.d / VE;
+    const int lane = SHORT ? in & (a.tpr - 1) : in, sub = SHORT ? in / a.tpr : 0, rows = SHORT ? 32 / a.tpr : 1;
     Ring<T> ring;
-    ring.init(ra, a.T, a.d, kRingThreads / a.tpr, own, lane == 0, s_ring, s_full);
+    ring.init(ra, a.T, a.d, kRingThreads / unit, own, in == 0, s_ring, s_full);
     pdl_wait();
     ring.start(ra, a.T, a.x, a.r, nullptr);
     uint64_t gain[NP], bias[NP];
@@ -370,33 +387,36 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_kernel(const NormArgs a,
     for (; ring.tile < ring.tiles; ring.next(ra)) {
         const uint8_t* at = ring.wait(ra);
         const int t0 = ring.tile * ra.per, t1 = min(t0 + ra.per, a.T);
-        for (int t = t0; t < t1; ++t, at += ring.row_bytes) {
+        at += sub * ring.row_bytes;
+        for (int first = t0; first < t1; first += rows, at += rows * ring.row_bytes) {
+            const int t = first + sub;
+            const bool live = !SHORT || t < t1;
             uint64_t v[NP];
             P part;
-            part.load(reinterpret_cast<const T*>(at), lane, a.tpr, nvec);
+            part.load(reinterpret_cast<const T*>(at), lane, a.tpr, nvec, live);
             part.pairs(v);
             if (RES) {
                 uint64_t w[NP];
-                part.load(reinterpret_cast<const T*>(at + ra.array_bytes), lane, a.tpr, nvec);
+                part.load(reinterpret_cast<const T*>(at + ra.array_bytes), lane, a.tpr, nvec, live);
                 part.pairs(w);
 #pragma unroll
                 for (int i = 0; i < NP; ++i) v[i] = add2(v[i], w[i]);
             }
-            const float mean = row_sum(pair_sum(v), a.tpr, own, s_red[0]) * a.inv_d;
-            if (t + 1 == t1) ring.refill(ra, a.T, a.x, a.r, nullptr);
-            if (RES) P::store(static_cast<T*>(a.total) + (int64_t)t * a.d, lane, a.tpr, nvec, v);
+            const float mean = row_sum<SHORT>(pair_sum(v), a.tpr, own, s_red[0]) * a.inv_d;
+            if (first + rows >= t1) ring.refill(ra, a.T, a.x, a.r, nullptr);
+            if (RES && live) P::store(static_cast<T*>(a.total) + (int64_t)t * a.d, lane, a.tpr, nvec, v);
             uint64_t sq[NP];
 #pragma unroll
             for (int i = 0; i < NP; ++i) v[i] = add2(v[i], splat2(-mean));
             P::cut(lane, a.tpr, nvec, v);
 #pragma unroll
             for (int i = 0; i < NP; ++i) sq[i] = mul2(v[i], v[i]);
-            const float var = row_sum(pair_sum(sq), a.tpr, own, s_red[1]) * a.inv_d;
+            const float var = row_sum<SHORT>(pair_sum(sq), a.tpr, own, s_red[1]) * a.inv_d;
             const float rstd = 1.0f / sqrtf(var + a.eps);
 #pragma unroll
             for (int i = 0; i < NP; ++i) v[i] = fma2(mul2(v[i], splat2(rstd)), gain[i], bias[i]);
-            P::store(static_cast<T*>(a.y) + (int64_t)t * a.d, lane, a.tpr, nvec, v);
-            if (lane == 0) {
+            if (live) P::store(static_cast<T*>(a.y) + (int64_t)t * a.d, lane, a.tpr, nvec, v);
+            if (lane == 0 && live) {
                 if (a.mean) a.mean[t] = mean;
                 if (a.rstd) a.rstd[t] = rstd;
             }
@@ -486,7 +506,7 @@ struct NormGradArgs {
 //
 // Bound by memory, with registers full of sums. Rows come through one ring to the block, as in Ring, but written
 // out: through that struct this kernel took 95 us where it took 89 (32768 x 2048 bf16).
-template <typename T, int VE, int NE, bool FULL>
+template <typename T, int VE, int NE, bool FULL, bool SHORT>
 __global__ void __launch_bounds__(kRingThreads, 1) norm_grad_kernel(const NormGradArgs a) {
     using P = Part<T, VE, NE, FULL>;
     constexpr int NP = NE / 2;
@@ -579,7 +599,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_grad_kernel(const NormGr
             float2 lo, hi;
             upk2(s1, lo.x, hi.x);
             upk2(s2, lo.y, hi.y);
-            const float2 all = row_sum2(make_float2(lo.x + hi.x, lo.y + hi.y), a.tpr, own, s_red[flip]);
+            const float2 all = row_sum2<SHORT>(make_float2(lo.x + hi.x, lo.y + hi.y), a.tpr, own, s_red[flip]);
             flip ^= 1;
             const uint64_t c1 = splat2(-all.x * a.inv_d), c2 = splat2(-all.y * a.inv_d);
 #pragma unroll
@@ -772,7 +792,8 @@ bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t
 
 // How a row is shared out: vector, threads to a row and bytes of it to a thread (16, 32 or 64; 0: too long
 // for registers). 32 bytes to a thread, and the next row's 32 in flight, keep the registers of a block of 512
-// threads; below 256 elements a warp takes 16 or 32 bytes a lane, and beyond 512 threads 64 of fp32. Measured with
+// threads; below 256 elements a warp takes 16 or 32 bytes a lane, rows of up to 256 bytes several to a warp (409600
+// rows of 64 bf16 101 us, so 38, the gradient 148 and 91), and beyond 512 threads 64 of fp32. Measured with
 // 16, 32 and 64 bytes to a thread: forward, 16384 rows of 1024 bf16 with a residual, 38, 25 and 41 us; the gradient
 // of 32768 rows of 2048 bf16 123, 89 and 267 us; of 2047 rows of 1023 fp32 13.0, 13.7 and 21.2 us. 64 bytes of bf16
 // are 32 elements, which spill: 3198 rows of 8195 forward 152 us and by the kernels for long rows 89, gradient 304
@@ -789,8 +810,12 @@ Shape norm_shape(const moe_norm_config_t& c, bool grad) {
     s.ve = row_vec(c.d, es);
     const bool few = s.ve == 1 && !grad;
     const int each = few ? 8 * es : 32, most = es == 2 || few ? each : 64;
-    s.tpr = 32;
-    while (s.tpr < kMaxRow && s.tpr * each < row) s.tpr *= 2;
+    s.tpr = row <= 256 ? 4 : 32;
+    if (s.tpr < 32) {
+        while (s.tpr * 16 < row) s.tpr *= 2;
+    } else {
+        while (s.tpr < kMaxRow && s.tpr * each < row) s.tpr *= 2;
+    }
     s.bytes = row <= s.tpr * 16 ? 16 : row <= s.tpr * 32 ? 32 : row <= s.tpr * 64 ? 64 : 0;
     if (s.bytes > most) s.bytes = 0;
     return s;
@@ -798,14 +823,14 @@ Shape norm_shape(const moe_norm_config_t& c, bool grad) {
 
 // The forward pass: adjacent rows to a copy, 2 KB of short ones, but not so many that groups of threads have none.
 int rows_per_copy(const moe_norm_config_t& c, const Shape& sh) {
-    const int row = c.d * (c.dtype == MOE_BF16 ? 2 : 4), groups = num_sms() * (kRingThreads / sh.tpr);
+    const int row = c.d * (c.dtype == MOE_BF16 ? 2 : 4), groups = num_sms() * (kRingThreads / std::max(32, sh.tpr));
     return std::max(1, std::min(2048 / row, c.T / groups));
 }
 
 template <typename T, int VE, int NE, bool FULL>
 cudaError_t launch_norm_ne(const moe_norm_config_t& c, const NormArgs& a, const Shape& sh, cudaStream_t s) {
     // as many stages as fit (2 at least)
-    const int groups = kRingThreads / sh.tpr;
+    const int groups = kRingThreads / std::max(32, sh.tpr);
     RingArgs r;
     r.arrays = a.r ? 2 : 1;
     r.per = rows_per_copy(c, sh);
@@ -814,7 +839,9 @@ cudaError_t launch_norm_ne(const moe_norm_config_t& c, const NormArgs& a, const 
     r.err = device_error_word();
     const size_t bytes = (size_t)groups * r.stages * r.arrays * r.array_bytes;
     const int blocks = std::min(ceil_div(ceil_div(c.T, r.per), groups), num_sms());
-    auto kern = a.r ? norm_kernel<T, VE, NE, FULL, true> : norm_kernel<T, VE, NE, FULL, false>;
+    auto kern = a.r ? norm_kernel<T, VE, NE, FULL, true, false> : norm_kernel<T, VE, NE, FULL, false, false>;
+    if constexpr (NE * sizeof(T) == 16)
+        if (sh.tpr < 32) kern = a.r ? norm_kernel<T, VE, NE, FULL, true, true> : norm_kernel<T, VE, NE, FULL, false, true>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(blocks), dim3(kRingThreads), bytes, s, a, r);
@@ -846,7 +873,9 @@ int grad_blocks(const moe_norm_config_t& c, const Shape& sh) {
 
 template <typename T, int VE, int NE, bool FULL>
 cudaError_t launch_grad_ne(const moe_norm_config_t& c, const NormGradArgs& a, const Shape& sh, cudaStream_t s) {
-    auto kern = norm_grad_kernel<T, VE, NE, FULL>;
+    auto kern = norm_grad_kernel<T, VE, NE, FULL, false>;
+    if constexpr (NE * sizeof(T) == 16)
+        if (sh.tpr < 32) kern = norm_grad_kernel<T, VE, NE, FULL, true>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
     if (e != cudaSuccess) return e;
     const size_t ring = (size_t)a.stages * (a.dtotal && a.dx ? 3 : 2) * a.array_bytes;
