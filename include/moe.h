@@ -531,8 +531,12 @@ MOE_API moe_status_t moe_layer_norm_backward(const moe_norm_config_t* cfg, const
  *                      x = x (1 - lr weight_decay) - lr scale orth(u)
  * m [count,rows,cols] fp32 (zeroed before the first step); x is the fp32 master if there is one (p is then
  * x rounded to its type), else p in dtype. precision: MOE_BF16: operands of the products hold 11 bits (fp16,
- * scaled), sums are fp32; orth(u) is off by 1e-3 of its size (root mean square), half of a rounding to bf16;
- * MOE_F32: operands hold two fp16 parts, 22 bits; off by 1e-6 to 4e-6, as fp32 products are. An element
+ * scaled), X between the steps 22, sums are fp32; MOE_F32: operands hold two fp16 parts, 22 bits.
+ * How far orth(u) is off, as a share of its size (root of the sums of squares; 5 steps, the usual
+ * coefficients): MOE_BF16: about 1e-3, half of a rounding to bf16, at any rank of u: 2e-3 at most of what was
+ * measured, 3e-3 of what was simulated (6e-3 with fewer than 16 rows or columns). MOE_F32: 1e-6 to 5e-6 at
+ * full rank. Where u's rank is lower, roundings in the directions that it lacks grow by `a` with every step, as
+ * they do in fp32 products: 2e-6 to 1.2e-5 at half to a quarter of it, 5e-5 at rank 1 (fp32 products: 1.4e-4). An element
  * that is not finite, or a matrix whose sum of squares is beyond fp32, gives NaN in all of its own matrix
  * and leaves the others alone.
  * lr (device fp32, replaces cfg->lr) and grad_scale (device fp32) may be null, as in moe_adamw. p, g, o,

@@ -127,7 +127,8 @@ def norm_backward(dy, x, gain, mean, rstd):
 
 def orth(u, steps=5, coef=(3.4445, -4.7750, 2.0315), eps=1e-7, held=None):
     """Newton-Schulz steps on one matrix. `held(x, what)` is what storage makes of an operand ("X", "A",
-    "B" without its diagonal); `held(x, ("sum", K))` of a product of length K."""
+    "B" without its diagonal); `held(x, ("sum", K))` of a product of length K. (With held = fp16_planes(1)
+    X is rounded to one fp16 number, which the kernels do not; orth_one_part has their roundings.)"""
     a, b, c = coef
     keep = held or (lambda x, what: x)
     tall = u.shape[0] > u.shape[1]
@@ -154,6 +155,34 @@ def fp16_planes(planes):
         hi = y.astype(np.float16).astype(np.float64)
         return (hi if planes == 1 else hi + (y - hi).astype(np.float16).astype(np.float64)) / scale[what]
     return held
+
+
+def two_parts(adds=24, seed=0):
+    """Storage in two fp16 parts, as fp16_planes(2), and sums as the tensor cores leave them where at most `adds`
+    additions go to one partial sum: each cuts off up to 2^-24 of it (more or less in one element than in the next:
+    what the cuts have in common shrinks a product, what differs stands in all directions)."""
+    held, rng = fp16_planes(2), np.random.default_rng(seed)
+    return lambda x, what: x * (1 - 2.0 ** -24 * adds * rng.random(x.shape)) if isinstance(what, tuple) else held(x, what)
+
+
+def orth_one_part(u, steps=5, coef=(3.4445, -4.7750, 2.0315), eps=1e-7):
+    """orth as the kernels round it with one-part products: A and B without its diagonal in one fp16 number; X in
+    two, of which the Gram product takes the high one, the last product both but for the last two steps, and
+    the diagonal of B both."""
+    a, b, c = coef
+    one, two = fp16_planes(1), fp16_planes(2)
+    tall = u.shape[0] > u.shape[1]
+    x = two(u / (np.sqrt((u * u).sum()) + eps), "X")
+    eye = np.eye(min(u.shape))
+    for k in range(steps):
+        hi = one(x, "X")
+        A = one(hi.T @ hi if tall else hi @ hi.T, "A")
+        B = a * eye + b * A + c * (A @ A)
+        D = np.diag(np.diag(B))
+        B = one(B - D, "B")
+        y = x if k + 2 < steps else hi
+        x = two((y @ B if tall else B @ y) + (x @ D if tall else D @ x), "X")
+    return x
 
 
 def muon(p, g, m, lr, momentum, decay, scale, nesterov, **kw):

@@ -15,6 +15,16 @@
 // 2^10, so that what is far smaller than the largest elements keeps its bits too. In MOE_F32 precision an
 // operand is two fp16 planes, x = hi + lo, and a product takes hi hi + hi lo + lo hi.
 //
+// X is kept in two parts in MOE_BF16 precision too. A rounding of X stands in all directions, also in those that u
+// does not have, and the steps that follow multiply small singular values by a each: with 11 bits of X a matrix of
+// 512 x 1024 is off by 8e-4 of its size at full rank, but by 1.4e-2 at rank 128 and by 0.1 at rank 1 (simulated;
+// gradients of experts that few tokens reached are such matrices). So D X takes both parts, and so does the product
+// (B - D) X in all steps but the last two, as a second run over K; A and B, whose roundings reach u's own directions
+// only, stay in one. That leaves 1e-3 at any rank (simulated, 129 x 129 to 700 x 720: 1.1e-3 at most for products of
+// random factors, 1.9e-3 where a few rows alone are not zero, 2.4e-3 for a matrix of ones; with the low part in D X
+// only 3.7e-3, 4.5e-2 and 8.6e-3; in the product of the first two steps, too, 2.6e-3, 4e-3 and 3.7e-3; of all five
+// 1.1e-3, 1.8e-3 and 3.3e-3). Measured: 16 x 4096 x 1024 a step 1.27 ms and, so, 1.60.
+//
 // The diagonal of B, which is near a = 3.4 where the rest is small, is not rounded with it: it stays in fp32 and
 // multiplies X in the epilogue of the product, B X = (B - D) X + D X. (Rounded, it is off by up to 2^-12 in one
 // direction in all rows alike: 2.7e-3 of the result for 35 x 3195 instead of 1.3e-3, simulated. And most of a
@@ -46,8 +56,9 @@ enum Op : int { kGram = 0, kPoly = 1, kApply = 2 };
 struct MuonGemm {
     int count, M, N, K;           // per matrix: out [M, N], reduction K
     int n_tiles, tiles;           // of a row of tiles; of one matrix
-    const uint16_t* side;         // [planes][count][M, ld]: poly: A; apply: X
+    const uint16_t* side;         // [planes][count][M, ld]: poly: A; apply: X (2 planes)
     int ld;
+    int twice;                    // apply, one part: X's low part is multiplied, too (before the high one)
     float* diag;                  // [count][dstride]: poly writes B's diagonal, apply reads it
     int dstride;
     const uint16_t* weights;      // last product with bf16 output: what it steps [count, M, N] (null: o is written)
@@ -180,6 +191,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                  const __grid_constant__ CUtensorMap tmO) {
     constexpr bool SYM = OP != kApply, SIDED = OP != kGram, TALL = OP == kApply && !B_MN;
+    constexpr bool TWO = SPLIT || OP == kApply;      // side input and output in two parts
     constexpr int PL = SPLIT ? 2 : 1, B_BYTES = NT / 2 * BK * 2, STAGE = stage_bytes(NT, SPLIT), STAGES = kRingBytes / STAGE;
     constexpr int BUFS = NT == kTile ? 2 : 4;      // sums in TMEM (1024 x 1024 in two parts: 295 us with 2, 263 with 4)
     extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -219,7 +231,9 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
     cluster_sync();   // both CTAs' barriers exist before any remote arrive or complete_tx
     const uint32_t tmem_base = *tmem_slot;
     const int num_tiles = p.count * p.tiles;
-    const int kblocks = (p.K + BK - 1) / BK;
+    const int kblocks1 = (p.K + BK - 1) / BK;
+    const bool twice = OP == kApply && !SPLIT && p.twice;
+    const int kblocks = twice ? 2 * kblocks1 : kblocks1;
     const int seg = SPLIT ? (NT == kTile ? kSegment : 1) : kblocks;      // k-blocks to an accumulator
 
     if (warp == 0) {
@@ -236,24 +250,25 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
                     const uint32_t sa = smem_u32(smem + s * STAGE), sb = sa + PL * kPartBytes;
                     const uint32_t fb = map_to_rank(smem_u32(full + s), 0);
                     if (leader) mbar_expect_tx(full + s, same ? 2 * kPartBytes : 2 * STAGE);
-                    const int k0 = kb * BK;
+                    const bool low = twice && kb < kblocks1;       // of X: the left operand of X B, the right one of B X
+                    const int k0 = (twice && !low ? kb - kblocks1 : kb) * BK;
 #pragma unroll
                     for (int part = 0; part < PL; ++part) {
-                        const int z = t.z + part * p.count;
+                        const int za = t.z + (part + (TALL && low)) * p.count, zb = t.z + (part + (!TALL && low)) * p.count;
                         if (!A_MN) {
-                            tma_load_3d_pair(sa + part * kPartBytes, &tmA, k0, mr, z, fb);
+                            tma_load_3d_pair(sa + part * kPartBytes, &tmA, k0, mr, za, fb);
                         } else {
 #pragma unroll
                             for (int j = 0; j < kHalf / 64; ++j)
-                                tma_load_3d_pair(sa + part * kPartBytes + j * (BK * 128), &tmA, mr + 64 * j, k0, z, fb);
+                                tma_load_3d_pair(sa + part * kPartBytes + j * (BK * 128), &tmA, mr + 64 * j, k0, za, fb);
                         }
                         if (same) {
                         } else if (!B_MN) {
-                            tma_load_3d_pair(sb + part * B_BYTES, &tmB, k0, nh, z, fb);
+                            tma_load_3d_pair(sb + part * B_BYTES, &tmB, k0, nh, zb, fb);
                         } else {
 #pragma unroll
                             for (int j = 0; j < NT / 128; ++j)
-                                tma_load_3d_pair(sb + part * B_BYTES + j * (BK * 128), &tmB, nh + 64 * j, k0, z, fb);
+                                tma_load_3d_pair(sb + part * B_BYTES + j * (BK * 128), &tmB, nh + 64 * j, k0, zb, fb);
                         }
                     }
                     ++issued;
@@ -356,8 +371,9 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
                     if (row + 8 * i < p.M && col < ld) to[i] = __ldcg(reinterpret_cast<const uint4*>(src + (size_t)8 * i * ld));
                 }
             };
-            uint4 ahead[4], weights[4];
+            uint4 ahead[4], low[4], weights[4];
             if (SIDED) fetch(p.side, p.ld, 0, 0, ahead);
+            if (TWO && !SPLIT) fetch(p.side, p.ld, 0, 1, low);
             if (OUT == kResult && p.weights) fetch(p.weights, p.N, 0, 0, weights);
             float drow = 0.f;              // D of the lane's row (X times it on the left)
             if (OP == kApply && !TALL && y + lane < p.M) drow = __ldg(p.diag + (size_t)t.z * p.dstride + y + lane);
@@ -382,8 +398,14 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
                         }
                     };
                     add(true);
-                    if (SPLIT) {
-                        fetch(p.side, p.ld, c, 1, own);
+                    if (TWO) {
+                        if (SPLIT) {
+                            fetch(p.side, p.ld, c, 1, own);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) own[i] = low[i];
+                            if (c + 32 < NT / 2) fetch(p.side, p.ld, c + 32, 1, low);
+                        }
                         st.to_rows(lane, own);
                         add(false);
                     }
@@ -442,7 +464,7 @@ muon_gemm_kernel(const MuonGemm p, const __grid_constant__ CUtensorMap tmA, cons
                 for (int i = 0; i < 16; ++i) h[i] = pack_half2(v[2 * i], v[2 * i + 1]);
                 st.store(lane, h, &tmO, x, y, t.z);
                 if (turn) st.store_turned(lane, h, &tmO, y, x, t.z);
-                if (SPLIT) {
+                if (TWO) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
@@ -523,7 +545,7 @@ struct MuonPrep {
     float* m;                 // momentum, or null (orthogonalize)
     const float* grad_scale;
     float* sums;              // [count, chunks] partial sums of squares
-    __half* X;                // [planes, count, rows, ld]
+    __half* X;                // [2, count, rows, ld]
     int64_t n, chunk;         // elements of a matrix, of a chunk
     int chunks, count, rows, cols, ld;
     float momentum, eps;
@@ -635,7 +657,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) muon_sums_kernel(const MuonPr
 }
 
 // Second pass: X = u / (|u| + eps), in fp16 parts.
-template <typename G, int V, bool SPLIT, bool MOMENTUM>
+template <typename G, int V, bool MOMENTUM>
 __global__ void __launch_bounds__(kPrepThreads, 4) muon_scale_kernel(const MuonPrep a) {
     constexpr int U = kAhead<MOMENTUM>;
     __shared__ float s_scale;
@@ -681,10 +703,10 @@ __global__ void __launch_bounds__(kPrepThreads, 4) muon_scale_kernel(const MuonP
                 }
                 if constexpr (V == 8) {
                     *reinterpret_cast<uint4*>(a.X + at) = *reinterpret_cast<uint4*>(hi);
-                    if (SPLIT) *reinterpret_cast<uint4*>(a.X + plane + at) = *reinterpret_cast<uint4*>(lo);
+                    *reinterpret_cast<uint4*>(a.X + plane + at) = *reinterpret_cast<uint4*>(lo);
                 } else {
                     a.X[at] = hi[0];
-                    if (SPLIT) a.X[plane + at] = lo[0];
+                    a.X[plane + at] = lo[0];
                 }
             }
         }
@@ -704,7 +726,7 @@ struct MuonFinish {
     bool step;                // p is stepped; else o is written
 };
 
-template <typename T, int V, bool SPLIT>
+template <typename T, int V>
 __global__ void __launch_bounds__(256) muon_finish_kernel(const MuonFinish a) {
     pdl_wait();
     const float lr = a.lr_dev ? __ldg(a.lr_dev) : a.lr;
@@ -718,16 +740,13 @@ __global__ void __launch_bounds__(256) muon_finish_kernel(const MuonFinish a) {
             const __half* h = reinterpret_cast<const __half*>(&h4);
 #pragma unroll
             for (int q = 0; q < V; ++q) x[q] = __half2float(h[q]);
-            if (SPLIT) {
-                const uint4 l4 = *reinterpret_cast<const uint4*>(a.X + plane + i);
-                const __half* l = reinterpret_cast<const __half*>(&l4);
+            const uint4 l4 = *reinterpret_cast<const uint4*>(a.X + plane + i);
+            const __half* l = reinterpret_cast<const __half*>(&l4);
 #pragma unroll
-                for (int q = 0; q < V; ++q) x[q] += __half2float(l[q]);
-            }
+            for (int q = 0; q < V; ++q) x[q] += __half2float(l[q]);
         } else {
             const int64_t row = i / a.cols, at = row * a.ld + (i - row * a.cols);
-            x[0] = __half2float(a.X[at]);
-            if (SPLIT) x[0] += __half2float(a.X[plane + at]);
+            x[0] = __half2float(a.X[at]) + __half2float(a.X[plane + at]);
         }
         if (!a.step) {
 #pragma unroll
@@ -867,8 +886,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
     constexpr int SUMS = SPLIT ? 4 : 1;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* sX = smem;
-    uint8_t* sA = sX + PL * kPlaneBytes;          // fp32 sums, A, B, and the result
+    uint8_t* sX = smem;                           // two parts
+    uint8_t* sA = sX + 2 * kPlaneBytes;           // fp32 sums, A, B, and the result
     uint8_t* sR = sA + 4 * kBlockBytes;           // sums of the CTA's rows from the others
     __shared__ uint64_t s_bar, s_sums, s_rows;    // products; sums, rows of A that have arrived
     __shared__ uint32_t s_tmem;
@@ -952,7 +971,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
         uint4 hi, lo;
         split8(u[i], hi, lo);
         *reinterpret_cast<uint4*>(sX + unit_at(r, e & 15)) = hi;
-        if (SPLIT) *reinterpret_cast<uint4*>(sX + kPlaneBytes + unit_at(r, e & 15)) = lo;
+        *reinterpret_cast<uint4*>(sX + kPlaneBytes + unit_at(r, e & 15)) = lo;
     }
     fence_async_smem();
     tc_fence_before();
@@ -960,12 +979,13 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
     tc_fence_after();
     const uint32_t tmem = s_tmem;
 
-    // One product of 128 x 128 into TMEM by thread 0, waited for by all. k: length of the reduction. A K step of
+    // One product of 128 x 128 into TMEM by thread 0, waited for by all. k: length of the reduction; terms (bits):
+    // lo hi, hi lo, hi hi. A K step of
     // 16 is 32 bytes of a K-major row (a block holds four), or 16 rows of an MN-major block; both are constants
     // in the unrolled loop, since the issuing thread's own instructions are what a small product waits for.
     bool ok = true;
     uint32_t phase = 0;
-    auto product = [&](const uint8_t* pa, auto a_mn, const uint8_t* pb, auto b_mn, int k) {
+    auto product = [&](const uint8_t* pa, auto a_mn, const uint8_t* pb, auto b_mn, int k, int terms) {
         constexpr bool AMN = decltype(a_mn)::value, BMN = decltype(b_mn)::value;
         if (tid == 0 && ok) {
             constexpr uint32_t idesc = idesc_fp16(kSide, kSide, AMN, BMN);
@@ -973,13 +993,15 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
             const uint64_t db = make_desc(smem_u32(pb), BMN ? kBlockBytes : 16, 1024);
             const int n = (k + 15) / 16;
 #pragma unroll
-            for (int term = SPLIT ? 0 : 2; term < 3; ++term) {
+            for (int term = 0; term < 3; ++term) {
+                if (!((terms >> term) & 1)) continue;
+                const bool first = !(terms & ((1 << term) - 1));
                 const uint64_t ta = da + (term == 0 ? kPlaneBytes >> 4 : 0), tb = db + (term == 1 ? kPlaneBytes >> 4 : 0);
 #pragma unroll
                 for (int q = 0; q < kSide / 16; ++q) {
                     const uint32_t major = ((q >> 2) * kBlockBytes + (q & 3) * 32) >> 4, minor = (q * 16 * 128) >> 4;
                     if (q < n) tc_mma(tmem + q % SUMS * kSide, ta + (AMN ? minor : major), tb + (BMN ? minor : major), idesc,
-                                      term == (SPLIT ? 0 : 2) && q < SUMS ? 0u : 1u);
+                                      first && q < SUMS ? 0u : 1u);
                 }
             }
             tc_commit(&s_bar);
@@ -991,14 +1013,15 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
     constexpr std::integral_constant<bool, TALL> tall{};
     constexpr std::false_type major{};
     constexpr std::true_type minor{};
+    constexpr int all = SPLIT ? 7 : 4;
     // Each thread has a row of the product (TMEM lane) and 32 of its columns.
     const int row = (warp & 3) * 32 + lane, part = warp >> 2;
     const uint32_t taddr = tmem + ((uint32_t)((warp & 3) * 32) << 16) + part * 32;
-    auto put8 = [&](uint8_t* to, int unit, const float* v) {
+    auto put8 = [&](uint8_t* to, int unit, const float* v, bool two) {
         uint4 hi, lo;
         split8(v, hi, lo);
         *reinterpret_cast<uint4*>(to + unit_at(row, unit)) = hi;
-        if (SPLIT) *reinterpret_cast<uint4*>(to + kPlaneBytes + unit_at(row, unit)) = lo;
+        if (two) *reinterpret_cast<uint4*>(to + kPlaneBytes + unit_at(row, unit)) = lo;
     };
     // The thread's columns of the product; k: the reduction's length.
     auto sums = [&](int k, float (&v)[32]) {
@@ -1017,17 +1040,17 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
         }
     };
     // 8 fp16 values (in parts) of the thread's row.
-    auto get8 = [&](const uint8_t* from, int unit, float* v) {
+    auto get8 = [&](const uint8_t* from, int unit, float* v, bool two) {
         const uint4 q4 = *reinterpret_cast<const uint4*>(from + unit_at(row, unit));
         const __half2* q = reinterpret_cast<const __half2*>(&q4);
         uint4 l4 = make_uint4(0, 0, 0, 0);
-        if (SPLIT) l4 = *reinterpret_cast<const uint4*>(from + kPlaneBytes + unit_at(row, unit));
+        if (two) l4 = *reinterpret_cast<const uint4*>(from + kPlaneBytes + unit_at(row, unit));
         const __half2* l = reinterpret_cast<const __half2*>(&l4);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 f = __half22float2(q[i]), g = __half22float2(l[i]);
-            v[2 * i] = SPLIT ? f.x + g.x : f.x;
-            v[2 * i + 1] = SPLIT ? f.y + g.y : f.y;
+            v[2 * i] = f.x + g.x;
+            v[2 * i + 1] = f.y + g.y;
         }
     };
     auto ready = [&]() {     // this CTA's writes are there for the next product or copy, and TMEM is read
@@ -1041,7 +1064,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
 
     for (int step = 0; step < a.steps; ++step) {
         // ---- gram
-        product(sX, tall, sX, tall, TALL ? nr : nc);
+        product(sX, tall, sX, tall, TALL ? nr : nc, all);
         {
             float v[32];
             sums(TALL ? nr : nc, v);
@@ -1049,7 +1072,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
             for (int i = 0; i < 32; ++i) v[i] *= kAScale / (kXScale * kXScale);
             if (CS == 1) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) put8(sA, part * 4 + j, v + 8 * j);
+                for (int j = 0; j < 4; ++j) put8(sA, part * 4 + j, v + 8 * j, SPLIT);
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
@@ -1112,14 +1135,14 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
             asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
         }
         // ---- poly: B = a I + b A + c A A in the place of A
-        product(sA, major, sA, major, a.side);
+        product(sA, major, sA, major, a.side, all);
         // every CTA has its rows of A, so none of this one's are still being read by a copy
         if (CS > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
         {
             float v[32], w[32];
             sums(a.side, v);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) get8(sA, part * 4 + j, w + 8 * j);
+            for (int j = 0; j < 4; ++j) get8(sA, part * 4 + j, w + 8 * j, SPLIT);
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
                 v[i] = fmaf(a.b * (kBScale / kAScale), w[i], a.c * (kBScale / (kAScale * kAScale)) * v[i]);
@@ -1129,19 +1152,20 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
                 }
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) put8(sA, part * 4 + j, v + 8 * j);
+            for (int j = 0; j < 4; ++j) put8(sA, part * 4 + j, v + 8 * j, SPLIT);
         }
         ready();
         // ---- apply
-        if constexpr (TALL) product(sX, major, sA, major, a.side);
-        else product(sA, major, sX, minor, a.side);
+        const int terms = SPLIT || step + 2 < a.steps ? all | (TALL ? 1 : 2) : all;      // (X's low part, too)
+        if constexpr (TALL) product(sX, major, sA, major, a.side, terms);
+        else product(sA, major, sX, minor, a.side, terms);
         const bool last = step + 1 == a.steps;
         const float drow = s_diag[row];
         {
             float v[32], w[32];
             sums(a.side, v);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) get8(sX, part * 4 + j, w + 8 * j);
+            for (int j = 0; j < 4; ++j) get8(sX, part * 4 + j, w + 8 * j, true);
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
                 float4 d = make_float4(drow, drow, drow, drow);
@@ -1158,7 +1182,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
                         make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
             } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) put8(sX, part * 4 + j, v + 8 * j);
+                for (int j = 0; j < 4; ++j) put8(sX, part * 4 + j, v + 8 * j, true);
             }
         }
         ready();
@@ -1190,7 +1214,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
                 const __half* hi = reinterpret_cast<const __half*>(sX + unit_at(r, e & 15));
                 const __half* lo = reinterpret_cast<const __half*>(sX + kPlaneBytes + unit_at(r, e & 15));
 #pragma unroll
-                for (int q = 0; q < 8; ++q) x[q] = __half2float(hi[q]) + (SPLIT ? __half2float(lo[q]) : 0.f);
+                for (int q = 0; q < 8; ++q) x[q] = __half2float(hi[q]) + __half2float(lo[q]);
             }
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
@@ -1210,8 +1234,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) muon_small_kernel(const Muon
     }
 }
 
-constexpr size_t small_smem(bool split) { return 1024 + (split ? 2 : 1) * (size_t)kPlaneBytes + 4 * kBlockBytes + kRecvBytes; }
-static_assert(small_smem(true) <= 227 * 1024 - 1024, "shared memory per CTA");
+constexpr size_t kSmallSmem = 1024 + 2 * (size_t)kPlaneBytes + 4 * kBlockBytes + kRecvBytes;
+static_assert(kSmallSmem <= 227 * 1024 - 1024, "shared memory per CTA");
 
 // ---------------------------------------------------------------- host
 moe_status_t check_muon(const moe_muon_config_t* c) {
@@ -1242,7 +1266,7 @@ struct MuonScratch {
     __half* B;
     float* diag;
     float* sums;
-    int planes, ld, lds, side;        // ld: of X; side, lds: of A and B
+    int planes, ld, lds, side;        // planes: of A and B (X has 2); ld: of X; side, lds: of A and B
     int dstride;
     int64_t chunk;
     int chunks;
@@ -1265,7 +1289,7 @@ size_t carve_muon(const moe_muon_config_t& c, void* base, MuonScratch* b) {
     b->chunks = (int)((n + b->chunk - 1) / b->chunk);
     const size_t all = (size_t)b->planes * c.count;
     b->sums = ws.take<float>((size_t)c.count * b->chunks + 1);
-    for (__half*& x : b->X) x = ws.take<__half>(all * c.rows * b->ld + 1);
+    for (__half*& x : b->X) x = ws.take<__half>((size_t)2 * c.count * c.rows * b->ld + 1);
     b->dstride = (int)align_up(b->side, 32);
     b->diag = ws.take<float>((size_t)c.count * b->dstride + kTile);
     b->A = ws.take<__half>(all * b->side * b->lds + 1);
@@ -1290,22 +1314,22 @@ bool map_3d(CUtensorMap* tm, const void* base, uint64_t cols, uint64_t rows, uin
 
 struct Operand {
     const void* base;
-    int rows, cols, ld;
+    int rows, cols, ld, planes;
 };
 
 // K-major operands come in boxes of 64 k x 128 rows (B: half a tile's columns), MN-major ones of 64 columns x 64 k.
 template <int OP, bool A_MN, bool B_MN, int NT>
-cudaError_t launch_gemm_as(MuonGemm p, int planes, const Operand& a, const Operand& b, const Operand& o, int out,
+cudaError_t launch_gemm_as(MuonGemm p, bool split, const Operand& a, const Operand& b, const Operand& o, int out,
                            cudaStream_t s) {
-    const uint64_t outer = (uint64_t)planes * p.count;
+    auto outer = [&](const Operand& q) { return (uint64_t)q.planes * p.count; };
     CUtensorMap ta, tb, to;
-    if (!map_3d(&ta, a.base, a.cols, a.rows, outer, a.ld, 64, A_MN ? BK : kHalf, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !map_3d(&tb, b.base, b.cols, b.rows, outer, b.ld, 64, B_MN ? BK : NT / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !map_3d(&to, o.base, o.cols, o.rows, outer, o.ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B,
+    if (!map_3d(&ta, a.base, a.cols, a.rows, outer(a), a.ld, 64, A_MN ? BK : kHalf, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !map_3d(&tb, b.base, b.cols, b.rows, outer(b), b.ld, 64, B_MN ? BK : NT / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !map_3d(&to, o.base, o.cols, o.rows, outer(o), o.ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B,
                 out == kResult ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16))
         return cudaErrorInvalidValue;
-    auto kern = planes == 2 ? muon_gemm_kernel<OP, A_MN, B_MN, true, kParts, NT>
-                            : muon_gemm_kernel<OP, A_MN, B_MN, false, kParts, NT>;
+    auto kern = split ? muon_gemm_kernel<OP, A_MN, B_MN, true, kParts, NT>
+                      : muon_gemm_kernel<OP, A_MN, B_MN, false, kParts, NT>;
     if constexpr (OP == kApply)
         if (out == kResult) kern = muon_gemm_kernel<OP, A_MN, B_MN, false, kResult, NT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem);
@@ -1327,7 +1351,7 @@ int tiles_of(const MuonGemm& p, bool sym, int nt) {
 // 1024 x 1024 in two parts: 34.7 us, 26.5 and 20.4), but a tile of half the columns takes 0.6 to 0.85 of the time
 // (4 x 2048 x 1024, two rounds for one: gram 42 us and 67, polynomial 37 and 45).
 template <int OP, bool A_MN, bool B_MN>
-cudaError_t launch_gemm(MuonGemm p, int planes, const Operand& a, const Operand& b, const Operand& o, cudaStream_t s,
+cudaError_t launch_gemm(MuonGemm p, bool split, const Operand& a, const Operand& b, const Operand& o, cudaStream_t s,
                         int out = kParts) {
     constexpr bool SYM = OP != kApply;
     constexpr int LEAST = B_MN ? 128 : 64;
@@ -1337,32 +1361,29 @@ cudaError_t launch_gemm(MuonGemm p, int planes, const Operand& a, const Operand&
     p.n_tiles = ceil_div(p.N, nt);
     p.tiles = tiles_of(p, SYM, nt);
     p.err = device_error_word();
-    if (nt == 256) return launch_gemm_as<OP, A_MN, B_MN, 256>(p, planes, a, b, o, out, s);
-    if (nt == 128) return launch_gemm_as<OP, A_MN, B_MN, 128>(p, planes, a, b, o, out, s);
-    if constexpr (LEAST == 64) return launch_gemm_as<OP, A_MN, B_MN, 64>(p, planes, a, b, o, out, s);
+    if (nt == 256) return launch_gemm_as<OP, A_MN, B_MN, 256>(p, split, a, b, o, out, s);
+    if (nt == 128) return launch_gemm_as<OP, A_MN, B_MN, 128>(p, split, a, b, o, out, s);
+    if constexpr (LEAST == 64) return launch_gemm_as<OP, A_MN, B_MN, 64>(p, split, a, b, o, out, s);
     return cudaErrorInvalidValue;
 }
 
 template <typename G, bool MOMENTUM>
-cudaError_t launch_prep(const MuonPrep& a, bool split, cudaStream_t s) {
+cudaError_t launch_prep(const MuonPrep& a, cudaStream_t s) {
     const int64_t work = (int64_t)a.count * a.chunks;
     const int grid = (int)std::min<int64_t>(work, (int64_t)num_sms() * 4);
     cudaError_t e = launch_pdl(a.n % 8 == 0 ? muon_sums_kernel<G, 8, MOMENTUM> : muon_sums_kernel<G, 1, MOMENTUM>,
                                dim3(grid), dim3(kPrepThreads), 0, s, a);
     count_launch();
     if (e != cudaSuccess) return e;
-    auto kern = a.cols % 8 == 0 ? (split ? muon_scale_kernel<G, 8, true, MOMENTUM> : muon_scale_kernel<G, 8, false, MOMENTUM>)
-                                : (split ? muon_scale_kernel<G, 1, true, MOMENTUM> : muon_scale_kernel<G, 1, false, MOMENTUM>);
-    e = launch_pdl(kern, dim3(grid), dim3(kPrepThreads), 0, s, a);
+    e = launch_pdl(a.cols % 8 == 0 ? muon_scale_kernel<G, 8, MOMENTUM> : muon_scale_kernel<G, 1, MOMENTUM>, dim3(grid), dim3(kPrepThreads), 0, s, a);
     count_launch();
     return e;
 }
 
 template <typename T>
-cudaError_t launch_finish(const MuonFinish& a, bool split, cudaStream_t s) {
+cudaError_t launch_finish(const MuonFinish& a, cudaStream_t s) {
     const int v = a.cols % 8 == 0 ? 8 : 1;
-    auto kern = v == 8 ? (split ? muon_finish_kernel<T, 8, true> : muon_finish_kernel<T, 8, false>)
-                       : (split ? muon_finish_kernel<T, 1, true> : muon_finish_kernel<T, 1, false>);
+    auto kern = v == 8 ? muon_finish_kernel<T, 8> : muon_finish_kernel<T, 1>;
     const int64_t need = (a.total + 256 * v - 1) / (256 * v);
     const cudaError_t e = launch_pdl(kern, dim3((unsigned)std::min<int64_t>(need, (int64_t)num_sms() * 32)), dim3(256),
                                      0, s, a);
@@ -1388,13 +1409,12 @@ cudaError_t launch_small(const moe_muon_config_t& c, const MuonPrep& pre, const 
     const bool tall = c.rows > c.cols;
     auto kern = split ? (tall ? muon_small_kernel<true, true> : muon_small_kernel<true, false>)
                       : (tall ? muon_small_kernel<false, true> : muon_small_kernel<false, false>);
-    const size_t smem = small_smem(split);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmallSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(c.count * a.cluster));
     cfg.blockDim = dim3(kSmallThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = kSmallSmem;
     cfg.stream = s;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1427,24 +1447,24 @@ cudaError_t launch_muon(const moe_muon_config_t& c, const void* g, float* m, con
     f.scale = (float)c.scale;
     if (small_matrix(c)) return launch_small(c, pre, f, split, s);
     cudaError_t e = c.grad_dtype == MOE_BF16
-                        ? (m ? launch_prep<__nv_bfloat16, true>(pre, split, s) : launch_prep<__nv_bfloat16, false>(pre, split, s))
-                        : (m ? launch_prep<float, true>(pre, split, s) : launch_prep<float, false>(pre, split, s));
+                        ? (m ? launch_prep<__nv_bfloat16, true>(pre, s) : launch_prep<__nv_bfloat16, false>(pre, s))
+                        : (m ? launch_prep<float, true>(pre, s) : launch_prep<float, false>(pre, s));
     if (e != cudaSuccess) return e;
-    const Operand A{b.A, b.side, b.side, b.lds}, B{b.B, b.side, b.side, b.lds};
+    const Operand A{b.A, b.side, b.side, b.lds, b.planes}, B{b.B, b.side, b.side, b.lds, b.planes};
     // the last product writes the result where that is bf16, in rows of whole 16-byte units
     const bool direct = !split && c.dtype == MOE_BF16 && !f.master && c.cols % 8 == 0;
     int at = 0;
     for (int k = 0; k < c.steps; ++k, at ^= 1) {
         const bool result = direct && k + 1 == c.steps;
-        const Operand X{b.X[at], c.rows, c.cols, b.ld};
-        const Operand Y{result ? f.out : b.X[at ^ 1], c.rows, c.cols, result ? c.cols : b.ld};
+        const Operand X{b.X[at], c.rows, c.cols, b.ld, 2};
+        const Operand Y{result ? f.out : b.X[at ^ 1], c.rows, c.cols, result ? c.cols : b.ld, result ? 1 : 2};
         MuonGemm p{};
         p.count = c.count;
         p.M = p.N = b.side;
         p.K = std::max(c.rows, c.cols);
         p.alpha = kAScale / (kXScale * kXScale);
-        e = tall ? launch_gemm<kGram, true, true>(p, b.planes, X, X, A, s)
-                 : launch_gemm<kGram, false, false>(p, b.planes, X, X, A, s);
+        e = tall ? launch_gemm<kGram, true, true>(p, split, X, X, A, s)
+                 : launch_gemm<kGram, false, false>(p, split, X, X, A, s);
         if (e != cudaSuccess) return e;
         p.K = b.side;
         p.side = reinterpret_cast<const uint16_t*>(b.A);
@@ -1454,13 +1474,14 @@ cudaError_t launch_muon(const moe_muon_config_t& c, const void* g, float* m, con
         p.alpha = (float)(c.c * kBScale / ((double)kAScale * kAScale));
         p.beta = (float)(c.b * kBScale / kAScale);
         p.a = (float)c.a;
-        e = launch_gemm<kPoly, false, false>(p, b.planes, A, A, B, s);
+        e = launch_gemm<kPoly, false, false>(p, split, A, A, B, s);
         if (e != cudaSuccess) return e;
         p.M = c.rows;
         p.N = c.cols;
         p.alpha = 1.f / kBScale;
         p.side = reinterpret_cast<const uint16_t*>(b.X[at]);
         p.ld = b.ld;
+        p.twice = !split && k + 2 < c.steps;
         if (result) {
             p.weights = f.step ? static_cast<const uint16_t*>(f.out) : nullptr;
             p.gain = 1.f / kXScale;
@@ -1470,13 +1491,13 @@ cudaError_t launch_muon(const moe_muon_config_t& c, const void* g, float* m, con
             p.scale = f.scale / kXScale;
         }
         const int out = result ? kResult : kParts;
-        e = tall ? launch_gemm<kApply, false, false>(p, b.planes, X, B, Y, s, out)
-                 : launch_gemm<kApply, false, true>(p, b.planes, B, X, Y, s, out);
+        e = tall ? launch_gemm<kApply, false, false>(p, split, X, B, Y, s, out)
+                 : launch_gemm<kApply, false, true>(p, split, B, X, Y, s, out);
         if (e != cudaSuccess) return e;
         if (result) return cudaSuccess;
     }
     f.X = b.X[at];
-    return c.dtype == MOE_BF16 ? launch_finish<__nv_bfloat16>(f, split, s) : launch_finish<float>(f, split, s);
+    return c.dtype == MOE_BF16 ? launch_finish<__nv_bfloat16>(f, s) : launch_finish<float>(f, s);
 }
 
 }  // namespace
