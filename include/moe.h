@@ -453,7 +453,7 @@ typedef struct {
     int32_t groups_kept;   /* 1 .. groups */
     int32_t group_top;     /* 1 or 2 */
     int32_t renormalise;   /* 0/1 */
-    float temperature;     /* > 0, with a finite reciprocal */
+    float temperature;     /* > 0, finite; log2(e) / temperature too (temperature from 4.24e-39 on) */
     float scale;           /* finite */
 } moe_score_config_t;
 /* Bytes of `ws` for moe_route_scores; 0 for an invalid cfg. */

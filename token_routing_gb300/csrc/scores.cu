@@ -1,5 +1,6 @@
 // Choice of experts from scores (softmax over all experts, or sigmoids), with a bias for balance,
 // expert groups and renormalised weights, and its gradient in the logits.
+#include <cfloat>
 #include <cmath>
 
 #include "internal.cuh"
@@ -594,6 +595,10 @@ __global__ void __launch_bounds__(kThreads) scores_grad_full_kernel(const ScoreG
 }
 
 // ---------------------------------------------------------------- host
+// log2(e) / temperature: what the comparison multiplies logits by. Where fp32 does not hold it the largest logit's
+// score would be 0 inf, and no expert the largest.
+double to_log2(float temperature) { return 1.4426950408889634 / (double)temperature; }
+
 moe_status_t check_scores(const moe_score_config_t* c) {
     if (!c) return MOE_ERR_INVALID_ARG;
     if (c->T < 0 || c->E < 1 || c->E > MOE_MAX_EXPERTS || c->groups < 1 || c->groups > 32 || c->E % c->groups ||
@@ -603,7 +608,7 @@ moe_status_t check_scores(const moe_score_config_t* c) {
     if ((c->score != MOE_SCORE_SOFTMAX && c->score != MOE_SCORE_SIGMOID) || (c->group_top != 1 && c->group_top != 2) ||
         (c->renormalise != 0 && c->renormalise != 1))
         return MOE_ERR_INVALID_ARG;
-    if (!(c->temperature > 0.0f) || !std::isfinite(c->temperature) || !std::isfinite(1.0f / c->temperature) ||
+    if (!(c->temperature > 0.0f) || !std::isfinite(c->temperature) || !(to_log2(c->temperature) <= FLT_MAX) ||
         !std::isfinite(c->scale))
         return MOE_ERR_INVALID_ARG;
     if (c->T > (1 << 27)) return MOE_ERR_UNSUPPORTED;
@@ -715,7 +720,7 @@ extern "C" MOE_API moe_status_t moe_route_scores(const moe_score_config_t* cfg, 
     reciprocal(c.temperature, &a.inv_hi, &a.inv_lo);
     const bool softmax = c.score == MOE_SCORE_SOFTMAX;
     const bool choice = bias || (c.groups_kept < c.groups && c.group_top == 2);
-    a.to_log2 = (float)(1.4426950408889634 / (double)c.temperature);
+    a.to_log2 = (float)to_log2(c.temperature);
     auto go = c.E == 256 ? launch_scores<8, true> : c.E == 128 ? launch_scores<4, true>
               : c.E == 64 ? launch_scores<2, true> : c.E == 32 ? launch_scores<1, true>
               : c.E > 128 ? launch_scores<8, false> : c.E > 64 ? launch_scores<4, false>
