@@ -456,7 +456,7 @@ typedef struct {
     float temperature;     /* > 0, finite; log2(e) / temperature too (temperature from 4.24e-39 on) */
     float scale;           /* finite */
 } moe_score_config_t;
-/* Bytes of `ws` for moe_route_scores; 0 for an invalid cfg. */
+/* Bytes of `ws` for moe_route_scores on the current device (by its number of SMs); 0 for an invalid cfg. */
 MOE_API size_t moe_route_scores_workspace_bytes(const moe_score_config_t* cfg);
 MOE_API moe_status_t moe_route_scores(const moe_score_config_t* cfg, const float* logits, const float* bias,
                                       int32_t* idx, float* w, int32_t* counts, float* balance_loss, void* ws,
@@ -514,7 +514,7 @@ typedef struct {
 MOE_API moe_status_t moe_layer_norm(const moe_norm_config_t* cfg, const void* x, const void* residual,
                                     const void* gain, const void* bias, void* total, void* y, float* mean,
                                     float* rstd, moe_stream_t stream);
-/* Bytes of `ws` for moe_layer_norm_backward; 0 for an invalid cfg. */
+/* Bytes of `ws` for moe_layer_norm_backward on the current device (by its number of SMs); 0 for an invalid cfg. */
 MOE_API size_t moe_norm_workspace_bytes(const moe_norm_config_t* cfg);
 MOE_API moe_status_t moe_layer_norm_backward(const moe_norm_config_t* cfg, const void* dy, const void* s,
                                              const void* gain, const float* mean, const float* rstd,

@@ -51,11 +51,17 @@ def _opt(what, t, dtype, shape, gpu):
     return None if t is None else _arg(what, t, dtype, shape, gpu)
 
 
-def _bytes(what, cfg, key):
-    """The C call's answer for this configuration, asked for once while the fields that it depends on stay."""
-    got = cfg.__dict__.get("_bytes")
+def _bytes(what, cfg, gpu, *fields):
+    """The C call's answer for this configuration on GPU `gpu` (it depends on its number of SMs), asked for once while
+    the fields that it depends on stay."""
+    got, key = cfg.__dict__.get("_bytes"), (what, gpu, *fields)
     if got is None or got[0] != key:
-        got = key, int(getattr(L.load(), what)(ctypes.byref(cfg)))
+        if gpu < 0 or torch._C._cuda_getDevice() == gpu:
+            need = getattr(L.load(), what)(ctypes.byref(cfg))
+        else:
+            with torch.cuda.device(gpu):
+                need = getattr(L.load(), what)(ctypes.byref(cfg))
+        got = key, int(need)
         if got[1]:                      # 0: the configuration is refused, as the call will be
             cfg._bytes = got
     return got[1]
@@ -313,7 +319,7 @@ def route_scores(cfg, logits, bias, idx, w, counts=None, balance_loss=None, ws=N
             _arg("idx", idx, i32, (T, k), gpu), _arg("w", w, f32, (T, k), gpu), _opt("counts", counts, i32, (E,), gpu),
             _opt("balance_loss", balance_loss, f32, (1,), gpu))
     tally = counts is not None or balance_loss is not None
-    at = _work(ws, _bytes("moe_route_scores_workspace_bytes", cfg, (T, E)), gpu) if tally else None
+    at = _work(ws, _bytes("moe_route_scores_workspace_bytes", cfg, gpu, T, E), gpu) if tally else None
     _launch("moe_route_scores", gpu, stream, ctypes.byref(cfg), *args, at)
 
 
@@ -360,7 +366,7 @@ def layer_norm_backward(cfg, dy, s, gain, mean, rstd, dx, dgain, dbias, ws, dtot
             _opt("dgain", dgain, f32, row, gpu), _opt("dbias", dbias, f32, row, gpu))
     sums = dgain is not None or dbias is not None
     _launch("moe_layer_norm_backward", gpu, stream, ctypes.byref(cfg), *args,
-            _work(ws, _bytes("moe_norm_workspace_bytes", cfg, (T, d, dt)), gpu) if sums else None)
+            _work(ws, _bytes("moe_norm_workspace_bytes", cfg, gpu, T, d, dt), gpu) if sums else None)
 
 
 # ---------------------------------------------------------------- orthogonalised updates (Muon)
