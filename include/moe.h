@@ -541,12 +541,14 @@ MOE_API moe_status_t moe_layer_norm_backward(const moe_norm_config_t* cfg, const
  * and leaves the others alone.
  * lr (device fp32, replaces cfg->lr) and grad_scale (device fp32) may be null, as in moe_adamw. p, g, o,
  * master, m and ws (moe_muon_workspace_bytes) are 16-byte aligned and do not overlap, but o may be g where
- * their types are the same. count = 0 is allowed. */
+ * their types are the same. count = 0 is allowed.
+ * Coefficients and steps with which a singular value in [0, 1] can bring X or A = X X^T above 31.9, or b A + c A A
+ * above 63.8 (all of them held in fp16, scaled), are refused (MOE_ERR_UNSUPPORTED); the usual ones stay below 1.5 and 3. */
 typedef struct {
     int32_t count;         /* matrices, 0 .. 65535; count * ceil(rows / 256) * ceil(cols / 256) to 2^30 */
     int32_t rows, cols;    /* 1 .. 65536 each */
     int32_t steps;         /* 0 .. 100 */
-    double a, b, c;        /* coefficients, magnitudes up to 16 */
+    double a, b, c;        /* coefficients, magnitudes up to 16; see above */
     double lr, momentum, weight_decay, scale, eps;   /* finite; momentum in [0, 1), eps in [1e-12, 1] */
     int32_t nesterov;      /* 0/1 */
     int32_t dtype;         /* moe_dtype_t of p, o */

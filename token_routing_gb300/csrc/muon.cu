@@ -1238,6 +1238,35 @@ constexpr size_t kSmallSmem = 1024 + 2 * (size_t)kPlaneBytes + 4 * kBlockBytes +
 static_assert(kSmallSmem <= 227 * 1024 - 1024, "shared memory per CTA");
 
 // ---------------------------------------------------------------- host
+// Whether fp16 holds, at their scales, all that the steps make of singular values in [0, 1]: the largest of X by the
+// maximum of |s (a + b s^2 + c s^4)| from step to step, A's by its square, and of B without its diagonal by that of
+// |b A + c A^2|; no element is larger than those. With 2^-9 to spare for roundings.
+bool fits_fp16(const moe_muon_config_t& c) {
+    constexpr double kMost = 65504.0 * (1.0 - 1.0 / 512), kSlack = 1.0 + 1.0 / 512;
+    double s = 1.0;                                    // largest singular value of X
+    for (int k = 0; k < c.steps; ++k) {
+        const double t = s * s;                        // and of A
+        auto poly = [&](double u) { return std::fabs(std::sqrt(u) * (c.a + u * (c.b + u * c.c))); };
+        auto rest = [&](double u) { return std::fabs(u * (c.b + u * c.c)); };
+        double x = poly(t), b = rest(t);
+        if (c.c != 0.0 && -c.b / (2.0 * c.c) > 0.0) b = std::max(b, rest(std::min(t, -c.b / (2.0 * c.c))));
+        // zeros of a + 3 b u + 5 c u^2
+        const double root = 9.0 * c.b * c.b - 20.0 * c.a * c.c;
+        if (c.c != 0.0 && root >= 0.0) {
+            for (double sign : {-1.0, 1.0}) {
+                const double u = (-3.0 * c.b + sign * std::sqrt(root)) / (10.0 * c.c);
+                if (u > 0.0 && u < t) x = std::max(x, poly(u));
+            }
+        } else if (c.c == 0.0 && c.b != 0.0) {
+            const double u = -c.a / (3.0 * c.b);
+            if (u > 0.0 && u < t) x = std::max(x, poly(u));
+        }
+        if (!(t * kAScale <= kMost && b * kBScale <= kMost && x * kXScale <= kMost)) return false;
+        s = x * kSlack;
+    }
+    return true;
+}
+
 moe_status_t check_muon(const moe_muon_config_t* c) {
     if (!c) return MOE_ERR_INVALID_ARG;
     if (c->count < 0 || c->rows < 1 || c->cols < 1 || c->steps < 0 || c->steps > 100) return MOE_ERR_INVALID_ARG;
@@ -1251,7 +1280,7 @@ moe_status_t check_muon(const moe_muon_config_t* c) {
         if (t != MOE_F32 && t != MOE_BF16) return MOE_ERR_INVALID_ARG;
     if (c->count > 65535 || c->rows > 65536 || c->cols > 65536) return MOE_ERR_UNSUPPORTED;
     const int64_t tiles = (int64_t)ceil_div(c->rows, kTile) * ceil_div(c->cols, kTile);
-    if (c->count * tiles > (1 << 30)) return MOE_ERR_UNSUPPORTED;
+    if (c->count * tiles > (1 << 30) || !fits_fp16(*c)) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
 

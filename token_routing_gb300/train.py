@@ -442,8 +442,8 @@ class Muon:
             t["cfg"] = cfg
             if count > 0:
                 size = muon_workspace_bytes(cfg)
-                if size == 0:
-                    L.check("moe_muon", L.MOE_ERR_INVALID_ARG)
+                if size == 0:               # refused: the call says why
+                    L.check("moe_muon", L.load().moe_muon(ctypes.byref(cfg), *[None] * 8))
                 need, device = max(need, size), p.device
             self.tensors.append(t)
         self.ws = torch.empty(need, dtype=torch.uint8, device=device)
