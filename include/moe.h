@@ -424,8 +424,10 @@ MOE_API moe_status_t moe_adamw(const moe_adamw_config_t* cfg, const moe_adamw_te
 
 /* Choice of experts from scores: what moe_route's top-k and softmax over the k do not cover. The
  * scores are a softmax over all experts or sigmoids; a bias for balance enters the choice but not
- * the weights; experts may stand in groups, of which only the best are open to a token. What is
- * compared is within 2^-21 of the exact value; weights are rounded as fp32 operations are.
+ * the weights; experts may stand in groups, of which only the best are open to a token. Scores are
+ * compared as hardware exponentials and reciprocals give them: within 2^-21 of the exact score for a sigmoid,
+ * 2^-19 for a softmax (E = 256; absolute bounds: scores far below 1 may round alike), plus the rounding of
+ * score + bias and, for groups, of the sum of two. Weights are rounded as fp32 operations are.
  *   logits [T,E] fp32 (moe_route's `logits`), bias [E] fp32 (nullable: 0)
  *   s_te = softmax(logits_t / temperature)_e   or   1 / (1 + exp(-logits_te / temperature)),
  *   c_te = s_te + bias_e; -inf where the logit is -inf or c is NaN,
@@ -436,8 +438,8 @@ MOE_API moe_status_t moe_adamw(const moe_adamw_config_t* cfg, const moe_adamw_te
  *     the softmax over the chosen logits alone; sigmoid: the sum plus 1e-20),
  *   counts [E] int32: choices of each expert (nullable), balance_loss [1] fp32 =
  *     mean_e (counts[e] - T k / E)^2 as moe_route's (nullable).
- * Ties, of experts and of groups, go to the lower id. Without a bias c is compared as the logit
- * (for groups with group_top 1 too), so that scores which round alike keep their order. idx are
+ * Ties, of experts and of groups, go to the lower id. Without a bias experts are compared by their logits
+ * (and groups by the largest, with group_top 1), so that scores which round alike keep their order. idx are
  * always k different experts of the open groups; one with a logit of -inf is taken only where the
  * open groups hold fewer than k others, and has weight 0. A softmax over a row that holds NaN or
  * +inf is NaN: the row's weights are NaN and its experts the first ones. A row of -inf alone has

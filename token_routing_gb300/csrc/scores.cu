@@ -42,11 +42,15 @@ __device__ __forceinline__ float warp_max(float v) {
     return r;
 }
 
-// One token by a warp, up to its list of chosen experts. CHOICE: experts are compared by score plus bias; else by
-// logit. FULL: E = 32 V, and a lane has V experts side by side, so that a group is a lane or more and needs no
+// What is compared: logits; scores plus bias; or, without a bias but with groups that are worth the sum of two scores,
+// scores for the groups and logits for the experts in them (scores that round alike keep the order of their logits).
+enum Compare : int { kLogits = 0, kScores = 1, kGroups = 2 };
+
+// One token by a warp, up to its list of chosen experts. FULL: E = 32 V, and a lane has V experts side by side, so that a group is a lane or more and needs no
 // exchange but shuffles; else expert lane + 32 i is the lane's i-th. Scores of all experts serve the comparison
-// only and are within 2^-21 (hardware exponential and reciprocal); weights are computed anew, in full precision,
-// from the chosen logits.
+// only, by hardware exponential and reciprocal: s (1 - s) times the argument's rounding (0.22 2^-23) and the exponential's
+// (0.25 2^-22), the sum's and the reciprocal's are 2.3 2^-23 for a sigmoid; a softmax has the roundings of its sum, too
+// (13 additions: 12.4 2^-23 in all). Weights are computed anew, in full precision, from the chosen logits.
 //
 // Bound by instructions: 32768 tokens of 256 experts in groups are 34 MB, 5 us at the copy rate, and take 22 us,
 // 518 warp instructions a token in 75% of the issue slots (700 with every 32nd expert to a lane, groups exchanged
@@ -54,9 +58,10 @@ __device__ __forceinline__ float warp_max(float v) {
 // 32 lanes' maxima bounds the k largest from below, so only experts at or above it (8 to 14 of 256 for k = 8) are
 // ranked, each by counting those ahead of it; a reduction over the warp is one instruction; weights are left to
 // route_weights, for four tokens at once.
-template <int V, bool SOFTMAX, bool CHOICE, bool FULL>
+template <int V, bool SOFTMAX, int COMPARE, bool FULL>
 __device__ __forceinline__ void route_token(const ScoreArgs& a, const float (&z)[V], const float (&bias)[V], int lane,
                                             float* s_row, float* s_val, int* s_id, int* pick, float2* norm) {
+    constexpr bool CHOICE = COMPARE != kLogits;
     const int E = a.E, k = a.k;
     const float inf = INFINITY;
     auto id_of = [&](int i) { return FULL ? lane * V + i : lane + 32 * i; };
@@ -103,7 +108,7 @@ __device__ __forceinline__ void route_token(const ScoreArgs& a, const float (&z)
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         // a logit of -inf, or a NaN, counts as -inf (fmaxf drops a NaN)
-        c[i] = CHOICE ? (z[i] > -inf ? c[i] + bias[i] : -inf) : fmaxf(z[i], -inf);
+        c[i] = CHOICE ? (z[i] > -inf ? COMPARE == kScores ? c[i] + bias[i] : c[i] : -inf) : fmaxf(z[i], -inf);
         if (SOFTMAX && bad) c[i] = -inf;
     }
 
@@ -179,6 +184,14 @@ __device__ __forceinline__ void route_token(const ScoreArgs& a, const float (&z)
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) top = fmaxf(top, c[i]);
+    }
+    if (COMPARE == kGroups) {
+        top = -inf;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (c[i] > -inf) c[i] = z[i];
+            if (!out) top = fmaxf(top, c[i]);
+        }
     }
 
     // a lower bound of the k largest (lanes that tie fall out together, which only lowers it)
@@ -325,7 +338,7 @@ __device__ __forceinline__ void block_balance(const int* s_counts, int T, int E,
     }
 }
 
-template <int V, bool SOFTMAX, bool CHOICE, bool FULL>
+template <int V, bool SOFTMAX, int COMPARE, bool FULL>
 __global__ void __launch_bounds__(kThreads, kScoreBlocks) route_scores_kernel(const ScoreArgs a, int32_t* counts,
                                                                              float* balance) {
     __shared__ float s_row[FULL ? 1 : kWarps][FULL ? 1 : 33 * V];
@@ -344,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, kScoreBlocks) route_scores_kernel(co
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int e = FULL ? lane * V + i : lane + 32 * i;
-        bias[i] = CHOICE && a.bias && e < a.E ? fmaxf(__ldg(a.bias + e), -INFINITY) : 0.f;     // (a NaN: never chosen)
+        bias[i] = COMPARE == kScores && e < a.E ? fmaxf(__ldg(a.bias + e), -INFINITY) : 0.f;     // (a NaN: never chosen)
     }
     int t = blockIdx.x * kWarps + warp;
     float z[V], next[V];
@@ -367,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, kScoreBlocks) route_scores_kernel(co
     if (t < a.T) fetch(t, z);
     for (int done = 0; t < a.T; t += nwarps) {
         fetch(t + nwarps, next);
-        route_token<V, SOFTMAX, CHOICE, FULL>(a, z, bias, lane, s_row[FULL ? 0 : warp], s_val[warp], s_id[warp],
+        route_token<V, SOFTMAX, COMPARE, FULL>(a, z, bias, lane, s_row[FULL ? 0 : warp], s_val[warp], s_id[warp],
                                               s_pick[warp] + done * MOE_MAX_K, s_norm[warp] + done);
         ++done;
         if (done == 4 || t + nwarps >= a.T) {
@@ -632,10 +645,14 @@ int score_blocks(const moe_score_config_t& c) {
 int score_width(const moe_score_config_t& c) { return c.E > 128 ? 8 : c.E > 64 ? 4 : c.E > 32 ? 2 : 1; }
 
 template <int V, bool FULL>
-cudaError_t launch_scores(const ScoreArgs& a, bool softmax, bool choice, int blocks, int32_t* counts, float* balance,
+cudaError_t launch_scores(const ScoreArgs& a, bool softmax, Compare by, int blocks, int32_t* counts, float* balance,
                           cudaStream_t s) {
-    auto kern = softmax ? (choice ? route_scores_kernel<V, true, true, FULL> : route_scores_kernel<V, true, false, FULL>)
-                        : (choice ? route_scores_kernel<V, false, true, FULL> : route_scores_kernel<V, false, false, FULL>);
+    auto kern = softmax ? (by == kScores   ? route_scores_kernel<V, true, kScores, FULL>
+                           : by == kGroups ? route_scores_kernel<V, true, kGroups, FULL>
+                                           : route_scores_kernel<V, true, kLogits, FULL>)
+                        : (by == kScores   ? route_scores_kernel<V, false, kScores, FULL>
+                           : by == kGroups ? route_scores_kernel<V, false, kGroups, FULL>
+                                           : route_scores_kernel<V, false, kLogits, FULL>);
     const cudaError_t e = launch_pdl(kern, dim3(blocks), dim3(kThreads), 0, s, a, counts, balance);
     count_launch();
     return e;
@@ -719,13 +736,13 @@ extern "C" MOE_API moe_status_t moe_route_scores(const moe_score_config_t* cfg, 
     while ((c.groups << (a.lanes_log + 1)) <= 32) ++a.lanes_log;
     reciprocal(c.temperature, &a.inv_hi, &a.inv_lo);
     const bool softmax = c.score == MOE_SCORE_SOFTMAX;
-    const bool choice = bias || (c.groups_kept < c.groups && c.group_top == 2);
+    const Compare by = bias ? kScores : c.groups_kept < c.groups && c.group_top == 2 ? kGroups : kLogits;
     a.to_log2 = (float)to_log2(c.temperature);
     auto go = c.E == 256 ? launch_scores<8, true> : c.E == 128 ? launch_scores<4, true>
               : c.E == 64 ? launch_scores<2, true> : c.E == 32 ? launch_scores<1, true>
               : c.E > 128 ? launch_scores<8, false> : c.E > 64 ? launch_scores<4, false>
               : c.E > 32 ? launch_scores<2, false> : launch_scores<1, false>;
-    cudaError_t e = go(a, softmax, choice, blocks, counts, balance_loss, s);
+    cudaError_t e = go(a, softmax, by, blocks, counts, balance_loss, s);
     if (e == cudaSuccess && tally && blocks > 1) e = launch_counts(c, a.part, blocks, counts, balance_loss, s);
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
