@@ -490,19 +490,20 @@ struct Slot {
 };
 
 // The gradient of the slot's logit z, by lanes of eight to a token. The derivative of a share in its own sum is
-// taken by differences of dw, since one share can be nearly all of the sum.
+// taken by differences of dw, since one share can be nearly all of the sum. A softmax subtracts the largest logit before
+// it divides by the temperature, as the forward pass does: quotients far from zero have lost what tells them apart.
 template <bool SOFTMAX>
 __device__ __forceinline__ float slot_grad(const ScoreGradArgs& a, const Slot& s, float z) {
-    const float x = scaled(z, a.inv_hi, a.inv_lo);
-    float score, slope;             // slope: d score / d x
+    float score, slope;             // slope: d score / d x, with x = z / temperature
     if (SOFTMAX) {
-        float mx = s.on ? x : -INFINITY;
+        float mx = s.on ? z : -INFINITY;
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         if (mx == -INFINITY) mx = 0.f;
-        score = s.on ? expf(x - mx) : 0.f;
+        score = s.on ? expf(scaled(z - mx, a.inv_hi, a.inv_lo)) : 0.f;
         slope = score;              // the part through the sum cancels in the shares
     } else {
+        const float x = scaled(z, a.inv_hi, a.inv_lo);
         score = s.on ? 1.0f / (1.0f + expf(-x)) : 0.f;
         // s (1 - s), with 1 - s = 1 / (1 + e^x) taken apart so that it does not cancel
         slope = score * (1.0f / (1.0f + expf(x)));
@@ -566,7 +567,7 @@ __global__ void __launch_bounds__(kThreads) scores_grad_full_kernel(const ScoreG
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int e = lane + 32 * i;
-            x[i] = e < a.E ? scaled(__ldg(a.logits + (size_t)t * a.E + e), a.inv_hi, a.inv_lo) : -INFINITY;
+            x[i] = e < a.E ? __ldg(a.logits + (size_t)t * a.E + e) : -INFINITY;
             bad |= !(x[i] < INFINITY);
             mx = fmaxf(mx, x[i]);
         }
@@ -587,7 +588,7 @@ __global__ void __launch_bounds__(kThreads) scores_grad_full_kernel(const ScoreG
         float gi[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            x[i] = expf(x[i] - mx);
+            x[i] = expf(scaled(x[i] - mx, a.inv_hi, a.inv_lo));
             sum += x[i];
             gi[i] = sg[lane + 32 * i];
             dot = fmaf(x[i], gi[i], dot);
