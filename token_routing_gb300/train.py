@@ -458,7 +458,11 @@ class Muon:
         if not self.ws.numel():
             return                      # nothing but empty stacks
         if self.placed is None:
-            self.placed = _one_gpu(self.ws, *(t[k] for t in self.tensors for k in ("p", "g", "m", "master")))
+            bound = [t[k] for t in self.tensors for k in ("p", "g", "m", "master")]
+            gpu = _one_gpu(self.ws, *bound)
+            if any(t is not None and t.data_ptr() % 16 for t in bound):      # (before the first tensor is stepped)
+                raise ValueError("p, g, m and master start on 16-byte boundaries")
+            self.placed = gpu
         gpu = _one_gpu(self.ws, lr, grad_scale)
         for t in self.tensors:
             _launch("moe_muon", gpu, stream, ctypes.byref(t["cfg"]), _ptr(t["p"]), _ptr(t["g"]),
