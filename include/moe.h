@@ -502,8 +502,10 @@ MOE_API moe_status_t moe_backward_scores(const moe_config_t* cfg, const moe_scor
  * that reaches the sum itself (a residual stream). dx may be dy, s or dtotal; any other overlap is not
  * allowed. dx may be null where only dgain or dbias is wanted. ws (moe_norm_workspace_bytes) is needed
  * with dgain or dbias; their sums are fp32 in a fixed order, so results repeat bit for bit.
- * T = 0 is allowed (dgain and dbias are zeroed unless accumulate). A row that holds NaN or an infinity
- * gives NaN in its own y and dx, and in dgain and dbias. Arrays of rows, gain, bias, dgain, dbias and ws are 16-byte aligned;
+ * T = 0 is allowed (dgain and dbias are zeroed unless accumulate). A row of s that holds NaN or an infinity
+ * gives NaN in its own y and dx and in all of dgain, and leaves dbias, the sum of dy, alone. What is not finite in
+ * dy leaves no finite element in its row of dx, and none in its column of dgain and dbias. Sums and squares are
+ * fp32: a row whose sum passes it gives NaN, one whose sum of squares alone does has rstd = 0 and y = bias. Arrays of rows, gain, bias, dgain, dbias and ws are 16-byte aligned;
  * d may be odd. */
 typedef struct {
     int32_t T;             /* rows, 0 .. 2^30 */
