@@ -476,7 +476,8 @@ MOE_API moe_status_t moe_route_scores_backward(const moe_score_config_t* cfg, co
  * with the gradient of the gate taken through the scores. scores->T, E and k are cfg's; logits [T,E] as
  * given to moe_route_scores; dlogits [T,E] fp32 is written as moe_route_scores_backward writes it, and
  * dx, dWg and dbg hold its part. cfg->temperature is not used. Dropped assignments give dw = 0 but still
- * enter their token's Jacobian. k = E is refused (MOE_ERR_UNSUPPORTED): dense routing wants slot j to be
+ * enter their token's Jacobian. A softmax that is not renormalised has its part of dx (dlogits Wg) added to dx in the
+ * layer's type: in bf16 dx is rounded twice, and off by up to a whole step of bf16. k = E is refused (MOE_ERR_UNSUPPORTED): dense routing wants slot j to be
  * expert j, and there is nothing to choose. */
 MOE_API moe_status_t moe_backward_scores(const moe_config_t* cfg, const moe_score_config_t* scores,
                                          const float* logits, float* dlogits, const void* dy, const void* x,

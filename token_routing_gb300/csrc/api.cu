@@ -415,7 +415,8 @@ static moe_status_t layer_backward(const moe_config_t* cfg, const ScoresGrad* sc
 
     // With scores the chosen logits' gradients stand in b.dz and all of them in scores->dlogits, both
     // before the branches part; dWg and dbg follow as they do for dense dz rows, and where every logit
-    // has a gradient dx takes its part after the join.
+    // has a gradient dx takes its part after the join. That part is added to the bf16 dx of the un-permute, which so is
+    // rounded twice: an fp32 dx between the two would be 4 T d bytes of workspace for every caller of the backward pass.
 
     // combine backward: dYp, dw, loss partials (padding rows of dYp zeroed)
     MOE_TRY(launch_combine_bwd(c, dy, Yp, w, offsets, row_token, slot_row, b.dYp, dwp, b.lossblk, s));

@@ -1301,8 +1301,8 @@ struct MuonScratch {
     int chunks;
 };
 
-// Whether a matrix fits a cluster of CTAs that keep it in shared memory (one 128 x 1024 fp32 matrix at the border:
-// 190 us by tiled products, 66 so).
+// Whether a matrix fits a cluster of CTAs (8, the portable most) that keep it in shared memory. At the border: 128 x 1024
+// 63 us in fp32 and 47 in bf16, 128 x 1025, by tiled products, 180 and 127; 128 x 2048 216 and 122, 256 x 1024 170 and 112.
 bool small_matrix(const moe_muon_config_t& c) {
     return std::min(c.rows, c.cols) <= kSide && std::max(c.rows, c.cols) <= kSide * kMaxCluster;
 }

@@ -666,7 +666,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_grad_kernel(const NormGr
     }
 }
 
-// Long rows: dx by a block to a row in two passes; dgain and dbias by column_kernel.
+// Long rows: dx by a block to a row in two passes; dgain and dbias by norm_columns_kernel.
 template <typename T, int VE>
 __global__ void __launch_bounds__(kLong) norm_grad_long_kernel(const NormGradArgs a) {
     __shared__ float2 s_red[2][32];
